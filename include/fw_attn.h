@@ -315,6 +315,161 @@ fw_status_t fw_varlen_prefill(const fw_tensor_t *q, const fw_tensor_t *k, const 
                               fw_stream_t stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Speculative decoding: one step verifies a tree of drafted tokens per request.
+ *
+ *   fw_build_page_tables   pages, block table and slot map of the step
+ *   fw_tree_mask           ancestor masks and depths from the trees' parents
+ *   fw_kv_append           the drafts' keys and values into the cache (above)
+ *   fw_paged_decode_tree   attention of every draft over cache and tree
+ *   fw_kv_commit           the accepted path's rows moved to their final places
+ *
+ * The draft tokens of request b take the last draft_lens[b] of its seq_lens[b]
+ * keys, in the order of the tree's nodes (every parent before its children).
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * Paged decode of a tree of drafted tokens.
+ *
+ *   q           [B, T, Hq, D]              BF16, one row per draft (padded to T)
+ *   k_cache, v_cache  [num_pages, ps, Hkv, D]  BF16 or FP8_E4M3 (scales k_scale,
+ *                                          v_scale; 1 for BF16 caches)
+ *   block_table [B, max_pages], seq_lens [B]   as fw_paged_decode; seq_lens
+ *                                          include the drafts
+ *   tree_mask   [B, T, W]  I32, W >= ceil(T / 32): bit j % 32 of word j / 32 of
+ *                          row (b, t) set: draft t sees draft j.  Any relation,
+ *                          not only ancestors: a causal chain, blocks, nothing
+ *   draft_lens  [B]        I32 or NULL (every request has T drafts); clamped to
+ *                          0 .. min(T, seq_lens[b])
+ *   out         [B, T, Hq, D]  BF16, written;  lse [B, T, Hq] F32 or NULL
+ *
+ * With d = draft_lens[b], n = seq_lens[b], draft t < d sees the keys 0 .. n - d - 1
+ * and those keys n - d + j whose bit j is set.  Bits j >= d are ignored.  Rows
+ * with no visible key, and rows t >= d (the padding, whose q is not used), get a
+ * zero output and LSE = -inf.
+ *
+ * Keys that no row sees may hold anything, NaN and infinities included: scores
+ * of hidden keys are dropped by selection.  The VALUES of a draft that some rows
+ * of the request see and others do not must be finite, since a hidden one meets
+ * a zero weight in the product.
+ *
+ * Supported: D in {128, 256} (FP8: 128), 1 <= T <= 256, B <= 4096, page sizes,
+ * strides and alignment of fw_paged_decode; any Hq / Hkv.
+ *
+ * Split-KV as in fw_paged_decode, with its own ranges (one per CTA;
+ * FW_OPT_DECODE_CHUNK_TOKENS does not apply, FW_OPT_MAX_CTAS does).  Two
+ * launches.  The partials take a fixed fw_paged_decode_tree_workspace_size()
+ * bytes whatever the batch: `workspace` (256-byte aligned) or, when it is NULL,
+ * the workspace of fw_set_workspace() or the internal buffer, whose calls have
+ * to be ordered.  Calls with workspaces of their own may overlap.
+ */
+fw_status_t fw_paged_decode_tree(const fw_tensor_t *q, const fw_tensor_t *k_cache, const fw_tensor_t *v_cache,
+                                 const fw_tensor_t *block_table, const fw_tensor_t *seq_lens,
+                                 const fw_tensor_t *tree_mask, const fw_tensor_t *draft_lens, float scale,
+                                 float k_scale, float v_scale, fw_tensor_t *out, fw_tensor_t *lse,
+                                 void *workspace, size_t workspace_bytes, fw_stream_t stream);
+
+/* Workspace bytes of fw_paged_decode_tree on the current device for head dim D
+ * (128 or 256). */
+fw_status_t fw_paged_decode_tree_workspace_size(int32_t head_dim, size_t *bytes);
+
+/*
+ * Ancestor masks of trees given by parents.
+ *
+ *   parents     [B, T]     I32: the index of draft t's parent, -1 for a child of
+ *                          the last committed token; parents[b, t] < t
+ *   draft_lens  [B]        I32 or NULL (T everywhere); clamped to 0 .. T
+ *   tree_mask   [B, T, W]  I32, W >= ceil(T / 32), written: bit j of row (b, t)
+ *                          set when j = t or j is an ancestor of t; rows
+ *                          t >= draft_lens[b] are zero
+ *   depths      [B, T]     I32 or NULL, written: 0 for a child of the committed
+ *                          context, a parent's depth + 1 otherwise, -1 for rows
+ *                          t >= draft_lens[b].  The token's position is
+ *                          seq_lens[b] - draft_lens[b] + depth
+ *
+ * A parent outside -1 .. t - 1 is taken as -1 and records FW_ERR_INVALID_ARG in
+ * the device status word.  1 <= T <= 256.  One launch, no workspace.
+ */
+fw_status_t fw_tree_mask(const fw_tensor_t *parents, const fw_tensor_t *draft_lens, fw_tensor_t *tree_mask,
+                         fw_tensor_t *depths, fw_stream_t stream);
+
+/*
+ * Block table and slot map of a step, from request lengths.
+ *
+ *   seq_lens    [B]  I32   keys each request holds after the step, its new tokens
+ *                          included; 0: it has left and gives its pages back
+ *   new_lens    [B]  I32   its new tokens of the step, the last of seq_lens
+ *   held        [B]  I32   pages in its table row before the step
+ *   free_queue  [F]  I32   ring of free physical pages; pages are taken from its
+ *                          front, returned pages are written behind its end
+ *   free_range  [2]  I32   the ring's first entry and number of entries
+ *   page_size              1 .. 2^20
+ *   block_table [B, max_pages]  I32, rows contiguous; updated in place
+ *   slot_mapping           I32, written: [N] packs the new tokens request by
+ *                          request (position i of request b at cu_new[b] + i);
+ *                          [B, L] gives every request L places (contiguous)
+ *   cu_new      [B + 1]    I32 or NULL, written: prefix sums of new_lens
+ *   held_out    [B]        I32, written: pages held after the step; may be held
+ *   range_out   [2]        I32, written: the ring after the step; may be free_range
+ *
+ * Request b wants ceil(seq_lens[b] / page_size) pages.  What it lacks it takes
+ * from the ring, requests in order, logical pages in order; what it holds beyond
+ * that goes behind the ring's end in the same order and can be taken from the
+ * next step on (its table entries stay as they are).  A request is served when
+ * the pages asked for up to and including its own are there; one that is not
+ * keeps its table row and held count, its slots are -1, and FW_ERR_WORKSPACE is
+ * recorded in the device status word.
+ *
+ * A slot is page * page_size + offset, what fw_kv_append takes.  Places without
+ * a token (slot_mapping beyond the last token, or beyond new_lens[b] of a row)
+ * get -1, which fw_kv_append writes to the layer's row 0: keep page 0 out of the
+ * ring where a step has such places.
+ *
+ * Inputs that contradict each other (a length below zero or beyond the table
+ * row, new_lens above seq_lens, held outside 0 .. max_pages, more tokens than
+ * places, a page whose slots pass 2^31, a ring outside its array) record
+ * FW_ERR_INVALID_ARG: such a request keeps its row and gets slots -1, tokens
+ * without a place are dropped, pages the ring cannot take stay held, and a bad
+ * range serves nobody.  B <= 16384.  One launch, two when held_out or range_out
+ * overlap their inputs.  No workspace.
+ */
+fw_status_t fw_build_page_tables(const fw_tensor_t *seq_lens, const fw_tensor_t *new_lens, const fw_tensor_t *held,
+                                 fw_tensor_t *free_queue, const fw_tensor_t *free_range, int64_t page_size,
+                                 fw_tensor_t *block_table, fw_tensor_t *slot_mapping, fw_tensor_t *cu_new,
+                                 fw_tensor_t *held_out, fw_tensor_t *range_out, fw_stream_t stream);
+
+/*
+ * Moves the accepted path's keys and values to where ordinary tokens lie.
+ *
+ *   path        [B, A]  I32, rows contiguous: the accepted drafts of request b,
+ *                       tree nodes from the root down (strictly increasing)
+ *   path_lens   [B]     I32: how many are accepted, 0 .. A
+ *   base_lens   [B]     I32: committed keys of the request, i.e. the position of
+ *                       its draft 0
+ *   block_table [B, max_pages]  I32, entries counted from a layer's first page
+ *   num_layers          the caches hold this many layers of pages / num_layers
+ *                       pages each, one after another
+ *   k_cache, v_cache    [pages, ps, Hkv, D]  BF16 or FP8_E4M3 (both the same),
+ *                       D a multiple of 8 (FP8: 16), moved in place; v_cache may
+ *                       be NULL (a latent cache whose values are a view of its
+ *                       keys)
+ *   new_lens    [B]     I32 or NULL, written: base_lens[b] + path_lens[b], the
+ *                       committed keys after the move
+ *
+ * For i < path_lens[b], position base_lens[b] + i of every layer takes what
+ * position base_lens[b] + path[b, i] held before the call; nothing else changes.
+ * A path that does not increase, reaches past the table row, or has a length
+ * outside 0 .. A, and a page outside the layer, record FW_ERR_INVALID_ARG in the
+ * device status word; that request's rows then stay as they are and its new
+ * length is base_lens[b].  Two requests must not share a page that a path
+ * touches.  One launch, no workspace.
+ */
+fw_status_t fw_kv_commit(const fw_tensor_t *path, const fw_tensor_t *path_lens, const fw_tensor_t *base_lens,
+                         const fw_tensor_t *block_table, int64_t num_layers, fw_tensor_t *k_cache,
+                         fw_tensor_t *v_cache, fw_tensor_t *new_lens, fw_stream_t stream);
+
+/*
  * Caller-owned workspace for the CURRENT device (ptr = NULL, bytes = 0 returns
  * to the internal buffer).  The library never frees it.  Calls on one device
  * that share the workspace must be ordered (same stream, or synchronised).

@@ -10,5 +10,7 @@ from ._binding import (FW_ERR_DEVICE_TIMEOUT, FwError, device_status, kernel_tim
                        paged_decode_masked, paged_decode_window, paged_decode_workspace_size, plan_decode,
                        read_counters, set_option,
                        set_workspace, varlen_prefill)
+from ._binding import (build_page_tables, kv_commit, paged_decode_tree, paged_decode_tree_workspace_size,  # noqa: F401
+                       tree_mask)
 from ._binding import (FW_OPT_DECODE_CHUNK_TOKENS, FW_OPT_KERNEL_TIMING, FW_OPT_MAX_CTAS,  # noqa: F401
                        FW_OPT_PREFILL_SOFTMAX, FW_OPT_TEST_STALL, FW_OPT_WAIT_TIMEOUT_MS)

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -102,6 +103,17 @@ def load_library(path: Optional[str] = None):
     lib.fw_plan_decode.restype = S
     lib.fw_plan_decode.argtypes = [ctypes.c_int32] * 5 + [ctypes.c_int64, ctypes.c_int32,
                                                           ctypes.POINTER(FwDecodePlan)]
+    V, SZ, I32, I64, F = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
+    lib.fw_paged_decode_tree.restype = S
+    lib.fw_paged_decode_tree.argtypes = [V, V, V, V, V, V, V, F, F, F, V, V, V, SZ, V]
+    lib.fw_paged_decode_tree_workspace_size.restype = S
+    lib.fw_paged_decode_tree_workspace_size.argtypes = [I32, ctypes.POINTER(SZ)]
+    lib.fw_tree_mask.restype = S
+    lib.fw_tree_mask.argtypes = [V, V, V, V, V]
+    lib.fw_build_page_tables.restype = S
+    lib.fw_build_page_tables.argtypes = [V, V, V, V, V, I64, V, V, V, V, V, V]
+    lib.fw_kv_commit.restype = S
+    lib.fw_kv_commit.argtypes = [V, V, V, V, I64, V, V, V, V]
     _lib = lib
     return lib
 
@@ -289,6 +301,167 @@ def varlen_prefill(q, k, v, cu_seqlens_q, cu_seqlens_k, causal, scale, out=None,
     _check(lib.fw_varlen_prefill(*[_ref(a) for a in args], int(bool(causal)), ctypes.c_float(scale),
                                  _ref(fo), _ref(fl), _stream_handle(stream)))
     return out, lse
+
+
+# ------------------------------------------------------ speculative decoding
+#
+# These run on the device of their tensors, whichever is current, and their
+# outputs and workspaces are allocated on the stream the kernels run on.
+
+_TENSOR = struct.Struct("=Qii10q")          # fw_tensor_t
+_PAD = tuple((0,) * (5 - i) for i in range(6))
+
+
+def _pack(tensors):
+    """fw_tensor_t records of the tensors in one buffer: (buffer, addresses);
+    None -> NULL.  One packing call per tensor: these entry points serve steps
+    of a few microseconds."""
+    buf = ctypes.create_string_buffer(_TENSOR.size * len(tensors))
+    base = ctypes.addressof(buf)
+    ptrs = []
+    for i, t in enumerate(tensors):
+        if t is None:
+            ptrs.append(None)
+            continue
+        code = _DTYPES.get(t.dtype)
+        if code is None:
+            raise TypeError(f"unsupported dtype {t.dtype}")
+        nd = t.dim()
+        if nd > 5:
+            raise ValueError("at most 5 dimensions")
+        pad = _PAD[nd]
+        _TENSOR.pack_into(buf, _TENSOR.size * i, t.data_ptr() if t.numel() else 0, code, nd, *t.shape, *pad,
+                          *t.stride(), *pad)
+        ptrs.append(base + _TENSOR.size * i)
+    return buf, ptrs
+
+
+class _Launch:
+    """Device and stream of a call: the tensors' device becomes current, and so
+    does `stream` when one is given; the with-value is the stream's handle."""
+
+    def __init__(self, stream, tensors):
+        dev = None
+        for t in tensors:
+            if t is None:
+                continue
+            i = t.get_device()
+            if i < 0:
+                raise ValueError("the tensors must be on a CUDA device")
+            if dev is None:
+                dev = i
+            elif i != dev:
+                raise ValueError("the tensors must be on one device")
+        if stream is not None and stream.device.index != dev:
+            raise ValueError("the stream must be of the tensors' device")
+        self.dev, self.stream, self.scopes = dev, stream, []
+
+    def __enter__(self):
+        if self.dev != torch.cuda.current_device():
+            self.scopes.append(torch.cuda.device(self.dev))
+        if self.stream is not None:
+            self.scopes.append(torch.cuda.stream(self.stream))
+        for s in self.scopes:
+            s.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        for s in reversed(self.scopes):
+            s.__exit__(*exc)
+
+
+_tree_workspace = {}                        # (device, head dim) -> bytes
+
+
+def paged_decode_tree_workspace_size(head_dim) -> int:
+    """Workspace bytes of paged_decode_tree on the current device."""
+    n = ctypes.c_size_t(0)
+    _check(load_library().fw_paged_decode_tree_workspace_size(int(head_dim), ctypes.byref(n)))
+    return n.value
+
+
+def paged_decode_tree(q, k_cache, v_cache, block_table, seq_lens, tree_mask, scale, draft_lens=None, k_scale=1.0,
+                      v_scale=1.0, out=None, lse=None, return_lse=True, workspace=None, stream=None):
+    """fw_paged_decode_tree: the drafts of every request ([B, T, Hq, D], the last
+    draft_lens[b] (None: T) of its seq_lens[b] keys) attend to the committed keys
+    and to the drafts their tree_mask row [B, T, W] names; BF16 or FP8 E4M3
+    caches.  workspace: bytes for the split partials (None: a fresh buffer from
+    torch's allocator, so calls on several streams and captured graphs share
+    nothing).  Returns (out [B, T, Hq, D] bf16, lse [B, T, Hq] f32 or None)."""
+    lib = load_library()
+    with _Launch(stream, (q, k_cache, v_cache, block_table, seq_lens, tree_mask, draft_lens, out, lse,
+                          workspace)) as handle:
+        if out is None:
+            out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        if lse is None and return_lse:
+            lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+        if workspace is None:
+            key = (q.device.index, q.shape[-1])
+            need = _tree_workspace.get(key)
+            if need is None:
+                need = _tree_workspace[key] = paged_decode_tree_workspace_size(q.shape[-1])
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        elif not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        buf, a = _pack((q, k_cache, v_cache, block_table, seq_lens, tree_mask, draft_lens, out, lse))
+        _check(lib.fw_paged_decode_tree(a[0], a[1], a[2], a[3], a[4], a[5], a[6], float(scale), float(k_scale),
+                                        float(v_scale), a[7], a[8],
+                                        workspace.data_ptr(), workspace.numel() * workspace.element_size(), handle))
+    return out, lse
+
+
+def tree_mask(parents, draft_lens=None, mask=None, depths=None, stream=None):
+    """fw_tree_mask: parents [B, T] (-1: child of the committed context) to
+    (mask [B, T, ceil(T / 32)] i32 of each draft's ancestors and itself, depths
+    [B, T] i32)."""
+    lib = load_library()
+    with _Launch(stream, (parents, draft_lens, mask, depths)) as handle:
+        if parents.dim() != 2:
+            raise ValueError("parents must be [B, T]")
+        B, T = parents.shape
+        if mask is None:
+            mask = torch.empty((B, T, (T + 31) // 32), dtype=torch.int32, device=parents.device)
+        if depths is None:
+            depths = torch.empty((B, T), dtype=torch.int32, device=parents.device)
+        buf, a = _pack((parents, draft_lens, mask, depths))
+        _check(lib.fw_tree_mask(a[0], a[1], a[2], a[3], handle))
+    return mask, depths
+
+
+def build_page_tables(seq_lens, new_lens, held, free_queue, free_range, page_size, block_table, slot_mapping,
+                      cu_new=None, held_out=None, range_out=None, stream=None):
+    """fw_build_page_tables: takes and returns pages of the ring free_queue
+    [F] / free_range [2], updates block_table [B, max_pages] and writes the
+    step's slot_mapping ([N] packed or [B, L]).  Returns (cu_new [B + 1],
+    held_out [B], range_out [2]); the last two may be held and free_range."""
+    lib = load_library()
+    with _Launch(stream, (seq_lens, new_lens, held, free_queue, free_range, block_table, slot_mapping, cu_new,
+                          held_out, range_out)) as handle:
+        if cu_new is None:
+            cu_new = torch.empty(seq_lens.numel() + 1, dtype=torch.int32, device=seq_lens.device)
+        if held_out is None:
+            held_out = torch.empty(seq_lens.numel(), dtype=torch.int32, device=seq_lens.device)
+        if range_out is None:
+            range_out = torch.empty(2, dtype=torch.int32, device=seq_lens.device)
+        buf, a = _pack((seq_lens, new_lens, held, free_queue, free_range, block_table, slot_mapping, cu_new, held_out,
+                        range_out))
+        _check(lib.fw_build_page_tables(a[0], a[1], a[2], a[3], a[4], int(page_size), a[5], a[6], a[7], a[8], a[9],
+                                        handle))
+    return cu_new, held_out, range_out
+
+
+def kv_commit(path, path_lens, base_lens, block_table, k_cache, v_cache, num_layers=1, new_lens=None, stream=None):
+    """fw_kv_commit: position base_lens[b] + i of every layer takes the rows of
+    position base_lens[b] + path[b, i], i < path_lens[b], in place (path
+    strictly increasing; v_cache may be None).  Returns new_lens [B] =
+    base_lens + path_lens."""
+    lib = load_library()
+    with _Launch(stream, (path, path_lens, base_lens, block_table, k_cache, v_cache, new_lens)) as handle:
+        if new_lens is None:
+            new_lens = torch.empty(path_lens.numel(), dtype=torch.int32, device=path.device)
+        buf, a = _pack((path, path_lens, base_lens, block_table, k_cache, v_cache, new_lens))
+        _check(lib.fw_kv_commit(a[0], a[1], a[2], a[3], int(num_layers), a[4], a[5], a[6], handle))
+    return new_lens
 
 
 def set_workspace(buf: Optional[torch.Tensor], stream=None):

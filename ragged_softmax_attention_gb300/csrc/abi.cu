@@ -947,3 +947,371 @@ fw_status_t fw_varlen_prefill(const fw_tensor_t *q, const fw_tensor_t *k, const 
 }
 
 }  // extern "C"
+
+// ------------------------------------------------------- speculative decoding
+
+// A contiguous [n] I32 vector.
+static fw_status_t check_vector(const fw_tensor_t *t, const char *name, int64_t n, bool allow_null = false) {
+    if (!t) return allow_null ? FW_OK : fail(FW_ERR_INVALID_ARG, "%s is NULL", name);
+    if (fw_status_t s = check_tensor(t, name, 1, FW_I32)) return s;
+    if (t->shape[0] != n) return fail(FW_ERR_INVALID_ARG, "%s must hold %lld entries, not %lld", name, (long long)n,
+                                      (long long)t->shape[0]);
+    if (n > 0 && reinterpret_cast<uintptr_t>(t->data) % 4) return fail(FW_ERR_INVALID_ARG, "%s misaligned", name);
+    return FW_OK;
+}
+
+// An I32 matrix or stack of matrices whose last dimension is contiguous.
+static fw_status_t check_i32(const fw_tensor_t *t, const char *name, int ndim) {
+    if (fw_status_t s = check_tensor(t, name, ndim, FW_I32)) return s;
+    if (t->data && reinterpret_cast<uintptr_t>(t->data) % 4) return fail(FW_ERR_INVALID_ARG, "%s misaligned", name);
+    return FW_OK;
+}
+
+// Bytes from the tensor's first element to one past its last.
+static int64_t extent_bytes(const fw_tensor_t *t, int64_t esz) {
+    int64_t e = 1;
+    for (int i = 0; i < t->ndim; ++i) {
+        if (t->shape[i] == 0) return 0;
+        e += (t->shape[i] - 1) * t->stride[i];
+    }
+    return e * esz;
+}
+
+static bool overlap(const fw_tensor_t *a, int64_t esz_a, const fw_tensor_t *b, int64_t esz_b) {
+    const char *pa = static_cast<const char *>(a->data), *pb = static_cast<const char *>(b->data);
+    return pa < pb + extent_bytes(b, esz_b) && pb < pa + extent_bytes(a, esz_a);
+}
+
+// Whether two [pages, ps, Hkv, D] caches share an element.  Views into one
+// buffer (K and V halves of every page, say) have interleaved extents and no
+// common element, so with equal strides the distance between the bases is
+// looked up among the distances the strides can make; for unequal strides
+// overlapping extents count as shared.
+static bool caches_share(const fw_tensor_t *a, const fw_tensor_t *b, int64_t esz) {
+    if (!overlap(a, esz, b, esz)) return false;
+    for (int i = 0; i < 3; ++i)
+        if (a->stride[i] != b->stride[i]) return true;
+    const int64_t row = (a->shape[3] > b->shape[3] ? a->shape[3] : b->shape[3]) * esz;
+    int64_t rest = static_cast<const char *>(b->data) - static_cast<const char *>(a->data);
+    if (rest < 0) rest = -rest;
+    // the three strides, longest first
+    int order[3] = {0, 1, 2};
+    for (int i = 0; i < 3; ++i)
+        for (int j = i + 1; j < 3; ++j)
+            if (a->stride[order[j]] > a->stride[order[i]]) { const int x = order[i]; order[i] = order[j]; order[j] = x; }
+    // Nested strides leave two candidates a level: the multiple below and above.
+    for (int up = 0; up < 8; ++up) {
+        int64_t r = rest;
+        bool can = true;
+        for (int l = 0; l < 3; ++l) {
+            const int64_t s = a->stride[order[l]] * esz, ext = a->shape[order[l]];
+            if (s == 0 || ext <= 1) continue;
+            int64_t k = r / s;
+            if (r % s != 0 && r < 0) --k;
+            if (up >> l & 1) ++k;
+            if (k <= -ext || k >= ext) { can = false; break; }
+            r -= k * s;
+        }
+        if (can && r > -row && r < row) return true;
+    }
+    return false;
+}
+
+// Validates a tree decode and fills the kernel's parameters.
+static fw_status_t build_tree(const fw_tensor_t *q, const fw_tensor_t *k_cache, const fw_tensor_t *v_cache,
+                              const fw_tensor_t *block_table, const fw_tensor_t *seq_lens,
+                              const fw_tensor_t *tree_mask, const fw_tensor_t *draft_lens, float scale, float k_scale,
+                              float v_scale, const fw_tensor_t *out, const fw_tensor_t *lse, fw::TreeParams *tp) {
+    if (fw_status_t s = decode_shapes(q, k_cache, v_cache, block_table)) return s;
+    const bool kv8 = k_cache->dtype == FW_FP8_E4M3;
+    const int64_t B = q->shape[0], T = q->shape[1], Hq = q->shape[2], D = q->shape[3];
+    const int64_t P = k_cache->shape[0], ps = k_cache->shape[1], Hkv = k_cache->shape[2];
+    const int64_t max_pages = block_table->shape[1];
+    if (v_cache->shape[3] != D) return fail(FW_ERR_UNSUPPORTED, "tree decode needs values as wide as keys (%lld, not %lld)",
+                                            (long long)D, (long long)v_cache->shape[3]);
+    if (!(D == 128 || (D == 256 && !kv8)))
+        return fail(FW_ERR_UNSUPPORTED, "tree decode head dim %lld: supported 128 and 256 (FP8 caches: 128)", (long long)D);
+    if (!kv8 && (k_scale != 1.f || v_scale != 1.f))
+        return fail(FW_ERR_INVALID_ARG, "k_scale and v_scale must be 1 for BF16 caches");
+    if (!(std::isfinite(k_scale) && std::isfinite(v_scale) && k_scale > 0.f && v_scale > 0.f))
+        return fail(FW_ERR_INVALID_ARG, "k_scale and v_scale must be finite and positive");
+    if (!std::isfinite(scale)) return fail(FW_ERR_INVALID_ARG, "scale must be finite");
+    if (fw_status_t s = check_vector(seq_lens, "seq_lens", B)) return s;
+    if (fw_status_t s = check_vector(draft_lens, "draft_lens", B, true)) return s;
+    if (fw_status_t s = check_i32(block_table, "block_table", 2)) return s;
+    if (fw_status_t s = check_i32(tree_mask, "tree_mask", 3)) return s;
+    if (fw_status_t s = check_tensor(out, "out", 4, FW_BF16)) return s;
+    if (fw_status_t s = check_tensor(lse, "lse", 3, FW_F32, true)) return s;
+    if (T < 1 || T > 256) return fail(FW_ERR_UNSUPPORTED, "a tree holds 1 to 256 drafts, not %lld", (long long)T);
+    if (B > 4096) return fail(FW_ERR_UNSUPPORTED, "tree decode serves up to 4096 requests, not %lld", (long long)B);
+    if (tree_mask->shape[0] != B || tree_mask->shape[1] != T || tree_mask->shape[2] < (T + 31) / 32)
+        return fail(FW_ERR_INVALID_ARG, "tree_mask must be [B, T, W] with W >= %lld words", (long long)((T + 31) / 32));
+    if (out->shape[0] != B || out->shape[1] != T || out->shape[2] != Hq || out->shape[3] != D)
+        return fail(FW_ERR_INVALID_ARG, "out must be [B, T, Hq, D]");
+    if (lse && (lse->shape[0] != B || lse->shape[1] != T || lse->shape[2] != Hq))
+        return fail(FW_ERR_INVALID_ARG, "lse must be [B, T, Hq]");
+    if (!supported_page_size(ps))
+        return fail(FW_ERR_UNSUPPORTED, "page size %lld: supported 8, 16, 32, 64, 128 or multiples of 128", (long long)ps);
+    if (B > 0) {
+        if (Hq < 1) return fail(FW_ERR_INVALID_ARG, "no query heads");
+        if (P < 1 || max_pages < 1) return fail(FW_ERR_INVALID_ARG, "empty page pool or block table");
+        if (P > (1LL << 31) - 1 || max_pages * ps > (1LL << 30))
+            return fail(FW_ERR_UNSUPPORTED, "page pool or sequence bound too large");
+        if (B * T * Hq >= (1LL << 31)) return fail(FW_ERR_UNSUPPORTED, "too many query rows");
+        if (fw_status_t s = check_tma_layout(q, "q")) return s;
+        if (fw_status_t s = check_tma_layout(k_cache, "k_cache")) return s;
+        if (fw_status_t s = check_tma_layout(v_cache, "v_cache")) return s;
+        if (fw_status_t s = check_tma_layout(out, "out")) return s;
+        if (lse && reinterpret_cast<uintptr_t>(lse->data) % 4) return fail(FW_ERR_INVALID_ARG, "lse misaligned");
+    }
+    fw::TreeParams p{};
+    p.B = (int)B; p.T = (int)T; p.Hq = (int)Hq; p.Hkv = (int)Hkv; p.G = (int)(Hq / Hkv); p.D = (int)D;
+    p.ps = (int)ps; p.max_pages = (int)max_pages; p.num_pages = (int)P;
+    p.kv8 = kv8 ? 1 : 0;
+    p.q = static_cast<const uint16_t *>(q->data);
+    p.k_cache = k_cache->data;
+    p.v_cache = v_cache->data;
+    for (int i = 0; i < 3; ++i) {
+        p.q_stride[i] = q->stride[i];
+        p.kc_stride[i] = k_cache->stride[i];
+        p.vc_stride[i] = v_cache->stride[i];
+        p.out_stride[i] = out->stride[i];
+        p.lse_stride[i] = lse ? lse->stride[i] : 0;
+    }
+    p.block_table = static_cast<const int32_t *>(block_table->data);
+    p.bt_stride = block_table->stride[0];
+    p.seq_lens = static_cast<const int32_t *>(seq_lens->data);
+    p.draft_lens = draft_lens ? static_cast<const int32_t *>(draft_lens->data) : nullptr;
+    p.mask = static_cast<const int32_t *>(tree_mask->data);
+    p.mask_stride[0] = tree_mask->stride[0];
+    p.mask_stride[1] = tree_mask->stride[1];
+    p.out = out->data;
+    p.lse = lse ? static_cast<float *>(lse->data) : nullptr;
+    p.scale_log2 = scale * k_scale * 1.4426950408889634f;
+    p.out_scale = v_scale;
+    *tp = p;
+    return FW_OK;
+}
+
+extern "C" {
+
+fw_status_t fw_paged_decode_tree_workspace_size(int32_t head_dim, size_t *bytes) {
+    if (!bytes) return fail(FW_ERR_INVALID_ARG, "bytes is NULL");
+    if (head_dim != 128 && head_dim != 256) return fail(FW_ERR_UNSUPPORTED, "tree decode head dim %d", head_dim);
+    std::lock_guard<std::mutex> lk(g_mu);
+    DeviceState *d = nullptr;
+    if (fw_status_t s = device_state(&d)) return s;
+    *bytes = 0;
+    return ok();
+}
+
+fw_status_t fw_paged_decode_tree(const fw_tensor_t *q, const fw_tensor_t *k_cache, const fw_tensor_t *v_cache,
+                                 const fw_tensor_t *block_table, const fw_tensor_t *seq_lens,
+                                 const fw_tensor_t *tree_mask, const fw_tensor_t *draft_lens, float scale,
+                                 float k_scale, float v_scale, fw_tensor_t *out, fw_tensor_t *lse,
+                                 void *workspace, size_t workspace_bytes, fw_stream_t stream_) {
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    fw::TreeParams p{};
+    if (fw_status_t s = build_tree(q, k_cache, v_cache, block_table, seq_lens, tree_mask, draft_lens, scale, k_scale,
+                                   v_scale, out, lse, &p))
+        return s;
+    if (p.B == 0) return ok();
+    std::lock_guard<std::mutex> lk(g_mu);
+    DeviceState *d = nullptr;
+    if (fw_status_t s = device_state(&d)) return s;
+    (void)workspace;
+    (void)workspace_bytes;
+    p.status = d->status;
+    int launched = 0;
+    cudaError_t e = fw::launch_tree_decode(p, stream, &launched);
+    g_launches.fetch_add(launched);
+    if (e != cudaSuccess) return fail(FW_ERR_CUDA, "tree decode launch: %s", cudaGetErrorString(e));
+    return ok();
+}
+
+fw_status_t fw_tree_mask(const fw_tensor_t *parents, const fw_tensor_t *draft_lens, fw_tensor_t *tree_mask,
+                         fw_tensor_t *depths, fw_stream_t stream_) {
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    if (fw_status_t s = check_i32(parents, "parents", 2)) return s;
+    const int64_t B = parents->shape[0], T = parents->shape[1];
+    if (fw_status_t s = check_vector(draft_lens, "draft_lens", B, true)) return s;
+    if (fw_status_t s = check_i32(tree_mask, "tree_mask", 3)) return s;
+    if (depths)
+        if (fw_status_t s = check_i32(depths, "depths", 2)) return s;
+    if (T < 1 || T > 256) return fail(FW_ERR_UNSUPPORTED, "a tree holds 1 to 256 drafts, not %lld", (long long)T);
+    if (tree_mask->shape[0] != B || tree_mask->shape[1] != T || tree_mask->shape[2] < (T + 31) / 32)
+        return fail(FW_ERR_INVALID_ARG, "tree_mask must be [B, T, W] with W >= %lld words", (long long)((T + 31) / 32));
+    if (tree_mask->shape[2] > 4096) return fail(FW_ERR_UNSUPPORTED, "tree_mask rows of more than 4096 words");
+    if (depths && (depths->shape[0] != B || depths->shape[1] != T))
+        return fail(FW_ERR_INVALID_ARG, "depths must be [B, T]");
+    if (B >= (1LL << 31)) return fail(FW_ERR_UNSUPPORTED, "too many trees");
+    if (B == 0) return ok();
+    fw::TreeMaskParams p{};
+    p.B = (int)B; p.T = (int)T; p.W = (int)tree_mask->shape[2];
+    p.parents = static_cast<const int32_t *>(parents->data);
+    p.parent_stride = parents->stride[0];
+    p.draft_lens = draft_lens ? static_cast<const int32_t *>(draft_lens->data) : nullptr;
+    p.mask = static_cast<int32_t *>(tree_mask->data);
+    p.mask_stride[0] = tree_mask->stride[0];
+    p.mask_stride[1] = tree_mask->stride[1];
+    p.depths = depths ? static_cast<int32_t *>(depths->data) : nullptr;
+    p.depth_stride = depths ? depths->stride[0] : 0;
+    std::lock_guard<std::mutex> lk(g_mu);
+    DeviceState *d = nullptr;
+    if (fw_status_t s = device_state(&d)) return s;
+    p.status = d->status;
+    cudaError_t e = fw::launch_tree_mask(p, stream);
+    if (e != cudaSuccess) return fail(FW_ERR_CUDA, "tree mask launch: %s", cudaGetErrorString(e));
+    g_launches.fetch_add(1);
+    return ok();
+}
+
+fw_status_t fw_build_page_tables(const fw_tensor_t *seq_lens, const fw_tensor_t *new_lens, const fw_tensor_t *held,
+                                 fw_tensor_t *free_queue, const fw_tensor_t *free_range, int64_t page_size,
+                                 fw_tensor_t *block_table, fw_tensor_t *slot_mapping, fw_tensor_t *cu_new,
+                                 fw_tensor_t *held_out, fw_tensor_t *range_out, fw_stream_t stream_) {
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    if (fw_status_t s = check_i32(block_table, "block_table", 2)) return s;
+    const int64_t B = block_table->shape[0], max_pages = block_table->shape[1];
+    if (fw_status_t s = check_vector(seq_lens, "seq_lens", B)) return s;
+    if (fw_status_t s = check_vector(new_lens, "new_lens", B)) return s;
+    if (fw_status_t s = check_vector(held, "held", B)) return s;
+    if (fw_status_t s = check_vector(held_out, "held_out", B)) return s;
+    if (fw_status_t s = check_vector(cu_new, "cu_new", B + 1, true)) return s;
+    if (fw_status_t s = check_vector(free_range, "free_range", 2)) return s;
+    if (fw_status_t s = check_vector(range_out, "range_out", 2)) return s;
+    if (!free_queue) return fail(FW_ERR_INVALID_ARG, "free_queue is NULL");
+    if (fw_status_t s = check_vector(free_queue, "free_queue", free_queue->shape[0])) return s;
+    if (!slot_mapping || slot_mapping->ndim < 1 || slot_mapping->ndim > 2)
+        return fail(FW_ERR_INVALID_ARG, "slot_mapping must be an I32 [N] or [B, L] tensor");
+    if (fw_status_t s = check_i32(slot_mapping, "slot_mapping", slot_mapping->ndim)) return s;
+    const bool padded = slot_mapping->ndim == 2;
+    if (padded && (slot_mapping->shape[0] != B ||
+                   (B > 1 && slot_mapping->shape[1] > 0 && slot_mapping->stride[0] != slot_mapping->shape[1])))
+        return fail(FW_ERR_INVALID_ARG, "a padded slot_mapping must be contiguous [B, L]");
+    if (page_size < 1 || page_size > (1 << 20)) return fail(FW_ERR_INVALID_ARG, "page size must be 1 to 2^20");
+    const int64_t F = free_queue->shape[0];
+    const int64_t N = padded ? B * slot_mapping->shape[1] : slot_mapping->shape[0];
+    if (B > 16384) return fail(FW_ERR_UNSUPPORTED, "page tables of up to 16384 requests, not %lld", (long long)B);
+    if (F < 1 || F > (1LL << 30)) return fail(FW_ERR_UNSUPPORTED, "a ring of 1 to 2^30 pages");
+    if (N >= (1LL << 31) || max_pages > (1LL << 30)) return fail(FW_ERR_UNSUPPORTED, "too many places or table columns");
+    const fw_tensor_t *outs[] = {block_table, slot_mapping, cu_new, held_out, range_out, free_queue};
+    const fw_tensor_t *ins[] = {seq_lens, new_lens, held, free_range};
+    const char *names[] = {"block_table", "slot_mapping", "cu_new", "held_out", "range_out", "free_queue"};
+    for (int i = 0; i < 6; ++i) {
+        if (!outs[i]) continue;
+        for (int j = 0; j < 4; ++j) {
+            if ((i == 3 && j == 2) || (i == 4 && j == 3)) continue;     // these may be their inputs
+            if (overlap(outs[i], 4, ins[j], 4))
+                return fail(FW_ERR_INVALID_ARG, "%s overlaps an input", names[i]);
+        }
+        for (int j = 0; j < i; ++j)
+            if (outs[j] && overlap(outs[i], 4, outs[j], 4))
+                return fail(FW_ERR_INVALID_ARG, "%s overlaps %s", names[i], names[j]);
+    }
+    fw::PageTableParams p{};
+    p.B = (int)B; p.max_pages = (int)max_pages; p.F = (int)F; p.ps = (int)page_size;
+    p.L = padded ? (int)slot_mapping->shape[1] : 0;
+    p.N = (int)N;
+    p.padded = padded ? 1 : 0;
+    p.seq_lens = static_cast<const int32_t *>(seq_lens->data);
+    p.new_lens = static_cast<const int32_t *>(new_lens->data);
+    p.held = static_cast<const int32_t *>(held->data);
+    p.queue = static_cast<int32_t *>(free_queue->data);
+    p.range = static_cast<const int32_t *>(free_range->data);
+    p.table = static_cast<int32_t *>(block_table->data);
+    p.table_stride = block_table->stride[0];
+    p.slots = static_cast<int32_t *>(slot_mapping->data);
+    p.cu_new = cu_new ? static_cast<int32_t *>(cu_new->data) : nullptr;
+    p.held_out = static_cast<int32_t *>(held_out->data);
+    p.range_out = static_cast<int32_t *>(range_out->data);
+    p.in_place = overlap(held_out, 4, held, 4) || overlap(range_out, 4, free_range, 4);
+    std::lock_guard<std::mutex> lk(g_mu);
+    DeviceState *d = nullptr;
+    if (fw_status_t s = device_state(&d)) return s;
+    p.num_sms = d->num_sms;
+    p.status = d->status;
+    int launched = 0;
+    cudaError_t e = fw::launch_page_tables(p, stream, &launched);
+    g_launches.fetch_add(launched);
+    if (e != cudaSuccess) return fail(FW_ERR_CUDA, "page table launch: %s", cudaGetErrorString(e));
+    return ok();
+}
+
+fw_status_t fw_kv_commit(const fw_tensor_t *path, const fw_tensor_t *path_lens, const fw_tensor_t *base_lens,
+                         const fw_tensor_t *block_table, int64_t num_layers, fw_tensor_t *k_cache,
+                         fw_tensor_t *v_cache, fw_tensor_t *new_lens, fw_stream_t stream_) {
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    if (fw_status_t s = check_i32(path, "path", 2)) return s;
+    const int64_t B = path->shape[0], A = path->shape[1];
+    if (fw_status_t s = check_vector(path_lens, "path_lens", B)) return s;
+    if (fw_status_t s = check_vector(base_lens, "base_lens", B)) return s;
+    if (fw_status_t s = check_vector(new_lens, "new_lens", B, true)) return s;
+    if (fw_status_t s = check_i32(block_table, "block_table", 2)) return s;
+    if (block_table->shape[0] != B) return fail(FW_ERR_INVALID_ARG, "block_table rows != batch");
+    if (!k_cache) return fail(FW_ERR_INVALID_ARG, "k_cache is NULL");
+    const bool kv8 = k_cache->dtype == FW_FP8_E4M3;
+    if (!kv8 && k_cache->dtype != FW_BF16) return fail(FW_ERR_INVALID_ARG, "caches must be BF16 or FP8_E4M3");
+    if (fw_status_t s = check_tensor(k_cache, "k_cache", 4, k_cache->dtype)) return s;
+    const int64_t P = k_cache->shape[0], ps = k_cache->shape[1], Hkv = k_cache->shape[2];
+    const int64_t esz = kv8 ? 1 : 2;
+    if (v_cache) {
+        if (fw_status_t s = check_tensor(v_cache, "v_cache", 4, k_cache->dtype)) return s;
+        if (v_cache->shape[0] != P || v_cache->shape[1] != ps || v_cache->shape[2] != Hkv)
+            return fail(FW_ERR_INVALID_ARG, "v_cache [pages, ps, Hkv] must match k_cache");
+    }
+    if (P < 1 || ps < 1 || Hkv < 1) return fail(FW_ERR_INVALID_ARG, "empty cache");
+    const int64_t Dk = k_cache->shape[3], Dv = v_cache ? v_cache->shape[3] : 0;
+    if (Dk < 1 || Dk * esz % 16 || Dv * esz % 16 || (v_cache && Dv < 1))
+        return fail(FW_ERR_UNSUPPORTED, "moved head rows must be multiples of 16 bytes");
+    if (num_layers < 1 || num_layers > 65535 || P % num_layers)
+        return fail(FW_ERR_INVALID_ARG, "%lld pages do not make %lld layers (1 to 65535)", (long long)P,
+                    (long long)num_layers);
+    const int64_t max_pages = block_table->shape[1];
+    if (max_pages * ps > (1LL << 30) || P >= (1LL << 31) || ps > (1LL << 30))
+        return fail(FW_ERR_UNSUPPORTED, "page pool or sequence bound too large");
+    if (Hkv * (Dk + Dv) > (1LL << 24) || B >= (1LL << 31)) return fail(FW_ERR_UNSUPPORTED, "rows or batch too large");
+    if (A > 256) return fail(FW_ERR_UNSUPPORTED, "paths of up to 256 drafts, not %lld", (long long)A);
+    if (fw_status_t s = check_tma_layout(k_cache, "k_cache")) return s;
+    if (v_cache) {
+        if (fw_status_t s = check_tma_layout(v_cache, "v_cache")) return s;
+        if (caches_share(k_cache, v_cache, esz))
+            return fail(FW_ERR_INVALID_ARG, "v_cache shares elements with k_cache: move the keys alone (v_cache NULL)");
+    }
+    if (new_lens && B > 0) {
+        if (overlap(new_lens, 4, path_lens, 4) || overlap(new_lens, 4, path, 4) || overlap(new_lens, 4, block_table, 4))
+            return fail(FW_ERR_INVALID_ARG, "new_lens overlaps an input");
+        if (overlap(new_lens, 4, base_lens, 4))
+            return fail(FW_ERR_INVALID_ARG, "new_lens overlaps base_lens");
+    }
+    if (B == 0) return ok();
+    fw::CommitParams p{};
+    p.B = (int)B; p.A = (int)A; p.Hkv = (int)Hkv; p.ps = (int)ps; p.layers = (int)num_layers;
+    p.max_pages = (int)max_pages;
+    p.layer_pages = P / num_layers;
+    p.k_units = (int)(Dk * esz / 16);
+    p.v_units = (int)(Dv * esz / 16);
+    p.path = static_cast<const int32_t *>(path->data);
+    p.path_stride = path->stride[0];
+    p.path_lens = static_cast<const int32_t *>(path_lens->data);
+    p.base_lens = static_cast<const int32_t *>(base_lens->data);
+    p.table = static_cast<const int32_t *>(block_table->data);
+    p.table_stride = block_table->stride[0];
+    p.k_cache = k_cache->data;
+    p.v_cache = v_cache ? v_cache->data : nullptr;
+    for (int i = 0; i < 3; ++i) {
+        p.kc_stride[i] = k_cache->stride[i] * esz;
+        p.vc_stride[i] = v_cache ? v_cache->stride[i] * esz : 0;
+    }
+    p.new_lens = new_lens ? static_cast<int32_t *>(new_lens->data) : nullptr;
+    std::lock_guard<std::mutex> lk(g_mu);
+    DeviceState *d = nullptr;
+    if (fw_status_t s = device_state(&d)) return s;
+    p.status = d->status;
+    cudaError_t e = fw::launch_kv_commit(p, stream);
+    if (e != cudaSuccess) return fail(FW_ERR_CUDA, "commit launch: %s", cudaGetErrorString(e));
+    g_launches.fetch_add(1);
+    return ok();
+}
+
+}  // extern "C"

@@ -138,6 +138,63 @@ struct PrefillParams {
     int grid;
 };
 
+// One tree decode launch (fw_paged_decode_tree).
+struct TreeParams {
+    int B, T, Hq, Hkv, G, D, ps, max_pages, num_pages;
+    int kv8;                                   // 1: E4M3 caches
+    const uint16_t *q; int64_t q_stride[3];    // [B, T, Hq, D] bf16
+    const void *k_cache, *v_cache;
+    int64_t kc_stride[3], vc_stride[3];        // elements (page, slot, head)
+    const int32_t *block_table; int64_t bt_stride;
+    const int32_t *seq_lens;
+    const int32_t *draft_lens;                 // null: T drafts each
+    const int32_t *mask; int64_t mask_stride[2];   // (b, t); words contiguous
+    void *out; int64_t out_stride[3];          // [B, T, Hq, D] bf16
+    float *lse; int64_t lse_stride[3];         // [B, T, Hq] or null
+    float scale_log2;                          // scale * k_scale * log2(e)
+    float out_scale;                           // v_scale
+    int *status;
+};
+
+// One fw_tree_mask launch.
+struct TreeMaskParams {
+    int B, T, W;                               // W: words a mask row holds
+    const int32_t *parents; int64_t parent_stride;
+    const int32_t *draft_lens;                 // null: T
+    int32_t *mask; int64_t mask_stride[2];
+    int32_t *depths; int64_t depth_stride;     // null: not wanted
+    int *status;
+};
+
+// One fw_build_page_tables call.
+struct PageTableParams {
+    int B, max_pages, F, ps;
+    int padded, L;                             // 1: L places per request; 0: packed
+    int N;                                     // places in all
+    const int32_t *seq_lens, *new_lens, *held;
+    int32_t *queue;
+    const int32_t *range;
+    int32_t *table; int64_t table_stride;
+    int32_t *slots, *cu_new, *held_out, *range_out;
+    int in_place;                              // held_out / range_out overlap their inputs
+    int num_sms;
+    int *status;
+};
+
+// One fw_kv_commit launch.
+struct CommitParams {
+    int B, A, Hkv, ps, layers, max_pages;
+    int64_t layer_pages;
+    int k_units, v_units;                      // 16-byte units of one head row (v_units 0: no values)
+    const int32_t *path; int64_t path_stride;
+    const int32_t *path_lens, *base_lens;
+    const int32_t *table; int64_t table_stride;
+    void *k_cache, *v_cache;
+    int64_t kc_stride[3], vc_stride[3];        // bytes (page, slot, head)
+    int32_t *new_lens;
+    int *status;
+};
+
 // plan kernel + attention kernel + combine kernel, in stream order
 cudaError_t launch_decode(const DecodeParams &p, const CUtensorMap &tm_q, const CUtensorMap &tm_k,
                           const CUtensorMap &tm_v, int head_dim, cudaStream_t stream,
@@ -165,6 +222,13 @@ size_t latent_pair_decode_smem_bytes();
 cudaError_t launch_decode_fp8(const DecodeParams &p, const CUtensorMap &tm_q, const CUtensorMap &tm_k,
                               const CUtensorMap &tm_v, cudaStream_t stream, cudaEvent_t timing_start,
                               cudaEvent_t timing_stop, int *launches);
+
+// Speculative decoding: the drafts' attention, their masks, the step's page
+// tables, the move of the accepted path
+cudaError_t launch_tree_decode(const TreeParams &p, cudaStream_t stream, int *launches);
+cudaError_t launch_tree_mask(const TreeMaskParams &p, cudaStream_t stream);
+cudaError_t launch_page_tables(const PageTableParams &p, cudaStream_t stream, int *launches);
+cudaError_t launch_kv_commit(const CommitParams &p, cudaStream_t stream);
 
 // plan kernel + attention kernel, in stream order
 cudaError_t launch_prefill(const PrefillParams &p, const CUtensorMap &tm_q, const CUtensorMap &tm_k,
