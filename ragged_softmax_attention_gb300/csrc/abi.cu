@@ -1087,8 +1087,24 @@ static fw_status_t build_tree(const fw_tensor_t *q, const fw_tensor_t *k_cache, 
     p.mask_stride[1] = tree_mask->stride[1];
     p.out = out->data;
     p.lse = lse ? static_cast<float *>(lse->data) : nullptr;
+    // A scale of zero would turn the -inf of hidden keys into NaN: the least
+    // magnitude used leaves every score it multiplies at zero for the exponential.
     p.scale_log2 = scale * k_scale * 1.4426950408889634f;
+    if (!std::isfinite(p.scale_log2)) return fail(FW_ERR_INVALID_ARG, "scale * k_scale overflows");
+    if (std::fabs(p.scale_log2) < 1e-30f) p.scale_log2 = std::copysign(1e-30f, p.scale_log2);
     p.out_scale = v_scale;
+    // Row tiles: whole drafts of up to 128 rows, or 128 heads of one draft.
+    if (p.G <= 128) {
+        p.tile_tokens = 128 / p.G < p.T ? 128 / p.G : p.T;
+        p.head_chunks = 1;
+        p.row_tiles = (p.T + p.tile_tokens - 1) / p.tile_tokens;
+    } else {
+        p.tile_tokens = 1;
+        p.head_chunks = (p.G + 127) / 128;
+        p.row_tiles = p.T * p.head_chunks;
+    }
+    p.min_span = fw::kTreeMinSpan;
+    p.piece_cost = fw::kTreePieceCost;
     *tp = p;
     return FW_OK;
 }
@@ -1101,7 +1117,7 @@ fw_status_t fw_paged_decode_tree_workspace_size(int32_t head_dim, size_t *bytes)
     std::lock_guard<std::mutex> lk(g_mu);
     DeviceState *d = nullptr;
     if (fw_status_t s = device_state(&d)) return s;
-    *bytes = 0;
+    *bytes = fw::tree_workspace_bytes(head_dim, d->num_sms);
     return ok();
 }
 
@@ -1119,11 +1135,39 @@ fw_status_t fw_paged_decode_tree(const fw_tensor_t *q, const fw_tensor_t *k_cach
     std::lock_guard<std::mutex> lk(g_mu);
     DeviceState *d = nullptr;
     if (fw_status_t s = device_state(&d)) return s;
-    (void)workspace;
-    (void)workspace_bytes;
+    p.grid = d->num_sms;
+    if (g_opt_max_ctas > 0 && p.grid > g_opt_max_ctas) p.grid = (int)g_opt_max_ctas;
+    // As in the decode: the KV heads ride on the CTA index when the grid holds whole groups of them.
+    p.ride = p.Hkv > 1 && p.grid % p.Hkv == 0;
+    const size_t need = fw::tree_workspace_bytes(p.D, d->num_sms);
+    void *ws = workspace;
+    if (ws) {
+        if (reinterpret_cast<uintptr_t>(ws) % 256) return fail(FW_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+        if (workspace_bytes < need)
+            return fail(FW_ERR_WORKSPACE, "workspace holds %zu bytes, %zu needed", workspace_bytes, need);
+    } else if (fw_status_t s = get_workspace(d, need, stream, &ws)) {
+        return s;
+    }
+    fw::tree_place_workspace(&p, ws);
+    p.timeout_ns = (uint64_t)g_opt_timeout_ms * 1000000ull;
     p.status = d->status;
+    CUtensorMap tq, tk, tv;
+    {
+        const uint64_t dims[4] = {(uint64_t)p.D, (uint64_t)p.Hq, (uint64_t)p.T, (uint64_t)p.B};
+        const uint64_t strides[3] = {(uint64_t)q->stride[2] * 2, (uint64_t)q->stride[1] * 2, (uint64_t)q->stride[0] * 2};
+        const uint32_t box[4] = {64, (uint32_t)(p.G < 128 ? p.G : 128), (uint32_t)p.tile_tokens, 1};
+        if (fw_status_t s = encode_bf16(&tq, q->data, 4, dims, strides, box, "q")) return s;
+        const uint32_t kbox[4] = {64, 1, (uint32_t)(p.ps < fw::kKvTile ? p.ps : fw::kKvTile), 1};
+        const fw_tensor_t *caches[2] = {k_cache, v_cache};
+        for (int i = 0; i < 2; ++i) {
+            const fw_tensor_t *c = caches[i];
+            const uint64_t cd[4] = {(uint64_t)p.D, (uint64_t)p.Hkv, (uint64_t)p.ps, (uint64_t)p.num_pages};
+            const uint64_t cs[3] = {(uint64_t)c->stride[2] * 2, (uint64_t)c->stride[1] * 2, (uint64_t)c->stride[0] * 2};
+            if (fw_status_t s = encode_bf16(i ? &tv : &tk, c->data, 4, cd, cs, kbox, i ? "v_cache" : "k_cache")) return s;
+        }
+    }
     int launched = 0;
-    cudaError_t e = fw::launch_tree_decode(p, stream, &launched);
+    cudaError_t e = fw::launch_tree_decode(p, tq, tk, tv, stream, &launched);
     g_launches.fetch_add(launched);
     if (e != cudaSuccess) return fail(FW_ERR_CUDA, "tree decode launch: %s", cudaGetErrorString(e));
     return ok();

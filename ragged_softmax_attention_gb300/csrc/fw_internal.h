@@ -44,6 +44,8 @@ constexpr int kLatentMinSpan = 32;    // latent-head decode: the same, for its h
 // carry equal work, piece starts included.
 constexpr int kDecodePieceCostBf16 = 4;
 constexpr int kDecodePieceCostFp8 = 5;
+constexpr int kTreeMinSpan = 2;       // tree decode: fewest KV tiles (and empty slots) one CTA range holds
+constexpr int kTreePieceCost = 3;     // tree decode: empty slots before a unit's tiles
 constexpr int kLatentRows = 64;       // latent-head decode: query heads per CTA (MMA N of one CTA)
 constexpr int kLatentPairRows = 128;  // latent-head decode on CTA pairs: query heads per pair
 
@@ -138,7 +140,12 @@ struct PrefillParams {
     int grid;
 };
 
-// One tree decode launch (fw_paged_decode_tree).
+// One tree decode call (fw_paged_decode_tree), fully resolved on the host.
+struct TreeCut {                               // a unit whose first piece ended a CTA's range
+    int count;                                 // its pieces, 0: none
+    int b, g, rt0, nrt, d;                     // request, KV head, row tiles, drafts
+    int pad_[2];
+};
 struct TreeParams {
     int B, T, Hq, Hkv, G, D, ps, max_pages, num_pages;
     int kv8;                                   // 1: E4M3 caches
@@ -153,6 +160,16 @@ struct TreeParams {
     float *lse; int64_t lse_stride[3];         // [B, T, Hq] or null
     float scale_log2;                          // scale * k_scale * log2(e)
     float out_scale;                           // v_scale
+    int tile_tokens;                           // whole drafts of a 128-row tile (G <= 128)
+    int head_chunks;                           // > 1: 128-head row tiles of one draft (G > 128)
+    int row_tiles;                             // row tiles of T drafts
+    int grid;                                  // CTAs
+    int ride;                                  // 1: the KV heads ride on the CTA index
+    int min_span, piece_cost;                  // least key tiles of a range; empty slots before a unit's tiles
+    float *part_o;                             // [2 * grid][row tiles of a unit * 128][D] unnormalised pieces
+    float2 *part_ml;                           // base (log2) and row sum of each of their rows
+    TreeCut *cuts;                             // [grid]
+    uint64_t timeout_ns;
     int *status;
 };
 
@@ -225,7 +242,10 @@ cudaError_t launch_decode_fp8(const DecodeParams &p, const CUtensorMap &tm_q, co
 
 // Speculative decoding: the drafts' attention, their masks, the step's page
 // tables, the move of the accepted path
-cudaError_t launch_tree_decode(const TreeParams &p, cudaStream_t stream, int *launches);
+cudaError_t launch_tree_decode(const TreeParams &p, const CUtensorMap &tm_q, const CUtensorMap &tm_k,
+                               const CUtensorMap &tm_v, cudaStream_t stream, int *launches);
+size_t tree_workspace_bytes(int head_dim, int grid);
+void tree_place_workspace(TreeParams *p, void *ws);
 cudaError_t launch_tree_mask(const TreeMaskParams &p, cudaStream_t stream);
 cudaError_t launch_page_tables(const PageTableParams &p, cudaStream_t stream, int *launches);
 cudaError_t launch_kv_commit(const CommitParams &p, cudaStream_t stream);

@@ -1,8 +1,33 @@
 // Paged decode of a tree of drafted tokens, sm_103a: draft t of request b sees
 // the committed keys 0 .. n - d - 1 and the drafts its mask row names.
 //
-// One block per (request, draft, query head): the keys pass in chunks of 128,
-// one per thread, through an online softmax in base 2.
+// With d drafts of G query heads each, the rows that share a KV head's keys
+// fill the MMA M axis (a decode of a few tokens, which puts the keys there,
+// has too few): a row tile is up to 128 (draft, head) rows, whole drafts,
+//   S [128 x 128]  = Q_tile * K_tile^T          (tcgen05, FP32 in TMEM)
+//   O [128 x D]   += P [128 x 128] * V_tile      (tcgen05, P and O in TMEM)
+// and one softmax thread owns one row, so maxima and sums need no exchange.
+// A row tile costs 1,024 MMA cycles per 128-key tile at D = 128 whether it
+// holds 8 rows or 128; an SM's share of HBM delivers such a K/V tile in ~2,700,
+// so up to two row tiles per CTA the cache, not the products, sets the time.
+//
+// A unit is (request, KV head, up to NT row tiles); units are laid end to end
+// in the order of their key tiles, each preceded by a few empty slots for the
+// cost of starting it, and every CTA takes one equal contiguous range, so the
+// partial results of a call take two slots per CTA whatever the batch: the
+// piece a range begins with and the one it ends with.  Ranges follow from the
+// lengths alone, and every CTA works them out for itself (a block-wide sum of
+// the requests' slots), which saves a planning launch.
+//
+// Streams.  D = 128 with more than 128 rows: two row tiles, each with its own
+// MMA-issuing thread, softmax warpgroup, S buffer and O, take turns on the
+// tensor core while they share every K/V load (NT = 2).  Otherwise one row
+// tile with two S buffers: the products of the next key tile run under the
+// softmax of this one (NT = 1).
+//
+// Warp roles: warp 0 copies (Q, then K and V tiles through a ring of 32 KiB
+// slots in the order the MMAs take them), warp 1 (and 2) issues the MMAs,
+// warp 3 writes the rows that see nothing, warps 4.. run the softmax.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -13,9 +38,807 @@
 namespace fw {
 namespace {
 
+using dec::ceil_div_i;
 using dec::warp_max;
 using dec::warp_sum;
+using dec::warp_wait;
 constexpr float kNegInf = -__builtin_huge_valf();
+// The base of a row's exponentials moves only when its maximum rose by more
+// than this many log2 units, so every weight is at most 2^8.
+constexpr float kRescaleSlack = 8.0f;
+constexpr int kErrInvalid = 1;     // FW_ERR_INVALID_ARG
+
+// One piece: a unit's key tiles inside one CTA range.  64 bytes.
+struct alignas(16) TreeUnit {
+    int b;             // request, -1 ends the CTA's work
+    int g;             // KV head
+    int rt0, nrt;      // first row tile and how many
+    int n, d;          // keys and drafts of the request
+    int tile0, ntiles; // key tiles
+    int part;          // partial slot, -1: the whole unit, written to the outputs
+    int pad_[7];
+};
+static_assert(sizeof(TreeUnit) == 64, "a unit record fills one 64-byte slot");
+
+template <int D_, int NT_>
+struct TreeCfg {
+    static constexpr int D = D_, NT = NT_;
+    static constexpr int kSB = NT == 2 ? 1 : 2;                 // S buffers of a stream = key tiles QK runs ahead
+    static constexpr int kTileSlots = D / 128;                  // ring slots of one K or V tile
+    static constexpr int kChunkBytes = 128 * 128;               // 128 rows x 64 bf16 columns
+    static constexpr int kSlotBytes = 2 * kChunkBytes;          // 128 rows x 128 columns
+    static constexpr int kQBytes = 128 * D * 2;
+    static constexpr int kSlots = (229376 - NT * kQBytes) / kSlotBytes;
+    static constexpr int kOffQ = 0;
+    static constexpr int kOffRing = NT * kQBytes;
+    static constexpr int kOffBar = kOffRing + kSlots * kSlotBytes;
+    static constexpr int kSched = 4;                            // unit records in flight
+    static constexpr int kBarSlotFull = 0;
+    static constexpr int kBarSlotEmpty = kBarSlotFull + kSlots;
+    static constexpr int kBarQFull = kBarSlotEmpty + kSlots;
+    static constexpr int kBarQEmpty = kBarQFull + 1;
+    static constexpr int kBarSFull = kBarQEmpty + 1;            // [NT][kSB]
+    static constexpr int kBarPHalf = kBarSFull + NT * kSB;      // [NT][kSB]
+    static constexpr int kBarPFull = kBarPHalf + NT * kSB;      // [NT][kSB]
+    static constexpr int kBarPvDone = kBarPFull + NT * kSB;     // [NT]
+    static constexpr int kBarIssued = kBarPvDone + NT;          // [NT]
+    static constexpr int kBarDrain = kBarIssued + NT;           // [NT]
+    static constexpr int kBarSchedFull = kBarDrain + NT;
+    static constexpr int kBarSchedEmpty = kBarSchedFull + kSched;
+    static constexpr int kNumBars = kBarSchedEmpty + kSched;
+    static constexpr int kOffSched = (kOffBar + kNumBars * 8 + 63) / 64 * 64;
+    static constexpr int kOffSeen = kOffSched + kSched * 64;    // [NT][2][4 warps][4 words]
+    static constexpr int kOffPlan = kOffSeen + NT * 128;        // long long: total, start of row b0; int b0
+    static constexpr int kOffScan = kOffPlan + 32;              // [12] warp sums
+    static constexpr int kOffMisc = kOffScan + 96;
+    static constexpr int kSmemBytes = kOffMisc + 16 + 1024;
+    static_assert(kSmemBytes <= 232448, "shared memory budget of one CTA exceeded");
+    static constexpr int kThreads = 128 + NT * 128;
+    static constexpr int kSchedReaders = NT + 4 * NT;           // issuers and softmax warps
+    // NT = 2: 384 threads launched at 168 registers; 128 x 80 + 256 x 208 = 63488 <= 64512.
+    static constexpr uint32_t kRegsControl = 80, kRegsSoftmax = 208;
+    static_assert(NT == 1 || 128 * kRegsControl + 256 * kRegsSoftmax <= 384 * 168, "register split");
+    static constexpr uint32_t kIdescQK = idesc_bf16_f32(128, kKvTile, false, false);
+    static constexpr uint32_t kIdescPV = idesc_bf16_f32(128, 128, false, true);
+    __device__ static constexpr uint32_t s_col(int x, int buf) { return (uint32_t)(x * kSB + buf) * 128u; }
+    __device__ static constexpr uint32_t o_col(int x) { return 256u + (uint32_t)x * 128u; }
+};
+
+// Keys and drafts of request b, both within what the call can hold.
+__device__ __forceinline__ void tree_row(const TreeParams &p, int b, int &n, int &d) {
+    n = min(max(__ldg(p.seq_lens + b), 0), p.max_pages * p.ps);
+    d = p.draft_lens ? min(max(__ldg(p.draft_lens + b), 0), p.T) : p.T;
+    d = min(d, n);
+}
+
+// Units of a request in the planned sequence (of one KV head when the heads
+// ride on the CTA index).
+template <int NT>
+__device__ __forceinline__ int tree_units(const TreeParams &p, int d) {
+    const int tiles = p.head_chunks > 1 ? d * p.head_chunks : ceil_div_i(d, p.tile_tokens);
+    return ceil_div_i(tiles, NT) * (p.ride ? 1 : p.Hkv);
+}
+
+// The (draft, head) of row r of row tile rt; false for padding.
+__device__ __forceinline__ bool tree_tile_row(const TreeParams &p, int rt, int g, int d, int r, int &t, int &h) {
+    if (p.head_chunks > 1) {
+        t = rt / p.head_chunks;
+        const int hh = (rt - t * p.head_chunks) * 128 + r;
+        h = g * p.G + hh;
+        return hh < p.G && t < d;
+    }
+    const int tt = r / p.G;
+    t = rt * p.tile_tokens + tt;
+    h = g * p.G + (r - tt * p.G);
+    return tt < p.tile_tokens && t < d;
+}
+
+// Bits of the 32 keys from draft ds on (ds < 0: committed keys first) that the
+// mask row shows, among the request's d drafts.
+__device__ __forceinline__ uint32_t draft_bits(const int32_t *row, int ds, int d) {
+    if (ds <= -32) return 0xffffffffu;
+    if (ds >= d) return 0u;
+    uint32_t v;
+    if (ds < 0) {
+        v = ((uint32_t)__ldg(row) << -ds) | ((1u << -ds) - 1u);
+    } else {
+        const int w = ds >> 5;
+        const uint32_t lo = (uint32_t)__ldg(row + w);
+        const uint32_t hi = (w + 1) * 32 < d ? (uint32_t)__ldg(row + w + 1) : 0u;
+        v = __funnelshift_r(lo, hi, ds & 31);
+    }
+    const int left = d - ds;
+    return left < 32 ? v & ((1u << left) - 1u) : v;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+    __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<uint32_t *>(&v);
+}
+
+// Ring positions, in units of whole K or V tiles, of a piece of n key tiles
+// when QK runs L tiles ahead of PV: K_0 .. K_{L-1}, then V_j K_{j+L}.
+template <int L>
+__device__ __forceinline__ int pos_v(int j, int n) { return min(L, n) + j + min(j, max(0, n - L)); }
+template <int L>
+__device__ __forceinline__ int pos_k(int j, int n) { return j < L ? j : pos_v<L>(j - L, n) + 1; }
+
+template <int D, int NT>
+__global__ void __launch_bounds__(TreeCfg<D, NT>::kThreads, 1)
+tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUtensorMap tm_q,
+                   const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
+    using C = TreeCfg<D, NT>;
+    constexpr int kSB = C::kSB, TS = C::kTileSlots;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *sQ = smem + C::kOffQ;
+    uint8_t *sRing = smem + C::kOffRing;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
+    uint64_t *slot_full = bars + C::kBarSlotFull;
+    uint64_t *slot_empty = bars + C::kBarSlotEmpty;
+    uint64_t *q_full = bars + C::kBarQFull;
+    uint64_t *q_empty = bars + C::kBarQEmpty;
+    uint64_t *s_full = bars + C::kBarSFull;
+    uint64_t *p_half = bars + C::kBarPHalf;
+    uint64_t *p_full = bars + C::kBarPFull;
+    uint64_t *pv_done = bars + C::kBarPvDone;
+    uint64_t *issued = bars + C::kBarIssued;
+    uint64_t *drain = bars + C::kBarDrain;
+    uint64_t *sched_full = bars + C::kBarSchedFull;
+    uint64_t *sched_empty = bars + C::kBarSchedEmpty;
+    TreeUnit *sched = reinterpret_cast<TreeUnit *>(smem + C::kOffSched);
+    uint32_t *seen_words = reinterpret_cast<uint32_t *>(smem + C::kOffSeen);
+    long long *plan = reinterpret_cast<long long *>(smem + C::kOffPlan);
+    long long *scan = reinterpret_cast<long long *>(smem + C::kOffScan);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffMisc);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::kOffMisc + 4);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kSlots; ++i) { mbar_init(&slot_full[i], 1); mbar_init(&slot_empty[i], NT); }
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, NT);
+        for (int i = 0; i < NT * kSB; ++i) { mbar_init(&s_full[i], 1); mbar_init(&p_half[i], 4); mbar_init(&p_full[i], 4); }
+        for (int i = 0; i < NT; ++i) { mbar_init(&pv_done[i], 1); mbar_init(&issued[i], 1); mbar_init(&drain[i], 1); }
+        for (int i = 0; i < C::kSched; ++i) { mbar_init(&sched_full[i], 1); mbar_init(&sched_empty[i], C::kSchedReaders); }
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&tm_q); tma_prefetch_desc(&tm_k); tma_prefetch_desc(&tm_v);
+    }
+    if (warp == 1) { tmem_alloc(tmem_slot, 512); tmem_relinquish(); }
+    pdl_launch_dependents();                       // the merge may take its place; it waits for this grid
+    // The planned sequence: request b takes units * (piece_cost + tiles) slots.
+    // Every thread sums a run of requests; the one whose run holds this CTA's
+    // first slot looks the request up.
+    const int per = (p.B + C::kThreads - 1) / C::kThreads;
+    auto row_slots = [&](int b) -> long long {
+        int n, d;
+        tree_row(p, b, n, d);
+        return (long long)tree_units<NT>(p, d) * (p.piece_cost + ceil_div_i(n, kKvTile));
+    };
+    {
+        long long mine = 0;
+        const int b0 = threadIdx.x * per;
+        for (int i = 0; i < per && b0 + i < p.B; ++i) mine += row_slots(b0 + i);
+        long long incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 31) scan[warp] = incl;
+        __syncthreads();
+        long long before = incl - mine, total = 0;
+        for (int w = 0; w < C::kThreads / 32; ++w) {
+            if (w < warp) before += scan[w];
+            total += scan[w];
+        }
+        const int nranges = p.ride ? (int)gridDim.x / p.Hkv : (int)gridDim.x;
+        const long long span = max((long long)p.min_span, (total + nranges - 1) / nranges);
+        const long long first = span * (p.ride ? (int)blockIdx.x / p.Hkv : (int)blockIdx.x);
+        if (mine > 0 && first >= before && first < before + mine) {
+            int b = b0;
+            for (long long s; first >= before + (s = row_slots(b)); ++b) before += s;
+            plan[1] = before;
+            plan[2] = b;
+        }
+        if (threadIdx.x == 0) { plan[0] = total; plan[3] = span; }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const WaitCtx wc{p.status, p.timeout_ns, abort_flag};
+    auto wait_unit = [&](int k) -> const TreeUnit * {
+        const int sl = k % C::kSched;
+        return mbar_wait(&sched_full[sl], (k / C::kSched) & 1, wc) ? &sched[sl] : nullptr;
+    };
+    auto free_unit = [&](int k) { mbar_arrive(&sched_empty[k % C::kSched]); };
+
+    if (warp < 4) {
+      if constexpr (NT == 2) setmaxnreg_dec<C::kRegsControl>();
+      if (warp == 0) {
+        // ------------------------------------------------------------ producer
+        const long long total = plan[0], span = plan[3];
+        const int range = p.ride ? (int)blockIdx.x / p.Hkv : (int)blockIdx.x;
+        long long pos = span * range;
+        const long long end = min(total, pos + span);
+        long long pb0 = plan[1];
+        int b = (int)plan[2];
+        int n = 0, d = 0, units = 0, tiles = 0;
+        auto open_row = [&]() {
+            tree_row(p, b, n, d);
+            units = tree_units<NT>(p, d);
+            tiles = ceil_div_i(n, kKvTile);
+        };
+        TreeCut cut{};
+        const int box_rows = p.ps < kKvTile ? p.ps : kKvTile;
+        const int pages_per_tile = p.ps < kKvTile ? kKvTile / p.ps : 1;
+        uint32_t rp = 0;                                  // ring slots filled so far
+        bool ok = true;
+        int k = 0;
+        if (pos < end) open_row();
+        while (ok) {
+            // ---- the next piece
+            TreeUnit u;
+            u.b = -1;
+            while (pos < end) {
+                const int v = p.piece_cost + tiles;
+                const long long row = (long long)units * v;
+                if (pos >= pb0 + row) { pb0 += row; ++b; open_row(); continue; }
+                const int ui = (int)((pos - pb0) / v);
+                const int vl = (int)(pos - pb0 - (long long)ui * v);
+                if (vl < p.piece_cost) { pos += p.piece_cost - vl; continue; }
+                const int tl = vl - p.piece_cost;
+                const int th = (int)min((long long)tiles, tl + (end - pos));
+                const long long ustart = pb0 + (long long)ui * v + p.piece_cost;
+                u.b = b;
+                const int per_head = p.ride ? units : units / p.Hkv;
+                u.g = p.ride ? (int)blockIdx.x % p.Hkv : ui / per_head;
+                const int rts = p.head_chunks > 1 ? d * p.head_chunks : ceil_div_i(d, p.tile_tokens);
+                u.rt0 = (p.ride ? ui : ui - u.g * per_head) * NT;
+                u.nrt = min(NT, rts - u.rt0);
+                u.n = n; u.d = d;
+                u.tile0 = tl; u.ntiles = th - tl;
+                u.part = -1;
+                if (tl > 0) {
+                    u.part = 2 * blockIdx.x;
+                } else if (th < tiles) {
+                    u.part = 2 * blockIdx.x + 1;
+                    cut.count = (int)((ustart + tiles - 1) / span) - range + 1;
+                    cut.b = b; cut.g = u.g; cut.rt0 = u.rt0; cut.nrt = u.nrt; cut.d = d;
+                }
+                pos += th - tl;
+                break;
+            }
+            {
+                const int sl = k % C::kSched;
+                ok = warp_wait(&sched_empty[sl], ((k / C::kSched) & 1) ^ 1, wc, lane);
+                if (!ok) break;
+                if (lane == 0) { sched[sl] = u; mbar_arrive(&sched_full[sl]); }
+                __syncwarp();
+            }
+            if (u.b < 0) break;
+            ok = warp_wait(q_empty, (k & 1) ^ 1, wc, lane);
+            if (!ok) break;
+            if (lane == 0) {
+                const uint32_t qrows = p.head_chunks > 1 ? 128u : (uint32_t)(p.G * p.tile_tokens);
+                mbar_arrive_expect_tx(q_full, (uint32_t)u.nrt * (D / 64) * qrows * 128u);
+                for (int x = 0; x < u.nrt; ++x) {
+                    const int rt = u.rt0 + x;
+                    int h0 = u.g * p.G, t0 = rt * p.tile_tokens;
+                    if (p.head_chunks > 1) { t0 = rt / p.head_chunks; h0 += (rt - t0 * p.head_chunks) * 128; }
+#pragma unroll
+                    for (int c = 0; c < D / 64; ++c)
+                        tma_load_4d(smem_u32(sQ + x * C::kQBytes + c * C::kChunkBytes), &tm_q, q_full, c * 64, h0, t0,
+                                    u.b);
+                }
+            }
+            __syncwarp();
+            // ---- K and V tiles in the order the MMAs take them.  Lane l holds
+            // the pages of one tile (at most 16); each lane copies its page.
+            const int32_t *bt_row = p.block_table + (int64_t)u.b * p.bt_stride;
+            auto tile_page = [&](int j) -> int {          // this lane's page of key tile j, -1: none
+                const int key = (u.tile0 + j) * kKvTile + (p.ps < kKvTile ? lane * p.ps : 0);
+                if (lane >= pages_per_tile || j >= u.ntiles || key >= u.n) return -1;
+                int phys = __ldg(bt_row + key / p.ps);
+                if ((unsigned)phys >= (unsigned)p.num_pages) { record_error(p.status, kErrInvalid); phys = 0; }
+                return phys;
+            };
+            auto copy_tile = [&](int j, int phys, bool is_v) -> bool {
+                const int key0 = (u.tile0 + j) * kKvTile;
+                const int slot0 = p.ps < kKvTile ? 0 : key0 % p.ps;
+                const unsigned who = __ballot_sync(0xffffffffu, phys >= 0);
+                const uint32_t bytes = (uint32_t)(__popc(who) * box_rows * 256);
+#pragma unroll
+                for (int s = 0; s < TS; ++s, ++rp) {
+                    const int sl = rp % C::kSlots;
+                    if (!warp_wait(&slot_empty[sl], ((rp / C::kSlots) & 1) ^ 1, wc, lane)) return false;
+                    if (lane == 0) mbar_arrive_expect_tx(&slot_full[sl], bytes);
+                    __syncwarp();
+                    if (phys >= 0) {
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+                            tma_load_4d(smem_u32(sRing + sl * C::kSlotBytes + c * C::kChunkBytes + lane * box_rows * 128),
+                                        is_v ? (const void *)&tm_v : (const void *)&tm_k, &slot_full[sl],
+                                        s * 128 + c * 64, u.g, slot0, phys);
+                    }
+                }
+                return true;
+            };
+            // Page numbers of the next tiles are fetched before this tile's
+            // slot is waited for: cur[i] is tile (next K) + i - kSB.
+            int pages[kSB + 2];
+#pragma unroll
+            for (int i = 0; i < kSB + 2; ++i) pages[i] = tile_page(i);
+            for (int j = 0; j < kSB && j < u.ntiles && ok; ++j) ok = copy_tile(j, j == 0 ? pages[0] : pages[kSB - 1], false);
+            for (int j = 0; j < u.ntiles && ok; ++j) {
+                ok = copy_tile(j, pages[0], true);
+                if (ok && j + kSB < u.ntiles) ok = copy_tile(j + kSB, pages[kSB], false);
+#pragma unroll
+                for (int i = 0; i < kSB + 1; ++i) pages[i] = pages[i + 1];
+                pages[kSB + 1] = tile_page(j + kSB + 2);
+            }
+            ++k;
+        }
+        if (lane == 0) {
+            p.cuts[blockIdx.x] = cut;
+            for (uint32_t i = 0; i < (uint32_t)C::kSlots && i < rp; ++i) {
+                const uint32_t r = rp - 1 - i;
+                mbar_wait_drain(&slot_full[r % C::kSlots], (r / C::kSlots) & 1, wc);
+            }
+        }
+        __syncwarp();
+      } else if (warp <= NT) {
+        // ----------------------------------------------------------------- MMA
+        if (lane == 0) {
+            const int x = warp - 1;
+            uint32_t rp = 0;                              // ring slots of earlier pieces
+            uint32_t steps = 0;                           // this stream's key tiles of earlier pieces
+            uint32_t turns = 0;                           // shared steps of earlier pieces (both streams present)
+            const SDesc q_d = sdesc_sw128_split(smem_u32(sQ + x * C::kQBytes), 16, 1024);
+            const SDesc k_d = sdesc_sw128_split(smem_u32(sRing), 16, 1024);
+            const SDesc v_d = sdesc_sw128_split(smem_u32(sRing), C::kChunkBytes, 1024);
+            auto wait_tile = [&](uint32_t r) -> bool {
+#pragma unroll
+                for (int s = 0; s < TS; ++s)
+                    if (!mbar_wait(&slot_full[(r + s) % C::kSlots], ((r + s) / C::kSlots) & 1, wc)) return false;
+                return true;
+            };
+            auto tile_there = [&](uint32_t r) -> bool {
+                bool there = true;
+#pragma unroll
+                for (int s = 0; s < TS; ++s)
+                    there &= mbar_try_wait(smem_u32(&slot_full[(r + s) % C::kSlots]), ((r + s) / C::kSlots) & 1);
+                return there;
+            };
+            auto release_tile = [&](uint32_t r) {
+#pragma unroll
+                for (int s = 0; s < TS; ++s) mma_commit(&slot_empty[(r + s) % C::kSlots]);
+            };
+            auto push_qk = [&](uint32_t r, int buf) {
+#pragma unroll
+                for (int s = 0; s < TS; ++s) {
+                    const SDesc kd{k_d.lo + ((r + s) % C::kSlots) * (C::kSlotBytes >> 4), k_d.hi};
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk) {
+                        const uint32_t off = (kk >> 2) * C::kChunkBytes + (kk & 3) * 32;
+                        mma_bf16_ss(tmem + C::s_col(x, buf), sdesc_at(q_d, s * C::kSlotBytes + off), sdesc_at(kd, off),
+                                    C::kIdescQK, s + kk > 0 ? 1u : 0u);
+                    }
+                }
+            };
+            // P of a key tile lies over the first 64 columns of its S buffer
+            // (two BF16 a column); each half of 64 keys goes out as it comes.
+            auto push_pv_half = [&](uint32_t r, int buf, int half, bool first) {
+#pragma unroll
+                for (int s = 0; s < TS; ++s) {
+                    const SDesc vd{v_d.lo + ((r + s) % C::kSlots) * (C::kSlotBytes >> 4), v_d.hi};
+#pragma unroll
+                    for (int k4 = 0; k4 < 4; ++k4) {
+                        const int kk = half * 4 + k4;
+                        mma_bf16_ts(tmem + C::o_col(x) + s * 128, tmem + C::s_col(x, buf) + kk * 8,
+                                    sdesc_at(vd, kk * 16 * 128), C::kIdescPV, (first && kk == 0) ? 0u : 1u);
+                    }
+                }
+            };
+            bool ok = true;
+            for (int k = 0; ok; ++k) {
+                const TreeUnit *ur = wait_unit(k);
+                const bool got = ur && ur->b >= 0;
+                const int n = got ? ur->ntiles : 0;
+                const int nrt = got ? ur->nrt : 0;
+                free_unit(k);
+                if (!got) break;
+                const uint32_t r0 = rp;
+                rp += (uint32_t)(2 * n * TS);
+                if (!mbar_wait(q_full, k & 1, wc)) break;
+                if (x >= nrt) {
+                    // No row tile for this stream: it still sees every copy land and
+                    // hands every slot back, so that its phases stay in step.
+                    mbar_arrive(q_empty);
+                    for (uint32_t r = r0; r < rp && ok; ++r) {
+                        ok = mbar_wait(&slot_full[r % C::kSlots], (r / C::kSlots) & 1, wc);
+                        if (ok) mbar_arrive(&slot_empty[r % C::kSlots]);
+                    }
+                    continue;
+                }
+                tc_fence_after();
+                auto rk = [&](int j) { return r0 + (uint32_t)(pos_k<kSB>(j, n) * TS); };
+                auto rv = [&](int j) { return r0 + (uint32_t)(pos_v<kSB>(j, n) * TS); };
+                for (int j = 0; j < kSB && j < n && ok; ++j) {
+                    ok = wait_tile(rk(j));
+                    if (!ok) break;
+                    tc_fence_after();
+                    push_qk(rk(j), (steps + j) % kSB);
+                    mma_commit(&s_full[x * kSB + (steps + j) % kSB]);
+                    release_tile(rk(j));
+                    if (j == n - 1) mma_commit(q_empty);
+                }
+                for (int j = 0; j < n && ok; ++j) {
+                    const uint32_t st = steps + j;
+                    const int buf = st % kSB;
+                    const uint32_t ph = (st / kSB) & 1;
+                    if (NT == 2 && nrt == 2) {
+                        // Turns: stream 1 follows stream 0's step j, stream 0 stream 1's
+                        // step j - 1, so that one's products run under the other's softmax.
+                        // (Steps count on across pieces, so neither gets two phases ahead.)
+                        const uint32_t dep = turns + j + x;
+                        if (dep > 0 && !mbar_wait(&issued[1 - x], (dep - 1) & 1, wc)) { ok = false; break; }
+                    }
+                    if (!wait_tile(rv(j)) || !mbar_wait(&p_half[x * kSB + buf], ph, wc)) { ok = false; break; }
+                    const bool next = j + kSB < n;
+                    const bool paired = next && tile_there(rk(j + kSB));
+                    tc_fence_after();
+                    push_pv_half(rv(j), buf, 0, j == 0);
+                    if (!mbar_wait(&p_full[x * kSB + buf], ph, wc)) { ok = false; break; }
+                    tc_fence_after();
+                    push_pv_half(rv(j), buf, 1, false);
+                    if (NT == 2 && nrt == 2) mbar_arrive(&issued[x]);
+                    // With the next K tile there, its product goes straight behind
+                    // (a wait between pushes lets the tensor pipe run dry); else
+                    // this tile's V is handed back first.
+                    if (paired) push_qk(rk(j + kSB), buf);
+                    if (kSB == 2 || j == n - 1) mma_commit(&pv_done[x]);
+                    release_tile(rv(j));
+                    if (next) {
+                        if (!paired) {
+                            if (!wait_tile(rk(j + kSB))) { ok = false; break; }
+                            tc_fence_after();
+                            push_qk(rk(j + kSB), buf);
+                        }
+                        mma_commit(&s_full[x * kSB + buf]);
+                        release_tile(rk(j + kSB));
+                        if (j + kSB == n - 1) mma_commit(q_empty);
+                    }
+                }
+                if (!ok) break;
+                steps += n;
+                if (nrt == 2) turns += n;
+            }
+            mma_commit(&drain[x]);
+            mbar_wait_drain(&drain[x], 0, wc);
+        }
+        __syncwarp();
+      } else if (warp == 3) {
+        // ------------------------------------------- rows that see nothing
+        for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+            int n, d;
+            tree_row(p, b, n, d);
+            const int rows = (p.T - d) * p.Hq;
+            for (int i = lane; i < rows * (D / 8); i += 32) {
+                const int r = i / (D / 8), c = i - r * (D / 8);
+                const int t = d + r / p.Hq, h = r % p.Hq;
+                __nv_bfloat16 *o = reinterpret_cast<__nv_bfloat16 *>(p.out) + b * p.out_stride[0] +
+                                   t * p.out_stride[1] + h * p.out_stride[2];
+                reinterpret_cast<uint4 *>(o)[c] = make_uint4(0, 0, 0, 0);
+                if (c == 0 && p.lse) p.lse[b * p.lse_stride[0] + t * p.lse_stride[1] + h * p.lse_stride[2]] = kNegInf;
+            }
+        }
+      }
+    } else {
+        if constexpr (NT == 2) setmaxnreg_inc<C::kRegsSoftmax>();
+        // ------------------------------------------------- softmax / epilogue
+        // A failed wait does not change the control flow, so the named barriers
+        // below are always met by all four warps of the stream.
+        const int x = (warp - 4) >> 2;
+        const int q4 = warp & 3;
+        const int row = q4 * 32 + lane;
+        const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
+        const bool scale_pos = p.scale_log2 >= 0.f;
+        uint32_t steps = 0, pieces = 0, rp = 0;
+        for (int k = 0;; ++k) {
+            const TreeUnit *ur = wait_unit(k);
+            const bool got = ur && ur->b >= 0;
+            TreeUnit u;
+            u.b = -1;
+            if (got) u = *ur;
+            __syncwarp();
+            if (lane == 0) free_unit(k);
+            if (!got) break;
+            const uint32_t r0 = rp;
+            rp += (uint32_t)(2 * u.ntiles * TS);
+            if (x >= u.nrt) continue;
+            int t, h;
+            const bool live = tree_tile_row(p, u.rt0 + x, u.g, u.d, row, t, h);
+            const bool warp_live = __any_sync(0xffffffffu, live);
+            const int base = u.n - u.d;                   // committed keys
+            const int32_t *mrow = p.mask + u.b * p.mask_stride[0] + (live ? t : 0) * p.mask_stride[1];
+            float m_ref = kNegInf, l_sum = 0.f;
+            for (int j = 0; j < u.ntiles; ++j, ++steps) {
+                const int buf = steps % kSB;
+                const int key0 = (u.tile0 + j) * kKvTile;
+                const bool drafts = key0 + kKvTile > base;    // the tile reaches past the committed keys
+                if (drafts) {
+                    // Values of keys nobody sees must not meet a zero weight: they
+                    // may be NaN.  A key is seen when some draft's mask shows it.
+                    uint32_t seen[4] = {0, 0, 0, 0};
+                    for (int tt = row; tt < u.d; tt += 128) {
+                        const int32_t *mr = p.mask + u.b * p.mask_stride[0] + tt * p.mask_stride[1];
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) seen[w] |= draft_bits(mr, key0 + 32 * w - base, u.d);
+                    }
+                    uint32_t *sw = seen_words + (x * 2 + (j & 1)) * 16;
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        seen[w] = __reduce_or_sync(0xffffffffu, seen[w]);
+                        if (lane == 0) sw[q4 * 4 + w] = seen[w];
+                    }
+                    named_bar_sync(1 + x, 128);
+                    const uint32_t mine = sw[q4] | sw[4 + q4] | sw[8 + q4] | sw[12 + q4];   // word q4: this warp's keys
+                    if (__any_sync(0xffffffffu, !(mine >> lane & 1))) {
+                        const uint32_t r = r0 + (uint32_t)(pos_v<kSB>(j, u.ntiles) * TS);
+#pragma unroll
+                        for (int s = 0; s < TS; ++s) {
+                            const uint32_t sl = (r + s) % C::kSlots;
+                            mbar_wait(&slot_full[sl], ((r + s) / C::kSlots) & 1, wc);
+                            if (!(mine >> lane & 1)) {
+#pragma unroll
+                                for (int c = 0; c < 2; ++c) {
+                                    uint4 *vr = reinterpret_cast<uint4 *>(sRing + sl * C::kSlotBytes +
+                                                                          c * C::kChunkBytes + row * 128);
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i) vr[i] = make_uint4(0, 0, 0, 0);
+                                }
+                            }
+                        }
+                        fence_proxy_async_smem();
+                    }
+                }
+                mbar_wait(&s_full[x * kSB + buf], (steps / kSB) & 1, wc);
+                tc_fence_after();
+                if (!warp_live) {                         // rows of padding: whatever lies there
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) { mbar_arrive(&p_half[x * kSB + buf]); mbar_arrive(&p_full[x * kSB + buf]); }
+                    continue;
+                }
+                const uint32_t sa = tmem + lane_off + C::s_col(x, buf);
+                float sv[kKvTile];
+#pragma unroll
+                for (int c = 0; c < kKvTile / 32; ++c) tmem_ld32(sa + c * 32, sv + c * 32);
+                tmem_wait_ld();
+                if (drafts) {
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const uint32_t bits = live ? draft_bits(mrow, key0 + 32 * w - base, u.d) : 0u;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (!(bits >> i & 1)) sv[w * 32 + i] = scale_pos ? kNegInf : -kNegInf;
+                    }
+                }
+                float e8[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) e8[i] = sv[i];
+                if (scale_pos) {
+#pragma unroll
+                    for (int i = 8; i < kKvTile; ++i) e8[i & 7] = fmaxf(e8[i & 7], sv[i]);
+                } else {
+#pragma unroll
+                    for (int i = 8; i < kKvTile; ++i) e8[i & 7] = fminf(e8[i & 7], sv[i]);
+                }
+                const float ext = scale_pos
+                    ? fmaxf(fmaxf(fmaxf(e8[0], e8[1]), fmaxf(e8[2], e8[3])), fmaxf(fmaxf(e8[4], e8[5]), fmaxf(e8[6], e8[7])))
+                    : fminf(fminf(fminf(e8[0], e8[1]), fminf(e8[2], e8[3])), fminf(fminf(e8[4], e8[5]), fminf(e8[6], e8[7])));
+                const bool none = ext == (scale_pos ? kNegInf : -kNegInf);
+                const float m_tile = none || !live ? kNegInf : ext * p.scale_log2;
+                const bool up = m_tile > m_ref + kRescaleSlack;   // also the first visible tile: m_ref = -inf
+                if (__any_sync(0xffffffffu, up)) {
+                    float alpha = 1.f;
+                    if (up) {
+                        alpha = ex2_approx(m_ref - m_tile);
+                        l_sum *= alpha;
+                        m_ref = m_tile;
+                    }
+                    if (j > 0) {
+                        // With one S buffer, S_j there means PV_{j-1} is done; with two
+                        // it may still run.
+                        if constexpr (kSB == 2) {
+                            mbar_wait(&pv_done[x], (steps - 1) & 1, wc);
+                            tc_fence_after();
+                        }
+#pragma unroll 1
+                        for (int c = 0; c < D / 32; ++c) {
+                            float o[32];
+                            const uint32_t oa = tmem + lane_off + C::o_col(x) + c * 32;
+                            tmem_ld32(oa, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] *= alpha;
+                            tmem_st32(oa, o);
+                        }
+                        tmem_wait_st();
+                    }
+                }
+                // P = 2^(s * scale * log2 e - m_ref), rounded to BF16 (the MMA's A
+                // operand shares V's type); the row sum takes it unrounded.
+                const float mu = m_ref == kNegInf ? 0.f : m_ref;
+                uint32_t pk[kKvTile / 2];
+                float a8[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) a8[i] = 0.f;
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                    for (int i = 0; i < kKvTile / 2; i += 2) {
+                        const int kx = half * (kKvTile / 2) + i;
+                        const float p0 = ex2_approx(fmaf(sv[kx], p.scale_log2, -mu));
+                        const float p1 = ex2_approx(fmaf(sv[kx + 1], p.scale_log2, -mu));
+                        a8[(i >> 1) & 7] += p0 + p1;
+                        pk[kx >> 1] = pack_bf16x2(p0, p1);
+                    }
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        tmem_st16u(sa + half * 32 + c * 16,
+                                   *reinterpret_cast<const uint32_t(*)[16]>(pk + half * 32 + c * 16));
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(half == 0 ? &p_half[x * kSB + buf] : &p_full[x * kSB + buf]);
+                }
+                l_sum += ((a8[0] + a8[1]) + (a8[2] + a8[3])) + ((a8[4] + a8[5]) + (a8[6] + a8[7]));
+            }
+            // ------------------------------------------------------ epilogue
+            ++pieces;
+            // Two S buffers: the last score tile proves all but the last two PVs
+            // done, so their phases are waited for one after the other (a wait on
+            // the last alone could pass two phases early).
+            if (kSB == 2 && steps >= 2) mbar_wait(&pv_done[x], (steps - 2) & 1, wc);
+            mbar_wait(&pv_done[x], ((kSB == 2 ? steps : pieces) - 1) & 1, wc);
+            tc_fence_after();
+            if (warp_live) {
+                const float inv = l_sum > 0.f ? p.out_scale / l_sum : 0.f;
+                __nv_bfloat16 *orow = reinterpret_cast<__nv_bfloat16 *>(p.out) + u.b * p.out_stride[0] +
+                                      t * p.out_stride[1] + h * p.out_stride[2];
+                const int64_t prow = (int64_t)u.part * (NT * 128) + x * 128 + row;
+                float4 *part = reinterpret_cast<float4 *>(p.part_o + prow * D);
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    float o[32];
+                    tmem_ld32(tmem + lane_off + C::o_col(x) + c * 32, o);
+                    tmem_wait_ld();
+                    if (!live) continue;
+                    if (u.part < 0) {
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            uint4 v;
+                            v.x = l_sum > 0.f ? pack_bf16x2(o[8 * w + 0] * inv, o[8 * w + 1] * inv) : 0u;
+                            v.y = l_sum > 0.f ? pack_bf16x2(o[8 * w + 2] * inv, o[8 * w + 3] * inv) : 0u;
+                            v.z = l_sum > 0.f ? pack_bf16x2(o[8 * w + 4] * inv, o[8 * w + 5] * inv) : 0u;
+                            v.w = l_sum > 0.f ? pack_bf16x2(o[8 * w + 6] * inv, o[8 * w + 7] * inv) : 0u;
+                            *reinterpret_cast<uint4 *>(orow + c * 32 + w * 8) = v;
+                        }
+                    } else {
+#pragma unroll
+                        for (int w = 0; w < 8; ++w)
+                            part[c * 8 + w] = make_float4(o[4 * w], o[4 * w + 1], o[4 * w + 2], o[4 * w + 3]);
+                    }
+                }
+                if (live) {
+                    if (u.part >= 0) p.part_ml[prow] = make_float2(m_ref, l_sum);
+                    else if (p.lse)
+                        p.lse[u.b * p.lse_stride[0] + t * p.lse_stride[1] + h * p.lse_stride[2]] =
+                            l_sum > 0.f ? (m_ref + log2f(l_sum)) * 0.69314718055994531f : kNegInf;
+                }
+            }
+            tc_fence_before();
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// Merges the pieces of the units that CTA ranges cut: with weighted sums o_i,
+// row sums l_i and bases m_i, M = max m_i, out = sum 2^(m_i - M) o_i /
+// sum 2^(m_i - M) l_i.  Block (chunk, c) takes 32 rows of the unit whose first
+// piece ended CTA c's range; its other pieces opened the following ranges.
+template <int D, int NT>
+__global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__ TreeParams p) {
+    pdl_wait();                                      // the pieces are written
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const TreeCut cut = p.cuts[blockIdx.y];
+    const int x = blockIdx.x / 4;
+    if (cut.count == 0 || x >= cut.nrt) return;
+    const int step = p.ride ? p.Hkv : 1;
+    for (int i = 0; i < 4; ++i) {
+        const int row = (blockIdx.x & 3) * 32 + warp * 4 + i;
+        int t, h;
+        if (!tree_tile_row(p, cut.rt0 + x, cut.g, cut.d, row, t, h)) continue;
+        auto slot_row = [&](int k) -> int64_t {
+            const int slot = k == 0 ? 2 * blockIdx.y + 1 : 2 * (blockIdx.y + k * step);
+            return (int64_t)slot * (NT * 128) + x * 128 + row;
+        };
+        float m = kNegInf;
+        for (int k = lane; k < cut.count; k += 32) {
+            const float2 ml = p.part_ml[slot_row(k)];
+            if (ml.y > 0.f) m = fmaxf(m, ml.x);
+        }
+        m = warp_max(m);
+        constexpr int V = D / 32;
+        float acc[V], l = 0.f;
+#pragma unroll
+        for (int c = 0; c < V; ++c) acc[c] = 0.f;
+        for (int k = 0; k < cut.count; ++k) {
+            const int64_t r = slot_row(k);
+            const float2 ml = p.part_ml[r];
+            if (!(ml.y > 0.f)) continue;
+            const float w = ex2_approx(ml.x - m);
+            l = fmaf(w, ml.y, l);
+            const float4 *src = reinterpret_cast<const float4 *>(p.part_o + r * D);
+#pragma unroll
+            for (int c = 0; c < V / 4; ++c) {
+                const float4 v = src[c * 32 + lane];
+                acc[4 * c + 0] = fmaf(w, v.x, acc[4 * c + 0]);
+                acc[4 * c + 1] = fmaf(w, v.y, acc[4 * c + 1]);
+                acc[4 * c + 2] = fmaf(w, v.z, acc[4 * c + 2]);
+                acc[4 * c + 3] = fmaf(w, v.w, acc[4 * c + 3]);
+            }
+        }
+        const float inv = l > 0.f ? p.out_scale / l : 0.f;
+        __nv_bfloat16 *o = reinterpret_cast<__nv_bfloat16 *>(p.out) + cut.b * p.out_stride[0] + t * p.out_stride[1] +
+                           h * p.out_stride[2];
+#pragma unroll
+        for (int c = 0; c < V / 4; ++c) {
+            uint2 v;
+            v.x = pack_bf16x2(acc[4 * c] * inv, acc[4 * c + 1] * inv);
+            v.y = pack_bf16x2(acc[4 * c + 2] * inv, acc[4 * c + 3] * inv);
+            reinterpret_cast<uint2 *>(o)[c * 32 + lane] = v;
+        }
+        if (lane == 0 && p.lse)
+            p.lse[cut.b * p.lse_stride[0] + t * p.lse_stride[1] + h * p.lse_stride[2]] =
+                l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : kNegInf;
+    }
+}
+
+template <int D, int NT>
+cudaError_t launch_tree_t(const TreeParams &p, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                          cudaStream_t stream, int *launches) {
+    using C = TreeCfg<D, NT>;
+    static bool configured[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (!configured[dev & 63]) {
+        e = cudaFuncSetAttribute(tree_decode_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+        if (e != cudaSuccess) return e;
+        configured[dev & 63] = true;
+    }
+    tree_decode_kernel<D, NT><<<p.grid, C::kThreads, C::kSmemBytes, stream>>>(p, tq, tk, tv);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    ++*launches;
+    e = launch_after_previous(tree_merge_kernel<D, NT>, dim3(NT * 4, p.grid), dim3(256), 0, stream, p);
+    if (e != cudaSuccess) return e;
+    ++*launches;
+    return cudaSuccess;
+}
 
 template <bool kKv8>
 __device__ __forceinline__ float cache_value(const void *base, int64_t i) {
@@ -94,14 +917,32 @@ __global__ void __launch_bounds__(128) tree_decode_simple_kernel(const __grid_co
 
 }  // namespace
 
-cudaError_t launch_tree_decode(const TreeParams &p, cudaStream_t stream, int *launches) {
-    const unsigned grid = (unsigned)((int64_t)p.B * p.T * p.Hq);
-    if (p.D == 128 && p.kv8) tree_decode_simple_kernel<128, true><<<grid, 128, 0, stream>>>(p);
-    else if (p.D == 128) tree_decode_simple_kernel<128, false><<<grid, 128, 0, stream>>>(p);
-    else if (p.D == 256) tree_decode_simple_kernel<256, false><<<grid, 128, 0, stream>>>(p);
-    else return cudaErrorInvalidValue;
-    *launches = 1;
-    return cudaGetLastError();
+size_t tree_workspace_bytes(int head_dim, int grid) {
+    const int rows = head_dim == 128 ? 256 : 128;
+    return (size_t)grid * (2 * (size_t)rows * (head_dim * 4 + 8) + sizeof(TreeCut));
+}
+
+void tree_place_workspace(TreeParams *p, void *ws) {
+    const int64_t rows = p->D == 128 ? 256 : 128;
+    char *at = static_cast<char *>(ws);
+    p->part_o = reinterpret_cast<float *>(at);
+    at += (int64_t)p->grid * 2 * rows * p->D * 4;
+    p->part_ml = reinterpret_cast<float2 *>(at);
+    at += (int64_t)p->grid * 2 * rows * 8;
+    p->cuts = reinterpret_cast<TreeCut *>(at);
+}
+
+cudaError_t launch_tree_decode(const TreeParams &p, const CUtensorMap &tq, const CUtensorMap &tk,
+                               const CUtensorMap &tv, cudaStream_t stream, int *launches) {
+    *launches = 0;
+    if (p.kv8) {
+        tree_decode_simple_kernel<128, true><<<(unsigned)((int64_t)p.B * p.T * p.Hq), 128, 0, stream>>>(p);
+        *launches = 1;
+        return cudaGetLastError();
+    }
+    if (p.D == 256) return launch_tree_t<256, 1>(p, tq, tk, tv, stream, launches);
+    if (p.row_tiles > 1) return launch_tree_t<128, 2>(p, tq, tk, tv, stream, launches);
+    return launch_tree_t<128, 1>(p, tq, tk, tv, stream, launches);
 }
 
 }  // namespace fw
