@@ -80,8 +80,8 @@ struct TreeCfg {
     static constexpr int kBarSFull = kBarQEmpty + 1;            // [NT][kSB]
     static constexpr int kBarPHalf = kBarSFull + NT * kSB;      // [NT][kSB]
     static constexpr int kBarPFull = kBarPHalf + NT * kSB;      // [NT][kSB]
-    static constexpr int kBarPvDone = kBarPFull + NT * kSB;     // [NT]
-    static constexpr int kBarIssued = kBarPvDone + NT;          // [NT]
+    static constexpr int kBarPvDone = kBarPFull + NT * kSB;     // [NT][kSB]
+    static constexpr int kBarIssued = kBarPvDone + NT * kSB;    // [NT]
     static constexpr int kBarDrain = kBarIssued + NT;           // [NT]
     static constexpr int kBarSchedFull = kBarDrain + NT;
     static constexpr int kBarSchedEmpty = kBarSchedFull + kSched;
@@ -200,8 +200,10 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
         for (int i = 0; i < C::kSlots; ++i) { mbar_init(&slot_full[i], 1); mbar_init(&slot_empty[i], NT); }
         mbar_init(q_full, 1);
         mbar_init(q_empty, NT);
-        for (int i = 0; i < NT * kSB; ++i) { mbar_init(&s_full[i], 1); mbar_init(&p_half[i], 4); mbar_init(&p_full[i], 4); }
-        for (int i = 0; i < NT; ++i) { mbar_init(&pv_done[i], 1); mbar_init(&issued[i], 1); mbar_init(&drain[i], 1); }
+        for (int i = 0; i < NT * kSB; ++i) {
+            mbar_init(&s_full[i], 1); mbar_init(&p_half[i], 4); mbar_init(&p_full[i], 4); mbar_init(&pv_done[i], 1);
+        }
+        for (int i = 0; i < NT; ++i) { mbar_init(&issued[i], 1); mbar_init(&drain[i], 1); }
         for (int i = 0; i < C::kSched; ++i) { mbar_init(&sched_full[i], 1); mbar_init(&sched_empty[i], C::kSchedReaders); }
         *abort_flag = 0;
         fence_barrier_init();
@@ -503,7 +505,7 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
                     // (a wait between pushes lets the tensor pipe run dry); else
                     // this tile's V is handed back first.
                     if (paired) push_qk(rk(j + kSB), buf);
-                    if (kSB == 2 || j == n - 1) mma_commit(&pv_done[x]);
+                    if (kSB == 2 || j == n - 1) mma_commit(&pv_done[x * kSB + buf]);
                     release_tile(rv(j));
                     if (next) {
                         if (!paired) {
@@ -550,6 +552,10 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
         const int row = q4 * 32 + lane;
         const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
         const bool scale_pos = p.scale_log2 >= 0.f;
+        // Two S buffers: PV of step i completes phase i / 2 of its buffer's barrier.
+        // (A barrier per step could be one phase behind or one ahead of a wait,
+        // which a parity does not tell apart.)
+        auto wait_pv = [&](uint32_t step) { mbar_wait(&pv_done[x * kSB + step % kSB], (step / kSB) & 1, wc); };
         uint32_t steps = 0, pieces = 0, rp = 0;
         for (int k = 0;; ++k) {
             const TreeUnit *ur = wait_unit(k);
@@ -573,6 +579,8 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
                 const int buf = steps % kSB;
                 const int key0 = (u.tile0 + j) * kKvTile;
                 const bool drafts = key0 + kKvTile > base;    // the tile reaches past the committed keys
+                mbar_wait(&s_full[x * kSB + buf], (steps / kSB) & 1, wc);
+                tc_fence_after();
                 if (drafts) {
                     // Values of keys nobody sees must not meet a zero weight: they
                     // may be NaN.  A key is seen when some draft's mask shows it.
@@ -592,6 +600,13 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
                     const uint32_t mine = sw[q4] | sw[4 + q4] | sw[8 + q4] | sw[12 + q4];   // word q4: this warp's keys
                     if (__any_sync(0xffffffffu, !(mine >> lane & 1))) {
                         const uint32_t r = r0 + (uint32_t)(pos_v<kSB>(j, u.ntiles) * TS);
+                        // A parity wait needs the slot's copy before V_j to have landed.
+                        // S_j there proves that for all copies up to K_j; with two slots
+                        // to a tile the one before V_j's may be V_{j-1}, which its
+                        // finished product proves.
+                        if constexpr (TS == 2) {
+                            if (steps > 0) wait_pv(steps - 1);
+                        }
 #pragma unroll
                         for (int s = 0; s < TS; ++s) {
                             const uint32_t sl = (r + s) % C::kSlots;
@@ -609,8 +624,6 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
                         fence_proxy_async_smem();
                     }
                 }
-                mbar_wait(&s_full[x * kSB + buf], (steps / kSB) & 1, wc);
-                tc_fence_after();
                 if (!warp_live) {                         // rows of padding: whatever lies there
                     tc_fence_before();
                     __syncwarp();
@@ -658,7 +671,7 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
                         // With one S buffer, S_j there means PV_{j-1} is done; with two
                         // it may still run.
                         if constexpr (kSB == 2) {
-                            mbar_wait(&pv_done[x], (steps - 1) & 1, wc);
+                            wait_pv(steps - 1);
                             tc_fence_after();
                         }
 #pragma unroll 1
@@ -704,11 +717,12 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
             }
             // ------------------------------------------------------ epilogue
             ++pieces;
-            // Two S buffers: the last score tile proves all but the last two PVs
-            // done, so their phases are waited for one after the other (a wait on
-            // the last alone could pass two phases early).
-            if (kSB == 2 && steps >= 2) mbar_wait(&pv_done[x], (steps - 2) & 1, wc);
-            mbar_wait(&pv_done[x], ((kSB == 2 ? steps : pieces) - 1) & 1, wc);
+            if constexpr (kSB == 2) {
+                if (steps >= 2) wait_pv(steps - 2);
+                wait_pv(steps - 1);
+            } else {
+                mbar_wait(&pv_done[x], (pieces - 1) & 1, wc);
+            }
             tc_fence_after();
             if (warp_live) {
                 const float inv = l_sum > 0.f ? p.out_scale / l_sum : 0.f;

@@ -165,6 +165,20 @@ def test_long_rows_are_split_and_merged(fw, D, kv8):
     run_and_check(fw, make(2, 9, 8, 2, D, 64, [9000, 77], None, "tree", kv8=kv8, seed=5), "long")
 
 
+@pytest.mark.parametrize("D,kv8", [(128, False), (128, True), (256, False)])
+@pytest.mark.parametrize("T,Hq,Hkv", [(24, 16, 16), (40, 16, 4)])
+def test_many_pieces_per_cta(fw, D, kv8, T, Hq, Hkv):
+    """Several units to a CTA, every one with a tile that holds drafts while the
+    copies of the next tiles and units are in flight."""
+    lens = [150 + 211 * i % 1800 for i in range(10)]
+    x = make(10, T, Hq, Hkv, D, 32, lens, [T - i for i in range(10)], "tree", kv8=kv8, seed=43)
+    first = run_and_check(fw, x, "many pieces")
+    g = on_gpu(x)
+    for _ in range(20):
+        again = fw.paged_decode_tree(**g)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
 @pytest.mark.parametrize("scale", [-0.7, 0.0, 1.5])
 def test_scales_that_move_the_maximum(fw, scale):
     """A large scale makes later tiles outgrow what the first ones showed; a
