@@ -16,10 +16,12 @@ def _f64(t: torch.Tensor) -> np.ndarray:
 
 def tree_attention(q, k_cache, v_cache, block_table, seq_lens, tree_mask, scale, draft_lens=None, k_scale=1.0,
                    v_scale=1.0):
-    """Returns (out, lse, absv, reach): the outputs [B, T, Hq, D], the natural
-    log-sum-exp [B, T, Hq], the softmax-weighted mean of |v| per output column,
-    and per row the largest sum_i |q_i k_i| * scale over its visible keys (what
-    the rounding of an FP32 score scales with)."""
+    """Returns (out, lse, absv, reach, spread): the outputs [B, T, Hq, D], the
+    natural log-sum-exp [B, T, Hq], the softmax-weighted mean of |v| per output
+    column, per row the largest sum_i |q_i k_i| * scale over its visible keys
+    (what the rounding of an FP32 score scales with), and, for 8-bit caches, the
+    largest max_i |q_i| * sum_i |k_i| * scale (what a score is off by when every
+    query element is off by a fraction of the row's largest; 0 otherwise)."""
     B, T, Hq, D = q.shape
     ps, Hkv = k_cache.shape[1], k_cache.shape[2]
     G = Hq // Hkv
@@ -27,7 +29,8 @@ def tree_attention(q, k_cache, v_cache, block_table, seq_lens, tree_mask, scale,
     bt, n_all, mask = block_table.cpu().numpy(), seq_lens.cpu().numpy(), tree_mask.cpu().numpy()
     d_all = np.full(B, T) if draft_lens is None else draft_lens.cpu().numpy()
     out, absv = np.zeros((B, T, Hq, D)), np.zeros((B, T, Hq, D))
-    lse, reach = np.full((B, T, Hq), -np.inf), np.zeros((B, T, Hq))
+    lse, reach, spread = np.full((B, T, Hq), -np.inf), np.zeros((B, T, Hq)), np.zeros((B, T, Hq))
+    kv8 = k_cache.dtype == torch.float8_e4m3fn
     for b in range(B):
         n = int(n_all[b])
         d = max(0, min(int(d_all[b]), T, n))
@@ -50,7 +53,9 @@ def tree_attention(q, k_cache, v_cache, block_table, seq_lens, tree_mask, scale,
                 out[b, t, h] = e @ v / z
                 absv[b, t, h] = e @ np.abs(v) / z
                 reach[b, t, h] = (np.abs(k) @ np.abs(Q[b, t, h])).max() * abs(scale)
-    return out, lse, absv, reach
+                if kv8:
+                    spread[b, t, h] = np.abs(Q[b, t, h]).max() * np.abs(k).sum(1).max() * abs(scale)
+    return out, lse, absv, reach, spread
 
 
 def tree_mask(parents, draft_lens=None):

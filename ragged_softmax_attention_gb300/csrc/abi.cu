@@ -1157,13 +1157,20 @@ fw_status_t fw_paged_decode_tree(const fw_tensor_t *q, const fw_tensor_t *k_cach
         const uint64_t strides[3] = {(uint64_t)q->stride[2] * 2, (uint64_t)q->stride[1] * 2, (uint64_t)q->stride[0] * 2};
         const uint32_t box[4] = {64, (uint32_t)(p.G < 128 ? p.G : 128), (uint32_t)p.tile_tokens, 1};
         if (fw_status_t s = encode_bf16(&tq, q->data, 4, dims, strides, box, "q")) return s;
-        const uint32_t kbox[4] = {64, 1, (uint32_t)(p.ps < fw::kKvTile ? p.ps : fw::kKvTile), 1};
+        const uint64_t esz = p.kv8 ? 1 : 2;
+        const uint32_t kbox[4] = {p.kv8 ? 128u : 64u, 1, (uint32_t)(p.ps < fw::kKvTile ? p.ps : fw::kKvTile), 1};
         const fw_tensor_t *caches[2] = {k_cache, v_cache};
         for (int i = 0; i < 2; ++i) {
             const fw_tensor_t *c = caches[i];
             const uint64_t cd[4] = {(uint64_t)p.D, (uint64_t)p.Hkv, (uint64_t)p.ps, (uint64_t)p.num_pages};
-            const uint64_t cs[3] = {(uint64_t)c->stride[2] * 2, (uint64_t)c->stride[1] * 2, (uint64_t)c->stride[0] * 2};
-            if (fw_status_t s = encode_bf16(i ? &tv : &tk, c->data, 4, cd, cs, kbox, i ? "v_cache" : "k_cache")) return s;
+            const uint64_t cs[3] = {(uint64_t)c->stride[2] * esz, (uint64_t)c->stride[1] * esz, (uint64_t)c->stride[0] * esz};
+            // As in the decode: a 128-byte FP8 row's neighbour is another head's,
+            // worth fetching with it only when the heads ride on the CTA index.
+            const bool narrow = p.kv8 && cs[1] != 128 && !p.ride;
+            if (fw_status_t s = encode_map(i ? &tv : &tk, p.kv8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                                           c->data, 4, cd, cs, kbox, i ? "v_cache" : "k_cache",
+                                           narrow ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
+                return s;
         }
     }
     int launched = 0;

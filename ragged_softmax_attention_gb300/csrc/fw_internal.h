@@ -244,6 +244,9 @@ cudaError_t launch_decode_fp8(const DecodeParams &p, const CUtensorMap &tm_q, co
 // tables, the move of the accepted path
 cudaError_t launch_tree_decode(const TreeParams &p, const CUtensorMap &tm_q, const CUtensorMap &tm_k,
                                const CUtensorMap &tm_v, cudaStream_t stream, int *launches);
+cudaError_t launch_tree_decode_fp8(const TreeParams &p, const CUtensorMap &tm_q, const CUtensorMap &tm_k,
+                                   const CUtensorMap &tm_v, cudaStream_t stream, int *launches);
+cudaError_t launch_tree_merge(const TreeParams &p, int row_tiles, cudaStream_t stream);
 size_t tree_workspace_bytes(int head_dim, int grid);
 void tree_place_workspace(TreeParams *p, void *ws);
 cudaError_t launch_tree_mask(const TreeMaskParams &p, cudaStream_t stream);

@@ -1,0 +1,304 @@
+// What the tree-decode kernels (BF16 and FP8 caches) share: the rows of a unit,
+// the walk over a CTA's range of the planned sequence, mask bits, the merge of
+// the pieces of cut units.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "decode_common.cuh"
+#include "fw_internal.h"
+#include "fw_ptx.cuh"
+
+namespace fw {
+namespace tree {
+
+using dec::ceil_div_i;
+using dec::warp_max;
+using dec::warp_wait;
+constexpr float kNegInf = -__builtin_huge_valf();
+// The base of a row's exponentials moves only when its maximum rose by more
+// than this many log2 units, so every weight is at most 2^8.
+constexpr float kRescaleSlack = 8.0f;
+constexpr int kErrInvalid = 1;     // FW_ERR_INVALID_ARG
+
+// One piece: a unit's key tiles inside one CTA range.  64 bytes.
+struct alignas(16) TreeUnit {
+    int b;             // request, -1 ends the CTA's work
+    int g;             // KV head
+    int rt0, nrt;      // first row tile and how many
+    int n, d;          // keys and drafts of the request
+    int tile0, ntiles; // key tiles
+    int part;          // partial slot, -1: the whole unit, written to the outputs
+    int pad_[7];
+};
+static_assert(sizeof(TreeUnit) == 64, "a unit record fills one 64-byte slot");
+
+// Keys and drafts of request b, both within what the call can hold.
+__device__ __forceinline__ void tree_row(const TreeParams &p, int b, int &n, int &d) {
+    n = min(max(__ldg(p.seq_lens + b), 0), p.max_pages * p.ps);
+    d = p.draft_lens ? min(max(__ldg(p.draft_lens + b), 0), p.T) : p.T;
+    d = min(d, n);
+}
+
+// Units of a request in the planned sequence (of one KV head when the heads
+// ride on the CTA index).
+template <int NT>
+__device__ __forceinline__ int tree_units(const TreeParams &p, int d) {
+    const int tiles = p.head_chunks > 1 ? d * p.head_chunks : ceil_div_i(d, p.tile_tokens);
+    return ceil_div_i(tiles, NT) * (p.ride ? 1 : p.Hkv);
+}
+
+// The (draft, head) of row r of row tile rt; false for padding.
+__device__ __forceinline__ bool tree_tile_row(const TreeParams &p, int rt, int g, int d, int r, int &t, int &h) {
+    if (p.head_chunks > 1) {
+        t = rt / p.head_chunks;
+        const int hh = (rt - t * p.head_chunks) * 128 + r;
+        h = g * p.G + hh;
+        return hh < p.G && t < d;
+    }
+    const int tt = r / p.G;
+    t = rt * p.tile_tokens + tt;
+    h = g * p.G + (r - tt * p.G);
+    return tt < p.tile_tokens && t < d;
+}
+
+// Bits of the 32 keys from draft ds on (ds < 0: committed keys first) that the
+// mask row shows, among the request's d drafts.
+__device__ __forceinline__ uint32_t draft_bits(const int32_t *row, int ds, int d) {
+    if (ds <= -32) return 0xffffffffu;
+    if (ds >= d) return 0u;
+    uint32_t v;
+    if (ds < 0) {
+        v = ((uint32_t)__ldg(row) << -ds) | ((1u << -ds) - 1u);
+    } else {
+        const int w = ds >> 5;
+        const uint32_t lo = (uint32_t)__ldg(row + w);
+        const uint32_t hi = (w + 1) * 32 < d ? (uint32_t)__ldg(row + w + 1) : 0u;
+        v = __funnelshift_r(lo, hi, ds & 31);
+    }
+    const int left = d - ds;
+    return left < 32 ? v & ((1u << left) - 1u) : v;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+    __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<uint32_t *>(&v);
+}
+
+// Ring positions, in units of whole K or V tiles, of a piece of n key tiles
+// when QK runs L tiles ahead of PV: K_0 .. K_{L-1}, then V_j K_{j+L}.
+template <int L>
+__device__ __forceinline__ int pos_v(int j, int n) { return min(L, n) + j + min(j, max(0, n - L)); }
+template <int L>
+__device__ __forceinline__ int pos_k(int j, int n) { return j < L ? j : pos_v<L>(j - L, n) + 1; }
+
+
+// The planned sequence: request b takes units * (piece_cost + tiles) slots.
+// Every thread sums a run of requests; the one whose run holds this CTA's first
+// slot looks the request up.  plan[0] = slots in all, plan[1], plan[2] = start
+// and number of the request holding the CTA's first slot, plan[3] = span.
+// Ends with every thread past a barrier but plan not yet published.
+template <int NT>
+__device__ __forceinline__ void plan_range(const TreeParams &p, long long *plan, long long *scan) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nthreads = blockDim.x;
+    const int per = (p.B + nthreads - 1) / nthreads;
+    auto row_slots = [&](int b) -> long long {
+        int n, d;
+        tree_row(p, b, n, d);
+        return (long long)tree_units<NT>(p, d) * (p.piece_cost + ceil_div_i(n, kKvTile));
+    };
+    long long mine = 0;
+    const int b0 = threadIdx.x * per;
+    for (int i = 0; i < per && b0 + i < p.B; ++i) mine += row_slots(b0 + i);
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) scan[warp] = incl;
+    __syncthreads();
+    long long before = incl - mine, total = 0;
+    for (int w = 0; w < nthreads / 32; ++w) {
+        if (w < warp) before += scan[w];
+        total += scan[w];
+    }
+    const int nranges = p.ride ? (int)gridDim.x / p.Hkv : (int)gridDim.x;
+    const long long span = max((long long)p.min_span, (total + nranges - 1) / nranges);
+    const long long first = span * (p.ride ? (int)blockIdx.x / p.Hkv : (int)blockIdx.x);
+    if (mine > 0 && first >= before && first < before + mine) {
+        int b = b0;
+        for (long long s; first >= before + (s = row_slots(b)); ++b) before += s;
+        plan[1] = before;
+        plan[2] = b;
+    }
+    if (threadIdx.x == 0) { plan[0] = total; plan[3] = span; }
+}
+
+// Walks the pieces of this CTA's range (the producer warp, all lanes alike).
+template <int NT>
+struct TreeWalk {
+    long long total, span, pos, end, pb0;
+    int range, b, n, d, units, tiles;
+    TreeCut cut;
+
+    __device__ void open_row(const TreeParams &p) {
+        tree_row(p, b, n, d);
+        units = tree_units<NT>(p, d);
+        tiles = ceil_div_i(n, kKvTile);
+    }
+    __device__ void init(const TreeParams &p, const long long *plan) {
+        total = plan[0];
+        span = plan[3];
+        range = p.ride ? (int)blockIdx.x / p.Hkv : (int)blockIdx.x;
+        pos = span * range;
+        end = min(total, pos + span);
+        cut = TreeCut{};
+        if (pos < end) {
+            pb0 = plan[1];
+            b = (int)plan[2];
+            open_row(p);
+        }
+    }
+    __device__ void next(const TreeParams &p, TreeUnit &u) {     // u.b = -1 at the end
+        u.b = -1;
+        while (pos < end) {
+            const int v = p.piece_cost + tiles;
+            const long long row = (long long)units * v;
+            if (pos >= pb0 + row) { pb0 += row; ++b; open_row(p); continue; }
+            const int ui = (int)((pos - pb0) / v);
+            const int vl = (int)(pos - pb0 - (long long)ui * v);
+            if (vl < p.piece_cost) { pos += p.piece_cost - vl; continue; }
+            const int tl = vl - p.piece_cost;
+            const int th = (int)min((long long)tiles, tl + (end - pos));
+            const long long ustart = pb0 + (long long)ui * v + p.piece_cost;
+            u.b = b;
+            const int per_head = p.ride ? units : units / p.Hkv;
+            u.g = p.ride ? (int)blockIdx.x % p.Hkv : ui / per_head;
+            const int rts = p.head_chunks > 1 ? d * p.head_chunks : ceil_div_i(d, p.tile_tokens);
+            u.rt0 = (p.ride ? ui : ui - u.g * per_head) * NT;
+            u.nrt = min(NT, rts - u.rt0);
+            u.n = n;
+            u.d = d;
+            u.tile0 = tl;
+            u.ntiles = th - tl;
+            u.part = -1;
+            if (tl > 0) {
+                u.part = 2 * blockIdx.x;
+            } else if (th < tiles) {
+                u.part = 2 * blockIdx.x + 1;
+                cut.count = (int)((ustart + tiles - 1) / span) - range + 1;
+                cut.b = b; cut.g = u.g; cut.rt0 = u.rt0; cut.nrt = u.nrt; cut.d = d;
+            }
+            pos += th - tl;
+            return;
+        }
+    }
+};
+
+// Zero output and -inf LSE for the rows past a request's drafts, requests
+// blockIdx.x, blockIdx.x + grid, ... (one warp).
+template <int D>
+__device__ __forceinline__ void write_padding_rows(const TreeParams &p) {
+    const int lane = threadIdx.x & 31;
+    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+        int n, d;
+        tree_row(p, b, n, d);
+        const int rows = (p.T - d) * p.Hq;
+        for (int i = lane; i < rows * (D / 8); i += 32) {
+            const int r = i / (D / 8), c = i - r * (D / 8);
+            const int t = d + r / p.Hq, h = r % p.Hq;
+            __nv_bfloat16 *o = reinterpret_cast<__nv_bfloat16 *>(p.out) + b * p.out_stride[0] +
+                               t * p.out_stride[1] + h * p.out_stride[2];
+            reinterpret_cast<uint4 *>(o)[c] = make_uint4(0, 0, 0, 0);
+            if (c == 0 && p.lse) p.lse[b * p.lse_stride[0] + t * p.lse_stride[1] + h * p.lse_stride[2]] = kNegInf;
+        }
+    }
+}
+
+// This warp's word of "some draft of the request sees key" over the 128 keys of
+// a tile: bit l of word w is key 32 w + l.  128 threads (`id`: their named
+// barrier) share the drafts; `words` is 16 words of shared memory that nobody
+// else writes before the next call but one.
+__device__ __forceinline__ uint32_t seen_keys(const TreeParams &p, const TreeUnit &u, int key0, int thread, uint32_t id,
+                                              uint32_t *words) {
+    const int lane = thread & 31, w4 = thread >> 5, base = u.n - u.d;
+    uint32_t seen[4] = {0, 0, 0, 0};
+    for (int t = thread; t < u.d; t += 128) {
+        const int32_t *mr = p.mask + u.b * p.mask_stride[0] + t * p.mask_stride[1];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) seen[w] |= draft_bits(mr, key0 + 32 * w - base, u.d);
+    }
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        seen[w] = __reduce_or_sync(0xffffffffu, seen[w]);
+        if (lane == 0) words[w4 * 4 + w] = seen[w];
+    }
+    named_bar_sync(id, 128);
+    return words[w4] | words[4 + w4] | words[8 + w4] | words[12 + w4];
+}
+
+// This thread's row of a finished piece: its output and LSE, or its partial.
+// `load` reads 32 columns of O (warp-collective).
+template <int D, int NT, typename Load>
+__device__ __forceinline__ void write_row(const TreeParams &p, const TreeUnit &u, int x, int row, bool live, int t,
+                                          int h, float base2, float l_sum, Load load) {
+    const float inv = l_sum > 0.f ? p.out_scale / l_sum : 0.f;
+    __nv_bfloat16 *orow = reinterpret_cast<__nv_bfloat16 *>(p.out) + u.b * p.out_stride[0] + t * p.out_stride[1] +
+                          h * p.out_stride[2];
+    const int64_t prow = (int64_t)u.part * (NT * 128) + x * 128 + row;
+    float4 *part = reinterpret_cast<float4 *>(p.part_o + prow * D);
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+        float o[32];
+        load(c, o);
+        if (!live) continue;
+        if (u.part < 0) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                uint4 v;
+                v.x = l_sum > 0.f ? pack_bf16x2(o[8 * w + 0] * inv, o[8 * w + 1] * inv) : 0u;
+                v.y = l_sum > 0.f ? pack_bf16x2(o[8 * w + 2] * inv, o[8 * w + 3] * inv) : 0u;
+                v.z = l_sum > 0.f ? pack_bf16x2(o[8 * w + 4] * inv, o[8 * w + 5] * inv) : 0u;
+                v.w = l_sum > 0.f ? pack_bf16x2(o[8 * w + 6] * inv, o[8 * w + 7] * inv) : 0u;
+                *reinterpret_cast<uint4 *>(orow + c * 32 + w * 8) = v;
+            }
+        } else {
+#pragma unroll
+            for (int w = 0; w < 8; ++w)
+                part[c * 8 + w] = make_float4(o[4 * w], o[4 * w + 1], o[4 * w + 2], o[4 * w + 3]);
+        }
+    }
+    if (!live) return;
+    if (u.part >= 0) p.part_ml[prow] = make_float2(base2, l_sum);
+    else if (p.lse)
+        p.lse[u.b * p.lse_stride[0] + t * p.lse_stride[1] + h * p.lse_stride[2]] =
+            l_sum > 0.f ? (base2 + log2f(l_sum)) * 0.69314718055994531f : kNegInf;
+}
+
+
+// One launch for the pieces, one for the merge of cut units.
+template <typename Kernel>
+inline cudaError_t launch_pieces(Kernel kernel, int NT, int threads, size_t smem, const TreeParams &p,
+                                 const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                                 cudaStream_t stream, bool (&configured)[64], int *launches) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (!configured[dev & 63]) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        configured[dev & 63] = true;
+    }
+    kernel<<<p.grid, threads, smem, stream>>>(p, tq, tk, tv);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    ++*launches;
+    e = launch_tree_merge(p, NT, stream);
+    if (e != cudaSuccess) return e;
+    ++*launches;
+    return cudaSuccess;
+}
+
+}  // namespace tree
+}  // namespace fw

@@ -1,0 +1,650 @@
+// Paged decode of a tree of drafted tokens over an FP8 E4M3 cache, sm_103a.
+// Units, ranges, pieces and the merge are those of the BF16 kernel
+// (tree_decode_kernel.cu); head dim 128.
+//
+// An SM's share of HBM delivers an E4M3 K/V tile of 128 keys (32 KiB) in ~1,350
+// cycles, half a BF16 tile's, so neither the tensor core nor shared memory can
+// afford to widen both caches:
+//   S = Q K^T   kind::f8f6f4 on the E4M3 bytes as they land.  Each BF16 query
+//               row is scaled by a power of two (largest magnitude in
+//               [128, 256)) and carried as two E4M3 terms, hi + mid, exact for
+//               every element down to 2^-10 of the row's largest; below, an
+//               element is off by at most 2^-17 of the largest.  Two terms of
+//               K = 32 products take the tensor core as long as one BF16 pass.
+//   O += P V    kind::f16 on FP16: four warps widen each V tile (E4M3 is exact
+//               in FP16) where it landed -- a key's 128 bytes lie in the second
+//               half of a 32 KiB slot and become 256, the thread that owns the
+//               key reads them all first.  P is rounded to FP16, scaled by 2^7
+//               so that weights down to 2^-21 of the largest keep 11 bits (base
+//               slack of 2^8 and that factor stay below FP16's 2^16).
+// The same warps split the queries, ahead of the softmax, and write zeros for
+// the values of keys nobody sees.
+//
+// Warp roles: 0 copies, 1 (and 2) issues MMAs, 3 writes the rows that see
+// nothing, 4-7 convert, 8.. softmax.
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "tree_common.cuh"
+
+namespace fw {
+namespace {
+
+using namespace tree;
+
+constexpr int D = 128;
+constexpr float kPShift = 7.0f;     // P carries 2^7
+
+// kind::f8f6f4, A and B E4M3 K-major, FP32 accumulation.
+constexpr uint32_t kIdescQK = (1u << 4) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+// kind::f16, A and B FP16, B MN-major, FP32 accumulation.
+constexpr uint32_t kIdescPV = (1u << 4) | (1u << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+
+template <int NT_>
+struct F8TreeCfg {
+    static constexpr int NT = NT_;
+    static constexpr int kSB = NT == 2 ? 1 : 2;
+    static constexpr int kQBytes = 128 * D * 2;                 // BF16 rows, then their two E4M3 terms in place
+    static constexpr int kKBytes = 128 * D;
+    static constexpr int kVBytes = 128 * D * 2;                 // FP16 values; E4M3 lands in the second half
+    static constexpr int kHalf = 128 * 128;
+    static constexpr int kKSlots = 4;
+    static constexpr int kVSlots = NT == 2 ? 3 : 4;
+    static constexpr int kOffQ = 0;
+    static constexpr int kOffK = kOffQ + NT * kQBytes;
+    static constexpr int kOffV = kOffK + kKSlots * kKBytes;
+    static constexpr int kOffBar = kOffV + kVSlots * kVBytes;
+    static constexpr int kSched = 4;
+    static constexpr int kBarKFull = 0;
+    static constexpr int kBarKEmpty = kBarKFull + kKSlots;
+    static constexpr int kBarVRaw = kBarKEmpty + kKSlots;       // E4M3 values landed
+    static constexpr int kBarVFull = kBarVRaw + kVSlots;        // widened
+    static constexpr int kBarVEmpty = kBarVFull + kVSlots;
+    static constexpr int kBarQFull = kBarVEmpty + kVSlots;
+    static constexpr int kBarQEmpty = kBarQFull + 1;
+    static constexpr int kBarQReady = kBarQEmpty + 1;           // [kSched] terms and exponents of unit k written
+    static constexpr int kBarSFull = kBarQReady + kSched;       // [NT][kSB]
+    static constexpr int kBarPHalf = kBarSFull + NT * kSB;
+    static constexpr int kBarPFull = kBarPHalf + NT * kSB;
+    static constexpr int kBarPvDone = kBarPFull + NT * kSB;
+    static constexpr int kBarIssued = kBarPvDone + NT * kSB;    // [NT]
+    static constexpr int kBarDrain = kBarIssued + NT;           // [NT]
+    static constexpr int kBarSchedFull = kBarDrain + NT;
+    static constexpr int kBarSchedEmpty = kBarSchedFull + kSched;
+    static constexpr int kNumBars = kBarSchedEmpty + kSched;
+    static constexpr int kOffSched = (kOffBar + kNumBars * 8 + 63) / 64 * 64;
+    static constexpr int kOffSeen = kOffSched + kSched * 64;    // [2][16 words]
+    static constexpr int kOffPlan = kOffSeen + 128;
+    static constexpr int kOffScan = kOffPlan + 32;              // [16]
+    static constexpr int kOffQScale = kOffScan + 128;           // [kSched][NT][128 halves]: exponents of the rows
+    static constexpr int kOffMisc = kOffQScale + kSched * NT * 128;
+    static constexpr int kSmemBytes = kOffMisc + 16 + 1024;
+    static_assert(kSmemBytes <= 232448, "shared memory budget of one CTA exceeded");
+    static constexpr int kThreads = 256 + NT * 128;
+    static constexpr int kSchedReaders = NT + 4 + 4 * NT;
+    // Launched at 168 (NT = 1: 384 threads) or 128 (NT = 2: 512) registers a
+    // thread: 128 x 80 + 128 x 112 + 128 x 208 = 51200 <= 64512 and
+    // 128 x 72 + 128 x 96 + 256 x 168 = 64512 <= 65536.
+    static constexpr uint32_t kRegsControl = NT == 2 ? 72 : 80;
+    static constexpr uint32_t kRegsConvert = NT == 2 ? 96 : 112;
+    static constexpr uint32_t kRegsSoftmax = NT == 2 ? 168 : 208;
+    static constexpr uint32_t kRegsLaunch = NT == 2 ? 128 : 168;
+    static_assert(128 * kRegsControl + 128 * kRegsConvert + NT * 128 * kRegsSoftmax <= kThreads * kRegsLaunch,
+                  "register split");
+    __device__ static constexpr uint32_t s_col(int x, int buf) { return (uint32_t)(x * kSB + buf) * 128u; }
+    __device__ static constexpr uint32_t o_col(int x) { return 256u + (uint32_t)x * 128u; }
+};
+
+// Four E4M3 values (one word) as four FP16, two words.
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
+    const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
+    lo = (uint32_t)a.x | ((uint32_t)a.y << 16);
+    hi = (uint32_t)b.x | ((uint32_t)b.y << 16);
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+template <int NT>
+__global__ void __launch_bounds__(F8TreeCfg<NT>::kThreads, 1)
+tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUtensorMap tm_q,
+                       const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
+    using C = F8TreeCfg<NT>;
+    constexpr int kSB = C::kSB;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *sQ = smem + C::kOffQ;
+    uint8_t *sK = smem + C::kOffK;
+    uint8_t *sV = smem + C::kOffV;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
+    uint64_t *k_full = bars + C::kBarKFull;
+    uint64_t *k_empty = bars + C::kBarKEmpty;
+    uint64_t *v_raw = bars + C::kBarVRaw;
+    uint64_t *v_full = bars + C::kBarVFull;
+    uint64_t *v_empty = bars + C::kBarVEmpty;
+    uint64_t *q_full = bars + C::kBarQFull;
+    uint64_t *q_empty = bars + C::kBarQEmpty;
+    uint64_t *q_ready = bars + C::kBarQReady;
+    uint64_t *s_full = bars + C::kBarSFull;
+    uint64_t *p_half = bars + C::kBarPHalf;
+    uint64_t *p_full = bars + C::kBarPFull;
+    uint64_t *pv_done = bars + C::kBarPvDone;
+    uint64_t *issued = bars + C::kBarIssued;
+    uint64_t *drain = bars + C::kBarDrain;
+    uint64_t *sched_full = bars + C::kBarSchedFull;
+    uint64_t *sched_empty = bars + C::kBarSchedEmpty;
+    TreeUnit *sched = reinterpret_cast<TreeUnit *>(smem + C::kOffSched);
+    uint32_t *seen_words = reinterpret_cast<uint32_t *>(smem + C::kOffSeen);
+    long long *plan = reinterpret_cast<long long *>(smem + C::kOffPlan);
+    long long *scan = reinterpret_cast<long long *>(smem + C::kOffScan);
+    int8_t *q_exp = reinterpret_cast<int8_t *>(smem + C::kOffQScale);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffMisc);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::kOffMisc + 4);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kKSlots; ++i) { mbar_init(&k_full[i], 1); mbar_init(&k_empty[i], NT); }
+        for (int i = 0; i < C::kVSlots; ++i) { mbar_init(&v_raw[i], 1); mbar_init(&v_full[i], 4); mbar_init(&v_empty[i], NT); }
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, NT);
+        for (int i = 0; i < NT * kSB; ++i) {
+            mbar_init(&s_full[i], 1); mbar_init(&p_half[i], 4); mbar_init(&p_full[i], 4); mbar_init(&pv_done[i], 1);
+        }
+        for (int i = 0; i < NT; ++i) { mbar_init(&issued[i], 1); mbar_init(&drain[i], 1); }
+        for (int i = 0; i < C::kSched; ++i) {
+            mbar_init(&q_ready[i], 4); mbar_init(&sched_full[i], 1); mbar_init(&sched_empty[i], C::kSchedReaders);
+        }
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&tm_q); tma_prefetch_desc(&tm_k); tma_prefetch_desc(&tm_v);
+    }
+    if (warp == 1) { tmem_alloc(tmem_slot, 512); tmem_relinquish(); }
+    pdl_launch_dependents();                       // the merge may take its place; it waits for this grid
+    plan_range<NT>(p, plan, scan);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const WaitCtx wc{p.status, p.timeout_ns, abort_flag};
+    auto wait_unit = [&](int k) -> const TreeUnit * {
+        const int sl = k % C::kSched;
+        return mbar_wait(&sched_full[sl], (k / C::kSched) & 1, wc) ? &sched[sl] : nullptr;
+    };
+    auto free_unit = [&](int k) { mbar_arrive(&sched_empty[k % C::kSched]); };
+
+    if (warp < 4) {
+      setmaxnreg_dec<C::kRegsControl>();
+      if (warp == 0) {
+        // ------------------------------------------------------------ producer
+        TreeWalk<NT> walk;
+        walk.init(p, plan);
+        const int box_rows = p.ps < kKvTile ? p.ps : kKvTile;
+        const int pages_per_tile = p.ps < kKvTile ? kKvTile / p.ps : 1;
+        uint32_t ik = 0, iv = 0;                          // K and V tiles issued
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+            TreeUnit u;
+            walk.next(p, u);
+            const int us = k % C::kSched;
+            ok = warp_wait(&sched_empty[us], ((k / C::kSched) & 1) ^ 1, wc, lane);
+            if (!ok) break;
+            if (lane == 0) { sched[us] = u; mbar_arrive(&sched_full[us]); }
+            __syncwarp();
+            if (u.b < 0) break;
+            ok = warp_wait(q_empty, (k & 1) ^ 1, wc, lane);
+            if (!ok) break;
+            if (lane == 0) {
+                const uint32_t qrows = p.head_chunks > 1 ? 128u : (uint32_t)(p.G * p.tile_tokens);
+                mbar_arrive_expect_tx(q_full, (uint32_t)u.nrt * 2u * qrows * 128u);
+                for (int x = 0; x < u.nrt; ++x) {
+                    const int rt = u.rt0 + x;
+                    int h0 = u.g * p.G, t0 = rt * p.tile_tokens;
+                    if (p.head_chunks > 1) { t0 = rt / p.head_chunks; h0 += (rt - t0 * p.head_chunks) * 128; }
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        tma_load_4d(smem_u32(sQ + x * C::kQBytes + c * C::kHalf), &tm_q, q_full, c * 64, h0, t0, u.b);
+                }
+            }
+            __syncwarp();
+            const int32_t *bt_row = p.block_table + (int64_t)u.b * p.bt_stride;
+            auto tile_page = [&](int j) -> int {          // this lane's page of key tile j, -1: none
+                const int key = (u.tile0 + j) * kKvTile + (p.ps < kKvTile ? lane * p.ps : 0);
+                if (lane >= pages_per_tile || j >= u.ntiles || key >= u.n) return -1;
+                int phys = __ldg(bt_row + key / p.ps);
+                if ((unsigned)phys >= (unsigned)p.num_pages) { record_error(p.status, kErrInvalid); phys = 0; }
+                return phys;
+            };
+            auto copy_tile = [&](int j, int phys, bool is_v) -> bool {
+                const int key0 = (u.tile0 + j) * kKvTile;
+                const int slot0 = p.ps < kKvTile ? 0 : key0 % p.ps;
+                const unsigned who = __ballot_sync(0xffffffffu, phys >= 0);
+                uint32_t &i = is_v ? iv : ik;
+                const uint32_t slots = is_v ? C::kVSlots : C::kKSlots;
+                const uint32_t sl = i % slots;
+                uint64_t *full = is_v ? &v_raw[sl] : &k_full[sl];
+                if (!warp_wait(is_v ? &v_empty[sl] : &k_empty[sl], ((i / slots) & 1) ^ 1, wc, lane)) return false;
+                if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(__popc(who) * box_rows * 128));
+                __syncwarp();
+                uint8_t *dst = is_v ? sV + sl * C::kVBytes + C::kHalf : sK + sl * C::kKBytes;
+                if (phys >= 0)
+                    tma_load_4d(smem_u32(dst + lane * box_rows * 128), is_v ? (const void *)&tm_v : (const void *)&tm_k,
+                                full, 0, u.g, slot0, phys);
+                ++i;
+                return true;
+            };
+            // Page numbers run two tiles ahead of the K copies.
+            int pages[kSB + 3];
+#pragma unroll
+            for (int i = 0; i < kSB + 3; ++i) pages[i] = tile_page(i);
+            for (int j = 0; j < kSB && j < u.ntiles && ok; ++j) ok = copy_tile(j, j == 0 ? pages[0] : pages[kSB - 1], false);
+            for (int j = 0; j < u.ntiles && ok; ++j) {
+                ok = copy_tile(j, pages[0], true);
+                if (ok && j + kSB < u.ntiles) ok = copy_tile(j + kSB, pages[kSB], false);
+#pragma unroll
+                for (int i = 0; i < kSB + 2; ++i) pages[i] = pages[i + 1];
+                pages[kSB + 2] = tile_page(j + kSB + 3);
+            }
+        }
+        if (lane == 0) {
+            p.cuts[blockIdx.x] = walk.cut;
+            for (uint32_t i = 0; i < (uint32_t)C::kKSlots && i < ik; ++i)
+                mbar_wait_drain(&k_full[(ik - 1 - i) % C::kKSlots], ((ik - 1 - i) / C::kKSlots) & 1, wc);
+            for (uint32_t i = 0; i < (uint32_t)C::kVSlots && i < iv; ++i)
+                mbar_wait_drain(&v_raw[(iv - 1 - i) % C::kVSlots], ((iv - 1 - i) / C::kVSlots) & 1, wc);
+        }
+        __syncwarp();
+      } else if (warp <= NT) {
+        // ----------------------------------------------------------------- MMA
+        if (lane == 0) {
+            const int x = warp - 1;
+            uint32_t tiles = 0;                           // K (and V) tiles of earlier pieces
+            uint32_t steps = 0;                           // this stream's among them
+            uint32_t turns = 0;                           // those both streams took part in
+            const SDesc q_d = sdesc_sw128_split(smem_u32(sQ + x * C::kQBytes), 16, 1024);
+            const SDesc k_d = sdesc_sw128_split(smem_u32(sK), 16, 1024);
+            const SDesc v_d = sdesc_sw128_split(smem_u32(sV), C::kHalf, 1024);
+            auto wait_k = [&](uint32_t i) { return mbar_wait(&k_full[i % C::kKSlots], (i / C::kKSlots) & 1, wc); };
+            auto wait_v = [&](uint32_t i) { return mbar_wait(&v_full[i % C::kVSlots], (i / C::kVSlots) & 1, wc); };
+            auto k_there = [&](uint32_t i) {
+                return mbar_try_wait(smem_u32(&k_full[i % C::kKSlots]), (i / C::kKSlots) & 1);
+            };
+            auto push_qk = [&](uint32_t i, int buf) {
+                const SDesc kd{k_d.lo + (i % C::kKSlots) * (C::kKBytes >> 4), k_d.hi};
+#pragma unroll
+                for (int term = 0; term < 2; ++term)
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_f8_ss(tmem + C::s_col(x, buf), sdesc_at(q_d, term * C::kHalf + kk * 32),
+                                  sdesc_at(kd, kk * 32), kIdescQK, term + kk > 0 ? 1u : 0u);
+            };
+            auto push_pv_half = [&](uint32_t i, int buf, int half, bool first) {
+                const SDesc vd{v_d.lo + (i % C::kVSlots) * (C::kVBytes >> 4), v_d.hi};
+#pragma unroll
+                for (int k4 = 0; k4 < 4; ++k4) {
+                    const int kk = half * 4 + k4;
+                    mma_bf16_ts(tmem + C::o_col(x), tmem + C::s_col(x, buf) + kk * 8, sdesc_at(vd, kk * 16 * 128),
+                                kIdescPV, (first && kk == 0) ? 0u : 1u);
+                }
+            };
+            bool ok = true;
+            for (int k = 0; ok; ++k) {
+                const TreeUnit *ur = wait_unit(k);
+                const bool got = ur && ur->b >= 0;
+                const int n = got ? ur->ntiles : 0;
+                const int nrt = got ? ur->nrt : 0;
+                free_unit(k);
+                if (!got) break;
+                const uint32_t i0 = tiles;
+                tiles += (uint32_t)n;
+                if (!mbar_wait(&q_ready[k % C::kSched], (k / C::kSched) & 1, wc)) break;
+                if (x >= nrt) {
+                    // No row tile for this stream: it still sees every tile come and
+                    // hands every slot back, so that its phases stay in step.
+                    mbar_arrive(q_empty);
+                    for (uint32_t i = i0; i < tiles && ok; ++i) {
+                        ok = wait_k(i);
+                        if (ok) mbar_arrive(&k_empty[i % C::kKSlots]);
+                        ok = ok && wait_v(i);
+                        if (ok) mbar_arrive(&v_empty[i % C::kVSlots]);
+                    }
+                    continue;
+                }
+                tc_fence_after();
+                for (int j = 0; j < kSB && j < n && ok; ++j) {
+                    ok = wait_k(i0 + j);
+                    if (!ok) break;
+                    tc_fence_after();
+                    push_qk(i0 + j, (steps + j) % kSB);
+                    mma_commit(&s_full[x * kSB + (steps + j) % kSB]);
+                    mma_commit(&k_empty[(i0 + j) % C::kKSlots]);
+                    if (j == n - 1) mma_commit(q_empty);
+                }
+                for (int j = 0; j < n && ok; ++j) {
+                    const uint32_t st = steps + j;
+                    const int buf = st % kSB;
+                    const uint32_t ph = (st / kSB) & 1;
+                    const uint32_t iv = i0 + j, ik = i0 + j + kSB;
+                    if (NT == 2 && nrt == 2) {
+                        // Turns, as in the BF16 kernel.
+                        const uint32_t dep = turns + j + x;
+                        if (dep > 0 && !mbar_wait(&issued[1 - x], (dep - 1) & 1, wc)) { ok = false; break; }
+                    }
+                    if (!wait_v(iv) || !mbar_wait(&p_half[x * kSB + buf], ph, wc)) { ok = false; break; }
+                    const bool next = j + kSB < n;
+                    const bool paired = next && k_there(ik);
+                    tc_fence_after();
+                    push_pv_half(iv, buf, 0, j == 0);
+                    if (!mbar_wait(&p_full[x * kSB + buf], ph, wc)) { ok = false; break; }
+                    tc_fence_after();
+                    push_pv_half(iv, buf, 1, false);
+                    if (NT == 2 && nrt == 2) mbar_arrive(&issued[x]);
+                    if (paired) push_qk(ik, buf);
+                    if (kSB == 2 || j == n - 1) mma_commit(&pv_done[x * kSB + buf]);
+                    mma_commit(&v_empty[iv % C::kVSlots]);
+                    if (next) {
+                        if (!paired) {
+                            if (!wait_k(ik)) { ok = false; break; }
+                            tc_fence_after();
+                            push_qk(ik, buf);
+                        }
+                        mma_commit(&s_full[x * kSB + buf]);
+                        mma_commit(&k_empty[ik % C::kKSlots]);
+                        if (j + kSB == n - 1) mma_commit(q_empty);
+                    }
+                }
+                if (!ok) break;
+                steps += n;
+                if (nrt == 2) turns += n;
+            }
+            mma_commit(&drain[x]);
+            mbar_wait_drain(&drain[x], 0, wc);
+        }
+        __syncwarp();
+      } else if (warp == 3) {
+        write_padding_rows<D>(p);
+      }
+    } else if (warp < 8) {
+        if constexpr (C::kRegsConvert < C::kRegsLaunch) setmaxnreg_dec<C::kRegsConvert>();
+        // ------------------------------------------------------------ converters
+        // Thread = query row of a tile, then = key of a tile.  After an abort
+        // every wait returns at once and the bounded loops run out.
+        const int row = threadIdx.x - 128;
+        const uint32_t sw = row & 7;
+        uint32_t i = 0;                                   // V tiles converted
+        for (int k = 0;; ++k) {
+            const TreeUnit *ur = wait_unit(k);
+            TreeUnit u;
+            u.b = -1;
+            if (ur) u = *ur;
+            __syncwarp();
+            if (lane == 0) free_unit(k);
+            if (u.b < 0) break;
+            mbar_wait(q_full, k & 1, wc);
+            for (int x = 0; x < u.nrt; ++x) {
+                // BF16 row * 2^e = hi + mid, both E4M3, over the row's own bytes.
+                uint8_t *qr = sQ + x * C::kQBytes + row * 128;
+                auto unit = [&](int c) {
+                    return *reinterpret_cast<const uint4 *>(qr + (c >> 3) * C::kHalf + (((c & 7) ^ sw) << 4));
+                };
+                uint32_t big = 0;                         // largest magnitude, as the bits of an FP32
+                auto fold = [&](uint32_t v) { big = max(big, max((v << 16) & 0x7fff0000u, v & 0x7fff0000u)); };
+#pragma unroll 4
+                for (int c = 0; c < 16; ++c) {
+                    const uint4 w = unit(c);
+                    fold(w.x); fold(w.y); fold(w.z); fold(w.w);
+                }
+                const int e = min(126, max(-120, 134 - (int)(big >> 23)));   // 7 - (exponent - 127)
+                // An infinite or NaN element makes the row's scores NaN.
+                const float up = __int_as_float(big >= 0x7f800000u ? 0x7fc00000 : (127 + e) << 23);
+                q_exp[(k % C::kSched * NT + x) * 128 + row] = (int8_t)e;
+                auto split4 = [&](uint32_t v0, uint32_t v1, uint32_t &hi, uint32_t &mid) {
+                    const float a = __uint_as_float(v0 << 16) * up, b = __uint_as_float(v0 & 0xffff0000u) * up;
+                    const float c = __uint_as_float(v1 << 16) * up, d = __uint_as_float(v1 & 0xffff0000u) * up;
+                    const __nv_fp8x2_storage_t h0 = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+                    const __nv_fp8x2_storage_t h1 = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+                    const float2 f0 = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(h0, __NV_E4M3)));
+                    const float2 f1 = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(h1, __NV_E4M3)));
+                    hi = (uint32_t)h0 | ((uint32_t)h1 << 16);
+                    mid = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a - f0.x, b - f0.y), __NV_SATFINITE, __NV_E4M3) |
+                          ((uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(c - f1.x, d - f1.y), __NV_SATFINITE, __NV_E4M3) << 16);
+                };
+                // Unit c of a term takes BF16 units 2c and 2c + 1; hi goes over unit c,
+                // mid over unit 8 + c: the first four mids wait until those are read.
+                auto split_unit = [&](int c, uint4 &hi, uint4 &mid) {
+                    const uint4 w0 = unit(2 * c), w1 = unit(2 * c + 1);
+                    split4(w0.x, w0.y, hi.x, mid.x);
+                    split4(w0.z, w0.w, hi.y, mid.y);
+                    split4(w1.x, w1.y, hi.z, mid.z);
+                    split4(w1.z, w1.w, hi.w, mid.w);
+                };
+                auto put = [&](int term, int c, const uint4 &v) {
+                    *reinterpret_cast<uint4 *>(qr + term * C::kHalf + ((c ^ sw) << 4)) = v;
+                };
+                uint4 hi[4], mid[4], mid2[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) split_unit(c, hi[c], mid[c]);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) put(0, c, hi[c]);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) split_unit(4 + c, hi[c], mid2[c]);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) { put(0, 4 + c, hi[c]); put(1, c, mid[c]); put(1, 4 + c, mid2[c]); }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&q_ready[k % C::kSched]);
+            const int base = u.n - u.d;
+            for (int j = 0; j < u.ntiles; ++j, ++i) {
+                const int key0 = (u.tile0 + j) * kKvTile;
+                bool hidden = false;
+                if (key0 + kKvTile > base)
+                    hidden = !(seen_keys(p, u, key0, row, 3, seen_words + (j & 1) * 16) >> lane & 1);
+                const uint32_t sl = i % C::kVSlots;
+                mbar_wait(&v_raw[sl], (i / C::kVSlots) & 1, wc);
+                uint8_t *vr = sV + sl * C::kVBytes + row * 128;
+                uint4 w[8];
+#pragma unroll
+                for (int c = 0; c < 8; ++c) w[c] = *reinterpret_cast<const uint4 *>(vr + C::kHalf + ((c ^ sw) << 4));
+                if (hidden) {
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) w[c] = make_uint4(0, 0, 0, 0);
+                }
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {             // 16 values: two units of FP16
+                    uint4 a, b;
+                    widen4(w[c].x, a.x, a.y);
+                    widen4(w[c].y, a.z, a.w);
+                    widen4(w[c].z, b.x, b.y);
+                    widen4(w[c].w, b.z, b.w);
+                    uint8_t *to = vr + (c >> 2) * C::kHalf;
+                    *reinterpret_cast<uint4 *>(to + (((2 * c) & 7) ^ sw) * 16) = a;
+                    *reinterpret_cast<uint4 *>(to + (((2 * c + 1) & 7) ^ sw) * 16) = b;
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&v_full[sl]);
+            }
+        }
+    } else {
+        setmaxnreg_inc<C::kRegsSoftmax>();
+        // ------------------------------------------------- softmax / epilogue
+        const int x = (warp - 8) >> 2;
+        const int q4 = warp & 3;
+        const int row = q4 * 32 + lane;
+        const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
+        const bool scale_pos = p.scale_log2 >= 0.f;
+        uint32_t steps = 0, pieces = 0;
+        auto wait_pv = [&](uint32_t step) { mbar_wait(&pv_done[x * kSB + step % kSB], (step / kSB) & 1, wc); };
+        for (int k = 0;; ++k) {
+            const TreeUnit *ur = wait_unit(k);
+            TreeUnit u;
+            u.b = -1;
+            if (ur) u = *ur;
+            // The row's exponent is read before the record goes back: unit k + 4,
+            // which reuses its place, cannot come before that.
+            if (u.b >= 0) mbar_wait(&q_ready[k % C::kSched], (k / C::kSched) & 1, wc);
+            const float rs = p.scale_log2 * __int_as_float((127 - q_exp[(k % C::kSched * NT + x) * 128 + row]) << 23);
+            __syncwarp();
+            if (lane == 0) free_unit(k);
+            if (u.b < 0) break;
+            if (x >= u.nrt) continue;
+            int t, h;
+            const bool live = tree_tile_row(p, u.rt0 + x, u.g, u.d, row, t, h);
+            const bool warp_live = __any_sync(0xffffffffu, live);
+            const int base = u.n - u.d;
+            const int32_t *mrow = p.mask + u.b * p.mask_stride[0] + (live ? t : 0) * p.mask_stride[1];
+            float m_ref = kNegInf, l_sum = 0.f;
+            for (int j = 0; j < u.ntiles; ++j, ++steps) {
+                const int buf = steps % kSB;
+                const int key0 = (u.tile0 + j) * kKvTile;
+                const bool drafts = key0 + kKvTile > base;
+                mbar_wait(&s_full[x * kSB + buf], (steps / kSB) & 1, wc);
+                tc_fence_after();
+                if (!warp_live) {                         // rows of padding: whatever lies there
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) { mbar_arrive(&p_half[x * kSB + buf]); mbar_arrive(&p_full[x * kSB + buf]); }
+                    continue;
+                }
+                const uint32_t sa = tmem + lane_off + C::s_col(x, buf);
+                uint32_t bits[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+                if (drafts) {
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) bits[w] = live ? draft_bits(mrow, key0 + 32 * w - base, u.d) : 0u;
+                }
+                const float gone = scale_pos ? kNegInf : -kNegInf;
+                // The row of S is read twice, for its maximum and for P: with two
+                // streams' softmax warps its 128 scores do not fit their registers.
+                float ext = gone;
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float v[64];
+                    tmem_ld32(sa + c * 64, v);
+                    tmem_ld32(sa + c * 64 + 32, v + 32);
+                    tmem_wait_ld();
+                    if (drafts) {
+#pragma unroll
+                        for (int i = 0; i < 64; ++i)
+                            if (!(bits[c * 2 + (i >> 5)] >> (i & 31) & 1)) v[i] = gone;
+                    }
+                    float e4[4] = {v[0], v[1], v[2], v[3]};
+                    if (scale_pos) {
+#pragma unroll
+                        for (int i = 4; i < 64; ++i) e4[i & 3] = fmaxf(e4[i & 3], v[i]);
+                        ext = fmaxf(ext, fmaxf(fmaxf(e4[0], e4[1]), fmaxf(e4[2], e4[3])));
+                    } else {
+#pragma unroll
+                        for (int i = 4; i < 64; ++i) e4[i & 3] = fminf(e4[i & 3], v[i]);
+                        ext = fminf(ext, fminf(fminf(e4[0], e4[1]), fminf(e4[2], e4[3])));
+                    }
+                }
+                const float m_tile = ext == gone || !live ? kNegInf : ext * rs;
+                const bool up = m_tile > m_ref + kRescaleSlack;
+                if (__any_sync(0xffffffffu, up)) {
+                    float alpha = 1.f;
+                    if (up) {
+                        alpha = ex2_approx(m_ref - m_tile);
+                        l_sum *= alpha;
+                        m_ref = m_tile;
+                    }
+                    if (j > 0) {
+                        if constexpr (kSB == 2) {
+                            wait_pv(steps - 1);
+                            tc_fence_after();
+                        }
+#pragma unroll 1
+                        for (int c = 0; c < D / 32; ++c) {
+                            float o[32];
+                            const uint32_t oa = tmem + lane_off + C::o_col(x) + c * 32;
+                            tmem_ld32(oa, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] *= alpha;
+                            tmem_st32(oa, o);
+                        }
+                        tmem_wait_st();
+                    }
+                }
+                // P = 2^(s * rs - m_ref + 7), rounded to FP16; the row sum takes it
+                // unrounded.
+                const float mu = (m_ref == kNegInf ? 0.f : m_ref) - kPShift;
+                float a8[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) a8[i] = 0.f;
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    float v[64];
+                    uint32_t pk[32];
+                    tmem_ld32(sa + half * 64, v);
+                    tmem_ld32(sa + half * 64 + 32, v + 32);
+                    tmem_wait_ld();
+                    if (drafts) {
+#pragma unroll
+                        for (int i = 0; i < 64; ++i)
+                            if (!(bits[half * 2 + (i >> 5)] >> (i & 31) & 1)) v[i] = gone;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 64; i += 2) {
+                        const float p0 = ex2_approx(fmaf(v[i], rs, -mu));
+                        const float p1 = ex2_approx(fmaf(v[i + 1], rs, -mu));
+                        a8[(i >> 1) & 7] += p0 + p1;
+                        pk[i >> 1] = pack_half2(p0, p1);
+                    }
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        tmem_st16u(sa + half * 32 + c * 16, *reinterpret_cast<const uint32_t(*)[16]>(pk + c * 16));
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(half == 0 ? &p_half[x * kSB + buf] : &p_full[x * kSB + buf]);
+                }
+                l_sum += ((a8[0] + a8[1]) + (a8[2] + a8[3])) + ((a8[4] + a8[5]) + (a8[6] + a8[7]));
+            }
+            // ------------------------------------------------------ epilogue
+            ++pieces;
+            if constexpr (kSB == 2) {
+                if (steps >= 2) wait_pv(steps - 2);
+                wait_pv(steps - 1);
+            } else {
+                mbar_wait(&pv_done[x], (pieces - 1) & 1, wc);
+            }
+            tc_fence_after();
+            if (warp_live)
+                write_row<D, NT>(p, u, x, row, live, t, h, m_ref - kPShift, l_sum, [&](int c, float (&o)[32]) {
+                    tmem_ld32(tmem + lane_off + C::o_col(x) + c * 32, o);
+                    tmem_wait_ld();
+                });
+            tc_fence_before();
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+template <int NT>
+cudaError_t launch_fp8(const TreeParams &p, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                       cudaStream_t stream, int *launches) {
+    using C = F8TreeCfg<NT>;
+    static bool configured[64] = {};
+    return launch_pieces(tree_decode_fp8_kernel<NT>, NT, C::kThreads, C::kSmemBytes, p, tq, tk, tv, stream, configured,
+                         launches);
+}
+
+}  // namespace
+
+cudaError_t launch_tree_decode_fp8(const TreeParams &p, const CUtensorMap &tq, const CUtensorMap &tk,
+                                   const CUtensorMap &tv, cudaStream_t stream, int *launches) {
+    return p.row_tiles > 1 ? launch_fp8<2>(p, tq, tk, tv, stream, launches) : launch_fp8<1>(p, tq, tk, tv, stream, launches);
+}
+
+}  // namespace fw

@@ -28,37 +28,12 @@
 // Warp roles: warp 0 copies (Q, then K and V tiles through a ring of 32 KiB
 // slots in the order the MMAs take them), warp 1 (and 2) issues the MMAs,
 // warp 3 writes the rows that see nothing, warps 4.. run the softmax.
-#include <cuda_bf16.h>
-#include <cuda_fp8.h>
-
-#include "decode_common.cuh"
-#include "fw_internal.h"
-#include "fw_ptx.cuh"
+#include "tree_common.cuh"
 
 namespace fw {
 namespace {
 
-using dec::ceil_div_i;
-using dec::warp_max;
-using dec::warp_sum;
-using dec::warp_wait;
-constexpr float kNegInf = -__builtin_huge_valf();
-// The base of a row's exponentials moves only when its maximum rose by more
-// than this many log2 units, so every weight is at most 2^8.
-constexpr float kRescaleSlack = 8.0f;
-constexpr int kErrInvalid = 1;     // FW_ERR_INVALID_ARG
-
-// One piece: a unit's key tiles inside one CTA range.  64 bytes.
-struct alignas(16) TreeUnit {
-    int b;             // request, -1 ends the CTA's work
-    int g;             // KV head
-    int rt0, nrt;      // first row tile and how many
-    int n, d;          // keys and drafts of the request
-    int tile0, ntiles; // key tiles
-    int part;          // partial slot, -1: the whole unit, written to the outputs
-    int pad_[7];
-};
-static_assert(sizeof(TreeUnit) == 64, "a unit record fills one 64-byte slot");
+using namespace tree;
 
 template <int D_, int NT_>
 struct TreeCfg {
@@ -103,65 +78,6 @@ struct TreeCfg {
     __device__ static constexpr uint32_t s_col(int x, int buf) { return (uint32_t)(x * kSB + buf) * 128u; }
     __device__ static constexpr uint32_t o_col(int x) { return 256u + (uint32_t)x * 128u; }
 };
-
-// Keys and drafts of request b, both within what the call can hold.
-__device__ __forceinline__ void tree_row(const TreeParams &p, int b, int &n, int &d) {
-    n = min(max(__ldg(p.seq_lens + b), 0), p.max_pages * p.ps);
-    d = p.draft_lens ? min(max(__ldg(p.draft_lens + b), 0), p.T) : p.T;
-    d = min(d, n);
-}
-
-// Units of a request in the planned sequence (of one KV head when the heads
-// ride on the CTA index).
-template <int NT>
-__device__ __forceinline__ int tree_units(const TreeParams &p, int d) {
-    const int tiles = p.head_chunks > 1 ? d * p.head_chunks : ceil_div_i(d, p.tile_tokens);
-    return ceil_div_i(tiles, NT) * (p.ride ? 1 : p.Hkv);
-}
-
-// The (draft, head) of row r of row tile rt; false for padding.
-__device__ __forceinline__ bool tree_tile_row(const TreeParams &p, int rt, int g, int d, int r, int &t, int &h) {
-    if (p.head_chunks > 1) {
-        t = rt / p.head_chunks;
-        const int hh = (rt - t * p.head_chunks) * 128 + r;
-        h = g * p.G + hh;
-        return hh < p.G && t < d;
-    }
-    const int tt = r / p.G;
-    t = rt * p.tile_tokens + tt;
-    h = g * p.G + (r - tt * p.G);
-    return tt < p.tile_tokens && t < d;
-}
-
-// Bits of the 32 keys from draft ds on (ds < 0: committed keys first) that the
-// mask row shows, among the request's d drafts.
-__device__ __forceinline__ uint32_t draft_bits(const int32_t *row, int ds, int d) {
-    if (ds <= -32) return 0xffffffffu;
-    if (ds >= d) return 0u;
-    uint32_t v;
-    if (ds < 0) {
-        v = ((uint32_t)__ldg(row) << -ds) | ((1u << -ds) - 1u);
-    } else {
-        const int w = ds >> 5;
-        const uint32_t lo = (uint32_t)__ldg(row + w);
-        const uint32_t hi = (w + 1) * 32 < d ? (uint32_t)__ldg(row + w + 1) : 0u;
-        v = __funnelshift_r(lo, hi, ds & 31);
-    }
-    const int left = d - ds;
-    return left < 32 ? v & ((1u << left) - 1u) : v;
-}
-
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-    __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<uint32_t *>(&v);
-}
-
-// Ring positions, in units of whole K or V tiles, of a piece of n key tiles
-// when QK runs L tiles ahead of PV: K_0 .. K_{L-1}, then V_j K_{j+L}.
-template <int L>
-__device__ __forceinline__ int pos_v(int j, int n) { return min(L, n) + j + min(j, max(0, n - L)); }
-template <int L>
-__device__ __forceinline__ int pos_k(int j, int n) { return j < L ? j : pos_v<L>(j - L, n) + 1; }
 
 template <int D, int NT>
 __global__ void __launch_bounds__(TreeCfg<D, NT>::kThreads, 1)
@@ -213,43 +129,7 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
     }
     if (warp == 1) { tmem_alloc(tmem_slot, 512); tmem_relinquish(); }
     pdl_launch_dependents();                       // the merge may take its place; it waits for this grid
-    // The planned sequence: request b takes units * (piece_cost + tiles) slots.
-    // Every thread sums a run of requests; the one whose run holds this CTA's
-    // first slot looks the request up.
-    const int per = (p.B + C::kThreads - 1) / C::kThreads;
-    auto row_slots = [&](int b) -> long long {
-        int n, d;
-        tree_row(p, b, n, d);
-        return (long long)tree_units<NT>(p, d) * (p.piece_cost + ceil_div_i(n, kKvTile));
-    };
-    {
-        long long mine = 0;
-        const int b0 = threadIdx.x * per;
-        for (int i = 0; i < per && b0 + i < p.B; ++i) mine += row_slots(b0 + i);
-        long long incl = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += v;
-        }
-        if (lane == 31) scan[warp] = incl;
-        __syncthreads();
-        long long before = incl - mine, total = 0;
-        for (int w = 0; w < C::kThreads / 32; ++w) {
-            if (w < warp) before += scan[w];
-            total += scan[w];
-        }
-        const int nranges = p.ride ? (int)gridDim.x / p.Hkv : (int)gridDim.x;
-        const long long span = max((long long)p.min_span, (total + nranges - 1) / nranges);
-        const long long first = span * (p.ride ? (int)blockIdx.x / p.Hkv : (int)blockIdx.x);
-        if (mine > 0 && first >= before && first < before + mine) {
-            int b = b0;
-            for (long long s; first >= before + (s = row_slots(b)); ++b) before += s;
-            plan[1] = before;
-            plan[2] = b;
-        }
-        if (threadIdx.x == 0) { plan[0] = total; plan[3] = span; }
-    }
+    plan_range<NT>(p, plan, scan);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -265,58 +145,16 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
       if constexpr (NT == 2) setmaxnreg_dec<C::kRegsControl>();
       if (warp == 0) {
         // ------------------------------------------------------------ producer
-        const long long total = plan[0], span = plan[3];
-        const int range = p.ride ? (int)blockIdx.x / p.Hkv : (int)blockIdx.x;
-        long long pos = span * range;
-        const long long end = min(total, pos + span);
-        long long pb0 = plan[1];
-        int b = (int)plan[2];
-        int n = 0, d = 0, units = 0, tiles = 0;
-        auto open_row = [&]() {
-            tree_row(p, b, n, d);
-            units = tree_units<NT>(p, d);
-            tiles = ceil_div_i(n, kKvTile);
-        };
-        TreeCut cut{};
+        TreeWalk<NT> walk;
+        walk.init(p, plan);
         const int box_rows = p.ps < kKvTile ? p.ps : kKvTile;
         const int pages_per_tile = p.ps < kKvTile ? kKvTile / p.ps : 1;
         uint32_t rp = 0;                                  // ring slots filled so far
         bool ok = true;
         int k = 0;
-        if (pos < end) open_row();
         while (ok) {
-            // ---- the next piece
             TreeUnit u;
-            u.b = -1;
-            while (pos < end) {
-                const int v = p.piece_cost + tiles;
-                const long long row = (long long)units * v;
-                if (pos >= pb0 + row) { pb0 += row; ++b; open_row(); continue; }
-                const int ui = (int)((pos - pb0) / v);
-                const int vl = (int)(pos - pb0 - (long long)ui * v);
-                if (vl < p.piece_cost) { pos += p.piece_cost - vl; continue; }
-                const int tl = vl - p.piece_cost;
-                const int th = (int)min((long long)tiles, tl + (end - pos));
-                const long long ustart = pb0 + (long long)ui * v + p.piece_cost;
-                u.b = b;
-                const int per_head = p.ride ? units : units / p.Hkv;
-                u.g = p.ride ? (int)blockIdx.x % p.Hkv : ui / per_head;
-                const int rts = p.head_chunks > 1 ? d * p.head_chunks : ceil_div_i(d, p.tile_tokens);
-                u.rt0 = (p.ride ? ui : ui - u.g * per_head) * NT;
-                u.nrt = min(NT, rts - u.rt0);
-                u.n = n; u.d = d;
-                u.tile0 = tl; u.ntiles = th - tl;
-                u.part = -1;
-                if (tl > 0) {
-                    u.part = 2 * blockIdx.x;
-                } else if (th < tiles) {
-                    u.part = 2 * blockIdx.x + 1;
-                    cut.count = (int)((ustart + tiles - 1) / span) - range + 1;
-                    cut.b = b; cut.g = u.g; cut.rt0 = u.rt0; cut.nrt = u.nrt; cut.d = d;
-                }
-                pos += th - tl;
-                break;
-            }
+            walk.next(p, u);
             {
                 const int sl = k % C::kSched;
                 ok = warp_wait(&sched_empty[sl], ((k / C::kSched) & 1) ^ 1, wc, lane);
@@ -388,7 +226,7 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
             ++k;
         }
         if (lane == 0) {
-            p.cuts[blockIdx.x] = cut;
+            p.cuts[blockIdx.x] = walk.cut;
             for (uint32_t i = 0; i < (uint32_t)C::kSlots && i < rp; ++i) {
                 const uint32_t r = rp - 1 - i;
                 mbar_wait_drain(&slot_full[r % C::kSlots], (r / C::kSlots) & 1, wc);
@@ -528,19 +366,7 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
         __syncwarp();
       } else if (warp == 3) {
         // ------------------------------------------- rows that see nothing
-        for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-            int n, d;
-            tree_row(p, b, n, d);
-            const int rows = (p.T - d) * p.Hq;
-            for (int i = lane; i < rows * (D / 8); i += 32) {
-                const int r = i / (D / 8), c = i - r * (D / 8);
-                const int t = d + r / p.Hq, h = r % p.Hq;
-                __nv_bfloat16 *o = reinterpret_cast<__nv_bfloat16 *>(p.out) + b * p.out_stride[0] +
-                                   t * p.out_stride[1] + h * p.out_stride[2];
-                reinterpret_cast<uint4 *>(o)[c] = make_uint4(0, 0, 0, 0);
-                if (c == 0 && p.lse) p.lse[b * p.lse_stride[0] + t * p.lse_stride[1] + h * p.lse_stride[2]] = kNegInf;
-            }
-        }
+        write_padding_rows<D>(p);
       }
     } else {
         if constexpr (NT == 2) setmaxnreg_inc<C::kRegsSoftmax>();
@@ -584,20 +410,7 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
                 if (drafts) {
                     // Values of keys nobody sees must not meet a zero weight: they
                     // may be NaN.  A key is seen when some draft's mask shows it.
-                    uint32_t seen[4] = {0, 0, 0, 0};
-                    for (int tt = row; tt < u.d; tt += 128) {
-                        const int32_t *mr = p.mask + u.b * p.mask_stride[0] + tt * p.mask_stride[1];
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) seen[w] |= draft_bits(mr, key0 + 32 * w - base, u.d);
-                    }
-                    uint32_t *sw = seen_words + (x * 2 + (j & 1)) * 16;
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        seen[w] = __reduce_or_sync(0xffffffffu, seen[w]);
-                        if (lane == 0) sw[q4 * 4 + w] = seen[w];
-                    }
-                    named_bar_sync(1 + x, 128);
-                    const uint32_t mine = sw[q4] | sw[4 + q4] | sw[8 + q4] | sw[12 + q4];   // word q4: this warp's keys
+                    const uint32_t mine = seen_keys(p, u, key0, row, 1 + x, seen_words + (x * 2 + (j & 1)) * 16);
                     if (__any_sync(0xffffffffu, !(mine >> lane & 1))) {
                         const uint32_t r = r0 + (uint32_t)(pos_v<kSB>(j, u.ntiles) * TS);
                         // A parity wait needs the slot's copy before V_j to have landed.
@@ -724,41 +537,11 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
                 mbar_wait(&pv_done[x], (pieces - 1) & 1, wc);
             }
             tc_fence_after();
-            if (warp_live) {
-                const float inv = l_sum > 0.f ? p.out_scale / l_sum : 0.f;
-                __nv_bfloat16 *orow = reinterpret_cast<__nv_bfloat16 *>(p.out) + u.b * p.out_stride[0] +
-                                      t * p.out_stride[1] + h * p.out_stride[2];
-                const int64_t prow = (int64_t)u.part * (NT * 128) + x * 128 + row;
-                float4 *part = reinterpret_cast<float4 *>(p.part_o + prow * D);
-#pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                    float o[32];
+            if (warp_live)
+                write_row<D, NT>(p, u, x, row, live, t, h, m_ref, l_sum, [&](int c, float (&o)[32]) {
                     tmem_ld32(tmem + lane_off + C::o_col(x) + c * 32, o);
                     tmem_wait_ld();
-                    if (!live) continue;
-                    if (u.part < 0) {
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) {
-                            uint4 v;
-                            v.x = l_sum > 0.f ? pack_bf16x2(o[8 * w + 0] * inv, o[8 * w + 1] * inv) : 0u;
-                            v.y = l_sum > 0.f ? pack_bf16x2(o[8 * w + 2] * inv, o[8 * w + 3] * inv) : 0u;
-                            v.z = l_sum > 0.f ? pack_bf16x2(o[8 * w + 4] * inv, o[8 * w + 5] * inv) : 0u;
-                            v.w = l_sum > 0.f ? pack_bf16x2(o[8 * w + 6] * inv, o[8 * w + 7] * inv) : 0u;
-                            *reinterpret_cast<uint4 *>(orow + c * 32 + w * 8) = v;
-                        }
-                    } else {
-#pragma unroll
-                        for (int w = 0; w < 8; ++w)
-                            part[c * 8 + w] = make_float4(o[4 * w], o[4 * w + 1], o[4 * w + 2], o[4 * w + 3]);
-                    }
-                }
-                if (live) {
-                    if (u.part >= 0) p.part_ml[prow] = make_float2(m_ref, l_sum);
-                    else if (p.lse)
-                        p.lse[u.b * p.lse_stride[0] + t * p.lse_stride[1] + h * p.lse_stride[2]] =
-                            l_sum > 0.f ? (m_ref + log2f(l_sum)) * 0.69314718055994531f : kNegInf;
-                }
-            }
+                });
             tc_fence_before();
         }
     }
@@ -832,104 +615,22 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__
 }
 
 template <int D, int NT>
-cudaError_t launch_tree_t(const TreeParams &p, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
-                          cudaStream_t stream, int *launches) {
+cudaError_t launch_bf16(const TreeParams &p, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                        cudaStream_t stream, int *launches) {
     using C = TreeCfg<D, NT>;
     static bool configured[64] = {};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (!configured[dev & 63]) {
-        e = cudaFuncSetAttribute(tree_decode_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
-        if (e != cudaSuccess) return e;
-        configured[dev & 63] = true;
-    }
-    tree_decode_kernel<D, NT><<<p.grid, C::kThreads, C::kSmemBytes, stream>>>(p, tq, tk, tv);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    ++*launches;
-    e = launch_after_previous(tree_merge_kernel<D, NT>, dim3(NT * 4, p.grid), dim3(256), 0, stream, p);
-    if (e != cudaSuccess) return e;
-    ++*launches;
-    return cudaSuccess;
-}
-
-template <bool kKv8>
-__device__ __forceinline__ float cache_value(const void *base, int64_t i) {
-    if constexpr (kKv8) {
-        const __nv_fp8_e4m3 v = reinterpret_cast<const __nv_fp8_e4m3 *>(base)[i];
-        return (float)v;
-    } else {
-        return __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(base)[i]);
-    }
-}
-
-template <int D, bool kKv8>
-__global__ void __launch_bounds__(128) tree_decode_simple_kernel(const __grid_constant__ TreeParams p) {
-    __shared__ float sq[D], sp[128], red[4];
-    __shared__ int64_t vrow[128];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int h = blockIdx.x % p.Hq, t = (blockIdx.x / p.Hq) % p.T, b = blockIdx.x / (p.Hq * p.T);
-    const int g = h / p.G;
-    const int n = min(max(__ldg(p.seq_lens + b), 0), p.max_pages * p.ps);
-    const int d = min(min(p.draft_lens ? max(__ldg(p.draft_lens + b), 0) : p.T, p.T), n);
-    float o[D / 128], m = kNegInf, l = 0.f;
-#pragma unroll
-    for (int i = 0; i < D / 128; ++i) o[i] = 0.f;
-    const uint16_t *qr = p.q + b * p.q_stride[0] + t * p.q_stride[1] + h * p.q_stride[2];
-    for (int i = tid; i < D; i += 128) sq[i] = __uint_as_float((uint32_t)qr[i] << 16);
-    __syncthreads();
-    if (t < d) {
-        const int32_t *mrow = p.mask + b * p.mask_stride[0] + t * p.mask_stride[1];
-        for (int k0 = 0; k0 < n; k0 += 128) {
-            const int key = k0 + tid, j = key - (n - d);
-            const bool seen = key < n && (j < 0 || (__ldg(mrow + (j >> 5)) >> (j & 31)) & 1);
-            float s = kNegInf;
-            vrow[tid] = -1;
-            if (seen) {
-                int page = __ldg(p.block_table + b * p.bt_stride + key / p.ps);
-                if ((unsigned)page >= (unsigned)p.num_pages) { record_error(p.status, 1); page = 0; }
-                const int64_t kr = page * p.kc_stride[0] + (key % p.ps) * p.kc_stride[1] + g * p.kc_stride[2];
-                vrow[tid] = page * p.vc_stride[0] + (key % p.ps) * p.vc_stride[1] + g * p.vc_stride[2];
-                float a = 0.f;
-                for (int i = 0; i < D; ++i) a = fmaf(sq[i], cache_value<kKv8>(p.k_cache, kr + i), a);
-                s = a * p.scale_log2;
-            }
-            float x = warp_max(s);
-            if (lane == 0) red[warp] = x;
-            __syncthreads();
-            const float mn = fmaxf(m, fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
-            const float mu = mn == kNegInf ? 0.f : mn;
-            const float alpha = exp2f(m - mu);
-            m = mn;
-            const float pr = exp2f(s - mu);
-            sp[tid] = pr;
-            x = warp_sum(pr);
-            __syncthreads();
-            if (lane == 0) red[warp] = x;
-            __syncthreads();
-            l = l * alpha + ((red[0] + red[1]) + (red[2] + red[3]));
-#pragma unroll
-            for (int i = 0; i < D / 128; ++i) {
-                float a = o[i] * alpha;
-                for (int k = 0; k < 128; ++k)
-                    if (vrow[k] >= 0) a = fmaf(sp[k], cache_value<kKv8>(p.v_cache, vrow[k] + i * 128 + tid), a);
-                o[i] = a;
-            }
-            __syncthreads();
-        }
-    }
-    __nv_bfloat16 *orow = reinterpret_cast<__nv_bfloat16 *>(p.out) + b * p.out_stride[0] + t * p.out_stride[1] +
-                          h * p.out_stride[2];
-#pragma unroll
-    for (int i = 0; i < D / 128; ++i)
-        orow[i * 128 + tid] = __float2bfloat16_rn(l > 0.f ? o[i] * (p.out_scale / l) : 0.f);
-    if (tid == 0 && p.lse)
-        p.lse[b * p.lse_stride[0] + t * p.lse_stride[1] + h * p.lse_stride[2]] =
-            l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : kNegInf;
+    return launch_pieces(tree_decode_kernel<D, NT>, NT, C::kThreads, C::kSmemBytes, p, tq, tk, tv, stream, configured,
+                         launches);
 }
 
 }  // namespace
+
+cudaError_t launch_tree_merge(const TreeParams &p, int row_tiles, cudaStream_t stream) {
+    const dim3 grid(row_tiles * 4, p.grid);
+    if (p.D == 256) return launch_after_previous(tree_merge_kernel<256, 1>, grid, dim3(256), 0, stream, p);
+    if (row_tiles == 2) return launch_after_previous(tree_merge_kernel<128, 2>, grid, dim3(256), 0, stream, p);
+    return launch_after_previous(tree_merge_kernel<128, 1>, grid, dim3(256), 0, stream, p);
+}
 
 size_t tree_workspace_bytes(int head_dim, int grid) {
     const int rows = head_dim == 128 ? 256 : 128;
@@ -949,14 +650,10 @@ void tree_place_workspace(TreeParams *p, void *ws) {
 cudaError_t launch_tree_decode(const TreeParams &p, const CUtensorMap &tq, const CUtensorMap &tk,
                                const CUtensorMap &tv, cudaStream_t stream, int *launches) {
     *launches = 0;
-    if (p.kv8) {
-        tree_decode_simple_kernel<128, true><<<(unsigned)((int64_t)p.B * p.T * p.Hq), 128, 0, stream>>>(p);
-        *launches = 1;
-        return cudaGetLastError();
-    }
-    if (p.D == 256) return launch_tree_t<256, 1>(p, tq, tk, tv, stream, launches);
-    if (p.row_tiles > 1) return launch_tree_t<128, 2>(p, tq, tk, tv, stream, launches);
-    return launch_tree_t<128, 1>(p, tq, tk, tv, stream, launches);
+    if (p.kv8) return launch_tree_decode_fp8(p, tq, tk, tv, stream, launches);
+    if (p.D == 256) return launch_bf16<256, 1>(p, tq, tk, tv, stream, launches);
+    if (p.row_tiles > 1) return launch_bf16<128, 2>(p, tq, tk, tv, stream, launches);
+    return launch_bf16<128, 1>(p, tq, tk, tv, stream, launches);
 }
 
 }  // namespace fw
