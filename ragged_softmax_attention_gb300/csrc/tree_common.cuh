@@ -14,11 +14,14 @@ namespace tree {
 
 using dec::ceil_div_i;
 using dec::warp_max;
+using dec::warp_sum;
 using dec::warp_wait;
 constexpr float kNegInf = -__builtin_huge_valf();
 // The base of a row's exponentials moves only when its maximum rose by more
 // than this many log2 units, so every weight is at most 2^8.
 constexpr float kRescaleSlack = 8.0f;
+// Instruction descriptor bit: A enters negated (scores of a negative scale).
+constexpr uint32_t kIdescNegateA = 1u << 13;
 constexpr int kErrInvalid = 1;     // FW_ERR_INVALID_ARG
 
 // One piece: a unit's key tiles inside one CTA range.  64 bytes.
@@ -248,7 +251,7 @@ __device__ __forceinline__ void write_row(const TreeParams &p, const TreeUnit &u
                           h * p.out_stride[2];
     const int64_t prow = (int64_t)u.part * (NT * 128) + x * 128 + row;
     float4 *part = reinterpret_cast<float4 *>(p.part_o + prow * D);
-#pragma unroll
+#pragma unroll 1
     for (int c = 0; c < D / 32; ++c) {
         float o[32];
         load(c, o);

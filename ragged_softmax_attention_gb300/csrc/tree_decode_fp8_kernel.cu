@@ -11,8 +11,8 @@
 //               every element down to 2^-10 of the row's largest; below, an
 //               element is off by at most 2^-17 of the largest.  Two terms of
 //               K = 32 products take the tensor core as long as one BF16 pass.
-//   O += P V    kind::f16 on FP16: four warps widen each V tile (E4M3 is exact
-//               in FP16) where it landed -- a key's 128 bytes lie in the second
+//   O += P V    kind::f16 on FP16: four warps widen each V tile (to a 256th,
+//               exact in FP16; the output scale makes up for it) where it landed -- a key's 128 bytes lie in the second
 //               half of a 32 KiB slot and become 256, the thread that owns the
 //               key reads them all first.  P is rounded to FP16, scaled by 2^7
 //               so that weights down to 2^-21 of the largest keep 11 bits (base
@@ -23,7 +23,6 @@
 // Warp roles: 0 copies, 1 (and 2) issues MMAs, 3 writes the rows that see
 // nothing, 4-7 convert, 8.. softmax.
 #include <cuda_fp16.h>
-#include <cuda_fp8.h>
 
 #include "tree_common.cuh"
 
@@ -95,12 +94,30 @@ struct F8TreeCfg {
     __device__ static constexpr uint32_t o_col(int x) { return 256u + (uint32_t)x * 128u; }
 };
 
-// Four E4M3 values (one word) as four FP16, two words.
+// Four E4M3 values (one word) as four FP16 values / 256, two words: the sign
+// and the seven other bits, moved to where FP16 has its sign, the low four bits
+// of its exponent and the high three of its mantissa, are exactly that, E4M3's
+// subnormals included.  (The conversion instruction would take the 16,384 values
+// of a tile some 4,000 cycles; this is four integer instructions for two.)  A NaN
+// code comes out as 480 / 256 and is put right by the caller.
 __device__ __forceinline__ void widen4(uint32_t w, uint32_t &lo, uint32_t &hi) {
-    const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
-    const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
-    lo = (uint32_t)a.x | ((uint32_t)a.y << 16);
-    hi = (uint32_t)b.x | ((uint32_t)b.y << 16);
+    const uint32_t a = __byte_perm(w, 0, 0x1404), b = __byte_perm(w, 0, 0x3424);   // bytes 0, 1 and 2, 3, each << 8
+    lo = ((a & 0x7f007f00u) >> 1) | (a & 0x80008000u);
+    hi = ((b & 0x7f007f00u) >> 1) | (b & 0x80008000u);
+}
+
+// FP16 NaN in place of the lanes that widen4 made of NaN codes.
+__device__ __forceinline__ uint32_t nan_lanes(uint32_t h) {
+    if ((h & 0x7fffu) == 0x3f80u) h |= 0x7fffu;
+    if ((h & 0x7fff0000u) == 0x3f800000u) h |= 0x7fff0000u;
+    return h;
+}
+
+// -inf in place of the scores of hidden keys.
+__device__ __forceinline__ void hide(float (&v)[64], uint32_t lo, uint32_t hi) {
+#pragma unroll
+    for (int i = 0; i < 64; ++i)
+        if (!((i < 32 ? lo : hi) >> (i & 31) & 1)) v[i] = kNegInf;
 }
 
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
@@ -275,6 +292,7 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
             auto k_there = [&](uint32_t i) {
                 return mbar_try_wait(smem_u32(&k_full[i % C::kKSlots]), (i / C::kKSlots) & 1);
             };
+            const uint32_t idesc_qk = kIdescQK | (p.scale_log2 < 0.f ? kIdescNegateA : 0u);
             auto push_qk = [&](uint32_t i, int buf) {
                 const SDesc kd{k_d.lo + (i % C::kKSlots) * (C::kKBytes >> 4), k_d.hi};
 #pragma unroll
@@ -282,7 +300,7 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
                         mma_f8_ss(tmem + C::s_col(x, buf), sdesc_at(q_d, term * C::kHalf + kk * 32),
-                                  sdesc_at(kd, kk * 32), kIdescQK, term + kk > 0 ? 1u : 0u);
+                                  sdesc_at(kd, kk * 32), idesc_qk, term + kk > 0 ? 1u : 0u);
             };
             auto push_pv_half = [&](uint32_t i, int buf, int half, bool first) {
                 const SDesc vd{v_d.lo + (i % C::kVSlots) * (C::kVBytes >> 4), v_d.hi};
@@ -388,54 +406,57 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
             if (u.b < 0) break;
             mbar_wait(q_full, k & 1, wc);
             for (int x = 0; x < u.nrt; ++x) {
-                // BF16 row * 2^e = hi + mid, both E4M3, over the row's own bytes.
-                uint8_t *qr = sQ + x * C::kQBytes + row * 128;
-                auto unit = [&](int c) {
-                    return *reinterpret_cast<const uint4 *>(qr + (c >> 3) * C::kHalf + (((c & 7) ^ sw) << 4));
-                };
-                uint32_t big = 0;                         // largest magnitude, as the bits of an FP32
-                auto fold = [&](uint32_t v) { big = max(big, max((v << 16) & 0x7fff0000u, v & 0x7fff0000u)); };
-#pragma unroll 4
-                for (int c = 0; c < 16; ++c) {
-                    const uint4 w = unit(c);
+                // BF16 row * 2^e = hi + mid, both E4M3, over the row's own bytes: 16 lanes
+                // hold a row's 16-byte units, two rows a pass, all read before any is
+                // written.
+                uint8_t *q0 = sQ + x * C::kQBytes;
+                const int un = lane & 15;
+#pragma unroll 1
+                for (int r = (row & ~31) + (lane >> 4); r < (row & ~31) + 32; r += 2) {
+                    const uint32_t rs = r & 7;
+                    const uint4 w = *reinterpret_cast<const uint4 *>(q0 + (un >> 3) * C::kHalf + r * 128 +
+                                                                     (((un & 7) ^ rs) << 4));
+                    uint32_t big = 0;                     // largest magnitude, as the bits of an FP32
+                    auto fold = [&](uint32_t v) { big = max(big, max((v << 16) & 0x7fff0000u, v & 0x7fff0000u)); };
                     fold(w.x); fold(w.y); fold(w.z); fold(w.w);
+#pragma unroll
+                    for (int o = 8; o > 0; o >>= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
+                    const int e = min(126, max(-120, 134 - (int)(big >> 23)));   // 7 - (exponent - 127)
+                    if (un == 0) q_exp[(k % C::kSched * NT + x) * 128 + r] = (int8_t)e;
+                    // Times 2^(e - 120), an FP32's exponent field is the E4M3 code's, and
+                    // its bits from 20 on are the code (truncated), subnormals included:
+                    // hi is the first four bits of the significand, mid the rest, rounded
+                    // to nearest where it is too small for four bits.  An infinite or NaN
+                    // element makes the row's scores NaN.
+                    const bool bad = big >= 0x7f800000u;
+                    const float up0 = __int_as_float((127 + (e - 120) / 2) << 23);
+                    const float up1 = __int_as_float((127 + (e - 120) - (e - 120) / 2) << 23);
+                    auto split1 = [&](uint32_t bits, uint32_t &hi, uint32_t &mid) {
+                        const float f = __uint_as_float(bits) * up0 * up1;
+                        const uint32_t fb = __float_as_uint(f);
+                        const uint32_t hb = fb & 0xfff00000u;
+                        const uint32_t mb = __float_as_uint(f - __uint_as_float(hb));
+                        const uint32_t mr = mb + 0x7ffffu + (mb >> 20 & 1u);
+                        hi = bad ? 0x7fu : (fb >> 24 & 0x80u) | (fb >> 20 & 0x7fu);
+                        mid = (fb >> 24 & 0x80u) | (mr >> 20 & 0x7fu);
+                    };
+                    auto split4 = [&](uint32_t v0, uint32_t v1, uint32_t &hi, uint32_t &mid) {
+                        uint32_t hc[4], mc[4];
+                        split1(v0 << 16, hc[0], mc[0]);
+                        split1(v0 & 0xffff0000u, hc[1], mc[1]);
+                        split1(v1 << 16, hc[2], mc[2]);
+                        split1(v1 & 0xffff0000u, hc[3], mc[3]);
+                        hi = __byte_perm(__byte_perm(hc[0], hc[1], 0x0040), __byte_perm(hc[2], hc[3], 0x0040), 0x5410);
+                        mid = __byte_perm(__byte_perm(mc[0], mc[1], 0x0040), __byte_perm(mc[2], mc[3], 0x0040), 0x5410);
+                    };
+                    uint2 hi, mid;
+                    split4(w.x, w.y, hi.x, mid.x);
+                    split4(w.z, w.w, hi.y, mid.y);
+                    __syncwarp();
+                    uint8_t *to = q0 + r * 128 + (((un >> 1) ^ rs) << 4) + (un & 1) * 8;
+                    *reinterpret_cast<uint2 *>(to) = hi;
+                    *reinterpret_cast<uint2 *>(to + C::kHalf) = mid;
                 }
-                const int e = min(126, max(-120, 134 - (int)(big >> 23)));   // 7 - (exponent - 127)
-                // An infinite or NaN element makes the row's scores NaN.
-                const float up = __int_as_float(big >= 0x7f800000u ? 0x7fc00000 : (127 + e) << 23);
-                q_exp[(k % C::kSched * NT + x) * 128 + row] = (int8_t)e;
-                auto split4 = [&](uint32_t v0, uint32_t v1, uint32_t &hi, uint32_t &mid) {
-                    const float a = __uint_as_float(v0 << 16) * up, b = __uint_as_float(v0 & 0xffff0000u) * up;
-                    const float c = __uint_as_float(v1 << 16) * up, d = __uint_as_float(v1 & 0xffff0000u) * up;
-                    const __nv_fp8x2_storage_t h0 = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-                    const __nv_fp8x2_storage_t h1 = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
-                    const float2 f0 = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(h0, __NV_E4M3)));
-                    const float2 f1 = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(h1, __NV_E4M3)));
-                    hi = (uint32_t)h0 | ((uint32_t)h1 << 16);
-                    mid = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a - f0.x, b - f0.y), __NV_SATFINITE, __NV_E4M3) |
-                          ((uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(c - f1.x, d - f1.y), __NV_SATFINITE, __NV_E4M3) << 16);
-                };
-                // Unit c of a term takes BF16 units 2c and 2c + 1; hi goes over unit c,
-                // mid over unit 8 + c: the first four mids wait until those are read.
-                auto split_unit = [&](int c, uint4 &hi, uint4 &mid) {
-                    const uint4 w0 = unit(2 * c), w1 = unit(2 * c + 1);
-                    split4(w0.x, w0.y, hi.x, mid.x);
-                    split4(w0.z, w0.w, hi.y, mid.y);
-                    split4(w1.x, w1.y, hi.z, mid.z);
-                    split4(w1.z, w1.w, hi.w, mid.w);
-                };
-                auto put = [&](int term, int c, const uint4 &v) {
-                    *reinterpret_cast<uint4 *>(qr + term * C::kHalf + ((c ^ sw) << 4)) = v;
-                };
-                uint4 hi[4], mid[4], mid2[4];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) split_unit(c, hi[c], mid[c]);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) put(0, c, hi[c]);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) split_unit(4 + c, hi[c], mid2[c]);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) { put(0, 4 + c, hi[c]); put(1, c, mid[c]); put(1, 4 + c, mid2[c]); }
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -449,23 +470,39 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
                 const uint32_t sl = i % C::kVSlots;
                 mbar_wait(&v_raw[sl], (i / C::kVSlots) & 1, wc);
                 uint8_t *vr = sV + sl * C::kVBytes + row * 128;
-                uint4 w[8];
+                // Half hh of the key's E4M3 bytes becomes its FP16 row in half hh of the
+                // slot; the second half overwrites the E4M3 bytes, its own read first.
+                // (Rolled: unrolled, this and the softmax evict each other from the
+                // instruction cache, which more than doubled both.)
+                uint32_t full = 0;                        // bit 7 of a byte: its other seven were all ones, a NaN
+#pragma unroll 1
+                for (int hh = 0; hh < 2; ++hh) {
+                    uint4 w[4];
 #pragma unroll
-                for (int c = 0; c < 8; ++c) w[c] = *reinterpret_cast<const uint4 *>(vr + C::kHalf + ((c ^ sw) << 4));
-                if (hidden) {
+                    for (int c = 0; c < 4; ++c)
+                        w[c] = *reinterpret_cast<const uint4 *>(vr + C::kHalf + (((hh * 4 + c) ^ sw) << 4));
+                    uint8_t *to = vr + hh * C::kHalf;
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) w[c] = make_uint4(0, 0, 0, 0);
+                    for (int c = 0; c < 4; ++c) {         // 16 values: two units of FP16
+                        if (hidden) w[c] = make_uint4(0, 0, 0, 0);
+                        uint4 a, b;
+                        widen4(w[c].x, a.x, a.y);
+                        widen4(w[c].y, a.z, a.w);
+                        widen4(w[c].z, b.x, b.y);
+                        widen4(w[c].w, b.z, b.w);
+                        full |= ((w[c].x & 0x7f7f7f7fu) + 0x01010101u) | ((w[c].y & 0x7f7f7f7fu) + 0x01010101u) |
+                                ((w[c].z & 0x7f7f7f7fu) + 0x01010101u) | ((w[c].w & 0x7f7f7f7fu) + 0x01010101u);
+                        *reinterpret_cast<uint4 *>(to + (((2 * c) ^ sw) << 4)) = a;
+                        *reinterpret_cast<uint4 *>(to + (((2 * c + 1) ^ sw) << 4)) = b;
+                    }
                 }
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {             // 16 values: two units of FP16
-                    uint4 a, b;
-                    widen4(w[c].x, a.x, a.y);
-                    widen4(w[c].y, a.z, a.w);
-                    widen4(w[c].z, b.x, b.y);
-                    widen4(w[c].w, b.z, b.w);
-                    uint8_t *to = vr + (c >> 2) * C::kHalf;
-                    *reinterpret_cast<uint4 *>(to + (((2 * c) & 7) ^ sw) * 16) = a;
-                    *reinterpret_cast<uint4 *>(to + (((2 * c + 1) & 7) ^ sw) * 16) = b;
+                if (full & 0x80808080u) {
+#pragma unroll 1
+                    for (int c = 0; c < 16; ++c) {
+                        uint4 *at = reinterpret_cast<uint4 *>(vr + (c >> 3) * C::kHalf + (((c & 7) ^ sw) << 4));
+                        const uint4 h = *at;
+                        *at = make_uint4(nan_lanes(h.x), nan_lanes(h.y), nan_lanes(h.z), nan_lanes(h.w));
+                    }
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -479,7 +516,6 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
         const int q4 = warp & 3;
         const int row = q4 * 32 + lane;
         const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
-        const bool scale_pos = p.scale_log2 >= 0.f;
         uint32_t steps = 0, pieces = 0;
         auto wait_pv = [&](uint32_t step) { mbar_wait(&pv_done[x * kSB + step % kSB], (step / kSB) & 1, wc); };
         for (int k = 0;; ++k) {
@@ -490,7 +526,7 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
             // The row's exponent is read before the record goes back: unit k + 4,
             // which reuses its place, cannot come before that.
             if (u.b >= 0) mbar_wait(&q_ready[k % C::kSched], (k / C::kSched) & 1, wc);
-            const float rs = p.scale_log2 * __int_as_float((127 - q_exp[(k % C::kSched * NT + x) * 128 + row]) << 23);
+            const float rs = fabsf(p.scale_log2) * __int_as_float((127 - q_exp[(k % C::kSched * NT + x) * 128 + row]) << 23);
             __syncwarp();
             if (lane == 0) free_unit(k);
             if (u.b < 0) break;
@@ -519,33 +555,23 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
 #pragma unroll
                     for (int w = 0; w < 4; ++w) bits[w] = live ? draft_bits(mrow, key0 + 32 * w - base, u.d) : 0u;
                 }
-                const float gone = scale_pos ? kNegInf : -kNegInf;
-                // The row of S is read twice, for its maximum and for P: with two
-                // streams' softmax warps its 128 scores do not fit their registers.
-                float ext = gone;
-#pragma unroll
+                // The row of S is read twice, for its maximum and for P, 64 keys at a
+                // time: two streams' softmax warps have no registers for all of it, and
+                // the rolled loops keep the code small.
+                float ext = kNegInf;
+#pragma unroll 1
                 for (int c = 0; c < 2; ++c) {
                     float v[64];
                     tmem_ld32(sa + c * 64, v);
                     tmem_ld32(sa + c * 64 + 32, v + 32);
                     tmem_wait_ld();
-                    if (drafts) {
-#pragma unroll
-                        for (int i = 0; i < 64; ++i)
-                            if (!(bits[c * 2 + (i >> 5)] >> (i & 31) & 1)) v[i] = gone;
-                    }
+                    if (drafts) hide(v, c == 0 ? bits[0] : bits[2], c == 0 ? bits[1] : bits[3]);
                     float e4[4] = {v[0], v[1], v[2], v[3]};
-                    if (scale_pos) {
 #pragma unroll
-                        for (int i = 4; i < 64; ++i) e4[i & 3] = fmaxf(e4[i & 3], v[i]);
-                        ext = fmaxf(ext, fmaxf(fmaxf(e4[0], e4[1]), fmaxf(e4[2], e4[3])));
-                    } else {
-#pragma unroll
-                        for (int i = 4; i < 64; ++i) e4[i & 3] = fminf(e4[i & 3], v[i]);
-                        ext = fminf(ext, fminf(fminf(e4[0], e4[1]), fminf(e4[2], e4[3])));
-                    }
+                    for (int i = 4; i < 64; ++i) e4[i & 3] = fmaxf(e4[i & 3], v[i]);
+                    ext = fmaxf(ext, fmaxf(fmaxf(e4[0], e4[1]), fmaxf(e4[2], e4[3])));
                 }
-                const float m_tile = ext == gone || !live ? kNegInf : ext * rs;
+                const float m_tile = ext == kNegInf || !live ? kNegInf : ext * rs;
                 const bool up = m_tile > m_ref + kRescaleSlack;
                 if (__any_sync(0xffffffffu, up)) {
                     float alpha = 1.f;
@@ -578,18 +604,14 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
                 float a8[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) a8[i] = 0.f;
-#pragma unroll
+#pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
                     float v[64];
                     uint32_t pk[32];
                     tmem_ld32(sa + half * 64, v);
                     tmem_ld32(sa + half * 64 + 32, v + 32);
                     tmem_wait_ld();
-                    if (drafts) {
-#pragma unroll
-                        for (int i = 0; i < 64; ++i)
-                            if (!(bits[half * 2 + (i >> 5)] >> (i & 31) & 1)) v[i] = gone;
-                    }
+                    if (drafts) hide(v, half == 0 ? bits[0] : bits[2], half == 0 ? bits[1] : bits[3]);
 #pragma unroll
                     for (int i = 0; i < 64; i += 2) {
                         const float p0 = ex2_approx(fmaf(v[i], rs, -mu));

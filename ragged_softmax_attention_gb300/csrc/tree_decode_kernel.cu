@@ -260,6 +260,7 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
 #pragma unroll
                 for (int s = 0; s < TS; ++s) mma_commit(&slot_empty[(r + s) % C::kSlots]);
             };
+            const uint32_t idesc_qk = C::kIdescQK | (p.scale_log2 < 0.f ? kIdescNegateA : 0u);
             auto push_qk = [&](uint32_t r, int buf) {
 #pragma unroll
                 for (int s = 0; s < TS; ++s) {
@@ -268,7 +269,7 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
                     for (int kk = 0; kk < 8; ++kk) {
                         const uint32_t off = (kk >> 2) * C::kChunkBytes + (kk & 3) * 32;
                         mma_bf16_ss(tmem + C::s_col(x, buf), sdesc_at(q_d, s * C::kSlotBytes + off), sdesc_at(kd, off),
-                                    C::kIdescQK, s + kk > 0 ? 1u : 0u);
+                                    idesc_qk, s + kk > 0 ? 1u : 0u);
                     }
                 }
             };
@@ -377,7 +378,7 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
         const int q4 = warp & 3;
         const int row = q4 * 32 + lane;
         const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
-        const bool scale_pos = p.scale_log2 >= 0.f;
+        const float scale = fabsf(p.scale_log2);      // the MMA negates Q for a negative one
         // Two S buffers: PV of step i completes phase i / 2 of its buffer's barrier.
         // (A barrier per step could be one phase behind or one ahead of a wait,
         // which a parity does not tell apart.)
@@ -454,24 +455,17 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
                         const uint32_t bits = live ? draft_bits(mrow, key0 + 32 * w - base, u.d) : 0u;
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            if (!(bits >> i & 1)) sv[w * 32 + i] = scale_pos ? kNegInf : -kNegInf;
+                            if (!(bits >> i & 1)) sv[w * 32 + i] = kNegInf;
                     }
                 }
                 float e8[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) e8[i] = sv[i];
-                if (scale_pos) {
 #pragma unroll
-                    for (int i = 8; i < kKvTile; ++i) e8[i & 7] = fmaxf(e8[i & 7], sv[i]);
-                } else {
-#pragma unroll
-                    for (int i = 8; i < kKvTile; ++i) e8[i & 7] = fminf(e8[i & 7], sv[i]);
-                }
-                const float ext = scale_pos
-                    ? fmaxf(fmaxf(fmaxf(e8[0], e8[1]), fmaxf(e8[2], e8[3])), fmaxf(fmaxf(e8[4], e8[5]), fmaxf(e8[6], e8[7])))
-                    : fminf(fminf(fminf(e8[0], e8[1]), fminf(e8[2], e8[3])), fminf(fminf(e8[4], e8[5]), fminf(e8[6], e8[7])));
-                const bool none = ext == (scale_pos ? kNegInf : -kNegInf);
-                const float m_tile = none || !live ? kNegInf : ext * p.scale_log2;
+                for (int i = 8; i < kKvTile; ++i) e8[i & 7] = fmaxf(e8[i & 7], sv[i]);
+                const float ext = fmaxf(fmaxf(fmaxf(e8[0], e8[1]), fmaxf(e8[2], e8[3])),
+                                        fmaxf(fmaxf(e8[4], e8[5]), fmaxf(e8[6], e8[7])));
+                const float m_tile = live ? ext * scale : kNegInf;    // -inf when it sees none of these keys
                 const bool up = m_tile > m_ref + kRescaleSlack;   // also the first visible tile: m_ref = -inf
                 if (__any_sync(0xffffffffu, up)) {
                     float alpha = 1.f;
@@ -512,8 +506,8 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
 #pragma unroll
                     for (int i = 0; i < kKvTile / 2; i += 2) {
                         const int kx = half * (kKvTile / 2) + i;
-                        const float p0 = ex2_approx(fmaf(sv[kx], p.scale_log2, -mu));
-                        const float p1 = ex2_approx(fmaf(sv[kx + 1], p.scale_log2, -mu));
+                        const float p0 = ex2_approx(fmaf(sv[kx], scale, -mu));
+                        const float p1 = ex2_approx(fmaf(sv[kx + 1], scale, -mu));
                         a8[(i >> 1) & 7] += p0 + p1;
                         pk[kx >> 1] = pack_bf16x2(p0, p1);
                     }
@@ -554,64 +548,77 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
 
 // Merges the pieces of the units that CTA ranges cut: with weighted sums o_i,
 // row sums l_i and bases m_i, M = max m_i, out = sum 2^(m_i - M) o_i /
-// sum 2^(m_i - M) l_i.  Block (chunk, c) takes 32 rows of the unit whose first
-// piece ended CTA c's range; its other pieces opened the following ranges.
+// sum 2^(m_i - M) l_i.  The pieces of the unit whose first one ended CTA c's
+// range opened the following ranges.  One warp per row, eight rows of that unit
+// to block (chunk, c); lanes share the pieces' bases, and the rows of O come
+// four pieces at a time, so that a row costs three dependent reads whatever the
+// number of pieces (four rows to a warp, a piece after the other, took 6.5 us
+// where this takes 2).
 template <int D, int NT>
 __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__ TreeParams p) {
     pdl_wait();                                      // the pieces are written
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const TreeCut cut = p.cuts[blockIdx.y];
-    const int x = blockIdx.x / 4;
-    if (cut.count == 0 || x >= cut.nrt) return;
+    const int x = blockIdx.x / 16;
+    const int row = (blockIdx.x & 15) * 8 + warp;
+    int t, h;
+    if (cut.count == 0 || x >= cut.nrt || !tree_tile_row(p, cut.rt0 + x, cut.g, cut.d, row, t, h)) return;
     const int step = p.ride ? p.Hkv : 1;
-    for (int i = 0; i < 4; ++i) {
-        const int row = (blockIdx.x & 3) * 32 + warp * 4 + i;
-        int t, h;
-        if (!tree_tile_row(p, cut.rt0 + x, cut.g, cut.d, row, t, h)) continue;
-        auto slot_row = [&](int k) -> int64_t {
-            const int slot = k == 0 ? 2 * blockIdx.y + 1 : 2 * (blockIdx.y + k * step);
-            return (int64_t)slot * (NT * 128) + x * 128 + row;
-        };
-        float m = kNegInf;
-        for (int k = lane; k < cut.count; k += 32) {
-            const float2 ml = p.part_ml[slot_row(k)];
-            if (ml.y > 0.f) m = fmaxf(m, ml.x);
-        }
-        m = warp_max(m);
-        constexpr int V = D / 32;
-        float acc[V], l = 0.f;
+    auto slot_row = [&](int k) -> int64_t {
+        const int slot = k == 0 ? 2 * blockIdx.y + 1 : 2 * (blockIdx.y + k * step);
+        return (int64_t)slot * (NT * 128) + x * 128 + row;
+    };
+    constexpr int V = D / 128;                       // float4 per lane and piece
+    float acc[4 * V], l = 0.f, m = kNegInf;
 #pragma unroll
-        for (int c = 0; c < V; ++c) acc[c] = 0.f;
-        for (int k = 0; k < cut.count; ++k) {
-            const int64_t r = slot_row(k);
-            const float2 ml = p.part_ml[r];
-            if (!(ml.y > 0.f)) continue;
-            const float w = ex2_approx(ml.x - m);
-            l = fmaf(w, ml.y, l);
-            const float4 *src = reinterpret_cast<const float4 *>(p.part_o + r * D);
+    for (int c = 0; c < 4 * V; ++c) acc[c] = 0.f;
+    for (int k0 = 0; k0 < cut.count; k0 += 32) {     // 32 pieces at a time, on a common base
+        const float2 ml = k0 + lane < cut.count ? p.part_ml[slot_row(k0 + lane)] : make_float2(kNegInf, 0.f);
+        const float mk = ml.y > 0.f ? ml.x : kNegInf;
+        const float mn = fmaxf(m, warp_max(mk));
+        if (mn == kNegInf) continue;                 // nothing visible so far
+        const float alpha = ex2_approx(m - mn);
+        const float w = ex2_approx(mk - mn);
+        l = l * alpha + warp_sum(ml.y > 0.f ? w * ml.y : 0.f);
+        m = mn;
 #pragma unroll
-            for (int c = 0; c < V / 4; ++c) {
-                const float4 v = src[c * 32 + lane];
-                acc[4 * c + 0] = fmaf(w, v.x, acc[4 * c + 0]);
-                acc[4 * c + 1] = fmaf(w, v.y, acc[4 * c + 1]);
-                acc[4 * c + 2] = fmaf(w, v.z, acc[4 * c + 2]);
-                acc[4 * c + 3] = fmaf(w, v.w, acc[4 * c + 3]);
+        for (int c = 0; c < 4 * V; ++c) acc[c] *= alpha;
+        const int nk = min(32, cut.count - k0);
+        for (int k = 0; k < nk; k += 4) {
+            float4 v[4][V];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float4 *src = reinterpret_cast<const float4 *>(p.part_o + slot_row(k0 + min(k + i, nk - 1)) * D);
+#pragma unroll
+                for (int c = 0; c < V; ++c) v[i][c] = src[c * 32 + lane];
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float wk = __shfl_sync(0xffffffffu, w, min(k + i, 31));
+                if (k + i >= nk || wk == 0.f) continue;
+#pragma unroll
+                for (int c = 0; c < V; ++c) {
+                    acc[4 * c + 0] = fmaf(wk, v[i][c].x, acc[4 * c + 0]);
+                    acc[4 * c + 1] = fmaf(wk, v[i][c].y, acc[4 * c + 1]);
+                    acc[4 * c + 2] = fmaf(wk, v[i][c].z, acc[4 * c + 2]);
+                    acc[4 * c + 3] = fmaf(wk, v[i][c].w, acc[4 * c + 3]);
+                }
             }
         }
-        const float inv = l > 0.f ? p.out_scale / l : 0.f;
-        __nv_bfloat16 *o = reinterpret_cast<__nv_bfloat16 *>(p.out) + cut.b * p.out_stride[0] + t * p.out_stride[1] +
-                           h * p.out_stride[2];
-#pragma unroll
-        for (int c = 0; c < V / 4; ++c) {
-            uint2 v;
-            v.x = pack_bf16x2(acc[4 * c] * inv, acc[4 * c + 1] * inv);
-            v.y = pack_bf16x2(acc[4 * c + 2] * inv, acc[4 * c + 3] * inv);
-            reinterpret_cast<uint2 *>(o)[c * 32 + lane] = v;
-        }
-        if (lane == 0 && p.lse)
-            p.lse[cut.b * p.lse_stride[0] + t * p.lse_stride[1] + h * p.lse_stride[2]] =
-                l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : kNegInf;
     }
+    const float inv = l > 0.f ? p.out_scale / l : 0.f;
+    __nv_bfloat16 *o = reinterpret_cast<__nv_bfloat16 *>(p.out) + cut.b * p.out_stride[0] + t * p.out_stride[1] +
+                       h * p.out_stride[2];
+#pragma unroll
+    for (int c = 0; c < V; ++c) {
+        uint2 v;
+        v.x = pack_bf16x2(acc[4 * c] * inv, acc[4 * c + 1] * inv);
+        v.y = pack_bf16x2(acc[4 * c + 2] * inv, acc[4 * c + 3] * inv);
+        reinterpret_cast<uint2 *>(o)[c * 32 + lane] = v;
+    }
+    if (lane == 0 && p.lse)
+        p.lse[cut.b * p.lse_stride[0] + t * p.lse_stride[1] + h * p.lse_stride[2]] =
+            l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : kNegInf;
 }
 
 template <int D, int NT>
@@ -626,7 +633,7 @@ cudaError_t launch_bf16(const TreeParams &p, const CUtensorMap &tq, const CUtens
 }  // namespace
 
 cudaError_t launch_tree_merge(const TreeParams &p, int row_tiles, cudaStream_t stream) {
-    const dim3 grid(row_tiles * 4, p.grid);
+    const dim3 grid(row_tiles * 16, p.grid);
     if (p.D == 256) return launch_after_previous(tree_merge_kernel<256, 1>, grid, dim3(256), 0, stream, p);
     if (row_tiles == 2) return launch_after_previous(tree_merge_kernel<128, 2>, grid, dim3(256), 0, stream, p);
     return launch_after_previous(tree_merge_kernel<128, 1>, grid, dim3(256), 0, stream, p);
