@@ -9,7 +9,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import struct
 from typing import Optional
 
 import torch
@@ -305,72 +304,44 @@ def varlen_prefill(q, k, v, cu_seqlens_q, cu_seqlens_k, causal, scale, out=None,
 
 # ------------------------------------------------------ speculative decoding
 #
-# These run on the device of their tensors, whichever is current, and their
-# outputs and workspaces are allocated on the stream the kernels run on.
+# A step of these takes the GPU a few microseconds, so their marshalling is in
+# C++ (csrc/fast_binding.cpp).  They run on the device of their tensors,
+# whichever is current, and their outputs and workspaces are allocated on the
+# stream the kernels run on: the current one, or `stream`.
 
-_TENSOR = struct.Struct("=Qii10q")          # fw_tensor_t
-_PAD = tuple((0,) * (5 - i) for i in range(6))
-
-
-def _pack(tensors):
-    """fw_tensor_t records of the tensors in one buffer: (buffer, addresses);
-    None -> NULL.  One packing call per tensor: these entry points serve steps
-    of a few microseconds."""
-    buf = ctypes.create_string_buffer(_TENSOR.size * len(tensors))
-    base = ctypes.addressof(buf)
-    ptrs = []
-    for i, t in enumerate(tensors):
-        if t is None:
-            ptrs.append(None)
-            continue
-        code = _DTYPES.get(t.dtype)
-        if code is None:
-            raise TypeError(f"unsupported dtype {t.dtype}")
-        nd = t.dim()
-        if nd > 5:
-            raise ValueError("at most 5 dimensions")
-        pad = _PAD[nd]
-        _TENSOR.pack_into(buf, _TENSOR.size * i, t.data_ptr() if t.numel() else 0, code, nd, *t.shape, *pad,
-                          *t.stride(), *pad)
-        ptrs.append(base + _TENSOR.size * i)
-    return buf, ptrs
+_FAST_ENTRIES = ("fw_paged_decode_tree", "fw_paged_decode_tree_workspace_size", "fw_tree_mask",
+                 "fw_build_page_tables", "fw_kv_commit")
+_fast_module = None
 
 
-class _Launch:
-    """Device and stream of a call: the tensors' device becomes current, and so
-    does `stream` when one is given; the with-value is the stream's handle."""
-
-    def __init__(self, stream, tensors):
-        dev = None
-        for t in tensors:
-            if t is None:
-                continue
-            i = t.get_device()
-            if i < 0:
-                raise ValueError("the tensors must be on a CUDA device")
-            if dev is None:
-                dev = i
-            elif i != dev:
-                raise ValueError("the tensors must be on one device")
-        if stream is not None and stream.device.index != dev:
-            raise ValueError("the stream must be of the tensors' device")
-        self.dev, self.stream, self.scopes = dev, stream, []
-
-    def __enter__(self):
-        if self.dev != torch.cuda.current_device():
-            self.scopes.append(torch.cuda.device(self.dev))
-        if self.stream is not None:
-            self.scopes.append(torch.cuda.stream(self.stream))
-        for s in self.scopes:
-            s.__enter__()
-        return torch.cuda.current_stream().cuda_stream
-
-    def __exit__(self, *exc):
-        for s in reversed(self.scopes):
-            s.__exit__(*exc)
+def _fast():
+    """The C++ marshalling module, connected to the loaded library; raises if it is missing."""
+    global _fast_module
+    if _fast_module is None:
+        import importlib.machinery
+        import importlib.util
+        path = os.path.join(_HERE, "_fw_fast.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is not built; run ragged_softmax_attention_gb300.build.build() first")
+        lib = load_library()
+        loader = importlib.machinery.ExtensionFileLoader("_fw_fast", path)
+        spec = importlib.util.spec_from_file_location("_fw_fast", path, loader=loader)
+        module = importlib.util.module_from_spec(spec)
+        loader.exec_module(module)
+        module.connect(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in _FAST_ENTRIES), _check)
+        _fast_module = module
+    return _fast_module
 
 
-_tree_workspace = {}                        # (device, head dim) -> bytes
+def _on(stream, call, *args):
+    """call(*args), on `stream` when one is given."""
+    if stream is None:
+        return call(*args)
+    first = next(a for a in args if isinstance(a, torch.Tensor))
+    if stream.device != first.device:
+        raise ValueError("the stream must be of the tensors' device")
+    with torch.cuda.stream(stream):
+        return call(*args)
 
 
 def paged_decode_tree_workspace_size(head_dim) -> int:
@@ -388,44 +359,15 @@ def paged_decode_tree(q, k_cache, v_cache, block_table, seq_lens, tree_mask, sca
     caches.  workspace: bytes for the split partials (None: a fresh buffer from
     torch's allocator, so calls on several streams and captured graphs share
     nothing).  Returns (out [B, T, Hq, D] bf16, lse [B, T, Hq] f32 or None)."""
-    lib = load_library()
-    with _Launch(stream, (q, k_cache, v_cache, block_table, seq_lens, tree_mask, draft_lens, out, lse,
-                          workspace)) as handle:
-        if out is None:
-            out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-        if lse is None and return_lse:
-            lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
-        if workspace is None:
-            key = (q.device.index, q.shape[-1])
-            need = _tree_workspace.get(key)
-            if need is None:
-                need = _tree_workspace[key] = paged_decode_tree_workspace_size(q.shape[-1])
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        elif not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous")
-        buf, a = _pack((q, k_cache, v_cache, block_table, seq_lens, tree_mask, draft_lens, out, lse))
-        _check(lib.fw_paged_decode_tree(a[0], a[1], a[2], a[3], a[4], a[5], a[6], float(scale), float(k_scale),
-                                        float(v_scale), a[7], a[8],
-                                        workspace.data_ptr(), workspace.numel() * workspace.element_size(), handle))
-    return out, lse
+    return _on(stream, (_fast_module or _fast()).paged_decode_tree, q, k_cache, v_cache, block_table, seq_lens,
+               tree_mask, draft_lens, scale, k_scale, v_scale, out, lse, return_lse, workspace)
 
 
 def tree_mask(parents, draft_lens=None, mask=None, depths=None, stream=None):
     """fw_tree_mask: parents [B, T] (-1: child of the committed context) to
     (mask [B, T, ceil(T / 32)] i32 of each draft's ancestors and itself, depths
     [B, T] i32)."""
-    lib = load_library()
-    with _Launch(stream, (parents, draft_lens, mask, depths)) as handle:
-        if parents.dim() != 2:
-            raise ValueError("parents must be [B, T]")
-        B, T = parents.shape
-        if mask is None:
-            mask = torch.empty((B, T, (T + 31) // 32), dtype=torch.int32, device=parents.device)
-        if depths is None:
-            depths = torch.empty((B, T), dtype=torch.int32, device=parents.device)
-        buf, a = _pack((parents, draft_lens, mask, depths))
-        _check(lib.fw_tree_mask(a[0], a[1], a[2], a[3], handle))
-    return mask, depths
+    return _on(stream, (_fast_module or _fast()).tree_mask, parents, draft_lens, mask, depths)
 
 
 def build_page_tables(seq_lens, new_lens, held, free_queue, free_range, page_size, block_table, slot_mapping,
@@ -434,20 +376,8 @@ def build_page_tables(seq_lens, new_lens, held, free_queue, free_range, page_siz
     [F] / free_range [2], updates block_table [B, max_pages] and writes the
     step's slot_mapping ([N] packed or [B, L]).  Returns (cu_new [B + 1],
     held_out [B], range_out [2]); the last two may be held and free_range."""
-    lib = load_library()
-    with _Launch(stream, (seq_lens, new_lens, held, free_queue, free_range, block_table, slot_mapping, cu_new,
-                          held_out, range_out)) as handle:
-        if cu_new is None:
-            cu_new = torch.empty(seq_lens.numel() + 1, dtype=torch.int32, device=seq_lens.device)
-        if held_out is None:
-            held_out = torch.empty(seq_lens.numel(), dtype=torch.int32, device=seq_lens.device)
-        if range_out is None:
-            range_out = torch.empty(2, dtype=torch.int32, device=seq_lens.device)
-        buf, a = _pack((seq_lens, new_lens, held, free_queue, free_range, block_table, slot_mapping, cu_new, held_out,
-                        range_out))
-        _check(lib.fw_build_page_tables(a[0], a[1], a[2], a[3], a[4], int(page_size), a[5], a[6], a[7], a[8], a[9],
-                                        handle))
-    return cu_new, held_out, range_out
+    return _on(stream, (_fast_module or _fast()).build_page_tables, seq_lens, new_lens, held, free_queue, free_range,
+               page_size, block_table, slot_mapping, cu_new, held_out, range_out)
 
 
 def kv_commit(path, path_lens, base_lens, block_table, k_cache, v_cache, num_layers=1, new_lens=None, stream=None):
@@ -455,13 +385,8 @@ def kv_commit(path, path_lens, base_lens, block_table, k_cache, v_cache, num_lay
     position base_lens[b] + path[b, i], i < path_lens[b], in place (path
     strictly increasing; v_cache may be None).  Returns new_lens [B] =
     base_lens + path_lens."""
-    lib = load_library()
-    with _Launch(stream, (path, path_lens, base_lens, block_table, k_cache, v_cache, new_lens)) as handle:
-        if new_lens is None:
-            new_lens = torch.empty(path_lens.numel(), dtype=torch.int32, device=path.device)
-        buf, a = _pack((path, path_lens, base_lens, block_table, k_cache, v_cache, new_lens))
-        _check(lib.fw_kv_commit(a[0], a[1], a[2], a[3], int(num_layers), a[4], a[5], a[6], handle))
-    return new_lens
+    return _on(stream, (_fast_module or _fast()).kv_commit, path, path_lens, base_lens, block_table, k_cache, v_cache,
+               num_layers, new_lens)
 
 
 def set_workspace(buf: Optional[torch.Tensor], stream=None):

@@ -2,7 +2,9 @@
 
 Each .cu under csrc/ is compiled to an object in parallel, then linked into
 one shared library with the CUDA runtime linked statically.  Objects are
-rebuilt when their source or any header changed.
+rebuilt when their source or any header changed.  Beside it, g++ compiles
+csrc/fast_binding.cpp against torch's headers into _fw_fast.so, the Python
+entry points of the operators whose calls take a few microseconds.
 """
 from __future__ import annotations
 
@@ -17,6 +19,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfw_attn.so")
+FAST_SRC = os.path.join(CSRC, "fast_binding.cpp")
+FAST = os.path.join(HERE, "_fw_fast.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
               "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]
@@ -35,6 +39,23 @@ def _newest_header() -> float:
     return max((os.path.getmtime(h) for h in hdrs), default=0.0)
 
 
+def _fast_command(out: str) -> list:
+    """g++ command of the Python module: torch's and Python's headers and torch's
+    libraries, at the versions of the running interpreter."""
+    import sysconfig
+
+    import torch
+    cuda_home = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    torch_dir = os.path.dirname(torch.__file__)
+    incs = [os.path.join(torch_dir, "include"), os.path.join(cuda_home, "include"), sysconfig.get_paths()["include"],
+            os.path.join(ROOT, "include")]
+    libdir = os.path.join(torch_dir, "lib")
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", FAST_SRC, "-o", out,
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            *(f"-isystem{i}" for i in incs), f"-L{libdir}", f"-Wl,-rpath,{libdir}", "-lc10", "-lc10_cuda",
+            "-ltorch_cpu", "-ltorch_python"]
+
+
 def build(verbose: bool = False, force: bool = False, extra_flags=()) -> str:
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
@@ -42,6 +63,14 @@ def build(verbose: bool = False, force: bool = False, extra_flags=()) -> str:
     hdr_time = _newest_header()
     procs = []
     objects = []
+    fast_stale = force or not os.path.exists(FAST) or os.path.getmtime(FAST) < max(
+        os.path.getmtime(FAST_SRC), os.path.getmtime(os.path.join(ROOT, "include", "fw_attn.h")))
+    fast_tmp = FAST + f".tmp{os.getpid()}"
+    if fast_stale:
+        fast_cmd = _fast_command(fast_tmp)
+        if verbose:
+            print(" ".join(fast_cmd), flush=True)
+        fast_proc = subprocess.Popen(fast_cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
     for src in sources:
         obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
         objects.append(obj)
@@ -63,9 +92,15 @@ def build(verbose: bool = False, force: bool = False, extra_flags=()) -> str:
             os.replace(obj + ".tmp", obj)
             if verbose and text.strip():
                 print(text, flush=True)
+    if fast_stale:
+        out, _ = fast_proc.communicate()
+        if fast_proc.returncode != 0:
+            failed.append((FAST, out.decode(errors="replace")))
+        else:
+            os.replace(fast_tmp, FAST)
     if failed:
         msg = "\n".join(f"--- {o}\n{t}" for o, t in failed)
-        raise RuntimeError(f"nvcc failed:\n{msg}")
+        raise RuntimeError(f"compilation failed:\n{msg}")
     if procs or not os.path.exists(LIB) or any(os.path.getmtime(o) > os.path.getmtime(LIB) for o in objects):
         tmp = LIB + f".tmp{os.getpid()}"
         cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objects, "-cudart", "static"]
