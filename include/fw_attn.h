@@ -431,7 +431,7 @@ fw_status_t fw_tree_mask(const fw_tensor_t *parents, const fw_tensor_t *draft_le
  * places, a page whose slots pass 2^31, a ring outside its array) record
  * FW_ERR_INVALID_ARG: such a request keeps its row and gets slots -1, tokens
  * without a place are dropped, pages the ring cannot take stay held, and a bad
- * range serves nobody.  B <= 16384.  One launch, two when held_out or range_out
+ * range serves nobody.  B <= 8192.  One launch, two when held_out or range_out
  * overlap their inputs.  No workspace.
  */
 fw_status_t fw_build_page_tables(const fw_tensor_t *seq_lens, const fw_tensor_t *new_lens, const fw_tensor_t *held,

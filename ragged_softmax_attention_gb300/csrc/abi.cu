@@ -1244,7 +1244,8 @@ fw_status_t fw_build_page_tables(const fw_tensor_t *seq_lens, const fw_tensor_t 
     if (page_size < 1 || page_size > (1 << 20)) return fail(FW_ERR_INVALID_ARG, "page size must be 1 to 2^20");
     const int64_t F = free_queue->shape[0];
     const int64_t N = padded ? B * slot_mapping->shape[1] : slot_mapping->shape[0];
-    if (B > 16384) return fail(FW_ERR_UNSUPPORTED, "page tables of up to 16384 requests, not %lld", (long long)B);
+    if (B > fw::kMaxTableRows)
+        return fail(FW_ERR_UNSUPPORTED, "page tables of up to %d requests, not %lld", fw::kMaxTableRows, (long long)B);
     if (F < 1 || F > (1LL << 30)) return fail(FW_ERR_UNSUPPORTED, "a ring of 1 to 2^30 pages");
     if (N >= (1LL << 31) || max_pages > (1LL << 30)) return fail(FW_ERR_UNSUPPORTED, "too many places or table columns");
     const fw_tensor_t *outs[] = {block_table, slot_mapping, cu_new, held_out, range_out, free_queue};
@@ -1266,6 +1267,9 @@ fw_status_t fw_build_page_tables(const fw_tensor_t *seq_lens, const fw_tensor_t 
     p.L = padded ? (int)slot_mapping->shape[1] : 0;
     p.N = (int)N;
     p.padded = padded ? 1 : 0;
+    p.ps_shift = -1;
+    for (int i = 0; i <= 20; ++i)
+        if (page_size == (1 << i)) p.ps_shift = i;
     p.seq_lens = static_cast<const int32_t *>(seq_lens->data);
     p.new_lens = static_cast<const int32_t *>(new_lens->data);
     p.held = static_cast<const int32_t *>(held->data);
@@ -1359,6 +1363,7 @@ fw_status_t fw_kv_commit(const fw_tensor_t *path, const fw_tensor_t *path_lens, 
     std::lock_guard<std::mutex> lk(g_mu);
     DeviceState *d = nullptr;
     if (fw_status_t s = device_state(&d)) return s;
+    p.num_sms = d->num_sms;
     p.status = d->status;
     cudaError_t e = fw::launch_kv_commit(p, stream);
     if (e != cudaSuccess) return fail(FW_ERR_CUDA, "commit launch: %s", cudaGetErrorString(e));

@@ -46,6 +46,7 @@ constexpr int kDecodePieceCostBf16 = 4;
 constexpr int kDecodePieceCostFp8 = 5;
 constexpr int kTreeMinSpan = 2;       // tree decode: fewest KV tiles (and empty slots) one CTA range holds
 constexpr int kTreePieceCost = 3;     // tree decode: empty slots before a unit's tiles
+constexpr int kMaxTableRows = 8192;   // page tables: requests whose sums fit a block's shared memory
 constexpr int kLatentRows = 64;       // latent-head decode: query heads per CTA (MMA N of one CTA)
 constexpr int kLatentPairRows = 128;  // latent-head decode on CTA pairs: query heads per pair
 
@@ -186,6 +187,7 @@ struct TreeMaskParams {
 // One fw_build_page_tables call.
 struct PageTableParams {
     int B, max_pages, F, ps;
+    int ps_shift;                              // log2 of ps, -1: not a power of two
     int padded, L;                             // 1: L places per request; 0: packed
     int N;                                     // places in all
     const int32_t *seq_lens, *new_lens, *held;
@@ -209,6 +211,7 @@ struct CommitParams {
     void *k_cache, *v_cache;
     int64_t kc_stride[3], vc_stride[3];        // bytes (page, slot, head)
     int32_t *new_lens;
+    int num_sms;
     int *status;
 };
 

@@ -130,7 +130,7 @@ def run_tables(fw, x, status=None, in_place=False):
 
 @pytest.mark.parametrize("in_place", [False, True])
 @pytest.mark.parametrize("B,ps,L", [(1, 16, 1), (1, 16, 0), (5, 8, 3), (33, 16, 8), (64, 128, 0), (64, 1, 0), (257, 24, 5),
-                                    (1025, 16, 0), (3000, 16, 4), (16384, 16, 1), (2048, 7, 0)])
+                                    (1025, 16, 0), (3000, 16, 4), (8192, 16, 1), (2048, 7, 0), (4000, 2, 100), (3000, 16, 96)])
 def test_tables_equal_the_definition(fw, B, ps, L, in_place):
     run_tables(fw, table_case(B, ps, L, seed=B + ps + L), in_place=in_place)
 
