@@ -242,17 +242,18 @@ __device__ __forceinline__ uint32_t seen_keys(const TreeParams &p, const TreeUni
 }
 
 // This thread's row of a finished piece: its output and LSE, or its partial.
-// `load` reads 32 columns of O (warp-collective).
+// `load` reads 32 columns of O (warp-collective); columns 32 c0 .. 32 c1.
 template <int D, int NT, typename Load>
 __device__ __forceinline__ void write_row(const TreeParams &p, const TreeUnit &u, int x, int row, bool live, int t,
-                                          int h, float base2, float l_sum, Load load) {
+                                          int h, float base2, float l_sum, Load load, int c0 = 0,
+                                          int c1 = D / 32) {
     const float inv = l_sum > 0.f ? p.out_scale / l_sum : 0.f;
     __nv_bfloat16 *orow = reinterpret_cast<__nv_bfloat16 *>(p.out) + u.b * p.out_stride[0] + t * p.out_stride[1] +
                           h * p.out_stride[2];
     const int64_t prow = (int64_t)u.part * (NT * 128) + x * 128 + row;
     float4 *part = reinterpret_cast<float4 *>(p.part_o + prow * D);
 #pragma unroll 1
-    for (int c = 0; c < D / 32; ++c) {
+    for (int c = c0; c < c1; ++c) {
         float o[32];
         load(c, o);
         if (!live) continue;
@@ -272,7 +273,7 @@ __device__ __forceinline__ void write_row(const TreeParams &p, const TreeUnit &u
                 part[c * 8 + w] = make_float4(o[4 * w], o[4 * w + 1], o[4 * w + 2], o[4 * w + 3]);
         }
     }
-    if (!live) return;
+    if (!live || c0 > 0) return;
     if (u.part >= 0) p.part_ml[prow] = make_float2(base2, l_sum);
     else if (p.lse)
         p.lse[u.b * p.lse_stride[0] + t * p.lse_stride[1] + h * p.lse_stride[2]] =

@@ -20,8 +20,10 @@
 // The same warps split the queries, ahead of the softmax, and write zeros for
 // the values of keys nobody sees.
 //
-// Warp roles: 0 copies, 1 (and 2) issues MMAs, 3 writes the rows that see
-// nothing, 4-7 convert, 8.. softmax.
+// Warp roles: 0 copies, 1 and 2 issue MMAs, 3 writes the rows that see
+// nothing, 4-7 convert, 8-15 softmax (a warpgroup per stream, or two for one:
+// a tile's softmax takes some 2,000 cycles of a warpgroup, more than the tile's
+// share of HBM).
 #include <cuda_fp16.h>
 
 #include "tree_common.cuh"
@@ -42,12 +44,13 @@ constexpr uint32_t kIdescPV = (1u << 4) | (1u << 16) | ((128u >> 3) << 17) | ((1
 template <int NT_>
 struct F8TreeCfg {
     static constexpr int NT = NT_;
-    static constexpr int kSB = NT == 2 ? 1 : 2;
+    static constexpr int kSB = NT == 2 ? 1 : 3;                 // S buffers of a stream
+    static constexpr int kWG = 2;                               // softmax warpgroups, NT = 1: every other tile each
     static constexpr int kQBytes = 128 * D * 2;                 // BF16 rows, then their two E4M3 terms in place
     static constexpr int kKBytes = 128 * D;
     static constexpr int kVBytes = 128 * D * 2;                 // FP16 values; E4M3 lands in the second half
     static constexpr int kHalf = 128 * 128;
-    static constexpr int kKSlots = 4;
+    static constexpr int kKSlots = NT == 2 ? 4 : 3;
     static constexpr int kVSlots = NT == 2 ? 3 : 4;
     static constexpr int kOffQ = 0;
     static constexpr int kOffK = kOffQ + NT * kQBytes;
@@ -67,8 +70,10 @@ struct F8TreeCfg {
     static constexpr int kBarPFull = kBarPHalf + NT * kSB;
     static constexpr int kBarPvDone = kBarPFull + NT * kSB;
     static constexpr int kBarIssued = kBarPvDone + NT * kSB;    // [NT]
-    static constexpr int kBarDrain = kBarIssued + NT;           // [NT]
-    static constexpr int kBarSchedFull = kBarDrain + NT;
+    static constexpr int kBarDrain = kBarIssued + NT;           // [2]
+    static constexpr int kBarBase = kBarDrain + 2;              // [2] base of the rows after a tile (NT = 1)
+    static constexpr int kBarOFree = kBarBase + 2;              // O read by both warpgroups (NT = 1)
+    static constexpr int kBarSchedFull = kBarOFree + 1;
     static constexpr int kBarSchedEmpty = kBarSchedFull + kSched;
     static constexpr int kNumBars = kBarSchedEmpty + kSched;
     static constexpr int kOffSched = (kOffBar + kNumBars * 8 + 63) / 64 * 64;
@@ -76,22 +81,19 @@ struct F8TreeCfg {
     static constexpr int kOffPlan = kOffSeen + 128;
     static constexpr int kOffScan = kOffPlan + 32;              // [16]
     static constexpr int kOffQScale = kOffScan + 128;           // [kSched][NT][128 halves]: exponents of the rows
-    static constexpr int kOffMisc = kOffQScale + kSched * NT * 128;
+    static constexpr int kOffBase = kOffQScale + kSched * NT * 128;   // NT = 1: [2][128] bases, [2][2][128] row sums
+    static constexpr int kOffMisc = kOffBase + (NT == 1 ? 3072 : 0);
     static constexpr int kSmemBytes = kOffMisc + 16 + 1024;
     static_assert(kSmemBytes <= 232448, "shared memory budget of one CTA exceeded");
-    static constexpr int kThreads = 256 + NT * 128;
-    static constexpr int kSchedReaders = NT + 4 + 4 * NT;
-    // Launched at 168 (NT = 1: 384 threads) or 128 (NT = 2: 512) registers a
-    // thread: 128 x 80 + 128 x 112 + 128 x 208 = 51200 <= 64512 and
-    // 128 x 72 + 128 x 96 + 256 x 168 = 64512 <= 65536.
-    static constexpr uint32_t kRegsControl = NT == 2 ? 72 : 80;
-    static constexpr uint32_t kRegsConvert = NT == 2 ? 96 : 112;
-    static constexpr uint32_t kRegsSoftmax = NT == 2 ? 168 : 208;
-    static constexpr uint32_t kRegsLaunch = NT == 2 ? 128 : 168;
-    static_assert(128 * kRegsControl + 128 * kRegsConvert + NT * 128 * kRegsSoftmax <= kThreads * kRegsLaunch,
+    static constexpr int kThreads = 256 + kWG * 128;
+    static constexpr int kSchedReaders = 2 + 4 + 4 * kWG;
+    // 512 threads launched at 128 registers: 128 x 72 + 128 x 96 + 256 x 168 =
+    // 64512 <= 65536.
+    static constexpr uint32_t kRegsControl = 72, kRegsConvert = 96, kRegsSoftmax = 168, kRegsLaunch = 128;
+    static_assert(128 * kRegsControl + 128 * kRegsConvert + kWG * 128 * kRegsSoftmax <= kThreads * kRegsLaunch,
                   "register split");
     __device__ static constexpr uint32_t s_col(int x, int buf) { return (uint32_t)(x * kSB + buf) * 128u; }
-    __device__ static constexpr uint32_t o_col(int x) { return 256u + (uint32_t)x * 128u; }
+    __device__ static constexpr uint32_t o_col(int x) { return (uint32_t)(NT * kSB + x) * 128u; }
 };
 
 // Four E4M3 values (one word) as four FP16 values / 256, two words: the sign
@@ -151,12 +153,16 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
     uint64_t *pv_done = bars + C::kBarPvDone;
     uint64_t *issued = bars + C::kBarIssued;
     uint64_t *drain = bars + C::kBarDrain;
+    uint64_t *base_set = bars + C::kBarBase;
+    uint64_t *o_free = bars + C::kBarOFree;
     uint64_t *sched_full = bars + C::kBarSchedFull;
     uint64_t *sched_empty = bars + C::kBarSchedEmpty;
     TreeUnit *sched = reinterpret_cast<TreeUnit *>(smem + C::kOffSched);
     uint32_t *seen_words = reinterpret_cast<uint32_t *>(smem + C::kOffSeen);
     long long *plan = reinterpret_cast<long long *>(smem + C::kOffPlan);
     long long *scan = reinterpret_cast<long long *>(smem + C::kOffScan);
+    float *bases = reinterpret_cast<float *>(smem + C::kOffBase);      // [2][128], NT = 1
+    float *sums = bases + 256;                                         // [2][2][128], NT = 1
     int8_t *q_exp = reinterpret_cast<int8_t *>(smem + C::kOffQScale);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::kOffMisc + 4);
@@ -172,7 +178,9 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
         for (int i = 0; i < NT * kSB; ++i) {
             mbar_init(&s_full[i], 1); mbar_init(&p_half[i], 4); mbar_init(&p_full[i], 4); mbar_init(&pv_done[i], 1);
         }
-        for (int i = 0; i < NT; ++i) { mbar_init(&issued[i], 1); mbar_init(&drain[i], 1); }
+        for (int i = 0; i < NT; ++i) mbar_init(&issued[i], 1);
+        for (int i = 0; i < 2; ++i) { mbar_init(&drain[i], 1); mbar_init(&base_set[i], 4); }
+        mbar_init(o_free, 4 * C::kWG);
         for (int i = 0; i < C::kSched; ++i) {
             mbar_init(&q_ready[i], 4); mbar_init(&sched_full[i], 1); mbar_init(&sched_empty[i], C::kSchedReaders);
         }
@@ -260,7 +268,9 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
             int pages[kSB + 3];
 #pragma unroll
             for (int i = 0; i < kSB + 3; ++i) pages[i] = tile_page(i);
-            for (int j = 0; j < kSB && j < u.ntiles && ok; ++j) ok = copy_tile(j, j == 0 ? pages[0] : pages[kSB - 1], false);
+#pragma unroll
+            for (int j = 0; j < kSB; ++j)
+                if (j < u.ntiles && ok) ok = copy_tile(j, pages[j], false);
             for (int j = 0; j < u.ntiles && ok; ++j) {
                 ok = copy_tile(j, pages[0], true);
                 if (ok && j + kSB < u.ntiles) ok = copy_tile(j + kSB, pages[kSB], false);
@@ -277,10 +287,10 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
                 mbar_wait_drain(&v_raw[(iv - 1 - i) % C::kVSlots], ((iv - 1 - i) / C::kVSlots) & 1, wc);
         }
         __syncwarp();
-      } else if (warp <= NT) {
+      } else if (warp < 3) {
         // ----------------------------------------------------------------- MMA
         if (lane == 0) {
-            const int x = warp - 1;
+            const int x = NT == 2 ? warp - 1 : 0;
             uint32_t tiles = 0;                           // K (and V) tiles of earlier pieces
             uint32_t steps = 0;                           // this stream's among them
             uint32_t turns = 0;                           // those both streams took part in
@@ -312,77 +322,114 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
                 }
             };
             bool ok = true;
-            for (int k = 0; ok; ++k) {
-                const TreeUnit *ur = wait_unit(k);
-                const bool got = ur && ur->b >= 0;
-                const int n = got ? ur->ntiles : 0;
-                const int nrt = got ? ur->nrt : 0;
-                free_unit(k);
-                if (!got) break;
-                const uint32_t i0 = tiles;
-                tiles += (uint32_t)n;
-                if (!mbar_wait(&q_ready[k % C::kSched], (k / C::kSched) & 1, wc)) break;
-                if (x >= nrt) {
-                    // No row tile for this stream: it still sees every tile come and
-                    // hands every slot back, so that its phases stay in step.
-                    mbar_arrive(q_empty);
-                    for (uint32_t i = i0; i < tiles && ok; ++i) {
-                        ok = wait_k(i);
-                        if (ok) mbar_arrive(&k_empty[i % C::kKSlots]);
-                        ok = ok && wait_v(i);
-                        if (ok) mbar_arrive(&v_empty[i % C::kVSlots]);
-                    }
-                    continue;
-                }
-                tc_fence_after();
-                for (int j = 0; j < kSB && j < n && ok; ++j) {
-                    ok = wait_k(i0 + j);
-                    if (!ok) break;
-                    tc_fence_after();
-                    push_qk(i0 + j, (steps + j) % kSB);
-                    mma_commit(&s_full[x * kSB + (steps + j) % kSB]);
-                    mma_commit(&k_empty[(i0 + j) % C::kKSlots]);
-                    if (j == n - 1) mma_commit(q_empty);
-                }
-                for (int j = 0; j < n && ok; ++j) {
-                    const uint32_t st = steps + j;
-                    const int buf = st % kSB;
-                    const uint32_t ph = (st / kSB) & 1;
-                    const uint32_t iv = i0 + j, ik = i0 + j + kSB;
-                    if (NT == 2 && nrt == 2) {
-                        // Turns, as in the BF16 kernel.
-                        const uint32_t dep = turns + j + x;
-                        if (dep > 0 && !mbar_wait(&issued[1 - x], (dep - 1) & 1, wc)) { ok = false; break; }
-                    }
-                    if (!wait_v(iv) || !mbar_wait(&p_half[x * kSB + buf], ph, wc)) { ok = false; break; }
-                    const bool next = j + kSB < n;
-                    const bool paired = next && k_there(ik);
-                    tc_fence_after();
-                    push_pv_half(iv, buf, 0, j == 0);
-                    if (!mbar_wait(&p_full[x * kSB + buf], ph, wc)) { ok = false; break; }
-                    tc_fence_after();
-                    push_pv_half(iv, buf, 1, false);
-                    if (NT == 2 && nrt == 2) mbar_arrive(&issued[x]);
-                    if (paired) push_qk(ik, buf);
-                    if (kSB == 2 || j == n - 1) mma_commit(&pv_done[x * kSB + buf]);
-                    mma_commit(&v_empty[iv % C::kVSlots]);
-                    if (next) {
-                        if (!paired) {
-                            if (!wait_k(ik)) { ok = false; break; }
+            if constexpr (NT == 1) {
+                // QK and PV from a thread each, as in the BF16 kernel.
+                for (int k = 0; ok; ++k) {
+                    const TreeUnit *ur = wait_unit(k);
+                    const bool got = ur && ur->b >= 0;
+                    const int n = got ? ur->ntiles : 0;
+                    free_unit(k);
+                    if (!got) break;
+                    if (warp == 2) ok = mbar_wait(&q_ready[k % C::kSched], (k / C::kSched) & 1, wc);
+                    else if (k > 0) ok = mbar_wait(o_free, (k - 1) & 1, wc);   // the last piece's O is read
+                    for (int j = 0; j < n && ok; ++j, ++steps) {
+                        const int buf = steps % kSB;
+                        const uint32_t ph = (steps / kSB) & 1;
+                        if (warp == 2) {
+                            ok = wait_k(steps) && (steps < kSB || mbar_wait(&pv_done[buf], ph ^ 1, wc));
+                            if (!ok) break;
                             tc_fence_after();
-                            push_qk(ik, buf);
+                            push_qk(steps, buf);
+                            mma_commit(&s_full[buf]);
+                            mma_commit(&k_empty[steps % C::kKSlots]);
+                            if (j == n - 1) mma_commit(q_empty);
+                        } else {
+                            ok = wait_v(steps) && mbar_wait(&p_half[buf], ph, wc);
+                            if (!ok) break;
+                            tc_fence_after();
+                            push_pv_half(steps, buf, 0, j == 0);
+                            ok = mbar_wait(&p_full[buf], ph, wc);
+                            if (!ok) break;
+                            tc_fence_after();
+                            push_pv_half(steps, buf, 1, false);
+                            mma_commit(&pv_done[buf]);
+                            mma_commit(&v_empty[steps % C::kVSlots]);
                         }
-                        mma_commit(&s_full[x * kSB + buf]);
-                        mma_commit(&k_empty[ik % C::kKSlots]);
-                        if (j + kSB == n - 1) mma_commit(q_empty);
                     }
                 }
-                if (!ok) break;
-                steps += n;
-                if (nrt == 2) turns += n;
+            } else {
+                for (int k = 0; ok; ++k) {
+                    const TreeUnit *ur = wait_unit(k);
+                    const bool got = ur && ur->b >= 0;
+                    const int n = got ? ur->ntiles : 0;
+                    const int nrt = got ? ur->nrt : 0;
+                    free_unit(k);
+                    if (!got) break;
+                    const uint32_t i0 = tiles;
+                    tiles += (uint32_t)n;
+                    if (!mbar_wait(&q_ready[k % C::kSched], (k / C::kSched) & 1, wc)) break;
+                    if (x >= nrt) {
+                        // No row tile for this stream: it still sees every tile come and
+                        // hands every slot back, so that its phases stay in step.
+                        mbar_arrive(q_empty);
+                        for (uint32_t i = i0; i < tiles && ok; ++i) {
+                            ok = wait_k(i);
+                            if (ok) mbar_arrive(&k_empty[i % C::kKSlots]);
+                            ok = ok && wait_v(i);
+                            if (ok) mbar_arrive(&v_empty[i % C::kVSlots]);
+                        }
+                        continue;
+                    }
+                    tc_fence_after();
+                    for (int j = 0; j < kSB && j < n && ok; ++j) {
+                        ok = wait_k(i0 + j);
+                        if (!ok) break;
+                        tc_fence_after();
+                        push_qk(i0 + j, (steps + j) % kSB);
+                        mma_commit(&s_full[x * kSB + (steps + j) % kSB]);
+                        mma_commit(&k_empty[(i0 + j) % C::kKSlots]);
+                        if (j == n - 1) mma_commit(q_empty);
+                    }
+                    for (int j = 0; j < n && ok; ++j) {
+                        const uint32_t st = steps + j;
+                        const int buf = st % kSB;
+                        const uint32_t ph = (st / kSB) & 1;
+                        const uint32_t iv = i0 + j, ik = i0 + j + kSB;
+                        if (nrt == 2) {
+                            // Turns, as in the BF16 kernel.
+                            const uint32_t dep = turns + j + x;
+                            if (dep > 0 && !mbar_wait(&issued[1 - x], (dep - 1) & 1, wc)) { ok = false; break; }
+                        }
+                        if (!wait_v(iv) || !mbar_wait(&p_half[x * kSB + buf], ph, wc)) { ok = false; break; }
+                        const bool next = j + kSB < n;
+                        const bool paired = next && k_there(ik);
+                        tc_fence_after();
+                        push_pv_half(iv, buf, 0, j == 0);
+                        if (!mbar_wait(&p_full[x * kSB + buf], ph, wc)) { ok = false; break; }
+                        tc_fence_after();
+                        push_pv_half(iv, buf, 1, false);
+                        if (nrt == 2) mbar_arrive(&issued[x]);
+                        if (paired) push_qk(ik, buf);
+                        if (j == n - 1) mma_commit(&pv_done[x]);
+                        mma_commit(&v_empty[iv % C::kVSlots]);
+                        if (next) {
+                            if (!paired) {
+                                if (!wait_k(ik)) { ok = false; break; }
+                                tc_fence_after();
+                                push_qk(ik, buf);
+                            }
+                            mma_commit(&s_full[x * kSB + buf]);
+                            mma_commit(&k_empty[ik % C::kKSlots]);
+                            if (j + kSB == n - 1) mma_commit(q_empty);
+                        }
+                    }
+                    if (!ok) break;
+                    steps += n;
+                    if (nrt == 2) turns += n;
+                }
             }
-            mma_commit(&drain[x]);
-            mbar_wait_drain(&drain[x], 0, wc);
+            mma_commit(&drain[warp - 1]);
+            mbar_wait_drain(&drain[warp - 1], 0, wc);
         }
         __syncwarp();
       } else if (warp == 3) {
@@ -512,7 +559,11 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
     } else {
         setmaxnreg_inc<C::kRegsSoftmax>();
         // ------------------------------------------------- softmax / epilogue
-        const int x = (warp - 8) >> 2;
+        // One stream: the two warpgroups take every other key tile.  A row's base
+        // passes from tile to tile through shared memory, each keeps the sum of its
+        // own tiles, and both write half of the outputs.
+        const int wg = (warp - 8) >> 2;
+        const int x = NT == 2 ? wg : 0;
         const int q4 = warp & 3;
         const int row = q4 * 32 + lane;
         const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
@@ -536,17 +587,26 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
             const bool warp_live = __any_sync(0xffffffffu, live);
             const int base = u.n - u.d;
             const int32_t *mrow = p.mask + u.b * p.mask_stride[0] + (live ? t : 0) * p.mask_stride[1];
-            float m_ref = kNegInf, l_sum = 0.f;
-            for (int j = 0; j < u.ntiles; ++j, ++steps) {
-                const int buf = steps % kSB;
+            float m_ref = kNegInf, l_sum = 0.f;           // l_sum relative to m_ref
+            constexpr int kEvery = NT == 2 ? 1 : C::kWG;
+            for (int j = NT == 2 ? 0 : (int)((steps ^ (uint32_t)wg) & 1); j < u.ntiles; j += kEvery) {
+                const uint32_t st = steps + j;
+                const int buf = st % kSB;
                 const int key0 = (u.tile0 + j) * kKvTile;
                 const bool drafts = key0 + kKvTile > base;
-                mbar_wait(&s_full[x * kSB + buf], (steps / kSB) & 1, wc);
+                mbar_wait(&s_full[x * kSB + buf], (st / kSB) & 1, wc);
                 tc_fence_after();
                 if (!warp_live) {                         // rows of padding: whatever lies there
+                    // The last tile's base is waited for all the same: this warp must not
+                    // stand in for one of the next phase's arrivals.
+                    if (NT == 1 && j > 0) mbar_wait(&base_set[(st - 1) & 1], ((st - 1) >> 1) & 1, wc);
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) { mbar_arrive(&p_half[x * kSB + buf]); mbar_arrive(&p_full[x * kSB + buf]); }
+                    if (lane == 0) {
+                        if (NT == 1) mbar_arrive(&base_set[st & 1]);
+                        mbar_arrive(&p_half[x * kSB + buf]);
+                        mbar_arrive(&p_full[x * kSB + buf]);
+                    }
                     continue;
                 }
                 const uint32_t sa = tmem + lane_off + C::s_col(x, buf);
@@ -572,31 +632,44 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
                     ext = fmaxf(ext, fmaxf(fmaxf(e4[0], e4[1]), fmaxf(e4[2], e4[3])));
                 }
                 const float m_tile = ext == kNegInf || !live ? kNegInf : ext * rs;
-                const bool up = m_tile > m_ref + kRescaleSlack;
-                if (__any_sync(0xffffffffu, up)) {
-                    float alpha = 1.f;
-                    if (up) {
-                        alpha = ex2_approx(m_ref - m_tile);
-                        l_sum *= alpha;
-                        m_ref = m_tile;
+                float m_prev = m_ref;                     // the rows' base so far
+                if constexpr (NT == 1) {
+                    if (j == 0) {
+                        m_prev = kNegInf;
+                    } else {
+                        mbar_wait(&base_set[(st - 1) & 1], ((st - 1) >> 1) & 1, wc);
+                        m_prev = bases[((st - 1) & 1) * 128 + row];
                     }
-                    if (j > 0) {
-                        if constexpr (kSB == 2) {
-                            wait_pv(steps - 1);
-                            tc_fence_after();
-                        }
+                }
+                const bool up = m_tile > m_prev + kRescaleSlack;
+                const float m_new = up ? m_tile : m_prev;
+                if (__any_sync(0xffffffffu, up) && j > 0) {
+                    const float alpha = up ? ex2_approx(m_prev - m_new) : 1.f;
+                    if constexpr (kSB > 1) {
+                        wait_pv(st - 1);
+                        tc_fence_after();
+                    }
 #pragma unroll 1
-                        for (int c = 0; c < D / 32; ++c) {
-                            float o[32];
-                            const uint32_t oa = tmem + lane_off + C::o_col(x) + c * 32;
-                            tmem_ld32(oa, o);
-                            tmem_wait_ld();
+                    for (int c = 0; c < D / 32; ++c) {
+                        float o[32];
+                        const uint32_t oa = tmem + lane_off + C::o_col(x) + c * 32;
+                        tmem_ld32(oa, o);
+                        tmem_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] *= alpha;
-                            tmem_st32(oa, o);
-                        }
-                        tmem_wait_st();
+                        for (int i = 0; i < 32; ++i) o[i] *= alpha;
+                        tmem_st32(oa, o);
                     }
+                    tmem_wait_st();
+                }
+                if constexpr (NT == 1) {
+                    bases[(st & 1) * 128 + row] = m_new;
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&base_set[st & 1]);
+                }
+                if (m_new != m_ref) {
+                    l_sum *= ex2_approx(m_ref - m_new);
+                    m_ref = m_new;
                 }
                 // P = 2^(s * rs - m_ref + 7), rounded to FP16; the row sum takes it
                 // unrounded.
@@ -631,9 +704,22 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
             }
             // ------------------------------------------------------ epilogue
             ++pieces;
-            if constexpr (kSB == 2) {
-                if (steps >= 2) wait_pv(steps - 2);
-                wait_pv(steps - 1);
+            steps += u.ntiles;
+            if constexpr (NT == 1) {
+                const uint32_t last = steps - 1;
+                float *sum = sums + (k & 1) * 256;
+                if (warp_live) {
+                    mbar_wait(&base_set[last & 1], (last >> 1) & 1, wc);
+                    const float m_end = bases[(last & 1) * 128 + row];
+                    if (m_end != m_ref) l_sum *= ex2_approx(m_ref - m_end);
+                    m_ref = m_end;
+                    sum[wg * 128 + row] = l_sum;
+                }
+                named_bar_sync(4, 128 * C::kWG);
+                l_sum = sum[row] + sum[128 + row];
+#pragma unroll
+                for (int i = kSB; i >= 1; --i)
+                    if (steps >= (uint32_t)i) wait_pv(steps - i);
             } else {
                 mbar_wait(&pv_done[x], (pieces - 1) & 1, wc);
             }
@@ -642,7 +728,12 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
                 write_row<D, NT>(p, u, x, row, live, t, h, m_ref - kPShift, l_sum, [&](int c, float (&o)[32]) {
                     tmem_ld32(tmem + lane_off + C::o_col(x) + c * 32, o);
                     tmem_wait_ld();
-                });
+                }, NT == 1 ? 2 * wg : 0, NT == 1 ? 2 * wg + 2 : D / 32);
+            if constexpr (NT == 1) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(o_free);
+            }
             tc_fence_before();
         }
     }

@@ -26,7 +26,8 @@
 // softmax of this one (NT = 1).
 //
 // Warp roles: warp 0 copies (Q, then K and V tiles through a ring of 32 KiB
-// slots in the order the MMAs take them), warp 1 (and 2) issues the MMAs,
+// slots in the order the MMAs take them), warps 1 and 2 issue the MMAs (of a
+// stream each, or of QK and PV),
 // warp 3 writes the rows that see nothing, warps 4.. run the softmax.
 #include "tree_common.cuh"
 
@@ -38,7 +39,8 @@ using namespace tree;
 template <int D_, int NT_>
 struct TreeCfg {
     static constexpr int D = D_, NT = NT_;
-    static constexpr int kSB = NT == 2 ? 1 : 2;                 // S buffers of a stream = key tiles QK runs ahead
+    // S buffers of a stream, i.e. key tiles QK runs ahead: what O leaves of TMEM.
+    static constexpr int kSB = NT == 2 ? 1 : D == 128 ? 3 : 2;
     static constexpr int kTileSlots = D / 128;                  // ring slots of one K or V tile
     static constexpr int kChunkBytes = 128 * 128;               // 128 rows x 64 bf16 columns
     static constexpr int kSlotBytes = 2 * kChunkBytes;          // 128 rows x 128 columns
@@ -57,8 +59,8 @@ struct TreeCfg {
     static constexpr int kBarPFull = kBarPHalf + NT * kSB;      // [NT][kSB]
     static constexpr int kBarPvDone = kBarPFull + NT * kSB;     // [NT][kSB]
     static constexpr int kBarIssued = kBarPvDone + NT * kSB;    // [NT]
-    static constexpr int kBarDrain = kBarIssued + NT;           // [NT]
-    static constexpr int kBarSchedFull = kBarDrain + NT;
+    static constexpr int kBarDrain = kBarIssued + NT;           // [2]
+    static constexpr int kBarSchedFull = kBarDrain + 2;
     static constexpr int kBarSchedEmpty = kBarSchedFull + kSched;
     static constexpr int kNumBars = kBarSchedEmpty + kSched;
     static constexpr int kOffSched = (kOffBar + kNumBars * 8 + 63) / 64 * 64;
@@ -69,14 +71,14 @@ struct TreeCfg {
     static constexpr int kSmemBytes = kOffMisc + 16 + 1024;
     static_assert(kSmemBytes <= 232448, "shared memory budget of one CTA exceeded");
     static constexpr int kThreads = 128 + NT * 128;
-    static constexpr int kSchedReaders = NT + 4 * NT;           // issuers and softmax warps
+    static constexpr int kSchedReaders = 2 + 4 * NT;            // issuers and softmax warps
     // NT = 2: 384 threads launched at 168 registers; 128 x 80 + 256 x 208 = 63488 <= 64512.
     static constexpr uint32_t kRegsControl = 80, kRegsSoftmax = 208;
     static_assert(NT == 1 || 128 * kRegsControl + 256 * kRegsSoftmax <= 384 * 168, "register split");
     static constexpr uint32_t kIdescQK = idesc_bf16_f32(128, kKvTile, false, false);
     static constexpr uint32_t kIdescPV = idesc_bf16_f32(128, 128, false, true);
     __device__ static constexpr uint32_t s_col(int x, int buf) { return (uint32_t)(x * kSB + buf) * 128u; }
-    __device__ static constexpr uint32_t o_col(int x) { return 256u + (uint32_t)x * 128u; }
+    __device__ static constexpr uint32_t o_col(int x) { return (uint32_t)(NT * kSB + x) * 128u; }
 };
 
 template <int D, int NT>
@@ -119,7 +121,8 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
         for (int i = 0; i < NT * kSB; ++i) {
             mbar_init(&s_full[i], 1); mbar_init(&p_half[i], 4); mbar_init(&p_full[i], 4); mbar_init(&pv_done[i], 1);
         }
-        for (int i = 0; i < NT; ++i) { mbar_init(&issued[i], 1); mbar_init(&drain[i], 1); }
+        for (int i = 0; i < NT; ++i) mbar_init(&issued[i], 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&drain[i], 1);
         for (int i = 0; i < C::kSched; ++i) { mbar_init(&sched_full[i], 1); mbar_init(&sched_empty[i], C::kSchedReaders); }
         *abort_flag = 0;
         fence_barrier_init();
@@ -215,7 +218,9 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
             int pages[kSB + 2];
 #pragma unroll
             for (int i = 0; i < kSB + 2; ++i) pages[i] = tile_page(i);
-            for (int j = 0; j < kSB && j < u.ntiles && ok; ++j) ok = copy_tile(j, j == 0 ? pages[0] : pages[kSB - 1], false);
+#pragma unroll
+            for (int j = 0; j < kSB; ++j)
+                if (j < u.ntiles && ok) ok = copy_tile(j, pages[j], false);
             for (int j = 0; j < u.ntiles && ok; ++j) {
                 ok = copy_tile(j, pages[0], true);
                 if (ok && j + kSB < u.ntiles) ok = copy_tile(j + kSB, pages[kSB], false);
@@ -233,10 +238,10 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
             }
         }
         __syncwarp();
-      } else if (warp <= NT) {
+      } else if (warp < 3) {
         // ----------------------------------------------------------------- MMA
         if (lane == 0) {
-            const int x = warp - 1;
+            const int x = NT == 2 ? warp - 1 : 0;
             uint32_t rp = 0;                              // ring slots of earlier pieces
             uint32_t steps = 0;                           // this stream's key tiles of earlier pieces
             uint32_t turns = 0;                           // shared steps of earlier pieces (both streams present)
@@ -288,81 +293,128 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
                 }
             };
             bool ok = true;
-            for (int k = 0; ok; ++k) {
-                const TreeUnit *ur = wait_unit(k);
-                const bool got = ur && ur->b >= 0;
-                const int n = got ? ur->ntiles : 0;
-                const int nrt = got ? ur->nrt : 0;
-                free_unit(k);
-                if (!got) break;
-                const uint32_t r0 = rp;
-                rp += (uint32_t)(2 * n * TS);
-                if (!mbar_wait(q_full, k & 1, wc)) break;
-                if (x >= nrt) {
-                    // No row tile for this stream: it still sees every copy land and
-                    // hands every slot back, so that its phases stay in step.
-                    mbar_arrive(q_empty);
-                    for (uint32_t r = r0; r < rp && ok; ++r) {
-                        ok = mbar_wait(&slot_full[r % C::kSlots], (r / C::kSlots) & 1, wc);
-                        if (ok) mbar_arrive(&slot_empty[r % C::kSlots]);
-                    }
-                    continue;
-                }
-                tc_fence_after();
-                auto rk = [&](int j) { return r0 + (uint32_t)(pos_k<kSB>(j, n) * TS); };
-                auto rv = [&](int j) { return r0 + (uint32_t)(pos_v<kSB>(j, n) * TS); };
-                for (int j = 0; j < kSB && j < n && ok; ++j) {
-                    ok = wait_tile(rk(j));
-                    if (!ok) break;
-                    tc_fence_after();
-                    push_qk(rk(j), (steps + j) % kSB);
-                    mma_commit(&s_full[x * kSB + (steps + j) % kSB]);
-                    release_tile(rk(j));
-                    if (j == n - 1) mma_commit(q_empty);
-                }
-                for (int j = 0; j < n && ok; ++j) {
-                    const uint32_t st = steps + j;
-                    const int buf = st % kSB;
-                    const uint32_t ph = (st / kSB) & 1;
-                    if (NT == 2 && nrt == 2) {
-                        // Turns: stream 1 follows stream 0's step j, stream 0 stream 1's
-                        // step j - 1, so that one's products run under the other's softmax.
-                        // (Steps count on across pieces, so neither gets two phases ahead.)
-                        const uint32_t dep = turns + j + x;
-                        if (dep > 0 && !mbar_wait(&issued[1 - x], (dep - 1) & 1, wc)) { ok = false; break; }
-                    }
-                    if (!wait_tile(rv(j)) || !mbar_wait(&p_half[x * kSB + buf], ph, wc)) { ok = false; break; }
-                    const bool next = j + kSB < n;
-                    const bool paired = next && tile_there(rk(j + kSB));
-                    tc_fence_after();
-                    push_pv_half(rv(j), buf, 0, j == 0);
-                    if (!mbar_wait(&p_full[x * kSB + buf], ph, wc)) { ok = false; break; }
-                    tc_fence_after();
-                    push_pv_half(rv(j), buf, 1, false);
-                    if (NT == 2 && nrt == 2) mbar_arrive(&issued[x]);
-                    // With the next K tile there, its product goes straight behind
-                    // (a wait between pushes lets the tensor pipe run dry); else
-                    // this tile's V is handed back first.
-                    if (paired) push_qk(rk(j + kSB), buf);
-                    if (kSB == 2 || j == n - 1) mma_commit(&pv_done[x * kSB + buf]);
-                    release_tile(rv(j));
-                    if (next) {
-                        if (!paired) {
-                            if (!wait_tile(rk(j + kSB))) { ok = false; break; }
+            if constexpr (NT == 1) {
+                // QK and PV from a thread each: neither's waits hold up the other's
+                // products (one thread for both spent 2,200 cycles a key tile, 1,024 of
+                // them on products).  Each waits for the other's step first: what lay
+                // in the ring slot before its tile has then landed, as a parity wait
+                // needs (K_j comes at most kSB tiles before V_j, less than the ring).
+                for (int k = 0; ok; ++k) {
+                    const TreeUnit *ur = wait_unit(k);
+                    const bool got = ur && ur->b >= 0;
+                    const int n = got ? ur->ntiles : 0;
+                    free_unit(k);
+                    if (!got) break;
+                    const uint32_t r0 = rp;
+                    rp += (uint32_t)(2 * n * TS);
+                    if (warp == 2 && !mbar_wait(q_full, k & 1, wc)) break;
+                    for (int j = 0; j < n && ok; ++j) {
+                        const uint32_t st = steps + j;
+                        const int buf = st % kSB;
+                        const uint32_t ph = (st / kSB) & 1;
+                        if (warp == 2) {
+                            const uint32_t r = r0 + (uint32_t)(pos_k<kSB>(j, n) * TS);
+                            // The buffer's last P has gone through the tensor core.
+                            ok = (st < kSB || mbar_wait(&pv_done[buf], ph ^ 1, wc)) && wait_tile(r);
+                            if (!ok) break;
                             tc_fence_after();
-                            push_qk(rk(j + kSB), buf);
+                            push_qk(r, buf);
+                            mma_commit(&s_full[buf]);
+                            release_tile(r);
+                            if (j == n - 1) mma_commit(q_empty);
+                        } else {
+                            const uint32_t r = r0 + (uint32_t)(pos_v<kSB>(j, n) * TS);
+                            ok = mbar_wait(&p_half[buf], ph, wc) && wait_tile(r);
+                            if (!ok) break;
+                            tc_fence_after();
+                            push_pv_half(r, buf, 0, j == 0);
+                            ok = mbar_wait(&p_full[buf], ph, wc);
+                            if (!ok) break;
+                            tc_fence_after();
+                            push_pv_half(r, buf, 1, false);
+                            mma_commit(&pv_done[buf]);
+                            release_tile(r);
                         }
-                        mma_commit(&s_full[x * kSB + buf]);
-                        release_tile(rk(j + kSB));
-                        if (j + kSB == n - 1) mma_commit(q_empty);
                     }
+                    steps += n;
                 }
-                if (!ok) break;
-                steps += n;
-                if (nrt == 2) turns += n;
+            } else {
+                for (int k = 0; ok; ++k) {
+                    const TreeUnit *ur = wait_unit(k);
+                    const bool got = ur && ur->b >= 0;
+                    const int n = got ? ur->ntiles : 0;
+                    const int nrt = got ? ur->nrt : 0;
+                    free_unit(k);
+                    if (!got) break;
+                    const uint32_t r0 = rp;
+                    rp += (uint32_t)(2 * n * TS);
+                    if (!mbar_wait(q_full, k & 1, wc)) break;
+                    if (x >= nrt) {
+                        // No row tile for this stream: it still sees every copy land and
+                        // hands every slot back, so that its phases stay in step.
+                        mbar_arrive(q_empty);
+                        for (uint32_t r = r0; r < rp && ok; ++r) {
+                            ok = mbar_wait(&slot_full[r % C::kSlots], (r / C::kSlots) & 1, wc);
+                            if (ok) mbar_arrive(&slot_empty[r % C::kSlots]);
+                        }
+                        continue;
+                    }
+                    tc_fence_after();
+                    auto rk = [&](int j) { return r0 + (uint32_t)(pos_k<kSB>(j, n) * TS); };
+                    auto rv = [&](int j) { return r0 + (uint32_t)(pos_v<kSB>(j, n) * TS); };
+                    for (int j = 0; j < kSB && j < n && ok; ++j) {
+                        ok = wait_tile(rk(j));
+                        if (!ok) break;
+                        tc_fence_after();
+                        push_qk(rk(j), (steps + j) % kSB);
+                        mma_commit(&s_full[x * kSB + (steps + j) % kSB]);
+                        release_tile(rk(j));
+                        if (j == n - 1) mma_commit(q_empty);
+                    }
+                    for (int j = 0; j < n && ok; ++j) {
+                        const uint32_t st = steps + j;
+                        const int buf = st % kSB;
+                        const uint32_t ph = (st / kSB) & 1;
+                        if (nrt == 2) {
+                            // Turns: stream 1 follows stream 0's step j, stream 0 stream 1's
+                            // step j - 1, so that one's products run under the other's softmax.
+                            // (Steps count on across pieces, so neither gets two phases ahead.)
+                            const uint32_t dep = turns + j + x;
+                            if (dep > 0 && !mbar_wait(&issued[1 - x], (dep - 1) & 1, wc)) { ok = false; break; }
+                        }
+                        if (!wait_tile(rv(j)) || !mbar_wait(&p_half[x * kSB + buf], ph, wc)) { ok = false; break; }
+                        const bool next = j + kSB < n;
+                        const bool paired = next && tile_there(rk(j + kSB));
+                        tc_fence_after();
+                        push_pv_half(rv(j), buf, 0, j == 0);
+                        if (!mbar_wait(&p_full[x * kSB + buf], ph, wc)) { ok = false; break; }
+                        tc_fence_after();
+                        push_pv_half(rv(j), buf, 1, false);
+                        if (nrt == 2) mbar_arrive(&issued[x]);
+                        // With the next K tile there, its product goes straight behind
+                        // (a wait between pushes lets the tensor pipe run dry); else
+                        // this tile's V is handed back first.
+                        if (paired) push_qk(rk(j + kSB), buf);
+                        if (j == n - 1) mma_commit(&pv_done[x]);
+                        release_tile(rv(j));
+                        if (next) {
+                            if (!paired) {
+                                if (!wait_tile(rk(j + kSB))) { ok = false; break; }
+                                tc_fence_after();
+                                push_qk(rk(j + kSB), buf);
+                            }
+                            mma_commit(&s_full[x * kSB + buf]);
+                            release_tile(rk(j + kSB));
+                            if (j + kSB == n - 1) mma_commit(q_empty);
+                        }
+                    }
+                    if (!ok) break;
+                    steps += n;
+                    if (nrt == 2) turns += n;
+                }
             }
-            mma_commit(&drain[x]);
-            mbar_wait_drain(&drain[x], 0, wc);
+            mma_commit(&drain[warp - 1]);
+            mbar_wait_drain(&drain[warp - 1], 0, wc);
         }
         __syncwarp();
       } else if (warp == 3) {
@@ -379,9 +431,9 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
         const int row = q4 * 32 + lane;
         const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
         const float scale = fabsf(p.scale_log2);      // the MMA negates Q for a negative one
-        // Two S buffers: PV of step i completes phase i / 2 of its buffer's barrier.
-        // (A barrier per step could be one phase behind or one ahead of a wait,
-        // which a parity does not tell apart.)
+        // PV of step i completes phase i / kSB of its S buffer's barrier.  (One barrier
+        // for all steps could be a phase behind or a phase ahead of a wait, which a
+        // parity does not tell apart.)
         auto wait_pv = [&](uint32_t step) { mbar_wait(&pv_done[x * kSB + step % kSB], (step / kSB) & 1, wc); };
         uint32_t steps = 0, pieces = 0, rp = 0;
         for (int k = 0;; ++k) {
@@ -475,9 +527,9 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
                         m_ref = m_tile;
                     }
                     if (j > 0) {
-                        // With one S buffer, S_j there means PV_{j-1} is done; with two
+                        // With one S buffer, S_j there means PV_{j-1} is done; with more
                         // it may still run.
-                        if constexpr (kSB == 2) {
+                        if constexpr (kSB > 1) {
                             wait_pv(steps - 1);
                             tc_fence_after();
                         }
@@ -524,9 +576,10 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
             }
             // ------------------------------------------------------ epilogue
             ++pieces;
-            if constexpr (kSB == 2) {
-                if (steps >= 2) wait_pv(steps - 2);
-                wait_pv(steps - 1);
+            if constexpr (NT == 1) {
+#pragma unroll
+                for (int i = kSB; i >= 1; --i)
+                    if (steps >= (uint32_t)i) wait_pv(steps - i);
             } else {
                 mbar_wait(&pv_done[x], (pieces - 1) & 1, wc);
             }
