@@ -1090,10 +1090,9 @@ static fw_status_t build_tree(const fw_tensor_t *q, const fw_tensor_t *k_cache, 
     // A scale of zero would turn the -inf of hidden keys into NaN: the least
     // magnitude used leaves every score it multiplies at zero for the exponential.
     p.scale_log2 = scale * k_scale * 1.4426950408889634f;
-    if (!std::isfinite(p.scale_log2) || !std::isfinite(v_scale * 256.f))
-        return fail(FW_ERR_INVALID_ARG, "scale * k_scale or v_scale * 256 overflows");
+    if (!std::isfinite(p.scale_log2)) return fail(FW_ERR_INVALID_ARG, "scale * k_scale overflows");
     if (std::fabs(p.scale_log2) < 1e-30f) p.scale_log2 = std::copysign(1e-30f, p.scale_log2);
-    p.out_scale = kv8 ? v_scale * 256.f : v_scale;   // the FP8 kernel's values are a 256th
+    p.out_scale = v_scale;
     // Row tiles: whole drafts of up to 128 rows, or 128 heads of one draft.
     if (p.G <= 128) {
         p.tile_tokens = 128 / p.G < p.T ? 128 / p.G : p.T;

@@ -219,12 +219,12 @@ __device__ __forceinline__ void write_padding_rows(const TreeParams &p) {
     }
 }
 
-// This warp's word of "some draft of the request sees key" over the 128 keys of
-// a tile: bit l of word w is key 32 w + l.  128 threads (`id`: their named
-// barrier) share the drafts; `words` is 16 words of shared memory that nobody
-// else writes before the next call but one.
-__device__ __forceinline__ uint32_t seen_keys(const TreeParams &p, const TreeUnit &u, int key0, int thread, uint32_t id,
-                                              uint32_t *words) {
+// Which keys of a 128-key tile some draft of the request sees: bit l of word w is
+// key 32 w + l.  128 threads (`id`: their named barrier) share the drafts; `words`
+// is 16 words of shared memory that nobody else writes before the next call but
+// one.  seen_word reads a word of the result.
+__device__ __forceinline__ void seen_keys(const TreeParams &p, const TreeUnit &u, int key0, int thread, uint32_t id,
+                                          uint32_t *words) {
     const int lane = thread & 31, w4 = thread >> 5, base = u.n - u.d;
     uint32_t seen[4] = {0, 0, 0, 0};
     for (int t = thread; t < u.d; t += 128) {
@@ -238,7 +238,9 @@ __device__ __forceinline__ uint32_t seen_keys(const TreeParams &p, const TreeUni
         if (lane == 0) words[w4 * 4 + w] = seen[w];
     }
     named_bar_sync(id, 128);
-    return words[w4] | words[4 + w4] | words[8 + w4] | words[12 + w4];
+}
+__device__ __forceinline__ uint32_t seen_word(const uint32_t *words, int w) {
+    return words[w] | words[4 + w] | words[8 + w] | words[12 + w];
 }
 
 // This thread's row of a finished piece: its output and LSE, or its partial.

@@ -11,12 +11,13 @@
 //               every element down to 2^-10 of the row's largest; below, an
 //               element is off by at most 2^-17 of the largest.  Two terms of
 //               K = 32 products take the tensor core as long as one BF16 pass.
-//   O += P V    kind::f16 on FP16: four warps widen each V tile (to a 256th,
-//               exact in FP16; the output scale makes up for it) where it landed -- a key's 128 bytes lie in the second
-//               half of a 32 KiB slot and become 256, the thread that owns the
-//               key reads them all first.  P is rounded to FP16, scaled by 2^7
-//               so that weights down to 2^-21 of the largest keep 11 bits (base
-//               slack of 2^8 and that factor stay below FP16's 2^16).
+//   O += P V    kind::f16 on FP16: four warps widen each V tile (exact in FP16),
+//               64 keys at a time, from the slot it landed in to one the products
+//               read; the small second ring leaves most of shared memory to the
+//               copies in flight.  P is rounded
+//               to FP16, scaled by 2^7 so that weights down to 2^-21 of the
+//               largest keep 11 bits (base slack of 2^8 and that factor stay below
+//               FP16's 2^16).
 // The same warps split the queries, ahead of the softmax, and write zeros for
 // the values of keys nobody sees.
 //
@@ -25,6 +26,7 @@
 // a tile's softmax takes some 2,000 cycles of a warpgroup, more than the tile's
 // share of HBM).
 #include <cuda_fp16.h>
+#include <cuda_fp8.h>
 
 #include "tree_common.cuh"
 
@@ -48,19 +50,23 @@ struct F8TreeCfg {
     static constexpr int kWG = 2;                               // softmax warpgroups, NT = 1: every other tile each
     static constexpr int kQBytes = 128 * D * 2;                 // BF16 rows, then their two E4M3 terms in place
     static constexpr int kKBytes = 128 * D;
-    static constexpr int kVBytes = 128 * D * 2;                 // FP16 values; E4M3 lands in the second half
-    static constexpr int kHalf = 128 * 128;
-    static constexpr int kKSlots = NT == 2 ? 4 : 3;
-    static constexpr int kVSlots = NT == 2 ? 3 : 4;
+    static constexpr int kHalf = 128 * 128;                     // 64 columns of the BF16 rows; one term
+    static constexpr int kVChunk = 64 * 128;                    // 64 keys x 64 FP16 columns
+    static constexpr int kVBytes = 2 * kVChunk;                 // FP16 values of half a tile's keys
+    static constexpr int kKSlots = NT == 2 ? 3 : 4;
+    static constexpr int kRSlots = NT == 2 ? 4 : 5;             // E4M3 values as they land
+    static constexpr int kVSlots = NT == 2 ? 3 : 2;
     static constexpr int kOffQ = 0;
     static constexpr int kOffK = kOffQ + NT * kQBytes;
-    static constexpr int kOffV = kOffK + kKSlots * kKBytes;
+    static constexpr int kOffR = kOffK + kKSlots * kKBytes;
+    static constexpr int kOffV = kOffR + kRSlots * kKBytes;
     static constexpr int kOffBar = kOffV + kVSlots * kVBytes;
     static constexpr int kSched = 4;
     static constexpr int kBarKFull = 0;
     static constexpr int kBarKEmpty = kBarKFull + kKSlots;
-    static constexpr int kBarVRaw = kBarKEmpty + kKSlots;       // E4M3 values landed
-    static constexpr int kBarVFull = kBarVRaw + kVSlots;        // widened
+    static constexpr int kBarRFull = kBarKEmpty + kKSlots;      // E4M3 values landed
+    static constexpr int kBarREmpty = kBarRFull + kRSlots;      // and read
+    static constexpr int kBarVFull = kBarREmpty + kRSlots;      // widened
     static constexpr int kBarVEmpty = kBarVFull + kVSlots;
     static constexpr int kBarQFull = kBarVEmpty + kVSlots;
     static constexpr int kBarQEmpty = kBarQFull + 1;
@@ -96,23 +102,18 @@ struct F8TreeCfg {
     __device__ static constexpr uint32_t o_col(int x) { return (uint32_t)(NT * kSB + x) * 128u; }
 };
 
-// Four E4M3 values (one word) as four FP16 values / 256, two words: the sign
-// and the seven other bits, moved to where FP16 has its sign, the low four bits
-// of its exponent and the high three of its mantissa, are exactly that, E4M3's
-// subnormals included.  (The conversion instruction would take the 16,384 values
-// of a tile some 4,000 cycles; this is four integer instructions for two.)  A NaN
-// code comes out as 480 / 256 and is put right by the caller.
+// Four E4M3 values (one word) as four FP16 values, two words.
 __device__ __forceinline__ void widen4(uint32_t w, uint32_t &lo, uint32_t &hi) {
-    const uint32_t a = __byte_perm(w, 0, 0x1404), b = __byte_perm(w, 0, 0x3424);   // bytes 0, 1 and 2, 3, each << 8
-    lo = ((a & 0x7f007f00u) >> 1) | (a & 0x80008000u);
-    hi = ((b & 0x7f007f00u) >> 1) | (b & 0x80008000u);
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi) : "r"(w));
 }
 
-// FP16 NaN in place of the lanes that widen4 made of NaN codes.
-__device__ __forceinline__ uint32_t nan_lanes(uint32_t h) {
-    if ((h & 0x7fffu) == 0x3f80u) h |= 0x7fffu;
-    if ((h & 0x7fff0000u) == 0x3f800000u) h |= 0x7fff0000u;
-    return h;
+// Two BF16 values (one word) times `up` as hi + mid, two E4M3 values each.
+__device__ __forceinline__ void split2(uint32_t w, float up, uint32_t &hi, uint32_t &mid) {
+    const float a = __uint_as_float(w << 16) * up, b = __uint_as_float(w & 0xffff0000u) * up;
+    hi = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    const float2 h = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi, __NV_E4M3)));
+    mid = __nv_cvt_float2_to_fp8x2(make_float2(a - h.x, b - h.y), __NV_SATFINITE, __NV_E4M3);
 }
 
 // -inf in place of the scores of hidden keys.
@@ -137,11 +138,13 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *sQ = smem + C::kOffQ;
     uint8_t *sK = smem + C::kOffK;
+    uint8_t *sR = smem + C::kOffR;
     uint8_t *sV = smem + C::kOffV;
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
     uint64_t *k_full = bars + C::kBarKFull;
     uint64_t *k_empty = bars + C::kBarKEmpty;
-    uint64_t *v_raw = bars + C::kBarVRaw;
+    uint64_t *r_full = bars + C::kBarRFull;
+    uint64_t *r_empty = bars + C::kBarREmpty;
     uint64_t *v_full = bars + C::kBarVFull;
     uint64_t *v_empty = bars + C::kBarVEmpty;
     uint64_t *q_full = bars + C::kBarQFull;
@@ -172,7 +175,8 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kKSlots; ++i) { mbar_init(&k_full[i], 1); mbar_init(&k_empty[i], NT); }
-        for (int i = 0; i < C::kVSlots; ++i) { mbar_init(&v_raw[i], 1); mbar_init(&v_full[i], 4); mbar_init(&v_empty[i], NT); }
+        for (int i = 0; i < C::kRSlots; ++i) { mbar_init(&r_full[i], 1); mbar_init(&r_empty[i], 4); }
+        for (int i = 0; i < C::kVSlots; ++i) { mbar_init(&v_full[i], 4); mbar_init(&v_empty[i], NT); }
         mbar_init(q_full, 1);
         mbar_init(q_empty, NT);
         for (int i = 0; i < NT * kSB; ++i) {
@@ -251,13 +255,13 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
                 const int slot0 = p.ps < kKvTile ? 0 : key0 % p.ps;
                 const unsigned who = __ballot_sync(0xffffffffu, phys >= 0);
                 uint32_t &i = is_v ? iv : ik;
-                const uint32_t slots = is_v ? C::kVSlots : C::kKSlots;
+                const uint32_t slots = is_v ? C::kRSlots : C::kKSlots;
                 const uint32_t sl = i % slots;
-                uint64_t *full = is_v ? &v_raw[sl] : &k_full[sl];
-                if (!warp_wait(is_v ? &v_empty[sl] : &k_empty[sl], ((i / slots) & 1) ^ 1, wc, lane)) return false;
+                uint64_t *full = is_v ? &r_full[sl] : &k_full[sl];
+                if (!warp_wait(is_v ? &r_empty[sl] : &k_empty[sl], ((i / slots) & 1) ^ 1, wc, lane)) return false;
                 if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(__popc(who) * box_rows * 128));
                 __syncwarp();
-                uint8_t *dst = is_v ? sV + sl * C::kVBytes + C::kHalf : sK + sl * C::kKBytes;
+                uint8_t *dst = (is_v ? sR : sK) + sl * C::kKBytes;
                 if (phys >= 0)
                     tma_load_4d(smem_u32(dst + lane * box_rows * 128), is_v ? (const void *)&tm_v : (const void *)&tm_k,
                                 full, 0, u.g, slot0, phys);
@@ -283,8 +287,8 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
             p.cuts[blockIdx.x] = walk.cut;
             for (uint32_t i = 0; i < (uint32_t)C::kKSlots && i < ik; ++i)
                 mbar_wait_drain(&k_full[(ik - 1 - i) % C::kKSlots], ((ik - 1 - i) / C::kKSlots) & 1, wc);
-            for (uint32_t i = 0; i < (uint32_t)C::kVSlots && i < iv; ++i)
-                mbar_wait_drain(&v_raw[(iv - 1 - i) % C::kVSlots], ((iv - 1 - i) / C::kVSlots) & 1, wc);
+            for (uint32_t i = 0; i < (uint32_t)C::kRSlots && i < iv; ++i)
+                mbar_wait_drain(&r_full[(iv - 1 - i) % C::kRSlots], ((iv - 1 - i) / C::kRSlots) & 1, wc);
         }
         __syncwarp();
       } else if (warp < 3) {
@@ -296,9 +300,14 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
             uint32_t turns = 0;                           // those both streams took part in
             const SDesc q_d = sdesc_sw128_split(smem_u32(sQ + x * C::kQBytes), 16, 1024);
             const SDesc k_d = sdesc_sw128_split(smem_u32(sK), 16, 1024);
-            const SDesc v_d = sdesc_sw128_split(smem_u32(sV), C::kHalf, 1024);
+            const SDesc v_d = sdesc_sw128_split(smem_u32(sV), C::kVChunk, 1024);
             auto wait_k = [&](uint32_t i) { return mbar_wait(&k_full[i % C::kKSlots], (i / C::kKSlots) & 1, wc); };
-            auto wait_v = [&](uint32_t i) { return mbar_wait(&v_full[i % C::kVSlots], (i / C::kVSlots) & 1, wc); };
+            // Half `half` of V tile i is number 2 i + half of the second ring.
+            auto wait_v = [&](uint32_t i, int half) {
+                const uint32_t h = 2 * i + half;
+                return mbar_wait(&v_full[h % C::kVSlots], (h / C::kVSlots) & 1, wc);
+            };
+            auto release_v = [&](uint32_t i, int half) { mma_commit(&v_empty[(2 * i + half) % C::kVSlots]); };
             auto k_there = [&](uint32_t i) {
                 return mbar_try_wait(smem_u32(&k_full[i % C::kKSlots]), (i / C::kKSlots) & 1);
             };
@@ -313,13 +322,11 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
                                   sdesc_at(kd, kk * 32), idesc_qk, term + kk > 0 ? 1u : 0u);
             };
             auto push_pv_half = [&](uint32_t i, int buf, int half, bool first) {
-                const SDesc vd{v_d.lo + (i % C::kVSlots) * (C::kVBytes >> 4), v_d.hi};
+                const SDesc vd{v_d.lo + ((2 * i + half) % C::kVSlots) * (C::kVBytes >> 4), v_d.hi};
 #pragma unroll
-                for (int k4 = 0; k4 < 4; ++k4) {
-                    const int kk = half * 4 + k4;
-                    mma_bf16_ts(tmem + C::o_col(x), tmem + C::s_col(x, buf) + kk * 8, sdesc_at(vd, kk * 16 * 128),
-                                kIdescPV, (first && kk == 0) ? 0u : 1u);
-                }
+                for (int k4 = 0; k4 < 4; ++k4)
+                    mma_bf16_ts(tmem + C::o_col(x), tmem + C::s_col(x, buf) + (half * 4 + k4) * 8,
+                                sdesc_at(vd, k4 * 16 * 128), kIdescPV, (first && half + k4 == 0) ? 0u : 1u);
             };
             bool ok = true;
             if constexpr (NT == 1) {
@@ -344,16 +351,17 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
                             mma_commit(&k_empty[steps % C::kKSlots]);
                             if (j == n - 1) mma_commit(q_empty);
                         } else {
-                            ok = wait_v(steps) && mbar_wait(&p_half[buf], ph, wc);
+                            ok = wait_v(steps, 0) && mbar_wait(&p_half[buf], ph, wc);
                             if (!ok) break;
                             tc_fence_after();
                             push_pv_half(steps, buf, 0, j == 0);
-                            ok = mbar_wait(&p_full[buf], ph, wc);
+                            release_v(steps, 0);
+                            ok = wait_v(steps, 1) && mbar_wait(&p_full[buf], ph, wc);
                             if (!ok) break;
                             tc_fence_after();
                             push_pv_half(steps, buf, 1, false);
                             mma_commit(&pv_done[buf]);
-                            mma_commit(&v_empty[steps % C::kVSlots]);
+                            release_v(steps, 1);
                         }
                     }
                 }
@@ -375,8 +383,10 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
                         for (uint32_t i = i0; i < tiles && ok; ++i) {
                             ok = wait_k(i);
                             if (ok) mbar_arrive(&k_empty[i % C::kKSlots]);
-                            ok = ok && wait_v(i);
-                            if (ok) mbar_arrive(&v_empty[i % C::kVSlots]);
+                            for (int half = 0; half < 2 && ok; ++half) {
+                                ok = wait_v(i, half);
+                                if (ok) mbar_arrive(&v_empty[(2 * i + half) % C::kVSlots]);
+                            }
                         }
                         continue;
                     }
@@ -400,18 +410,19 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
                             const uint32_t dep = turns + j + x;
                             if (dep > 0 && !mbar_wait(&issued[1 - x], (dep - 1) & 1, wc)) { ok = false; break; }
                         }
-                        if (!wait_v(iv) || !mbar_wait(&p_half[x * kSB + buf], ph, wc)) { ok = false; break; }
+                        if (!wait_v(iv, 0) || !mbar_wait(&p_half[x * kSB + buf], ph, wc)) { ok = false; break; }
                         const bool next = j + kSB < n;
                         const bool paired = next && k_there(ik);
                         tc_fence_after();
                         push_pv_half(iv, buf, 0, j == 0);
-                        if (!mbar_wait(&p_full[x * kSB + buf], ph, wc)) { ok = false; break; }
+                        if (!wait_v(iv, 1) || !mbar_wait(&p_full[x * kSB + buf], ph, wc)) { ok = false; break; }
                         tc_fence_after();
                         push_pv_half(iv, buf, 1, false);
                         if (nrt == 2) mbar_arrive(&issued[x]);
                         if (paired) push_qk(ik, buf);
                         if (j == n - 1) mma_commit(&pv_done[x]);
-                        mma_commit(&v_empty[iv % C::kVSlots]);
+                        release_v(iv, 0);
+                        release_v(iv, 1);
                         if (next) {
                             if (!paired) {
                                 if (!wait_k(ik)) { ok = false; break; }
@@ -441,7 +452,6 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
         // Thread = query row of a tile, then = key of a tile.  After an abort
         // every wait returns at once and the bounded loops run out.
         const int row = threadIdx.x - 128;
-        const uint32_t sw = row & 7;
         uint32_t i = 0;                                   // V tiles converted
         for (int k = 0;; ++k) {
             const TreeUnit *ur = wait_unit(k);
@@ -454,55 +464,45 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
             mbar_wait(q_full, k & 1, wc);
             for (int x = 0; x < u.nrt; ++x) {
                 // BF16 row * 2^e = hi + mid, both E4M3, over the row's own bytes: 16 lanes
-                // hold a row's 16-byte units, two rows a pass, all read before any is
-                // written.
+                // hold a row's 16-byte units, eight rows a pass (each pass waits for its
+                // reads and its maxima once), all read before any is written.
                 uint8_t *q0 = sQ + x * C::kQBytes;
                 const int un = lane & 15;
 #pragma unroll 1
-                for (int r = (row & ~31) + (lane >> 4); r < (row & ~31) + 32; r += 2) {
-                    const uint32_t rs = r & 7;
-                    const uint4 w = *reinterpret_cast<const uint4 *>(q0 + (un >> 3) * C::kHalf + r * 128 +
-                                                                     (((un & 7) ^ rs) << 4));
-                    uint32_t big = 0;                     // largest magnitude, as the bits of an FP32
-                    auto fold = [&](uint32_t v) { big = max(big, max((v << 16) & 0x7fff0000u, v & 0x7fff0000u)); };
-                    fold(w.x); fold(w.y); fold(w.z); fold(w.w);
+                for (int r0 = (row & ~31) + (lane >> 4); r0 < (row & ~31) + 32; r0 += 8) {
+                    uint4 w[4];
+                    uint32_t big[4];                      // largest magnitude, as the bits of an FP32
 #pragma unroll
-                    for (int o = 8; o > 0; o >>= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
-                    const int e = min(126, max(-120, 134 - (int)(big >> 23)));   // 7 - (exponent - 127)
-                    if (un == 0) q_exp[(k % C::kSched * NT + x) * 128 + r] = (int8_t)e;
-                    // Times 2^(e - 120), an FP32's exponent field is the E4M3 code's, and
-                    // its bits from 20 on are the code (truncated), subnormals included:
-                    // hi is the first four bits of the significand, mid the rest, rounded
-                    // to nearest where it is too small for four bits.  An infinite or NaN
-                    // element makes the row's scores NaN.
-                    const bool bad = big >= 0x7f800000u;
-                    const float up0 = __int_as_float((127 + (e - 120) / 2) << 23);
-                    const float up1 = __int_as_float((127 + (e - 120) - (e - 120) / 2) << 23);
-                    auto split1 = [&](uint32_t bits, uint32_t &hi, uint32_t &mid) {
-                        const float f = __uint_as_float(bits) * up0 * up1;
-                        const uint32_t fb = __float_as_uint(f);
-                        const uint32_t hb = fb & 0xfff00000u;
-                        const uint32_t mb = __float_as_uint(f - __uint_as_float(hb));
-                        const uint32_t mr = mb + 0x7ffffu + (mb >> 20 & 1u);
-                        hi = bad ? 0x7fu : (fb >> 24 & 0x80u) | (fb >> 20 & 0x7fu);
-                        mid = (fb >> 24 & 0x80u) | (mr >> 20 & 0x7fu);
-                    };
-                    auto split4 = [&](uint32_t v0, uint32_t v1, uint32_t &hi, uint32_t &mid) {
-                        uint32_t hc[4], mc[4];
-                        split1(v0 << 16, hc[0], mc[0]);
-                        split1(v0 & 0xffff0000u, hc[1], mc[1]);
-                        split1(v1 << 16, hc[2], mc[2]);
-                        split1(v1 & 0xffff0000u, hc[3], mc[3]);
-                        hi = __byte_perm(__byte_perm(hc[0], hc[1], 0x0040), __byte_perm(hc[2], hc[3], 0x0040), 0x5410);
-                        mid = __byte_perm(__byte_perm(mc[0], mc[1], 0x0040), __byte_perm(mc[2], mc[3], 0x0040), 0x5410);
-                    };
-                    uint2 hi, mid;
-                    split4(w.x, w.y, hi.x, mid.x);
-                    split4(w.z, w.w, hi.y, mid.y);
-                    __syncwarp();
-                    uint8_t *to = q0 + r * 128 + (((un >> 1) ^ rs) << 4) + (un & 1) * 8;
-                    *reinterpret_cast<uint2 *>(to) = hi;
-                    *reinterpret_cast<uint2 *>(to + C::kHalf) = mid;
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = r0 + 2 * i;
+                        w[i] = *reinterpret_cast<const uint4 *>(q0 + (un >> 3) * C::kHalf + r * 128 + (((un & 7) ^ (r & 7)) << 4));
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        auto top = [](uint32_t v) { return max((v << 16) & 0x7fff0000u, v & 0x7fff0000u); };
+                        big[i] = max(max(top(w[i].x), top(w[i].y)), max(top(w[i].z), top(w[i].w)));
+                    }
+#pragma unroll
+                    for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) big[i] = max(big[i], __shfl_xor_sync(0xffffffffu, big[i], o));
+                    __syncwarp();                         // the rows are read
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = r0 + 2 * i;
+                        const int e = min(126, max(-120, 134 - (int)(big[i] >> 23)));   // 7 - (exponent - 127)
+                        if (un == 0) q_exp[(k % C::kSched * NT + x) * 128 + r] = (int8_t)e;
+                        // An infinite or NaN element makes the row's scores NaN.
+                        const float up = __int_as_float(big[i] >= 0x7f800000u ? 0x7fc00000 : (127 + e) << 23);
+                        uint32_t hi[4], mid[4];
+                        split2(w[i].x, up, hi[0], mid[0]);
+                        split2(w[i].y, up, hi[1], mid[1]);
+                        split2(w[i].z, up, hi[2], mid[2]);
+                        split2(w[i].w, up, hi[3], mid[3]);
+                        uint8_t *to = q0 + r * 128 + (((un >> 1) ^ (r & 7)) << 4) + (un & 1) * 8;
+                        *reinterpret_cast<uint2 *>(to) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+                        *reinterpret_cast<uint2 *>(to + C::kHalf) = make_uint2(mid[0] | mid[1] << 16, mid[2] | mid[3] << 16);
+                    }
                 }
             }
             fence_proxy_async_smem();
@@ -511,49 +511,47 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
             const int base = u.n - u.d;
             for (int j = 0; j < u.ntiles; ++j, ++i) {
                 const int key0 = (u.tile0 + j) * kKvTile;
-                bool hidden = false;
-                if (key0 + kKvTile > base)
-                    hidden = !(seen_keys(p, u, key0, row, 3, seen_words + (j & 1) * 16) >> lane & 1);
-                const uint32_t sl = i % C::kVSlots;
-                mbar_wait(&v_raw[sl], (i / C::kVSlots) & 1, wc);
-                uint8_t *vr = sV + sl * C::kVBytes + row * 128;
-                // Half hh of the key's E4M3 bytes becomes its FP16 row in half hh of the
-                // slot; the second half overwrites the E4M3 bytes, its own read first.
-                // (Rolled: unrolled, this and the softmax evict each other from the
-                // instruction cache, which more than doubled both.)
-                uint32_t full = 0;                        // bit 7 of a byte: its other seven were all ones, a NaN
+                uint32_t *words = seen_words + (j & 1) * 16;
+                const bool drafts = key0 + kKvTile > base;
+                if (drafts) seen_keys(p, u, key0, row, 3, words);
+                const uint32_t rl = i % C::kRSlots;
+                mbar_wait(&r_full[rl], (i / C::kRSlots) & 1, wc);
+                // Keys key and 64 + key, columns 64 ch .. 64 ch + 63 of each.  (Rolled:
+                // unrolled, this and the softmax evict each other from the instruction
+                // cache, which more than doubled both.)
+                const int key = row & 63, ch = row >> 6;
+                const uint32_t sw = key & 7;
 #pragma unroll 1
-                for (int hh = 0; hh < 2; ++hh) {
+                for (int half = 0; half < 2; ++half) {
+                    const uint32_t hv = 2 * i + half, sl = hv % C::kVSlots;
+                    const uint8_t *from = sR + rl * C::kKBytes + (half * 64 + key) * 128;
+                    uint8_t *to = sV + sl * C::kVBytes + ch * C::kVChunk + key * 128;
                     uint4 w[4];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        w[c] = *reinterpret_cast<const uint4 *>(vr + C::kHalf + (((hh * 4 + c) ^ sw) << 4));
-                    uint8_t *to = vr + hh * C::kHalf;
+                    for (int c = 0; c < 4; ++c) w[c] = *reinterpret_cast<const uint4 *>(from + (((ch * 4 + c) ^ sw) << 4));
+                    // Values of keys nobody sees must not meet a zero weight: they may be NaN.
+                    if (drafts && !(seen_word(words, half * 2 + (key >> 5)) >> (key & 31) & 1)) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) w[c] = make_uint4(0, 0, 0, 0);
+                    }
+                    mbar_wait(&v_empty[sl], ((hv / C::kVSlots) & 1) ^ 1, wc);
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {         // 16 values: two units of FP16
-                        if (hidden) w[c] = make_uint4(0, 0, 0, 0);
                         uint4 a, b;
                         widen4(w[c].x, a.x, a.y);
                         widen4(w[c].y, a.z, a.w);
                         widen4(w[c].z, b.x, b.y);
                         widen4(w[c].w, b.z, b.w);
-                        full |= ((w[c].x & 0x7f7f7f7fu) + 0x01010101u) | ((w[c].y & 0x7f7f7f7fu) + 0x01010101u) |
-                                ((w[c].z & 0x7f7f7f7fu) + 0x01010101u) | ((w[c].w & 0x7f7f7f7fu) + 0x01010101u);
                         *reinterpret_cast<uint4 *>(to + (((2 * c) ^ sw) << 4)) = a;
                         *reinterpret_cast<uint4 *>(to + (((2 * c + 1) ^ sw) << 4)) = b;
                     }
-                }
-                if (full & 0x80808080u) {
-#pragma unroll 1
-                    for (int c = 0; c < 16; ++c) {
-                        uint4 *at = reinterpret_cast<uint4 *>(vr + (c >> 3) * C::kHalf + (((c & 7) ^ sw) << 4));
-                        const uint4 h = *at;
-                        *at = make_uint4(nan_lanes(h.x), nan_lanes(h.y), nan_lanes(h.z), nan_lanes(h.w));
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (half == 1) mbar_arrive(&r_empty[rl]);
+                        mbar_arrive(&v_full[sl]);
                     }
                 }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&v_full[sl]);
             }
         }
     } else {

@@ -463,7 +463,9 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
                 if (drafts) {
                     // Values of keys nobody sees must not meet a zero weight: they
                     // may be NaN.  A key is seen when some draft's mask shows it.
-                    const uint32_t mine = seen_keys(p, u, key0, row, 1 + x, seen_words + (x * 2 + (j & 1)) * 16);
+                    uint32_t *words = seen_words + (x * 2 + (j & 1)) * 16;
+                    seen_keys(p, u, key0, row, 1 + x, words);
+                    const uint32_t mine = seen_word(words, q4);       // this warp's keys
                     if (__any_sync(0xffffffffu, !(mine >> lane & 1))) {
                         const uint32_t r = r0 + (uint32_t)(pos_v<kSB>(j, u.ntiles) * TS);
                         // A parity wait needs the slot's copy before V_j to have landed.
