@@ -1067,6 +1067,9 @@ static fw_status_t build_tree(const fw_tensor_t *q, const fw_tensor_t *k_cache, 
     fw::TreeParams p{};
     p.B = (int)B; p.T = (int)T; p.Hq = (int)Hq; p.Hkv = (int)Hkv; p.G = (int)(Hq / Hkv); p.D = (int)D;
     p.ps = (int)ps; p.max_pages = (int)max_pages; p.num_pages = (int)P;
+    p.ps_shift = -1;
+    for (int i = 3; i <= 20; ++i)
+        if (ps == (1LL << i)) p.ps_shift = i;
     p.kv8 = kv8 ? 1 : 0;
     p.q = static_cast<const uint16_t *>(q->data);
     p.k_cache = k_cache->data;

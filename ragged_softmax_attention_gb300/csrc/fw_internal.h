@@ -149,6 +149,7 @@ struct TreeCut {                               // a unit whose first piece ended
 };
 struct TreeParams {
     int B, T, Hq, Hkv, G, D, ps, max_pages, num_pages;
+    int ps_shift;                              // log2 of ps, -1: not a power of two
     int kv8;                                   // 1: E4M3 caches
     const uint16_t *q; int64_t q_stride[3];    // [B, T, Hq, D] bf16
     const void *k_cache, *v_cache;

@@ -138,11 +138,12 @@ __device__ __forceinline__ void plan_range(const TreeParams &p, long long *plan,
     if (threadIdx.x == 0) { plan[0] = total; plan[3] = span; }
 }
 
-// Walks the pieces of this CTA's range (the producer warp, all lanes alike).
+// Walks the pieces of this CTA's range (the producer warp, all lanes alike).  It
+// stands at slot `vl` of unit `ui` of request b, so that a step divides nothing.
 template <int NT>
 struct TreeWalk {
-    long long total, span, pos, end, pb0;
-    int range, b, n, d, units, tiles;
+    long long span, left, row0;                       // slots left in the range; the request's first slot
+    int range, b, n, d, units, tiles, ui, vl;
     TreeCut cut;
 
     __device__ void open_row(const TreeParams &p) {
@@ -151,30 +152,36 @@ struct TreeWalk {
         tiles = ceil_div_i(n, kKvTile);
     }
     __device__ void init(const TreeParams &p, const long long *plan) {
-        total = plan[0];
         span = plan[3];
         range = p.ride ? (int)blockIdx.x / p.Hkv : (int)blockIdx.x;
-        pos = span * range;
-        end = min(total, pos + span);
+        const long long pos = span * range;
+        left = min(plan[0], pos + span) - pos;
         cut = TreeCut{};
-        if (pos < end) {
-            pb0 = plan[1];
+        if (left > 0) {
+            row0 = plan[1];
             b = (int)plan[2];
             open_row(p);
+            ui = (int)((pos - row0) / (p.piece_cost + tiles));
+            vl = (int)(pos - row0 - (long long)ui * (p.piece_cost + tiles));
         }
     }
     __device__ void next(const TreeParams &p, TreeUnit &u) {     // u.b = -1 at the end
         u.b = -1;
-        while (pos < end) {
-            const int v = p.piece_cost + tiles;
-            const long long row = (long long)units * v;
-            if (pos >= pb0 + row) { pb0 += row; ++b; open_row(p); continue; }
-            const int ui = (int)((pos - pb0) / v);
-            const int vl = (int)(pos - pb0 - (long long)ui * v);
-            if (vl < p.piece_cost) { pos += p.piece_cost - vl; continue; }
+        while (left > 0) {
+            if (ui >= units) {                        // on to the next request
+                row0 += (long long)units * (p.piece_cost + tiles);
+                ++b;
+                ui = 0;
+                open_row(p);
+                continue;
+            }
+            if (vl < p.piece_cost) {
+                left -= p.piece_cost - vl;
+                vl = p.piece_cost;
+                continue;
+            }
             const int tl = vl - p.piece_cost;
-            const int th = (int)min((long long)tiles, tl + (end - pos));
-            const long long ustart = pb0 + (long long)ui * v + p.piece_cost;
+            const int th = (int)min((long long)tiles, tl + left);
             u.b = b;
             const int per_head = p.ride ? units : units / p.Hkv;
             u.g = p.ride ? (int)blockIdx.x % p.Hkv : ui / per_head;
@@ -190,33 +197,44 @@ struct TreeWalk {
                 u.part = 2 * blockIdx.x;
             } else if (th < tiles) {
                 u.part = 2 * blockIdx.x + 1;
-                cut.count = (int)((ustart + tiles - 1) / span) - range + 1;
+                const long long last = row0 + (long long)ui * (p.piece_cost + tiles) + p.piece_cost + tiles - 1;
+                cut.count = (int)(last / span) - range + 1;
                 cut.b = b; cut.g = u.g; cut.rt0 = u.rt0; cut.nrt = u.nrt; cut.d = d;
             }
-            pos += th - tl;
+            left -= th - tl;
+            vl += th - tl;
+            if (th == tiles) { ++ui; vl = 0; }
             return;
         }
     }
 };
 
-// Zero output and -inf LSE for the rows past a request's drafts, requests
-// blockIdx.x, blockIdx.x + grid, ... (one warp).
-template <int D>
-__device__ __forceinline__ void write_padding_rows(const TreeParams &p) {
-    const int lane = threadIdx.x & 31;
-    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-        int n, d;
-        tree_row(p, b, n, d);
-        const int rows = (p.T - d) * p.Hq;
-        for (int i = lane; i < rows * (D / 8); i += 32) {
-            const int r = i / (D / 8), c = i - r * (D / 8);
-            const int t = d + r / p.Hq, h = r % p.Hq;
-            __nv_bfloat16 *o = reinterpret_cast<__nv_bfloat16 *>(p.out) + b * p.out_stride[0] +
-                               t * p.out_stride[1] + h * p.out_stride[2];
-            reinterpret_cast<uint4 *>(o)[c] = make_uint4(0, 0, 0, 0);
-            if (c == 0 && p.lse) p.lse[b * p.lse_stride[0] + t * p.lse_stride[1] + h * p.lse_stride[2]] = kNegInf;
-        }
+// The queries of a unit (one lane): `nrt` row tiles of 128-byte-swizzled 64-column
+// chunks, `chunk` bytes apart.
+template <int D, int NT>
+__device__ __forceinline__ void copy_queries(const TreeParams &p, const TreeUnit &u, const CUtensorMap &tm_q, uint8_t *sQ,
+                                             uint32_t tile_bytes, uint32_t chunk, uint64_t *q_full) {
+    const uint32_t qrows = p.head_chunks > 1 ? 128u : (uint32_t)(p.G * p.tile_tokens);
+    mbar_arrive_expect_tx(q_full, (uint32_t)u.nrt * (D / 64) * qrows * 128u);
+    for (int x = 0; x < u.nrt; ++x) {
+        const int rt = u.rt0 + x;
+        int h0 = u.g * p.G, t0 = rt * p.tile_tokens;
+        if (p.head_chunks > 1) { t0 = rt / p.head_chunks; h0 += (rt - t0 * p.head_chunks) * 128; }
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)
+            tma_load_4d(smem_u32(sQ + x * tile_bytes + c * chunk), &tm_q, q_full, c * 64, h0, t0, u.b);
     }
+}
+
+// The page of key tile j of a unit that this lane copies, -1: none.  A tile has up
+// to 16 pages, one to a lane.
+__device__ __forceinline__ int lane_page(const TreeParams &p, const TreeUnit &u, int j) {
+    const int lane = threadIdx.x & 31;
+    const int key = (u.tile0 + j) * kKvTile + (p.ps < kKvTile ? lane * p.ps : 0);
+    if ((lane > 0 && p.ps >= kKvTile) || lane * p.ps >= kKvTile || j >= u.ntiles || key >= u.n) return -1;
+    int phys = __ldg(p.block_table + (int64_t)u.b * p.bt_stride + (p.ps_shift >= 0 ? key >> p.ps_shift : key / p.ps));
+    if ((unsigned)phys >= (unsigned)p.num_pages) { record_error(p.status, kErrInvalid); phys = 0; }
+    return phys;
 }
 
 // Which keys of a 128-key tile some draft of the request sees: bit l of word w is

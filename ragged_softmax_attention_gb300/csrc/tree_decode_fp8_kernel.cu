@@ -21,8 +21,8 @@
 // The same warps split the queries, ahead of the softmax, and write zeros for
 // the values of keys nobody sees.
 //
-// Warp roles: 0 copies, 1 and 2 issue MMAs, 3 writes the rows that see
-// nothing, 4-7 convert, 8-15 softmax (a warpgroup per stream, or two for one:
+// Warp roles: 0 copies keys and values, 1 and 2 issue MMAs, 3 copies queries,
+// 4-7 convert, 8-15 softmax (a warpgroup per stream, or two for one:
 // a tile's softmax takes some 2,000 cycles of a warpgroup, more than the tile's
 // share of HBM).
 #include <cuda_fp16.h>
@@ -92,7 +92,7 @@ struct F8TreeCfg {
     static constexpr int kSmemBytes = kOffMisc + 16 + 1024;
     static_assert(kSmemBytes <= 232448, "shared memory budget of one CTA exceeded");
     static constexpr int kThreads = 256 + kWG * 128;
-    static constexpr int kSchedReaders = 2 + 4 + 4 * kWG;
+    static constexpr int kSchedReaders = 3 + 4 + 4 * kWG;            // issuers, queries, converters, softmax
     // 512 threads launched at 128 registers: 128 x 72 + 128 x 96 + 256 x 168 =
     // 64512 <= 65536.
     static constexpr uint32_t kRegsControl = 72, kRegsConvert = 96, kRegsSoftmax = 168, kRegsLaunch = 128;
@@ -215,41 +215,17 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
         TreeWalk<NT> walk;
         walk.init(p, plan);
         const int box_rows = p.ps < kKvTile ? p.ps : kKvTile;
-        const int pages_per_tile = p.ps < kKvTile ? kKvTile / p.ps : 1;
         uint32_t ik = 0, iv = 0;                          // K and V tiles issued
         bool ok = true;
+        TreeUnit u, un;
+        walk.next(p, u);
         for (int k = 0; ok; ++k) {
-            TreeUnit u;
-            walk.next(p, u);
             const int us = k % C::kSched;
             ok = warp_wait(&sched_empty[us], ((k / C::kSched) & 1) ^ 1, wc, lane);
             if (!ok) break;
             if (lane == 0) { sched[us] = u; mbar_arrive(&sched_full[us]); }
             __syncwarp();
             if (u.b < 0) break;
-            ok = warp_wait(q_empty, (k & 1) ^ 1, wc, lane);
-            if (!ok) break;
-            if (lane == 0) {
-                const uint32_t qrows = p.head_chunks > 1 ? 128u : (uint32_t)(p.G * p.tile_tokens);
-                mbar_arrive_expect_tx(q_full, (uint32_t)u.nrt * 2u * qrows * 128u);
-                for (int x = 0; x < u.nrt; ++x) {
-                    const int rt = u.rt0 + x;
-                    int h0 = u.g * p.G, t0 = rt * p.tile_tokens;
-                    if (p.head_chunks > 1) { t0 = rt / p.head_chunks; h0 += (rt - t0 * p.head_chunks) * 128; }
-#pragma unroll
-                    for (int c = 0; c < 2; ++c)
-                        tma_load_4d(smem_u32(sQ + x * C::kQBytes + c * C::kHalf), &tm_q, q_full, c * 64, h0, t0, u.b);
-                }
-            }
-            __syncwarp();
-            const int32_t *bt_row = p.block_table + (int64_t)u.b * p.bt_stride;
-            auto tile_page = [&](int j) -> int {          // this lane's page of key tile j, -1: none
-                const int key = (u.tile0 + j) * kKvTile + (p.ps < kKvTile ? lane * p.ps : 0);
-                if (lane >= pages_per_tile || j >= u.ntiles || key >= u.n) return -1;
-                int phys = __ldg(bt_row + key / p.ps);
-                if ((unsigned)phys >= (unsigned)p.num_pages) { record_error(p.status, kErrInvalid); phys = 0; }
-                return phys;
-            };
             auto copy_tile = [&](int j, int phys, bool is_v) -> bool {
                 const int key0 = (u.tile0 + j) * kKvTile;
                 const int slot0 = p.ps < kKvTile ? 0 : key0 % p.ps;
@@ -268,20 +244,25 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
                 ++i;
                 return true;
             };
-            // Page numbers run two tiles ahead of the K copies.
+            // Page numbers run two tiles ahead of the K copies, and the next piece is
+            // worked out once the ring is full: at the piece's end that took 10,000
+            // cycles, most of them for instructions gone from the cache.
             int pages[kSB + 3];
 #pragma unroll
-            for (int i = 0; i < kSB + 3; ++i) pages[i] = tile_page(i);
+            for (int i = 0; i < kSB + 3; ++i) pages[i] = lane_page(p, u, i);
 #pragma unroll
             for (int j = 0; j < kSB; ++j)
                 if (j < u.ntiles && ok) ok = copy_tile(j, pages[j], false);
+            const int ahead = min(4, u.ntiles - 1);
             for (int j = 0; j < u.ntiles && ok; ++j) {
                 ok = copy_tile(j, pages[0], true);
                 if (ok && j + kSB < u.ntiles) ok = copy_tile(j + kSB, pages[kSB], false);
 #pragma unroll
                 for (int i = 0; i < kSB + 2; ++i) pages[i] = pages[i + 1];
-                pages[kSB + 2] = tile_page(j + kSB + 3);
+                pages[kSB + 2] = lane_page(p, u, j + kSB + 3);
+                if (j == ahead) walk.next(p, un);
             }
+            u = un;
         }
         if (lane == 0) {
             p.cuts[blockIdx.x] = walk.cut;
@@ -444,7 +425,29 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
         }
         __syncwarp();
       } else if (warp == 3) {
-        write_padding_rows<D>(p);
+        // ------------------------------------------------------------- queries
+        // They have a warp of their own, so that the next piece's keys need
+        // not wait behind them for this piece's last product.
+        for (int k = 0;; ++k) {
+            const TreeUnit *ur = wait_unit(k);
+            TreeUnit u;
+            u.b = -1;
+            if (ur) u = *ur;
+            __syncwarp();
+            if (lane == 0) free_unit(k);
+            if (u.b >= 0 && warp_wait(q_empty, (k & 1) ^ 1, wc, lane)) {
+                if (lane == 0) copy_queries<D, NT>(p, u, tm_q, sQ, C::kQBytes, C::kHalf, q_full);
+                __syncwarp();
+            } else {
+                u.b = -1;
+            }
+            if (u.b < 0) {
+                // The copies land before the CTA leaves.
+                if (lane == 0 && k > 0) mbar_wait_drain(q_full, (k - 1) & 1, wc);
+                break;
+            }
+        }
+        __syncwarp();
       }
     } else if (warp < 8) {
         if constexpr (C::kRegsConvert < C::kRegsLaunch) setmaxnreg_dec<C::kRegsConvert>();
@@ -467,9 +470,11 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
                 // hold a row's 16-byte units, eight rows a pass (each pass waits for its
                 // reads and its maxima once), all read before any is written.
                 uint8_t *q0 = sQ + x * C::kQBytes;
+                const int rows = p.head_chunks > 1 ? 128 : p.G * p.tile_tokens;
                 const int un = lane & 15;
 #pragma unroll 1
-                for (int r0 = (row & ~31) + (lane >> 4); r0 < (row & ~31) + 32; r0 += 8) {
+                for (int rb = 8 * (warp - 4); rb < rows; rb += 32) {
+                    const int r0 = rb + (lane >> 4);
                     uint4 w[4];
                     uint32_t big[4];                      // largest magnitude, as the bits of an FP32
 #pragma unroll

@@ -28,7 +28,7 @@
 // Warp roles: warp 0 copies (Q, then K and V tiles through a ring of 32 KiB
 // slots in the order the MMAs take them), warps 1 and 2 issue the MMAs (of a
 // stream each, or of QK and PV),
-// warp 3 writes the rows that see nothing, warps 4.. run the softmax.
+// warp 3 copies the queries, warps 4.. run the softmax.
 #include "tree_common.cuh"
 
 namespace fw {
@@ -71,7 +71,7 @@ struct TreeCfg {
     static constexpr int kSmemBytes = kOffMisc + 16 + 1024;
     static_assert(kSmemBytes <= 232448, "shared memory budget of one CTA exceeded");
     static constexpr int kThreads = 128 + NT * 128;
-    static constexpr int kSchedReaders = 2 + 4 * NT;            // issuers and softmax warps
+    static constexpr int kSchedReaders = 3 + 4 * NT;            // issuers, queries, softmax warps
     // NT = 2: 384 threads launched at 168 registers; 128 x 80 + 256 x 208 = 63488 <= 64512.
     static constexpr uint32_t kRegsControl = 80, kRegsSoftmax = 208;
     static_assert(NT == 1 || 128 * kRegsControl + 256 * kRegsSoftmax <= 384 * 168, "register split");
@@ -151,13 +151,11 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
         TreeWalk<NT> walk;
         walk.init(p, plan);
         const int box_rows = p.ps < kKvTile ? p.ps : kKvTile;
-        const int pages_per_tile = p.ps < kKvTile ? kKvTile / p.ps : 1;
         uint32_t rp = 0;                                  // ring slots filled so far
         bool ok = true;
-        int k = 0;
-        while (ok) {
-            TreeUnit u;
-            walk.next(p, u);
+        TreeUnit u, un;
+        walk.next(p, u);
+        for (int k = 0; ok; ++k) {
             {
                 const int sl = k % C::kSched;
                 ok = warp_wait(&sched_empty[sl], ((k / C::kSched) & 1) ^ 1, wc, lane);
@@ -166,32 +164,7 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
                 __syncwarp();
             }
             if (u.b < 0) break;
-            ok = warp_wait(q_empty, (k & 1) ^ 1, wc, lane);
-            if (!ok) break;
-            if (lane == 0) {
-                const uint32_t qrows = p.head_chunks > 1 ? 128u : (uint32_t)(p.G * p.tile_tokens);
-                mbar_arrive_expect_tx(q_full, (uint32_t)u.nrt * (D / 64) * qrows * 128u);
-                for (int x = 0; x < u.nrt; ++x) {
-                    const int rt = u.rt0 + x;
-                    int h0 = u.g * p.G, t0 = rt * p.tile_tokens;
-                    if (p.head_chunks > 1) { t0 = rt / p.head_chunks; h0 += (rt - t0 * p.head_chunks) * 128; }
-#pragma unroll
-                    for (int c = 0; c < D / 64; ++c)
-                        tma_load_4d(smem_u32(sQ + x * C::kQBytes + c * C::kChunkBytes), &tm_q, q_full, c * 64, h0, t0,
-                                    u.b);
-                }
-            }
-            __syncwarp();
-            // ---- K and V tiles in the order the MMAs take them.  Lane l holds
-            // the pages of one tile (at most 16); each lane copies its page.
-            const int32_t *bt_row = p.block_table + (int64_t)u.b * p.bt_stride;
-            auto tile_page = [&](int j) -> int {          // this lane's page of key tile j, -1: none
-                const int key = (u.tile0 + j) * kKvTile + (p.ps < kKvTile ? lane * p.ps : 0);
-                if (lane >= pages_per_tile || j >= u.ntiles || key >= u.n) return -1;
-                int phys = __ldg(bt_row + key / p.ps);
-                if ((unsigned)phys >= (unsigned)p.num_pages) { record_error(p.status, kErrInvalid); phys = 0; }
-                return phys;
-            };
+            // ---- K and V tiles in the order the MMAs take them
             auto copy_tile = [&](int j, int phys, bool is_v) -> bool {
                 const int key0 = (u.tile0 + j) * kKvTile;
                 const int slot0 = p.ps < kKvTile ? 0 : key0 % p.ps;
@@ -213,22 +186,25 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
                 }
                 return true;
             };
-            // Page numbers of the next tiles are fetched before this tile's
-            // slot is waited for: cur[i] is tile (next K) + i - kSB.
-            int pages[kSB + 2];
+            // Page numbers run two tiles ahead of the K copies, and the next piece is
+            // worked out once the ring is full: at the piece's end that took 10,000
+            // cycles, most of them for instructions gone from the cache.
+            int pages[kSB + 3];
 #pragma unroll
-            for (int i = 0; i < kSB + 2; ++i) pages[i] = tile_page(i);
+            for (int i = 0; i < kSB + 3; ++i) pages[i] = lane_page(p, u, i);
 #pragma unroll
             for (int j = 0; j < kSB; ++j)
                 if (j < u.ntiles && ok) ok = copy_tile(j, pages[j], false);
+            const int ahead = min(4, u.ntiles - 1);
             for (int j = 0; j < u.ntiles && ok; ++j) {
                 ok = copy_tile(j, pages[0], true);
                 if (ok && j + kSB < u.ntiles) ok = copy_tile(j + kSB, pages[kSB], false);
 #pragma unroll
-                for (int i = 0; i < kSB + 1; ++i) pages[i] = pages[i + 1];
-                pages[kSB + 1] = tile_page(j + kSB + 2);
+                for (int i = 0; i < kSB + 2; ++i) pages[i] = pages[i + 1];
+                pages[kSB + 2] = lane_page(p, u, j + kSB + 3);
+                if (j == ahead) walk.next(p, un);
             }
-            ++k;
+            u = un;
         }
         if (lane == 0) {
             p.cuts[blockIdx.x] = walk.cut;
@@ -418,8 +394,29 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
         }
         __syncwarp();
       } else if (warp == 3) {
-        // ------------------------------------------- rows that see nothing
-        write_padding_rows<D>(p);
+        // ------------------------------------------------------------- queries
+        // They have a warp of their own, so that the next piece's keys need
+        // not wait behind them for this piece's last product.
+        for (int k = 0;; ++k) {
+            const TreeUnit *ur = wait_unit(k);
+            TreeUnit u;
+            u.b = -1;
+            if (ur) u = *ur;
+            __syncwarp();
+            if (lane == 0) free_unit(k);
+            if (u.b >= 0 && warp_wait(q_empty, (k & 1) ^ 1, wc, lane)) {
+                if (lane == 0) copy_queries<D, NT>(p, u, tm_q, sQ, C::kQBytes, C::kChunkBytes, q_full);
+                __syncwarp();
+            } else {
+                u.b = -1;
+            }
+            if (u.b < 0) {
+                // The copies land before the CTA leaves.
+                if (lane == 0 && k > 0) mbar_wait_drain(q_full, (k - 1) & 1, wc);
+                break;
+            }
+        }
+        __syncwarp();
       }
     } else {
         if constexpr (NT == 2) setmaxnreg_inc<C::kRegsSoftmax>();
@@ -611,8 +608,23 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
 // where this takes 2).
 template <int D, int NT>
 __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__ TreeParams p) {
-    pdl_wait();                                      // the pieces are written
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // The rows past a request's drafts: zeros and -inf, a warp to a draft.  They
+    // wait for nothing.
+    const int nwarps = gridDim.x * gridDim.y * 8;
+    for (int i = (blockIdx.y * gridDim.x + blockIdx.x) * 8 + warp; i < p.B * p.T; i += nwarps) {
+        const int b = i / p.T, pt = i - b * p.T;
+        int n, d;
+        tree_row(p, b, n, d);
+        if (pt < d) continue;
+        __nv_bfloat16 *o = reinterpret_cast<__nv_bfloat16 *>(p.out) + b * p.out_stride[0] + pt * p.out_stride[1];
+        for (int c = lane; c < p.Hq * (D / 8); c += 32)
+            reinterpret_cast<uint4 *>(o + (c / (D / 8)) * p.out_stride[2])[c % (D / 8)] = make_uint4(0, 0, 0, 0);
+        if (p.lse)
+            for (int ph = lane; ph < p.Hq; ph += 32)
+                p.lse[b * p.lse_stride[0] + pt * p.lse_stride[1] + ph * p.lse_stride[2]] = kNegInf;
+    }
+    pdl_wait();                                      // the pieces are written
     const TreeCut cut = p.cuts[blockIdx.y];
     const int x = blockIdx.x / 16;
     const int row = (blockIdx.x & 15) * 8 + warp;
