@@ -88,6 +88,57 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     return *reinterpret_cast<uint32_t *>(&v);
 }
 
+// The softmax's instructions, not its latencies, set a tile's time once several
+// warps share a scheduler: maxima of three, and products and sums in pairs.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+__device__ __forceinline__ void split_pair(uint64_t v, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+// Largest of N values.
+template <int N>
+__device__ __forceinline__ float max_of(const float *v) {
+    float m[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+    for (int i = 4; i + 1 < N; i += 2) m[(i >> 1) & 3] = max3(m[(i >> 1) & 3], v[i], v[i + 1]);
+    return fmaxf(max3(m[0], m[1], m[2]), m[3]);
+}
+// 2^(v * scale + shift) of 64 values, in place, their sum added to four pairs.
+__device__ __forceinline__ void exp_64(float *v, float scale, float shift, uint64_t (&sum)[4]) {
+    const uint64_t sc = pair_of(scale, scale), sh = pair_of(shift, shift);
+#pragma unroll
+    for (int i = 0; i < 64; i += 2) {
+        float a, b;
+        split_pair(fma_pair(pair_of(v[i], v[i + 1]), sc, sh), a, b);
+        v[i] = ex2_approx(a);
+        v[i + 1] = ex2_approx(b);
+        sum[(i >> 1) & 3] = add_pair(sum[(i >> 1) & 3], pair_of(v[i], v[i + 1]));
+    }
+}
+__device__ __forceinline__ float sum_of(const uint64_t (&sum)[4]) {
+    float a, b;
+    split_pair(add_pair(add_pair(sum[0], sum[1]), add_pair(sum[2], sum[3])), a, b);
+    return a + b;
+}
+
 // Ring positions, in units of whole K or V tiles, of a piece of n key tiles
 // when QK runs L tiles ahead of PV: K_0 .. K_{L-1}, then V_j K_{j+L}.
 template <int L>
@@ -138,7 +189,7 @@ __device__ __forceinline__ void plan_range(const TreeParams &p, long long *plan,
     if (threadIdx.x == 0) { plan[0] = total; plan[3] = span; }
 }
 
-// Walks the pieces of this CTA's range (the producer warp, all lanes alike).  It
+// Walks the pieces of this CTA's range (one warp, all lanes alike).  It
 // stands at slot `vl` of unit `ui` of request b, so that a step divides nothing.
 template <int NT>
 struct TreeWalk {
@@ -226,15 +277,27 @@ __device__ __forceinline__ void copy_queries(const TreeParams &p, const TreeUnit
     }
 }
 
-// The page of key tile j of a unit that this lane copies, -1: none.  A tile has up
-// to 16 pages, one to a lane.
+// Whether this lane copies a page of key tile j of a unit: a tile has up to 16
+// pages, one to a lane.
+__device__ __forceinline__ bool lane_copies(const TreeParams &p, const TreeUnit &u, int j) {
+    const int lane = threadIdx.x & 31;
+    const int key = (u.tile0 + j) * kKvTile + (p.ps < kKvTile ? lane * p.ps : 0);
+    return lane * p.ps < kKvTile && (lane == 0 || p.ps < kKvTile) && j < u.ntiles && key < u.n;
+}
+// Its entry of the block table, read ahead: nothing looks at the value before the
+// copy does (a check here would wait for it, a thousand cycles a tile).
 __device__ __forceinline__ int lane_page(const TreeParams &p, const TreeUnit &u, int j) {
     const int lane = threadIdx.x & 31;
     const int key = (u.tile0 + j) * kKvTile + (p.ps < kKvTile ? lane * p.ps : 0);
-    if ((lane > 0 && p.ps >= kKvTile) || lane * p.ps >= kKvTile || j >= u.ntiles || key >= u.n) return -1;
-    int phys = __ldg(p.block_table + (int64_t)u.b * p.bt_stride + (p.ps_shift >= 0 ? key >> p.ps_shift : key / p.ps));
-    if ((unsigned)phys >= (unsigned)p.num_pages) { record_error(p.status, kErrInvalid); phys = 0; }
-    return phys;
+    return lane_copies(p, u, j)
+               ? __ldg(p.block_table + (int64_t)u.b * p.bt_stride + (p.ps_shift >= 0 ? key >> p.ps_shift : key / p.ps))
+               : 0;
+}
+// The page to copy, inside the pool whatever the table says.
+__device__ __forceinline__ int checked_page(const TreeParams &p, int phys) {
+    if ((unsigned)phys < (unsigned)p.num_pages) return phys;
+    record_error(p.status, kErrInvalid);
+    return 0;
 }
 
 // Which keys of a 128-key tile some draft of the request sees: bit l of word w is

@@ -21,8 +21,8 @@
 // The same warps split the queries, ahead of the softmax, and write zeros for
 // the values of keys nobody sees.
 //
-// Warp roles: 0 copies keys and values, 1 and 2 issue MMAs, 3 copies queries,
-// 4-7 convert, 8-15 softmax (a warpgroup per stream, or two for one:
+// Warp roles: 0 copies keys and values, 1 and 2 issue MMAs, 3 works out the
+// pieces and copies queries, 4-7 convert, 8-15 softmax (a warpgroup per stream, or two for one:
 // a tile's softmax takes some 2,000 cycles of a warpgroup, more than the tile's
 // share of HBM).
 #include <cuda_fp16.h>
@@ -92,7 +92,7 @@ struct F8TreeCfg {
     static constexpr int kSmemBytes = kOffMisc + 16 + 1024;
     static_assert(kSmemBytes <= 232448, "shared memory budget of one CTA exceeded");
     static constexpr int kThreads = 256 + kWG * 128;
-    static constexpr int kSchedReaders = 3 + 4 + 4 * kWG;            // issuers, queries, converters, softmax
+    static constexpr int kSchedReaders = 3 + 4 + 4 * kWG;            // issuers, the producer, converters, softmax
     // 512 threads launched at 128 registers: 128 x 72 + 128 x 96 + 256 x 168 =
     // 64512 <= 65536.
     static constexpr uint32_t kRegsControl = 72, kRegsConvert = 96, kRegsSoftmax = 168, kRegsLaunch = 128;
@@ -212,24 +212,22 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
       setmaxnreg_dec<C::kRegsControl>();
       if (warp == 0) {
         // ------------------------------------------------------------ producer
-        TreeWalk<NT> walk;
-        walk.init(p, plan);
         const int box_rows = p.ps < kKvTile ? p.ps : kKvTile;
         uint32_t ik = 0, iv = 0;                          // K and V tiles issued
         bool ok = true;
-        TreeUnit u, un;
-        walk.next(p, u);
         for (int k = 0; ok; ++k) {
-            const int us = k % C::kSched;
-            ok = warp_wait(&sched_empty[us], ((k / C::kSched) & 1) ^ 1, wc, lane);
-            if (!ok) break;
-            if (lane == 0) { sched[us] = u; mbar_arrive(&sched_full[us]); }
+            const TreeUnit *ur = wait_unit(k);
+            TreeUnit u;
+            u.b = -1;
+            if (ur) u = *ur;
             __syncwarp();
+            if (lane == 0) free_unit(k);
             if (u.b < 0) break;
-            auto copy_tile = [&](int j, int phys, bool is_v) -> bool {
+            auto copy_tile = [&](int j, int entry, bool is_v) -> bool {
                 const int key0 = (u.tile0 + j) * kKvTile;
-                const int slot0 = p.ps < kKvTile ? 0 : key0 % p.ps;
-                const unsigned who = __ballot_sync(0xffffffffu, phys >= 0);
+                const int slot0 = p.ps < kKvTile ? 0 : p.ps_shift >= 0 ? key0 & (p.ps - 1) : key0 % p.ps;
+                const bool mine = lane_copies(p, u, j);
+                const unsigned who = __ballot_sync(0xffffffffu, mine);
                 uint32_t &i = is_v ? iv : ik;
                 const uint32_t slots = is_v ? C::kRSlots : C::kKSlots;
                 const uint32_t sl = i % slots;
@@ -238,34 +236,28 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
                 if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(__popc(who) * box_rows * 128));
                 __syncwarp();
                 uint8_t *dst = (is_v ? sR : sK) + sl * C::kKBytes;
-                if (phys >= 0)
+                if (mine)
                     tma_load_4d(smem_u32(dst + lane * box_rows * 128), is_v ? (const void *)&tm_v : (const void *)&tm_k,
-                                full, 0, u.g, slot0, phys);
+                                full, 0, u.g, slot0, checked_page(p, entry));
                 ++i;
                 return true;
             };
-            // Page numbers run two tiles ahead of the K copies, and the next piece is
-            // worked out once the ring is full: at the piece's end that took 10,000
-            // cycles, most of them for instructions gone from the cache.
+            // Page numbers run two tiles ahead of the K copies.
             int pages[kSB + 3];
 #pragma unroll
             for (int i = 0; i < kSB + 3; ++i) pages[i] = lane_page(p, u, i);
 #pragma unroll
             for (int j = 0; j < kSB; ++j)
                 if (j < u.ntiles && ok) ok = copy_tile(j, pages[j], false);
-            const int ahead = min(4, u.ntiles - 1);
             for (int j = 0; j < u.ntiles && ok; ++j) {
                 ok = copy_tile(j, pages[0], true);
                 if (ok && j + kSB < u.ntiles) ok = copy_tile(j + kSB, pages[kSB], false);
 #pragma unroll
                 for (int i = 0; i < kSB + 2; ++i) pages[i] = pages[i + 1];
                 pages[kSB + 2] = lane_page(p, u, j + kSB + 3);
-                if (j == ahead) walk.next(p, un);
             }
-            u = un;
         }
         if (lane == 0) {
-            p.cuts[blockIdx.x] = walk.cut;
             for (uint32_t i = 0; i < (uint32_t)C::kKSlots && i < ik; ++i)
                 mbar_wait_drain(&k_full[(ik - 1 - i) % C::kKSlots], ((ik - 1 - i) / C::kKSlots) & 1, wc);
             for (uint32_t i = 0; i < (uint32_t)C::kRSlots && i < iv; ++i)
@@ -425,28 +417,29 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
         }
         __syncwarp();
       } else if (warp == 3) {
-        // ------------------------------------------------------------- queries
-        // They have a warp of their own, so that the next piece's keys need
-        // not wait behind them for this piece's last product.
+        // ----------------------------------------------- the pieces; queries
+        // A warp of their own: the next piece is worked out, and its keys copied,
+        // while this one's products run.  (Where the copying warp did it, a piece's
+        // end cost 10,000 cycles, most of them for instructions gone from the cache.)
+        TreeWalk<NT> walk;
+        walk.init(p, plan);
         for (int k = 0;; ++k) {
-            const TreeUnit *ur = wait_unit(k);
             TreeUnit u;
-            u.b = -1;
-            if (ur) u = *ur;
+            walk.next(p, u);
+            const int sl = k % C::kSched;
+            bool ok = warp_wait(&sched_empty[sl], ((k / C::kSched) & 1) ^ 1, wc, lane);
+            if (ok && lane == 0) { sched[sl] = u; mbar_arrive(&sched_full[sl]); }
             __syncwarp();
-            if (lane == 0) free_unit(k);
-            if (u.b >= 0 && warp_wait(q_empty, (k & 1) ^ 1, wc, lane)) {
-                if (lane == 0) copy_queries<D, NT>(p, u, tm_q, sQ, C::kQBytes, C::kHalf, q_full);
-                __syncwarp();
-            } else {
-                u.b = -1;
-            }
-            if (u.b < 0) {
+            ok = ok && u.b >= 0 && warp_wait(q_empty, (k & 1) ^ 1, wc, lane);
+            if (!ok) {
                 // The copies land before the CTA leaves.
                 if (lane == 0 && k > 0) mbar_wait_drain(q_full, (k - 1) & 1, wc);
                 break;
             }
+            if (lane == 0) copy_queries<D, NT>(p, u, tm_q, sQ, C::kQBytes, C::kHalf, q_full);
+            __syncwarp();
         }
+        if (lane == 0) p.cuts[blockIdx.x] = walk.cut;
         __syncwarp();
       }
     } else if (warp < 8) {
@@ -629,10 +622,7 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
                     tmem_ld32(sa + c * 64 + 32, v + 32);
                     tmem_wait_ld();
                     if (drafts) hide(v, c == 0 ? bits[0] : bits[2], c == 0 ? bits[1] : bits[3]);
-                    float e4[4] = {v[0], v[1], v[2], v[3]};
-#pragma unroll
-                    for (int i = 4; i < 64; ++i) e4[i & 3] = fmaxf(e4[i & 3], v[i]);
-                    ext = fmaxf(ext, fmaxf(fmaxf(e4[0], e4[1]), fmaxf(e4[2], e4[3])));
+                    ext = fmaxf(ext, max_of<64>(v));
                 }
                 const float m_tile = ext == kNegInf || !live ? kNegInf : ext * rs;
                 float m_prev = m_ref;                     // the rows' base so far
@@ -677,9 +667,7 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
                 // P = 2^(s * rs - m_ref + 7), rounded to FP16; the row sum takes it
                 // unrounded.
                 const float mu = (m_ref == kNegInf ? 0.f : m_ref) - kPShift;
-                float a8[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) a8[i] = 0.f;
+                uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
                     float v[64];
@@ -688,13 +676,9 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
                     tmem_ld32(sa + half * 64 + 32, v + 32);
                     tmem_wait_ld();
                     if (drafts) hide(v, half == 0 ? bits[0] : bits[2], half == 0 ? bits[1] : bits[3]);
+                    exp_64(v, rs, -mu, sum);
 #pragma unroll
-                    for (int i = 0; i < 64; i += 2) {
-                        const float p0 = ex2_approx(fmaf(v[i], rs, -mu));
-                        const float p1 = ex2_approx(fmaf(v[i + 1], rs, -mu));
-                        a8[(i >> 1) & 7] += p0 + p1;
-                        pk[i >> 1] = pack_half2(p0, p1);
-                    }
+                    for (int i = 0; i < 64; i += 2) pk[i >> 1] = pack_half2(v[i], v[i + 1]);
 #pragma unroll
                     for (int c = 0; c < 2; ++c)
                         tmem_st16u(sa + half * 32 + c * 16, *reinterpret_cast<const uint32_t(*)[16]>(pk + c * 16));
@@ -703,7 +687,7 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
                     __syncwarp();
                     if (lane == 0) mbar_arrive(half == 0 ? &p_half[x * kSB + buf] : &p_full[x * kSB + buf]);
                 }
-                l_sum += ((a8[0] + a8[1]) + (a8[2] + a8[3])) + ((a8[4] + a8[5]) + (a8[6] + a8[7]));
+                l_sum += sum_of(sum);
             }
             // ------------------------------------------------------ epilogue
             ++pieces;

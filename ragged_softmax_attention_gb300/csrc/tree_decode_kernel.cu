@@ -28,7 +28,7 @@
 // Warp roles: warp 0 copies (Q, then K and V tiles through a ring of 32 KiB
 // slots in the order the MMAs take them), warps 1 and 2 issue the MMAs (of a
 // stream each, or of QK and PV),
-// warp 3 copies the queries, warps 4.. run the softmax.
+// warp 3 works out the pieces and copies the queries, warps 4.. run the softmax.
 #include "tree_common.cuh"
 
 namespace fw {
@@ -71,7 +71,7 @@ struct TreeCfg {
     static constexpr int kSmemBytes = kOffMisc + 16 + 1024;
     static_assert(kSmemBytes <= 232448, "shared memory budget of one CTA exceeded");
     static constexpr int kThreads = 128 + NT * 128;
-    static constexpr int kSchedReaders = 3 + 4 * NT;            // issuers, queries, softmax warps
+    static constexpr int kSchedReaders = 3 + 4 * NT;            // issuers, the producer, softmax warps
     // NT = 2: 384 threads launched at 168 registers; 128 x 80 + 256 x 208 = 63488 <= 64512.
     static constexpr uint32_t kRegsControl = 80, kRegsSoftmax = 208;
     static_assert(NT == 1 || 128 * kRegsControl + 256 * kRegsSoftmax <= 384 * 168, "register split");
@@ -148,27 +148,23 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
       if constexpr (NT == 2) setmaxnreg_dec<C::kRegsControl>();
       if (warp == 0) {
         // ------------------------------------------------------------ producer
-        TreeWalk<NT> walk;
-        walk.init(p, plan);
         const int box_rows = p.ps < kKvTile ? p.ps : kKvTile;
         uint32_t rp = 0;                                  // ring slots filled so far
         bool ok = true;
-        TreeUnit u, un;
-        walk.next(p, u);
         for (int k = 0; ok; ++k) {
-            {
-                const int sl = k % C::kSched;
-                ok = warp_wait(&sched_empty[sl], ((k / C::kSched) & 1) ^ 1, wc, lane);
-                if (!ok) break;
-                if (lane == 0) { sched[sl] = u; mbar_arrive(&sched_full[sl]); }
-                __syncwarp();
-            }
+            const TreeUnit *ur = wait_unit(k);
+            TreeUnit u;
+            u.b = -1;
+            if (ur) u = *ur;
+            __syncwarp();
+            if (lane == 0) free_unit(k);
             if (u.b < 0) break;
             // ---- K and V tiles in the order the MMAs take them
-            auto copy_tile = [&](int j, int phys, bool is_v) -> bool {
+            auto copy_tile = [&](int j, int entry, bool is_v) -> bool {
                 const int key0 = (u.tile0 + j) * kKvTile;
-                const int slot0 = p.ps < kKvTile ? 0 : key0 % p.ps;
-                const unsigned who = __ballot_sync(0xffffffffu, phys >= 0);
+                const int slot0 = p.ps < kKvTile ? 0 : p.ps_shift >= 0 ? key0 & (p.ps - 1) : key0 % p.ps;
+                const bool mine = lane_copies(p, u, j);
+                const unsigned who = __ballot_sync(0xffffffffu, mine);
                 const uint32_t bytes = (uint32_t)(__popc(who) * box_rows * 256);
 #pragma unroll
                 for (int s = 0; s < TS; ++s, ++rp) {
@@ -176,7 +172,8 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
                     if (!warp_wait(&slot_empty[sl], ((rp / C::kSlots) & 1) ^ 1, wc, lane)) return false;
                     if (lane == 0) mbar_arrive_expect_tx(&slot_full[sl], bytes);
                     __syncwarp();
-                    if (phys >= 0) {
+                    if (mine) {
+                        const int phys = checked_page(p, entry);
 #pragma unroll
                         for (int c = 0; c < 2; ++c)
                             tma_load_4d(smem_u32(sRing + sl * C::kSlotBytes + c * C::kChunkBytes + lane * box_rows * 128),
@@ -186,28 +183,22 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
                 }
                 return true;
             };
-            // Page numbers run two tiles ahead of the K copies, and the next piece is
-            // worked out once the ring is full: at the piece's end that took 10,000
-            // cycles, most of them for instructions gone from the cache.
+            // Page numbers run two tiles ahead of the K copies.
             int pages[kSB + 3];
 #pragma unroll
             for (int i = 0; i < kSB + 3; ++i) pages[i] = lane_page(p, u, i);
 #pragma unroll
             for (int j = 0; j < kSB; ++j)
                 if (j < u.ntiles && ok) ok = copy_tile(j, pages[j], false);
-            const int ahead = min(4, u.ntiles - 1);
             for (int j = 0; j < u.ntiles && ok; ++j) {
                 ok = copy_tile(j, pages[0], true);
                 if (ok && j + kSB < u.ntiles) ok = copy_tile(j + kSB, pages[kSB], false);
 #pragma unroll
                 for (int i = 0; i < kSB + 2; ++i) pages[i] = pages[i + 1];
                 pages[kSB + 2] = lane_page(p, u, j + kSB + 3);
-                if (j == ahead) walk.next(p, un);
             }
-            u = un;
         }
         if (lane == 0) {
-            p.cuts[blockIdx.x] = walk.cut;
             for (uint32_t i = 0; i < (uint32_t)C::kSlots && i < rp; ++i) {
                 const uint32_t r = rp - 1 - i;
                 mbar_wait_drain(&slot_full[r % C::kSlots], (r / C::kSlots) & 1, wc);
@@ -394,28 +385,29 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
         }
         __syncwarp();
       } else if (warp == 3) {
-        // ------------------------------------------------------------- queries
-        // They have a warp of their own, so that the next piece's keys need
-        // not wait behind them for this piece's last product.
+        // ----------------------------------------------- the pieces; queries
+        // A warp of their own: the next piece is worked out, and its keys copied,
+        // while this one's products run.  (Where the copying warp did it, a piece's
+        // end cost 10,000 cycles, most of them for instructions gone from the cache.)
+        TreeWalk<NT> walk;
+        walk.init(p, plan);
         for (int k = 0;; ++k) {
-            const TreeUnit *ur = wait_unit(k);
             TreeUnit u;
-            u.b = -1;
-            if (ur) u = *ur;
+            walk.next(p, u);
+            const int sl = k % C::kSched;
+            bool ok = warp_wait(&sched_empty[sl], ((k / C::kSched) & 1) ^ 1, wc, lane);
+            if (ok && lane == 0) { sched[sl] = u; mbar_arrive(&sched_full[sl]); }
             __syncwarp();
-            if (lane == 0) free_unit(k);
-            if (u.b >= 0 && warp_wait(q_empty, (k & 1) ^ 1, wc, lane)) {
-                if (lane == 0) copy_queries<D, NT>(p, u, tm_q, sQ, C::kQBytes, C::kChunkBytes, q_full);
-                __syncwarp();
-            } else {
-                u.b = -1;
-            }
-            if (u.b < 0) {
+            ok = ok && u.b >= 0 && warp_wait(q_empty, (k & 1) ^ 1, wc, lane);
+            if (!ok) {
                 // The copies land before the CTA leaves.
                 if (lane == 0 && k > 0) mbar_wait_drain(q_full, (k - 1) & 1, wc);
                 break;
             }
+            if (lane == 0) copy_queries<D, NT>(p, u, tm_q, sQ, C::kQBytes, C::kChunkBytes, q_full);
+            __syncwarp();
         }
+        if (lane == 0) p.cuts[blockIdx.x] = walk.cut;
         __syncwarp();
       }
     } else {
@@ -509,13 +501,7 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
                             if (!(bits >> i & 1)) sv[w * 32 + i] = kNegInf;
                     }
                 }
-                float e8[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) e8[i] = sv[i];
-#pragma unroll
-                for (int i = 8; i < kKvTile; ++i) e8[i & 7] = fmaxf(e8[i & 7], sv[i]);
-                const float ext = fmaxf(fmaxf(fmaxf(e8[0], e8[1]), fmaxf(e8[2], e8[3])),
-                                        fmaxf(fmaxf(e8[4], e8[5]), fmaxf(e8[6], e8[7])));
+                const float ext = max_of<kKvTile>(sv);
                 const float m_tile = live ? ext * scale : kNegInf;    // -inf when it sees none of these keys
                 const bool up = m_tile > m_ref + kRescaleSlack;   // also the first visible tile: m_ref = -inf
                 if (__any_sync(0xffffffffu, up)) {
@@ -549,19 +535,13 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
                 // operand shares V's type); the row sum takes it unrounded.
                 const float mu = m_ref == kNegInf ? 0.f : m_ref;
                 uint32_t pk[kKvTile / 2];
-                float a8[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) a8[i] = 0.f;
+                uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
+                    exp_64(sv + half * 64, scale, -mu, sum);
 #pragma unroll
-                    for (int i = 0; i < kKvTile / 2; i += 2) {
-                        const int kx = half * (kKvTile / 2) + i;
-                        const float p0 = ex2_approx(fmaf(sv[kx], scale, -mu));
-                        const float p1 = ex2_approx(fmaf(sv[kx + 1], scale, -mu));
-                        a8[(i >> 1) & 7] += p0 + p1;
-                        pk[kx >> 1] = pack_bf16x2(p0, p1);
-                    }
+                    for (int i = 0; i < 64; i += 2)
+                        pk[half * 32 + (i >> 1)] = pack_bf16x2(sv[half * 64 + i], sv[half * 64 + i + 1]);
 #pragma unroll
                     for (int c = 0; c < 2; ++c)
                         tmem_st16u(sa + half * 32 + c * 16,
@@ -571,7 +551,7 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
                     __syncwarp();
                     if (lane == 0) mbar_arrive(half == 0 ? &p_half[x * kSB + buf] : &p_full[x * kSB + buf]);
                 }
-                l_sum += ((a8[0] + a8[1]) + (a8[2] + a8[3])) + ((a8[4] + a8[5]) + (a8[6] + a8[7]));
+                l_sum += sum_of(sum);
             }
             // ------------------------------------------------------ epilogue
             ++pieces;
