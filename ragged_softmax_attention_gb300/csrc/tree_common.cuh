@@ -284,15 +284,40 @@ __device__ __forceinline__ bool lane_copies(const TreeParams &p, const TreeUnit 
     const int key = (u.tile0 + j) * kKvTile + (p.ps < kKvTile ? lane * p.ps : 0);
     return lane * p.ps < kKvTile && (lane == 0 || p.ps < kKvTile) && j < u.ntiles && key < u.n;
 }
-// Its entry of the block table, read ahead: nothing looks at the value before the
-// copy does (a check here would wait for it, a thousand cycles a tile).
-__device__ __forceinline__ int lane_page(const TreeParams &p, const TreeUnit &u, int j) {
-    const int lane = threadIdx.x & 31;
-    const int key = (u.tile0 + j) * kKvTile + (p.ps < kKvTile ? lane * p.ps : 0);
-    return lane_copies(p, u, j)
-               ? __ldg(p.block_table + (int64_t)u.b * p.bt_stride + (p.ps_shift >= 0 ? key >> p.ps_shift : key / p.ps))
-               : 0;
-}
+// The block-table entries of a piece, 64 at a time in two registers a lane; the
+// next 32 are fetched while these are in use.  (Fetched tile by tile, an entry's
+// latency is the least a tile can take, some 1,000 cycles: an E4M3 tile's share
+// of HBM is 1,350, and the two add up.)
+struct PageWindow {
+    const int32_t *row;
+    int win, last, cur, nxt;
+
+    __device__ __forceinline__ int page_number(const TreeParams &p, int key) const {
+        return p.ps_shift >= 0 ? key >> p.ps_shift : key / p.ps;
+    }
+    __device__ __forceinline__ int entry(int lp) const { return lp <= last ? __ldg(row + lp) : 0; }
+    __device__ __forceinline__ void open(const TreeParams &p, const TreeUnit &u) {
+        const int lane = threadIdx.x & 31;
+        row = p.block_table + (int64_t)u.b * p.bt_stride;
+        win = page_number(p, u.tile0 * kKvTile);
+        last = page_number(p, min(u.n, (u.tile0 + u.ntiles) * kKvTile) - 1);
+        cur = entry(win + lane);
+        nxt = entry(win + 32 + lane);
+    }
+    // This lane's entry of key tile j (tiles in order; all lanes call).
+    __device__ __forceinline__ int at(const TreeParams &p, const TreeUnit &u, int j) {
+        const int lane = threadIdx.x & 31;
+        const int lp = page_number(p, (u.tile0 + j) * kKvTile);
+        if (lp >= win + 32) {
+            win += 32;
+            cur = nxt;
+            nxt = entry(win + 32 + lane);
+        }
+        const int idx = lp + lane - win;               // < 64 for the lanes that copy
+        const int a = __shfl_sync(0xffffffffu, cur, idx & 31), b = __shfl_sync(0xffffffffu, nxt, idx & 31);
+        return idx < 32 ? a : b;
+    }
+};
 // The page to copy, inside the pool whatever the table says.
 __device__ __forceinline__ int checked_page(const TreeParams &p, int phys) {
     if ((unsigned)phys < (unsigned)p.num_pages) return phys;

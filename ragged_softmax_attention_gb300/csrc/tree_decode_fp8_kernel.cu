@@ -242,19 +242,23 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
                 ++i;
                 return true;
             };
-            // Page numbers run two tiles ahead of the K copies.
-            int pages[kSB + 3];
+            PageWindow table;
+            table.open(p, u);
+            int entries[kSB];                             // of the tiles whose V copy is to come
 #pragma unroll
-            for (int i = 0; i < kSB + 3; ++i) pages[i] = lane_page(p, u, i);
-#pragma unroll
-            for (int j = 0; j < kSB; ++j)
-                if (j < u.ntiles && ok) ok = copy_tile(j, pages[j], false);
+            for (int j = 0; j < kSB; ++j) {
+                if (j >= u.ntiles || !ok) continue;
+                entries[j] = table.at(p, u, j);
+                ok = copy_tile(j, entries[j], false);
+            }
             for (int j = 0; j < u.ntiles && ok; ++j) {
-                ok = copy_tile(j, pages[0], true);
-                if (ok && j + kSB < u.ntiles) ok = copy_tile(j + kSB, pages[kSB], false);
+                ok = copy_tile(j, entries[0], true);
 #pragma unroll
-                for (int i = 0; i < kSB + 2; ++i) pages[i] = pages[i + 1];
-                pages[kSB + 2] = lane_page(p, u, j + kSB + 3);
+                for (int i = 0; i + 1 < kSB; ++i) entries[i] = entries[i + 1];
+                if (ok && j + kSB < u.ntiles) {
+                    entries[kSB - 1] = table.at(p, u, j + kSB);
+                    ok = copy_tile(j + kSB, entries[kSB - 1], false);
+                }
             }
         }
         if (lane == 0) {
