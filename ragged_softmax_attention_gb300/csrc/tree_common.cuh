@@ -277,12 +277,11 @@ __device__ __forceinline__ void copy_queries(const TreeParams &p, const TreeUnit
     }
 }
 
-// Whether this lane copies a page of key tile j of a unit: a tile has up to 16
-// pages, one to a lane.
-__device__ __forceinline__ bool lane_copies(const TreeParams &p, const TreeUnit &u, int j) {
-    const int lane = threadIdx.x & 31;
-    const int key = (u.tile0 + j) * kKvTile + (p.ps < kKvTile ? lane * p.ps : 0);
-    return lane * p.ps < kKvTile && (lane == 0 || p.ps < kKvTile) && j < u.ntiles && key < u.n;
+// Whether page `l` of key tile j of a unit is copied: a tile has up to 16 pages,
+// one to a lane.
+__device__ __forceinline__ bool page_copied(const TreeParams &p, const TreeUnit &u, int j, int l) {
+    const int key = (u.tile0 + j) * kKvTile + (p.ps < kKvTile ? l * p.ps : 0);
+    return l * p.ps < kKvTile && (l == 0 || p.ps < kKvTile) && j < u.ntiles && key < u.n;
 }
 // The block-table entries of a piece, 64 at a time in two registers a lane; the
 // next 32 are fetched while these are in use.  (Fetched tile by tile, an entry's
@@ -304,7 +303,7 @@ struct PageWindow {
         cur = entry(win + lane);
         nxt = entry(win + 32 + lane);
     }
-    // This lane's entry of key tile j (tiles in order; all lanes call).
+    // The entry of page lane % 16 of key tile j (tiles in order; all lanes call).
     __device__ __forceinline__ int at(const TreeParams &p, const TreeUnit &u, int j) {
         const int lane = threadIdx.x & 31;
         const int lp = page_number(p, (u.tile0 + j) * kKvTile);
@@ -313,7 +312,7 @@ struct PageWindow {
             cur = nxt;
             nxt = entry(win + 32 + lane);
         }
-        const int idx = lp + lane - win;               // < 64 for the lanes that copy
+        const int idx = lp + (lane & 15) - win;        // < 64 for the pages copied
         const int a = __shfl_sync(0xffffffffu, cur, idx & 31), b = __shfl_sync(0xffffffffu, nxt, idx & 31);
         return idx < 32 ? a : b;
     }

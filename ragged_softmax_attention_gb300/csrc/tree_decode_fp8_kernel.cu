@@ -223,42 +223,42 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
             __syncwarp();
             if (lane == 0) free_unit(k);
             if (u.b < 0) break;
-            auto copy_tile = [&](int j, int entry, bool is_v) -> bool {
-                const int key0 = (u.tile0 + j) * kKvTile;
-                const int slot0 = p.ps < kKvTile ? 0 : p.ps_shift >= 0 ? key0 & (p.ps - 1) : key0 % p.ps;
-                const bool mine = lane_copies(p, u, j);
-                const unsigned who = __ballot_sync(0xffffffffu, mine);
-                uint32_t &i = is_v ? iv : ik;
-                const uint32_t slots = is_v ? C::kRSlots : C::kKSlots;
-                const uint32_t sl = i % slots;
-                uint64_t *full = is_v ? &r_full[sl] : &k_full[sl];
-                if (!warp_wait(is_v ? &r_empty[sl] : &k_empty[sl], ((i / slots) & 1) ^ 1, wc, lane)) return false;
-                if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(__popc(who) * box_rows * 128));
-                __syncwarp();
-                uint8_t *dst = (is_v ? sR : sK) + sl * C::kKBytes;
-                if (mine)
-                    tma_load_4d(smem_u32(dst + lane * box_rows * 128), is_v ? (const void *)&tm_v : (const void *)&tm_k,
-                                full, 0, u.g, slot0, checked_page(p, entry));
-                ++i;
-                return true;
-            };
+            // K tile i and V tile i - kSB go out together, a half warp each: one
+            // after the other, a copy's barrier and copy instructions take this warp
+            // 1,100 cycles beside the others, and a tile two of them.
             PageWindow table;
             table.open(p, u);
-            int entries[kSB];                             // of the tiles whose V copy is to come
+            const bool is_v = lane >= 16;
+            const int l = lane & 15;
+            int entries[kSB + 1];                         // of the last tiles: V comes kSB later
 #pragma unroll
-            for (int j = 0; j < kSB; ++j) {
-                if (j >= u.ntiles || !ok) continue;
-                entries[j] = table.at(p, u, j);
-                ok = copy_tile(j, entries[j], false);
-            }
-            for (int j = 0; j < u.ntiles && ok; ++j) {
-                ok = copy_tile(j, entries[0], true);
+            for (int i = 0; i <= kSB; ++i) entries[i] = 0;
+            for (int i = 0; i < u.ntiles + kSB && ok; ++i) {
 #pragma unroll
-                for (int i = 0; i + 1 < kSB; ++i) entries[i] = entries[i + 1];
-                if (ok && j + kSB < u.ntiles) {
-                    entries[kSB - 1] = table.at(p, u, j + kSB);
-                    ok = copy_tile(j + kSB, entries[kSB - 1], false);
+                for (int e = 0; e < kSB; ++e) entries[e] = entries[e + 1];
+                if (i < u.ntiles) entries[kSB] = table.at(p, u, i);
+                const int j = is_v ? i - kSB : i;
+                const bool there = j >= 0 && j < u.ntiles;
+                const uint32_t slots = is_v ? C::kRSlots : C::kKSlots;
+                const uint32_t c = is_v ? iv : ik, sl = c % slots;
+                uint64_t *full = is_v ? &r_full[sl] : &k_full[sl];
+                const bool mine = there && page_copied(p, u, j, l);
+                const unsigned who = __ballot_sync(0xffffffffu, mine) & (is_v ? 0xffff0000u : 0xffffu);
+                bool landed = true;
+                if (l == 0 && there) landed = mbar_wait(is_v ? &r_empty[sl] : &k_empty[sl], ((c / slots) & 1) ^ 1, wc);
+                ok = __all_sync(0xffffffffu, landed);
+                if (!ok) break;
+                if (l == 0 && there) mbar_arrive_expect_tx(full, (uint32_t)(__popc(who) * box_rows * 128));
+                __syncwarp();
+                if (mine) {
+                    const int key0 = (u.tile0 + j) * kKvTile;
+                    const int slot0 = p.ps < kKvTile ? 0 : p.ps_shift >= 0 ? key0 & (p.ps - 1) : key0 % p.ps;
+                    tma_load_4d(smem_u32((is_v ? sR : sK) + sl * C::kKBytes + l * box_rows * 128),
+                                is_v ? (const void *)&tm_v : (const void *)&tm_k, full, 0, u.g, slot0,
+                                checked_page(p, is_v ? entries[0] : entries[kSB]));
                 }
+                if (i < u.ntiles) ++ik;
+                if (i >= kSB) ++iv;
             }
         }
         if (lane == 0) {

@@ -163,7 +163,7 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
             auto copy_tile = [&](int j, int entry, bool is_v) -> bool {
                 const int key0 = (u.tile0 + j) * kKvTile;
                 const int slot0 = p.ps < kKvTile ? 0 : p.ps_shift >= 0 ? key0 & (p.ps - 1) : key0 % p.ps;
-                const bool mine = lane_copies(p, u, j);
+                const bool mine = lane < 16 && page_copied(p, u, j, lane);
                 const unsigned who = __ballot_sync(0xffffffffu, mine);
                 const uint32_t bytes = (uint32_t)(__popc(who) * box_rows * 256);
 #pragma unroll
