@@ -585,18 +585,21 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
 // Merges the pieces of the units that CTA ranges cut: with weighted sums o_i,
 // row sums l_i and bases m_i, M = max m_i, out = sum 2^(m_i - M) o_i /
 // sum 2^(m_i - M) l_i.  The pieces of the unit whose first one ended CTA c's
-// range opened the following ranges.  One warp per row, eight rows of that unit
+// range opened the following ranges.  One warp per row, four rows of that unit
 // to block (chunk, c); lanes share the pieces' bases, and the rows of O come
 // four pieces at a time, so that a row costs three dependent reads whatever the
 // number of pieces (four rows to a warp, a piece after the other, took 6.5 us
 // where this takes 2).
+constexpr int kMergeThreads = 128;   // a block fits beside an attention CTA's registers: it is there when that ends
+
 template <int D, int NT>
-__global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__ TreeParams p) {
+__global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_constant__ TreeParams p) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // The rows past a request's drafts: zeros and -inf, a warp to a draft.  They
     // wait for nothing.
-    const int nwarps = gridDim.x * gridDim.y * 8;
-    for (int i = (blockIdx.y * gridDim.x + blockIdx.x) * 8 + warp; i < p.B * p.T; i += nwarps) {
+    constexpr int kWarps = kMergeThreads / 32;
+    const int nwarps = gridDim.x * gridDim.y * kWarps;
+    for (int i = (blockIdx.y * gridDim.x + blockIdx.x) * kWarps + warp; i < p.B * p.T; i += nwarps) {
         const int b = i / p.T, pt = i - b * p.T;
         int n, d;
         tree_row(p, b, n, d);
@@ -610,8 +613,8 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__
     }
     pdl_wait();                                      // the pieces are written
     const TreeCut cut = p.cuts[blockIdx.y];
-    const int x = blockIdx.x / 16;
-    const int row = (blockIdx.x & 15) * 8 + warp;
+    const int x = blockIdx.x / (128 / kWarps);
+    const int row = blockIdx.x % (128 / kWarps) * kWarps + warp;
     int t, h;
     if (cut.count == 0 || x >= cut.nrt || !tree_tile_row(p, cut.rt0 + x, cut.g, cut.d, row, t, h)) return;
     const int step = p.ride ? p.Hkv : 1;
@@ -684,10 +687,10 @@ cudaError_t launch_bf16(const TreeParams &p, const CUtensorMap &tq, const CUtens
 }  // namespace
 
 cudaError_t launch_tree_merge(const TreeParams &p, int row_tiles, cudaStream_t stream) {
-    const dim3 grid(row_tiles * 16, p.grid);
-    if (p.D == 256) return launch_after_previous(tree_merge_kernel<256, 1>, grid, dim3(256), 0, stream, p);
-    if (row_tiles == 2) return launch_after_previous(tree_merge_kernel<128, 2>, grid, dim3(256), 0, stream, p);
-    return launch_after_previous(tree_merge_kernel<128, 1>, grid, dim3(256), 0, stream, p);
+    const dim3 grid(row_tiles * (128 / (kMergeThreads / 32)), p.grid), block(kMergeThreads);
+    if (p.D == 256) return launch_after_previous(tree_merge_kernel<256, 1>, grid, block, 0, stream, p);
+    if (row_tiles == 2) return launch_after_previous(tree_merge_kernel<128, 2>, grid, block, 0, stream, p);
+    return launch_after_previous(tree_merge_kernel<128, 1>, grid, block, 0, stream, p);
 }
 
 size_t tree_workspace_bytes(int head_dim, int grid) {
