@@ -1107,7 +1107,7 @@ static fw_status_t build_tree(const fw_tensor_t *q, const fw_tensor_t *k_cache, 
         p.row_tiles = p.T * p.head_chunks;
     }
     p.min_span = fw::kTreeMinSpan;
-    p.piece_cost = fw::kTreePieceCost;
+    p.piece_cost = kv8 || (D == 128 && p.row_tiles > 1) ? fw::kTreePieceCost : fw::kTreePieceCostOne;
     *tp = p;
     return FW_OK;
 }

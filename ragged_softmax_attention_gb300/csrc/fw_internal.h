@@ -44,8 +44,15 @@ constexpr int kLatentMinSpan = 32;    // latent-head decode: the same, for its h
 // carry equal work, piece starts included.
 constexpr int kDecodePieceCostBf16 = 4;
 constexpr int kDecodePieceCostFp8 = 5;
-constexpr int kTreeMinSpan = 2;       // tree decode: fewest KV tiles (and empty slots) one CTA range holds
-constexpr int kTreePieceCost = 3;     // tree decode: empty slots before a unit's tiles
+constexpr int kTreeMinSpan = 2;       // tree decode: fewest KV tiles (and empty slots) one CTA range holds (4: a
+                                      // 700-key request takes 17.0 us instead of 14.1)
+// Tree decode: empty slots before a unit's tiles.  One row tile over a BF16
+// cache streams a tile in 1.4 us, and starting a unit costs about as much (16
+// ragged requests, hd 128: 56.6 us at 1 slot, 57.9 at 3, 58.5 at 5); an FP8 tile
+// takes half of that (144 us at 1, 139 at 5), and two row tiles share a unit's
+// longer start and end (121-draft trees: 146 at 1, 141 at 5).
+constexpr int kTreePieceCostOne = 1;
+constexpr int kTreePieceCost = 5;
 constexpr int kMaxTableRows = 8192;   // page tables: requests whose sums fit a block's shared memory
 constexpr int kLatentRows = 64;       // latent-head decode: query heads per CTA (MMA N of one CTA)
 constexpr int kLatentPairRows = 128;  // latent-head decode on CTA pairs: query heads per pair
