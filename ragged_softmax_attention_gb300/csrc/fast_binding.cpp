@@ -82,6 +82,28 @@ at::Tensor empty(at::IntArrayRef shape, at::ScalarType type, int device) {
     return at::empty(shape, at::TensorOptions().dtype(type).device(at::kCUDA, (c10::DeviceIndex)device));
 }
 
+// Contiguous int32 outputs of one call, cut from one allocation: taking a buffer
+// from torch's allocator costs the host as much as a quarter of a launch, and
+// these calls are as short as that.
+struct Outputs {
+    at::Tensor buffer;
+    int64_t used = 0;
+
+    static int64_t room(int64_t n) { return (n + 63) / 64 * 64; }      // 256-byte pieces
+    Outputs(int64_t total, int device) {
+        if (total > 0) buffer = empty({total}, at::kInt, device);
+    }
+    at::Tensor cut(at::IntArrayRef shape) {
+        int64_t n = 1;
+        for (const int64_t s : shape) n *= s;
+        auto impl = c10::make_intrusive<c10::TensorImpl>(c10::Storage(buffer.storage()), buffer.key_set(), buffer.dtype());
+        impl->set_storage_offset(used);
+        impl->set_sizes_contiguous(shape);
+        used += room(n);
+        return at::Tensor(std::move(impl));
+    }
+};
+
 // The current stream of the call's device, which is current while this lives.
 struct Where {
     c10::cuda::CUDAGuard guard;
@@ -182,8 +204,10 @@ PyObject *tree_mask(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (par.dim() != 2) raise(PyExc_ValueError, "parents must be [B, T]");
     Where where(args.device);
     const int64_t B = par.size(0), T = par.size(1);
-    if (!mask.defined()) mask = empty({B, T, (T + 31) / 32}, at::kInt, args.device);
-    if (!depths.defined()) depths = empty({B, T}, at::kInt, args.device);
+    const int64_t W = (T + 31) / 32;
+    Outputs outs((mask.defined() ? 0 : Outputs::room(B * T * W)) + (depths.defined() ? 0 : Outputs::room(B * T)), args.device);
+    if (!mask.defined()) mask = outs.buffer.defined() ? outs.cut({B, T, W}) : empty({B, T, W}, at::kInt, args.device);
+    if (!depths.defined()) depths = outs.buffer.defined() ? outs.cut({B, T}) : empty({B, T}, at::kInt, args.device);
     fw_tensor_t *v0 = args.add(par), *v1 = args.add(dl), *v2 = args.add(mask), *v3 = args.add(depths);
     if (failed(g_mask(v0, v1, v2, v3, where.stream()))) return nullptr;
     return pair(mask, depths);
@@ -209,9 +233,13 @@ PyObject *build_page_tables(PyObject *, PyObject *const *a, Py_ssize_t n) {
     }
     Where where(args.device);
     const int64_t B = t[0].numel();
-    if (!t[8].defined()) t[8] = empty({B + 1}, at::kInt, args.device);
-    if (!t[9].defined()) t[9] = empty({B}, at::kInt, args.device);
-    if (!t[10].defined()) t[10] = empty({2}, at::kInt, args.device);
+    int64_t total = 0;
+    const int64_t sizes[3] = {B + 1, B, 2};
+    for (int i = 0; i < 3; ++i)
+        if (!t[8 + i].defined()) total += Outputs::room(sizes[i]) + 64;
+    Outputs outs(total, args.device);
+    for (int i = 0; i < 3; ++i)
+        if (!t[8 + i].defined()) t[8 + i] = outs.cut({sizes[i]});
     fw_tensor_t *v[11];
     for (int i = 0; i < 11; ++i) v[i] = i == 5 ? nullptr : args.add(t[i]);
     if (failed(g_tables(v[0], v[1], v[2], v[3], v[4], page_size, v[6], v[7], v[8], v[9], v[10], where.stream())))
