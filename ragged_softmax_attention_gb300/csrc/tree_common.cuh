@@ -13,8 +13,6 @@ namespace fw {
 namespace tree {
 
 using dec::ceil_div_i;
-using dec::warp_max;
-using dec::warp_sum;
 using dec::warp_wait;
 constexpr float kNegInf = -__builtin_huge_valf();
 // The base of a row's exponentials moves only when its maximum rose by more
@@ -348,45 +346,72 @@ __device__ __forceinline__ uint32_t seen_word(const uint32_t *words, int w) {
     return words[w] | words[4 + w] | words[8 + w] | words[12 + w];
 }
 
+// A piece's partial rows: 16-byte units of four columns, the rows of a unit side by
+// side, so that a warp whose lanes are rows writes and reads whole lines.  (Row by
+// row, 32 lanes touch 32 lines a store, and a piece's end took 8,000 cycles.)
+template <int D, int NT>
+__device__ __forceinline__ float4 *part_unit(const TreeParams &p, int64_t slot, int unit, int row) {
+    return reinterpret_cast<float4 *>(p.part_o) + (slot * (D / 4) + unit) * (NT * 128) + row;
+}
+
 // This thread's row of a finished piece: its output and LSE, or its partial.
 // `load` reads 32 columns of O (warp-collective); columns 32 c0 .. 32 c1.
 template <int D, int NT, typename Load>
 __device__ __forceinline__ void write_row(const TreeParams &p, const TreeUnit &u, int x, int row, bool live, int t,
                                           int h, float base2, float l_sum, Load load, int c0 = 0,
                                           int c1 = D / 32) {
+    const int lane = threadIdx.x & 31;
     const float inv = l_sum > 0.f ? p.out_scale / l_sum : 0.f;
-    __nv_bfloat16 *orow = reinterpret_cast<__nv_bfloat16 *>(p.out) + u.b * p.out_stride[0] + t * p.out_stride[1] +
-                          h * p.out_stride[2];
-    const int64_t prow = (int64_t)u.part * (NT * 128) + x * 128 + row;
-    float4 *part = reinterpret_cast<float4 *>(p.part_o + prow * D);
+    // Outputs: four lanes exchange their rows' four 16-byte units of a chunk, so that
+    // each store writes 64 bytes of a row.
+    const long long at = live ? u.b * p.out_stride[0] + t * p.out_stride[1] + h * p.out_stride[2] : -1;
+    long long to[4];
+    if (u.part < 0) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) to[k] = __shfl_sync(0xffffffffu, at, (lane & ~3) + k);
+    }
 #pragma unroll 1
     for (int c = c0; c < c1; ++c) {
         float o[32];
         load(c, o);
-        if (!live) continue;
         if (u.part < 0) {
+            uint32_t v[4][4];
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                uint4 v;
-                v.x = l_sum > 0.f ? pack_bf16x2(o[8 * w + 0] * inv, o[8 * w + 1] * inv) : 0u;
-                v.y = l_sum > 0.f ? pack_bf16x2(o[8 * w + 2] * inv, o[8 * w + 3] * inv) : 0u;
-                v.z = l_sum > 0.f ? pack_bf16x2(o[8 * w + 4] * inv, o[8 * w + 5] * inv) : 0u;
-                v.w = l_sum > 0.f ? pack_bf16x2(o[8 * w + 6] * inv, o[8 * w + 7] * inv) : 0u;
-                *reinterpret_cast<uint4 *>(orow + c * 32 + w * 8) = v;
+            for (int w = 0; w < 4; ++w)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    v[w][i] = l_sum > 0.f ? pack_bf16x2(o[8 * w + 2 * i] * inv, o[8 * w + 2 * i + 1] * inv) : 0u;
+#pragma unroll
+            for (int s = 1; s <= 2; s <<= 1) {
+                const bool hi = lane & s;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (k & s) continue;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t got = __shfl_xor_sync(0xffffffffu, hi ? v[k][i] : v[k | s][i], s);
+                        if (hi) v[k][i] = got; else v[k | s][i] = got;
+                    }
+                }
             }
-        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (to[k] >= 0)
+                    *reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(p.out) + to[k] + c * 32 + (lane & 3) * 8) =
+                        make_uint4(v[k][0], v[k][1], v[k][2], v[k][3]);
+        } else if (live) {
 #pragma unroll
             for (int w = 0; w < 8; ++w)
-                part[c * 8 + w] = make_float4(o[4 * w], o[4 * w + 1], o[4 * w + 2], o[4 * w + 3]);
+                *part_unit<D, NT>(p, u.part, c * 8 + w, x * 128 + row) =
+                    make_float4(o[4 * w], o[4 * w + 1], o[4 * w + 2], o[4 * w + 3]);
         }
     }
     if (!live || c0 > 0) return;
-    if (u.part >= 0) p.part_ml[prow] = make_float2(base2, l_sum);
+    if (u.part >= 0) p.part_ml[(int64_t)u.part * (NT * 128) + x * 128 + row] = make_float2(base2, l_sum);
     else if (p.lse)
         p.lse[u.b * p.lse_stride[0] + t * p.lse_stride[1] + h * p.lse_stride[2]] =
             l_sum > 0.f ? (base2 + log2f(l_sum)) * 0.69314718055994531f : kNegInf;
 }
-
 
 // One launch for the pieces, one for the merge of cut units.
 template <typename Kernel>

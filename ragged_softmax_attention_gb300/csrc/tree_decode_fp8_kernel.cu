@@ -594,6 +594,11 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
                 const int buf = st % kSB;
                 const int key0 = (u.tile0 + j) * kKvTile;
                 const bool drafts = key0 + kKvTile > base;
+                uint32_t bits[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+                if (drafts) {
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) bits[w] = live ? draft_bits(mrow, key0 + 32 * w - base, u.d) : 0u;
+                }
                 mbar_wait(&s_full[x * kSB + buf], (st / kSB) & 1, wc);
                 tc_fence_after();
                 if (!warp_live) {                         // rows of padding: whatever lies there
@@ -610,11 +615,6 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
                     continue;
                 }
                 const uint32_t sa = tmem + lane_off + C::s_col(x, buf);
-                uint32_t bits[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
-                if (drafts) {
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) bits[w] = live ? draft_bits(mrow, key0 + 32 * w - base, u.d) : 0u;
-                }
                 // The row of S is read twice, for its maximum and for P, 64 keys at a
                 // time: two streams' softmax warps have no registers for all of it, and
                 // the rolled loops keep the code small.

@@ -451,14 +451,21 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
                 const int buf = steps % kSB;
                 const int key0 = (u.tile0 + j) * kKvTile;
                 const bool drafts = key0 + kKvTile > base;    // the tile reaches past the committed keys
+                // What the masks say of the tile, worked out while its scores are.
+                uint32_t mine = 0xffffffffu;                  // this warp's keys that somebody sees
+                uint32_t bits[4] = {0, 0, 0, 0};              // the keys this row sees
+                if (drafts) {
+                    uint32_t *words = seen_words + (x * 2 + (j & 1)) * 16;
+                    seen_keys(p, u, key0, row, 1 + x, words);
+                    mine = seen_word(words, q4);
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) bits[w] = live ? draft_bits(mrow, key0 + 32 * w - base, u.d) : 0u;
+                }
                 mbar_wait(&s_full[x * kSB + buf], (steps / kSB) & 1, wc);
                 tc_fence_after();
                 if (drafts) {
                     // Values of keys nobody sees must not meet a zero weight: they
-                    // may be NaN.  A key is seen when some draft's mask shows it.
-                    uint32_t *words = seen_words + (x * 2 + (j & 1)) * 16;
-                    seen_keys(p, u, key0, row, 1 + x, words);
-                    const uint32_t mine = seen_word(words, q4);       // this warp's keys
+                    // may be NaN.
                     if (__any_sync(0xffffffffu, !(mine >> lane & 1))) {
                         const uint32_t r = r0 + (uint32_t)(pos_v<kSB>(j, u.ntiles) * TS);
                         // A parity wait needs the slot's copy before V_j to have landed.
@@ -498,12 +505,10 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
                 tmem_wait_ld();
                 if (drafts) {
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        const uint32_t bits = live ? draft_bits(mrow, key0 + 32 * w - base, u.d) : 0u;
+                    for (int w = 0; w < 4; ++w)
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            if (!(bits >> i & 1)) sv[w * 32 + i] = kNegInf;
-                    }
+                            if (!(bits[w] >> i & 1)) sv[w * 32 + i] = kNegInf;
                 }
                 const float ext = max_of<kKvTile>(sv);
                 const float m_tile = live ? ext * scale : kNegInf;    // -inf when it sees none of these keys
@@ -585,21 +590,21 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
 // Merges the pieces of the units that CTA ranges cut: with weighted sums o_i,
 // row sums l_i and bases m_i, M = max m_i, out = sum 2^(m_i - M) o_i /
 // sum 2^(m_i - M) l_i.  The pieces of the unit whose first one ended CTA c's
-// range opened the following ranges.  One warp per row, four rows of that unit
-// to block (chunk, c); lanes share the pieces' bases, and the rows of O come
-// four pieces at a time, so that a row costs three dependent reads whatever the
-// number of pieces (four rows to a warp, a piece after the other, took 6.5 us
-// where this takes 2).
-constexpr int kMergeThreads = 128;   // a block fits beside an attention CTA's registers: it is there when that ends
+// range opened the following ranges.  Block (chunk, c) takes 32 rows of that
+// unit, a lane a row and a warp an eighth of the columns, as the pieces lie, four
+// pieces' bases, sums and columns read at once, and turns the result round in
+// shared memory.  The rows past a request's drafts are written here too.
+constexpr int kMergeThreads = 256;
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_constant__ TreeParams p) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // The rows past a request's drafts: zeros and -inf, a warp to a draft.  They
-    // wait for nothing.
-    constexpr int kWarps = kMergeThreads / 32;
-    const int nwarps = gridDim.x * gridDim.y * kWarps;
-    for (int i = (blockIdx.y * gridDim.x + blockIdx.x) * kWarps + warp; i < p.B * p.T; i += nwarps) {
+    constexpr int kUnits = D / 4 / (kMergeThreads / 32);   // 16-byte FP32 units of a warp's columns
+    __shared__ uint4 stage[32][D / 8 + 1];           // BF16 rows
+    __shared__ long long offset[32];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // Zeros and -inf, a warp to a draft; these wait for nothing.
+    const int nwarps = gridDim.x * gridDim.y * (kMergeThreads / 32);
+    for (int i = (blockIdx.y * gridDim.x + blockIdx.x) * (kMergeThreads / 32) + warp; i < p.B * p.T; i += nwarps) {
         const int b = i / p.T, pt = i - b * p.T;
         int n, d;
         tree_row(p, b, n, d);
@@ -613,66 +618,71 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
     }
     pdl_wait();                                      // the pieces are written
     const TreeCut cut = p.cuts[blockIdx.y];
-    const int x = blockIdx.x / (128 / kWarps);
-    const int row = blockIdx.x % (128 / kWarps) * kWarps + warp;
+    const int x = blockIdx.x / 4, row = (blockIdx.x & 3) * 32 + lane;
+    if (cut.count == 0 || x >= cut.nrt) return;
     int t, h;
-    if (cut.count == 0 || x >= cut.nrt || !tree_tile_row(p, cut.rt0 + x, cut.g, cut.d, row, t, h)) return;
+    const bool live = tree_tile_row(p, cut.rt0 + x, cut.g, cut.d, row, t, h);
+    if (!__syncthreads_or(live)) return;
     const int step = p.ride ? p.Hkv : 1;
-    auto slot_row = [&](int k) -> int64_t {
-        const int slot = k == 0 ? 2 * blockIdx.y + 1 : 2 * (blockIdx.y + k * step);
-        return (int64_t)slot * (NT * 128) + x * 128 + row;
-    };
-    constexpr int V = D / 128;                       // float4 per lane and piece
-    float acc[4 * V], l = 0.f, m = kNegInf;
+    auto slot = [&](int k) -> int64_t { return k == 0 ? 2 * blockIdx.y + 1 : 2 * (blockIdx.y + k * step); };
+    float4 acc[kUnits];
 #pragma unroll
-    for (int c = 0; c < 4 * V; ++c) acc[c] = 0.f;
-    for (int k0 = 0; k0 < cut.count; k0 += 32) {     // 32 pieces at a time, on a common base
-        const float2 ml = k0 + lane < cut.count ? p.part_ml[slot_row(k0 + lane)] : make_float2(kNegInf, 0.f);
-        const float mk = ml.y > 0.f ? ml.x : kNegInf;
-        const float mn = fmaxf(m, warp_max(mk));
-        if (mn == kNegInf) continue;                 // nothing visible so far
-        const float alpha = ex2_approx(m - mn);
-        const float w = ex2_approx(mk - mn);
-        l = l * alpha + warp_sum(ml.y > 0.f ? w * ml.y : 0.f);
-        m = mn;
+    for (int i = 0; i < kUnits; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f, m = kNegInf;
+    if (live) {
+        for (int k0 = 0; k0 < cut.count; k0 += 4) {
+            float2 ml[4];
+            float4 v[4][kUnits];
 #pragma unroll
-        for (int c = 0; c < 4 * V; ++c) acc[c] *= alpha;
-        const int nk = min(32, cut.count - k0);
-        for (int k = 0; k < nk; k += 4) {
-            float4 v[4][V];
+            for (int k = 0; k < 4; ++k) {
+                const int64_t sl = slot(min(k0 + k, cut.count - 1));
+                ml[k] = p.part_ml[sl * (NT * 128) + x * 128 + row];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float4 *src = reinterpret_cast<const float4 *>(p.part_o + slot_row(k0 + min(k + i, nk - 1)) * D);
-#pragma unroll
-                for (int c = 0; c < V; ++c) v[i][c] = src[c * 32 + lane];
+                for (int i = 0; i < kUnits; ++i) v[k][i] = *part_unit<D, NT>(p, sl, warp * kUnits + i, x * 128 + row);
             }
+            float mn = m;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float wk = __shfl_sync(0xffffffffu, w, min(k + i, 31));
-                if (k + i >= nk || wk == 0.f) continue;
+            for (int k = 0; k < 4; ++k)
+                if (ml[k].y > 0.f) mn = fmaxf(mn, ml[k].x);
+            if (mn == kNegInf) continue;             // nothing visible so far
+            const float alpha = ex2_approx(m - mn);
+            m = mn;
+            l *= alpha;
 #pragma unroll
-                for (int c = 0; c < V; ++c) {
-                    acc[4 * c + 0] = fmaf(wk, v[i][c].x, acc[4 * c + 0]);
-                    acc[4 * c + 1] = fmaf(wk, v[i][c].y, acc[4 * c + 1]);
-                    acc[4 * c + 2] = fmaf(wk, v[i][c].z, acc[4 * c + 2]);
-                    acc[4 * c + 3] = fmaf(wk, v[i][c].w, acc[4 * c + 3]);
+            for (int i = 0; i < kUnits; ++i) { acc[i].x *= alpha; acc[i].y *= alpha; acc[i].z *= alpha; acc[i].w *= alpha; }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (k0 + k >= cut.count || !(ml[k].y > 0.f)) continue;
+                const float w = ex2_approx(ml[k].x - m);
+                l = fmaf(w, ml[k].y, l);
+#pragma unroll
+                for (int i = 0; i < kUnits; ++i) {
+                    acc[i].x = fmaf(w, v[k][i].x, acc[i].x);
+                    acc[i].y = fmaf(w, v[k][i].y, acc[i].y);
+                    acc[i].z = fmaf(w, v[k][i].z, acc[i].z);
+                    acc[i].w = fmaf(w, v[k][i].w, acc[i].w);
                 }
             }
         }
     }
     const float inv = l > 0.f ? p.out_scale / l : 0.f;
-    __nv_bfloat16 *o = reinterpret_cast<__nv_bfloat16 *>(p.out) + cut.b * p.out_stride[0] + t * p.out_stride[1] +
-                       h * p.out_stride[2];
 #pragma unroll
-    for (int c = 0; c < V; ++c) {
-        uint2 v;
-        v.x = pack_bf16x2(acc[4 * c] * inv, acc[4 * c + 1] * inv);
-        v.y = pack_bf16x2(acc[4 * c + 2] * inv, acc[4 * c + 3] * inv);
-        reinterpret_cast<uint2 *>(o)[c * 32 + lane] = v;
+    for (int i = 0; i < kUnits; i += 2)
+        stage[lane][(warp * kUnits + i) / 2] =
+            make_uint4(pack_bf16x2(acc[i].x * inv, acc[i].y * inv), pack_bf16x2(acc[i].z * inv, acc[i].w * inv),
+                       pack_bf16x2(acc[i + 1].x * inv, acc[i + 1].y * inv), pack_bf16x2(acc[i + 1].z * inv, acc[i + 1].w * inv));
+    if (warp == 0) {
+        offset[lane] = live ? cut.b * p.out_stride[0] + t * p.out_stride[1] + h * p.out_stride[2] : -1;
+        if (live && p.lse)
+            p.lse[cut.b * p.lse_stride[0] + t * p.lse_stride[1] + h * p.lse_stride[2]] =
+                l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : kNegInf;
     }
-    if (lane == 0 && p.lse)
-        p.lse[cut.b * p.lse_stride[0] + t * p.lse_stride[1] + h * p.lse_stride[2]] =
-            l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : kNegInf;
+    __syncthreads();
+    for (int i = tid; i < 32 * (D / 8); i += kMergeThreads) {
+        const int r = i / (D / 8), c = i % (D / 8);
+        if (offset[r] >= 0)
+            reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(p.out) + offset[r])[c] = stage[r][c];
+    }
 }
 
 template <int D, int NT>
@@ -687,7 +697,7 @@ cudaError_t launch_bf16(const TreeParams &p, const CUtensorMap &tq, const CUtens
 }  // namespace
 
 cudaError_t launch_tree_merge(const TreeParams &p, int row_tiles, cudaStream_t stream) {
-    const dim3 grid(row_tiles * (128 / (kMergeThreads / 32)), p.grid), block(kMergeThreads);
+    const dim3 grid(row_tiles * 4, p.grid), block(kMergeThreads);
     if (p.D == 256) return launch_after_previous(tree_merge_kernel<256, 1>, grid, block, 0, stream, p);
     if (row_tiles == 2) return launch_after_previous(tree_merge_kernel<128, 2>, grid, block, 0, stream, p);
     return launch_after_previous(tree_merge_kernel<128, 1>, grid, block, 0, stream, p);
