@@ -326,6 +326,8 @@ fw_status_t fw_varlen_prefill(const fw_tensor_t *q, const fw_tensor_t *k, const 
  *
  * The draft tokens of request b take the last draft_lens[b] of its seq_lens[b]
  * keys, in the order of the tree's nodes (every parent before its children).
+ * Outputs must not share elements with inputs (but where said otherwise) or with
+ * one another, nor hold an element twice (an expanded view).
  * ---------------------------------------------------------------------------
  */
 
@@ -347,12 +349,19 @@ fw_status_t fw_varlen_prefill(const fw_tensor_t *q, const fw_tensor_t *k, const 
  * With d = draft_lens[b], n = seq_lens[b], draft t < d sees the keys 0 .. n - d - 1
  * and those keys n - d + j whose bit j is set.  Bits j >= d are ignored.  Rows
  * with no visible key, and rows t >= d (the padding, whose q is not used), get a
- * zero output and LSE = -inf.
+ * zero output and LSE = -inf.  A NaN that a row sees, in a key or its own q, makes
+ * the row and its LSE NaN.
  *
  * Keys that no row sees may hold anything, NaN and infinities included: scores
  * of hidden keys are dropped by selection.  The VALUES of a draft that some rows
  * of the request see and others do not must be finite, since a hidden one meets
  * a zero weight in the product.
+ *
+ * Arithmetic: products of BF16 values summed in FP32, weights rounded to BF16 for
+ * the product with V and summed unrounded.  Over an FP8 cache q is carried as the
+ * sum of two E4M3 terms on a power of two of its own per row (elements to within
+ * 2^-17 of the row's largest), V is widened to FP16 exactly, and weights are
+ * rounded to FP16.
  *
  * Supported: D in {128, 256} (FP8: 128), 1 <= T <= 256, B <= 4096, page sizes,
  * strides and alignment of fw_paged_decode; any Hq / Hkv.

@@ -361,7 +361,9 @@ __device__ __forceinline__ void write_row(const TreeParams &p, const TreeUnit &u
                                           int h, float base2, float l_sum, Load load, int c0 = 0,
                                           int c1 = D / 32) {
     const int lane = threadIdx.x & 31;
-    const float inv = l_sum > 0.f ? p.out_scale / l_sum : 0.f;
+    // (A NaN sum is not zero: a NaN that the row sees comes out as NaN.)
+    const bool some = l_sum != 0.f;
+    const float inv = some ? p.out_scale / l_sum : 0.f;
     // Outputs: four lanes exchange their rows' four 16-byte units of a chunk, so that
     // each store writes 64 bytes of a row.
     const long long at = live ? u.b * p.out_stride[0] + t * p.out_stride[1] + h * p.out_stride[2] : -1;
@@ -380,7 +382,7 @@ __device__ __forceinline__ void write_row(const TreeParams &p, const TreeUnit &u
             for (int w = 0; w < 4; ++w)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    v[w][i] = l_sum > 0.f ? pack_bf16x2(o[8 * w + 2 * i] * inv, o[8 * w + 2 * i + 1] * inv) : 0u;
+                    v[w][i] = some ? pack_bf16x2(o[8 * w + 2 * i] * inv, o[8 * w + 2 * i + 1] * inv) : 0u;
 #pragma unroll
             for (int s = 1; s <= 2; s <<= 1) {
                 const bool hi = lane & s;
@@ -410,7 +412,7 @@ __device__ __forceinline__ void write_row(const TreeParams &p, const TreeUnit &u
     if (u.part >= 0) p.part_ml[(int64_t)u.part * (NT * 128) + x * 128 + row] = make_float2(base2, l_sum);
     else if (p.lse)
         p.lse[u.b * p.lse_stride[0] + t * p.lse_stride[1] + h * p.lse_stride[2]] =
-            l_sum > 0.f ? (base2 + log2f(l_sum)) * 0.69314718055994531f : kNegInf;
+            some ? (base2 + log2f(l_sum)) * 0.69314718055994531f : kNegInf;
 }
 
 // One launch for the pieces, one for the merge of cut units.

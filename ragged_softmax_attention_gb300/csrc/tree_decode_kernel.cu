@@ -451,7 +451,13 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
                 const int buf = steps % kSB;
                 const int key0 = (u.tile0 + j) * kKvTile;
                 const bool drafts = key0 + kKvTile > base;    // the tile reaches past the committed keys
-                // What the masks say of the tile, worked out while its scores are.
+                // What the masks say of the tile, worked out while its scores are (131 us
+                // against 134 at 242 rows of dim 128).  At dim 256, where a step waits for
+                // the copies, after them: 99.8 us against 101.2 (8 requests, 24 rows).
+                if constexpr (D == 256) {
+                    mbar_wait(&s_full[x * kSB + buf], (steps / kSB) & 1, wc);
+                    tc_fence_after();
+                }
                 uint32_t mine = 0xffffffffu;                  // this warp's keys that somebody sees
                 uint32_t bits[4] = {0, 0, 0, 0};              // the keys this row sees
                 if (drafts) {
@@ -461,8 +467,10 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
 #pragma unroll
                     for (int w = 0; w < 4; ++w) bits[w] = live ? draft_bits(mrow, key0 + 32 * w - base, u.d) : 0u;
                 }
-                mbar_wait(&s_full[x * kSB + buf], (steps / kSB) & 1, wc);
-                tc_fence_after();
+                if constexpr (D != 256) {
+                    mbar_wait(&s_full[x * kSB + buf], (steps / kSB) & 1, wc);
+                    tc_fence_after();
+                }
                 if (drafts) {
                     // Values of keys nobody sees must not meet a zero weight: they
                     // may be NaN.
@@ -591,14 +599,17 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
 // row sums l_i and bases m_i, M = max m_i, out = sum 2^(m_i - M) o_i /
 // sum 2^(m_i - M) l_i.  The pieces of the unit whose first one ended CTA c's
 // range opened the following ranges.  Block (chunk, c) takes 32 rows of that
-// unit, a lane a row and a warp an eighth of the columns, as the pieces lie, four
-// pieces' bases, sums and columns read at once, and turns the result round in
-// shared memory.  The rows past a request's drafts are written here too.
+// unit, a lane a row and a warp an eighth of the columns, as the pieces lie, and
+// turns the result round in shared memory.  Four pieces are read at once; two at
+// dim 256, where a lane's share of a piece is twice as many registers (99.8 us
+// against 101.1 for a step of 8 requests, 24 rows).  The rows past a request's
+// drafts are written here too.
 constexpr int kMergeThreads = 256;
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_constant__ TreeParams p) {
     constexpr int kUnits = D / 4 / (kMergeThreads / 32);   // 16-byte FP32 units of a warp's columns
+    constexpr int kPieces = D == 256 ? 2 : 4;
     __shared__ uint4 stage[32][D / 8 + 1];           // BF16 rows
     __shared__ long long offset[32];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -630,11 +641,11 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
     for (int i = 0; i < kUnits; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     float l = 0.f, m = kNegInf;
     if (live) {
-        for (int k0 = 0; k0 < cut.count; k0 += 4) {
-            float2 ml[4];
-            float4 v[4][kUnits];
+        for (int k0 = 0; k0 < cut.count; k0 += kPieces) {
+            float2 ml[kPieces];
+            float4 v[kPieces][kUnits];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < kPieces; ++k) {
                 const int64_t sl = slot(min(k0 + k, cut.count - 1));
                 ml[k] = p.part_ml[sl * (NT * 128) + x * 128 + row];
 #pragma unroll
@@ -642,18 +653,18 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
             }
             float mn = m;
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (ml[k].y > 0.f) mn = fmaxf(mn, ml[k].x);
-            if (mn == kNegInf) continue;             // nothing visible so far
-            const float alpha = ex2_approx(m - mn);
+            for (int k = 0; k < kPieces; ++k)
+                if (ml[k].y != 0.f) mn = fmaxf(mn, ml[k].x);
+            const float mu = mn == kNegInf ? 0.f : mn;       // nothing visible so far, or NaN scores alone
+            const float alpha = ex2_approx(m - mu);
             m = mn;
             l *= alpha;
 #pragma unroll
             for (int i = 0; i < kUnits; ++i) { acc[i].x *= alpha; acc[i].y *= alpha; acc[i].z *= alpha; acc[i].w *= alpha; }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                if (k0 + k >= cut.count || !(ml[k].y > 0.f)) continue;
-                const float w = ex2_approx(ml[k].x - m);
+            for (int k = 0; k < kPieces; ++k) {
+                if (k0 + k >= cut.count || ml[k].y == 0.f) continue;
+                const float w = ex2_approx(ml[k].x - mu);
                 l = fmaf(w, ml[k].y, l);
 #pragma unroll
                 for (int i = 0; i < kUnits; ++i) {
@@ -665,7 +676,7 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
             }
         }
     }
-    const float inv = l > 0.f ? p.out_scale / l : 0.f;
+    const float inv = l != 0.f ? p.out_scale / l : 0.f;
 #pragma unroll
     for (int i = 0; i < kUnits; i += 2)
         stage[lane][(warp * kUnits + i) / 2] =
@@ -675,7 +686,7 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
         offset[lane] = live ? cut.b * p.out_stride[0] + t * p.out_stride[1] + h * p.out_stride[2] : -1;
         if (live && p.lse)
             p.lse[cut.b * p.lse_stride[0] + t * p.lse_stride[1] + h * p.lse_stride[2]] =
-                l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : kNegInf;
+                l != 0.f ? (m + log2f(l)) * 0.69314718055994531f : kNegInf;
     }
     __syncthreads();
     for (int i = tid; i < 32 * (D / 8); i += kMergeThreads) {

@@ -363,3 +363,78 @@ def test_a_cache_past_32_bit_offsets(fw):
     torch.cuda.synchronize()
     assert fw.device_status() == 0
     check(out, lse, spec.tree_attention(**x), D, "large cache")
+
+
+@pytest.mark.parametrize("D,kv8", [(128, False), (128, True), (256, False)])
+@pytest.mark.parametrize("T,Hq", [(9, 8), (70, 8)])
+def test_nan_stays_in_the_rows_that_see_it(fw, D, kv8, T, Hq):
+    """NaN in a query row, in a committed key (one KV head of one request) and in
+    the key of a draft some rows see: those rows are NaN, LSE too, all others
+    what they are without it; in rows of one piece and of many."""
+    Hkv, ps = 2, 64
+    x = make(3, T, Hq, Hkv, D, ps, [9000, 300, 5000], [T, T - 2, T], "tree", kv8=kv8, seed=41)
+    ref = spec.tree_attention(**x)
+    hit = torch.zeros(3, T, Hq, dtype=torch.bool)
+    y = {k: (v.clone() if isinstance(v, torch.Tensor) else v) for k, v in x.items()}
+
+    def spoil(b, pos, g):
+        k = y["k_cache"].view(torch.uint8 if kv8 else torch.int16)
+        k[int(x["block_table"][b, pos // ps]), pos % ps, g, 3] = 0x7f if kv8 else 0x7fff
+
+    y["q"][0, 1, 2, 7] = math.nan
+    y["q"][1, 3, 5, 0] = math.nan
+    hit[0, 1, 2] = hit[1, 3, 5] = True
+    spoil(1, 100, 1)
+    hit[1, :T - 2, Hq // 2:] = True
+    j = 4                                                     # a draft of request 2
+    spoil(2, 5000 - T + j, 0)
+    sees = (x["tree_mask"][2, :, j // 32].numpy().astype(np.int64) >> (j % 32)) & 1
+    hit[2, :, :Hq // 2] |= torch.from_numpy(sees.astype(bool))[:, None]
+    assert sees.any() and not sees.all()
+    out, lse = fw.paged_decode_tree(**on_gpu(y))
+    torch.cuda.synchronize()
+    assert fw.device_status() == 0
+    out, lse = out.cpu(), lse.cpu()
+    assert torch.isnan(out[hit]).all() and torch.isnan(lse[hit]).all()
+    out[hit] = torch.from_numpy(ref[0])[hit].to(torch.bfloat16)
+    lse[hit] = torch.from_numpy(ref[1])[hit].float()
+    check(out, lse, ref, D, "rows without NaN")
+
+
+def test_the_largest_batch(fw):
+    lens = [(7 * i) % 41 for i in range(4096)]
+    x = make(4096, 2, 2, 1, 128, 16, lens, [i % 3 for i in range(4096)], "chain", seed=43)
+    run_and_check(fw, x, "4096 requests")
+
+
+@pytest.mark.parametrize("kv8", [False, True])
+def test_pages_shared_by_requests(fw, kv8):
+    """One prompt's pages in several rows, and the same page twice in a row."""
+    x = make(4, 12, 8, 2, 128, 32, [500, 500, 700, 300], None, "tree", kv8=kv8, seed=45)
+    x["block_table"][1, :10] = x["block_table"][0, :10]
+    x["block_table"][2, :10] = x["block_table"][0, :10]
+    x["block_table"][3, 5] = x["block_table"][3, 2]
+    run_and_check(fw, x, "shared pages")
+
+
+def test_two_graphs_on_one_workspace(fw):
+    """Graphs captured with the same workspace, replayed one after another."""
+    xs = [on_gpu(make(3, 20, 40, 8, 128, 64, [2500 + 700 * i, 90, 3100], None, "tree", seed=47 + i)) for i in range(2)]
+    alone = [fw.paged_decode_tree(**x) for x in xs]
+    ws = torch.empty(fw.paged_decode_tree_workspace_size(128), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    graphs, got = [], []
+    for x in xs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got.append(fw.paged_decode_tree(**x, workspace=ws))
+        graphs.append(g)
+    for order in ((0, 1), (1, 0), (0, 0, 1)):
+        for i in order:
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        for i in (0, 1):
+            assert torch.equal(got[i][0], alone[i][0]) and torch.equal(got[i][1], alone[i][1])
+        for o, l in got:
+            o.zero_(), l.zero_()
+    assert fw.device_status() == 0
