@@ -982,6 +982,41 @@ static bool overlap(const fw_tensor_t *a, int64_t esz_a, const fw_tensor_t *b, i
     return pa < pb + extent_bytes(b, esz_b) && pb < pa + extent_bytes(a, esz_a);
 }
 
+// Whether two I32 tensors share an element.  Columns of one buffer have
+// interleaved extents and nothing in common: with equal row strides that the rows
+// fit in, what counts is where the rows start within a stride.
+static bool i32_share(const fw_tensor_t *a, const fw_tensor_t *b) {
+    if (!overlap(a, 4, b, 4)) return false;
+    if (a->ndim < 2 || b->ndim < 2 || a->stride[0] != b->stride[0] || a->stride[0] == 0) return true;
+    fw_tensor_t ra = *a, rb = *b;
+    ra.shape[0] = rb.shape[0] = 1;
+    const int64_t st = a->stride[0] * 4, ea = extent_bytes(&ra, 4), eb = extent_bytes(&rb, 4);
+    int64_t at = (static_cast<const char *>(b->data) - static_cast<const char *>(a->data)) % st;
+    if (at < 0) at += st;
+    return at < ea || st - at < eb;
+}
+
+// A tensor that is written holds every element once: each stride passes what the
+// shorter ones reach.
+static fw_status_t check_written(const fw_tensor_t *t, const char *name) {
+    if (!t) return FW_OK;
+    int order[5] = {0, 1, 2, 3, 4};
+    for (int i = 0; i < t->ndim; ++i) {
+        if (t->shape[i] == 0) return FW_OK;
+        for (int j = i + 1; j < t->ndim; ++j)
+            if (t->stride[order[j]] < t->stride[order[i]]) { const int x = order[i]; order[i] = order[j]; order[j] = x; }
+    }
+    int64_t reach = 1;
+    for (int i = 0; i < t->ndim; ++i) {
+        const int d = order[i];
+        if (t->shape[d] == 1) continue;
+        if (t->stride[d] < reach) return fail(FW_ERR_INVALID_ARG, "%s: written elements overlap (stride[%d] = %lld)", name,
+                                              d, (long long)t->stride[d]);
+        reach += (t->shape[d] - 1) * t->stride[d];
+    }
+    return FW_OK;
+}
+
 // Whether two [pages, ps, Hkv, D] caches share an element.  Views into one
 // buffer (K and V halves of every page, say) have interleaved extents and no
 // common element, so with equal strides the distance between the bases is
@@ -1063,6 +1098,8 @@ static fw_status_t build_tree(const fw_tensor_t *q, const fw_tensor_t *k_cache, 
         if (fw_status_t s = check_tma_layout(v_cache, "v_cache")) return s;
         if (fw_status_t s = check_tma_layout(out, "out")) return s;
         if (lse && reinterpret_cast<uintptr_t>(lse->data) % 4) return fail(FW_ERR_INVALID_ARG, "lse misaligned");
+        if (fw_status_t s = check_written(out, "out")) return s;
+        if (fw_status_t s = check_written(lse, "lse")) return s;
     }
     fw::TreeParams p{};
     p.B = (int)B; p.T = (int)T; p.Hq = (int)Hq; p.Hkv = (int)Hkv; p.G = (int)(Hq / Hkv); p.D = (int)D;
@@ -1200,6 +1237,12 @@ fw_status_t fw_tree_mask(const fw_tensor_t *parents, const fw_tensor_t *draft_le
         return fail(FW_ERR_INVALID_ARG, "depths must be [B, T]");
     if (B >= (1LL << 31)) return fail(FW_ERR_UNSUPPORTED, "too many trees");
     if (B == 0) return ok();
+    if (fw_status_t s = check_written(tree_mask, "tree_mask")) return s;
+    if (fw_status_t s = check_written(depths, "depths")) return s;
+    if (i32_share(tree_mask, parents) || (depths && i32_share(depths, parents)) ||
+        (draft_lens && (i32_share(tree_mask, draft_lens) || (depths && i32_share(depths, draft_lens)))))
+        return fail(FW_ERR_INVALID_ARG, "an output overlaps an input");
+    if (depths && i32_share(depths, tree_mask)) return fail(FW_ERR_INVALID_ARG, "depths overlaps tree_mask");
     fw::TreeMaskParams p{};
     p.B = (int)B; p.T = (int)T; p.W = (int)tree_mask->shape[2];
     p.parents = static_cast<const int32_t *>(parents->data);
@@ -1250,13 +1293,14 @@ fw_status_t fw_build_page_tables(const fw_tensor_t *seq_lens, const fw_tensor_t 
         return fail(FW_ERR_UNSUPPORTED, "page tables of up to %d requests, not %lld", fw::kMaxTableRows, (long long)B);
     if (F < 1 || F > (1LL << 30)) return fail(FW_ERR_UNSUPPORTED, "a ring of 1 to 2^30 pages");
     if (N >= (1LL << 31) || max_pages > (1LL << 30)) return fail(FW_ERR_UNSUPPORTED, "too many places or table columns");
+    if (fw_status_t s = check_written(block_table, "block_table")) return s;
     const fw_tensor_t *outs[] = {block_table, slot_mapping, cu_new, held_out, range_out, free_queue};
     const fw_tensor_t *ins[] = {seq_lens, new_lens, held, free_range};
     const char *names[] = {"block_table", "slot_mapping", "cu_new", "held_out", "range_out", "free_queue"};
     for (int i = 0; i < 6; ++i) {
         if (!outs[i]) continue;
         for (int j = 0; j < 4; ++j) {
-            if ((i == 3 && j == 2) || (i == 4 && j == 3)) continue;     // these may be their inputs
+            if (((i == 3 && j == 2) || (i == 4 && j == 3)) && outs[i]->data == ins[j]->data) continue;  // the same vector
             if (overlap(outs[i], 4, ins[j], 4))
                 return fail(FW_ERR_INVALID_ARG, "%s overlaps an input", names[i]);
         }
@@ -1331,8 +1375,10 @@ fw_status_t fw_kv_commit(const fw_tensor_t *path, const fw_tensor_t *path_lens, 
     if (Hkv * (Dk + Dv) > (1LL << 24) || B >= (1LL << 31)) return fail(FW_ERR_UNSUPPORTED, "rows or batch too large");
     if (A > 256) return fail(FW_ERR_UNSUPPORTED, "paths of up to 256 drafts, not %lld", (long long)A);
     if (fw_status_t s = check_tma_layout(k_cache, "k_cache")) return s;
+    if (fw_status_t s = check_written(k_cache, "k_cache")) return s;
     if (v_cache) {
         if (fw_status_t s = check_tma_layout(v_cache, "v_cache")) return s;
+        if (fw_status_t s = check_written(v_cache, "v_cache")) return s;
         if (caches_share(k_cache, v_cache, esz))
             return fail(FW_ERR_INVALID_ARG, "v_cache shares elements with k_cache: move the keys alone (v_cache NULL)");
     }

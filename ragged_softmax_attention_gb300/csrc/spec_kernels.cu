@@ -458,14 +458,17 @@ cudaError_t launch_tree_mask(const TreeMaskParams &p, cudaStream_t stream) {
 cudaError_t launch_page_tables(const PageTableParams &p, cudaStream_t stream, int *launches) {
     *launches = 0;
     const size_t smem = ((size_t)5 * p.B + 3) * sizeof(int);
-    static bool configured = false;
-    if (!configured) {
+    static bool configured[64] = {};                 // by device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (!configured[dev & 63]) {
         const int most = (5 * kMaxTableRows + 3) * (int)sizeof(int);
-        cudaError_t e = cudaFuncSetAttribute(page_table_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+        e = cudaFuncSetAttribute(page_table_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
         if (e == cudaSuccess)
             e = cudaFuncSetAttribute(page_table_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
         if (e != cudaSuccess) return e;
-        configured = true;
+        configured[dev & 63] = true;
     }
     // A place to a thread as long as the GPU's blocks have enough of them (the
     // shortest way for the maps of a decode step); beyond, octets where they can
@@ -483,7 +486,7 @@ cudaError_t launch_page_tables(const PageTableParams &p, cudaStream_t stream, in
     // written by a launch that waits for the fill.
     const bool split = p.in_place && grid > 1;
     page_table_kernel<true><<<grid, threads, smem, stream>>>(p, split ? 0 : 1, octets);
-    cudaError_t e = cudaGetLastError();
+    e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     ++*launches;
     if (split) {

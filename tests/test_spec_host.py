@@ -61,6 +61,9 @@ def setter(name, value):
     (setter("out", fake([2, 5, 8, 128], BF, strides=[5 * 8 * 132, 8 * 132, 132, 1])), INVALID),
     (setter("lse", fake([2, 5, 7], F32)), INVALID),
     (setter("lse", fake([2, 5, 8], BF)), INVALID),
+    (setter("out", fake([2, 5, 8, 128], BF, strides=[0, 1024, 128, 1])), INVALID),         # rows written twice
+    (setter("out", fake([2, 5, 8, 128], BF, strides=[5120, 1024, 64, 1])), INVALID),
+    (setter("lse", fake([2, 5, 8], F32, strides=[40, 0, 1])), INVALID),
     (setter("q", fake([2, 5, 8, 128], BF, ptr=0x10004)), INVALID),
     (setter("k", fake([10, 16, 2, 128], BF, strides=[16 * 260, 260, 130, 1])), INVALID),
 ])
@@ -100,6 +103,13 @@ def test_tree_mask_refusals(fwlib):  # noqa: F811
     assert call_mask(fwlib, p, d, fake([2, 40, 1], I32), e) == INVALID
     assert call_mask(fwlib, p, d, m, fake([2, 39], I32)) == INVALID
     assert call_mask(fwlib, p, d, fake([2, 40, 2], I32, strides=[160, 4, 2]), e) == INVALID
+    p, d, m, e = at([2, 40], I32, 0x10000), at([2], I32, 0x20000), at([2, 40, 2], I32, 0x30000), at([2, 40], I32, 0x40000)
+    assert call_mask(fwlib, p, d, at([2, 40, 2], I32, 0x30000, [0, 2, 1]), e) == INVALID
+    assert call_mask(fwlib, p, d, m, at([2, 40], I32, 0x40000, [39, 1])) == INVALID
+    assert call_mask(fwlib, p, d, m, p) == INVALID
+    assert call_mask(fwlib, p, d, at([2, 40, 2], I32, 0x10080), e) == INVALID
+    assert call_mask(fwlib, p, d, m, at([2, 40], I32, 0x30004)) == INVALID
+    assert call_mask(fwlib, p, d, m, at([2, 40], I32, 0x10000 + 4 * 39, [80, 1])) == INVALID
     assert call_mask(fwlib, fake([2, 257], I32), d, fake([2, 257, 9], I32), None) == UNSUPPORTED
     assert call_mask(fwlib, fake([2, 0], I32), d, fake([2, 0, 0], I32), None) == UNSUPPORTED
 
@@ -126,6 +136,9 @@ def call_tables(fw, a):
     setter("cu", at([4], I32, 0x80000)), setter("held_out", None), setter("range_out", at([1], I32, 0xa0000)),
     setter("slots", at([20], I32, 0x10000)),                                 # over seq_lens
     setter("held_out", at([4], I32, 0x20004)),                               # over new_lens
+    setter("held_out", at([4], I32, 0x30004)),                               # held, but for one entry
+    setter("range_out", at([2], I32, 0x50004)),
+    setter("bt", at([4, 6], I32, 0x60000, [0, 1])), setter("bt", at([4, 6], I32, 0x60000, [5, 1])),
     setter("cu", at([5], I32, 0x70000)),                                     # over the slots
     setter("queue", at([50], I32, 0x60010)),                                 # over the table
 ])
@@ -168,6 +181,7 @@ def call_commit(fw, a):
     (setter("v", fake([12, 16, 2, 128], BF, 0x100000)), INVALID),            # the keys themselves
     (setter("v", fake([12, 16, 2, 64], BF, 0x100080, [16 * 256, 256, 128, 1])), INVALID),   # a view of the keys
     (setter("v", fake([12, 16, 2, 128], BF, 0x900008)), INVALID),
+    (setter("k", fake([12, 16, 2, 128], BF, 0x900000, [0, 256, 128, 1])), INVALID),         # a page written many times
     (setter("path", fake([3, 257], I32, 0x1000)), UNSUPPORTED),
     (setter("new", fake([3], I32, 0x3004)), INVALID),                        # over base_lens
 ])
@@ -197,6 +211,8 @@ def test_valid_calls_without_a_gpu_fail_loudly(fwlib):  # noqa: F811
     same["held_out"], same["range_out"] = same["held"], same["range"]        # may be their inputs
     for rc in (call_tree(fwlib, tree_args()), call_tree(fwlib, tree_args(kv=E4M3)),
                call_mask(fwlib, fake([2, 40], I32), None, fake([2, 40, 2], I32, 0x90000), None),
+               call_mask(fwlib, at([2, 40], I32, 0x10000, [80, 1]), None, fake([2, 40, 2], I32, 0x90000),
+                         at([2, 40], I32, 0x10000 + 160, [80, 1])),       # columns of one buffer
                call_tables(fwlib, table_args()), call_tables(fwlib, table_args(L=5)), call_tables(fwlib, same),
                call_commit(fwlib, commit_args()), call_commit(fwlib, half)):
         assert rc in (2, 4), fwlib.load_library().fw_last_error()

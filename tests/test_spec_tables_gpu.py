@@ -230,6 +230,42 @@ def test_tables_of_nobody(fw):
     assert cu.tolist() == [0] and left.tolist() == [2, 3] and (slots == -1).all() and fw.device_status() == 0
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("leave", [False, True])
+def test_many_pages_for_few_places(fw, in_place, leave):
+    """Rows that take, or give back, hundreds of pages for a token each."""
+    B, width, ps = 150, 1400, 8
+    F = B * width + 5
+    held = [width if leave else 0] * B
+    bt = torch.full((B, width), -1, dtype=torch.int32)
+    if leave:
+        bt[:] = torch.arange(B * width, dtype=torch.int32).flip(0).view(B, width)
+    seq = [0 if leave and b % 3 else width * ps - b for b in range(B)]
+    x = dict(seq_lens=i32(seq), new_lens=i32([min(1, s) for s in seq]), held=i32(held),
+             free_queue=torch.arange(F, dtype=torch.int32), free_range=i32([F - 3, 4 if leave else F]), page_size=ps,
+             block_table=bt, slot_mapping=torch.zeros(B, 1, dtype=torch.int32))
+    run_tables(fw, x, status=0, in_place=in_place)
+
+
+def test_tables_on_two_streams(fw):
+    cases = [table_case(300, 16, 0, seed=21 + i, new=300) for i in range(2)]
+    refs = [spec.page_tables(**x) for x in cases]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    runs = []
+    for _ in range(6):
+        gs = [on_gpu(x) for x in cases]
+        torch.cuda.synchronize()
+        for g, s in zip(gs, streams):
+            runs.append((g, fw.build_page_tables(**g, held_out=g["held"], range_out=g["free_range"], stream=s)))
+    torch.cuda.synchronize()
+    assert fw.device_status() == 0
+    for i, (g, (cu, held, left)) in enumerate(runs):
+        bt, slots, cu_r, held_r, queue, left_r, _ = refs[i % 2]
+        assert torch.equal(cu.cpu(), cu_r) and torch.equal(held.cpu(), held_r) and torch.equal(left.cpu(), left_r)
+        assert torch.equal(g["block_table"].cpu(), bt) and torch.equal(g["slot_mapping"].cpu(), slots)
+        assert torch.equal(g["free_queue"].cpu(), queue)
+
+
 # ---------------------------------------------------------------- path commit
 
 def commit_case(B, A, T, layers, Hkv, Dk, Dv, ps, kv8, seed, spare=2):
@@ -403,3 +439,74 @@ def test_speculative_steps_end_to_end(fw, kv8):
                 want = [torch.cat([raw(h[i]) for h in history[l][b]]) for i in (0, 1)]
                 assert n == want[0].shape[0]
                 assert torch.equal(rows[0], want[0]) and torch.equal(rows[1], want[1]), (step, l, b)
+
+
+def test_a_captured_step_equals_the_eager_one(fw):
+    """One graph of a whole step, state updated in place, replayed for steps of
+    other lengths, trees and queries, against eager calls on state of their own;
+    the cache, the tables and the outputs are equal bit for bit."""
+    r = random.Random(15)
+    g = torch.Generator().manual_seed(19)
+    B, T, Hq, Hkv, D, ps, layers, width, F = 6, 20, 8, 2, 128, 16, 2, 40, 260
+    bf = torch.bfloat16
+
+    def state():
+        return dict(kc=torch.zeros(layers * F, ps, Hkv, D, dtype=bf, device="cuda"),
+                    vc=torch.zeros(layers * F, ps, Hkv, D, dtype=bf, device="cuda"),
+                    table=torch.full((B, width), -1, dtype=torch.int32, device="cuda"),
+                    held=torch.zeros(B, dtype=torch.int32, device="cuda"),
+                    ring=torch.arange(1, F, dtype=torch.int32, device="cuda"),
+                    left=i32([0, F - 1]).cuda(), slots=torch.zeros(B, T, dtype=torch.int32, device="cuda"),
+                    lens=torch.zeros(B, dtype=torch.int32, device="cuda"))
+
+    def step(s, x):
+        seq = s["lens"] + x["dl"]
+        mask, depths = fw.tree_mask(x["par"], draft_lens=x["dl"])
+        fw.build_page_tables(seq, x["dl"], s["held"], s["ring"], s["left"], ps, s["table"], s["slots"],
+                             held_out=s["held"], range_out=s["left"])
+        outs = [mask, depths]
+        for l in range(layers):
+            fw.kv_append(x["k"][l], x["v"][l], s["slots"], l * F * ps, s["kc"], s["vc"])
+            outs += fw.paged_decode_tree(x["q"], s["kc"][l * F:(l + 1) * F], s["vc"][l * F:(l + 1) * F], s["table"], seq,
+                                         mask, 0.09, draft_lens=x["dl"])
+        s["lens"].copy_(fw.kv_commit(x["path"], x["m"], s["lens"], s["table"], s["kc"], s["vc"], num_layers=layers))
+        return outs
+
+    def inputs(seed):
+        drafts = [r.randint(0, T) for _ in range(B)]
+        par = parents_of("tree", B, T, seed=seed)
+        path, m = torch.zeros(B, T, dtype=torch.int32), []
+        for b in range(B):
+            u, way = drafts[b] - 1, []
+            while u >= 0:
+                way.append(u)
+                u = int(par[b, u])
+            path[b, :len(way)] = i32(way[::-1])
+            m.append(len(way))
+        rnd = lambda *s: torch.randn(*s, generator=g).to(bf)
+        return {k: v.cuda() for k, v in dict(
+            par=par, dl=i32(drafts), path=path, m=i32(m), q=rnd(B, T, Hq, D), k=rnd(layers, B, T, Hkv, D),
+            v=rnd(layers, B, T, Hkv, D)).items()}
+
+    static = inputs(0)
+    warm, graph_state, eager_state = state(), state(), state()
+    step(warm, static)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = step(graph_state, static)
+    for n in range(5):
+        x = inputs(n + 1)
+        for k in static:
+            static[k].copy_(x[k])
+        graph.replay()
+        want = step(eager_state, x)
+        torch.cuda.synchronize()
+        assert fw.device_status() == 0
+        for a, b in zip(captured, want):
+            assert torch.equal(a, b), n
+        for s in (graph_state, eager_state):
+            for k in ("kc", "vc"):                # row 0 of a layer takes every place without a token, in any order
+                s[k].view(layers, F, ps, Hkv, D)[:, 0, 0] = 0
+        for k in eager_state:
+            assert torch.equal(graph_state[k], eager_state[k]), (n, k)
