@@ -646,7 +646,9 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
             float4 v[kPieces][kUnits];
 #pragma unroll
             for (int k = 0; k < kPieces; ++k) {
-                const int64_t sl = slot(min(k0 + k, cut.count - 1));
+                ml[k] = make_float2(kNegInf, 0.f);
+                if (k0 + k >= cut.count) continue;
+                const int64_t sl = slot(k0 + k);
                 ml[k] = p.part_ml[sl * (NT * 128) + x * 128 + row];
 #pragma unroll
                 for (int i = 0; i < kUnits; ++i) v[k][i] = *part_unit<D, NT>(p, sl, warp * kUnits + i, x * 128 + row);
@@ -663,7 +665,7 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
             for (int i = 0; i < kUnits; ++i) { acc[i].x *= alpha; acc[i].y *= alpha; acc[i].z *= alpha; acc[i].w *= alpha; }
 #pragma unroll
             for (int k = 0; k < kPieces; ++k) {
-                if (k0 + k >= cut.count || ml[k].y == 0.f) continue;
+                if (ml[k].y == 0.f) continue;
                 const float w = ex2_approx(ml[k].x - mu);
                 l = fmaf(w, ml[k].y, l);
 #pragma unroll
