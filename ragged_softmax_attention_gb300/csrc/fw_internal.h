@@ -50,7 +50,8 @@ constexpr int kTreeMinSpan = 2;       // tree decode: fewest KV tiles (and empty
 // cache streams a tile in 1.4 us, and starting a unit costs about as much (16
 // ragged requests, hd 128: 56.6 us at 1 slot, 57.9 at 3, 58.5 at 5); an FP8 tile
 // takes half of that (144 us at 1, 139 at 5), and two row tiles share a unit's
-// longer start and end (121-draft trees: 146 at 1, 141 at 5).
+// longer start and end (121-draft trees: 146 at 1, 141 at 5; since pieces end
+// faster 3 .. 7 are within 1 us, FP8 136 at 3, 133 at 5, 132.6 at 7).
 constexpr int kTreePieceCostOne = 1;
 constexpr int kTreePieceCost = 5;
 constexpr int kMaxTableRows = 8192;   // page tables: requests whose sums fit a block's shared memory

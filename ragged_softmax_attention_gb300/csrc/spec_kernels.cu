@@ -19,7 +19,7 @@ constexpr int kErrWorkspace = 3;   // FW_ERR_WORKSPACE
 // which a tree of depth d finishes after ceil(log2 d) rounds.  The launch bounds
 // it: 1,024 trees of 121 nodes read 0.5 MB, write 2.4 MB.  (Walking up node by
 // node spends some 25 instructions a step, and a thread's step is its warp's:
-// 8.6 us at that size, against 5.)
+// 8.6 us at that size, against 4.1.)
 
 constexpr int kMaxTree = 256;
 
@@ -78,7 +78,9 @@ __global__ void __launch_bounds__(kMaxTree) tree_mask_kernel(const __grid_consta
 // of a list belongs to the last request whose prefix is <= k.  Every block
 // computes the three prefixes for itself, which takes less time than a second
 // launch that waits for a first, and writes one contiguous share of each list,
-// so that its searches span a few requests.
+// so that its searches span a few requests.  Measured: a decode step of 32 requests
+// 5.0 us, all of it latencies; the maps of 2,048 prompts (7.9 M places, 0.5 M pages)
+// 17.4 us, of which the sums take 3.6, the stores of 32 MB 8.
 
 struct TableRow {
     int seq, fresh, held, want;
@@ -389,7 +391,9 @@ __global__ void __launch_bounds__(kTableThreads) page_table_kernel(const __grid_
 // before it writes them, since row base + path[i + 3] is written later still, if
 // at all.  A block checks one request's path and looks its pages up once, then
 // takes every gridDim.y-th layer, two at a time: a thread has up to eight rows in
-// flight.
+// flight.  Measured: 192 requests, 6 accepted drafts, 32 layers of 8 heads of dim
+// 128, 101 MB read and written in 19.3 us, 0.77 of the measured copy rate; 8
+// requests in one layer 3.7 us, the launch and three dependent reads.
 
 constexpr int kCommitThreads = 256;
 constexpr int kCommitRows = 256;                     // longest path
