@@ -59,6 +59,16 @@ def test_mask_views_and_clamped_counts(fw):
     assert (buf[:, :, 4:] == 7).all() and (dep[:, :5] == 7).all() and (dep[:, 45:] == 7).all()
 
 
+def test_one_tree_for_every_request(fw):
+    """Parents as an expanded view, counts of their own."""
+    parents = parents_of("tree", 1, 50, 3)
+    drafts = i32([50, 0, 31, 32, 33, 1])
+    mask, depths = fw.tree_mask(parents.cuda().expand(6, -1), draft_lens=drafts.cuda())
+    torch.cuda.synchronize()
+    m, d = spec.tree_mask(parents.expand(6, -1), drafts)
+    assert fw.device_status() == 0 and torch.equal(mask.cpu(), m) and torch.equal(depths.cpu(), d)
+
+
 def test_bad_parents_are_reported_and_become_roots(fw):
     par = i32([[-1, 1, 0, 7, -2, 4], [-1, 0, 1, 2, 3, 99]])
     mask, depths = fw.tree_mask(par.cuda(), draft_lens=i32([6, 5]).cuda())
@@ -266,6 +276,18 @@ def test_tables_on_two_streams(fw):
         assert torch.equal(g["free_queue"].cpu(), queue)
 
 
+def test_pages_without_new_tokens(fw):
+    """Pages reserved ahead: no new token, no place."""
+    B, width, ps = 5, 8, 16
+    x = dict(seq_lens=i32([100, 0, 17, 128, 1]), new_lens=i32([0] * B), held=i32([0, 2, 0, 3, 1]),
+             free_queue=torch.arange(100, 140, dtype=torch.int32), free_range=i32([35, 30]), page_size=ps,
+             block_table=torch.arange(B * width, dtype=torch.int32).view(B, width),
+             slot_mapping=torch.empty(0, dtype=torch.int32))
+    run_tables(fw, x, status=0)
+    x["slot_mapping"] = torch.empty(B, 0, dtype=torch.int32)
+    run_tables(fw, x, status=0, in_place=True)
+
+
 # ---------------------------------------------------------------- path commit
 
 def commit_case(B, A, T, layers, Hkv, Dk, Dv, ps, kv8, seed, spare=2):
@@ -340,6 +362,15 @@ def test_bad_paths_leave_the_cache(fw):
     assert fw.device_status() == 1
     assert new.tolist() == [int(new_ref[0])] + base[1:].tolist()
     assert torch.equal(dk.cpu(), refs[0]) and torch.equal(dv.cpu(), refs[1])
+
+
+def test_commit_of_nothing(fw):
+    path, lens, base, bt, k, v = commit_case(4, 3, 9, 2, 2, 128, 128, 16, False, seed=9)
+    dk, dv = k.cuda(), v.cuda()
+    new = fw.kv_commit(path[:, :0].cuda(), torch.zeros_like(lens).cuda(), base.cuda(), bt.cuda(), dk, dv, num_layers=2)
+    torch.cuda.synchronize()
+    assert fw.device_status() == 0 and torch.equal(new.cpu(), base)
+    assert torch.equal(raw(dk).cpu(), raw(k)) and torch.equal(raw(dv).cpu(), raw(v))
 
 
 # ------------------------------------------------------------- a whole step

@@ -438,3 +438,76 @@ def test_two_graphs_on_one_workspace(fw):
         for o, l in got:
             o.zero_(), l.zero_()
     assert fw.device_status() == 0
+
+
+@pytest.mark.parametrize("D,kv8", [(128, False), (128, True), (256, False)])
+@pytest.mark.parametrize("T", [5, 70])
+def test_pages_that_are_no_power_of_two(fw, D, kv8, T):
+    x = make(2, T, 8, 2, D, 384, [1500, 385], [T, T - 1], "tree", kv8=kv8, seed=51)
+    run_and_check(fw, x, "384-slot pages")
+
+
+@pytest.mark.parametrize("Hq,Hkv,T", [(160, 1, 3), (300, 2, 2), (128, 1, 6), (7, 1, 40)])
+def test_fp8_odd_groups(fw, Hq, Hkv, T):
+    run_and_check(fw, make(2, T, Hq, Hkv, 128, 16, [700, 130], None, "noise", kv8=True, seed=53), "odd groups")
+
+
+def test_fp8_strided_views(fw):
+    """K and V the halves of one 8-bit cache, Q and out inside wider buffers."""
+    x = make(2, 7, 8, 2, 128, 32, [100, 260], [7, 5], "tree", kv8=True, seed=55)
+    g = on_gpu(x)
+    kv = torch.stack([g["k_cache"].view(torch.uint8), g["v_cache"].view(torch.uint8)], 3).view(torch.float8_e4m3fn)
+    q = torch.full((2, 9, 16, 128), math.nan, dtype=torch.bfloat16, device="cuda")
+    q[:, 1:8, 4:12] = g["q"]
+    obuf = torch.full((2, 9, 10, 160), 7.0, dtype=torch.bfloat16, device="cuda")
+    g.update(q=q[:, 1:8, 4:12], k_cache=kv[:, :, :, 0], v_cache=kv[:, :, :, 1])
+    out, lse = fw.paged_decode_tree(**g, out=obuf[:, 1:8, 1:9, 16:144])
+    torch.cuda.synchronize()
+    assert fw.device_status() == 0
+    check(out, lse, spec.tree_attention(**x), 128, "FP8 views")
+    keep = torch.ones_like(obuf, dtype=torch.bool)
+    keep[:, 1:8, 1:9, 16:144] = False
+    assert (obuf[keep] == 7).all(), "written outside the output view"
+
+
+@pytest.mark.parametrize("kv8", [False, True])
+def test_expanded_inputs(fw, kv8):
+    """One tree and one table row for every request, as expanded views."""
+    x = make(1, 12, 8, 2, 128, 32, [500], None, "tree", kv8=kv8, seed=57)
+    B = 3
+    y = dict(x)
+    y["block_table"], y["tree_mask"] = x["block_table"].expand(B, -1), x["tree_mask"].expand(B, -1, -1)
+    y["seq_lens"] = torch.tensor([500, 100, 12], dtype=torch.int32)
+    y["q"] = torch.cat([x["q"], -x["q"], x["q"].flip(1)])
+    g = on_gpu(y)
+    g["block_table"], g["tree_mask"] = x["block_table"].cuda().expand(B, -1), x["tree_mask"].cuda().expand(B, -1, -1)
+    assert g["tree_mask"].stride(0) == 0 and g["block_table"].stride(0) == 0
+    out, lse = fw.paged_decode_tree(**g)
+    torch.cuda.synchronize()
+    assert fw.device_status() == 0
+    check(out, lse, spec.tree_attention(**y), 128, "expanded")
+
+
+@pytest.mark.parametrize("D,kv8", [(128, False), (128, True), (256, False)])
+def test_nobody_drafts(fw, D, kv8):
+    x = on_gpu(make(3, 9, 8, 2, D, 16, [100, 0, 7], [0, 5, -3], "tree", kv8=kv8, seed=59))
+    out = torch.full((3, 9, 8, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    _, lse = fw.paged_decode_tree(**x, out=out)
+    torch.cuda.synchronize()
+    assert fw.device_status() == 0 and (out == 0).all() and torch.isneginf(lse).all()
+
+
+def test_workspaces_that_do_not_fit(fw):
+    x = on_gpu(make(1, 4, 8, 2, 128, 16, [100], None, "tree", seed=61))
+    n = fw.paged_decode_tree_workspace_size(128)
+    ws = torch.empty(n + 256, dtype=torch.uint8, device="cuda")
+    before = fw.launch_count()
+    with pytest.raises(fw.FwError, match="workspace"):
+        fw.paged_decode_tree(**x, workspace=ws[:n - 1])
+    with pytest.raises(fw.FwError, match="aligned"):
+        fw.paged_decode_tree(**x, workspace=ws[16:])
+    with pytest.raises(ValueError, match="contiguous"):
+        fw.paged_decode_tree(**x, workspace=ws[::2])
+    with pytest.raises(ValueError, match="CUDA"):
+        fw.paged_decode_tree(**x, workspace=torch.empty(n, dtype=torch.uint8))
+    assert fw.launch_count() == before
