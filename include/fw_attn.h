@@ -440,8 +440,8 @@ fw_status_t fw_tree_mask(const fw_tensor_t *parents, const fw_tensor_t *draft_le
  * places, a page whose slots pass 2^31, a ring outside its array) record
  * FW_ERR_INVALID_ARG: such a request keeps its row and gets slots -1, tokens
  * without a place are dropped, pages the ring cannot take stay held, and a bad
- * range serves nobody.  B <= 8192.  One launch, two when held_out or range_out
- * overlap their inputs.  No workspace.
+ * range serves nobody.  B <= 8192, F and the places at most 2^30.  One launch, two
+ * when held_out or range_out are their inputs.  No workspace.
  */
 fw_status_t fw_build_page_tables(const fw_tensor_t *seq_lens, const fw_tensor_t *new_lens, const fw_tensor_t *held,
                                  fw_tensor_t *free_queue, const fw_tensor_t *free_range, int64_t page_size,
@@ -471,8 +471,8 @@ fw_status_t fw_build_page_tables(const fw_tensor_t *seq_lens, const fw_tensor_t 
  * A path that does not increase, reaches past the table row, or has a length
  * outside 0 .. A, and a page outside the layer, record FW_ERR_INVALID_ARG in the
  * device status word; that request's rows then stay as they are and its new
- * length is base_lens[b].  Two requests must not share a page that a path
- * touches.  One launch, no workspace.
+ * length is base_lens[b].  A page that a path touches must be in one place of one
+ * request's row.  A <= 256.  One launch, no workspace.
  */
 fw_status_t fw_kv_commit(const fw_tensor_t *path, const fw_tensor_t *path_lens, const fw_tensor_t *base_lens,
                          const fw_tensor_t *block_table, int64_t num_layers, fw_tensor_t *k_cache,

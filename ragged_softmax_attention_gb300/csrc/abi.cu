@@ -1292,7 +1292,7 @@ fw_status_t fw_build_page_tables(const fw_tensor_t *seq_lens, const fw_tensor_t 
     if (B > fw::kMaxTableRows)
         return fail(FW_ERR_UNSUPPORTED, "page tables of up to %d requests, not %lld", fw::kMaxTableRows, (long long)B);
     if (F < 1 || F > (1LL << 30)) return fail(FW_ERR_UNSUPPORTED, "a ring of 1 to 2^30 pages");
-    if (N >= (1LL << 31) || max_pages > (1LL << 30)) return fail(FW_ERR_UNSUPPORTED, "too many places or table columns");
+    if (N > (1LL << 30) || max_pages > (1LL << 30)) return fail(FW_ERR_UNSUPPORTED, "too many places or table columns");
     if (fw_status_t s = check_written(block_table, "block_table")) return s;
     const fw_tensor_t *outs[] = {block_table, slot_mapping, cu_new, held_out, range_out, free_queue};
     const fw_tensor_t *ins[] = {seq_lens, new_lens, held, free_range};

@@ -204,7 +204,7 @@ struct PageTableParams {
     const int32_t *range;
     int32_t *table; int64_t table_stride;
     int32_t *slots, *cu_new, *held_out, *range_out;
-    int in_place;                              // held_out / range_out overlap their inputs
+    int in_place;                              // held_out is held, or range_out free_range
     int num_sms;
     int *status;
 };

@@ -152,6 +152,9 @@ def test_page_table_sizes(fwlib):  # noqa: F811
     a = table_args()
     a["queue"] = at([0], I32, 0x40000)
     assert call_tables(fwlib, a) == UNSUPPORTED
+    a = table_args()
+    a["slots"] = at([2 ** 30 + 1], I32, 0x70000)
+    assert call_tables(fwlib, a) == UNSUPPORTED
     B = 8193
     a = table_args(B=B, width=0, N=1)
     for i, k in enumerate(("seq", "new", "held", "held_out", "slots", "cu")):
