@@ -352,10 +352,10 @@ fw_status_t fw_varlen_prefill(const fw_tensor_t *q, const fw_tensor_t *k, const 
  * zero output and LSE = -inf.  A NaN that a row sees, in a key or its own q, makes
  * the row and its LSE NaN.
  *
- * Keys that no row sees may hold anything, NaN and infinities included: scores
- * of hidden keys are dropped by selection.  The VALUES of a draft that some rows
- * of the request see and others do not must be finite, since a hidden one meets
- * a zero weight in the product.
+ * Hidden places may hold anything, NaN and infinities included: scores of hidden
+ * keys are dropped by selection, values that no row sees do not reach the product,
+ * and a draft's value that is not finite makes the rows that see the draft NaN (all
+ * columns, not their LSE) and leaves the others alone.
  *
  * Arithmetic: products of BF16 values summed in FP32, weights rounded to BF16 for
  * the product with V and summed unrounded.  Over an FP8 cache q is carried as the

@@ -346,6 +346,27 @@ __device__ __forceinline__ uint32_t seen_word(const uint32_t *words, int w) {
     return words[w] | words[4 + w] | words[8 + w] | words[12 + w];
 }
 
+// Values that are not finite.  A committed key's reach every row as they are.  Those
+// of a draft, which some rows see and others do not, must not meet the others' zero
+// weights: they are cleared before the products, and the rows that see that draft
+// come out as NaN.  A bit to a draft, in the words of unit k % kBadUnits; the unit
+// records keep a writer at most four units ahead of a reader.  Cleared when a unit
+// begins; the writers meet in seen_keys before the first bit.
+constexpr int kBadUnits = 5, kBadWords = 8;
+__device__ __forceinline__ void mark_bad(uint32_t *bad, int k, int draft) {
+    atomicOr(bad + k % kBadUnits * kBadWords + (draft >> 5), 1u << (draft & 31));
+}
+__device__ __forceinline__ bool sees_bad(const uint32_t *bad, const TreeUnit &u, int k, const int32_t *mrow) {
+    if ((u.tile0 + u.ntiles) * kKvTile <= u.n - u.d) return false;     // no drafts in this piece
+    const uint4 *words = reinterpret_cast<const uint4 *>(bad + k % kBadUnits * kBadWords);
+    const uint4 a = words[0], b = words[1];
+    if (__builtin_expect((a.x | a.y | a.z | a.w | b.x | b.y | b.z | b.w) == 0, 1)) return false;
+    uint32_t hit = 0;
+#pragma unroll 1
+    for (int w = 0; 32 * w < u.d; ++w) hit |= bad[k % kBadUnits * kBadWords + w] & (uint32_t)__ldg(mrow + w);
+    return hit != 0;
+}
+
 // A piece's partial rows: 16-byte units of four columns, the rows of a unit side by
 // side, so that a warp whose lanes are rows writes and reads whole lines.  (Row by
 // row, 32 lanes touch 32 lines a store, and a piece's end took 8,000 cycles.)
@@ -358,12 +379,13 @@ __device__ __forceinline__ float4 *part_unit(const TreeParams &p, int64_t slot, 
 // `load` reads 32 columns of O (warp-collective); columns 32 c0 .. 32 c1.
 template <int D, int NT, typename Load>
 __device__ __forceinline__ void write_row(const TreeParams &p, const TreeUnit &u, int x, int row, bool live, int t,
-                                          int h, float base2, float l_sum, Load load, int c0 = 0,
+                                          int h, float base2, float l_sum, bool poison, Load load,
+                                          int c0 = 0,
                                           int c1 = D / 32) {
     const int lane = threadIdx.x & 31;
     // (A NaN sum is not zero: a NaN that the row sees comes out as NaN.)
     const bool some = l_sum != 0.f;
-    const float inv = some ? p.out_scale / l_sum : 0.f;
+    const float inv = poison ? __int_as_float(0x7fc00000) : some ? p.out_scale / l_sum : 0.f;
     // Outputs: four lanes exchange their rows' four 16-byte units of a chunk, so that
     // each store writes 64 bytes of a row.
     const long long at = live ? u.b * p.out_stride[0] + t * p.out_stride[1] + h * p.out_stride[2] : -1;
@@ -402,6 +424,10 @@ __device__ __forceinline__ void write_row(const TreeParams &p, const TreeUnit &u
                     *reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(p.out) + to[k] + c * 32 + (lane & 3) * 8) =
                         make_uint4(v[k][0], v[k][1], v[k][2], v[k][3]);
         } else if (live) {
+            if (poison) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = inv;
+            }
 #pragma unroll
             for (int w = 0; w < 8; ++w)
                 *part_unit<D, NT>(p, u.part, c * 8 + w, x * 128 + row) =

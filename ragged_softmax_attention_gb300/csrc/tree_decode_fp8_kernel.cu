@@ -91,9 +91,10 @@ struct F8TreeCfg {
     static constexpr int kNumBars = kBarSchedEmpty + kSched;
     static constexpr int kOffSched = (kOffBar + kNumBars * 8 + 63) / 64 * 64;
     static constexpr int kOffSeen = kOffSched + kSched * 64;    // [2][16 words]
-    static constexpr int kOffPlan = kOffSeen + 128;
+    static constexpr int kOffBad = kOffSeen + 128;              // drafts whose values are NaN
+    static constexpr int kOffQScale = kOffBad + kBadUnits * kBadWords * 4;   // [kSched][NT][128 bytes]: exponents of the rows
+    static constexpr int kOffPlan = kOffQScale;                 // the plan is used up before the first of them
     static constexpr int kOffScan = kOffPlan + 32;              // [16]
-    static constexpr int kOffQScale = kOffScan + 128;           // [kSched][NT][128 halves]: exponents of the rows
     static constexpr int kOffBase = kOffQScale + kSched * NT * 128;   // NT = 1: [2][128] bases, [2][2][128] row sums
     static constexpr int kOffMisc = kOffBase + (NT == 1 ? 3072 : 0);
     static constexpr int kSmemBytes = kOffMisc + 16 + 1024;
@@ -169,6 +170,7 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
     uint64_t *sched_empty = bars + C::kBarSchedEmpty;
     TreeUnit *sched = reinterpret_cast<TreeUnit *>(smem + C::kOffSched);
     uint32_t *seen_words = reinterpret_cast<uint32_t *>(smem + C::kOffSeen);
+    uint32_t *bad = reinterpret_cast<uint32_t *>(smem + C::kOffBad);
     long long *plan = reinterpret_cast<long long *>(smem + C::kOffPlan);
     long long *scan = reinterpret_cast<long long *>(smem + C::kOffScan);
     float *bases = reinterpret_cast<float *>(smem + C::kOffBase);      // [2][128], NT = 1
@@ -468,6 +470,7 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
             __syncwarp();
             if (lane == 0) free_unit(k);
             if (u.b < 0) break;
+            if (row < kBadWords) bad[k % kBadUnits * kBadWords + row] = 0;
             mbar_wait(q_full, k & 1, wc);
             for (int x = 0; x < u.nrt; ++x) {
                 // BF16 row * 2^e = hi + mid, both E4M3, over the row's own bytes: 16 lanes
@@ -525,6 +528,30 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
                 if (drafts) seen_keys(p, u, key0, row, 3, words);
                 const uint32_t rl = i % C::kRSlots;
                 mbar_wait(&r_full[rl], (i / C::kRSlots) & 1, wc);
+                if (drafts) {
+                    // Values of keys nobody sees must not meet a zero weight: they may be
+                    // NaN; nor a draft's NaN the weights of rows that do not see it.  A
+                    // thread looks after one key, in the slot it landed in.
+                    const bool seen = seen_word(words, row >> 5) >> (row & 31) & 1;
+                    const int draft = key0 + row - base;
+                    uint4 *vr = reinterpret_cast<uint4 *>(sR + rl * C::kKBytes + row * 128);
+                    uint32_t wild = 0;                    // the bits of a NaN carry into the sign's place
+                    if (seen && draft >= 0) {
+#pragma unroll 1
+                        for (int c = 0; c < 8; ++c) {
+                            const uint4 w = vr[c ^ (row & 7)];
+                            wild |= ((w.x & 0x7f7f7f7fu) + 0x01010101u) | ((w.y & 0x7f7f7f7fu) + 0x01010101u) |
+                                    ((w.z & 0x7f7f7f7fu) + 0x01010101u) | ((w.w & 0x7f7f7f7fu) + 0x01010101u);
+                        }
+                        wild &= 0x80808080u;
+                        if (wild) mark_bad(bad, k, draft);
+                    }
+                    if (!seen || wild) {
+#pragma unroll 1
+                        for (int c = 0; c < 8; ++c) vr[c ^ (row & 7)] = make_uint4(0, 0, 0, 0);
+                    }
+                    named_bar_sync(3, 128);
+                }
                 // Keys key and 64 + key, columns 64 ch .. 64 ch + 63 of each.  (Rolled:
                 // unrolled, this and the softmax evict each other from the instruction
                 // cache, which more than doubled both.)
@@ -538,11 +565,6 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
                     uint4 w[4];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) w[c] = *reinterpret_cast<const uint4 *>(from + (((ch * 4 + c) ^ sw) << 4));
-                    // Values of keys nobody sees must not meet a zero weight: they may be NaN.
-                    if (drafts && !(seen_word(words, half * 2 + (key >> 5)) >> (key & 31) & 1)) {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) w[c] = make_uint4(0, 0, 0, 0);
-                    }
                     mbar_wait(&v_empty[sl], ((hv / C::kVSlots) & 1) ^ 1, wc);
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {         // 16 values: two units of FP16
@@ -723,7 +745,8 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
             }
             tc_fence_after();
             if (warp_live)
-                write_row<D, NT>(p, u, x, row, live, t, h, m_ref - kPShift, l_sum, [&](int c, float (&o)[32]) {
+                write_row<D, NT>(p, u, x, row, live, t, h, m_ref - kPShift, l_sum, live && sees_bad(bad, u, k, mrow),
+                                 [&](int c, float (&o)[32]) {
                     tmem_ld32(tmem + lane_off + C::o_col(x) + c * 32, o);
                     tmem_wait_ld();
                 }, NT == 1 ? 2 * wg : 0, NT == 1 ? 2 * wg + 2 : D / 32);

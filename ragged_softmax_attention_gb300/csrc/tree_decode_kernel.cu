@@ -74,8 +74,9 @@ struct TreeCfg {
     static constexpr int kBarSchedEmpty = kBarSchedFull + kSched;
     static constexpr int kNumBars = kBarSchedEmpty + kSched;
     static constexpr int kOffSched = (kOffBar + kNumBars * 8 + 63) / 64 * 64;
-    static constexpr int kOffSeen = kOffSched + kSched * 64;    // [NT][2][4 warps][4 words]
-    static constexpr int kOffPlan = kOffSeen + NT * 128;        // long long: total, start of row b0; int b0
+    static constexpr int kOffSeen = kOffSched + kSched * 64;    // [2][4 warps][4 words]
+    static constexpr int kOffBad = kOffSeen + 128;              // drafts whose values are not finite
+    static constexpr int kOffPlan = kOffBad + kBadUnits * kBadWords * 4;        // long long: total, start of row b0; int b0
     static constexpr int kOffScan = kOffPlan + 32;              // [12] warp sums
     static constexpr int kOffMisc = kOffScan + 96;
     static constexpr int kSmemBytes = kOffMisc + 16 + 1024;
@@ -116,6 +117,7 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
     uint64_t *sched_empty = bars + C::kBarSchedEmpty;
     TreeUnit *sched = reinterpret_cast<TreeUnit *>(smem + C::kOffSched);
     uint32_t *seen_words = reinterpret_cast<uint32_t *>(smem + C::kOffSeen);
+    uint32_t *bad = reinterpret_cast<uint32_t *>(smem + C::kOffBad);
     long long *plan = reinterpret_cast<long long *>(smem + C::kOffPlan);
     long long *scan = reinterpret_cast<long long *>(smem + C::kOffScan);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffMisc);
@@ -451,6 +453,7 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
             const uint32_t r0 = rp;
             rp += (uint32_t)(2 * u.ntiles * TS);
             if (x >= u.nrt) continue;
+            if (x == 0 && row < kBadWords) bad[k % kBadUnits * kBadWords + row] = 0;
             int t, h;
             const bool live = tree_tile_row(p, u.rt0 + x, u.g, u.d, row, t, h);
             const bool warp_live = __any_sync(0xffffffffu, live);
@@ -461,124 +464,167 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
                 const int buf = steps % kSB;
                 const int key0 = (u.tile0 + j) * kKvTile;
                 const bool drafts = key0 + kKvTile > base;    // the tile reaches past the committed keys
-                // What the masks say of the tile, worked out while its scores are (131 us
-                // against 134 at 242 rows of dim 128).  At dim 256, where a step waits for
-                // the copies, after them: 99.8 us against 101.2 (8 requests, 24 rows).
-                if constexpr (D == 256) {
-                    mbar_wait(&s_full[x * kSB + buf], (steps / kSB) & 1, wc);
-                    tc_fence_after();
-                }
-                uint32_t mine = 0xffffffffu;                  // this warp's keys that somebody sees
+                // What the masks say of the tile is worked out while its scores are (131 us
+                // against 134 at 242 rows).
+                // With drafts in the tile, stream 0 sees to its values, for both streams
+                // (stream 1's product follows stream 0's).
+                const bool values = drafts && x == 0;
+                uint32_t mine = 0;                            // this warp's keys that somebody sees
                 uint32_t bits[4] = {0, 0, 0, 0};              // the keys this row sees
                 if (drafts) {
-                    uint32_t *words = seen_words + (x * 2 + (j & 1)) * 16;
-                    seen_keys(p, u, key0, row, 1 + x, words);
-                    mine = seen_word(words, q4);
+                    if (x == 0) {
+                        uint32_t *words = seen_words + (j & 1) * 16;
+                        seen_keys(p, u, key0, row, 1, words);
+                        mine = seen_word(words, q4);
+                    }
 #pragma unroll
                     for (int w = 0; w < 4; ++w) bits[w] = live ? draft_bits(mrow, key0 + 32 * w - base, u.d) : 0u;
                 }
-                if constexpr (D != 256) {
-                    mbar_wait(&s_full[x * kSB + buf], (steps / kSB) & 1, wc);
-                    tc_fence_after();
-                }
-                if (drafts) {
-                    // Values of keys nobody sees must not meet a zero weight: they
-                    // may be NaN.
-                    if (__any_sync(0xffffffffu, !(mine >> lane & 1))) {
-                        const uint32_t r = r0 + (uint32_t)(pos_v<kSB>(j, u.ntiles) * TS);
-                        // A parity wait needs the slot's copy before V_j to have landed.
-                        // S_j there proves that for all copies up to K_j; with two slots
-                        // to a tile the one before V_j's may be V_{j-1}, which its
-                        // finished product proves.
-                        if constexpr (TS == 2) {
-                            if (steps > 0) wait_pv(steps - 1);
+                mbar_wait(&s_full[x * kSB + buf], (steps / kSB) & 1, wc);
+                tc_fence_after();
+                if (warp_live) {                          // else rows of padding: whatever lies there
+                    const uint32_t sa = tmem + lane_off + C::s_col(x, buf);
+                    // One stream: the row of S is read twice, for its maximum and for P, 64 keys
+                    // at a time in rolled loops, whose code stays small (dim 256: two us of 100
+                    // less; dim 128 the same).  Two streams hide less and read it once (130 us
+                    // against 142 for 121-draft trees).
+                    auto read_s = [&](int half, float *v) {
+                        tmem_ld32(sa + half * 64, v);
+                        tmem_ld32(sa + half * 64 + 32, v + 32);
+                    };
+                    auto hide = [&](int half, float *v) {
+                        const uint32_t lo = half == 0 ? bits[0] : bits[2], hi = half == 0 ? bits[1] : bits[3];
+#pragma unroll
+                        for (int i = 0; i < 64; ++i)
+                            if (!((i < 32 ? lo : hi) >> (i & 31) & 1)) v[i] = kNegInf;
+                    };
+                    float sv[NT == 2 ? kKvTile : 1], ext = kNegInf;
+                    if constexpr (NT == 2) {
+                        read_s(0, sv);
+                        read_s(1, sv + 64);
+                        tmem_wait_ld();
+                        if (drafts) { hide(0, sv); hide(1, sv + 64); }
+                        ext = max_of<kKvTile>(sv);
+                    } else {
+#pragma unroll 1
+                        for (int half = 0; half < 2; ++half) {
+                            float v[64];
+                            read_s(half, v);
+                            tmem_wait_ld();
+                            if (drafts) hide(half, v);
+                            ext = fmaxf(ext, max_of<64>(v));
                         }
-#pragma unroll
-                        for (int s = 0; s < TS; ++s) {
-                            const uint32_t sl = (r + s) % C::kSlots;
-                            mbar_wait(&slot_full[sl], ((r + s) / C::kSlots) & 1, wc);
-                            if (!(mine >> lane & 1)) {
-#pragma unroll
-                                for (int c = 0; c < 2; ++c) {
-                                    uint4 *vr = reinterpret_cast<uint4 *>(sRing + sl * C::kSlotBytes +
-                                                                          c * C::kChunkBytes + row * 128);
-#pragma unroll
-                                    for (int i = 0; i < 8; ++i) vr[i] = make_uint4(0, 0, 0, 0);
-                                }
-                            }
-                        }
-                        fence_proxy_async_smem();
                     }
+                    const float m_tile = live ? ext * scale : kNegInf;    // -inf when it sees none of these keys
+                    const bool up = m_tile > m_ref + kRescaleSlack;   // also the first visible tile: m_ref = -inf
+                    if (__any_sync(0xffffffffu, up)) {
+                        float alpha = 1.f;
+                        if (up) {
+                            alpha = ex2_approx(m_ref - m_tile);
+                            l_sum *= alpha;
+                            m_ref = m_tile;
+                        }
+                        if (j > 0) {
+                            // With one S buffer, S_j there means PV_{j-1} is done; with more
+                            // it may still run.
+                            if constexpr (kSB > 1) {
+                                wait_pv(steps - 1);
+                                tc_fence_after();
+                            }
+#pragma unroll 1
+                            for (int c = 0; c < D / 32; ++c) {
+                                float o[32];
+                                const uint32_t oa = tmem + lane_off + C::o_col(x) + c * 32;
+                                tmem_ld32(oa, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) o[i] *= alpha;
+                                tmem_st32(oa, o);
+                            }
+                            tmem_wait_st();
+                        }
+                    }
+                    // P = 2^(s * scale * log2 e - m_ref), rounded to BF16 (the MMA's A
+                    // operand shares V's type); the row sum takes it unrounded.
+                    const float mu = m_ref == kNegInf ? 0.f : m_ref;
+                    uint64_t sum[4] = {0, 0, 0, 0};
+                    auto put_half = [&](int half, float *v) {
+                        uint32_t pk[32];
+                        exp_64(v, scale, -mu, sum);
+#pragma unroll
+                        for (int i = 0; i < 64; i += 2) pk[i >> 1] = pack_bf16x2(v[i], v[i + 1]);
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+                            tmem_st16u(sa + half * 32 + c * 16, *reinterpret_cast<const uint32_t(*)[16]>(pk + c * 16));
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0 && !values) mbar_arrive(half == 0 ? &p_half[x * kSB + buf] : &p_full[x * kSB + buf]);
+                    };
+                    if constexpr (NT == 2) {
+                        put_half(0, sv);
+                        put_half(1, sv + 64);
+                    } else {
+#pragma unroll 1
+                        for (int half = 0; half < 2; ++half) {
+                            float v[64];
+                            read_s(half, v);
+                            tmem_wait_ld();
+                            if (drafts) hide(half, v);
+                            put_half(half, v);
+                        }
+                    }
+                    l_sum += sum_of(sum);
                 }
-                if (!warp_live) {                         // rows of padding: whatever lies there
+                if (values) {
+                    // Values of keys nobody sees must not meet a zero weight: they may be
+                    // NaN; nor a draft's that are not finite the weights of rows that do
+                    // not see it.  A thread looks after one key, when its row of P is done:
+                    // the values have landed meanwhile.  (Before it: 106 us against 99 at dim 256;
+                    // by the copying warp 130.)
+                    const uint32_t r = r0 + (uint32_t)(pos_v<kSB>(j, u.ntiles) * TS);
+                    // A parity wait needs the slot's copy before V_j to have landed.
+                    // S_j there proves that for all copies up to K_j; with two slots
+                    // to a tile the one before V_j's may be V_{j-1}, which its
+                    // finished product proves.
+                    if constexpr (TS == 2) {
+                        if (steps > 0) wait_pv(steps - 1);
+                    }
+                    const bool seen = mine >> lane & 1;
+                    const int draft = key0 + row - base;
+#pragma unroll 1
+                    for (int s = 0; s < TS; ++s) {
+                        const uint32_t sl = (r + s) % C::kSlots;
+                        mbar_wait(&slot_full[sl], ((r + s) / C::kSlots) & 1, wc);
+                        uint8_t *vr = sRing + sl * C::kSlotBytes + row * 128;
+                        uint32_t wild = 0;                // an exponent of all ones carries into the sign's place
+                        if (seen && draft >= 0) {
+#pragma unroll 1
+                            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    const uint4 w = reinterpret_cast<const uint4 *>(vr + c * C::kChunkBytes)[i ^ (row & 7)];
+                                    wild |= ((w.x & 0x7f807f80u) + 0x00800080u) | ((w.y & 0x7f807f80u) + 0x00800080u) |
+                                            ((w.z & 0x7f807f80u) + 0x00800080u) | ((w.w & 0x7f807f80u) + 0x00800080u);
+                                }
+                            wild &= 0x80008000u;
+                            if (wild) mark_bad(bad, k, draft);
+                        }
+                        if (!seen || wild) {
+#pragma unroll 1
+                            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                                for (int i = 0; i < 8; ++i)
+                                    reinterpret_cast<uint4 *>(vr + c * C::kChunkBytes)[i ^ (row & 7)] = make_uint4(0, 0, 0, 0);
+                        }
+                    }
+                    fence_proxy_async_smem();
+                }
+                if (values || !warp_live) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) { mbar_arrive(&p_half[x * kSB + buf]); mbar_arrive(&p_full[x * kSB + buf]); }
-                    continue;
                 }
-                const uint32_t sa = tmem + lane_off + C::s_col(x, buf);
-                float sv[kKvTile];
-#pragma unroll
-                for (int c = 0; c < kKvTile / 32; ++c) tmem_ld32(sa + c * 32, sv + c * 32);
-                tmem_wait_ld();
-                if (drafts) {
-#pragma unroll
-                    for (int w = 0; w < 4; ++w)
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (!(bits[w] >> i & 1)) sv[w * 32 + i] = kNegInf;
-                }
-                const float ext = max_of<kKvTile>(sv);
-                const float m_tile = live ? ext * scale : kNegInf;    // -inf when it sees none of these keys
-                const bool up = m_tile > m_ref + kRescaleSlack;   // also the first visible tile: m_ref = -inf
-                if (__any_sync(0xffffffffu, up)) {
-                    float alpha = 1.f;
-                    if (up) {
-                        alpha = ex2_approx(m_ref - m_tile);
-                        l_sum *= alpha;
-                        m_ref = m_tile;
-                    }
-                    if (j > 0) {
-                        // With one S buffer, S_j there means PV_{j-1} is done; with more
-                        // it may still run.
-                        if constexpr (kSB > 1) {
-                            wait_pv(steps - 1);
-                            tc_fence_after();
-                        }
-#pragma unroll 1
-                        for (int c = 0; c < D / 32; ++c) {
-                            float o[32];
-                            const uint32_t oa = tmem + lane_off + C::o_col(x) + c * 32;
-                            tmem_ld32(oa, o);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] *= alpha;
-                            tmem_st32(oa, o);
-                        }
-                        tmem_wait_st();
-                    }
-                }
-                // P = 2^(s * scale * log2 e - m_ref), rounded to BF16 (the MMA's A
-                // operand shares V's type); the row sum takes it unrounded.
-                const float mu = m_ref == kNegInf ? 0.f : m_ref;
-                uint32_t pk[kKvTile / 2];
-                uint64_t sum[4] = {0, 0, 0, 0};
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    exp_64(sv + half * 64, scale, -mu, sum);
-#pragma unroll
-                    for (int i = 0; i < 64; i += 2)
-                        pk[half * 32 + (i >> 1)] = pack_bf16x2(sv[half * 64 + i], sv[half * 64 + i + 1]);
-#pragma unroll
-                    for (int c = 0; c < 2; ++c)
-                        tmem_st16u(sa + half * 32 + c * 16,
-                                   *reinterpret_cast<const uint32_t(*)[16]>(pk + half * 32 + c * 16));
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(half == 0 ? &p_half[x * kSB + buf] : &p_full[x * kSB + buf]);
-                }
-                l_sum += sum_of(sum);
             }
             // ------------------------------------------------------ epilogue
             ++pieces;
@@ -591,7 +637,8 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
             }
             tc_fence_after();
             if (warp_live)
-                write_row<D, NT>(p, u, x, row, live, t, h, m_ref, l_sum, [&](int c, float (&o)[32]) {
+                write_row<D, NT>(p, u, x, row, live, t, h, m_ref, l_sum, live && sees_bad(bad, u, k, mrow),
+                                 [&](int c, float (&o)[32]) {
                     tmem_ld32(tmem + lane_off + C::o_col(x) + c * 32, o);
                     tmem_wait_ld();
                 });
@@ -611,8 +658,8 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
 // range opened the following ranges.  Block (chunk, c) takes 32 rows of that
 // unit, a lane a row and a warp an eighth of the columns, as the pieces lie, and
 // turns the result round in shared memory.  Four pieces are read at once; two at
-// dim 256, where a lane's share of a piece is twice as many registers (99.8 us
-// against 101.1 for a step of 8 requests, 24 rows).  The rows past a request's
+// dim 256, where a lane's share of a piece is twice as many registers (1.3 us less
+// for a step of 8 requests, 24 rows).  The rows past a request's
 // drafts are written here too.
 constexpr int kMergeThreads = 256;
 

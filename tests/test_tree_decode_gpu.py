@@ -511,3 +511,46 @@ def test_workspaces_that_do_not_fit(fw):
     with pytest.raises(ValueError, match="CUDA"):
         fw.paged_decode_tree(**x, workspace=torch.empty(n, dtype=torch.uint8))
     assert fw.launch_count() == before
+
+
+@pytest.mark.parametrize("D,kv8", [(128, False), (128, True), (256, False)])
+@pytest.mark.parametrize("T,Hq", [(9, 8), (70, 8), (200, 2)])
+def test_values_that_are_not_finite(fw, D, kv8, T, Hq):
+    """A draft's NaN or infinite value reaches the rows that see the draft, in one
+    KV head, and nobody else; a committed key's reaches every row."""
+    Hkv, ps = 2, 64
+    lens, drafts = [9000, 300, 5003, 640], [T, T - 2, T, T - 1]
+    x = make(4, T, Hq, Hkv, D, ps, lens, drafts, "tree", kv8=kv8, seed=63)
+    ref = spec.tree_attention(**x)
+    y = dict(x, v_cache=x["v_cache"].clone())
+    hit = torch.zeros(4, T, Hq, dtype=torch.bool)
+    G = Hq // Hkv
+
+    def spoil(b, pos, g, col, bits):
+        v = y["v_cache"].view(torch.uint8 if kv8 else torch.int16)
+        v[int(x["block_table"][b, pos // ps]), pos % ps, g, col] = bits
+
+    def sees(b, j):
+        return torch.from_numpy(((x["tree_mask"][b, :, j // 32].numpy().astype(np.int64) >> (j % 32)) & 1).astype(bool))
+
+    nan, inf = (0x7f, 0xff) if kv8 else (0x7fc1, 0x7f80)     # E4M3 has no infinity: both NaNs
+    for b, j, g, col, bits in ((0, 4, 0, 3, nan), (0, T - 1, 1, D - 1, inf), (2, 0, 1, 64, inf), (3, 2, 0, 0, nan)):
+        spoil(b, lens[b] - drafts[b] + j, g, col, bits)
+        if j < drafts[b]:
+            s = sees(b, j)
+            s[drafts[b]:] = False
+            hit[b, :, g * G:(g + 1) * G] |= s[:, None]
+    assert hit.any() and not hit[0].all()
+    out, lse = fw.paged_decode_tree(**on_gpu(y))
+    torch.cuda.synchronize()
+    assert fw.device_status() == 0
+    out, lse = out.cpu(), lse.cpu()
+    assert torch.isnan(out[hit]).all()
+    out[hit] = torch.from_numpy(ref[0])[hit].to(torch.bfloat16)
+    check(out, lse, ref, D, "rows without such values")
+
+    spoil(1, 7, 1, 5, nan)                                    # committed
+    out, _ = fw.paged_decode_tree(**on_gpu(y))
+    torch.cuda.synchronize()
+    assert torch.isnan(out[1, :T - 2, G:, 5]).all() and torch.isfinite(out[1, :, :G]).all()
+    assert torch.isfinite(out[1, :T - 2, G:, :5]).all()
