@@ -656,23 +656,28 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
 // row sums l_i and bases m_i, M = max m_i, out = sum 2^(m_i - M) o_i /
 // sum 2^(m_i - M) l_i.  The pieces of the unit whose first one ended CTA c's
 // range opened the following ranges.  Block (chunk, c) takes 32 rows of that
-// unit, a lane a row and a warp an eighth of the columns, as the pieces lie, and
-// turns the result round in shared memory.  Four pieces are read at once; two at
-// dim 256, where a lane's share of a piece is twice as many registers (1.3 us less
-// for a step of 8 requests, 24 rows).  The rows past a request's
-// drafts are written here too.
-constexpr int kMergeThreads = 256;
+// unit, a lane a row and a warp an equal share of the columns, as the pieces lie, and
+// turns the result round in shared memory.  Pieces are read four at once where a
+// lane's share of one is 64 bytes, two where it is 128 (four: 1.3 us more at dim 256).
+// Two row tiles, whose partials are the most, take blocks of four warps, of which
+// more are there when the last CTA ends (129 -> 127 us for 16 requests with 121
+// drafts; one row tile, often of more pieces, is better off with eight: 13.4 us
+// against 14.1 for one request).  The rows past a request's drafts are written here
+// too.
+template <int NT>
+constexpr int kMergeThreads = NT == 2 ? 128 : 256;
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_constant__ TreeParams p) {
-    constexpr int kUnits = D / 4 / (kMergeThreads / 32);   // 16-byte FP32 units of a warp's columns
-    constexpr int kPieces = D == 256 ? 2 : 4;
+__global__ void __launch_bounds__(kMergeThreads<NT>) tree_merge_kernel(const __grid_constant__ TreeParams p) {
+    constexpr int kThreads = kMergeThreads<NT>;
+    constexpr int kUnits = D / 4 / (kThreads / 32);   // 16-byte FP32 units of a warp's columns
+    constexpr int kPieces = 16 / kUnits;
     __shared__ uint4 stage[32][D / 8 + 1];           // BF16 rows
     __shared__ long long offset[32];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     // Zeros and -inf, a warp to a draft; these wait for nothing.
-    const int nwarps = gridDim.x * gridDim.y * (kMergeThreads / 32);
-    for (int i = (blockIdx.y * gridDim.x + blockIdx.x) * (kMergeThreads / 32) + warp; i < p.B * p.T; i += nwarps) {
+    const int nwarps = gridDim.x * gridDim.y * (kThreads / 32);
+    for (int i = (blockIdx.y * gridDim.x + blockIdx.x) * (kThreads / 32) + warp; i < p.B * p.T; i += nwarps) {
         const int b = i / p.T, pt = i - b * p.T;
         int n, d;
         tree_row(p, b, n, d);
@@ -748,7 +753,7 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
                 l != 0.f ? (m + log2f(l)) * 0.69314718055994531f : kNegInf;
     }
     __syncthreads();
-    for (int i = tid; i < 32 * (D / 8); i += kMergeThreads) {
+    for (int i = tid; i < 32 * (D / 8); i += kThreads) {
         const int r = i / (D / 8), c = i % (D / 8);
         if (offset[r] >= 0)
             reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(p.out) + offset[r])[c] = stage[r][c];
@@ -767,7 +772,7 @@ cudaError_t launch_bf16(const TreeParams &p, const CUtensorMap &tq, const CUtens
 }  // namespace
 
 cudaError_t launch_tree_merge(const TreeParams &p, int row_tiles, cudaStream_t stream) {
-    const dim3 grid(row_tiles * 4, p.grid), block(kMergeThreads);
+    const dim3 grid(row_tiles * 4, p.grid), block(row_tiles == 2 ? kMergeThreads<2> : kMergeThreads<1>);
     if (p.D == 256) return launch_after_previous(tree_merge_kernel<256, 1>, grid, block, 0, stream, p);
     if (row_tiles == 2) return launch_after_previous(tree_merge_kernel<128, 2>, grid, block, 0, stream, p);
     return launch_after_previous(tree_merge_kernel<128, 1>, grid, block, 0, stream, p);
