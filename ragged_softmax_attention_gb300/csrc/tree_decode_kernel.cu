@@ -33,7 +33,7 @@
 // drafts (NT = 2): 4.84 GB in 860 .. 955 us by machine, 0.75 .. 0.83; a step takes
 // 3,050 cycles, the chain S, softmax (1,390), PV, next QK of two streams in turn,
 // where HBM's share is 2,700.  16 requests with 121 drafts of 32/8 heads (NT = 2):
-// 134 GFLOP in 130 us, 1.03 PFLOP/s, the same chain.
+// 134 GFLOP in 128 us, 1.05 PFLOP/s, the same chain.
 //
 // Warp roles: warp 0 copies (Q, then K and V tiles through a ring of 32 KiB
 // slots in the order the MMAs take them), warps 1 and 2 issue the MMAs (of a
