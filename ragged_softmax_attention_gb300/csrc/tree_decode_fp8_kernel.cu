@@ -96,7 +96,7 @@ struct F8TreeCfg {
     static constexpr int kOffPlan = kOffQScale;                 // the plan is used up before the first of them
     static constexpr int kOffScan = kOffPlan + 32;              // [16]
     static constexpr int kOffBase = kOffQScale + kSched * NT * 128;   // NT = 1: [2][128] bases, [2][2][128] row sums
-    static constexpr int kOffMisc = kOffBase + (NT == 1 ? 3072 : 0);
+    static constexpr int kOffMisc = kOffBase + (NT == 1 ? (2 + 4) * 128 * 4 : 0);
     static constexpr int kSmemBytes = kOffMisc + 16 + 1024;
     static_assert(kSmemBytes <= 232448, "shared memory budget of one CTA exceeded");
     static constexpr int kThreads = 256 + kWG * 128;
