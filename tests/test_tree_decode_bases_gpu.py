@@ -1,5 +1,6 @@
-"""Tree decode where the score factor vanishes, over every kind of cache and on
-both sides of 128 rows.
+"""Tree decode where the base of a row's exponentials moves, where the score
+factor vanishes, and where one key carries a row, over every kind of cache and
+on both sides of 128 rows.
 
 Bounds, beside those of test_tree_decode_gpu.py: over an 8-bit cache a weight is
 rounded to FP16, half a step 2^-11 of it, against a row sum of unrounded ones.
@@ -7,6 +8,8 @@ It carries 2^7 over a base that the row's largest weight is never below, so
 weights under 2^-14 / 2^7 of that are off by half a subnormal step, 2^-25, each:
 n keys move an output by at most n * 2^-32 * max |v|.
 """
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -24,6 +27,14 @@ ROWS = [(12, 8, 2), (40, 16, 4)]               # 48 rows of a KV head, and 160
 @pytest.fixture(scope="module")
 def fw():
     return built_library()
+
+
+def capped(fw, ctas, call):
+    fw.set_option(fw.FW_OPT_MAX_CTAS, ctas)
+    try:
+        return call()
+    finally:
+        fw.set_option(fw.FW_OPT_MAX_CTAS, 0)
 
 
 def run_tight(fw, x, what):
@@ -48,6 +59,62 @@ def run_tight(fw, x, what):
     diff = np.abs(o - o_ref)
     worst = np.unravel_index(np.argmax(diff / bound), diff.shape)
     assert diff[worst] <= bound[worst], (what, worst, diff[worst], bound[worst], o_ref[worst])
+
+
+@pytest.mark.parametrize("ctas", [0, 1])       # rows cut into pieces, and kept whole
+@pytest.mark.parametrize("scale", [-0.7, 0.0, 1.5])
+@pytest.mark.parametrize("T,Hq,Hkv", ROWS)
+@pytest.mark.parametrize("D,kv8", KINDS)
+def test_scales(fw, D, kv8, T, Hq, Hkv, scale, ctas):
+    x = make(2, T, Hq, Hkv, D, 32, [1100, 390], [T, T - 3], "tree", kv8=kv8, seed=71)
+    x["scale"] = scale
+    capped(fw, ctas, lambda: run_tight(fw, x, f"scale {scale}"))
+
+
+@pytest.mark.parametrize("ctas", [0, 1])
+@pytest.mark.parametrize("turn", [1, -1])
+@pytest.mark.parametrize("T,Hq,Hkv", ROWS)
+@pytest.mark.parametrize("D,kv8", KINDS)
+def test_scores_that_rise_in_every_tile(fw, D, kv8, T, Hq, Hkv, turn, ctas):
+    """All queries near one direction, keys along it that grow by some 9 log2 units a
+    tile (turn 1), or against it under a negative scale (turn -1)."""
+    n, ps = 1500, 64
+    x = make(1, T, Hq, Hkv, D, ps, [n], None, "tree", kv8=kv8, seed=73)
+    g = torch.Generator().manual_seed(74)
+    u = torch.randn(D, generator=g)
+    u *= math.sqrt(D) / u.norm()
+    x["q"] = (u + 0.2 * torch.randn(1, T, Hq, D, generator=g)).to(torch.bfloat16)
+    grow = torch.linspace(0, 70.0 / math.sqrt(D), n)           # score = grow * D / sqrt(D)
+    pages = x["block_table"][0, :-(-n // ps)].long()
+    k = torch.zeros(len(pages) * ps, Hkv, D)
+    k[:n] = (turn * grow[:, None, None] * u + 0.05 * torch.randn(n, Hkv, D, generator=g)) / x["k_scale"]
+    if kv8:
+        k.clamp_(-448, 448)
+    x["k_cache"][pages] = k.view(len(pages), ps, Hkv, D).to(x["k_cache"].dtype)
+    x["scale"] *= turn
+    capped(fw, ctas, lambda: run_tight(fw, x, "rising scores"))
+
+
+@pytest.mark.parametrize("ctas", [0, 1, 3])
+@pytest.mark.parametrize("T,Hq,Hkv", [(30, 8, 2), (60, 8, 2)])
+@pytest.mark.parametrize("D,kv8", KINDS)
+def test_one_key_carries_a_row(fw, D, kv8, T, Hq, Hkv, ctas):
+    """Every row's weight lies on a key of its own, next to an edge of a page, of half a
+    tile, of a tile or of a piece: a value taken from elsewhere, or cleared, shows."""
+    n, ps = 64 * T + 21, 32
+    x = make(1, T, Hq, Hkv, D, ps, [n], None, "tree", kv8=kv8, seed=77)
+    base, G = n - T, Hq // Hkv
+    k = x["k_cache"]
+    for t in range(T):
+        for h in range(Hq):
+            # the keys before and behind place 64 t and 64 t + 32, a row each
+            j = min(max(0, 64 * t + (h % G >> 1) * 32 - (h & 1)), base - 1)
+            page, off = int(x["block_table"][0, j // ps]), j % ps
+            key = x["q"][0, t, h].float() * 4.0 / x["k_scale"]
+            k[page, off, h // G] = (key.clamp(-448, 448) if kv8 else key).to(k.dtype)
+    ref = spec.tree_attention(**x)
+    assert (np.abs(ref[0]).max(-1) > 0.5 * ref[2].max(-1)).mean() > 0.9      # one key's value, not an average
+    capped(fw, ctas, lambda: run_tight(fw, x, "one key"))
 
 
 @pytest.mark.parametrize("T,Hq,Hkv", ROWS)
