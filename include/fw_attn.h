@@ -527,12 +527,13 @@ typedef enum {
                                        softmax with a conditional rescale (the base moves when a
                                        row max rises more than 8 log2 units).  Same result up to
                                        rounding; kept for comparison. */
-    FW_OPT_TEST_STALL = 5           /* test hook, default 0.  1: the grouped-query decode kernel's
-                                       copy warp first waits on a barrier that nothing completes,
+    FW_OPT_TEST_STALL = 5           /* test hook, default 0.  1: the copy warp of the grouped-query
+                                       decode kernel and of the tree decode kernels first waits on a barrier that nothing completes,
                                        so that wait runs out after FW_OPT_WAIT_TIMEOUT_MS: the call
                                        records FW_ERR_DEVICE_TIMEOUT (read by fw_get_device_status)
-                                       and its outputs are not valid.  Nothing is copied or
-                                       multiplied before the wait, so no work is left in flight. */
+                                       and its outputs are not valid.  No key or value is
+                                       copied and nothing multiplied before the wait, so no such
+                                       work is left in flight. */
 } fw_option_t;
 
 fw_status_t fw_set_option(int32_t option, int64_t value);

@@ -1189,6 +1189,7 @@ fw_status_t fw_paged_decode_tree(const fw_tensor_t *q, const fw_tensor_t *k_cach
         return s;
     }
     fw::tree_place_workspace(&p, ws);
+    p.test_stall = g_opt_test_stall ? 1 : 0;
     p.timeout_ns = (uint64_t)g_opt_timeout_ms * 1000000ull;
     p.status = d->status;
     CUtensorMap tq, tk, tv;

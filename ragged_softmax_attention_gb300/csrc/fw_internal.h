@@ -179,6 +179,7 @@ struct TreeParams {
     float *part_o;                             // [2 * grid][row tiles of a unit * 128][D] unnormalised pieces
     float2 *part_ml;                           // base (log2) and row sum of each of their rows
     TreeCut *cuts;                             // [grid]
+    int test_stall;                            // test hook: the producer first waits on a barrier nothing completes
     uint64_t timeout_ns;
     int *status;
 };

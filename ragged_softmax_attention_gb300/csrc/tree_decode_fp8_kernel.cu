@@ -88,7 +88,8 @@ struct F8TreeCfg {
     static constexpr int kBarOFree = kBarBase + 2;              // O read by both warpgroups (NT = 1)
     static constexpr int kBarSchedFull = kBarOFree + 1;
     static constexpr int kBarSchedEmpty = kBarSchedFull + kSched;
-    static constexpr int kNumBars = kBarSchedEmpty + kSched;
+    static constexpr int kBarNever = kBarSchedEmpty + kSched;   // test hook: no thread ever arrives on it
+    static constexpr int kNumBars = kBarNever + 1;
     static constexpr int kOffSched = (kOffBar + kNumBars * 8 + 63) / 64 * 64;
     static constexpr int kOffSeen = kOffSched + kSched * 64;    // [2][16 words]
     static constexpr int kOffBad = kOffSeen + 128;              // drafts whose values are NaN
@@ -197,6 +198,7 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
         for (int i = 0; i < C::kSched; ++i) {
             mbar_init(&q_ready[i], 4); mbar_init(&sched_full[i], 1); mbar_init(&sched_empty[i], C::kSchedReaders);
         }
+        mbar_init(bars + C::kBarNever, 1);
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -223,7 +225,8 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
         // ------------------------------------------------------------ producer
         const int box_rows = p.ps < kKvTile ? p.ps : kKvTile;
         uint32_t ik = 0, iv = 0;                          // K and V tiles issued
-        bool ok = true;
+        // Test hook for the bounded waits, as in the BF16 kernel.
+        bool ok = !p.test_stall || warp_wait(bars + C::kBarNever, 0, wc, lane);
         for (int k = 0; ok; ++k) {
             const TreeUnit *ur = wait_unit(k);
             TreeUnit u;
@@ -231,7 +234,7 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
             if (ur) u = *ur;
             __syncwarp();
             if (lane == 0) free_unit(k);
-            if (u.b < 0) break;
+            if (!__all_sync(0xffffffffu, u.b >= 0)) break;
             // K tile i and V tile i - kSB go out together, a half warp each: one
             // after the other, a copy's barrier and copy instructions take this warp
             // 1,100 cycles beside the others, and a tile two of them.
@@ -459,7 +462,9 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
         if constexpr (C::kRegsConvert < C::kRegsLaunch) setmaxnreg_dec<C::kRegsConvert>();
         // ------------------------------------------------------------ converters
         // Thread = query row of a tile, then = key of a tile.  After an abort
-        // every wait returns at once and the bounded loops run out.
+        // every wait returns at once and the bounded loops run out; the four warps,
+        // which share a named barrier, take or leave a unit together, as do the softmax
+        // warps below.
         const int row = threadIdx.x - 128;
         uint32_t i = 0;                                   // V tiles converted
         for (int k = 0;; ++k) {
@@ -469,7 +474,7 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
             if (ur) u = *ur;
             __syncwarp();
             if (lane == 0) free_unit(k);
-            if (u.b < 0) break;
+            if (!named_bar_all(3, 128, u.b >= 0)) break;
             if (row < kBadWords) bad[k % kBadUnits * kBadWords + row] = 0;
             mbar_wait(q_full, k & 1, wc);
             for (int x = 0; x < u.nrt; ++x) {
@@ -614,7 +619,7 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
                                    1e-37f);
             __syncwarp();
             if (lane == 0) free_unit(k);
-            if (u.b < 0) break;
+            if (!(NT == 1 ? named_bar_all(4, 128 * C::kWG, u.b >= 0) : __all_sync(0xffffffffu, u.b >= 0) != 0)) break;
             if (x >= u.nrt) continue;
             int t, h;
             const bool live = tree_tile_row(p, u.rt0 + x, u.g, u.d, row, t, h);

@@ -72,7 +72,8 @@ struct TreeCfg {
     static constexpr int kBarDrain = kBarIssued + NT;           // [2]
     static constexpr int kBarSchedFull = kBarDrain + 2;
     static constexpr int kBarSchedEmpty = kBarSchedFull + kSched;
-    static constexpr int kNumBars = kBarSchedEmpty + kSched;
+    static constexpr int kBarNever = kBarSchedEmpty + kSched;   // test hook: no thread ever arrives on it
+    static constexpr int kNumBars = kBarNever + 1;
     static constexpr int kOffSched = (kOffBar + kNumBars * 8 + 63) / 64 * 64;
     static constexpr int kOffSeen = kOffSched + kSched * 64;    // [2][4 warps][4 words]
     static constexpr int kOffBad = kOffSeen + 128;              // drafts whose values are not finite
@@ -136,6 +137,7 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
         for (int i = 0; i < NT; ++i) mbar_init(&issued[i], 1);
         for (int i = 0; i < 2; ++i) mbar_init(&drain[i], 1);
         for (int i = 0; i < C::kSched; ++i) { mbar_init(&sched_full[i], 1); mbar_init(&sched_empty[i], C::kSchedReaders); }
+        mbar_init(bars + C::kBarNever, 1);
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -162,7 +164,10 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
         // ------------------------------------------------------------ producer
         const int box_rows = p.ps < kKvTile ? p.ps : kKvTile;
         uint32_t rp = 0;                                  // ring slots filled so far
-        bool ok = true;
+        // Test hook for the bounded waits: before it copies anything, this warp waits on
+        // a barrier that nothing completes.  Nor do products then begin; the other roles
+        // wind down over the units at hand.
+        bool ok = !p.test_stall || warp_wait(bars + C::kBarNever, 0, wc, lane);
         for (int k = 0; ok; ++k) {
             const TreeUnit *ur = wait_unit(k);
             TreeUnit u;
@@ -170,7 +175,7 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
             if (ur) u = *ur;
             __syncwarp();
             if (lane == 0) free_unit(k);
-            if (u.b < 0) break;
+            if (!__all_sync(0xffffffffu, u.b >= 0)) break;
             // ---- K and V tiles in the order the MMAs take them
             auto copy_tile = [&](int j, int entry, bool is_v) -> bool {
                 const int key0 = (u.tile0 + j) * kKvTile;
@@ -429,8 +434,9 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
     } else {
         if constexpr (NT == 2) setmaxnreg_inc<C::kRegsSoftmax>();
         // ------------------------------------------------- softmax / epilogue
-        // A failed wait does not change the control flow, so the named barriers
-        // below are always met by all four warps of the stream.
+        // The named barriers below have no limit, so the warps that share them never part:
+        // a failed wait inside a unit does not change the control flow, and a unit that
+        // not all of them see (a wait for its record ran out) is taken by none.
         const int x = (warp - 4) >> 2;
         const int q4 = warp & 3;
         const int row = q4 * 32 + lane;
@@ -443,13 +449,12 @@ tree_decode_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
         uint32_t steps = 0, pieces = 0, rp = 0;
         for (int k = 0;; ++k) {
             const TreeUnit *ur = wait_unit(k);
-            const bool got = ur && ur->b >= 0;
             TreeUnit u;
             u.b = -1;
-            if (got) u = *ur;
+            if (ur) u = *ur;
             __syncwarp();
             if (lane == 0) free_unit(k);
-            if (!got) break;
+            if (!(x == 0 ? named_bar_all(1, 128, u.b >= 0) : __all_sync(0xffffffffu, u.b >= 0) != 0)) break;
             const uint32_t r0 = rp;
             rp += (uint32_t)(2 * u.ntiles * TS);
             if (x >= u.nrt) continue;
