@@ -15,6 +15,7 @@
 
 #include "fw_attn.h"
 #include "fw_internal.h"
+#include "tensor_share.h"
 
 namespace {
 
@@ -967,35 +968,6 @@ static fw_status_t check_i32(const fw_tensor_t *t, const char *name, int ndim) {
     return FW_OK;
 }
 
-// Bytes from the tensor's first element to one past its last.
-static int64_t extent_bytes(const fw_tensor_t *t, int64_t esz) {
-    int64_t e = 1;
-    for (int i = 0; i < t->ndim; ++i) {
-        if (t->shape[i] == 0) return 0;
-        e += (t->shape[i] - 1) * t->stride[i];
-    }
-    return e * esz;
-}
-
-static bool overlap(const fw_tensor_t *a, int64_t esz_a, const fw_tensor_t *b, int64_t esz_b) {
-    const char *pa = static_cast<const char *>(a->data), *pb = static_cast<const char *>(b->data);
-    return pa < pb + extent_bytes(b, esz_b) && pb < pa + extent_bytes(a, esz_a);
-}
-
-// Whether two I32 tensors share an element.  Columns of one buffer have
-// interleaved extents and nothing in common: with equal row strides that the rows
-// fit in, what counts is where the rows start within a stride.
-static bool i32_share(const fw_tensor_t *a, const fw_tensor_t *b) {
-    if (!overlap(a, 4, b, 4)) return false;
-    if (a->ndim < 2 || b->ndim < 2 || a->stride[0] != b->stride[0] || a->stride[0] == 0) return true;
-    fw_tensor_t ra = *a, rb = *b;
-    ra.shape[0] = rb.shape[0] = 1;
-    const int64_t st = a->stride[0] * 4, ea = extent_bytes(&ra, 4), eb = extent_bytes(&rb, 4);
-    int64_t at = (static_cast<const char *>(b->data) - static_cast<const char *>(a->data)) % st;
-    if (at < 0) at += st;
-    return at < ea || st - at < eb;
-}
-
 // A tensor that is written holds every element once: each stride passes what the
 // shorter ones reach.
 static fw_status_t check_written(const fw_tensor_t *t, const char *name) {
@@ -1017,39 +989,13 @@ static fw_status_t check_written(const fw_tensor_t *t, const char *name) {
     return FW_OK;
 }
 
-// Whether two [pages, ps, Hkv, D] caches share an element.  Views into one
-// buffer (K and V halves of every page, say) have interleaved extents and no
-// common element, so with equal strides the distance between the bases is
-// looked up among the distances the strides can make; for unequal strides
-// overlapping extents count as shared.
-static bool caches_share(const fw_tensor_t *a, const fw_tensor_t *b, int64_t esz) {
-    if (!overlap(a, esz, b, esz)) return false;
-    for (int i = 0; i < 3; ++i)
-        if (a->stride[i] != b->stride[i]) return true;
-    const int64_t row = (a->shape[3] > b->shape[3] ? a->shape[3] : b->shape[3]) * esz;
-    int64_t rest = static_cast<const char *>(b->data) - static_cast<const char *>(a->data);
-    if (rest < 0) rest = -rest;
-    // the three strides, longest first
-    int order[3] = {0, 1, 2};
-    for (int i = 0; i < 3; ++i)
-        for (int j = i + 1; j < 3; ++j)
-            if (a->stride[order[j]] > a->stride[order[i]]) { const int x = order[i]; order[i] = order[j]; order[j] = x; }
-    // Nested strides leave two candidates a level: the multiple below and above.
-    for (int up = 0; up < 8; ++up) {
-        int64_t r = rest;
-        bool can = true;
-        for (int l = 0; l < 3; ++l) {
-            const int64_t s = a->stride[order[l]] * esz, ext = a->shape[order[l]];
-            if (s == 0 || ext <= 1) continue;
-            int64_t k = r / s;
-            if (r % s != 0 && r < 0) --k;
-            if (up >> l & 1) ++k;
-            if (k <= -ext || k >= ext) { can = false; break; }
-            r -= k * s;
-        }
-        if (can && r > -row && r < row) return true;
-    }
-    return false;
+static int64_t element_bytes(const fw_tensor_t *t) {
+    return t->dtype == FW_BF16 ? 2 : t->dtype == FW_FP8_E4M3 ? 1 : 4;
+}
+
+// Whether two tensors, either of which may be NULL, have an element in common.
+static bool share(const fw_tensor_t *a, const fw_tensor_t *b) {
+    return a && b && fw::tensors_share(a, element_bytes(a), b, element_bytes(b));
 }
 
 // Validates a tree decode and fills the kernel's parameters.
@@ -1188,6 +1134,20 @@ fw_status_t fw_paged_decode_tree(const fw_tensor_t *q, const fw_tensor_t *k_cach
     } else if (fw_status_t s = get_workspace(d, need, stream, &ws)) {
         return s;
     }
+    // Nothing that is written lies over anything else of the call.
+    fw_tensor_t room{};
+    room.data = ws;
+    room.dtype = FW_I32;
+    room.ndim = 1;
+    room.shape[0] = (int64_t)need / 4;
+    room.stride[0] = 1;
+    const fw_tensor_t *tensors[] = {&room, out, lse, q, k_cache, v_cache, block_table, seq_lens, tree_mask, draft_lens};
+    const char *names[] = {"the workspace", "out", "lse", "q", "k_cache", "v_cache", "block_table", "seq_lens", "tree_mask",
+                           "draft_lens"};
+    for (int i = 0; i < 3; ++i)
+        for (int j = i + 1; j < 10; ++j)
+            if (share(tensors[i], tensors[j]))
+                return fail(FW_ERR_INVALID_ARG, "%s overlaps %s", names[i], names[j]);
     fw::tree_place_workspace(&p, ws);
     p.test_stall = g_opt_test_stall ? 1 : 0;
     p.timeout_ns = (uint64_t)g_opt_timeout_ms * 1000000ull;
@@ -1240,10 +1200,9 @@ fw_status_t fw_tree_mask(const fw_tensor_t *parents, const fw_tensor_t *draft_le
     if (B == 0) return ok();
     if (fw_status_t s = check_written(tree_mask, "tree_mask")) return s;
     if (fw_status_t s = check_written(depths, "depths")) return s;
-    if (i32_share(tree_mask, parents) || (depths && i32_share(depths, parents)) ||
-        (draft_lens && (i32_share(tree_mask, draft_lens) || (depths && i32_share(depths, draft_lens)))))
+    if (share(tree_mask, parents) || share(depths, parents) || share(tree_mask, draft_lens) || share(depths, draft_lens))
         return fail(FW_ERR_INVALID_ARG, "an output overlaps an input");
-    if (depths && i32_share(depths, tree_mask)) return fail(FW_ERR_INVALID_ARG, "depths overlaps tree_mask");
+    if (share(depths, tree_mask)) return fail(FW_ERR_INVALID_ARG, "depths overlaps tree_mask");
     fw::TreeMaskParams p{};
     p.B = (int)B; p.T = (int)T; p.W = (int)tree_mask->shape[2];
     p.parents = static_cast<const int32_t *>(parents->data);
@@ -1302,11 +1261,11 @@ fw_status_t fw_build_page_tables(const fw_tensor_t *seq_lens, const fw_tensor_t 
         if (!outs[i]) continue;
         for (int j = 0; j < 4; ++j) {
             if (((i == 3 && j == 2) || (i == 4 && j == 3)) && outs[i]->data == ins[j]->data) continue;  // the same vector
-            if (overlap(outs[i], 4, ins[j], 4))
+            if (fw::extents_overlap(outs[i], 4, ins[j], 4))
                 return fail(FW_ERR_INVALID_ARG, "%s overlaps an input", names[i]);
         }
         for (int j = 0; j < i; ++j)
-            if (outs[j] && overlap(outs[i], 4, outs[j], 4))
+            if (outs[j] && fw::extents_overlap(outs[i], 4, outs[j], 4))
                 return fail(FW_ERR_INVALID_ARG, "%s overlaps %s", names[i], names[j]);
     }
     fw::PageTableParams p{};
@@ -1328,7 +1287,7 @@ fw_status_t fw_build_page_tables(const fw_tensor_t *seq_lens, const fw_tensor_t 
     p.cu_new = cu_new ? static_cast<int32_t *>(cu_new->data) : nullptr;
     p.held_out = static_cast<int32_t *>(held_out->data);
     p.range_out = static_cast<int32_t *>(range_out->data);
-    p.in_place = overlap(held_out, 4, held, 4) || overlap(range_out, 4, free_range, 4);
+    p.in_place = fw::extents_overlap(held_out, 4, held, 4) || fw::extents_overlap(range_out, 4, free_range, 4);
     std::lock_guard<std::mutex> lk(g_mu);
     DeviceState *d = nullptr;
     if (fw_status_t s = device_state(&d)) return s;
@@ -1380,13 +1339,14 @@ fw_status_t fw_kv_commit(const fw_tensor_t *path, const fw_tensor_t *path_lens, 
     if (v_cache) {
         if (fw_status_t s = check_tma_layout(v_cache, "v_cache")) return s;
         if (fw_status_t s = check_written(v_cache, "v_cache")) return s;
-        if (caches_share(k_cache, v_cache, esz))
+        if (share(k_cache, v_cache))
             return fail(FW_ERR_INVALID_ARG, "v_cache shares elements with k_cache: move the keys alone (v_cache NULL)");
     }
     if (new_lens && B > 0) {
-        if (overlap(new_lens, 4, path_lens, 4) || overlap(new_lens, 4, path, 4) || overlap(new_lens, 4, block_table, 4))
+        if (fw::extents_overlap(new_lens, 4, path_lens, 4) || fw::extents_overlap(new_lens, 4, path, 4) ||
+            fw::extents_overlap(new_lens, 4, block_table, 4))
             return fail(FW_ERR_INVALID_ARG, "new_lens overlaps an input");
-        if (overlap(new_lens, 4, base_lens, 4))
+        if (fw::extents_overlap(new_lens, 4, base_lens, 4))
             return fail(FW_ERR_INVALID_ARG, "new_lens overlaps base_lens");
     }
     if (B == 0) return ok();
