@@ -182,8 +182,11 @@ PyObject *paged_decode_tree(PyObject *, PyObject *const *a, Py_ssize_t n) {
     fw_tensor_t *v[7];
     for (int i = 0; i < 7; ++i) v[i] = args.add(t[i]);
     fw_tensor_t *vo = args.add(out), *vl = args.add(lse);
-    if (failed(g_tree(v[0], v[1], v[2], v[3], v[4], v[5], v[6], (float)scale, (float)ks, (float)vs, vo, vl,
-                      ws.data_ptr(), ws.nbytes(), where.stream())))
+    // NULL would mean the library's own buffer, which calls on several streams share: a
+    // caller's empty tensor is a workspace of no bytes (at an address that is not read).
+    void *room = ws.nbytes() > 0 ? ws.data_ptr() : reinterpret_cast<void *>(256);
+    if (failed(g_tree(v[0], v[1], v[2], v[3], v[4], v[5], v[6], (float)scale, (float)ks, (float)vs, vo, vl, room,
+                      ws.nbytes(), where.stream())))
         return nullptr;
     return pair(out, lse);
     END_HANDLE_TH_ERRORS
