@@ -322,7 +322,8 @@ def _fast():
         import importlib.util
         path = os.path.join(_HERE, "_fw_fast.so")
         if not os.path.exists(path):
-            raise RuntimeError(f"{path} is not built; run ragged_softmax_attention_gb300.build.build() first")
+            raise RuntimeError(f"{path} is not built; run ragged_softmax_attention_gb300.build.build() first, which "
+                               "warns when the module cannot be compiled")
         lib = load_library()
         loader = importlib.machinery.ExtensionFileLoader("_fw_fast", path)
         spec = importlib.util.spec_from_file_location("_fw_fast", path, loader=loader)

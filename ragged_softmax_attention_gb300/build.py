@@ -4,7 +4,9 @@ Each .cu under csrc/ is compiled to an object in parallel, then linked into
 one shared library with the CUDA runtime linked statically.  Objects are
 rebuilt when their source or any header changed.  Beside it, g++ compiles
 csrc/fast_binding.cpp against torch's headers into _fw_fast.so, the Python
-entry points of the operators whose calls take a few microseconds.
+entry points of the operators whose calls take a few microseconds.  The library
+does not depend on it: where the module cannot be compiled (no g++, no headers of
+Python or torch), build() links the library all the same and warns.
 """
 from __future__ import annotations
 
@@ -13,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sys
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -66,11 +69,15 @@ def build(verbose: bool = False, force: bool = False, extra_flags=()) -> str:
     fast_stale = force or not os.path.exists(FAST) or os.path.getmtime(FAST) < max(
         os.path.getmtime(FAST_SRC), os.path.getmtime(os.path.join(ROOT, "include", "fw_attn.h")))
     fast_tmp = FAST + f".tmp{os.getpid()}"
+    fast_proc = fast_error = None
     if fast_stale:
-        fast_cmd = _fast_command(fast_tmp)
-        if verbose:
-            print(" ".join(fast_cmd), flush=True)
-        fast_proc = subprocess.Popen(fast_cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+        try:
+            fast_cmd = _fast_command(fast_tmp)
+            if verbose:
+                print(" ".join(fast_cmd), flush=True)
+            fast_proc = subprocess.Popen(fast_cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+        except (ImportError, OSError) as e:                # no torch, no g++
+            fast_error = str(e)
     for src in sources:
         obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
         objects.append(obj)
@@ -92,15 +99,15 @@ def build(verbose: bool = False, force: bool = False, extra_flags=()) -> str:
             os.replace(obj + ".tmp", obj)
             if verbose and text.strip():
                 print(text, flush=True)
-    if fast_stale:
+    if fast_proc is not None:
         out, _ = fast_proc.communicate()
         if fast_proc.returncode != 0:
-            failed.append((FAST, out.decode(errors="replace")))
+            fast_error = out.decode(errors="replace")
         else:
             os.replace(fast_tmp, FAST)
     if failed:
         msg = "\n".join(f"--- {o}\n{t}" for o, t in failed)
-        raise RuntimeError(f"compilation failed:\n{msg}")
+        raise RuntimeError(f"nvcc failed:\n{msg}")
     if procs or not os.path.exists(LIB) or any(os.path.getmtime(o) > os.path.getmtime(LIB) for o in objects):
         tmp = LIB + f".tmp{os.getpid()}"
         cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objects, "-cudart", "static"]
@@ -108,6 +115,10 @@ def build(verbose: bool = False, force: bool = False, extra_flags=()) -> str:
             print(" ".join(cmd), flush=True)
         subprocess.check_call(cmd)
         os.replace(tmp, LIB)
+    if fast_error is not None:
+        if os.path.exists(FAST):                           # made from older sources
+            os.remove(FAST)
+        warnings.warn(f"{FAST} was not built, its Python entry points will raise:\n{fast_error}", RuntimeWarning)
     return LIB
 
 
