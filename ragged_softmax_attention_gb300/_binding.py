@@ -320,7 +320,9 @@ def _fast():
     if _fast_module is None:
         import importlib.machinery
         import importlib.util
-        path = os.path.join(_HERE, "_fw_fast.so")
+
+        from .build import fast_path
+        path = fast_path()
         if not os.path.exists(path):
             raise RuntimeError(f"{path} is not built; run ragged_softmax_attention_gb300.build.build() first, which "
                                "warns when the module cannot be compiled")

@@ -3,8 +3,10 @@
 Each .cu under csrc/ is compiled to an object in parallel, then linked into
 one shared library with the CUDA runtime linked statically.  Objects are
 rebuilt when their source or any header changed.  Beside it, g++ compiles
-csrc/fast_binding.cpp against torch's headers into _fw_fast.so, the Python
-entry points of the operators whose calls take a few microseconds.  The library
+csrc/fast_binding.cpp against torch's headers into a module, the Python entry
+points of the operators whose calls take a few microseconds.  Its file name holds
+the versions it was compiled for, so that no other torch or interpreter loads it
+(their objects may be laid out otherwise).  The library
 does not depend on it: where the module cannot be compiled (no g++, no headers of
 Python or torch), build() links the library all the same and warns.
 """
@@ -23,7 +25,6 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfw_attn.so")
 FAST_SRC = os.path.join(CSRC, "fast_binding.cpp")
-FAST = os.path.join(HERE, "_fw_fast.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
               "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]
@@ -40,6 +41,14 @@ def _newest_header() -> float:
     hdrs = glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
         glob.glob(os.path.join(ROOT, "include", "*.h"))
     return max((os.path.getmtime(h) for h in hdrs), default=0.0)
+
+
+def fast_path() -> str:
+    """The Python module's file for the running interpreter and its torch."""
+    import sysconfig
+
+    import torch
+    return os.path.join(HERE, f"_fw_fast.{sysconfig.get_config_var('SOABI')}-torch-{torch.__version__}.so")
 
 
 def _fast_command(out: str) -> list:
@@ -66,18 +75,18 @@ def build(verbose: bool = False, force: bool = False, extra_flags=()) -> str:
     hdr_time = _newest_header()
     procs = []
     objects = []
-    fast_stale = force or not os.path.exists(FAST) or os.path.getmtime(FAST) < max(
-        os.path.getmtime(FAST_SRC), os.path.getmtime(os.path.join(ROOT, "include", "fw_attn.h")))
-    fast_tmp = FAST + f".tmp{os.getpid()}"
-    fast_proc = fast_error = None
-    if fast_stale:
-        try:
+    fast = fast_proc = fast_error = None
+    try:
+        fast = fast_path()
+        fast_tmp = fast + f".tmp{os.getpid()}"
+        if force or not os.path.exists(fast) or os.path.getmtime(fast) < max(
+                os.path.getmtime(FAST_SRC), os.path.getmtime(os.path.join(ROOT, "include", "fw_attn.h"))):
             fast_cmd = _fast_command(fast_tmp)
             if verbose:
                 print(" ".join(fast_cmd), flush=True)
             fast_proc = subprocess.Popen(fast_cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
-        except (ImportError, OSError) as e:                # no torch, no g++
-            fast_error = str(e)
+    except (ImportError, OSError) as e:                    # no torch, no g++
+        fast_error = str(e)
     for src in sources:
         obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
         objects.append(obj)
@@ -104,7 +113,7 @@ def build(verbose: bool = False, force: bool = False, extra_flags=()) -> str:
         if fast_proc.returncode != 0:
             fast_error = out.decode(errors="replace")
         else:
-            os.replace(fast_tmp, FAST)
+            os.replace(fast_tmp, fast)
     if failed:
         msg = "\n".join(f"--- {o}\n{t}" for o, t in failed)
         raise RuntimeError(f"nvcc failed:\n{msg}")
@@ -116,9 +125,10 @@ def build(verbose: bool = False, force: bool = False, extra_flags=()) -> str:
         subprocess.check_call(cmd)
         os.replace(tmp, LIB)
     if fast_error is not None:
-        if os.path.exists(FAST):                           # made from older sources
-            os.remove(FAST)
-        warnings.warn(f"{FAST} was not built, its Python entry points will raise:\n{fast_error}", RuntimeWarning)
+        if fast and os.path.exists(fast):                  # made from older sources
+            os.remove(fast)
+        warnings.warn(f"{fast or '_fw_fast'} was not built, its Python entry points will raise:\n{fast_error}",
+                      RuntimeWarning)
     return LIB
 
 

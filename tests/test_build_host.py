@@ -18,7 +18,7 @@ def tree(tmp_path, monkeypatch):
     monkeypatch.setattr(fwbuild, "_nvcc", lambda: str(nvcc))
     monkeypatch.setattr(fwbuild, "BUILD", str(tmp_path / "_build"))
     monkeypatch.setattr(fwbuild, "LIB", str(tmp_path / "libfw_attn.so"))
-    monkeypatch.setattr(fwbuild, "FAST", str(tmp_path / "_fw_fast.so"))
+    monkeypatch.setattr(fwbuild, "fast_path", lambda: str(tmp_path / "_fw_fast.so"))
     return tmp_path
 
 
@@ -60,3 +60,26 @@ def test_an_up_to_date_module_stays(tree, monkeypatch):
         assert len(calls) == 1
         fwbuild.build(force=True)
     assert len(calls) == 2
+
+
+def test_a_module_of_other_versions_is_not_loaded(tree, monkeypatch):
+    """Another torch makes a module of its own beside the first, and looks only there."""
+    import torch
+
+    from ragged_softmax_attention_gb300 import _binding
+    monkeypatch.undo()
+    monkeypatch.setattr(fwbuild, "HERE", str(tree))
+    monkeypatch.setattr(fwbuild, "_nvcc", lambda: str(tree / "nvcc"))
+    monkeypatch.setattr(fwbuild, "BUILD", str(tree / "_build"))
+    monkeypatch.setattr(fwbuild, "LIB", str(tree / "libfw_attn.so"))
+    monkeypatch.setattr(fwbuild, "_fast_command", lambda out: ["touch", out])
+    fwbuild.build()
+    first = fwbuild.fast_path()
+    assert os.path.exists(first)
+    monkeypatch.setattr(torch, "__version__", "99.0")
+    assert fwbuild.fast_path() != first
+    monkeypatch.setattr(_binding, "_fast_module", None)
+    with pytest.raises(RuntimeError, match="not built"):
+        _binding._fast()
+    fwbuild.build()
+    assert os.path.exists(first) and os.path.exists(fwbuild.fast_path())
