@@ -364,7 +364,8 @@ fw_status_t fw_varlen_prefill(const fw_tensor_t *q, const fw_tensor_t *k, const 
  * rounded to FP16.
  *
  * Supported: D in {128, 256} (FP8: 128), 1 <= T <= 256, B <= 4096, page sizes,
- * strides and alignment of fw_paged_decode; any Hq / Hkv.
+ * strides and alignment of fw_paged_decode; any Hq / Hkv, B * T * Hq and
+ * Hq * D / 8 below 2^31.
  *
  * Split-KV as in fw_paged_decode, with its own ranges (one per CTA;
  * FW_OPT_DECODE_CHUNK_TOKENS does not apply, FW_OPT_MAX_CTAS does).  Two

@@ -1038,7 +1038,9 @@ static fw_status_t build_tree(const fw_tensor_t *q, const fw_tensor_t *k_cache, 
         if (P < 1 || max_pages < 1) return fail(FW_ERR_INVALID_ARG, "empty page pool or block table");
         if (P > (1LL << 31) - 1 || max_pages * ps > (1LL << 30))
             return fail(FW_ERR_UNSUPPORTED, "page pool or sequence bound too large");
-        if (B * T * Hq >= (1LL << 31)) return fail(FW_ERR_UNSUPPORTED, "too many query rows");
+        // (The last: a draft's 16-byte units are counted in 32 bits.)
+        if (B * T * Hq >= (1LL << 31) || Hq * (D / 8) >= (1LL << 31))
+            return fail(FW_ERR_UNSUPPORTED, "too many query rows or heads");
         if (fw_status_t s = check_tma_layout(q, "q")) return s;
         if (fw_status_t s = check_tma_layout(k_cache, "k_cache")) return s;
         if (fw_status_t s = check_tma_layout(v_cache, "v_cache")) return s;
