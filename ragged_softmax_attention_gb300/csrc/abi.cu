@@ -1351,6 +1351,8 @@ fw_status_t fw_kv_commit(const fw_tensor_t *path, const fw_tensor_t *path_lens, 
         if (fw::extents_overlap(new_lens, 4, base_lens, 4))
             return fail(FW_ERR_INVALID_ARG, "new_lens overlaps base_lens");
     }
+    for (const fw_tensor_t *t : {path, path_lens, base_lens, block_table, static_cast<const fw_tensor_t *>(new_lens)})
+        if (share(t, k_cache) || share(t, v_cache)) return fail(FW_ERR_INVALID_ARG, "a cache overlaps a vector of the call");
     if (B == 0) return ok();
     fw::CommitParams p{};
     p.B = (int)B; p.A = (int)A; p.Hkv = (int)Hkv; p.ps = (int)ps; p.layers = (int)num_layers;
