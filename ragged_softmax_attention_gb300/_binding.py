@@ -340,7 +340,9 @@ def _on(stream, call, *args):
     """call(*args), on `stream` when one is given."""
     if stream is None:
         return call(*args)
-    first = next(a for a in args if isinstance(a, torch.Tensor))
+    first = next((a for a in args if isinstance(a, torch.Tensor)), None)
+    if first is None:
+        return call(*args)                      # which names what is missing
     if stream.device != first.device:
         raise ValueError("the stream must be of the tensors' device")
     with torch.cuda.stream(stream):

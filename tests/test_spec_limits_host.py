@@ -29,3 +29,12 @@ def test_commit_vectors_inside_a_cache(fwlib, name, shape, cache):  # noqa: F811
         a[c] = fake([12, 16, 2, 128], BF, 0x100000 + 2 * page * i, [2 * page + 256, 256, 128, 1])
     a[name] = fake(shape, I32, 0x100000 + 4 * page)
     assert call_commit(fwlib, a) != INVALID, fwlib.load_library().fw_last_error()
+
+
+def test_a_stream_without_tensors(fwlib):  # noqa: F811
+    """The error names the argument, with a stream as without one."""
+    for stream in (None, object()):
+        with pytest.raises(TypeError, match="parents is required"):
+            fwlib.tree_mask(None, stream=stream)
+        with pytest.raises(TypeError, match="q must be a torch.Tensor"):
+            fwlib.paged_decode_tree([1], None, None, None, None, None, 1.0, stream=stream)
