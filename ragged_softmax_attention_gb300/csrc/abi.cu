@@ -10,6 +10,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <limits>
 #include <mutex>
 #include <vector>
 
@@ -1075,11 +1076,12 @@ static fw_status_t build_tree(const fw_tensor_t *q, const fw_tensor_t *k_cache, 
     p.mask_stride[1] = tree_mask->stride[1];
     p.out = out->data;
     p.lse = lse ? static_cast<float *>(lse->data) : nullptr;
-    // A scale of zero would turn the -inf of hidden keys into NaN: the least
-    // magnitude used leaves every score it multiplies at zero for the exponential.
+    // A scale of zero would turn the -inf of hidden keys into NaN: the least positive
+    // number leaves every score it multiplies at zero for the exponential.  (No larger
+    // one does: finite scores reach 2^128, and scales down there have their use.)
     p.scale_log2 = scale * k_scale * 1.4426950408889634f;
     if (!std::isfinite(p.scale_log2)) return fail(FW_ERR_INVALID_ARG, "scale * k_scale overflows");
-    if (std::fabs(p.scale_log2) < 1e-30f) p.scale_log2 = std::copysign(1e-30f, p.scale_log2);
+    if (p.scale_log2 == 0.f) p.scale_log2 = std::numeric_limits<float>::denorm_min();
     p.out_scale = v_scale;
     // Row tiles: whole drafts of up to 128 rows, or 128 heads of one draft.
     if (p.G <= 128) {

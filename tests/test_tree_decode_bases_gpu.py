@@ -133,3 +133,16 @@ def test_score_factors_that_vanish(fw, D, kv8, T, Hq, Hkv, what):
     if what == "k_scale":
         x["k_scale"] = 1e-20 if kv8 else 1.0
     run_tight(fw, x, what)
+
+
+@pytest.mark.parametrize("turn", [1, -1])
+@pytest.mark.parametrize("T,Hq,Hkv", ROWS)
+@pytest.mark.parametrize("D,kv8", KINDS)
+def test_small_scales_of_large_scores(fw, D, kv8, T, Hq, Hkv, turn):
+    """Queries and keys of large magnitudes under a scale that undoes them."""
+    x = make(2, T, Hq, Hkv, D, 32, [700, T], None, "tree", kv8=kv8, seed=83)
+    x["q"] *= 2.0 ** (110 if kv8 else 58)
+    if not kv8:
+        x["k_cache"] *= 2.0 ** 52
+    x["scale"] *= turn * 2.0 ** -110
+    run_tight(fw, x, "large scores")
