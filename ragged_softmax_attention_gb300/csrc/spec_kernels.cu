@@ -204,7 +204,10 @@ __global__ void __launch_bounds__(kTableThreads) page_table_kernel(const __grid_
 #pragma unroll 1
     for (int b = tid * per; b < min(p.B, (tid + 1) * per); ++b) {
         const TableRow r = table_row(p, b);
-        tok[b] = clamp31(v[0]);
+        // (Padded places need the rows' own counts alone, which wrapped sums still give
+        // behind a contradictory count.)
+        tok[b] = p.padded ? (int)v[0] : clamp31(v[0]);
+        if (kFill && p.cu_new && blockIdx.x == 0) p.cu_new[b] = clamp31(v[0]);
         need[b] = clamp31(v[1]);
         back[b] = clamp31(v[2]);
         v[0] += max(r.fresh, 0);
@@ -221,7 +224,8 @@ __global__ void __launch_bounds__(kTableThreads) page_table_kernel(const __grid_
     if (taken) atomicMax(&s_taken, taken);
     if (given) atomicMax(&s_back, given);
     if (tid == 0) {
-        tok[p.B] = clamp31(total[0]);
+        tok[p.B] = p.padded ? (int)total[0] : clamp31(total[0]);
+        if (kFill && p.cu_new && blockIdx.x == 0) p.cu_new[p.B] = clamp31(total[0]);
         need[p.B] = clamp31(total[1]);
         back[p.B] = clamp31(total[2]);
         bad |= !p.padded && total[0] > p.N;
@@ -352,9 +356,6 @@ __global__ void __launch_bounds__(kTableThreads) page_table_kernel(const __grid_
 #pragma unroll 1
             for (int64_t i = b0 + tid; i < min((int64_t)p.N, b0 + per_block); i += nthreads) p.slots[i] = -1;
         }
-        if (blockIdx.x == 0 && p.cu_new)
-#pragma unroll 1
-            for (int b = tid; b <= p.B; b += nthreads) p.cu_new[b] = tok[b];
     }
     if (write_state && blockIdx.x == 0) {
         if constexpr (!kFill) pdl_wait();             // the fill has read what this overwrites
