@@ -146,3 +146,23 @@ def test_small_scales_of_large_scores(fw, D, kv8, T, Hq, Hkv, turn):
         x["k_cache"] *= 2.0 ** 52
     x["scale"] *= turn * 2.0 ** -110
     run_tight(fw, x, "large scores")
+
+
+@pytest.mark.parametrize("T,Hq,Hkv", ROWS)
+@pytest.mark.parametrize("D,kv8", KINDS)
+def test_orders_of_dimensions(fw, D, kv8, T, Hq, Hkv):
+    """Caches with a page's heads before its slots, queries with heads before drafts,
+    outputs and LSE with the batch last."""
+    x = make(3, T, Hq, Hkv, D, 32, [700, T, 130], [T, T, T - 2], "tree", kv8=kv8, seed=85)
+    g = on_gpu(x)
+    for name in ("k_cache", "v_cache"):
+        raw = g[name].view(torch.uint8) if kv8 else g[name]
+        g[name] = raw.permute(0, 2, 1, 3).contiguous().view(g[name].dtype).permute(0, 2, 1, 3)
+    g["q"] = g["q"].permute(0, 2, 1, 3).contiguous().permute(0, 2, 1, 3)
+    plain = fw.paged_decode_tree(**on_gpu(x))
+    out = torch.full((Hq, T, 3, D), 7.0, dtype=torch.bfloat16, device="cuda").permute(2, 1, 0, 3)
+    lse = torch.full((T, 3, Hq), 7.0, device="cuda").permute(1, 0, 2)
+    fw.paged_decode_tree(**g, out=out, lse=lse)
+    torch.cuda.synchronize()
+    assert fw.device_status() == 0
+    assert torch.equal(out, plain[0]) and torch.equal(lse, plain[1])
