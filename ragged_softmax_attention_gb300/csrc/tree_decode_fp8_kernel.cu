@@ -22,11 +22,13 @@
 // the values of keys nobody sees.
 //
 // Measured: 32 requests of 512 .. 16,384 keys, 16 drafts of 40/8 heads, 529 MB in
-// 133 us, 0.59 of the measured copy rate.  A key tile takes some 2,000 cycles: the
-// widened V tile's round (convert 1,100, PV behind QK, the slot back) and the
-// softmax of two warpgroups in turn; more slots for widened values make it slower
-// (139 us), P as two E4M3 terms would need no widening but loses the weights below
-// 2^-17 of the largest.
+// 134.5 us, 0.58 of the measured copy rate; with 32 drafts (two row tiles) 227 us.  A
+// key tile takes some 1,900 cycles (3,480): the widened V tile's round (convert
+// 1,100, PV behind QK, the slot back) and the softmax of two warpgroups in turn, 103
+// us in all; starts and ends of pieces take 18, the way to the first scores 8 of them
+// (13 with two row tiles, whose queries the converting warps split as well).  More
+// slots for widened values make it slower (139 us), P as two E4M3 terms would need no
+// widening but loses the weights below 2^-17 of the largest.
 //
 // Warp roles: 0 copies keys and values, 1 and 2 issue MMAs, 3 works out the
 // pieces and copies queries, 4-7 convert, 8-15 softmax (a warpgroup per stream, or two for one:

@@ -29,11 +29,12 @@
 // 6,782 GB/s): 16 requests of 512 .. 8,192 keys, 16 drafts of 40/8 heads (NT = 1)
 // 279 MB in 56 us, 0.74 of copy: inside a piece HBM is the bound, the rest is the
 // first tile's way (6 us), uneven ends and the merge.  Head dim 256, 8 requests, 24
-// drafts of 16/16 heads: 512 MB in 100 us, 0.76.  64 requests of up to 32,768 keys, 32
+// drafts of 16/16 heads: 512 MB in 99 us, 0.76.  64 requests of up to 32,768 keys, 32
 // drafts (NT = 2): 4.84 GB in 860 .. 955 us by machine, 0.75 .. 0.83; a step takes
-// 3,050 cycles, the chain S, softmax (1,390), PV, next QK of two streams in turn,
+// 3,060 cycles, the chain S, softmax (1,390), PV, next QK of two streams in turn,
 // where HBM's share is 2,700.  16 requests with 121 drafts of 32/8 heads (NT = 2):
-// 134 GFLOP in 128 us, 1.05 PFLOP/s, the same chain.
+// 134 GFLOP in 128 us, 1.05 PFLOP/s: the same chain takes 95 us of it, the first
+// scores 8, pieces' ends 10, the last CTA and the merge 14.
 //
 // Warp roles: warp 0 copies (Q, then K and V tiles through a ring of 32 KiB
 // slots in the order the MMAs take them), warps 1 and 2 issue the MMAs (of a
