@@ -1078,10 +1078,11 @@ static fw_status_t build_tree(const fw_tensor_t *q, const fw_tensor_t *k_cache, 
     p.lse = lse ? static_cast<float *>(lse->data) : nullptr;
     // A scale of zero would turn the -inf of hidden keys into NaN: the least positive
     // number leaves every score it multiplies at zero for the exponential.  (No larger
-    // one does: finite scores reach 2^128, and scales down there have their use.)
+    // one does: finite scores reach 2^128, and scales down there have their use.  Over
+    // FP8 caches, whose rows bring powers of two of their own, the kernel sees to it.)
     p.scale_log2 = scale * k_scale * 1.4426950408889634f;
     if (!std::isfinite(p.scale_log2)) return fail(FW_ERR_INVALID_ARG, "scale * k_scale overflows");
-    if (p.scale_log2 == 0.f) p.scale_log2 = std::numeric_limits<float>::denorm_min();
+    if (p.scale_log2 == 0.f && !kv8) p.scale_log2 = std::numeric_limits<float>::denorm_min();
     p.out_scale = v_scale;
     // Row tiles: whole drafts of up to 128 rows, or 128 heads of one draft.
     if (p.G <= 128) {

@@ -613,8 +613,8 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
             // The row's exponent is read before the record goes back: unit k + 4,
             // which reuses its place, cannot come before that.
             if (u.b >= 0) mbar_wait(&q_ready[k % C::kSched], (k / C::kSched) & 1, wc);
-            // (Bounded from below: a small scale times the 2^-126 of a row of zeros would
-            // vanish and turn the -inf of hidden keys into NaN.  Sums here
+            // (Bounded from below: a scale of zero, or a small one times the 2^-126 of a row
+            // of zeros, would turn the -inf of hidden keys into NaN.  Sums here
             // stay below 2^24, so under the bound every score is zero to the exponential.)
             const float rs = fmaxf(fabsf(p.scale_log2) *
                                        __int_as_float((127 - q_exp[(k % C::kSched * NT + x) * 128 + row]) << 23),

@@ -166,3 +166,14 @@ def test_orders_of_dimensions(fw, D, kv8, T, Hq, Hkv):
     torch.cuda.synchronize()
     assert fw.device_status() == 0
     assert torch.equal(out, plain[0]) and torch.equal(lse, plain[1])
+
+
+@pytest.mark.parametrize("T,Hq,Hkv", ROWS)
+@pytest.mark.parametrize("D,kv8", KINDS)
+def test_scale_zero_of_the_largest_queries(fw, D, kv8, T, Hq, Hkv):
+    """Every visible key weighs the same whatever the magnitude of the queries."""
+    x = make(3, T, Hq, Hkv, D, 32, [700, T, 130], [T, T, T - 2], "tree", kv8=kv8, seed=87)
+    x["q"] *= 2.0 ** (125 if kv8 else 115)                 # BF16 scores stay finite in FP32
+    x["scale"] = 0.0
+    assert torch.isfinite(x["q"]).all()
+    run_tight(fw, x, "largest queries")
