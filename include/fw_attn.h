@@ -326,8 +326,10 @@ fw_status_t fw_varlen_prefill(const fw_tensor_t *q, const fw_tensor_t *k, const 
  *
  * The draft tokens of request b take the last draft_lens[b] of its seq_lens[b]
  * keys, in the order of the tree's nodes (every parent before its children).
- * Outputs must not share elements with inputs (but where said otherwise) or with
- * one another, nor hold an element twice (an expanded view).
+ * Outputs and workspaces must not share elements with inputs (but where said
+ * otherwise) or with one another, nor hold an element twice (an expanded view):
+ * such calls are refused.  Views of one buffer that have no element in common are
+ * fine.
  * ---------------------------------------------------------------------------
  */
 
