@@ -482,6 +482,102 @@ fw_status_t fw_kv_commit(const fw_tensor_t *path, const fw_tensor_t *path_lens, 
                          fw_tensor_t *v_cache, fw_tensor_t *new_lens, fw_stream_t stream);
 
 /*
+ * Verification of drafted trees against the target's probabilities: the path that
+ * fw_kv_commit takes, and the token that follows it.
+ *
+ *   tokens      [B, T]  I32: the drafts
+ *   parents     [B, T]  I32, as in fw_tree_mask
+ *   draft_lens  [B]     I32 or NULL (T everywhere); clamped to 0 .. T
+ *   target_probs [B, R, V]  F32, V <= 2^24: the target's probabilities of the token that
+ *                       follows.  R = T: row t follows draft t, and draft 0 is the
+ *                       token that the last step gave (next_tokens): it is accepted
+ *                       as it is, other drafts without a parent are nobody's.  R = T +
+ *                       1: row 0 follows the committed context, row t + 1 draft t
+ *   draft_probs [B, R, V]   F32 or NULL: the probabilities that the children of a row's
+ *                       node were drawn from, one after another.  NULL: each draft
+ *                       was proposed with certainty (the draft model's likeliest
+ *                       tokens, a lookup)
+ *   uniforms    [B, T + 1]  F32 in [0, 1): entry t decides draft t, entry T draws the
+ *                       next token
+ *   path        [B, A]  I32, written: accepted drafts from the root down, then -1; no
+ *                       more than A are accepted.  1 <= A <= 256
+ *   path_lens   [B]     I32, written
+ *   next_tokens [B]     I32, written
+ *
+ * With p the row of the node reached and q the draft model's (1 at a draft's token, 0
+ * elsewhere, without one), R = p and S = 1 at first, the node's children are tried in
+ * order: draft c is accepted when uniforms[c] * q(c) < R(c) / S; else R becomes
+ * max(R - S q, 0) and S its sum (unless that is 0: then both stay).  At the end of the
+ * path next_tokens is the first token x with R(0) + ... + R(x) > uniforms[T] * sum R.
+ * Accepted drafts and next token together are so distributed as the target's samples.
+ * Rows need not add up to 1 exactly; sums are exact in units of 2^-60, the same in
+ * every run.
+ *
+ * Probabilities below 0 and NaN count as 0, those above 1 as 1.  A parent outside -1 ..
+ * t - 1 is taken as -1; a draft whose token is outside 0 .. V - 1 is passed over; a row
+ * that adds up to 4 or more stops there.  These record FW_ERR_INVALID_ARG in the device
+ * status word, and so does a request with nothing to draw from (R all zero, or no drafts
+ * and R = T), whose next token is -1.  1 <= T <= 256.  One launch, no workspace.
+ */
+fw_status_t fw_verify_drafts(const fw_tensor_t *tokens, const fw_tensor_t *parents, const fw_tensor_t *draft_lens,
+                             const fw_tensor_t *target_probs, const fw_tensor_t *draft_probs,
+                             const fw_tensor_t *uniforms, fw_tensor_t *path, fw_tensor_t *path_lens,
+                             fw_tensor_t *next_tokens, fw_stream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * What comes before the attention: norms and positions of queries and keys.
+ * ---------------------------------------------------------------------------
+ *
+ * Root-mean-square norm of every query and key head, then the rotation by position:
+ *   y = x * rsqrt(mean(x^2) + eps) * weight
+ *   (y_i, y_i') = (y_i cos a - y_i' sin a, y_i' cos a + y_i sin a),
+ *   a = positions[axis_map[i], n] * inv_freq[i]
+ *
+ *   q [N, Hq, D], k [N, Hkv, D]  BF16, last dim contiguous (columns of one projection,
+ *                  say), strides multiples of 8 elements, 16-byte aligned; D in {64,
+ *                  128, 256}
+ *   q_weight, k_weight  [D]  BF16 or F32; NULL: those heads are not normed
+ *   eps            finite, >= 0
+ *   inv_freq       [F]  F32, finite; the first 2 F elements of a head rotate, the rest
+ *                  is normed alone.  F a multiple of 4, 2 F <= D
+ *   positions      [N] or [axes, N]  I32, any value; axes <= 64
+ *   axis_map       [F]  I32: the axis (time, height, width, ...) whose position turns
+ *                  pair i; NULL: axis 0 (required with several axes)
+ *   interleaved    0: i' = i + F; else pairs are neighbours, (2 i, 2 i + 1)
+ *   q_out [N, Hq, D], k_out [N, Hkv, D]  BF16, written; may be q and k themselves
+ *
+ * Arithmetic in FP32, one rounding at the end; angles exact to 2^-32 of a turn for every
+ * position.  An axis outside 0 .. axes - 1 is taken as 0 and records FW_ERR_INVALID_ARG
+ * in the device status word.  Squares are added in FP32: a head whose elements pass
+ * 2^60 comes out as zeros.  One launch, no workspace.
+ */
+fw_status_t fw_qk_norm_rope(const fw_tensor_t *q, const fw_tensor_t *k, const fw_tensor_t *q_weight,
+                            const fw_tensor_t *k_weight, float eps, const fw_tensor_t *inv_freq,
+                            const fw_tensor_t *positions, const fw_tensor_t *axis_map, int32_t interleaved,
+                            fw_tensor_t *q_out, fw_tensor_t *k_out, fw_stream_t stream);
+
+/*
+ * The same, with the keys and the values v [N, Hkv, D] (as k; not normed, not rotated)
+ * put straight into their cache rows:
+ *
+ *   slot_mapping   N I32 entries, [N] or [B, L], contiguous; -1 (any negative entry): the
+ *                  token's key and value are not written (fw_kv_append writes such a
+ *                  token to the layer's row 0); its query is
+ *   layer_base_rows, k_cache, v_cache, k_scale, v_scale  as fw_kv_append; FP8 caches
+ *                  take E4M3(y / scale) of the FP32 value.  v and v_cache may both be NULL
+ *
+ * Nothing else in the caches changes.  A row at or past pages * ps records
+ * FW_ERR_INVALID_ARG and is skipped.  Two tokens must not share a slot.
+ */
+fw_status_t fw_qk_norm_rope_append(const fw_tensor_t *q, const fw_tensor_t *k, const fw_tensor_t *v,
+                                   const fw_tensor_t *q_weight, const fw_tensor_t *k_weight, float eps,
+                                   const fw_tensor_t *inv_freq, const fw_tensor_t *positions,
+                                   const fw_tensor_t *axis_map, int32_t interleaved, const fw_tensor_t *slot_mapping,
+                                   int64_t layer_base_rows, fw_tensor_t *q_out, fw_tensor_t *k_cache,
+                                   fw_tensor_t *v_cache, float k_scale, float v_scale, fw_stream_t stream);
+
+/*
  * Caller-owned workspace for the CURRENT device (ptr = NULL, bytes = 0 returns
  * to the internal buffer).  The library never frees it.  Calls on one device
  * that share the workspace must be ordered (same stream, or synchronised).

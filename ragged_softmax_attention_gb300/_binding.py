@@ -113,6 +113,12 @@ def load_library(path: Optional[str] = None):
     lib.fw_build_page_tables.argtypes = [V, V, V, V, V, I64, V, V, V, V, V, V]
     lib.fw_kv_commit.restype = S
     lib.fw_kv_commit.argtypes = [V, V, V, V, I64, V, V, V, V]
+    lib.fw_verify_drafts.restype = S
+    lib.fw_verify_drafts.argtypes = [V] * 10
+    lib.fw_qk_norm_rope.restype = S
+    lib.fw_qk_norm_rope.argtypes = [V, V, V, V, F, V, V, V, I32, V, V, V]
+    lib.fw_qk_norm_rope_append.restype = S
+    lib.fw_qk_norm_rope_append.argtypes = [V, V, V, V, V, F, V, V, V, I32, V, I64, V, V, V, F, F, V]
     _lib = lib
     return lib
 
@@ -302,7 +308,7 @@ def varlen_prefill(q, k, v, cu_seqlens_q, cu_seqlens_k, causal, scale, out=None,
     return out, lse
 
 
-# ------------------------------------------------------ speculative decoding
+# ---------------------- speculative decoding, and what is around a step's attention
 #
 # A step of these takes the GPU a few microseconds, so their marshalling is in
 # C++ (csrc/fast_binding.cpp).  They run on the device of their tensors,
@@ -310,7 +316,8 @@ def varlen_prefill(q, k, v, cu_seqlens_q, cu_seqlens_k, causal, scale, out=None,
 # stream the kernels run on: the current one, or `stream`.
 
 _FAST_ENTRIES = ("fw_paged_decode_tree", "fw_paged_decode_tree_workspace_size", "fw_tree_mask",
-                 "fw_build_page_tables", "fw_kv_commit")
+                 "fw_build_page_tables", "fw_kv_commit", "fw_verify_drafts", "fw_qk_norm_rope",
+                 "fw_qk_norm_rope_append")
 _fast_module = None
 
 
@@ -392,6 +399,39 @@ def kv_commit(path, path_lens, base_lens, block_table, k_cache, v_cache, num_lay
     base_lens + path_lens."""
     return _on(stream, (_fast_module or _fast()).kv_commit, path, path_lens, base_lens, block_table, k_cache, v_cache,
                num_layers, new_lens)
+
+
+def verify_drafts(tokens, parents, target_probs, uniforms, draft_probs=None, draft_lens=None, max_path=None, path=None,
+                  path_lens=None, next_tokens=None, stream=None):
+    """fw_verify_drafts: drafts tokens / parents [B, T] against target_probs [B, T,
+    V] (row t follows draft t; draft 0 is accepted as it is) or [B, T + 1, V] (row
+    0 follows the committed context), drawn from draft_probs (the same shape; None:
+    proposed with certainty); uniforms [B, T + 1].  Returns (path [B, max_path]
+    padded with -1, path_lens [B], next_tokens [B]), the first two as kv_commit
+    takes them; max_path defaults to T."""
+    return _on(stream, (_fast_module or _fast()).verify_drafts, tokens, parents, target_probs, uniforms, draft_probs,
+               draft_lens, max_path, path, path_lens, next_tokens)
+
+
+def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e-6, axis_map=None, interleaved=False,
+                 q_out=None, k_out=None, stream=None):
+    """fw_qk_norm_rope: q [N, Hq, D] and k [N, Hkv, D] normed for each head (where a
+    weight [D] is given) and rotated by positions [N] (or [axes, N] with axis_map
+    [F] naming each frequency's axis) times inv_freq [F]; interleaved: pairs are
+    neighbours.  Returns (q_out, k_out), which may be q and k."""
+    return _on(stream, (_fast_module or _fast()).qk_norm_rope, q, k, positions, inv_freq, q_weight, k_weight, eps,
+               axis_map, interleaved, q_out, k_out)
+
+
+def qk_norm_rope_append(q, k, v, positions, inv_freq, slot_mapping, layer_base_rows, k_cache, v_cache, q_weight=None,
+                        k_weight=None, eps=1e-6, axis_map=None, interleaved=False, k_scale=1.0, v_scale=1.0, q_out=None,
+                        stream=None):
+    """fw_qk_norm_rope_append: qk_norm_rope with the keys, and the values v [N, Hkv,
+    D] as they are, written to cache rows layer_base_rows + slot_mapping[n] (a
+    negative slot: not written) of k_cache / v_cache.  v and v_cache may both be
+    None.  Returns q_out."""
+    return _on(stream, (_fast_module or _fast()).qk_norm_rope_append, q, k, v, positions, inv_freq, slot_mapping,
+               layer_base_rows, k_cache, v_cache, q_weight, k_weight, eps, axis_map, interleaved, k_scale, v_scale, q_out)
 
 
 def set_workspace(buf: Optional[torch.Tensor], stream=None):

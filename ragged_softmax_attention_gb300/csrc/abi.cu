@@ -1387,4 +1387,265 @@ fw_status_t fw_kv_commit(const fw_tensor_t *path, const fw_tensor_t *path_lens, 
     return ok();
 }
 
+// ------------------------------------------------- norms, rotation, verification
+
+}  // extern "C"
+
+// A norm's weights: D values, BF16 or F32.
+static fw_status_t check_weight(const fw_tensor_t *t, const char *name, int64_t D) {
+    if (!t) return FW_OK;
+    if (t->dtype != FW_BF16 && t->dtype != FW_F32)
+        return fail(FW_ERR_INVALID_ARG, "%s must be BF16 or F32", name);
+    if (fw_status_t s = check_tensor(t, name, 1, t->dtype)) return s;
+    if (t->shape[0] != D) return fail(FW_ERR_INVALID_ARG, "%s must hold %lld values", name, (long long)D);
+    if (reinterpret_cast<uintptr_t>(t->data) % element_bytes(t)) return fail(FW_ERR_INVALID_ARG, "%s misaligned", name);
+    return FW_OK;
+}
+
+// Whether b is a itself: the same elements in the same places.
+static bool same_tensor(const fw_tensor_t *a, const fw_tensor_t *b) {
+    if (a->data != b->data || a->dtype != b->dtype || a->ndim != b->ndim) return false;
+    for (int i = 0; i < a->ndim; ++i)
+        if (a->shape[i] != b->shape[i] || (a->shape[i] > 1 && a->stride[i] != b->stride[i])) return false;
+    return true;
+}
+
+// Shared body of fw_qk_norm_rope (k_out) and fw_qk_norm_rope_append (slots, caches).
+static fw_status_t norm_rope(const fw_tensor_t *q, const fw_tensor_t *k, const fw_tensor_t *v,
+                             const fw_tensor_t *q_weight, const fw_tensor_t *k_weight, float eps,
+                             const fw_tensor_t *inv_freq, const fw_tensor_t *positions, const fw_tensor_t *axis_map,
+                             int32_t interleaved, const fw_tensor_t *slots, int64_t layer_base_rows,
+                             const fw_tensor_t *q_out, const fw_tensor_t *k_out, const fw_tensor_t *k_cache,
+                             const fw_tensor_t *v_cache, float k_scale, float v_scale, bool append,
+                             cudaStream_t stream) {
+    if (fw_status_t s = check_tensor(q, "q", 3, FW_BF16)) return s;
+    if (fw_status_t s = check_tensor(k, "k", 3, FW_BF16)) return s;
+    const int64_t N = q->shape[0], Hq = q->shape[1], D = q->shape[2], Hkv = k->shape[1];
+    if (k->shape[0] != N || k->shape[2] != D) return fail(FW_ERR_INVALID_ARG, "k must be [N, Hkv, D] as q is [N, Hq, D]");
+    if (D != 64 && D != 128 && D != 256)
+        return fail(FW_ERR_UNSUPPORTED, "norm and rotation head dim %lld: supported 64, 128 and 256", (long long)D);
+    if (Hq < 1 || Hkv < 1) return fail(FW_ERR_INVALID_ARG, "no heads");
+    if (Hq >= (1LL << 24) || Hkv >= (1LL << 24) || N >= (1LL << 40)) return fail(FW_ERR_UNSUPPORTED, "too many tokens or heads");
+    if (fw_status_t s = check_weight(q_weight, "q_weight", D)) return s;
+    if (fw_status_t s = check_weight(k_weight, "k_weight", D)) return s;
+    if (!std::isfinite(eps) || eps < 0.f) return fail(FW_ERR_INVALID_ARG, "eps must be finite and not negative");
+    if (fw_status_t s = check_tensor(inv_freq, "inv_freq", 1, FW_F32)) return s;
+    const int64_t rot = 2 * inv_freq->shape[0];
+    if (rot < 8 || rot > D || rot % 8)
+        return fail(FW_ERR_UNSUPPORTED, "inv_freq holds %lld frequencies: supported multiples of 4, at most D / 2",
+                    (long long)inv_freq->shape[0]);
+    if (reinterpret_cast<uintptr_t>(inv_freq->data) % 4) return fail(FW_ERR_INVALID_ARG, "inv_freq misaligned");
+    if (!positions) return fail(FW_ERR_INVALID_ARG, "positions is NULL");
+    if (positions->ndim != 1 && positions->ndim != 2)
+        return fail(FW_ERR_INVALID_ARG, "positions must be [N] or [axes, N]");
+    if (fw_status_t s = check_i32(positions, "positions", positions->ndim)) return s;
+    const int64_t axes = positions->ndim == 2 ? positions->shape[0] : 1;
+    if (positions->shape[positions->ndim - 1] != N) return fail(FW_ERR_INVALID_ARG, "positions must hold N entries an axis");
+    if (axes < 1 || axes > 64) return fail(FW_ERR_UNSUPPORTED, "1 to 64 axes of positions, not %lld", (long long)axes);
+    if (axes > 1 && !axis_map) return fail(FW_ERR_INVALID_ARG, "positions of several axes need an axis_map");
+    if (fw_status_t s = check_vector(axis_map, "axis_map", rot / 2, true)) return s;
+    if (fw_status_t s = check_tensor(q_out, "q_out", 3, FW_BF16)) return s;
+    if (q_out->shape[0] != N || q_out->shape[1] != Hq || q_out->shape[2] != D)
+        return fail(FW_ERR_INVALID_ARG, "q_out must be [N, Hq, D]");
+    fw::NormRopeParams p{};
+    if (append) {
+        // As fw_kv_append, of [N, 1, Hkv, D] tokens.
+        fw_tensor_t k4 = *k, v4{};
+        auto as4 = [](const fw_tensor_t *t) {
+            fw_tensor_t x = *t;
+            x.ndim = 4;
+            x.shape[3] = t->shape[2]; x.shape[2] = t->shape[1]; x.shape[1] = 1;
+            x.stride[3] = t->stride[2]; x.stride[2] = t->stride[1]; x.stride[1] = 0;
+            return x;
+        };
+        k4 = as4(k);
+        if (v) {
+            if (fw_status_t s = check_tensor(v, "v", 3, FW_BF16)) return s;
+            v4 = as4(v);
+        }
+        const AppendArgs aa{&k4, v ? &v4 : nullptr, slots, layer_base_rows};
+        fw::AppendParams ap{};
+        if (fw_status_t s = build_append(aa, k_cache, v_cache, k_scale, v_scale, &ap)) return s;
+        if (v && v->shape[2] != D) return fail(FW_ERR_UNSUPPORTED, "values must be as wide as keys");
+        if (N > 0 && reinterpret_cast<uintptr_t>(slots->data) % 4) return fail(FW_ERR_INVALID_ARG, "slot_mapping misaligned");
+        if (ap.cache_rows / ap.ps >= (1LL << 31)) return fail(FW_ERR_UNSUPPORTED, "page pool too large");
+        if (fw_status_t s = check_written(k_cache, "k_cache")) return s;
+        if (fw_status_t s = check_written(v_cache, "v_cache")) return s;
+        p.slots = ap.slot_mapping;
+        p.layer_base = ap.layer_base;
+        p.cache_rows = ap.cache_rows;
+        p.ps = ap.ps;
+        p.ps_shift = -1;
+        for (int i = 0; i < 31; ++i)
+            if (ap.ps == 1LL << i) p.ps_shift = i;
+        p.kv8 = ap.kv8;
+        p.k_cache = ap.k_cache;
+        p.v_cache = ap.v_cache;
+        for (int i = 0; i < 3; ++i) {
+            p.kc_stride[i] = ap.kc_stride[i];
+            p.vc_stride[i] = ap.vc_stride[i];
+        }
+        p.k_scale = k_scale;
+        p.v_scale = v_scale;
+    } else {
+        if (fw_status_t s = check_tensor(k_out, "k_out", 3, FW_BF16)) return s;
+        if (k_out->shape[0] != N || k_out->shape[1] != Hkv || k_out->shape[2] != D)
+            return fail(FW_ERR_INVALID_ARG, "k_out must be [N, Hkv, D]");
+    }
+    if (N == 0) return ok();
+    const fw_tensor_t *rows[] = {q, k, q_out, append ? v : k_out};
+    const char *row_names[] = {"q", "k", "q_out", append ? "v" : "k_out"};
+    for (int i = 0; i < 4; ++i)
+        if (rows[i])
+            if (fw_status_t s = check_tma_layout(rows[i], row_names[i])) return s;
+    if (fw_status_t s = check_written(q_out, "q_out")) return s;
+    if (!append)
+        if (fw_status_t s = check_written(k_out, "k_out")) return s;
+    // Nothing that is written lies over anything else of the call, but q_out may be q and
+    // k_out k: a head is read before it is written.
+    const fw_tensor_t *written[] = {q_out, append ? k_cache : k_out, append ? v_cache : nullptr};
+    const char *written_names[] = {"q_out", append ? "k_cache" : "k_out", "v_cache"};
+    const fw_tensor_t *read[] = {q, k, v, q_weight, k_weight, inv_freq, positions, axis_map, append ? slots : nullptr};
+    const char *read_names[] = {"q", "k", "v", "q_weight", "k_weight", "inv_freq", "positions", "axis_map", "slot_mapping"};
+    for (int i = 0; i < 3; ++i) {
+        for (int j = i + 1; j < 3; ++j)
+            if (share(written[i], written[j]))
+                return fail(FW_ERR_INVALID_ARG, "%s overlaps %s", written_names[i], written_names[j]);
+        for (int j = 0; j < 9; ++j) {
+            if (!share(written[i], read[j])) continue;
+            const bool in_place = (i == 0 && j == 0) || (i == 1 && j == 1 && !append);
+            if (!(in_place && same_tensor(written[i], read[j])))
+                return fail(FW_ERR_INVALID_ARG, "%s overlaps %s", written_names[i], read_names[j]);
+        }
+    }
+    p.N = N;
+    p.Hq = (int)Hq; p.Hkv = (int)Hkv; p.D = (int)D; p.rot = (int)rot; p.axes = (int)axes;
+    p.interleaved = interleaved ? 1 : 0;
+    p.q = static_cast<const uint16_t *>(q->data);
+    p.k = static_cast<const uint16_t *>(k->data);
+    p.v = append && v ? static_cast<const uint16_t *>(v->data) : nullptr;
+    p.q_out = static_cast<uint16_t *>(q_out->data);
+    p.k_out = append ? nullptr : static_cast<uint16_t *>(k_out->data);
+    for (int i = 0; i < 2; ++i) {
+        p.q_stride[i] = q->stride[i];
+        p.k_stride[i] = k->stride[i];
+        p.v_stride[i] = p.v ? v->stride[i] : 0;
+        p.qo_stride[i] = q_out->stride[i];
+        p.ko_stride[i] = append ? 0 : k_out->stride[i];
+        const fw_tensor_t *w = i ? k_weight : q_weight;
+        p.weight[i] = w ? w->data : nullptr;
+        p.weight_f32[i] = w && w->dtype == FW_F32;
+    }
+    p.eps = eps;
+    p.inv_freq = static_cast<const float *>(inv_freq->data);
+    p.positions = static_cast<const int32_t *>(positions->data);
+    p.pos_stride = positions->ndim == 2 ? positions->stride[0] : 0;
+    p.axis_map = axis_map ? static_cast<const int32_t *>(axis_map->data) : nullptr;
+    std::lock_guard<std::mutex> lk(g_mu);
+    DeviceState *d = nullptr;
+    if (fw_status_t s = device_state(&d)) return s;
+    p.num_sms = d->num_sms;
+    p.status = d->status;
+    cudaError_t e = fw::launch_norm_rope(p, stream);
+    if (e != cudaSuccess) return fail(FW_ERR_CUDA, "norm and rotation launch: %s", cudaGetErrorString(e));
+    g_launches.fetch_add(1);
+    return ok();
+}
+
+extern "C" {
+
+fw_status_t fw_qk_norm_rope(const fw_tensor_t *q, const fw_tensor_t *k, const fw_tensor_t *q_weight,
+                            const fw_tensor_t *k_weight, float eps, const fw_tensor_t *inv_freq,
+                            const fw_tensor_t *positions, const fw_tensor_t *axis_map, int32_t interleaved,
+                            fw_tensor_t *q_out, fw_tensor_t *k_out, fw_stream_t stream) {
+    return norm_rope(q, k, nullptr, q_weight, k_weight, eps, inv_freq, positions, axis_map, interleaved, nullptr, 0,
+                     q_out, k_out, nullptr, nullptr, 1.f, 1.f, false, reinterpret_cast<cudaStream_t>(stream));
+}
+
+fw_status_t fw_qk_norm_rope_append(const fw_tensor_t *q, const fw_tensor_t *k, const fw_tensor_t *v,
+                                   const fw_tensor_t *q_weight, const fw_tensor_t *k_weight, float eps,
+                                   const fw_tensor_t *inv_freq, const fw_tensor_t *positions,
+                                   const fw_tensor_t *axis_map, int32_t interleaved, const fw_tensor_t *slot_mapping,
+                                   int64_t layer_base_rows, fw_tensor_t *q_out, fw_tensor_t *k_cache,
+                                   fw_tensor_t *v_cache, float k_scale, float v_scale, fw_stream_t stream) {
+    return norm_rope(q, k, v, q_weight, k_weight, eps, inv_freq, positions, axis_map, interleaved, slot_mapping,
+                     layer_base_rows, q_out, nullptr, k_cache, v_cache, k_scale, v_scale, true,
+                     reinterpret_cast<cudaStream_t>(stream));
+}
+
+fw_status_t fw_verify_drafts(const fw_tensor_t *tokens, const fw_tensor_t *parents, const fw_tensor_t *draft_lens,
+                             const fw_tensor_t *target_probs, const fw_tensor_t *draft_probs,
+                             const fw_tensor_t *uniforms, fw_tensor_t *path, fw_tensor_t *path_lens,
+                             fw_tensor_t *next_tokens, fw_stream_t stream_) {
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    if (fw_status_t s = check_i32(tokens, "tokens", 2)) return s;
+    if (fw_status_t s = check_i32(parents, "parents", 2)) return s;
+    const int64_t B = tokens->shape[0], T = tokens->shape[1];
+    if (parents->shape[0] != B || parents->shape[1] != T) return fail(FW_ERR_INVALID_ARG, "parents must be [B, T] as tokens");
+    if (fw_status_t s = check_vector(draft_lens, "draft_lens", B, true)) return s;
+    if (T < 1 || T > 256) return fail(FW_ERR_UNSUPPORTED, "a tree holds 1 to 256 drafts, not %lld", (long long)T);
+    if (fw_status_t s = check_tensor(target_probs, "target_probs", 3, FW_F32)) return s;
+    if (fw_status_t s = check_tensor(draft_probs, "draft_probs", 3, FW_F32, true)) return s;
+    if (fw_status_t s = check_tensor(uniforms, "uniforms", 2, FW_F32)) return s;
+    const int64_t R = target_probs->shape[1], V = target_probs->shape[2];
+    if (target_probs->shape[0] != B || (R != T && R != T + 1))
+        return fail(FW_ERR_INVALID_ARG, "target_probs must be [B, T, V] or [B, T + 1, V]");
+    if (draft_probs && (draft_probs->shape[0] != B || draft_probs->shape[1] != R || draft_probs->shape[2] != V))
+        return fail(FW_ERR_INVALID_ARG, "draft_probs must have target_probs' shape");
+    if (V < 1 || V > (1LL << 24)) return fail(FW_ERR_UNSUPPORTED, "vocabularies of 1 to 2^24 tokens, not %lld", (long long)V);
+    if (B > (1LL << 24)) return fail(FW_ERR_UNSUPPORTED, "batch too large");
+    if (uniforms->shape[0] != B || uniforms->shape[1] != T + 1) return fail(FW_ERR_INVALID_ARG, "uniforms must be [B, T + 1]");
+    for (const fw_tensor_t *t : {target_probs, draft_probs, uniforms})
+        if (t && reinterpret_cast<uintptr_t>(t->data) % 4)
+            return fail(FW_ERR_INVALID_ARG, "probabilities or uniforms misaligned");
+    if (fw_status_t s = check_i32(path, "path", 2)) return s;
+    const int64_t A = path->shape[1];
+    if (path->shape[0] != B || A < 1 || A > 256) return fail(FW_ERR_INVALID_ARG, "path must be [B, A], A of 1 to 256");
+    if (fw_status_t s = check_vector(path_lens, "path_lens", B)) return s;
+    if (fw_status_t s = check_vector(next_tokens, "next_tokens", B)) return s;
+    const fw_tensor_t *written[] = {path, path_lens, next_tokens};
+    const char *written_names[] = {"path", "path_lens", "next_tokens"};
+    const fw_tensor_t *read[] = {tokens, parents, draft_lens, target_probs, draft_probs, uniforms};
+    const char *read_names[] = {"tokens", "parents", "draft_lens", "target_probs", "draft_probs", "uniforms"};
+    for (int i = 0; i < 3; ++i) {
+        if (fw_status_t s = check_written(written[i], written_names[i])) return s;
+        for (int j = i + 1; j < 3; ++j)
+            if (share(written[i], written[j]))
+                return fail(FW_ERR_INVALID_ARG, "%s overlaps %s", written_names[i], written_names[j]);
+        for (int j = 0; j < 6; ++j)
+            if (share(written[i], read[j]))
+                return fail(FW_ERR_INVALID_ARG, "%s overlaps %s", written_names[i], read_names[j]);
+    }
+    if (B == 0) return ok();
+    fw::VerifyParams p{};
+    p.B = (int)B; p.T = (int)T; p.V = (int)V; p.A = (int)A;
+    p.context = R > T ? 1 : 0;
+    p.tokens = static_cast<const int32_t *>(tokens->data);
+    p.token_stride = tokens->stride[0];
+    p.parents = static_cast<const int32_t *>(parents->data);
+    p.parent_stride = parents->stride[0];
+    p.draft_lens = draft_lens ? static_cast<const int32_t *>(draft_lens->data) : nullptr;
+    p.target = static_cast<const float *>(target_probs->data);
+    p.draft = draft_probs ? static_cast<const float *>(draft_probs->data) : nullptr;
+    for (int i = 0; i < 2; ++i) {
+        p.target_stride[i] = target_probs->stride[i];
+        p.draft_stride[i] = draft_probs ? draft_probs->stride[i] : 0;
+    }
+    p.uniforms = static_cast<const float *>(uniforms->data);
+    p.uniform_stride = uniforms->stride[0];
+    p.path = static_cast<int32_t *>(path->data);
+    p.path_stride = path->stride[0];
+    p.path_lens = static_cast<int32_t *>(path_lens->data);
+    p.next_tokens = static_cast<int32_t *>(next_tokens->data);
+    std::lock_guard<std::mutex> lk(g_mu);
+    DeviceState *d = nullptr;
+    if (fw_status_t s = device_state(&d)) return s;
+    p.num_sms = d->num_sms;
+    p.status = d->status;
+    cudaError_t e = fw::launch_verify(p, stream);
+    if (e != cudaSuccess) return fail(FW_ERR_CUDA, "verification launch: %s", cudaGetErrorString(e));
+    g_launches.fetch_add(1);
+    return ok();
+}
+
 }  // extern "C"

@@ -1,4 +1,5 @@
-// Python entry points of the speculative-decoding operators over the C ABI.
+// Python entry points of the speculative-decoding operators and of those around a
+// step's attention over the C ABI.
 //
 // A step of these operators takes the GPU a few microseconds, while marshalling
 // ten tensors through ctypes took the host 20 to 40: this module reads the
@@ -27,6 +28,9 @@ decltype(&fw_paged_decode_tree_workspace_size) g_tree_workspace;
 decltype(&fw_tree_mask) g_mask;
 decltype(&fw_build_page_tables) g_tables;
 decltype(&fw_kv_commit) g_commit;
+decltype(&fw_verify_drafts) g_verify;
+decltype(&fw_qk_norm_rope) g_norm_rope;
+decltype(&fw_qk_norm_rope_append) g_norm_rope_append;
 PyObject *g_check;                     // raises FwError for a status
 
 [[noreturn]] void raise(PyObject *type, const char *format, ...) {
@@ -42,7 +46,7 @@ PyObject *g_check;                     // raises FwError for a status
 // The tensors of one call: views for the C ABI, and the one device they share.
 struct Args {
     int device = -1;
-    std::array<fw_tensor_t, 10> view;
+    std::array<fw_tensor_t, 16> view;
     int count = 0;
 
     // The tensor behind a Python object; None gives an undefined one.
@@ -275,11 +279,107 @@ PyObject *kv_commit(PyObject *, PyObject *const *a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
-// (addresses of the five C entry points, the status check)
+// (tokens, parents, target_probs, uniforms, draft_probs, draft_lens, max_path, path,
+//  path_lens, next_tokens)
+PyObject *verify_drafts(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (!arity(n, 10)) return nullptr;
+    const char *names[10] = {"tokens", "parents", "target_probs", "uniforms", "draft_probs", "draft_lens", "", "path",
+                             "path_lens", "next_tokens"};
+    at::Tensor t[10];
+    Args args;
+    for (int i = 0; i < 10; ++i) {
+        if (i == 6) continue;
+        t[i] = Args::take(a[i], names[i]);
+        if (i < 4) need(t[i], names[i]);
+        args.place(t[i]);
+    }
+    if (t[0].dim() != 2) raise(PyExc_ValueError, "tokens must be [B, T]");
+    const int64_t B = t[0].size(0);
+    long long most = t[0].size(1);
+    if (a[6] != Py_None && !whole(a[6], &most)) return nullptr;
+    if (!t[7].defined() && (most < 1 || most > 256)) raise(PyExc_ValueError, "max_path must be 1 to 256");
+    Where where(args.device);
+    const int64_t sizes[3] = {B * (int64_t)most, B, B};
+    int64_t total = 0;
+    for (int i = 0; i < 3; ++i)
+        if (!t[7 + i].defined()) total += Outputs::room(sizes[i]) + 64;
+    Outputs outs(total, args.device);
+    if (!t[7].defined()) t[7] = outs.cut({B, (int64_t)most});
+    for (int i = 1; i < 3; ++i)
+        if (!t[7 + i].defined()) t[7 + i] = outs.cut({B});
+    fw_tensor_t *v[10];
+    for (int i = 0; i < 10; ++i) v[i] = i == 6 ? nullptr : args.add(t[i]);
+    if (failed(g_verify(v[0], v[1], v[5], v[2], v[4], v[3], v[7], v[8], v[9], where.stream()))) return nullptr;
+    return Py_BuildValue("NNN", THPVariable_Wrap(t[7]), THPVariable_Wrap(t[8]), THPVariable_Wrap(t[9]));
+    END_HANDLE_TH_ERRORS
+}
+
+// (q, k, positions, inv_freq, q_weight, k_weight, eps, axis_map, interleaved, q_out, k_out)
+PyObject *qk_norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (!arity(n, 11)) return nullptr;
+    double eps;
+    if (!number(a[6], &eps)) return nullptr;
+    const int interleaved = PyObject_IsTrue(a[8]);
+    if (interleaved < 0) return nullptr;
+    const char *names[11] = {"q", "k", "positions", "inv_freq", "q_weight", "k_weight", "", "axis_map", "", "q_out", "k_out"};
+    at::Tensor t[11];
+    Args args;
+    for (int i = 0; i < 11; ++i) {
+        if (i == 6 || i == 8) continue;
+        t[i] = Args::take(a[i], names[i]);
+        if (i < 4) need(t[i], names[i]);
+        args.place(t[i]);
+    }
+    Where where(args.device);
+    for (int i = 0; i < 2; ++i)
+        if (!t[9 + i].defined()) t[9 + i] = empty(t[i].sizes(), at::kBFloat16, args.device);
+    fw_tensor_t *v[11];
+    for (int i = 0; i < 11; ++i) v[i] = i == 6 || i == 8 ? nullptr : args.add(t[i]);
+    if (failed(g_norm_rope(v[0], v[1], v[4], v[5], (float)eps, v[3], v[2], v[7], interleaved, v[9], v[10], where.stream())))
+        return nullptr;
+    return pair(t[9], t[10]);
+    END_HANDLE_TH_ERRORS
+}
+
+// (q, k, v, positions, inv_freq, slot_mapping, layer_base_rows, k_cache, v_cache,
+//  q_weight, k_weight, eps, axis_map, interleaved, k_scale, v_scale, q_out)
+PyObject *qk_norm_rope_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (!arity(n, 17)) return nullptr;
+    double eps, ks, vs;
+    long long base;
+    if (!whole(a[6], &base) || !number(a[11], &eps) || !number(a[14], &ks) || !number(a[15], &vs)) return nullptr;
+    const int interleaved = PyObject_IsTrue(a[13]);
+    if (interleaved < 0) return nullptr;
+    const char *names[17] = {"q", "k", "v", "positions", "inv_freq", "slot_mapping", "", "k_cache", "v_cache", "q_weight",
+                             "k_weight", "", "axis_map", "", "", "", "q_out"};
+    at::Tensor t[17];
+    Args args;
+    for (int i = 0; i < 17; ++i) {
+        if (!names[i][0]) continue;
+        t[i] = Args::take(a[i], names[i]);
+        if (i < 8 && i != 2) need(t[i], names[i]);
+        args.place(t[i]);
+    }
+    Where where(args.device);
+    if (!t[16].defined()) t[16] = empty(t[0].sizes(), at::kBFloat16, args.device);
+    fw_tensor_t *v[17];
+    for (int i = 0; i < 17; ++i) v[i] = names[i][0] ? args.add(t[i]) : nullptr;
+    if (failed(g_norm_rope_append(v[0], v[1], v[2], v[9], v[10], (float)eps, v[4], v[3], v[12], interleaved, v[5], base,
+                                  v[16], v[7], v[8], (float)ks, (float)vs, where.stream())))
+        return nullptr;
+    return THPVariable_Wrap(t[16]);
+    END_HANDLE_TH_ERRORS
+}
+
+// (addresses of the C entry points, the status check)
 PyObject *connect(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    if (!arity(n, 6)) return nullptr;
-    void *f[5];
-    for (int i = 0; i < 5; ++i) {
+    constexpr int kEntries = 8;
+    if (!arity(n, kEntries + 1)) return nullptr;
+    void *f[kEntries];
+    for (int i = 0; i < kEntries; ++i) {
         f[i] = PyLong_AsVoidPtr(a[i]);
         if (!f[i]) {
             if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "a NULL entry point");
@@ -291,7 +391,10 @@ PyObject *connect(PyObject *, PyObject *const *a, Py_ssize_t n) {
     g_mask = reinterpret_cast<decltype(g_mask)>(f[2]);
     g_tables = reinterpret_cast<decltype(g_tables)>(f[3]);
     g_commit = reinterpret_cast<decltype(g_commit)>(f[4]);
-    Py_XSETREF(g_check, Py_NewRef(a[5]));
+    g_verify = reinterpret_cast<decltype(g_verify)>(f[5]);
+    g_norm_rope = reinterpret_cast<decltype(g_norm_rope)>(f[6]);
+    g_norm_rope_append = reinterpret_cast<decltype(g_norm_rope_append)>(f[7]);
+    Py_XSETREF(g_check, Py_NewRef(a[kEntries]));
     Py_RETURN_NONE;
 }
 
@@ -301,6 +404,9 @@ PyMethodDef methods[] = {
     {"tree_mask", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(tree_mask)), METH_FASTCALL, nullptr},
     {"build_page_tables", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(build_page_tables)), METH_FASTCALL, nullptr},
     {"kv_commit", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(kv_commit)), METH_FASTCALL, nullptr},
+    {"verify_drafts", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(verify_drafts)), METH_FASTCALL, nullptr},
+    {"qk_norm_rope", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(qk_norm_rope)), METH_FASTCALL, nullptr},
+    {"qk_norm_rope_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(qk_norm_rope_append)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fw_fast", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -225,6 +225,47 @@ struct CommitParams {
     int *status;
 };
 
+// One fw_verify_drafts launch.
+struct VerifyParams {
+    int B, T, V, A;
+    int context;                               // 1: the rows begin with the committed context's
+    const int32_t *tokens; int64_t token_stride;
+    const int32_t *parents; int64_t parent_stride;
+    const int32_t *draft_lens;                 // null: T
+    const float *target; int64_t target_stride[2];     // (b, row)
+    const float *draft; int64_t draft_stride[2];       // null: drafts proposed with certainty
+    const float *uniforms; int64_t uniform_stride;
+    int32_t *path; int64_t path_stride;
+    int32_t *path_lens, *next_tokens;
+    int num_sms;
+    int *status;
+};
+
+// One fw_qk_norm_rope or fw_qk_norm_rope_append launch.
+struct NormRopeParams {
+    int64_t N;                                 // tokens
+    int Hq, Hkv, D, rot, axes, interleaved;
+    const uint16_t *q, *k, *v;                 // v null: keys go to k_out, or values are not appended
+    int64_t q_stride[2], k_stride[2], v_stride[2];     // elements (token, head)
+    uint16_t *q_out, *k_out;                   // k_out null: keys go to the cache
+    int64_t qo_stride[2], ko_stride[2];
+    const void *weight[2];                     // of queries and keys; null: not normed
+    int weight_f32[2];
+    float eps;
+    const float *inv_freq;                     // [rot / 2]
+    const int32_t *positions; int64_t pos_stride;      // (axis); tokens contiguous
+    const int32_t *axis_map;                   // [rot / 2] or null
+    const int32_t *slots;                      // [N], null: no append
+    int64_t layer_base, cache_rows;
+    int ps, ps_shift, kv8;                     // ps_shift: log2 of ps, -1: not a power of two
+    void *k_cache, *v_cache;
+    int64_t kc_stride[3], vc_stride[3];        // elements (page, slot, head)
+    float k_scale, v_scale;
+    int parts;                                 // warps that share a token's heads
+    int num_sms;
+    int *status;
+};
+
 // plan kernel + attention kernel + combine kernel, in stream order
 cudaError_t launch_decode(const DecodeParams &p, const CUtensorMap &tm_q, const CUtensorMap &tm_k,
                           const CUtensorMap &tm_v, int head_dim, cudaStream_t stream,
@@ -265,6 +306,8 @@ void tree_place_workspace(TreeParams *p, void *ws);
 cudaError_t launch_tree_mask(const TreeMaskParams &p, cudaStream_t stream);
 cudaError_t launch_page_tables(const PageTableParams &p, cudaStream_t stream, int *launches);
 cudaError_t launch_kv_commit(const CommitParams &p, cudaStream_t stream);
+cudaError_t launch_verify(const VerifyParams &p, cudaStream_t stream);
+cudaError_t launch_norm_rope(const NormRopeParams &p, cudaStream_t stream);
 
 // plan kernel + attention kernel, in stream order
 cudaError_t launch_prefill(const PrefillParams &p, const CUtensorMap &tm_q, const CUtensorMap &tm_k,
