@@ -525,6 +525,59 @@ fw_status_t fw_verify_drafts(const fw_tensor_t *tokens, const fw_tensor_t *paren
                              fw_tensor_t *next_tokens, fw_stream_t stream);
 
 /*
+ * Attention of chunks of new tokens over the paged cache: a later part of a prompt, a
+ * prompt behind a cached prefix, a batch in which some requests bring one token and
+ * others a chunk, or (not causal) tokens against a cached encoder's states.
+ *
+ *   q            [total_q, Hq, D]   BF16, the requests' new tokens one after another
+ *   k_cache, v_cache  [num_pages, ps, Hkv, D]  BF16 or FP8_E4M3 (scales k_scale,
+ *                                   v_scale; 1 for BF16 caches)
+ *   block_table  [B, max_pages]     I32, as fw_paged_decode; entries of pages that no
+ *                                   token of the request sees are never read
+ *   cu_seqlens_q [B + 1]  I32: request b's tokens are rows cu[b] .. cu[b + 1] - 1
+ *                         (none is fine).  Rows of no request are left as they were.  A
+ *                         request whose rows go down or past total_q is skipped and
+ *                         records FW_ERR_INVALID_ARG in the device status word
+ *   seq_lens     [B]      I32: keys of request b, its new tokens included (fw_kv_append or
+ *                         fw_qk_norm_rope_append put them there before); clamped to 0 ..
+ *                         max_pages * ps
+ *   causal       nonzero: token t of a request with d new tokens and n keys sees the keys
+ *                up to its own position n - d + t (bottom-right alignment: with d > n the
+ *                first see none); zero: all n
+ *   window_left  -1: none; W >= 0: the keys a token sees start at max(0, n - d + t - W),
+ *                causal or not
+ *   out          [total_q, Hq, D]  BF16, written;  lse [total_q, Hq] F32 or NULL
+ *
+ * Rows with no visible key get a zero output and LSE = -inf.  Hidden places may hold
+ * anything, NaN and infinities included: scores of hidden keys are dropped by selection,
+ * and in the tiles of 128 keys that some token of a unit (up to 256 rows) does not see
+ * whole, a value that is not finite makes the rows that see it NaN (all columns, not
+ * their LSE) and leaves the others alone.
+ *
+ * Arithmetic as fw_paged_decode_tree over BF16 caches: products of BF16 values summed in
+ * FP32, weights rounded to BF16 for the product with V and summed unrounded.  E4M3 values
+ * are widened to BF16, which holds every one.
+ *
+ * Supported: D in {128, 256} (FP8: 128), B <= 4096, any chunk lengths, page sizes, strides
+ * and alignment of fw_paged_decode; any Hq / Hkv, total_q * Hq and Hq * D / 8 below 2^31.
+ * Work is shared out by the keys that each 256 rows walk, in equal ranges to the CTAs
+ * (FW_OPT_MAX_CTAS applies).  Two launches.  The partials of units that a range's end cuts
+ * take a fixed fw_paged_prefill_workspace_size() bytes whatever the batch: `workspace`
+ * (256-byte aligned) or, when it is NULL, the workspace of fw_set_workspace() or the
+ * internal buffer, whose calls have to be ordered.  Calls with workspaces of their own may
+ * overlap.  Outputs and the workspace must not share elements with inputs or with one
+ * another.
+ */
+fw_status_t fw_paged_prefill(const fw_tensor_t *q, const fw_tensor_t *k_cache, const fw_tensor_t *v_cache,
+                             const fw_tensor_t *block_table, const fw_tensor_t *cu_seqlens_q,
+                             const fw_tensor_t *seq_lens, float scale, float k_scale, float v_scale, int32_t causal,
+                             int32_t window_left, fw_tensor_t *out, fw_tensor_t *lse, void *workspace,
+                             size_t workspace_bytes, fw_stream_t stream);
+
+/* Workspace bytes of fw_paged_prefill on the current device for head dim D (128 or 256). */
+fw_status_t fw_paged_prefill_workspace_size(int32_t head_dim, size_t *bytes);
+
+/*
  * ---------------------------------------------------------------------------
  * What comes before the attention: norms and positions of queries and keys.
  * ---------------------------------------------------------------------------

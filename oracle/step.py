@@ -101,3 +101,52 @@ def verify(tokens, parents, target, uniforms, draft=None, draft_lens=None, max_p
         lens.append(len(path))
         drawn.append(token)
     return paths, lens, drawn
+
+
+def paged_prefill(q, k_cache, v_cache, block_table, cu_seqlens_q, seq_lens, scale, causal=True, window_left=-1, k_scale=1.0,
+                  v_scale=1.0):
+    """(out, lse, absv, reach) for every packed row, as spec.tree_attention gives
+    them; rows of no request stay NaN."""
+    N, Hq, D = q.shape
+    ps, Hkv = k_cache.shape[1], k_cache.shape[2]
+    G = Hq // Hkv
+    Q, bt = _f64(q), block_table.cpu().numpy()
+    out, absv = np.full((N, Hq, D), np.nan), np.zeros((N, Hq, D))
+    lse, reach = np.full((N, Hq), np.nan), np.zeros((N, Hq))
+    cu = cu_seqlens_q.tolist()
+    for b in range(len(cu) - 1):
+        d, n = cu[b + 1] - cu[b], max(0, min(int(seq_lens[b]), bt.shape[1] * ps))
+        if d <= 0:
+            continue
+        rows = slice(cu[b], cu[b + 1])
+        t = np.arange(d)
+        hi = n - d + t + 1 if causal else np.full(d, n)
+        lo = np.zeros(d, dtype=np.int64) if window_left < 0 else np.maximum(0, n - d + t - window_left)
+        key = np.arange(n)
+        seen = (key[None] < hi[:, None]) & (key[None] >= lo[:, None])
+        some = seen.any(1)
+        out[rows], lse[rows] = 0.0, -np.inf
+        if not some.any():
+            continue
+        first = int(lo[some].min())                        # earlier pages may be gone
+        pages = np.zeros(-(-n // ps), dtype=np.int64)
+        pages[first // ps:] = bt[b, first // ps:-(-n // ps)]
+        used = key[first:]
+        K, V = (c.float().view(-1, Hkv, D)[torch.from_numpy(pages[used // ps] * ps + used % ps)] for c in (k_cache, v_cache))
+        K, V = _f64(K) * k_scale, _f64(V) * v_scale
+        seen = seen[:, first:]
+        for h in range(Hq):
+            k, v = K[:, h // G], V[:, h // G]
+            # Keys that no row sees may be NaN.
+            ok = seen.any(0)
+            k, v = np.where(ok[:, None], k, 0.0), np.where(ok[:, None], v, 0.0)
+            x = Q[rows, h]
+            s = np.where(seen, x @ k.T * scale, -np.inf)
+            m = np.where(some, s.max(1, initial=-np.inf), 0.0)
+            e = np.exp(s - m[:, None])
+            z = np.where(some, e.sum(1), 1.0)
+            out[rows, h] = e @ v / z[:, None]
+            absv[rows, h] = e @ np.abs(v) / z[:, None]
+            lse[rows, h] = np.where(some, m + np.log(z), -np.inf)
+            reach[rows, h] = np.where(seen, np.abs(x) @ np.abs(k).T, 0.0).max(1) * abs(scale)
+    return out, lse, absv, reach

@@ -113,6 +113,10 @@ def load_library(path: Optional[str] = None):
     lib.fw_build_page_tables.argtypes = [V, V, V, V, V, I64, V, V, V, V, V, V]
     lib.fw_kv_commit.restype = S
     lib.fw_kv_commit.argtypes = [V, V, V, V, I64, V, V, V, V]
+    lib.fw_paged_prefill.restype = S
+    lib.fw_paged_prefill.argtypes = [V, V, V, V, V, V, F, F, F, I32, I32, V, V, V, SZ, V]
+    lib.fw_paged_prefill_workspace_size.restype = S
+    lib.fw_paged_prefill_workspace_size.argtypes = [I32, ctypes.POINTER(SZ)]
     lib.fw_verify_drafts.restype = S
     lib.fw_verify_drafts.argtypes = [V] * 10
     lib.fw_qk_norm_rope.restype = S
@@ -317,7 +321,7 @@ def varlen_prefill(q, k, v, cu_seqlens_q, cu_seqlens_k, causal, scale, out=None,
 
 _FAST_ENTRIES = ("fw_paged_decode_tree", "fw_paged_decode_tree_workspace_size", "fw_tree_mask",
                  "fw_build_page_tables", "fw_kv_commit", "fw_verify_drafts", "fw_qk_norm_rope",
-                 "fw_qk_norm_rope_append")
+                 "fw_qk_norm_rope_append", "fw_paged_prefill", "fw_paged_prefill_workspace_size")
 _fast_module = None
 
 
@@ -399,6 +403,25 @@ def kv_commit(path, path_lens, base_lens, block_table, k_cache, v_cache, num_lay
     base_lens + path_lens."""
     return _on(stream, (_fast_module or _fast()).kv_commit, path, path_lens, base_lens, block_table, k_cache, v_cache,
                num_layers, new_lens)
+
+
+def paged_prefill_workspace_size(head_dim) -> int:
+    """Workspace bytes of paged_prefill on the current device."""
+    n = ctypes.c_size_t(0)
+    _check(load_library().fw_paged_prefill_workspace_size(int(head_dim), ctypes.byref(n)))
+    return n.value
+
+
+def paged_prefill(q, k_cache, v_cache, block_table, cu_seqlens_q, seq_lens, scale, causal=True, window_left=-1, k_scale=1.0,
+                  v_scale=1.0, out=None, lse=None, return_lse=True, workspace=None, stream=None):
+    """fw_paged_prefill: the new tokens of every request (rows cu_seqlens_q[b] ..
+    cu_seqlens_q[b + 1] - 1 of q [total_q, Hq, D], the last of its seq_lens[b] keys
+    when causal) attend over the paged cache; BF16 or FP8 E4M3.  workspace: bytes
+    for the split partials (None: a fresh buffer from torch's allocator, so calls on
+    several streams and captured graphs share nothing).  Returns (out [total_q, Hq,
+    D] bf16, lse [total_q, Hq] f32 or None); rows of no request are not written."""
+    return _on(stream, (_fast_module or _fast()).paged_prefill, q, k_cache, v_cache, block_table, cu_seqlens_q, seq_lens,
+               scale, causal, window_left, k_scale, v_scale, out, lse, return_lse, workspace)
 
 
 def verify_drafts(tokens, parents, target_probs, uniforms, draft_probs=None, draft_lens=None, max_path=None, path=None,

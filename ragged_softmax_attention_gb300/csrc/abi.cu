@@ -1648,4 +1648,163 @@ fw_status_t fw_verify_drafts(const fw_tensor_t *tokens, const fw_tensor_t *paren
     return ok();
 }
 
+fw_status_t fw_paged_prefill_workspace_size(int32_t head_dim, size_t *bytes) {
+    if (!bytes) return fail(FW_ERR_INVALID_ARG, "bytes is NULL");
+    if (head_dim != 128 && head_dim != 256) return fail(FW_ERR_UNSUPPORTED, "paged prefill head dim %d", head_dim);
+    std::lock_guard<std::mutex> lk(g_mu);
+    DeviceState *d = nullptr;
+    if (fw_status_t s = device_state(&d)) return s;
+    *bytes = fw::chunk_workspace_bytes(head_dim, d->num_sms);
+    return ok();
+}
+
+fw_status_t fw_paged_prefill(const fw_tensor_t *q, const fw_tensor_t *k_cache, const fw_tensor_t *v_cache,
+                             const fw_tensor_t *block_table, const fw_tensor_t *cu_seqlens_q,
+                             const fw_tensor_t *seq_lens, float scale, float k_scale, float v_scale, int32_t causal,
+                             int32_t window_left, fw_tensor_t *out, fw_tensor_t *lse, void *workspace,
+                             size_t workspace_bytes, fw_stream_t stream_) {
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    if (fw_status_t s = check_tensor(q, "q", 3, FW_BF16)) return s;
+    if (!k_cache) return fail(FW_ERR_INVALID_ARG, "k_cache is NULL");
+    const bool kv8 = k_cache->dtype == FW_FP8_E4M3;
+    if (!kv8 && k_cache->dtype != FW_BF16) return fail(FW_ERR_INVALID_ARG, "caches must be BF16 or FP8_E4M3");
+    if (fw_status_t s = check_tensor(k_cache, "k_cache", 4, k_cache->dtype)) return s;
+    if (fw_status_t s = check_tensor(v_cache, "v_cache", 4, k_cache->dtype)) return s;
+    if (fw_status_t s = check_i32(block_table, "block_table", 2)) return s;
+    const int64_t N = q->shape[0], Hq = q->shape[1], D = q->shape[2];
+    const int64_t P = k_cache->shape[0], ps = k_cache->shape[1], Hkv = k_cache->shape[2];
+    const int64_t B = block_table->shape[0], max_pages = block_table->shape[1];
+    if (k_cache->shape[3] != D) return fail(FW_ERR_INVALID_ARG, "k_cache head dim != q head dim");
+    if (v_cache->shape[0] != P || v_cache->shape[1] != ps || v_cache->shape[2] != Hkv)
+        return fail(FW_ERR_INVALID_ARG, "v_cache [pages, ps, Hkv] must match k_cache");
+    if (v_cache->shape[3] != D) return fail(FW_ERR_UNSUPPORTED, "paged prefill needs values as wide as keys (%lld, not %lld)",
+                                            (long long)D, (long long)v_cache->shape[3]);
+    if (!(D == 128 || (D == 256 && !kv8)))
+        return fail(FW_ERR_UNSUPPORTED, "paged prefill head dim %lld: supported 128 and 256 (FP8 caches: 128)", (long long)D);
+    if (Hq < 1 || Hkv < 1 || Hq % Hkv != 0)
+        return fail(FW_ERR_INVALID_ARG, "Hq (%lld) must be a positive multiple of Hkv (%lld)", (long long)Hq, (long long)Hkv);
+    if (!kv8 && (k_scale != 1.f || v_scale != 1.f))
+        return fail(FW_ERR_INVALID_ARG, "k_scale and v_scale must be 1 for BF16 caches");
+    if (!(std::isfinite(k_scale) && std::isfinite(v_scale) && k_scale > 0.f && v_scale > 0.f))
+        return fail(FW_ERR_INVALID_ARG, "k_scale and v_scale must be finite and positive");
+    if (!std::isfinite(scale)) return fail(FW_ERR_INVALID_ARG, "scale must be finite");
+    if (window_left < -1) return fail(FW_ERR_INVALID_ARG, "window_left must be -1 or more, not %d", (int)window_left);
+    if (fw_status_t s = check_vector(cu_seqlens_q, "cu_seqlens_q", B + 1)) return s;
+    if (fw_status_t s = check_vector(seq_lens, "seq_lens", B)) return s;
+    if (fw_status_t s = check_tensor(out, "out", 3, FW_BF16)) return s;
+    if (fw_status_t s = check_tensor(lse, "lse", 2, FW_F32, true)) return s;
+    if (out->shape[0] != N || out->shape[1] != Hq || out->shape[2] != D)
+        return fail(FW_ERR_INVALID_ARG, "out must be [total_q, Hq, D]");
+    if (lse && (lse->shape[0] != N || lse->shape[1] != Hq)) return fail(FW_ERR_INVALID_ARG, "lse must be [total_q, Hq]");
+    if (B > 4096) return fail(FW_ERR_UNSUPPORTED, "paged prefill serves up to 4096 requests, not %lld", (long long)B);
+    if (!supported_page_size(ps))
+        return fail(FW_ERR_UNSUPPORTED, "page size %lld: supported 8, 16, 32, 64, 128 or multiples of 128", (long long)ps);
+    fw::ChunkParams p{};
+    p.scale_log2 = scale * k_scale * 1.4426950408889634f;
+    if (!std::isfinite(p.scale_log2)) return fail(FW_ERR_INVALID_ARG, "scale * k_scale overflows");
+    // A scale of zero would turn the -inf of hidden keys into NaN: the least positive
+    // number leaves every score it multiplies at zero for the exponential.
+    if (p.scale_log2 == 0.f) p.scale_log2 = std::numeric_limits<float>::denorm_min();
+    if (B == 0 || N == 0) return ok();
+    if (P < 1 || max_pages < 1) return fail(FW_ERR_INVALID_ARG, "empty page pool or block table");
+    if (P > (1LL << 31) - 1 || max_pages * ps > (1LL << 30))
+        return fail(FW_ERR_UNSUPPORTED, "page pool or sequence bound too large");
+    if (N > (1LL << 30) || N * Hq >= (1LL << 31) || Hq * (D / 8) >= (1LL << 31))
+        return fail(FW_ERR_UNSUPPORTED, "too many query rows or heads");
+    const fw_tensor_t *rows[] = {q, k_cache, v_cache, out};
+    const char *row_names[] = {"q", "k_cache", "v_cache", "out"};
+    for (int i = 0; i < 4; ++i)
+        if (fw_status_t s = check_tma_layout(rows[i], row_names[i])) return s;
+    if (lse && reinterpret_cast<uintptr_t>(lse->data) % 4) return fail(FW_ERR_INVALID_ARG, "lse misaligned");
+    if (fw_status_t s = check_written(out, "out")) return s;
+    if (fw_status_t s = check_written(lse, "lse")) return s;
+    p.B = (int)B; p.Hq = (int)Hq; p.Hkv = (int)Hkv; p.G = (int)(Hq / Hkv); p.D = (int)D;
+    p.ps = (int)ps; p.max_pages = (int)max_pages; p.num_pages = (int)P;
+    p.ps_shift = -1;
+    for (int i = 3; i <= 20; ++i)
+        if (ps == (1LL << i)) p.ps_shift = i;
+    p.kv8 = kv8 ? 1 : 0;
+    p.causal = causal ? 1 : 0;
+    p.window = window_left;
+    p.total_q = N;
+    p.cu = static_cast<const int32_t *>(cu_seqlens_q->data);
+    p.seq_lens = static_cast<const int32_t *>(seq_lens->data);
+    p.block_table = static_cast<const int32_t *>(block_table->data);
+    p.bt_stride = block_table->stride[0];
+    p.out = out->data;
+    p.lse = lse ? static_cast<float *>(lse->data) : nullptr;
+    for (int i = 0; i < 2; ++i) {
+        p.out_stride[i] = out->stride[i];
+        p.lse_stride[i] = lse ? lse->stride[i] : 0;
+    }
+    p.out_scale = v_scale;
+    // Row tiles: whole tokens of up to 128 rows, or 128 heads of one token.
+    p.tile_tokens = p.G <= 128 ? (int)(128 / p.G < N ? 128 / p.G : N) : 1;
+    p.head_chunks = p.G <= 128 ? 1 : (p.G + 127) / 128;
+    // Two row tiles a unit where the requests bring more than one on average.
+    p.row_tiles = D == 128 && (p.head_chunks > 1 || N * p.G > 128 * B) ? 2 : 1;
+    p.min_span = fw::kChunkMinSpan;
+    p.piece_cost = kv8 || p.row_tiles > 1 ? fw::kChunkPieceCost : fw::kChunkPieceCostOne;
+    std::lock_guard<std::mutex> lk(g_mu);
+    DeviceState *d = nullptr;
+    if (fw_status_t s = device_state(&d)) return s;
+    p.grid = d->num_sms;
+    if (g_opt_max_ctas > 0 && p.grid > g_opt_max_ctas) p.grid = (int)g_opt_max_ctas;
+    // As in the decode: the KV heads ride on the CTA index when the grid holds whole groups of them.
+    p.ride = p.Hkv > 1 && p.grid % p.Hkv == 0;
+    const size_t need = fw::chunk_workspace_bytes(p.D, d->num_sms);
+    void *ws = workspace;
+    if (ws) {
+        if (reinterpret_cast<uintptr_t>(ws) % 256) return fail(FW_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+        if (workspace_bytes < need)
+            return fail(FW_ERR_WORKSPACE, "workspace holds %zu bytes, %zu needed", workspace_bytes, need);
+    } else if (fw_status_t s = get_workspace(d, need, stream, &ws)) {
+        return s;
+    }
+    // Nothing that is written lies over anything else of the call.
+    fw_tensor_t room{};
+    room.data = ws;
+    room.dtype = FW_I32;
+    room.ndim = 1;
+    room.shape[0] = (int64_t)need / 4;
+    room.stride[0] = 1;
+    const fw_tensor_t *tensors[] = {&room, out, lse, q, k_cache, v_cache, block_table, cu_seqlens_q, seq_lens};
+    const char *names[] = {"the workspace", "out", "lse", "q", "k_cache", "v_cache", "block_table", "cu_seqlens_q", "seq_lens"};
+    for (int i = 0; i < 3; ++i)
+        for (int j = i + 1; j < 9; ++j)
+            if (share(tensors[i], tensors[j]))
+                return fail(FW_ERR_INVALID_ARG, "%s overlaps %s", names[i], names[j]);
+    fw::chunk_place_workspace(&p, ws);
+    p.test_stall = g_opt_test_stall ? 1 : 0;
+    p.timeout_ns = (uint64_t)g_opt_timeout_ms * 1000000ull;
+    p.status = d->status;
+    CUtensorMap tq, tk, tv;
+    {
+        const uint64_t dims[3] = {(uint64_t)p.D, (uint64_t)p.Hq, (uint64_t)N};
+        const uint64_t strides[2] = {(uint64_t)q->stride[1] * 2, (uint64_t)q->stride[0] * 2};
+        const uint32_t box[3] = {64, (uint32_t)(p.G < 128 ? p.G : 128), (uint32_t)p.tile_tokens};
+        if (fw_status_t s = encode_bf16(&tq, q->data, 3, dims, strides, box, "q")) return s;
+        const uint64_t esz = p.kv8 ? 1 : 2;
+        const uint32_t kbox[4] = {p.kv8 ? 128u : 64u, 1, (uint32_t)(p.ps < fw::kKvTile ? p.ps : fw::kKvTile), 1};
+        const fw_tensor_t *caches[2] = {k_cache, v_cache};
+        for (int i = 0; i < 2; ++i) {
+            const fw_tensor_t *c = caches[i];
+            const uint64_t cd[4] = {(uint64_t)p.D, (uint64_t)p.Hkv, (uint64_t)p.ps, (uint64_t)p.num_pages};
+            const uint64_t cs[3] = {(uint64_t)c->stride[2] * esz, (uint64_t)c->stride[1] * esz, (uint64_t)c->stride[0] * esz};
+            // As in the decode: a 128-byte FP8 row's neighbour is another head's,
+            // worth fetching with it only when the heads ride on the CTA index.
+            const bool narrow = p.kv8 && cs[1] != 128 && !p.ride;
+            if (fw_status_t s = encode_map(i ? &tv : &tk, p.kv8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                                           c->data, 4, cd, cs, kbox, i ? "v_cache" : "k_cache",
+                                           narrow ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
+                return s;
+        }
+    }
+    int launched = 0;
+    cudaError_t e = fw::launch_chunk(p, tq, tk, tv, stream, &launched);
+    g_launches.fetch_add(launched);
+    if (e != cudaSuccess) return fail(FW_ERR_CUDA, "paged prefill launch: %s", cudaGetErrorString(e));
+    return ok();
+}
+
 }  // extern "C"

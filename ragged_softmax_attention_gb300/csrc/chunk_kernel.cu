@@ -1,0 +1,1109 @@
+// Attention of chunks of new tokens over a paged KV cache, sm_103a: token t of a
+// request with d new tokens and n keys (the chunk included) sees the keys lo_t ..
+// hi_t - 1, hi_t = n - d + t + 1 (causal) or n, lo_t = max(0, n - d + t - window) or 0.
+//
+// The (token, head) rows that share a KV head's keys fill the MMA M axis, whole
+// tokens, up to 128 rows a row tile, as in the tree decode:
+//   S [128 x 128]  = Q_tile * K_tile^T          (tcgen05, FP32 in TMEM)
+//   O [128 x D]   += P [128 x 128] * V_tile      (tcgen05, P and O in TMEM)
+// with a thread to a row and a conditional rescale (the base of the exponentials moves
+// when a maximum rose by more than 8 log2 units).
+//
+// A unit is (request, KV head, NT consecutive row tiles).  Units are laid end to end by
+// weight -- the keys that they walk and what it costs to start one -- and every CTA takes
+// an equal contiguous range, so one long request, many short ones and a mixed batch all
+// fill the GPU; a unit that a range's border cuts leaves partial rows, at most two pieces
+// a CTA whatever the batch, which a second launch merges.  A unit's weight is linear in
+// its number within the request (but for the window's start), so sums over units are
+// closed forms: every CTA works out its range from the lengths by itself, one pass over
+// the requests and one binary search, and no planning launch is needed.
+//
+// D = 128 with more than a row tile a request: NT = 2, two row tiles take turns on the
+// tensor core over shared K and V tiles, each with its own MMA-issuing thread, softmax
+// warpgroup, S buffer and O.  Otherwise NT = 1 with three S buffers (two at D = 256), QK
+// and PV issued by a thread each.
+//
+// FP8 caches: tiles land as bytes, four warps widen them to BF16 (exact) into the ring
+// that the MMAs read, so that everything behind is the BF16 kernel.
+//
+// Warp roles: warp 0 copies K and V tiles, warps 1 and 2 issue the MMAs, warp 3 works out
+// the pieces and copies the queries, then NT warpgroups of softmax, then (FP8) a
+// warpgroup that widens.
+#include <cuda_fp8.h>
+
+#include "tree_common.cuh"
+
+namespace fw {
+namespace {
+
+using namespace tree;
+
+// One piece: a unit's key tiles inside one CTA range.  64 bytes.
+struct alignas(16) ChunkUnit {
+    int b;             // request, -1 ends the CTA's work
+    int g;             // KV head
+    int rt0, nrt;      // first row tile and how many
+    int n, d, q0;      // keys and new tokens of the request, its first packed row
+    int tile0, ntiles; // key tiles
+    int part;          // partial slot, -1: the whole unit, written to the outputs
+    int lo;            // first key that a row sees: pages wholly before it are not copied
+    int pad_[5];
+};
+static_assert(sizeof(ChunkUnit) == 64, "a unit record fills one 64-byte slot");
+
+// ------------------------------------------------------------------ the plan
+
+// A request's units: `steps` runs of tokens (the first `v0` of which see nothing) times
+// `reps` (KV heads, and parts of a token's heads).  All weights in keys.
+struct ChunkRow {
+    int n, d, q0, steps, v0, reps;
+};
+template <int NT>
+__device__ __forceinline__ int step_tokens(const ChunkParams &p) { return p.head_chunks > 1 ? 1 : NT * p.tile_tokens; }
+
+template <int NT>
+__device__ __forceinline__ ChunkRow chunk_row(const ChunkParams &p, int b) {
+    ChunkRow r;
+    r.q0 = __ldg(p.cu + b);
+    const int end = __ldg(p.cu + b + 1);
+    const bool ok = r.q0 >= 0 && end >= r.q0 && end <= p.total_q;
+    if (!ok && blockIdx.x == 0) record_error(p.status, kErrInvalid);
+    r.d = ok ? end - r.q0 : 0;
+    r.n = min(max(__ldg(p.seq_lens + b), 0), p.max_pages * p.ps);
+    const int s = step_tokens<NT>(p);
+    r.steps = ceil_div_i(r.d, s);
+    r.v0 = r.n == 0 ? r.steps : p.causal && r.d > r.n ? (r.d - r.n) / s : 0;
+    r.reps = (p.head_chunks > 1 ? ceil_div_i(p.head_chunks, NT) : 1) * (p.ride ? 1 : p.Hkv);
+    return r;
+}
+// Weight of step v, and of steps v0 .. v - 1.
+template <int NT>
+__device__ __forceinline__ long long step_weight(const ChunkParams &p, const ChunkRow &r, int v) {
+    const long long s = step_tokens<NT>(p), base = r.n - r.d;
+    const long long hi = p.causal ? base + (v + 1) * s : r.n;
+    const long long lo = p.window < 0 ? 0 : max(0ll, base - p.window + v * s);
+    return p.piece_cost + 128 + hi - lo;
+}
+template <int NT>
+__device__ __forceinline__ long long steps_weight(const ChunkParams &p, const ChunkRow &r, int v) {
+    const long long s = step_tokens<NT>(p), base = r.n - r.d, m = v - r.v0;
+    auto sum = [](long long a, long long e) { return (e - a) * (a + e - 1) / 2; };      // a + .. + e - 1
+    long long w = m * (p.piece_cost + 128);
+    w += p.causal ? m * (base + s) + s * sum(r.v0, v) : m * r.n;
+    if (p.window >= 0) {
+        const long long z = base - p.window;                     // lo = z + i s where that is above zero
+        const long long first = max((long long)r.v0, z >= 0 ? 0 : -z / s + 1);
+        if (first < v) w -= (v - first) * z + s * sum(first, v);
+    }
+    return w;
+}
+
+// plan[0] = weight in all, plan[1], plan[2] = start and number of the request that holds
+// the CTA's first key, plan[3] = span.  Ends with every thread past a barrier but plan not
+// yet published.
+template <int NT>
+__device__ __forceinline__ void chunk_plan(const ChunkParams &p, long long *plan, long long *scan) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nthreads = blockDim.x;
+    const int per = (p.B + nthreads - 1) / nthreads;
+    auto weight = [&](int b) -> long long {
+        const ChunkRow r = chunk_row<NT>(p, b);
+        return r.v0 < r.steps ? r.reps * steps_weight<NT>(p, r, r.steps) : 0;
+    };
+    long long mine = 0;
+    const int b0 = threadIdx.x * per;
+    for (int i = 0; i < per && b0 + i < p.B; ++i) mine += weight(b0 + i);
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) scan[warp] = incl;
+    __syncthreads();
+    long long before = incl - mine, total = 0;
+    for (int w = 0; w < nthreads / 32; ++w) {
+        if (w < warp) before += scan[w];
+        total += scan[w];
+    }
+    const int nranges = p.ride ? (int)gridDim.x / p.Hkv : (int)gridDim.x;
+    const long long span = max((long long)p.min_span, (total + nranges - 1) / nranges);
+    const long long first = span * (p.ride ? (int)blockIdx.x / p.Hkv : (int)blockIdx.x);
+    if (mine > 0 && first >= before && first < before + mine) {
+        int b = b0;
+        for (long long s; first >= before + (s = weight(b)); ++b) before += s;
+        plan[1] = before;
+        plan[2] = b;
+    }
+    if (threadIdx.x == 0) { plan[0] = total; plan[3] = span; }
+}
+
+// Walks the pieces of this CTA's range (one warp, all lanes alike).  A border at weight
+// x of a unit cuts it before tile (x - cost) / 128, for the ranges on both sides alike;
+// a piece without tiles is none.
+template <int NT>
+struct ChunkWalk {
+    long long span, pos, end, start;                  // the range; start of the unit
+    int range, b, rep, v;
+    ChunkRow r;
+    ChunkCut cut;
+
+    __device__ int tile_at(const ChunkParams &p, long long x, int tiles) const {
+        x -= p.piece_cost;
+        return x <= 0 ? 0 : (int)min((long long)tiles, x >> 7);
+    }
+    __device__ void init(const ChunkParams &p, const long long *plan) {
+        span = plan[3];
+        range = p.ride ? (int)blockIdx.x / p.Hkv : (int)blockIdx.x;
+        pos = span * range;
+        end = min(plan[0], pos + span);
+        cut = ChunkCut{};
+        start = end;
+        if (pos >= end) return;
+        b = (int)plan[2];
+        r = chunk_row<NT>(p, b);
+        const long long all = steps_weight<NT>(p, r, r.steps);
+        rep = (int)((pos - plan[1]) / all);
+        const long long off = pos - plan[1] - rep * all;
+        int lo = r.v0, hi = r.steps - 1;              // the last step that starts at or before off
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (steps_weight<NT>(p, r, mid) <= off) lo = mid; else hi = mid - 1;
+        }
+        v = lo;
+        start = plan[1] + rep * all + steps_weight<NT>(p, r, v);
+    }
+    __device__ void next(const ChunkParams &p, ChunkUnit &u) {   // u.b = -1 at the end
+        u.b = -1;
+        const int s = step_tokens<NT>(p);
+        while (start < end) {
+            if (v >= r.steps) {                       // the next KV head, the next request
+                v = r.v0;
+                if (v >= r.steps || ++rep >= r.reps) {
+                    if (++b >= p.B) return;           // (weight is left, so there is one)
+                    r = chunk_row<NT>(p, b);
+                    rep = 0;
+                    v = r.v0;
+                }
+                continue;
+            }
+            const long long w = step_weight<NT>(p, r, v);
+            const int t0 = v * s, t1 = min(r.d, t0 + s) - 1;
+            const int lo = p.window < 0 ? 0 : (int)max(0ll, (long long)r.n - r.d + t0 - p.window);
+            const int hi = p.causal ? r.n - r.d + t1 + 1 : r.n;
+            const int tile0 = lo / kKvTile, tiles = ceil_div_i(hi, kKvTile) - tile0;
+            const int a = tile_at(p, pos - start, tiles);
+            const int e = end >= start + w ? tiles : tile_at(p, end - start, tiles);
+            const long long at = start;
+            const int step = v;
+            start += w;
+            ++v;
+            if (a >= e) continue;
+            const int parts = p.head_chunks > 1 ? ceil_div_i(p.head_chunks, NT) : 1;
+            const int g = rep / parts, part = rep - g * parts;
+            u.b = b;
+            u.g = p.ride ? (int)blockIdx.x % p.Hkv : g;
+            u.rt0 = p.head_chunks > 1 ? step * p.head_chunks + part * NT : step * NT;
+            u.nrt = min(NT, p.head_chunks > 1 ? p.head_chunks - part * NT : ceil_div_i(r.d, p.tile_tokens) - u.rt0);
+            u.n = r.n;
+            u.d = r.d;
+            u.q0 = r.q0;
+            u.tile0 = tile0 + a;
+            u.ntiles = e - a;
+            u.lo = lo;
+            u.part = -1;
+            if (a > 0) {
+                u.part = 2 * blockIdx.x;
+            } else if (e < tiles) {
+                u.part = 2 * blockIdx.x + 1;
+                const long long last = min((at + p.piece_cost + 128ll * tiles + span - 1) / span, (at + w + span - 1) / span);
+                cut.count = (int)last - range;
+                cut.g = u.g; cut.rt0 = u.rt0; cut.nrt = u.nrt; cut.d = r.d; cut.q0 = r.q0;
+            }
+            return;
+        }
+    }
+};
+
+// The (token, head) of row r of row tile rt; false for padding.
+__device__ __forceinline__ bool chunk_tile_row(const ChunkParams &p, int rt, int g, int d, int r, int &t, int &h) {
+    if (p.head_chunks > 1) {
+        t = rt / p.head_chunks;
+        const int hh = (rt - t * p.head_chunks) * 128 + r;
+        h = g * p.G + hh;
+        return hh < p.G && t < d;
+    }
+    const int tt = r / p.G;
+    t = rt * p.tile_tokens + tt;
+    h = g * p.G + (r - tt * p.G);
+    return tt < p.tile_tokens && t < d;
+}
+
+// First and last key that token t sees, as [lo, hi).
+__device__ __forceinline__ int key_lo(const ChunkParams &p, const ChunkUnit &u, int t) {
+    return p.window < 0 ? 0 : (int)max(0ll, (long long)u.n - u.d + t - p.window);
+}
+__device__ __forceinline__ int key_hi(const ChunkParams &p, const ChunkUnit &u, int t) {
+    return p.causal ? max(0, u.n - u.d + t + 1) : u.n;
+}
+// The bits lo .. hi - 1 of 32 keys from `key` on.
+__device__ __forceinline__ uint32_t range_bits(int lo, int hi, int key) {
+    lo = max(lo - key, 0);
+    hi = min(hi - key, 32);
+    if (lo >= hi) return 0u;
+    return (0xffffffffu >> (32 - (hi - lo))) << lo;
+}
+
+// Values that are not finite, in tiles that some row of the unit does not see whole: they
+// must not meet the zero weights of rows that do not see them.  They are cleared before
+// the products, and the rows that see them come out as NaN.  Such tiles are few, for a
+// unit's 256 tokens at most three at either end: bits of a tile's keys in the words of unit
+// k % kBadUnits (a writer is at most four units ahead of a reader), behind a word that
+// says whether there are any.
+constexpr int kBadUnitWords = 4 + 8 * 4;
+__device__ __forceinline__ uint32_t *bad_words(uint32_t *marks, int tile, int any_lo, int all_hi) {
+    const int upper = tile - all_hi / kKvTile;            // >= 0: reaches past what the first row sees
+    return marks + 4 + 4 * ((upper >= 0 ? 4 + upper : tile - any_lo / kKvTile) & 7);
+}
+
+template <int D_, int NT_, bool KV8_>
+struct ChunkCfg {
+    static constexpr int D = D_, NT = NT_;
+    static constexpr bool KV8 = KV8_;
+    // S buffers of a stream, i.e. key tiles QK runs ahead: what O leaves of TMEM.
+    static constexpr int kSB = NT == 2 ? 1 : D == 128 ? 3 : 2;
+    static constexpr int kTileSlots = D / 128;                  // ring slots of one K or V tile
+    static constexpr int kChunkBytes = 128 * 128;               // 128 rows x 64 bf16 columns
+    static constexpr int kSlotBytes = 2 * kChunkBytes;          // 128 rows x 128 columns
+    static constexpr int kQBytes = 128 * D * 2;
+    static constexpr int kRaw = KV8 ? (NT == 2 ? 2 : 4) : 0;    // E4M3 tiles as they land
+    static constexpr int kRawBytes = 128 * 128;
+    static constexpr int kSlots = (229376 - NT * kQBytes - kRaw * kRawBytes) / kSlotBytes;
+    static constexpr int kOffQ = 0;
+    static constexpr int kOffRing = NT * kQBytes;
+    static constexpr int kOffRaw = kOffRing + kSlots * kSlotBytes;
+    static constexpr int kOffBar = kOffRaw + kRaw * kRawBytes;
+    static constexpr int kSched = 4;                            // unit records in flight
+    static constexpr int kBarSlotFull = 0;
+    static constexpr int kBarSlotEmpty = kBarSlotFull + kSlots;
+    static constexpr int kBarRawFull = kBarSlotEmpty + kSlots;
+    static constexpr int kBarRawEmpty = kBarRawFull + kRaw;
+    static constexpr int kBarQFull = kBarRawEmpty + kRaw;
+    static constexpr int kBarQEmpty = kBarQFull + 1;
+    static constexpr int kBarSFull = kBarQEmpty + 1;            // [NT][kSB]
+    static constexpr int kBarPHalf = kBarSFull + NT * kSB;      // [NT][kSB]
+    static constexpr int kBarPFull = kBarPHalf + NT * kSB;      // [NT][kSB]
+    static constexpr int kBarPvDone = kBarPFull + NT * kSB;     // [NT][kSB]
+    static constexpr int kBarIssued = kBarPvDone + NT * kSB;    // [NT]
+    static constexpr int kBarDrain = kBarIssued + NT;           // [2]
+    static constexpr int kBarSchedFull = kBarDrain + 2;
+    static constexpr int kBarSchedEmpty = kBarSchedFull + kSched;
+    static constexpr int kBarNever = kBarSchedEmpty + kSched;   // test hook: no thread ever arrives on it
+    static constexpr int kNumBars = kBarNever + 1;
+    static constexpr int kOffSched = (kOffBar + kNumBars * 8 + 63) / 64 * 64;
+    static constexpr int kOffBad = kOffSched + kSched * 64;
+    static constexpr int kOffPlan = (kOffBad + kBadUnits * kBadUnitWords * 4 + 15) / 16 * 16;
+    static constexpr int kOffScan = kOffPlan + 32;              // [16] warp sums
+    static constexpr int kOffMisc = kOffScan + 128;
+    static constexpr int kSmemBytes = kOffMisc + 16 + 1024;
+    static_assert(kSmemBytes <= 232448, "shared memory budget of one CTA exceeded");
+    static constexpr int kThreads = 128 + NT * 128 + (KV8 ? 128 : 0);
+    static constexpr int kSchedReaders = 3 + 4 * NT + (KV8 ? 4 : 0);    // issuers, the producer, softmax, widening warps
+    // NT = 2: launched at 168 registers (FP8: 128) a thread; after the split
+    // 128 x 80 + 256 x 208 = 63488 <= 384 x 168, FP8 128 x 80 + 256 x 176 + 128 x 80 = 512 x 128.
+    static constexpr uint32_t kRegsControl = 80, kRegsSoftmax = KV8 ? 176 : 208;
+    static_assert(NT == 1 || KV8 || 128 * kRegsControl + 256 * kRegsSoftmax <= 384 * 168, "register split");
+    static_assert(NT == 1 || !KV8 || 256 * kRegsControl + 256 * kRegsSoftmax <= 512 * 128, "register split");
+    static constexpr uint32_t kIdescQK = idesc_bf16_f32(128, kKvTile, false, false);
+    static constexpr uint32_t kIdescPV = idesc_bf16_f32(128, 128, false, true);
+    __device__ static constexpr uint32_t s_col(int x, int buf) { return (uint32_t)(x * kSB + buf) * 128u; }
+    __device__ static constexpr uint32_t o_col(int x) { return (uint32_t)(NT * kSB + x) * 128u; }
+    // Ring positions, in whole K or V tiles, of a piece of n key tiles: two streams take
+    // K_j and V_j in turn; one runs QK kSB tiles ahead.
+    __device__ static __forceinline__ int ring_k(int j, int n) { return NT == 2 ? 2 * j : pos_k<kSB>(j, n); }
+    __device__ static __forceinline__ int ring_v(int j, int n) { return NT == 2 ? 2 * j + 1 : pos_v<kSB>(j, n); }
+};
+
+// Four E4M3 bytes as BF16 (exact; NaN stays NaN).
+__device__ __forceinline__ uint2 widen4(uint32_t w) {
+    uint32_t h0, h1;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+        : "=r"(h0), "=r"(h1) : "r"(w));
+    uint2 r;
+    float a, b, c, d;
+    asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.f32.f16 %0, x;\n\tcvt.f32.f16 %1, y;\n\t}" : "=f"(a), "=f"(b) : "r"(h0));
+    asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.f32.f16 %0, x;\n\tcvt.f32.f16 %1, y;\n\t}" : "=f"(c), "=f"(d) : "r"(h1));
+    r.x = pack_bf16x2(a, b);
+    r.y = pack_bf16x2(c, d);
+    return r;
+}
+
+template <int D, int NT, bool KV8>
+__global__ void __launch_bounds__(ChunkCfg<D, NT, KV8>::kThreads, 1)
+chunk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
+             const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
+    using C = ChunkCfg<D, NT, KV8>;
+    constexpr int kSB = C::kSB, TS = C::kTileSlots;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *sQ = smem + C::kOffQ;
+    uint8_t *sRing = smem + C::kOffRing;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
+    uint64_t *slot_full = bars + C::kBarSlotFull;
+    uint64_t *slot_empty = bars + C::kBarSlotEmpty;
+    uint64_t *raw_full = bars + C::kBarRawFull;
+    uint64_t *raw_empty = bars + C::kBarRawEmpty;
+    uint64_t *q_full = bars + C::kBarQFull;
+    uint64_t *q_empty = bars + C::kBarQEmpty;
+    uint64_t *s_full = bars + C::kBarSFull;
+    uint64_t *p_half = bars + C::kBarPHalf;
+    uint64_t *p_full = bars + C::kBarPFull;
+    uint64_t *pv_done = bars + C::kBarPvDone;
+    uint64_t *issued = bars + C::kBarIssued;
+    uint64_t *drain = bars + C::kBarDrain;
+    uint64_t *sched_full = bars + C::kBarSchedFull;
+    uint64_t *sched_empty = bars + C::kBarSchedEmpty;
+    ChunkUnit *sched = reinterpret_cast<ChunkUnit *>(smem + C::kOffSched);
+    uint32_t *bad = reinterpret_cast<uint32_t *>(smem + C::kOffBad);
+    long long *plan = reinterpret_cast<long long *>(smem + C::kOffPlan);
+    long long *scan = reinterpret_cast<long long *>(smem + C::kOffScan);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffMisc);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::kOffMisc + 4);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kSlots; ++i) { mbar_init(&slot_full[i], KV8 ? 4 : 1); mbar_init(&slot_empty[i], NT); }
+        for (int i = 0; i < C::kRaw; ++i) { mbar_init(&raw_full[i], 1); mbar_init(&raw_empty[i], 4); }
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, NT);
+        for (int i = 0; i < NT * kSB; ++i) {
+            mbar_init(&s_full[i], 1); mbar_init(&p_half[i], 4); mbar_init(&p_full[i], 4); mbar_init(&pv_done[i], 1);
+        }
+        for (int i = 0; i < NT; ++i) mbar_init(&issued[i], 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&drain[i], 1);
+        for (int i = 0; i < C::kSched; ++i) { mbar_init(&sched_full[i], 1); mbar_init(&sched_empty[i], C::kSchedReaders); }
+        mbar_init(bars + C::kBarNever, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&tm_q); tma_prefetch_desc(&tm_k); tma_prefetch_desc(&tm_v);
+    }
+    if (warp == 1) { tmem_alloc(tmem_slot, 512); tmem_relinquish(); }
+    pdl_launch_dependents();                       // the merge may take its place; it waits for this grid
+    chunk_plan<NT>(p, plan, scan);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const WaitCtx wc{p.status, p.timeout_ns, abort_flag};
+    auto wait_unit = [&](int k) -> const ChunkUnit * {
+        const int sl = k % C::kSched;
+        return mbar_wait(&sched_full[sl], (k / C::kSched) & 1, wc) ? &sched[sl] : nullptr;
+    };
+    auto free_unit = [&](int k) { mbar_arrive(&sched_empty[k % C::kSched]); };
+    // A unit record for a whole warp; b < 0 at the end.
+    auto warp_unit = [&](int k) -> ChunkUnit {
+        const ChunkUnit *ur = wait_unit(k);
+        ChunkUnit u;
+        u.b = -1;
+        if (ur) u = *ur;
+        __syncwarp();
+        if (lane == 0) free_unit(k);
+        return u;
+    };
+
+    if (warp < 4) {
+      if constexpr (NT == 2) setmaxnreg_dec<C::kRegsControl>();
+      if (warp == 0) {
+        // ------------------------------------------------------------ producer
+        // Copies tiles into the ring (BF16) or to where the widening warps find them.
+        constexpr int kInto = KV8 ? C::kRaw : C::kSlots;
+        uint64_t *full = KV8 ? raw_full : slot_full, *empty = KV8 ? raw_empty : slot_empty;
+        const int box_rows = p.ps < kKvTile ? p.ps : kKvTile;
+        uint32_t rp = 0;                                  // slots filled so far
+        // Test hook for the bounded waits: before it copies anything, this warp waits on
+        // a barrier that nothing completes.  Nor do products then begin; the other roles
+        // wind down over the units at hand.
+        bool ok = !p.test_stall || warp_wait(bars + C::kBarNever, 0, wc, lane);
+        for (int k = 0; ok; ++k) {
+            const ChunkUnit u = warp_unit(k);
+            if (!__all_sync(0xffffffffu, u.b >= 0)) break;
+            auto copy_tile = [&](int j, int entry, bool is_v) -> bool {
+                const int key0 = (u.tile0 + j) * kKvTile;
+                const int slot0 = p.ps < kKvTile ? 0 : p.ps_shift >= 0 ? key0 & (p.ps - 1) : key0 % p.ps;
+                const bool mine = lane < 16 && page_copied(p, u, j, lane) &&
+                                  (p.ps >= kKvTile || key0 + (lane + 1) * p.ps > u.lo);
+                const unsigned who = __ballot_sync(0xffffffffu, mine);
+                const uint32_t bytes = (uint32_t)(__popc(who) * box_rows * (KV8 ? 128 : 256));
+#pragma unroll
+                for (int s = 0; s < TS; ++s, ++rp) {
+                    const int sl = rp % kInto;
+                    if (!warp_wait(&empty[sl], ((rp / kInto) & 1) ^ 1, wc, lane)) return false;
+                    if (lane == 0) mbar_arrive_expect_tx(&full[sl], bytes);
+                    __syncwarp();
+                    if (mine) {
+                        const int phys = checked_page(p, entry);
+                        const void *map = is_v ? (const void *)&tm_v : (const void *)&tm_k;
+                        if constexpr (KV8) {
+                            tma_load_4d(smem_u32(smem + C::kOffRaw + sl * C::kRawBytes + lane * box_rows * 128), map, &full[sl],
+                                        0, u.g, slot0, phys);
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < 2; ++c)
+                                tma_load_4d(smem_u32(sRing + sl * C::kSlotBytes + c * C::kChunkBytes + lane * box_rows * 128), map,
+                                            &full[sl], s * 128 + c * 64, u.g, slot0, phys);
+                        }
+                    }
+                }
+                return true;
+            };
+            PageWindow table;
+            table.open(p, u);
+            if constexpr (NT == 2) {
+                for (int j = 0; j < u.ntiles && ok; ++j) {
+                    const int entry = table.at(p, u, j);
+                    ok = copy_tile(j, entry, false) && copy_tile(j, entry, true);
+                }
+            } else {
+                int entries[kSB];                         // of the tiles whose V copy is to come
+#pragma unroll
+                for (int j = 0; j < kSB; ++j) {
+                    if (j >= u.ntiles || !ok) continue;
+                    entries[j] = table.at(p, u, j);
+                    ok = copy_tile(j, entries[j], false);
+                }
+                for (int j = 0; j < u.ntiles && ok; ++j) {
+                    ok = copy_tile(j, entries[0], true);
+#pragma unroll
+                    for (int i = 0; i + 1 < kSB; ++i) entries[i] = entries[i + 1];
+                    if (ok && j + kSB < u.ntiles) {
+                        entries[kSB - 1] = table.at(p, u, j + kSB);
+                        ok = copy_tile(j + kSB, entries[kSB - 1], false);
+                    }
+                }
+            }
+        }
+        if (lane == 0) {
+            for (uint32_t i = 0; i < (uint32_t)kInto && i < rp; ++i) {
+                const uint32_t r = rp - 1 - i;
+                mbar_wait_drain(&full[r % kInto], (r / kInto) & 1, wc);
+            }
+        }
+        __syncwarp();
+      } else if (warp < 3) {
+        // ----------------------------------------------------------------- MMA
+        if (lane == 0) {
+            const int x = NT == 2 ? warp - 1 : 0;
+            uint32_t rp = 0;                              // ring slots of earlier pieces
+            uint32_t steps = 0;                           // this stream's key tiles of earlier pieces
+            uint32_t turns = 0;                           // shared steps of earlier pieces (both streams present)
+            const SDesc q_d = sdesc_sw128_split(smem_u32(sQ + x * C::kQBytes), 16, 1024);
+            const SDesc k_d = sdesc_sw128_split(smem_u32(sRing), 16, 1024);
+            const SDesc v_d = sdesc_sw128_split(smem_u32(sRing), C::kChunkBytes, 1024);
+            auto wait_tile = [&](uint32_t r) -> bool {
+#pragma unroll
+                for (int s = 0; s < TS; ++s)
+                    if (!mbar_wait(&slot_full[(r + s) % C::kSlots], ((r + s) / C::kSlots) & 1, wc)) return false;
+                return true;
+            };
+            auto release_tile = [&](uint32_t r) {
+#pragma unroll
+                for (int s = 0; s < TS; ++s) mma_commit(&slot_empty[(r + s) % C::kSlots]);
+            };
+            const uint32_t idesc_qk = C::kIdescQK | (p.scale_log2 < 0.f ? kIdescNegateA : 0u);
+            auto push_qk = [&](uint32_t r, int buf) {
+#pragma unroll
+                for (int s = 0; s < TS; ++s) {
+                    const SDesc kd{k_d.lo + ((r + s) % C::kSlots) * (C::kSlotBytes >> 4), k_d.hi};
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk) {
+                        const uint32_t off = (kk >> 2) * C::kChunkBytes + (kk & 3) * 32;
+                        mma_bf16_ss(tmem + C::s_col(x, buf), sdesc_at(q_d, s * C::kSlotBytes + off), sdesc_at(kd, off),
+                                    idesc_qk, s + kk > 0 ? 1u : 0u);
+                    }
+                }
+            };
+            // P of a key tile lies over the first 64 columns of its S buffer
+            // (two BF16 a column); each half of 64 keys goes out as it comes.
+            auto push_pv_half = [&](uint32_t r, int buf, int half, bool first) {
+#pragma unroll
+                for (int s = 0; s < TS; ++s) {
+                    const SDesc vd{v_d.lo + ((r + s) % C::kSlots) * (C::kSlotBytes >> 4), v_d.hi};
+#pragma unroll
+                    for (int k4 = 0; k4 < 4; ++k4) {
+                        const int kk = half * 4 + k4;
+                        mma_bf16_ts(tmem + C::o_col(x) + s * 128, tmem + C::s_col(x, buf) + kk * 8,
+                                    sdesc_at(vd, kk * 16 * 128), C::kIdescPV, (first && kk == 0) ? 0u : 1u);
+                    }
+                }
+            };
+            bool ok = true;
+            for (int k = 0; ok; ++k) {
+                const ChunkUnit *ur = wait_unit(k);
+                const bool got = ur && ur->b >= 0;
+                const int n = got ? ur->ntiles : 0;
+                const int nrt = got ? ur->nrt : 0;
+                free_unit(k);
+                if (!got) break;
+                const uint32_t r0 = rp;
+                rp += (uint32_t)(2 * n * TS);
+                auto rk = [&](int j) { return r0 + (uint32_t)(C::ring_k(j, n) * TS); };
+                auto rv = [&](int j) { return r0 + (uint32_t)(C::ring_v(j, n) * TS); };
+                if constexpr (NT == 1) {
+                    // QK from one thread (warp 2), PV from the other: neither's waits hold up
+                    // the other's products.  Each waits for the other's step first: what lay
+                    // in the ring slot before its tile has then landed, as a parity wait
+                    // needs (K_j comes at most kSB tiles before V_j, less than the ring).
+                    if (warp == 2 && !mbar_wait(q_full, k & 1, wc)) break;
+                    for (int j = 0; j < n && ok; ++j) {
+                        const uint32_t st = steps + j;
+                        const int buf = st % kSB;
+                        const uint32_t ph = (st / kSB) & 1;
+                        if (warp == 2) {
+                            // The buffer's last P has gone through the tensor core.
+                            ok = (st < kSB || mbar_wait(&pv_done[buf], ph ^ 1, wc)) && wait_tile(rk(j));
+                            if (!ok) break;
+                            tc_fence_after();
+                            push_qk(rk(j), buf);
+                            mma_commit(&s_full[buf]);
+                            release_tile(rk(j));
+                            if (j == n - 1) mma_commit(q_empty);
+                        } else {
+                            ok = mbar_wait(&p_half[buf], ph, wc) && wait_tile(rv(j));
+                            if (!ok) break;
+                            tc_fence_after();
+                            push_pv_half(rv(j), buf, 0, j == 0);
+                            ok = mbar_wait(&p_full[buf], ph, wc);
+                            if (!ok) break;
+                            tc_fence_after();
+                            push_pv_half(rv(j), buf, 1, false);
+                            mma_commit(&pv_done[buf]);
+                            release_tile(rv(j));
+                        }
+                    }
+                    steps += n;
+                } else {
+                    if (!mbar_wait(q_full, k & 1, wc)) break;
+                    if (x >= nrt) {
+                        // No row tile for this stream: it still sees every copy land and
+                        // hands every slot back, so that its phases stay in step.
+                        mbar_arrive(q_empty);
+                        for (uint32_t r = r0; r < rp && ok; ++r) {
+                            ok = mbar_wait(&slot_full[r % C::kSlots], (r / C::kSlots) & 1, wc);
+                            if (ok) mbar_arrive(&slot_empty[r % C::kSlots]);
+                        }
+                        continue;
+                    }
+                    if (!wait_tile(rk(0))) break;
+                    tc_fence_after();
+                    push_qk(rk(0), 0);
+                    mma_commit(&s_full[x]);
+                    release_tile(rk(0));
+                    if (n == 1) mma_commit(q_empty);
+                    for (int j = 0; j < n && ok; ++j) {
+                        const uint32_t ph = (steps + j) & 1;
+                        if (nrt == 2) {
+                            // Turns: stream 1 follows stream 0's step j, stream 0 stream 1's
+                            // step j - 1, so that one's products run under the other's softmax.
+                            // (Steps count on across pieces, so neither gets two phases ahead.)
+                            const uint32_t dep = turns + j + x;
+                            if (dep > 0 && !mbar_wait(&issued[1 - x], (dep - 1) & 1, wc)) { ok = false; break; }
+                        }
+                        // A wait between pushes lets the tensor pipe run dry: the tiles of the
+                        // whole step first.  (K_{j+1} needs only older slots handed back.)
+                        const bool next = j + 1 < n;
+                        if (!wait_tile(rv(j)) || (next && !wait_tile(rk(j + 1))) || !mbar_wait(&p_half[x], ph, wc)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        push_pv_half(rv(j), 0, 0, j == 0);
+                        if (!mbar_wait(&p_full[x], ph, wc)) { ok = false; break; }
+                        tc_fence_after();
+                        push_pv_half(rv(j), 0, 1, false);
+                        // The turn goes over while this step's QK is still being pushed: the
+                        // other issuer's waits overlap that, and its PV queues right behind.
+                        if (nrt == 2) mbar_arrive(&issued[x]);
+                        if (next) push_qk(rk(j + 1), 0);
+                        else mma_commit(&pv_done[x]);
+                        release_tile(rv(j));
+                        if (next) {
+                            mma_commit(&s_full[x]);
+                            release_tile(rk(j + 1));
+                            if (j + 2 == n) mma_commit(q_empty);
+                        }
+                    }
+                    if (!ok) break;
+                    steps += n;
+                    if (nrt == 2) turns += n;
+                }
+            }
+            mma_commit(&drain[warp - 1]);
+            mbar_wait_drain(&drain[warp - 1], 0, wc);
+        }
+        __syncwarp();
+      } else if (warp == 3) {
+        // ----------------------------------------------- the pieces; queries
+        ChunkWalk<NT> walk;
+        walk.init(p, plan);
+        for (int k = 0;; ++k) {
+            ChunkUnit u;
+            walk.next(p, u);
+            const int sl = k % C::kSched;
+            bool ok = warp_wait(&sched_empty[sl], ((k / C::kSched) & 1) ^ 1, wc, lane);
+            if (ok && lane == 0) { sched[sl] = u; mbar_arrive(&sched_full[sl]); }
+            __syncwarp();
+            ok = ok && u.b >= 0 && warp_wait(q_empty, (k & 1) ^ 1, wc, lane);
+            if (!ok) {
+                // The copies land before the CTA leaves.
+                if (lane == 0 && k > 0) mbar_wait_drain(q_full, (k - 1) & 1, wc);
+                break;
+            }
+            if (lane == 0) {
+                const uint32_t qrows = p.head_chunks > 1 ? 128u : (uint32_t)(p.G * p.tile_tokens);
+                mbar_arrive_expect_tx(q_full, (uint32_t)u.nrt * (D / 64) * qrows * 128u);
+                for (int x = 0; x < u.nrt; ++x) {
+                    const int rt = u.rt0 + x;
+                    int h0 = u.g * p.G, t0 = rt * p.tile_tokens;
+                    if (p.head_chunks > 1) { t0 = rt / p.head_chunks; h0 += (rt - t0 * p.head_chunks) * 128; }
+#pragma unroll
+                    for (int c = 0; c < D / 64; ++c)
+                        tma_load_3d(smem_u32(sQ + x * C::kQBytes + c * C::kChunkBytes), &tm_q, q_full, c * 64, h0, u.q0 + t0);
+                }
+            }
+            __syncwarp();
+        }
+        if (lane == 0) p.cuts[blockIdx.x] = walk.cut;
+        __syncwarp();
+      }
+    } else if (KV8 && warp >= 4 + 4 * NT) {
+        if constexpr (KV8) {
+            // ------------------------------------------------------ widening
+            // Eight lanes take four 16-byte units of two rows whose numbers differ in bits 0
+            // and 2: their swizzled places then fall on different banks, read and written.
+            if constexpr (NT == 2) setmaxnreg_dec<C::kRegsControl>();
+            const int w4 = warp & 3, half = lane >> 4, pair = lane >> 3 & 1, unit = (lane & 3) + 4 * half;
+            uint32_t rp = 0;
+            bool ok = true;
+            for (int k = 0; ok; ++k) {
+                const ChunkUnit u = warp_unit(k);
+                if (!__all_sync(0xffffffffu, u.b >= 0)) break;
+                for (int i = 0; i < 2 * u.ntiles && ok; ++i, ++rp) {
+                    const int rs = rp % C::kRaw, sl = rp % C::kSlots;
+                    ok = warp_wait(&raw_full[rs], (rp / C::kRaw) & 1, wc, lane) &&
+                         warp_wait(&slot_empty[sl], ((rp / C::kSlots) & 1) ^ 1, wc, lane);
+                    if (!ok) break;
+                    const uint8_t *raw = smem + C::kOffRaw + rs * C::kRawBytes;
+                    uint8_t *to = sRing + sl * C::kSlotBytes + (unit >> 2) * C::kChunkBytes;
+#pragma unroll
+                    for (int it = 0; it < 8; ++it) {
+                        // rows 32 w4 + 8 (it / 2) + {r, r ^ 5}, r = 2 (it & 1) + pair
+                        int r = 2 * (it & 1) + pair;
+                        if (lane & 4) r ^= 5;
+                        const int row = w4 * 32 + (it >> 1) * 8 + r;
+                        const uint4 b = *reinterpret_cast<const uint4 *>(raw + row * 128 + ((unit ^ r) << 4));
+                        const uint2 x0 = widen4(b.x), x1 = widen4(b.y), x2 = widen4(b.z), x3 = widen4(b.w);
+                        uint8_t *line = to + row * 128;
+                        const int c = 2 * (unit & 3);
+                        *reinterpret_cast<uint4 *>(line + ((c ^ r) << 4)) = make_uint4(x0.x, x0.y, x1.x, x1.y);
+                        *reinterpret_cast<uint4 *>(line + (((c + 1) ^ r) << 4)) = make_uint4(x2.x, x2.y, x3.x, x3.y);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) { mbar_arrive(&raw_empty[rs]); mbar_arrive(&slot_full[sl]); }
+                }
+            }
+        }
+    } else {
+        if constexpr (NT == 2) {
+            if constexpr (C::kRegsSoftmax > (KV8 ? 128 : 168)) setmaxnreg_inc<C::kRegsSoftmax>();
+        }
+        // ------------------------------------------------- softmax / epilogue
+        // The named barriers below have no limit, so the warps that share them never part:
+        // a failed wait inside a unit does not change the control flow, and a unit that
+        // not all of them see (a wait for its record ran out) is taken by none.
+        const int x = (warp - 4) >> 2;
+        const int q4 = warp & 3;
+        const int row = q4 * 32 + lane;
+        const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
+        const float scale = fabsf(p.scale_log2);      // the MMA negates Q for a negative one
+        auto wait_pv = [&](uint32_t step) { mbar_wait(&pv_done[x * kSB + step % kSB], (step / kSB) & 1, wc); };
+        uint32_t steps = 0, pieces = 0, rp = 0;
+        for (int k = 0;; ++k) {
+            const ChunkUnit u = warp_unit(k);
+            if (!(x == 0 ? named_bar_all(1, 128, u.b >= 0) : __all_sync(0xffffffffu, u.b >= 0) != 0)) break;
+            const uint32_t r0 = rp;
+            rp += (uint32_t)(2 * u.ntiles * TS);
+            if (x >= u.nrt) continue;
+            uint32_t *marks = bad + k % kBadUnits * kBadUnitWords;
+            if (x == 0) {
+                if (row < kBadUnitWords) marks[row] = 0;
+                named_bar_sync(1, 128);
+            }
+            int t, h;
+            const bool live = chunk_tile_row(p, u.rt0 + x, u.g, u.d, row, t, h);
+            const bool warp_live = __any_sync(0xffffffffu, live);
+            const int lo = live ? key_lo(p, u, t) : 0, hi = live ? key_hi(p, u, t) : 0;
+            // Keys that every row of the unit sees, and that some row does: [all_lo, all_hi) and
+            // [any_lo, any_hi).
+            int t0 = u.rt0 * p.tile_tokens, t1 = min(u.d, (u.rt0 + u.nrt) * p.tile_tokens) - 1;
+            if (p.head_chunks > 1) t0 = t1 = u.rt0 / p.head_chunks;
+            const int all_lo = key_lo(p, u, t1), all_hi = key_hi(p, u, t0);
+            const int any_lo = key_lo(p, u, t0), any_hi = key_hi(p, u, t1);
+            float m_ref = kNegInf, l_sum = 0.f;
+            for (int j = 0; j < u.ntiles; ++j, ++steps) {
+                const int buf = steps % kSB;
+                const int key0 = (u.tile0 + j) * kKvTile;
+                const bool masked = key0 < all_lo || key0 + kKvTile > all_hi;
+                // In such a tile stream 0 sees to the values, for both streams (stream 1's
+                // product follows stream 0's).
+                const bool values = masked && x == 0;
+                uint32_t bits[4] = {0, 0, 0, 0};              // the keys this row sees
+                if (masked) {
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) bits[w] = range_bits(lo, hi, key0 + 32 * w);
+                }
+                mbar_wait(&s_full[x * kSB + buf], (steps / kSB) & 1, wc);
+                tc_fence_after();
+                if (warp_live) {                          // else rows of padding: whatever lies there
+                    const uint32_t sa = tmem + lane_off + C::s_col(x, buf);
+                    auto read_s = [&](int half, float *v) {
+                        tmem_ld32(sa + half * 64, v);
+                        tmem_ld32(sa + half * 64 + 32, v + 32);
+                    };
+                    auto hide = [&](int half, float *v) {
+                        const uint32_t b0 = half == 0 ? bits[0] : bits[2], b1 = half == 0 ? bits[1] : bits[3];
+#pragma unroll
+                        for (int i = 0; i < 64; ++i)
+                            if (!((i < 32 ? b0 : b1) >> (i & 31) & 1)) v[i] = kNegInf;
+                    };
+                    // Two streams read the row of S once; one reads it twice, for its maximum and
+                    // for P, 64 keys at a time in rolled loops, whose code stays small.
+                    float sv[NT == 2 ? kKvTile : 1], ext = kNegInf;
+                    if constexpr (NT == 2) {
+                        read_s(0, sv);
+                        read_s(1, sv + 64);
+                        tmem_wait_ld();
+                        if (masked) { hide(0, sv); hide(1, sv + 64); }
+                        ext = max_of<kKvTile>(sv);
+                    } else {
+#pragma unroll 1
+                        for (int half = 0; half < 2; ++half) {
+                            float v[64];
+                            read_s(half, v);
+                            tmem_wait_ld();
+                            if (masked) hide(half, v);
+                            ext = fmaxf(ext, max_of<64>(v));
+                        }
+                    }
+                    const float m_tile = live ? ext * scale : kNegInf;    // -inf when it sees none of these keys
+                    const bool up = m_tile > m_ref + kRescaleSlack;   // also the first visible tile: m_ref = -inf
+                    if (__any_sync(0xffffffffu, up)) {
+                        float alpha = 1.f;
+                        if (up) {
+                            alpha = ex2_approx(m_ref - m_tile);
+                            l_sum *= alpha;
+                            m_ref = m_tile;
+                        }
+                        if (j > 0) {
+                            // With one S buffer, S_j there means PV_{j-1} is done; with more
+                            // it may still run.
+                            if constexpr (kSB > 1) {
+                                wait_pv(steps - 1);
+                                tc_fence_after();
+                            }
+#pragma unroll 1
+                            for (int c = 0; c < D / 32; ++c) {
+                                float o[32];
+                                const uint32_t oa = tmem + lane_off + C::o_col(x) + c * 32;
+                                tmem_ld32(oa, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) o[i] *= alpha;
+                                tmem_st32(oa, o);
+                            }
+                            tmem_wait_st();
+                        }
+                    }
+                    // P = 2^(s * scale * log2 e - m_ref), rounded to BF16 (the MMA's A
+                    // operand shares V's type); the row sum takes it unrounded.
+                    const float mu = m_ref == kNegInf ? 0.f : m_ref;
+                    uint64_t sum[4] = {0, 0, 0, 0};
+                    auto put_half = [&](int half, float *v) {
+                        uint32_t pk[32];
+                        exp_64(v, scale, -mu, sum);
+#pragma unroll
+                        for (int i = 0; i < 64; i += 2) pk[i >> 1] = pack_bf16x2(v[i], v[i + 1]);
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+                            tmem_st16u(sa + half * 32 + c * 16, *reinterpret_cast<const uint32_t(*)[16]>(pk + c * 16));
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0 && !values) mbar_arrive(half == 0 ? &p_half[x * kSB + buf] : &p_full[x * kSB + buf]);
+                    };
+                    if constexpr (NT == 2) {
+                        put_half(0, sv);
+                        put_half(1, sv + 64);
+                    } else {
+#pragma unroll 1
+                        for (int half = 0; half < 2; ++half) {
+                            float v[64];
+                            read_s(half, v);
+                            tmem_wait_ld();
+                            if (masked) hide(half, v);
+                            put_half(half, v);
+                        }
+                    }
+                    l_sum += sum_of(sum);
+                }
+                if (values) {
+                    // Values of keys that nobody sees must not meet a zero weight: they may be
+                    // NaN; nor those that are not finite the weights of rows that do not see
+                    // them.  A thread looks after one key, when its row of P is done: the values
+                    // have landed meanwhile.
+                    const uint32_t r = r0 + (uint32_t)(C::ring_v(j, u.ntiles) * TS);
+                    // A parity wait needs the slot's copy before V_j to have landed.
+                    // S_j there proves that for all copies up to K_j; with two slots
+                    // to a tile the one before V_j's may be V_{j-1}, which its
+                    // finished product proves; with one stream over four slots it may
+                    // be V_{j-2}, which comes after K_j too.
+                    if constexpr (TS == 2) {
+                        if (steps > 0) wait_pv(steps - 1);
+                    } else if constexpr (NT == 1 && C::kSlots < 2 * kSB) {
+                        if (steps > 1) wait_pv(steps - 2);
+                    }
+                    const int key = key0 + row;
+                    const bool seen = key >= any_lo && key < any_hi;
+#pragma unroll 1
+                    for (int s = 0; s < TS; ++s) {
+                        const uint32_t sl = (r + s) % C::kSlots;
+                        mbar_wait(&slot_full[sl], ((r + s) / C::kSlots) & 1, wc);
+                        uint8_t *vr = sRing + sl * C::kSlotBytes + row * 128;
+                        uint32_t wild = 0;                // an exponent of all ones carries into the sign's place
+                        if (seen) {
+#pragma unroll 1
+                            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    const uint4 w = reinterpret_cast<const uint4 *>(vr + c * C::kChunkBytes)[i ^ (row & 7)];
+                                    wild |= ((w.x & 0x7f807f80u) + 0x00800080u) | ((w.y & 0x7f807f80u) + 0x00800080u) |
+                                            ((w.z & 0x7f807f80u) + 0x00800080u) | ((w.w & 0x7f807f80u) + 0x00800080u);
+                                }
+                            wild &= 0x80008000u;
+                            if (wild) {
+                                atomicOr(bad_words(marks, u.tile0 + j, any_lo, all_hi) + (row >> 5), 1u << (row & 31));
+                                atomicOr(marks, 1u);
+                            }
+                        }
+                        if (!seen || wild) {
+#pragma unroll 1
+                            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                                for (int i = 0; i < 8; ++i)
+                                    reinterpret_cast<uint4 *>(vr + c * C::kChunkBytes)[i ^ (row & 7)] = make_uint4(0, 0, 0, 0);
+                        }
+                    }
+                    fence_proxy_async_smem();
+                }
+                if (values || !warp_live) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) { mbar_arrive(&p_half[x * kSB + buf]); mbar_arrive(&p_full[x * kSB + buf]); }
+                }
+            }
+            // ------------------------------------------------------ epilogue
+            ++pieces;
+            if constexpr (NT == 1) {
+#pragma unroll
+                for (int i = kSB; i >= 1; --i)
+                    if (steps >= (uint32_t)i) wait_pv(steps - i);
+            } else {
+                mbar_wait(&pv_done[x], (pieces - 1) & 1, wc);
+            }
+            tc_fence_after();
+            if (warp_live) {
+                bool poison = false;
+                if (__builtin_expect(*reinterpret_cast<volatile uint32_t *>(marks) != 0, 0)) {
+#pragma unroll 1
+                    for (int j = 0; j < u.ntiles; ++j) {
+                        const int key0 = (u.tile0 + j) * kKvTile;
+                        if (key0 >= all_lo && key0 + kKvTile <= all_hi) continue;
+                        const uint32_t *words = bad_words(marks, u.tile0 + j, any_lo, all_hi);
+                        for (int w = 0; w < 4; ++w) poison |= (words[w] & range_bits(lo, hi, key0 + 32 * w)) != 0;
+                    }
+                }
+                write_row_at<D, NT>(p, u, x, row, live, (int64_t)(u.q0 + t) * p.out_stride[0] + h * p.out_stride[1],
+                                    (int64_t)(u.q0 + t) * p.lse_stride[0] + h * p.lse_stride[1], m_ref, l_sum, live && poison,
+                                    [&](int c, float (&o)[32]) {
+                    tmem_ld32(tmem + lane_off + C::o_col(x) + c * 32, o);
+                    tmem_wait_ld();
+                });
+            }
+            tc_fence_before();
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// Merges the pieces of the units that CTA ranges cut, as the tree decode's merge does:
+// with weighted sums o_i, row sums l_i and bases m_i, M = max m_i, out = sum 2^(m_i - M)
+// o_i / sum 2^(m_i - M) l_i.  The pieces of the unit whose first one ended CTA c's range
+// opened the following ranges.  Block (chunk, c) takes 32 rows of that unit, a lane a row
+// and a warp an equal share of the columns, and turns the result round in shared memory.
+// The rows of units that see no key are written here too.
+constexpr int kMergeThreads = 128;
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid_constant__ ChunkParams p) {
+    constexpr int kUnits = D / 4 / (kMergeThreads / 32);   // 16-byte FP32 units of a warp's columns
+    constexpr int kPieces = 16 / kUnits;
+    __shared__ uint4 stage[32][D / 8 + 1];           // BF16 rows
+    __shared__ long long offset[32];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // Zeros and -inf, a warp to a request; these wait for nothing.
+    const int nwarps = gridDim.x * gridDim.y * (kMergeThreads / 32);
+    for (int b = (blockIdx.y * gridDim.x + blockIdx.x) * (kMergeThreads / 32) + warp; b < p.B; b += nwarps) {
+        const ChunkRow r = chunk_row<NT>(p, b);
+        const int64_t empty = min((int64_t)r.d, (int64_t)r.v0 * step_tokens<NT>(p));
+        for (int64_t i = lane; i < empty * p.Hq * (D / 8); i += 32) {
+            const int64_t t = i / (p.Hq * (D / 8));
+            const int c = (int)(i - t * (p.Hq * (D / 8)));
+            reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(p.out) + (r.q0 + t) * p.out_stride[0] +
+                                      (c / (D / 8)) * p.out_stride[1])[c % (D / 8)] = make_uint4(0, 0, 0, 0);
+        }
+        if (p.lse)
+            for (int64_t i = lane; i < empty * p.Hq; i += 32) {
+                const int64_t t = i / p.Hq;
+                p.lse[(r.q0 + t) * p.lse_stride[0] + (i - t * p.Hq) * p.lse_stride[1]] = kNegInf;
+            }
+    }
+    pdl_wait();                                      // the pieces are written
+    const ChunkCut cut = p.cuts[blockIdx.y];
+    const int x = blockIdx.x / 4, row = (blockIdx.x & 3) * 32 + lane;
+    if (cut.count == 0 || x >= cut.nrt) return;
+    int t, h;
+    const bool live = chunk_tile_row(p, cut.rt0 + x, cut.g, cut.d, row, t, h);
+    if (!__syncthreads_or(live)) return;
+    const int step = p.ride ? p.Hkv : 1;
+    auto slot = [&](int k) -> int64_t { return k == 0 ? 2 * blockIdx.y + 1 : 2 * (blockIdx.y + k * step); };
+    float4 acc[kUnits];
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f, m = kNegInf;
+    if (live) {
+        for (int k0 = 0; k0 < cut.count; k0 += kPieces) {
+            float2 ml[kPieces];
+            float4 v[kPieces][kUnits];
+#pragma unroll
+            for (int k = 0; k < kPieces; ++k) {
+                ml[k] = make_float2(kNegInf, 0.f);
+                if (k0 + k >= cut.count) continue;
+                const int64_t sl = slot(k0 + k);
+                ml[k] = p.part_ml[sl * (NT * 128) + x * 128 + row];
+#pragma unroll
+                for (int i = 0; i < kUnits; ++i) v[k][i] = *part_unit<D, NT>(p, sl, warp * kUnits + i, x * 128 + row);
+            }
+            float mn = m;
+#pragma unroll
+            for (int k = 0; k < kPieces; ++k)
+                if (ml[k].y != 0.f) mn = fmaxf(mn, ml[k].x);
+            const float mu = mn == kNegInf ? 0.f : mn;       // nothing visible so far, or NaN scores alone
+            const float alpha = ex2_approx(m - mu);
+            m = mn;
+            l *= alpha;
+#pragma unroll
+            for (int i = 0; i < kUnits; ++i) { acc[i].x *= alpha; acc[i].y *= alpha; acc[i].z *= alpha; acc[i].w *= alpha; }
+#pragma unroll
+            for (int k = 0; k < kPieces; ++k) {
+                if (ml[k].y == 0.f) continue;
+                const float w = ex2_approx(ml[k].x - mu);
+                l = fmaf(w, ml[k].y, l);
+#pragma unroll
+                for (int i = 0; i < kUnits; ++i) {
+                    acc[i].x = fmaf(w, v[k][i].x, acc[i].x);
+                    acc[i].y = fmaf(w, v[k][i].y, acc[i].y);
+                    acc[i].z = fmaf(w, v[k][i].z, acc[i].z);
+                    acc[i].w = fmaf(w, v[k][i].w, acc[i].w);
+                }
+            }
+        }
+    }
+    const float inv = l != 0.f ? p.out_scale / l : 0.f;
+#pragma unroll
+    for (int i = 0; i < kUnits; i += 2)
+        stage[lane][(warp * kUnits + i) / 2] =
+            make_uint4(pack_bf16x2(acc[i].x * inv, acc[i].y * inv), pack_bf16x2(acc[i].z * inv, acc[i].w * inv),
+                       pack_bf16x2(acc[i + 1].x * inv, acc[i + 1].y * inv), pack_bf16x2(acc[i + 1].z * inv, acc[i + 1].w * inv));
+    if (warp == 0) {
+        offset[lane] = live ? (int64_t)(cut.q0 + t) * p.out_stride[0] + h * p.out_stride[1] : -1;
+        if (live && p.lse)
+            p.lse[(int64_t)(cut.q0 + t) * p.lse_stride[0] + h * p.lse_stride[1]] =
+                l != 0.f ? (m + log2f(l)) * 0.69314718055994531f : kNegInf;
+    }
+    __syncthreads();
+    for (int i = tid; i < 32 * (D / 8); i += kMergeThreads) {
+        const int r = i / (D / 8), c = i % (D / 8);
+        if (offset[r] >= 0)
+            reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(p.out) + offset[r])[c] = stage[r][c];
+    }
+}
+
+template <int D, int NT, bool KV8>
+cudaError_t launch_t(const ChunkParams &p, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                     cudaStream_t stream, int *launches) {
+    using C = ChunkCfg<D, NT, KV8>;
+    static bool configured[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (!configured[dev & 63]) {
+        e = cudaFuncSetAttribute(chunk_kernel<D, NT, KV8>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+        if (e != cudaSuccess) return e;
+        configured[dev & 63] = true;
+    }
+    chunk_kernel<D, NT, KV8><<<p.grid, C::kThreads, C::kSmemBytes, stream>>>(p, tq, tk, tv);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    ++*launches;
+    e = launch_after_previous(chunk_merge_kernel<D, NT>, dim3(NT * 4, p.grid), dim3(kMergeThreads), 0, stream, p);
+    if (e != cudaSuccess) return e;
+    ++*launches;
+    return cudaSuccess;
+}
+
+}  // namespace
+
+size_t chunk_workspace_bytes(int head_dim, int grid) {
+    const int rows = head_dim == 128 ? 256 : 128;
+    return (size_t)grid * (2 * (size_t)rows * (head_dim * 4 + 8) + sizeof(ChunkCut));
+}
+
+void chunk_place_workspace(ChunkParams *p, void *ws) {
+    const int64_t rows = p->D == 128 ? 256 : 128;
+    char *at = static_cast<char *>(ws);
+    p->part_o = reinterpret_cast<float *>(at);
+    at += (int64_t)p->grid * 2 * rows * p->D * 4;
+    p->part_ml = reinterpret_cast<float2 *>(at);
+    at += (int64_t)p->grid * 2 * rows * 8;
+    p->cuts = reinterpret_cast<ChunkCut *>(at);
+}
+
+cudaError_t launch_chunk(const ChunkParams &p, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                         cudaStream_t stream, int *launches) {
+    *launches = 0;
+    if (p.D == 256) return launch_t<256, 1, false>(p, tq, tk, tv, stream, launches);
+    if (p.kv8)
+        return p.row_tiles == 2 ? launch_t<128, 2, true>(p, tq, tk, tv, stream, launches)
+                                : launch_t<128, 1, true>(p, tq, tk, tv, stream, launches);
+    return p.row_tiles == 2 ? launch_t<128, 2, false>(p, tq, tk, tv, stream, launches)
+                            : launch_t<128, 1, false>(p, tq, tk, tv, stream, launches);
+}
+
+}  // namespace fw

@@ -29,6 +29,8 @@ decltype(&fw_tree_mask) g_mask;
 decltype(&fw_build_page_tables) g_tables;
 decltype(&fw_kv_commit) g_commit;
 decltype(&fw_verify_drafts) g_verify;
+decltype(&fw_paged_prefill) g_prefill;
+decltype(&fw_paged_prefill_workspace_size) g_prefill_workspace;
 decltype(&fw_qk_norm_rope) g_norm_rope;
 decltype(&fw_qk_norm_rope_append) g_norm_rope_append;
 PyObject *g_check;                     // raises FwError for a status
@@ -374,9 +376,56 @@ PyObject *qk_norm_rope_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// (q, k_cache, v_cache, block_table, cu_seqlens_q, seq_lens, scale, causal,
+//  window_left, k_scale, v_scale, out, lse, return_lse, workspace)
+PyObject *paged_prefill(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (!arity(n, 15)) return nullptr;
+    double scale, ks, vs;
+    long long window;
+    if (!number(a[6], &scale) || !whole(a[8], &window) || !number(a[9], &ks) || !number(a[10], &vs)) return nullptr;
+    const int causal = PyObject_IsTrue(a[7]), want_lse = PyObject_IsTrue(a[13]);
+    if (causal < 0 || want_lse < 0) return nullptr;
+    if (window > INT32_MAX) window = INT32_MAX;        // no key is that far
+    if (window < -1) raise(PyExc_ValueError, "window_left must be -1 or more");
+    const char *names[6] = {"q", "k_cache", "v_cache", "block_table", "cu_seqlens_q", "seq_lens"};
+    at::Tensor t[6];
+    Args args;
+    for (int i = 0; i < 6; ++i) {
+        t[i] = Args::take(a[i], names[i]);
+        need(t[i], names[i]);
+        args.place(t[i]);
+    }
+    at::Tensor out = Args::take(a[11], "out"), lse = Args::take(a[12], "lse"), ws = Args::take(a[14], "workspace");
+    args.place(out);
+    args.place(lse);
+    args.place(ws);
+    if (t[0].dim() != 3) raise(PyExc_ValueError, "q must be [total_q, Hq, D]");
+    Where where(args.device);
+    if (!out.defined()) out = empty(t[0].sizes(), at::kBFloat16, args.device);
+    if (!lse.defined() && want_lse) lse = empty(t[0].sizes().slice(0, 2), at::kFloat, args.device);
+    if (!ws.defined()) {
+        size_t bytes = 0;
+        if (failed(g_prefill_workspace((int32_t)t[0].size(2), &bytes))) return nullptr;
+        ws = empty({(int64_t)bytes}, at::kByte, args.device);
+    } else if (!ws.is_contiguous()) {
+        raise(PyExc_ValueError, "workspace must be contiguous");
+    }
+    fw_tensor_t *v[6];
+    for (int i = 0; i < 6; ++i) v[i] = args.add(t[i]);
+    fw_tensor_t *vo = args.add(out), *vl = args.add(lse);
+    // As in paged_decode_tree: a caller's empty tensor is a workspace of no bytes.
+    void *room = ws.nbytes() > 0 ? ws.data_ptr() : reinterpret_cast<void *>(256);
+    if (failed(g_prefill(v[0], v[1], v[2], v[3], v[4], v[5], (float)scale, (float)ks, (float)vs, causal, (int32_t)window, vo,
+                         vl, room, ws.nbytes(), where.stream())))
+        return nullptr;
+    return pair(out, lse);
+    END_HANDLE_TH_ERRORS
+}
+
 // (addresses of the C entry points, the status check)
 PyObject *connect(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    constexpr int kEntries = 8;
+    constexpr int kEntries = 10;
     if (!arity(n, kEntries + 1)) return nullptr;
     void *f[kEntries];
     for (int i = 0; i < kEntries; ++i) {
@@ -394,6 +443,8 @@ PyObject *connect(PyObject *, PyObject *const *a, Py_ssize_t n) {
     g_verify = reinterpret_cast<decltype(g_verify)>(f[5]);
     g_norm_rope = reinterpret_cast<decltype(g_norm_rope)>(f[6]);
     g_norm_rope_append = reinterpret_cast<decltype(g_norm_rope_append)>(f[7]);
+    g_prefill = reinterpret_cast<decltype(g_prefill)>(f[8]);
+    g_prefill_workspace = reinterpret_cast<decltype(g_prefill_workspace)>(f[9]);
     Py_XSETREF(g_check, Py_NewRef(a[kEntries]));
     Py_RETURN_NONE;
 }
@@ -404,6 +455,7 @@ PyMethodDef methods[] = {
     {"tree_mask", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(tree_mask)), METH_FASTCALL, nullptr},
     {"build_page_tables", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(build_page_tables)), METH_FASTCALL, nullptr},
     {"kv_commit", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(kv_commit)), METH_FASTCALL, nullptr},
+    {"paged_prefill", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(paged_prefill)), METH_FASTCALL, nullptr},
     {"verify_drafts", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(verify_drafts)), METH_FASTCALL, nullptr},
     {"qk_norm_rope", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(qk_norm_rope)), METH_FASTCALL, nullptr},
     {"qk_norm_rope_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(qk_norm_rope_append)), METH_FASTCALL, nullptr},

@@ -54,6 +54,11 @@ constexpr int kTreeMinSpan = 2;       // tree decode: fewest KV tiles (and empty
 // faster 3 .. 7 are within 1 us, FP8 136 at 3, 133 at 5, 132.6 at 7).
 constexpr int kTreePieceCostOne = 1;
 constexpr int kTreePieceCost = 5;
+// Chunk attention: the same, in keys; every unit weighs a tile more than its keys, for
+// the tiles that its first and last key share.
+constexpr int kChunkMinSpan = 256;
+constexpr int kChunkPieceCostOne = 128;
+constexpr int kChunkPieceCost = 640;
 constexpr int kMaxTableRows = 8192;   // page tables: requests whose sums fit a block's shared memory
 constexpr int kLatentRows = 64;       // latent-head decode: query heads per CTA (MMA N of one CTA)
 constexpr int kLatentPairRows = 128;  // latent-head decode on CTA pairs: query heads per pair
@@ -225,6 +230,39 @@ struct CommitParams {
     int *status;
 };
 
+// One chunk attention call (fw_paged_prefill), fully resolved on the host.
+struct ChunkCut {                              // a unit whose first piece ended a CTA's range
+    int count;                                 // its pieces, 0: none
+    int g, rt0, nrt, d, q0;                    // KV head, row tiles, the request's tokens and first packed row
+    int pad_[2];
+};
+struct ChunkParams {
+    int B, Hq, Hkv, G, D, ps, max_pages, num_pages;
+    int ps_shift;                              // log2 of ps, -1: not a power of two
+    int kv8;                                   // 1: E4M3 caches
+    int causal, window;                        // window < 0: none
+    int64_t total_q;
+    const int32_t *cu;                         // [B + 1] first packed rows
+    const int32_t *seq_lens;
+    const int32_t *block_table; int64_t bt_stride;
+    void *out; int64_t out_stride[2];          // [total_q, Hq, D] bf16
+    float *lse; int64_t lse_stride[2];         // [total_q, Hq] or null
+    float scale_log2;                          // scale * k_scale * log2(e)
+    float out_scale;                           // v_scale
+    int tile_tokens;                           // whole tokens of a 128-row tile (G <= 128)
+    int head_chunks;                           // > 1: 128-head row tiles of one token (G > 128)
+    int row_tiles;                             // row tiles of a unit, 1 or 2
+    int grid;                                  // CTAs
+    int ride;                                  // 1: the KV heads ride on the CTA index
+    int min_span, piece_cost;                  // in keys: least a range holds; what a unit's start weighs
+    float *part_o;                             // [2 * grid][row tiles of a unit * 128][D] unnormalised pieces
+    float2 *part_ml;                           // base (log2) and row sum of each of their rows
+    ChunkCut *cuts;                            // [grid]
+    int test_stall;                            // test hook: the producer first waits on a barrier nothing completes
+    uint64_t timeout_ns;
+    int *status;
+};
+
 // One fw_verify_drafts launch.
 struct VerifyParams {
     int B, T, V, A;
@@ -306,6 +344,10 @@ void tree_place_workspace(TreeParams *p, void *ws);
 cudaError_t launch_tree_mask(const TreeMaskParams &p, cudaStream_t stream);
 cudaError_t launch_page_tables(const PageTableParams &p, cudaStream_t stream, int *launches);
 cudaError_t launch_kv_commit(const CommitParams &p, cudaStream_t stream);
+cudaError_t launch_chunk(const ChunkParams &p, const CUtensorMap &tm_q, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
+                         cudaStream_t stream, int *launches);
+size_t chunk_workspace_bytes(int head_dim, int grid);
+void chunk_place_workspace(ChunkParams *p, void *ws);
 cudaError_t launch_verify(const VerifyParams &p, cudaStream_t stream);
 cudaError_t launch_norm_rope(const NormRopeParams &p, cudaStream_t stream);
 

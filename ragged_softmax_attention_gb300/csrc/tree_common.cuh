@@ -1,6 +1,8 @@
 // What the tree-decode kernels (BF16 and FP8 caches) share: the rows of a unit,
 // the walk over a CTA's range of the planned sequence, mask bits, the merge of
-// the pieces of cut units.
+// the pieces of cut units.  The chunk kernels take the softmax's arithmetic, the
+// page windows and the way rows are written from here (Params, Unit: theirs or the
+// tree's).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -277,7 +279,8 @@ __device__ __forceinline__ void copy_queries(const TreeParams &p, const TreeUnit
 
 // Whether page `l` of key tile j of a unit is copied: a tile has up to 16 pages,
 // one to a lane.
-__device__ __forceinline__ bool page_copied(const TreeParams &p, const TreeUnit &u, int j, int l) {
+template <typename Params, typename Unit>
+__device__ __forceinline__ bool page_copied(const Params &p, const Unit &u, int j, int l) {
     const int key = (u.tile0 + j) * kKvTile + (p.ps < kKvTile ? l * p.ps : 0);
     return l * p.ps < kKvTile && (l == 0 || p.ps < kKvTile) && j < u.ntiles && key < u.n;
 }
@@ -289,11 +292,13 @@ struct PageWindow {
     const int32_t *row;
     int win, last, cur, nxt;
 
-    __device__ __forceinline__ int page_number(const TreeParams &p, int key) const {
+    template <typename Params>
+    __device__ __forceinline__ int page_number(const Params &p, int key) const {
         return p.ps_shift >= 0 ? key >> p.ps_shift : key / p.ps;
     }
     __device__ __forceinline__ int entry(int lp) const { return lp <= last ? __ldg(row + lp) : 0; }
-    __device__ __forceinline__ void open(const TreeParams &p, const TreeUnit &u) {
+    template <typename Params, typename Unit>
+    __device__ __forceinline__ void open(const Params &p, const Unit &u) {
         const int lane = threadIdx.x & 31;
         row = p.block_table + (int64_t)u.b * p.bt_stride;
         win = page_number(p, u.tile0 * kKvTile);
@@ -302,7 +307,8 @@ struct PageWindow {
         nxt = entry(win + 32 + lane);
     }
     // The entry of page lane % 16 of key tile j (tiles in order; all lanes call).
-    __device__ __forceinline__ int at(const TreeParams &p, const TreeUnit &u, int j) {
+    template <typename Params, typename Unit>
+    __device__ __forceinline__ int at(const Params &p, const Unit &u, int j) {
         const int lane = threadIdx.x & 31;
         const int lp = page_number(p, (u.tile0 + j) * kKvTile);
         if (lp >= win + 32) {
@@ -316,7 +322,8 @@ struct PageWindow {
     }
 };
 // The page to copy, inside the pool whatever the table says.
-__device__ __forceinline__ int checked_page(const TreeParams &p, int phys) {
+template <typename Params>
+__device__ __forceinline__ int checked_page(const Params &p, int phys) {
     if ((unsigned)phys < (unsigned)p.num_pages) return phys;
     record_error(p.status, kErrInvalid);
     return 0;
@@ -370,25 +377,26 @@ __device__ __forceinline__ bool sees_bad(const uint32_t *bad, const TreeUnit &u,
 // A piece's partial rows: 16-byte units of four columns, the rows of a unit side by
 // side, so that a warp whose lanes are rows writes and reads whole lines.  (Row by
 // row, 32 lanes touch 32 lines a store, and a piece's end took 8,000 cycles.)
-template <int D, int NT>
-__device__ __forceinline__ float4 *part_unit(const TreeParams &p, int64_t slot, int unit, int row) {
+template <int D, int NT, typename Params>
+__device__ __forceinline__ float4 *part_unit(const Params &p, int64_t slot, int unit, int row) {
     return reinterpret_cast<float4 *>(p.part_o) + (slot * (D / 4) + unit) * (NT * 128) + row;
 }
 
 // This thread's row of a finished piece: its output and LSE, or its partial.
-// `load` reads 32 columns of O (warp-collective); columns 32 c0 .. 32 c1.
-template <int D, int NT, typename Load>
-__device__ __forceinline__ void write_row(const TreeParams &p, const TreeUnit &u, int x, int row, bool live, int t,
-                                          int h, float base2, float l_sum, bool poison, Load load,
-                                          int c0 = 0,
-                                          int c1 = D / 32) {
+// `at` and `lse_at` say where its output and LSE lie; `load` reads 32 columns of O
+// (warp-collective); columns 32 c0 .. 32 c1.
+template <int D, int NT, typename Params, typename Unit, typename Load>
+__device__ __forceinline__ void write_row_at(const Params &p, const Unit &u, int x, int row, bool live, long long out_at,
+                                             long long lse_at, float base2, float l_sum, bool poison, Load load,
+                                             int c0 = 0,
+                                             int c1 = D / 32) {
     const int lane = threadIdx.x & 31;
     // (A NaN sum is not zero: a NaN that the row sees comes out as NaN.)
     const bool some = l_sum != 0.f;
     const float inv = poison ? __int_as_float(0x7fc00000) : some ? p.out_scale / l_sum : 0.f;
     // Outputs: four lanes exchange their rows' four 16-byte units of a chunk, so that
     // each store writes 64 bytes of a row.
-    const long long at = live ? u.b * p.out_stride[0] + t * p.out_stride[1] + h * p.out_stride[2] : -1;
+    const long long at = live ? out_at : -1;
     long long to[4];
     if (u.part < 0) {
 #pragma unroll
@@ -436,9 +444,15 @@ __device__ __forceinline__ void write_row(const TreeParams &p, const TreeUnit &u
     }
     if (!live || c0 > 0) return;
     if (u.part >= 0) p.part_ml[(int64_t)u.part * (NT * 128) + x * 128 + row] = make_float2(base2, l_sum);
-    else if (p.lse)
-        p.lse[u.b * p.lse_stride[0] + t * p.lse_stride[1] + h * p.lse_stride[2]] =
-            some ? (base2 + log2f(l_sum)) * 0.69314718055994531f : kNegInf;
+    else if (p.lse) p.lse[lse_at] = some ? (base2 + log2f(l_sum)) * 0.69314718055994531f : kNegInf;
+}
+template <int D, int NT, typename Load>
+__device__ __forceinline__ void write_row(const TreeParams &p, const TreeUnit &u, int x, int row, bool live, int t,
+                                          int h, float base2, float l_sum, bool poison, Load load,
+                                          int c0 = 0,
+                                          int c1 = D / 32) {
+    write_row_at<D, NT>(p, u, x, row, live, u.b * p.out_stride[0] + t * p.out_stride[1] + h * p.out_stride[2],
+                        u.b * p.lse_stride[0] + t * p.lse_stride[1] + h * p.lse_stride[2], base2, l_sum, poison, load, c0, c1);
 }
 
 // One launch for the pieces, one for the merge of cut units.
