@@ -299,7 +299,7 @@ struct NormRopeParams {
     void *k_cache, *v_cache;
     int64_t kc_stride[3], vc_stride[3];        // elements (page, slot, head)
     float k_scale, v_scale;
-    int parts;                                 // warps that share a token's heads
+    float k_inv, v_inv;                        // their reciprocals; 0: the kernel divides
     int num_sms;
     int *status;
 };

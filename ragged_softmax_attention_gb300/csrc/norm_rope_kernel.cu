@@ -6,10 +6,20 @@
 // with i' = i + rot / 2 (halves) or the odd neighbour (interleaved).
 //
 // Every element is read and written once: DRAM bounds it from a few thousand
-// tokens on, latencies below.  A head takes D / 8 lanes, and a lane's eight
-// elements are four whole pairs, so the rotation needs no exchange and the sum of
-// squares log2(D / 8) shuffles; angles are a token's, so a warp keeps a lane's four
-// cosines and sines in registers over all heads that it takes of a token.
+// tokens on, latencies below.  A head takes D / 16 lanes, and a lane's sixteen
+// elements are eight whole pairs, so the rotation needs no exchange and the sum of
+// squares log2(D / 16) shuffles (eight elements a lane cost a third more instructions;
+// kept for rotations of an odd number of eights).  A warp has a token, or a share of one's
+// heads, to itself: it works out the cosines and sines once, a lane's share of them times
+// the weights stays in registers over all heads, and copies run ahead through a ring of
+// shared memory, past the end of the token, in which a lane reads what it copied itself,
+// so that nothing waits for another warp.
+//
+// Measured (GB300): 8,191 tokens of 40/8 heads into an FP8 cache, 218 MB in 36 us, 0.90 of
+// copy; 5,000 of 32/8 heads with three axes, 102 MB in 19.7, 0.76; 48 tokens 4.0, all of it
+// round trips.  On the way, first case: every warp that shares a token working out its
+// angles, loads by round 85 us; a block's tokens together 64; copies ahead 57; a warp to a
+// token 47; the head groups of all tokens in equal runs, codes without division 36.
 //
 // An angle is needed modulo one turn, and pos * inv_freq in 32 bits loses it (1e5
 // radians are good to 0.008).  inv_freq / 2 pi is kept as a 64-bit fraction of a
@@ -26,190 +36,415 @@ namespace {
 
 constexpr int kErrInvalid = 1;     // FW_ERR_INVALID_ARG
 constexpr int kRopeWarps = 8;
-constexpr int kAhead = 4;          // heads of a lane in flight
-
+constexpr int kRopeThreads = kRopeWarps * 32;
+constexpr int kRopeBlocks = 2;     // resident blocks an SM
+constexpr int kStages = 6;         // head groups of a warp on their way or in hand
+typedef uint64_t f32x2;
+__device__ __forceinline__ f32x2 two(float lo, float hi) {
+    f32x2 d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+__device__ __forceinline__ float2 both(f32x2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<uint32_t *>(&v);
 }
-__device__ __forceinline__ uint2 pack_bf16x4(const float *v) {
-    return make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-}
-// Codes of v / scale as the append stores them.
-__device__ __forceinline__ uint32_t pack_e4m3x4(const float *v, float scale) {
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(v[0], scale), __fdiv_rn(v[1], scale)),
-                                                 __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(v[2], scale), __fdiv_rn(v[3], scale)),
-                                                 __NV_SATFINITE, __NV_E4M3);
-    return lo | hi << 16;
-}
-__device__ __forceinline__ void unpack_bf16x4(uint2 w, float *v) {
-    v[0] = __uint_as_float(w.x << 16);
-    v[1] = __uint_as_float(w.x & 0xffff0000u);
-    v[2] = __uint_as_float(w.y << 16);
-    v[3] = __uint_as_float(w.y & 0xffff0000u);
+__device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// E4M3 codes of v / scale, as the append divides.  With inv = 1 / scale rounded to nearest,
+// q = v * inv is off by two roundings, and q + (v - q scale) inv, the remainder being
+// exact, by less than 2^-46 before its own rounding (Markstein, "Computation of elementary
+// functions on the IBM RISC System/6000 processor", section 8), as long as nothing over-
+// or underflows: for scales of 2^-60 .. 2^60 and quotients below 2^10; those so small that
+// the remainder is not exact have code 0, and their sign is put back.  Other scales (inv =
+// 0), and lanes with a quotient that large, an infinity or a NaN, divide.  (Division alone:
+// 115 us for 4,864 tokens of 128 key and value heads, 94 so.)
+template <int N>
+__device__ __forceinline__ void codes(const float *v, float scale, float inv, uint32_t *out) {
+    float r[N], most = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+        const f32x2 x = two(v[i], v[i + 1]), y = two(inv, inv), q = mul2(x, y);
+        const float2 a = both(q), z = both(fma2(fma2(q, two(-scale, -scale), x), y, q));
+        // (fmaxf drops a NaN; a sum would not, but inf - inf may come of one.)
+        most = fmaxf(most, fmaxf(fabsf(a.x), fabsf(a.y)));
+        r[i] = __uint_as_float(__float_as_uint(z.x) | (__float_as_uint(v[i]) & 0x80000000u));
+        r[i + 1] = __uint_as_float(__float_as_uint(z.y) | (__float_as_uint(v[i + 1]) & 0x80000000u));
+    }
+    if (__builtin_expect(!(most < 1024.f) || inv == 0.f, 0)) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) r[i] = __fdiv_rn(v[i], scale);
+    }
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+        out[i / 4] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(r[i], r[i + 1]), __NV_SATFINITE, __NV_E4M3) |
+                     (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(r[i + 2], r[i + 3]), __NV_SATFINITE, __NV_E4M3) << 16;
 }
 
-template <int D, bool kInter>
-__global__ void __launch_bounds__(kRopeWarps * 32, 4) norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
-    constexpr int L = D / 8, HPW = 32 / L;           // lanes of a head, heads of a warp
+// A run of half a lane's elements, as it lies in memory: E / 2 BF16 values.
+template <int E> struct Run;
+template <> struct Run<8> { uint2 w; __device__ uint32_t at(int i) const { return i ? w.y : w.x; } };
+template <> struct Run<16> {
+    uint4 w;
+    __device__ uint32_t at(int i) const { return i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w; }
+};
+
+template <int E>
+__device__ __forceinline__ void copy_run(Run<E> *to, const uint16_t *from) {
+    if constexpr (E == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+}
+
+// A lane's E elements of a head: run 0 and run 1.  Pair i is element i of either run
+// (halves), or neighbours (interleaved); a[] and b[] are the pairs' parts, two pairs each.
+template <int E, bool kInter>
+struct Pairs {
+    static constexpr int P = E / 4;
+    f32x2 a[P], b[P];
+    __device__ __forceinline__ void unpack(const Run<E> &r0, const Run<E> &r1) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            if (kInter) {
+                const Run<E> &r = i < P / 2 ? r0 : r1;
+                const uint32_t w0 = r.at(2 * i % P), w1 = r.at(2 * i % P + 1);
+                a[i] = two(low(w0), low(w1));
+                b[i] = two(high(w0), high(w1));
+            } else {
+                a[i] = two(low(r0.at(i)), high(r0.at(i)));
+                b[i] = two(low(r1.at(i)), high(r1.at(i)));
+            }
+        }
+    }
+    __device__ __forceinline__ void values(float (&v)[E]) const {             // run 0, then run 1
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const float2 x = both(a[i]), y = both(b[i]);
+            if (kInter) { v[4 * i] = x.x; v[4 * i + 1] = y.x; v[4 * i + 2] = x.y; v[4 * i + 3] = y.y; }
+            else { v[2 * i] = x.x; v[2 * i + 1] = x.y; v[E / 2 + 2 * i] = y.x; v[E / 2 + 2 * i + 1] = y.y; }
+        }
+    }
+    __device__ __forceinline__ float squares() const {
+        f32x2 s = mul2(a[0], a[0]), t = mul2(b[0], b[0]);
+#pragma unroll
+        for (int i = 1; i < P; ++i) { s = fma2(a[i], a[i], s); t = fma2(b[i], b[i], t); }
+        const float2 x = both(s), y = both(t);
+        return (x.x + x.y) + (y.x + y.y);
+    }
+};
+template <int E>
+__device__ __forceinline__ void store_bf16(char *to, const float *v) {
+    if constexpr (E == 16)
+        *reinterpret_cast<uint4 *>(to) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                                                    pack_bf16x2(v[6], v[7]));
+    else
+        *reinterpret_cast<uint2 *>(to) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+}
+template <int E>
+__device__ __forceinline__ void store_codes(char *to0, char *to1, const float *v, float scale, float inv) {
+    uint32_t w[E / 4];
+    codes<E>(v, scale, inv, w);
+    if constexpr (E == 16) {
+        *reinterpret_cast<uint2 *>(to0) = make_uint2(w[0], w[1]);
+        *reinterpret_cast<uint2 *>(to1) = make_uint2(w[2], w[3]);
+    } else {
+        *reinterpret_cast<uint32_t *>(to0) = w[0];
+        *reinterpret_cast<uint32_t *>(to1) = w[1];
+    }
+}
+
+template <int D, int E, bool kInter, bool kPartial>
+__global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
+    constexpr int L = D / E, H = E / 2, P = E / 4;   // lanes of a head; elements and f32x2s of a run
+    constexpr int HPW = 32 / L;                      // heads of a warp, a group
+    constexpr int kAngles = D / 64;                  // of a lane
     __shared__ uint64_t turn[D / 2];                 // inv_freq / 2 pi in 2^-64 turns
     __shared__ int axis[D / 2];
-    __shared__ __align__(16) float weight[2][D];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int i = threadIdx.x; i < p.rot / 2; i += blockDim.x) {
-        const double t = (double)__ldg(p.inv_freq + i) * 0.15915494309189533577;
-        turn[i] = __double2ull_rn((t - floor(t)) * 18446744073709551616.0);
-        int a = p.axis_map ? __ldg(p.axis_map + i) : 0;
-        if ((unsigned)a >= (unsigned)p.axes) {
-            record_error(p.status, kErrInvalid);
-            a = 0;
-        }
-        axis[i] = a;
-    }
-    for (int i = threadIdx.x; i < 2 * D; i += blockDim.x) {
-        const void *w = p.weight[i / D];
-        if (w) weight[i / D][i % D] = p.weight_f32[i / D] ? static_cast<const float *>(w)[i % D]
-                                                          : __bfloat162float(static_cast<const __nv_bfloat16 *>(w)[i % D]);
-    }
-    __syncthreads();
-
-    // This lane's elements of a head: two runs of four, o0 and o1 on; as pairs
-    // (o0 + i, o1 + i) for halves, neighbours when interleaved.
+    __shared__ __align__(16) float weight[2][D];     // the first parts of the pairs in order, then the second
+    __shared__ __align__(16) float cosine[kRopeWarps][D / 2], sine[kRopeWarps][D / 2];
+    extern __shared__ __align__(16) uint8_t ring_bytes[];
+    Run<E> (*ring)[2][kRopeThreads] = reinterpret_cast<Run<E> (*)[2][kRopeThreads]>(ring_bytes);      // [kStages]
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, half = p.rot / 2;
+    // This lane's elements of a head: two runs, o0 and o1 on; its pairs' numbers begin at
+    // H j (elements that do not turn make pairs of their own).
     const int j = lane % L, sub = lane / L;
-    const bool rotates = 8 * j < p.rot;
-    const int o0 = kInter || !rotates ? 8 * j : 4 * j;
-    const int o1 = kInter || !rotates ? 8 * j + 4 : p.rot / 2 + 4 * j;
+    const bool rotates = !kPartial || E * j < p.rot;
+    const int o0 = kInter || !rotates ? E * j : H * j;
+    const int o1 = kInter || !rotates ? E * j + H : half + H * j;
+
+    // A token's head groups are queries, keys, values in that order; those of all tokens,
+    // end to end, go to the warps in equal runs.
     const int nq = (p.Hq + HPW - 1) / HPW, nk = (p.Hkv + HPW - 1) / HPW;
     const int groups = nq + nk + (p.v ? nk : 0);
-    const int64_t items = p.N * p.parts;
-    for (int64_t item = (int64_t)blockIdx.x * kRopeWarps + warp; item < items; item += (int64_t)gridDim.x * kRopeWarps) {
-        int64_t n = item;
-        int part = 0;
-        if (p.parts > 1) {
-            n = item < (1ll << 31) ? (int64_t)((uint32_t)item / (uint32_t)p.parts) : item / p.parts;
-            part = (int)(item - n * p.parts);
+    const int64_t total = p.N * groups, warps = (int64_t)gridDim.x * kRopeWarps;
+    const int64_t me = (int64_t)blockIdx.x * kRopeWarps + warp;
+    const int64_t from = total / warps * me + min(me, total % warps);     // the first total % warps take one more
+    const int64_t count = total / warps + (me < total % warps);
+    const int64_t n_first = from / groups;
+    const int g_first = (int)(from - n_first * groups);
+
+    // The copies, kStages - 1 groups ahead.
+    int64_t f_n = n_first, f_rest = count, f_step = 0;
+    int f_kind = 0, f_left = 0, f_heads = 0, f_stage = 0, f_g = g_first;
+    const uint16_t *f_src = nullptr;
+    auto fetch = [&]() {
+        if (f_left == 0 && f_rest > 0) {                  // the next kind of heads, the next token
+            if (f_g == groups) { f_g = 0; ++f_n; }
+            f_kind = f_g < nq ? 0 : f_g < nq + nk ? 1 : 2;
+            const int begin = f_kind == 0 ? 0 : f_kind == 1 ? nq : nq + nk, end = f_kind == 0 ? nq : f_kind == 1 ? nq + nk : groups;
+            f_left = (int)min((int64_t)(end - f_g), f_rest);
+            const int h = (f_g - begin) * HPW + sub;
+            f_g += f_left;
+            f_rest -= f_left;
+            const int64_t step = f_kind == 0 ? p.q_stride[1] : f_kind == 1 ? p.k_stride[1] : p.v_stride[1];
+            f_src = (f_kind == 0 ? p.q + f_n * p.q_stride[0] : f_kind == 1 ? p.k + f_n * p.k_stride[0] : p.v + f_n * p.v_stride[0]) +
+                    h * step + (f_kind == 2 ? E * j : o0);
+            f_step = step * HPW;
+            f_heads = (f_kind == 0 ? p.Hq : p.Hkv) - h;
         }
-        const int g0 = (int)((int64_t)groups * part / p.parts), g1 = (int)((int64_t)groups * (part + 1) / p.parts);
+        if (f_left > 0) {
+            if (f_heads > 0) {
+                copy_run(&ring[f_stage][0][tid], f_src);
+                copy_run(&ring[f_stage][1][tid], f_src + (f_kind == 2 ? H : o1 - o0));
+            }
+            --f_left;
+            f_heads -= HPW;
+            f_src += f_step;
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        f_stage = f_stage + 1 == kStages ? 0 : f_stage + 1;
+    };
+#pragma unroll 1
+    for (int i = 0; i < kStages - 1; ++i) fetch();
+
+    // What the next token's angles and place need, on its way while this one goes through.
+    int32_t pos[kAngles], slot = -1;
+    auto look = [&](int64_t n) {
+        if (n >= p.N) return;
+#pragma unroll
+        for (int k = 0; k < kAngles; ++k) {
+            const int f = lane + 32 * k;
+            pos[k] = f < half ? __ldg(p.positions + (p.axes > 1 ? axis[f] * p.pos_stride : 0) + n) : 0;
+        }
+        slot = p.slots ? __ldg(p.slots + n) : -1;
+    };
+    // The block's tables, their loads (and the first token's) all on their way before the
+    // first is used: with few tokens these round trips are most of the time.
+    static_assert(D <= kRopeThreads, "a thread to a table entry");
+    const float freq = tid < half ? __ldg(p.inv_freq + tid) : 0.f;
+    const int on_axis = tid < half && p.axis_map ? __ldg(p.axis_map + tid) : 0;
+    float w_of[2] = {1.f, 1.f};                               // pair tid / 2's first or second part
+    if (tid < D) {
+        const int pr = tid >> 1, lj = pr / H;
+        const int e = kInter ? tid : E * lj >= p.rot ? E * lj + pr % H + H * (tid & 1) : pr + (tid & 1) * half;
+#pragma unroll
+        for (int kind = 0; kind < 2; ++kind) {
+            const void *w = p.weight[kind];
+            if (w) w_of[kind] = p.weight_f32[kind] ? __ldg(static_cast<const float *>(w) + e)
+                                                   : __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t *>(w) + e) << 16);
+        }
+    }
+    if (p.axes == 1) look(n_first);
+    if (tid < half) {
+        const double t = (double)freq * 0.15915494309189533577;
+        turn[tid] = __double2ull_rn((t - floor(t)) * 18446744073709551616.0);
+        if ((unsigned)on_axis >= (unsigned)p.axes) record_error(p.status, kErrInvalid);
+        axis[tid] = (unsigned)on_axis < (unsigned)p.axes ? on_axis : 0;
+    }
+    if (tid < D) {
+        weight[0][(tid >> 1) + (tid & 1) * (D / 2)] = w_of[0];
+        weight[1][(tid >> 1) + (tid & 1) * (D / 2)] = w_of[1];
+    }
+    __syncthreads();
+    if (p.axes > 1) look(n_first);
+
+    int stage = 0, g = g_first;
+    int64_t rest = count;
+    for (int64_t token = n_first; rest > 0; ++token, g = 0) {
+        const int last = (int)min((int64_t)groups, g + rest);
+        rest -= last - g;
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < kAngles; ++k) {
+            const int f = lane + 32 * k;
+            float c = 1.f, s = 0.f;
+            if (f < half) {
+                const int32_t frac = (int32_t)((uint64_t)(int64_t)pos[k] * turn[f] >> 32);
+                sincospif((float)frac * 4.656612873077393e-10f, &s, &c);     // 2^-31: half turns
+            }
+            cosine[warp][f] = c;
+            sine[warp][f] = s;
+        }
+        __syncwarp();
         // The token's cache row, if it has one.
         int64_t kdst = -1, vdst = -1;
-        if (p.slots && g1 > nq) {
-            const int s = __ldg(p.slots + n);
-            const int64_t row = p.layer_base + s;
-            if (s >= 0 && row < p.cache_rows) {
+        if (p.slots && last > nq) {
+            const int64_t row = p.layer_base + slot;
+            if (slot >= 0 && row < p.cache_rows) {
                 const int64_t page = p.ps_shift >= 0 ? row >> p.ps_shift : row / p.ps;
                 const int64_t off = row - page * p.ps;
                 kdst = page * p.kc_stride[0] + off * p.kc_stride[1];
                 vdst = page * p.vc_stride[0] + off * p.vc_stride[1];
-            } else if (s >= 0 && lane == 0) {
+            } else if (slot >= 0 && lane == 0) {
                 record_error(p.status, kErrInvalid);
             }
         }
-        float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
-        if (rotates && g0 < nq + nk) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int64_t pos = __ldg(p.positions + axis[4 * j + i] * p.pos_stride + n);
-                const int32_t frac = (int32_t)((uint64_t)pos * turn[4 * j + i] >> 32);
-                sincospif((float)frac * 4.656612873077393e-10f, &s[i], &c[i]);      // 2^-31: half turns
+        if (rest > 0) look(token + 1);
+#pragma unroll 1
+        for (int kind = 0; kind < 3; ++kind) {
+            const int end = min(last, kind == 0 ? nq : kind == 1 ? nq + nk : groups);
+            if (g >= end) continue;
+            int left = end - g;
+            int h = (g - (kind == 0 ? 0 : kind == 1 ? nq : nq + nk)) * HPW + sub;
+            g = end;
+            const bool code = kind > 0 && p.slots && p.kv8;
+            const float scale = kind == 1 ? p.k_scale : p.v_scale, inv = kind == 1 ? p.k_inv : p.v_inv;
+            int64_t step;                                     // bytes
+            char *dst;
+            if (kind == 0) {
+                step = 2 * p.qo_stride[1];
+                dst = reinterpret_cast<char *>(p.q_out + token * p.qo_stride[0]);
+            } else if (!p.slots) {
+                step = 2 * p.ko_stride[1];
+                dst = reinterpret_cast<char *>(p.k_out + token * p.ko_stride[0]);
+            } else {
+                const int size = p.kv8 ? 1 : 2;
+                step = size * (kind == 1 ? p.kc_stride[2] : p.vc_stride[2]);
+                dst = static_cast<char *>(kind == 1 ? p.k_cache : p.v_cache) + size * (kind == 1 ? kdst : vdst);
             }
-        }
-        for (int g = g0; g < g1; g += kAhead) {
-            uint2 in[kAhead][2];
+            dst += h * step;
+            step *= HPW;
+            h = (kind == 0 ? p.Hq : p.Hkv) - h;               // > 0: this lane's head is one
+            if (kind > 0 && p.slots && kdst < 0) h = 0;       // a token without a slot
+            if (kind == 2) {
+                // Values: as they came, or as codes.
+#pragma unroll 1
+                for (; left > 0; --left, h -= HPW, dst += step) {
+                    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+                    const Run<E> r0 = ring[stage][0][tid], r1 = ring[stage][1][tid];
+                    stage = stage + 1 == kStages ? 0 : stage + 1;
+                    fetch();
+                    if (h <= 0) continue;
+                    if (code) {
+                        float v[E];
 #pragma unroll
-            for (int a = 0; a < kAhead; ++a) {
-                const int gg = g + a;
-                if (gg >= g1) continue;
-                const int kind = gg < nq ? 0 : gg < nq + nk ? 1 : 2;
-                const int h = (gg - (kind == 0 ? 0 : kind == 1 ? nq : nq + nk)) * HPW + sub;
-                if (h >= (kind == 0 ? p.Hq : p.Hkv)) continue;
-                const uint16_t *src = kind == 0 ? p.q + n * p.q_stride[0] + h * p.q_stride[1]
-                                    : kind == 1 ? p.k + n * p.k_stride[0] + h * p.k_stride[1]
-                                                : p.v + n * p.v_stride[0] + h * p.v_stride[1];
-                in[a][0] = *reinterpret_cast<const uint2 *>(src + o0);
-                in[a][1] = *reinterpret_cast<const uint2 *>(src + o1);
-            }
-#pragma unroll
-            for (int a = 0; a < kAhead; ++a) {
-                const int gg = g + a;
-                if (gg >= g1) break;
-                const int kind = gg < nq ? 0 : gg < nq + nk ? 1 : 2;
-                const int h = (gg - (kind == 0 ? 0 : kind == 1 ? nq : nq + nk)) * HPW + sub;
-                const bool live = h < (kind == 0 ? p.Hq : p.Hkv);
-                if (kind > 0 && p.slots && kdst < 0) continue;          // a token without a slot
-                float v[8];
-                unpack_bf16x4(in[a][0], v);
-                unpack_bf16x4(in[a][1], v + 4);
-                if (kind < 2) {
-                    if (p.weight[kind]) {
-                        float sq = 0.f;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) sq = fmaf(v[i], v[i], sq);
-#pragma unroll
-                        for (int o = L / 2; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
-                        const float r = rsqrtf(sq * (1.f / D) + p.eps);
-                        const float4 w0 = *reinterpret_cast<const float4 *>(&weight[kind][o0]);
-                        const float4 w1 = *reinterpret_cast<const float4 *>(&weight[kind][o1]);
-                        v[0] *= r * w0.x; v[1] *= r * w0.y; v[2] *= r * w0.z; v[3] *= r * w0.w;
-                        v[4] *= r * w1.x; v[5] *= r * w1.y; v[6] *= r * w1.z; v[7] *= r * w1.w;
-                    }
-                    if (rotates) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int x = kInter ? 2 * i : i, y = kInter ? 2 * i + 1 : i + 4;
-                            const float a0 = v[x], b0 = v[y];
-                            v[x] = fmaf(a0, c[i], -b0 * s[i]);
-                            v[y] = fmaf(b0, c[i], a0 * s[i]);
+                        for (int i = 0; i < P; ++i) {
+                            v[2 * i] = low(r0.at(i));     v[2 * i + 1] = high(r0.at(i));
+                            v[H + 2 * i] = low(r1.at(i)); v[H + 2 * i + 1] = high(r1.at(i));
                         }
+                        store_codes<E>(dst + E * j, dst + E * j + H, v, scale, inv);
+                    } else {
+                        *reinterpret_cast<Run<E> *>(dst + 2 * E * j) = r0;
+                        *reinterpret_cast<Run<E> *>(dst + 2 * E * j + E) = r1;
                     }
                 }
-                if (!live) continue;
-                if (kind > 0 && p.kv8) {
-                    const float scale = kind == 1 ? p.k_scale : p.v_scale;
-                    uint8_t *dst = kind == 1 ? static_cast<uint8_t *>(p.k_cache) + kdst + h * p.kc_stride[2]
-                                             : static_cast<uint8_t *>(p.v_cache) + vdst + h * p.vc_stride[2];
-                    *reinterpret_cast<uint32_t *>(dst + o0) = pack_e4m3x4(v, scale);
-                    *reinterpret_cast<uint32_t *>(dst + o1) = pack_e4m3x4(v + 4, scale);
+                continue;
+            }
+            // What a pair's parts are multiplied by: a' = a ca - b sb, b' = b cb + a sa.
+            f32x2 ca[P], sb[P], cb[P], sa[P];
+#pragma unroll
+            for (int i = 0; i < P; i += 2) {
+                const float4 wa = *reinterpret_cast<const float4 *>(&weight[kind][H * j + 2 * i]);
+                const float4 wb = *reinterpret_cast<const float4 *>(&weight[kind][D / 2 + H * j + 2 * i]);
+                const float4 c = *reinterpret_cast<const float4 *>(&cosine[warp][H * j + 2 * i]);
+                const float4 s = *reinterpret_cast<const float4 *>(&sine[warp][H * j + 2 * i]);
+                ca[i] = mul2(two(wa.x, wa.y), two(c.x, c.y));   ca[i + 1] = mul2(two(wa.z, wa.w), two(c.z, c.w));
+                cb[i] = mul2(two(wb.x, wb.y), two(c.x, c.y));   cb[i + 1] = mul2(two(wb.z, wb.w), two(c.z, c.w));
+                sa[i] = mul2(two(wa.x, wa.y), two(s.x, s.y));   sa[i + 1] = mul2(two(wa.z, wa.w), two(s.z, s.w));
+                sb[i] = mul2(two(wb.x, wb.y), two(-s.x, -s.y)); sb[i + 1] = mul2(two(wb.z, wb.w), two(-s.z, -s.w));
+            }
+            const bool norm = p.weight[kind] != nullptr;
+#pragma unroll 1
+            for (; left > 0; --left, h -= HPW, dst += step) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+                Pairs<E, kInter> x;
+                x.unpack(ring[stage][0][tid], ring[stage][1][tid]);
+                stage = stage + 1 == kStages ? 0 : stage + 1;
+                fetch();
+                float r = 1.f;
+                if (norm) {
+                    float sq = x.squares();
+#pragma unroll
+                    for (int o = L / 2; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+                    r = rsqrtf(sq * (1.f / D) + p.eps);
+                }
+                const f32x2 rr = two(r, r);
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    // (A lane of elements that do not turn leaves its pairs' other parts out.)
+                    const f32x2 u = mul2(x.a[i], ca[i]), w = mul2(x.b[i], cb[i]);
+                    const f32x2 ya = rotates ? fma2(x.b[i], sb[i], u) : u, yb = rotates ? fma2(x.a[i], sa[i], w) : w;
+                    x.a[i] = mul2(ya, rr);
+                    x.b[i] = mul2(yb, rr);
+                }
+                if (h <= 0) continue;
+                float v[E];
+                x.values(v);
+                if (code) {
+                    store_codes<E>(dst + o0, dst + o1, v, scale, inv);
                 } else {
-                    uint16_t *dst = kind == 0 ? p.q_out + n * p.qo_stride[0] + h * p.qo_stride[1]
-                                  : kind == 2 ? static_cast<uint16_t *>(p.v_cache) + vdst + h * p.vc_stride[2]
-                                  : p.slots   ? static_cast<uint16_t *>(p.k_cache) + kdst + h * p.kc_stride[2]
-                                              : p.k_out + n * p.ko_stride[0] + h * p.ko_stride[1];
-                    // Values go through as they came (their bits: a NaN's too).
-                    *reinterpret_cast<uint2 *>(dst + o0) = kind == 2 ? in[a][0] : pack_bf16x4(v);
-                    *reinterpret_cast<uint2 *>(dst + o1) = kind == 2 ? in[a][1] : pack_bf16x4(v + 4);
+                    store_bf16<E>(dst + 2 * o0, v);
+                    store_bf16<E>(dst + 2 * o1, v + H);
                 }
             }
         }
     }
 }
 
-template <int D>
+template <int D, int E>
 cudaError_t launch_dim(const NormRopeParams &p, cudaStream_t stream) {
-    constexpr int HPW = 256 / D;
+    constexpr int HPW = 32 * E / D;
     NormRopeParams a = p;
     const int nk = (p.Hkv + HPW - 1) / HPW;
     const int groups = (p.Hq + HPW - 1) / HPW + nk + (p.v ? nk : 0);
-    // A token's heads are shared out among so many warps that each SM has some 32 with
-    // a few rounds each; with many tokens a warp takes a token whole.
-    const int64_t warps = (int64_t)p.num_sms * 32;
-    const int64_t parts = (4 * warps + p.N - 1) / p.N;
-    a.parts = (int)(parts < groups ? parts : groups);
-    if (a.parts < 1) a.parts = 1;
-    const int64_t blocks = (p.N * a.parts + kRopeWarps - 1) / kRopeWarps;
-    const int64_t most = (int64_t)p.num_sms * 4;
+    // As many warps as fit, or as there are head groups.
+    const int64_t most = (int64_t)p.num_sms * kRopeBlocks, blocks = (p.N * groups + kRopeWarps - 1) / kRopeWarps;
     const unsigned grid = (unsigned)(blocks < most ? blocks : most);
-    if (p.interleaved) norm_rope_kernel<D, true><<<grid, kRopeWarps * 32, 0, stream>>>(a);
-    else norm_rope_kernel<D, false><<<grid, kRopeWarps * 32, 0, stream>>>(a);
+    auto usual = [](float x) { return x >= 8.67e-19f && x <= 1.15e18f; };      // 2^-60 .. 2^60
+    a.k_inv = p.kv8 && usual(p.k_scale) ? 1.f / p.k_scale : 0.f;
+    a.v_inv = p.kv8 && usual(p.v_scale) ? 1.f / p.v_scale : 0.f;
+    const int which = 2 * (p.interleaved ? 1 : 0) + (p.rot < D ? 1 : 0);
+    auto kernel = p.interleaved ? norm_rope_kernel<D, E, true, true> : norm_rope_kernel<D, E, false, true>;
+    if constexpr (E == 16)
+        if (p.rot == D) kernel = p.interleaved ? norm_rope_kernel<D, E, true, false> : norm_rope_kernel<D, E, false, false>;
+    const int smem = kStages * 2 * kRopeThreads * (int)sizeof(Run<E>);
+    static bool configured[64][4] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (!configured[dev & 63][which]) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        configured[dev & 63][which] = true;
+    }
+    kernel<<<grid, kRopeThreads, smem, stream>>>(a);
     return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_norm_rope(const NormRopeParams &p, cudaStream_t stream) {
-    if (p.D == 64) return launch_dim<64>(p, stream);
-    if (p.D == 128) return launch_dim<128>(p, stream);
-    return launch_dim<256>(p, stream);
+    // Sixteen elements a lane where the rotated part divides so.
+    if (p.rot % 16)
+        return p.D == 64 ? launch_dim<64, 8>(p, stream) : p.D == 128 ? launch_dim<128, 8>(p, stream) : launch_dim<256, 8>(p, stream);
+    return p.D == 64 ? launch_dim<64, 16>(p, stream) : p.D == 128 ? launch_dim<128, 16>(p, stream) : launch_dim<256, 16>(p, stream);
 }
 
 }  // namespace fw

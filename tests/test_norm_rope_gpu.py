@@ -183,6 +183,23 @@ def test_append(fw, dtype, N, Hq, Hkv, D, ps, base):
     assert fw.device_status() == 0
 
 
+@pytest.mark.parametrize("scale", [1.0, 0.013, 1 / 3, 0.75, 1.9999999, 448.0, 2.0 ** -70, 1e-30, 1e25, 3e38, 0.1, 7e-4])
+def test_every_value_is_coded_as_the_append_codes_it(fw, scale):
+    every = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(torch.bfloat16).view(256, 2, 128).cuda()
+    x, _ = make(256, 2, 2, 128, norm=False, seed=4)
+    slots = torch.arange(256, dtype=torch.int32, device="cuda")
+    a, b = (torch.zeros(16, 16, 2, 128, dtype=torch.float8_e4m3fn, device="cuda") for _ in range(2))
+    k = torch.zeros_like(a)
+    x["positions"].zero_()                            # keys by no angle: as they are
+    x["k"] = every
+    fw.qk_norm_rope_append(v=every, slot_mapping=slots, layer_base_rows=0, k_cache=k, v_cache=a, k_scale=scale, v_scale=scale, **x)
+    fw.kv_append(every[:, None], None, slots[:, None].contiguous(), 0, b, None, k_scale=scale)
+    assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    # (A turn by nothing adds zeros, which a key whose partner is not finite does not survive.)
+    ok = torch.isfinite(every) & torch.isfinite(every.roll(64, 2)) & (every != 0)
+    assert torch.equal(k.view(torch.uint8).view(256, 2, 128)[ok], b.view(torch.uint8).view(256, 2, 128)[ok])
+
+
 def test_append_of_keys_alone_padded_slots_and_strided_cache(fw):
     x, _ = make(12, 4, 2, 128, seed=1)
     big = torch.zeros(4, 2, 16, 2, 128, dtype=torch.bfloat16, device="cuda")   # K and V halves of every page
