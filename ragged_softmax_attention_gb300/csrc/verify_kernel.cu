@@ -22,6 +22,12 @@
 // CTAs, a segment to a warp, with the segments' sums left in shared memory, so that
 // the draw looks again at one segment alone.  The walking thread tells the other CTAs
 // what to do, so that they meet the same number of times whatever they read.
+//
+// Measured (GB300): 64 trees of 24 drafts over 152,000 tokens, one to six sweeps each, 71 us;
+// a sweep takes a CTA of eight 6.3 us, bound by its instructions (some 40 an element where
+// a product is subtracted), and the request with the most sweeps 54 us.  With every
+// rejection gone through for each element 137 us.  A chain of 6 over 32,000 tokens: 9.8 us,
+// launch, two rounds of loads, three meetings of the cluster.
 #include "fw_internal.h"
 #include "fw_ptx.cuh"
 
@@ -59,13 +65,14 @@ __device__ __forceinline__ void store_remote(const u64 *p, uint32_t rank, u64 v)
 }
 
 // A probability in units of 2^-60; NaN and what is negative count as 0, more than 1 as 1.
+// The 24-bit significand stands above the place of 1 and moves down by the exponent (a
+// shift past 63 gives 0: zeros, subnormals and what is below 2^-61).
 __device__ __forceinline__ u64 fixed(float v) {
-    if (!(v > 0.f)) return 0;
-    if (v >= 1.f) return kOne;
-    const uint32_t b = __float_as_uint(v);
-    const int e = (int)(b >> 23) - 90;                    // 2^(exponent - 127 - 23) / 2^-60
-    const u64 m = (b & 0x7fffffu) | 0x800000u;            // (a subnormal's is lost either way)
-    return e >= 0 ? m << e : e > -24 ? m >> -e : 0;
+    const uint32_t b = __float_as_uint(__saturatef(v));
+    const u64 m = (u64)((b & 0x7fffffu) | 0x800000u) << 37;
+    u64 r;
+    asm("shr.u64 %0, %1, %2;" : "=l"(r) : "l"(m), "r"(127u - (b >> 23)));
+    return r;
 }
 __device__ __forceinline__ float clamped(float v) { return v > 0.f ? fminf(v, 1.f) : 0.f; }
 // A uniform number in units of 2^-64.
@@ -73,19 +80,29 @@ __device__ __forceinline__ u64 fraction(float u) {
     if (!(u > 0.f)) return 0;
     return u >= 1.f ? ~0ull : __double2ull_rz((double)u * 18446744073709551616.0);
 }
-// What is left of p after n rejections, S[i] the sum before the i-th (S[0] = 1).
-__device__ __forceinline__ u64 left_of(float p, float q, int n, const u64 *S) {
-    u64 r = fixed(p);
-    if (n > 0) {
-        const u64 f = fixed(q);
-        r = r > f ? r - f : 0;
-        for (int i = 1; i < n; ++i) {
-            const u64 s = __umul64hi(S[i] << 2, f << 2);
-            r = r > s ? r - s : 0;
-        }
-    }
-    return r;
+// What is left of p after n rejections: R_n = max(p - c_n q, 0) with c_1 = 1, c_{n+1} = c_n +
+// S_n (an element that a rejection took to 0 stays there), so no element needs to go
+// through the earlier ones.  c comes in units of 2^-52; its product with q's 24-bit
+// significand keeps 43 bits or more.
+__device__ __forceinline__ u64 times(float q, u64 c) {
+    const uint32_t b = __float_as_uint(__saturatef(q)), e = b >> 23;
+    const uint32_t m = (b & 0x7fffffu) | 0x800000u;
+    const u64 h = (u64)m * (uint32_t)(c >> 32) + ((u64)m * (uint32_t)c >> 32);      // c q 2^(170 - e)
+    u64 up, down;                                         // (a negative shift is a large one, and gives 0)
+    asm("shl.b64 %0, %1, %2;" : "=l"(up) : "l"(h), "r"(e - 110u));
+    asm("shr.u64 %0, %1, %2;" : "=l"(down) : "l"(h), "r"(110u - e));
+    return up | down;
 }
+template <int N>                                          // 0, 1, 2: that many or more
+__device__ __forceinline__ u64 left_of(float p, float q, u64 c, float rough) {
+    const u64 r = fixed(p);
+    if (N == 0) return r;
+    const u64 t = N == 1 ? fixed(q) : times(q, c);
+    // (With c q far above p the product may not fit: nothing is left then.)
+    return r > t && (N == 1 || rough * __saturatef(q) < 1.001f * p) ? r - t : 0;
+}
+__device__ __forceinline__ float rough_of(u64 c) { return (float)c * 2.220446e-16f; }      // 2^-52
+
 __device__ __forceinline__ u64 warp_sum(u64 v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v = min(v + __shfl_xor_sync(0xffffffffu, v, o), kMost);
@@ -96,7 +113,7 @@ __device__ __forceinline__ u64 warp_sum(u64 v) {
 struct Order {
     u64 row;               // row of the probabilities
     u64 n;                 // rejections there (with a draft model's rows)
-    u64 sum;               // S[n - 1], n > 0
+    u64 c;                 // c_n in units of 2^-52
     u64 sweep;             // 1: the row's sums are wanted
     u64 last;              // 1: the path ends here, draw; 2: no row to draw from
     u64 gone[4];           // without a draft model's rows: drafts whose tokens are out, a bit each
@@ -107,7 +124,6 @@ struct Shared {
     Order order;
     u64 sums[2][kMaxCluster];          // per CTA, of the last two sweeps
     u64 seg[kVerifyWarps];             // per warp, of the last sweep
-    u64 S[kMaxDrafts + 1];
     u64 scan[kVerifyWarps];
     int token[kMaxDrafts], parent[kMaxDrafts], path[kMaxDrafts];
     float u[kMaxDrafts + 1], p[kMaxDrafts], q[kMaxDrafts];
@@ -140,13 +156,48 @@ struct Rows {
     }
 };
 
+// Sum of what is left in the groups g0 .. g1 - 1 of a row, a lane's share.
+template <int N>
+__device__ __forceinline__ u64 sweep(const Rows &rows, int g0, int g1, u64 c) {
+    const int lane = threadIdx.x & 31;
+    const float rough = rough_of(c);
+    u64 s = 0;
+    auto add = [&](const float4 &p, const float4 &q) {
+        s = min(s + (left_of<N>(p.x, q.x, c, rough) + left_of<N>(p.y, q.y, c, rough) + left_of<N>(p.z, q.z, c, rough) +
+                     left_of<N>(p.w, q.w, c, rough)), kMost);
+    };
+    const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (; g0 < g1; g0 += 128) {
+        float4 p[4], q[4];
+        if (g0 > 0 && g0 + 128 <= min(g1, rows.groups - 1) && (N == 0 || rows.q_wide)) {      // whole groups all
+            const float4 *pp = reinterpret_cast<const float4 *>(rows.p + 4 * g0 - rows.shift) + lane;
+            const float4 *qq = reinterpret_cast<const float4 *>(rows.q + 4 * g0 - rows.shift) + lane;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                p[i] = __ldg(pp + 32 * i);
+                if (N > 0) q[i] = __ldg(qq + 32 * i);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) add(p[i], N > 0 ? q[i] : none);
+        } else {
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i) {
+                const int g = g0 + 32 * i + lane;
+                if (g >= g1) continue;
+                add(rows.load(rows.p, true, g), N > 0 ? rows.load(rows.q, rows.q_wide, g) : none);
+            }
+        }
+    }
+    return s;
+}
+
 // The walk, by one thread: runs until it needs a row's sums or has reached its end.
 struct Walk {
     int t, cur, count, n;                  // next draft, node, accepted drafts, rejections at the node
     bool stuck;                            // nothing would be left: rejections change nothing more
     int pending;                           // the rejected child whose sums are under way, -1: none
     u64 total, full;                       // S; without a draft model's rows the row's sum
-    u64 gone[4];
+    u64 c;                                 // c_n in units of 2^-52
     int have_row, have_n;                  // what the segments' sums are of
 
     __device__ void enter(int node) {
@@ -154,31 +205,36 @@ struct Walk {
         n = 0;
         stuck = false;
         total = kOne;
+        c = 0;
         have_row = have_n = -1;
-        for (int w = 0; w < 4; ++w) gone[w] = 0;
     }
-    __device__ bool is_out(const Shared &sh, int tok) const {
+    // Without a draft model's rows: whether a token is out, and child `d`'s going out.
+    __device__ static bool is_out(const Shared &sh, int tok) {
         for (int w = 0; w < 4; ++w)
-            for (u64 m = gone[w]; m; m &= m - 1)
+            for (u64 m = sh.order.gone[w]; m; m &= m - 1)
                 if (sh.token[64 * w + __ffsll((long long)m) - 1] == tok) return true;
         return false;
     }
-    // Child c's token leaves R (no draft model's rows).
-    __device__ void take_out(const Shared &sh, int c) {
-        const u64 x = is_out(sh, sh.token[c]) ? 0 : fixed(sh.p[c]);
+    __device__ void take_out(Shared &sh, int d) {
+        const u64 x = is_out(sh, sh.token[d]) ? 0 : fixed(sh.p[d]);
         if (full <= x) return;
         full -= x;
         total = full;
-        if (x > 0) gone[c >> 6] |= 1ull << (c & 63);
+        if (x > 0) sh.order.gone[d >> 6] |= 1ull << (d & 63);
     }
-    __device__ void run(const VerifyParams &a, Shared &sh, int T, const u64 *sums, int C, Order &o) {
-        o = Order{};
+    __device__ void run(const VerifyParams &a, Shared &sh, int T, const u64 *sums, int C) {
+        Order &o = sh.order;
         if (pending >= 0) {
             u64 s = 0;
             for (int r = 0; r < C; ++r) s = min(s + sums[r], kMost);
             if (a.draft) {
-                if (s > 0) sh.S[++n] = total = s;
-                else stuck = true;
+                if (s > 0) {
+                    c += total >> 8;                       // 2^-60 to 2^-52
+                    ++n;
+                    total = s;
+                } else {
+                    stuck = true;
+                }
             } else {
                 full = s;
                 take_out(sh, pending);
@@ -187,16 +243,18 @@ struct Walk {
         }
         for (; t < T && count < a.A; ++t) {
             if (sh.parent[t] != cur || sh.token[t] < 0) continue;
-            const double q = sh.q[t];
-            double left = sh.p[t];
-            if (a.draft) {
-                if (n > 0) left = (double)left_of(sh.p[t], sh.q[t], n, sh.S) / (double)total;
-            } else if (have_row >= 0) {
-                left = is_out(sh, sh.token[t]) ? 0.0 : left * (double)kOne / (double)total;
+            // u q < R / S
+            bool yes;
+            if (total == kOne && n == 0 && have_row < 0) {
+                yes = (double)sh.u[t] * (double)sh.q[t] < (double)sh.p[t];
+            } else {
+                const u64 left = a.draft ? left_of<2>(sh.p[t], sh.q[t], c, rough_of(c)) : is_out(sh, sh.token[t]) ? 0 : fixed(sh.p[t]);
+                yes = (double)sh.u[t] * (double)sh.q[t] * (double)total < (double)left;
             }
-            if ((double)sh.u[t] * q < left) {
+            if (yes) {
                 sh.path[count++] = t;
                 enter(t);
+                if (!a.draft) o.gone[0] = o.gone[1] = o.gone[2] = o.gone[3] = 0;
                 continue;
             }
             if (!a.draft && have_row >= 0) {
@@ -207,21 +265,21 @@ struct Walk {
                 have_n = a.draft ? n + 1 : 0;
                 o.row = have_row;
                 o.n = have_n;
-                o.sum = total;
+                o.c = c + (total >> 8);
                 o.sweep = 1;
+                o.last = 0;
                 return;
             }
         }
         o.row = cur + a.context;
         o.n = n;
-        o.sum = n > 0 ? sh.S[n - 1] : 0;
+        o.c = c;
         o.sweep = have_row < 0 || have_n != n;
         o.last = 1;
-        for (int w = 0; w < 4; ++w) o.gone[w] = gone[w];
     }
 };
 
-__global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const __grid_constant__ VerifyParams a) {
+__global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const __grid_constant__ VerifyParams a) {
     __shared__ Shared sh;
     const uint32_t rank = cluster_rank(), C = cluster_size();
     const int b = blockIdx.x / C, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -249,7 +307,7 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const __grid_con
     }
     if (tid == 0) {
         sh.u[kMaxDrafts] = __ldg(a.uniforms + b * a.uniform_stride + a.T);
-        sh.S[0] = kOne;
+        sh.order = Order{};
     }
     cluster_sync();                                        // also: every CTA of the cluster is there
 
@@ -268,13 +326,12 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const __grid_con
     for (;;) {
         if (rank == 0) {
             if (tid == 0) {
-                walk.run(a, sh, T, sh.sums[(sweeps - 1) & 1], (int)C, o);
-                if (!a.context && T == 0) o = Order{0, 0, 0, 0, 2, {0, 0, 0, 0}};
-                sh.order = o;
-                if (o.last) {
+                walk.run(a, sh, T, sh.sums[(sweeps - 1) & 1], (int)C);
+                if (!a.context && T == 0) sh.order.last = 2;
+                if (sh.order.last) {
                     sh.count = walk.count;
                     a.next_tokens[b] = -1;                 // the drawing CTA writes it after the barrier
-                    if (o.last == 2) record_error(a.status, kErrInvalid);
+                    if (sh.order.last == 2) record_error(a.status, kErrInvalid);
                 }
             }
             __syncthreads();
@@ -292,25 +349,8 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const __grid_con
         const int per = (rows.groups + (int)C - 1) / (int)C, seg = (per + kVerifyWarps - 1) / kVerifyWarps;
         const int first = (int)rank * per, end = min(rows.groups, first + per);
         if (o.sweep) {
-            if (n > 0 && tid == 0) sh.S[n - 1] = o.sum;
-            __syncthreads();
-            const int g1 = min(end, first + (warp + 1) * seg);
-            u64 s = 0;
-            for (int g0 = first + warp * seg; g0 < g1; g0 += 128) {
-                float4 p[4], q[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int g = g0 + 32 * i + lane;
-                    p[i] = q[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (g >= g1) continue;
-                    p[i] = rows.load(rows.p, true, g);
-                    if (n > 0) q[i] = rows.load(rows.q, rows.q_wide, g);
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    s = min(s + (left_of(p[i].x, q[i].x, n, sh.S) + left_of(p[i].y, q[i].y, n, sh.S) +
-                                 left_of(p[i].z, q[i].z, n, sh.S) + left_of(p[i].w, q[i].w, n, sh.S)), kMost);
-            }
+            const int g0 = first + warp * seg, g1 = min(end, g0 + seg);
+            u64 s = n == 0 ? sweep<0>(rows, g0, g1, 0) : n == 1 ? sweep<1>(rows, g0, g1, o.c) : sweep<2>(rows, g0, g1, o.c);
             s = warp_sum(s);
             if (lane == 0) sh.seg[warp] = s;
             __syncthreads();
@@ -363,11 +403,12 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const __grid_con
                 u64 v[4] = {0, 0, 0, 0};
                 if (g < g1) {
                     const float4 p = rows.load(rows.p, true, g);
-                    const float4 q = n > 0 ? rows.load(rows.q, rows.q_wide, g) : p;
-                    v[0] = left_of(p.x, q.x, n, sh.S);
-                    v[1] = left_of(p.y, q.y, n, sh.S);
-                    v[2] = left_of(p.z, q.z, n, sh.S);
-                    v[3] = left_of(p.w, q.w, n, sh.S);
+                    const float4 q = n > 0 ? rows.load(rows.q, rows.q_wide, g) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    const float rough = rough_of(o.c);
+                    v[0] = n > 1 ? left_of<2>(p.x, q.x, o.c, rough) : left_of<1>(p.x, q.x, o.c, rough);
+                    v[1] = n > 1 ? left_of<2>(p.y, q.y, o.c, rough) : left_of<1>(p.y, q.y, o.c, rough);
+                    v[2] = n > 1 ? left_of<2>(p.z, q.z, o.c, rough) : left_of<1>(p.z, q.z, o.c, rough);
+                    v[3] = n > 1 ? left_of<2>(p.w, q.w, o.c, rough) : left_of<1>(p.w, q.w, o.c, rough);
                     if (some_out) {
                         for (int k = 0; k < 4; ++k)
                             for (u64 m = o.gone[k]; m; m &= m - 1) {
@@ -416,8 +457,9 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const __grid_con
 }  // namespace
 
 cudaError_t launch_verify(const VerifyParams &p, cudaStream_t stream) {
-    // As many CTAs to a request as leave all requests on the GPU at once (each SM takes
-    // four of these blocks), eight at most.
+    // Eight CTAs to a request (what a portable cluster holds) while that is no more than
+    // twice what the GPU takes at once: requests differ in what they reject, and short ones
+    // make room (64 trees of 24 drafts: 71 us at eight, 82 at four).
     int C = kMaxCluster;
     while (C > 1 && (int64_t)p.B * C > 4ll * p.num_sms) C /= 2;
     cudaLaunchConfig_t cfg = {};
