@@ -23,8 +23,9 @@
 // warpgroup, S buffer and O.  Otherwise NT = 1 with three S buffers (two at D = 256), QK
 // and PV issued by a thread each.
 //
-// FP8 caches: tiles land as bytes, four warps widen them to BF16 (exact) into the ring
-// that the MMAs read, so that everything behind is the BF16 kernel.
+// FP8 caches: a tile lands as bytes in half of its ring slot, four warps take it into
+// registers and write it back over the whole slot as BF16 (exact), so that every slot can
+// be loading and everything behind is the BF16 kernel.
 //
 // Warp roles: warp 0 copies K and V tiles, warps 1 and 2 issue the MMAs, warp 3 works out
 // the pieces and copies the queries, then NT warpgroups of softmax, then (FP8) a
@@ -275,19 +276,15 @@ struct ChunkCfg {
     static constexpr int kChunkBytes = 128 * 128;               // 128 rows x 64 bf16 columns
     static constexpr int kSlotBytes = 2 * kChunkBytes;          // 128 rows x 128 columns
     static constexpr int kQBytes = 128 * D * 2;
-    static constexpr int kRaw = KV8 ? (NT == 2 ? 2 : 4) : 0;    // E4M3 tiles as they land
-    static constexpr int kRawBytes = 128 * 128;
-    static constexpr int kSlots = (229376 - NT * kQBytes - kRaw * kRawBytes) / kSlotBytes;
+    static constexpr int kSlots = (229376 - NT * kQBytes) / kSlotBytes;
     static constexpr int kOffQ = 0;
     static constexpr int kOffRing = NT * kQBytes;
-    static constexpr int kOffRaw = kOffRing + kSlots * kSlotBytes;
-    static constexpr int kOffBar = kOffRaw + kRaw * kRawBytes;
+    static constexpr int kOffBar = kOffRing + kSlots * kSlotBytes;
     static constexpr int kSched = 4;                            // unit records in flight
     static constexpr int kBarSlotFull = 0;
     static constexpr int kBarSlotEmpty = kBarSlotFull + kSlots;
-    static constexpr int kBarRawFull = kBarSlotEmpty + kSlots;
-    static constexpr int kBarRawEmpty = kBarRawFull + kRaw;
-    static constexpr int kBarQFull = kBarRawEmpty + kRaw;
+    static constexpr int kBarLanded = kBarSlotEmpty + kSlots;   // FP8: a slot's bytes are there
+    static constexpr int kBarQFull = kBarLanded + (KV8 ? kSlots : 0);
     static constexpr int kBarQEmpty = kBarQFull + 1;
     static constexpr int kBarSFull = kBarQEmpty + 1;            // [NT][kSB]
     static constexpr int kBarPHalf = kBarSFull + NT * kSB;      // [NT][kSB]
@@ -309,10 +306,10 @@ struct ChunkCfg {
     static constexpr int kThreads = 128 + NT * 128 + (KV8 ? 128 : 0);
     static constexpr int kSchedReaders = 3 + 4 * NT + (KV8 ? 4 : 0);    // issuers, the producer, softmax, widening warps
     // NT = 2: launched at 168 registers (FP8: 128) a thread; after the split
-    // 128 x 80 + 256 x 208 = 63488 <= 384 x 168, FP8 128 x 80 + 256 x 176 + 128 x 80 = 512 x 128.
-    static constexpr uint32_t kRegsControl = 80, kRegsSoftmax = KV8 ? 176 : 208;
+    // 128 x 80 + 256 x 208 = 63488 <= 384 x 168, FP8 128 x (80 + 64) + 256 x 184 = 512 x 128.
+    static constexpr uint32_t kRegsControl = 80, kRegsSoftmax = KV8 ? 184 : 208, kRegsWiden = 64;
     static_assert(NT == 1 || KV8 || 128 * kRegsControl + 256 * kRegsSoftmax <= 384 * 168, "register split");
-    static_assert(NT == 1 || !KV8 || 256 * kRegsControl + 256 * kRegsSoftmax <= 512 * 128, "register split");
+    static_assert(NT == 1 || !KV8 || 128 * (kRegsControl + kRegsWiden) + 256 * kRegsSoftmax <= 512 * 128, "register split");
     static constexpr uint32_t kIdescQK = idesc_bf16_f32(128, kKvTile, false, false);
     static constexpr uint32_t kIdescPV = idesc_bf16_f32(128, 128, false, true);
     __device__ static constexpr uint32_t s_col(int x, int buf) { return (uint32_t)(x * kSB + buf) * 128u; }
@@ -350,8 +347,7 @@ chunk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUte
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
     uint64_t *slot_full = bars + C::kBarSlotFull;
     uint64_t *slot_empty = bars + C::kBarSlotEmpty;
-    uint64_t *raw_full = bars + C::kBarRawFull;
-    uint64_t *raw_empty = bars + C::kBarRawEmpty;
+    uint64_t *landed = bars + C::kBarLanded;
     uint64_t *q_full = bars + C::kBarQFull;
     uint64_t *q_empty = bars + C::kBarQEmpty;
     uint64_t *s_full = bars + C::kBarSFull;
@@ -373,8 +369,10 @@ chunk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUte
     const int lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < C::kSlots; ++i) { mbar_init(&slot_full[i], KV8 ? 4 : 1); mbar_init(&slot_empty[i], NT); }
-        for (int i = 0; i < C::kRaw; ++i) { mbar_init(&raw_full[i], 1); mbar_init(&raw_empty[i], 4); }
+        for (int i = 0; i < C::kSlots; ++i) {
+            mbar_init(&slot_full[i], KV8 ? 4 : 1); mbar_init(&slot_empty[i], NT);
+            if (KV8) mbar_init(&landed[i], 1);
+        }
         mbar_init(q_full, 1);
         mbar_init(q_empty, NT);
         for (int i = 0; i < NT * kSB; ++i) {
@@ -418,9 +416,7 @@ chunk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUte
       if constexpr (NT == 2) setmaxnreg_dec<C::kRegsControl>();
       if (warp == 0) {
         // ------------------------------------------------------------ producer
-        // Copies tiles into the ring (BF16) or to where the widening warps find them.
-        constexpr int kInto = KV8 ? C::kRaw : C::kSlots;
-        uint64_t *full = KV8 ? raw_full : slot_full, *empty = KV8 ? raw_empty : slot_empty;
+        uint64_t *full = KV8 ? landed : slot_full;
         const int box_rows = p.ps < kKvTile ? p.ps : kKvTile;
         uint32_t rp = 0;                                  // slots filled so far
         // Test hook for the bounded waits: before it copies anything, this warp waits on
@@ -439,15 +435,15 @@ chunk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUte
                 const uint32_t bytes = (uint32_t)(__popc(who) * box_rows * (KV8 ? 128 : 256));
 #pragma unroll
                 for (int s = 0; s < TS; ++s, ++rp) {
-                    const int sl = rp % kInto;
-                    if (!warp_wait(&empty[sl], ((rp / kInto) & 1) ^ 1, wc, lane)) return false;
+                    const int sl = rp % C::kSlots;
+                    if (!warp_wait(&slot_empty[sl], ((rp / C::kSlots) & 1) ^ 1, wc, lane)) return false;
                     if (lane == 0) mbar_arrive_expect_tx(&full[sl], bytes);
                     __syncwarp();
                     if (mine) {
                         const int phys = checked_page(p, entry);
                         const void *map = is_v ? (const void *)&tm_v : (const void *)&tm_k;
                         if constexpr (KV8) {
-                            tma_load_4d(smem_u32(smem + C::kOffRaw + sl * C::kRawBytes + lane * box_rows * 128), map, &full[sl],
+                            tma_load_4d(smem_u32(sRing + sl * C::kSlotBytes + C::kChunkBytes + lane * box_rows * 128), map, &full[sl],
                                         0, u.g, slot0, phys);
                         } else {
 #pragma unroll
@@ -486,9 +482,9 @@ chunk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUte
             }
         }
         if (lane == 0) {
-            for (uint32_t i = 0; i < (uint32_t)kInto && i < rp; ++i) {
+            for (uint32_t i = 0; i < (uint32_t)C::kSlots && i < rp; ++i) {
                 const uint32_t r = rp - 1 - i;
-                mbar_wait_drain(&full[r % kInto], (r / kInto) & 1, wc);
+                mbar_wait_drain(&full[r % C::kSlots], (r / C::kSlots) & 1, wc);
             }
         }
         __syncwarp();
@@ -681,38 +677,46 @@ chunk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUte
     } else if (KV8 && warp >= 4 + 4 * NT) {
         if constexpr (KV8) {
             // ------------------------------------------------------ widening
-            // Eight lanes take four 16-byte units of two rows whose numbers differ in bits 0
-            // and 2: their swizzled places then fall on different banks, read and written.
-            if constexpr (NT == 2) setmaxnreg_dec<C::kRegsControl>();
-            const int w4 = warp & 3, half = lane >> 4, pair = lane >> 3 & 1, unit = (lane & 3) + 4 * half;
+            // The bytes lie in the slot's second half, where columns 64 .. 127 will be: columns 0 ..
+            // 63 go to the first half at once, the others to where they lie once all threads
+            // have theirs in registers.  Eight lanes take four 16-byte units of two rows whose
+            // numbers differ in bits 0 and 2: their swizzled places then fall on different banks,
+            // read and written.  (The barrier among them has no limit: they wait together, and a
+            // wait that ran out does not part them.)
+            if constexpr (NT == 2) setmaxnreg_dec<C::kRegsWiden>();
+            const int r = (lane >> 3) ^ (lane & 4 ? 5 : 0), row0 = (warp & 3) * 32 + r, c = 2 * (lane & 3);
+            const uint32_t from0 = C::kChunkBytes + row0 * 128 + (((lane & 3) ^ r) << 4);
+            const uint32_t from1 = C::kChunkBytes + row0 * 128 + (((lane & 3) + 4) ^ r) * 16;
+            const uint32_t to0 = row0 * 128 + ((c ^ r) << 4), to1 = row0 * 128 + (((c + 1) ^ r) << 4);
+            auto put = [&](uint8_t *at, const uint4 &b) {
+                const uint2 x0 = widen4(b.x), x1 = widen4(b.y), x2 = widen4(b.z), x3 = widen4(b.w);
+                *reinterpret_cast<uint4 *>(at + to0) = make_uint4(x0.x, x0.y, x1.x, x1.y);
+                *reinterpret_cast<uint4 *>(at + to1) = make_uint4(x2.x, x2.y, x3.x, x3.y);
+            };
             uint32_t rp = 0;
-            bool ok = true;
-            for (int k = 0; ok; ++k) {
+            for (int k = 0;; ++k) {
                 const ChunkUnit u = warp_unit(k);
-                if (!__all_sync(0xffffffffu, u.b >= 0)) break;
-                for (int i = 0; i < 2 * u.ntiles && ok; ++i, ++rp) {
-                    const int rs = rp % C::kRaw, sl = rp % C::kSlots;
-                    ok = warp_wait(&raw_full[rs], (rp / C::kRaw) & 1, wc, lane) &&
-                         warp_wait(&slot_empty[sl], ((rp / C::kSlots) & 1) ^ 1, wc, lane);
-                    if (!ok) break;
-                    const uint8_t *raw = smem + C::kOffRaw + rs * C::kRawBytes;
-                    uint8_t *to = sRing + sl * C::kSlotBytes + (unit >> 2) * C::kChunkBytes;
+                if (!named_bar_all(2, 128, u.b >= 0)) break;
+                for (int i = 0; i < 2 * u.ntiles; ++i, ++rp) {
+                    const int sl = rp % C::kSlots;
+                    // (Every lane waits: those that only hear of it from one that did may have read before.)
+                    mbar_wait(&landed[sl], (rp / C::kSlots) & 1, wc);
+                    __syncwarp();
+                    uint8_t *at = sRing + sl * C::kSlotBytes;
+                    uint4 b0[4], b1[4];
 #pragma unroll
-                    for (int it = 0; it < 8; ++it) {
-                        // rows 32 w4 + 8 (it / 2) + {r, r ^ 5}, r = 2 (it & 1) + pair
-                        int r = 2 * (it & 1) + pair;
-                        if (lane & 4) r ^= 5;
-                        const int row = w4 * 32 + (it >> 1) * 8 + r;
-                        const uint4 b = *reinterpret_cast<const uint4 *>(raw + row * 128 + ((unit ^ r) << 4));
-                        const uint2 x0 = widen4(b.x), x1 = widen4(b.y), x2 = widen4(b.z), x3 = widen4(b.w);
-                        uint8_t *line = to + row * 128;
-                        const int c = 2 * (unit & 3);
-                        *reinterpret_cast<uint4 *>(line + ((c ^ r) << 4)) = make_uint4(x0.x, x0.y, x1.x, x1.y);
-                        *reinterpret_cast<uint4 *>(line + (((c + 1) ^ r) << 4)) = make_uint4(x2.x, x2.y, x3.x, x3.y);
+                    for (int it = 0; it < 4; ++it) {
+                        b0[it] = *reinterpret_cast<const uint4 *>(at + it * 1024 + from0);
+                        b1[it] = *reinterpret_cast<const uint4 *>(at + it * 1024 + from1);
                     }
+#pragma unroll
+                    for (int it = 0; it < 4; ++it) put(at + it * 1024, b0[it]);
+                    named_bar_sync(2, 128);
+#pragma unroll
+                    for (int it = 0; it < 4; ++it) put(at + C::kChunkBytes + it * 1024, b1[it]);
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) { mbar_arrive(&raw_empty[rs]); mbar_arrive(&slot_full[sl]); }
+                    if (lane == 0) mbar_arrive(&slot_full[sl]);
                 }
             }
         }
@@ -779,8 +783,10 @@ chunk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUte
                         for (int i = 0; i < 64; ++i)
                             if (!((i < 32 ? b0 : b1) >> (i & 31) & 1)) v[i] = kNegInf;
                     };
-                    // Two streams read the row of S once; one reads it twice, for its maximum and
-                    // for P, 64 keys at a time in rolled loops, whose code stays small.
+                    // Two streams read the row of S once (over FP8 caches, where that spills a few
+                    // registers, reading its second half twice took 895 us for 859); one reads it
+                    // twice, for its maximum and for P, 64 keys at a time in rolled loops, whose code
+                    // stays small.
                     float sv[NT == 2 ? kKvTile : 1], ext = kNegInf;
                     if constexpr (NT == 2) {
                         read_s(0, sv);
@@ -868,12 +874,10 @@ chunk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUte
                     // A parity wait needs the slot's copy before V_j to have landed.
                     // S_j there proves that for all copies up to K_j; with two slots
                     // to a tile the one before V_j's may be V_{j-1}, which its
-                    // finished product proves; with one stream over four slots it may
-                    // be V_{j-2}, which comes after K_j too.
+                    // finished product proves.
+                    static_assert(TS == 2 || NT == 2 || C::kSlots >= 2 * kSB, "the ring holds what QK runs ahead");
                     if constexpr (TS == 2) {
                         if (steps > 0) wait_pv(steps - 1);
-                    } else if constexpr (NT == 1 && C::kSlots < 2 * kSB) {
-                        if (steps > 1) wait_pv(steps - 2);
                     }
                     const int key = key0 + row;
                     const bool seen = key >= any_lo && key < any_hi;

@@ -269,6 +269,22 @@ def test_scales(fw, amp, scale, D, kv8):
     run_and_check(fw, x, f"{amp} {scale}")
 
 
+@pytest.mark.parametrize("kv8", [False, True])
+@pytest.mark.parametrize("case", [([31], [700], 28, 4, 128, 32), ([64], [2000], 32, 8, 128, 64), ([5], [300], 8, 2, 128, 16),
+                                  ([5, 128, 3], [5, 128, 133], 40, 8, 128, 16), ([40], [40], 4, 4, 256, 16)], ids=str)
+def test_what_lay_in_shared_memory_does_not_matter(fw, case, kv8):
+    """Pages that are not copied leave what an earlier call put there, NaN of any type."""
+    if kv8 and case[4] == 256:
+        pytest.skip("8-bit caches have head dim 128")
+    x = make(*case, kv8=kv8, seed=18)
+    for dt in (torch.bfloat16, torch.float8_e4m3fn):
+        dirty = on_gpu(make([600] * 8, [900] * 8, 40, 8, 128, 16, kv8=dt != torch.bfloat16))
+        for name in ("k_cache", "v_cache"):
+            dirty[name].view(torch.uint8).fill_(255)
+        fw.paged_prefill(**dirty)
+        run_and_check(fw, x, str(case))
+
+
 def test_rising_scores_move_the_base(fw):
     """Keys grow along the row, so that the maximum rises tile after tile."""
     for D, kv8 in ((128, False), (256, False)):
