@@ -1744,7 +1744,7 @@ fw_status_t fw_paged_prefill(const fw_tensor_t *q, const fw_tensor_t *k_cache, c
     // Two row tiles a unit where the requests bring more than one on average.
     p.row_tiles = D == 128 && (p.head_chunks > 1 || N * p.G > 128 * B) ? 2 : 1;
     p.min_span = fw::kChunkMinSpan;
-    p.piece_cost = kv8 || p.row_tiles > 1 ? fw::kChunkPieceCost : fw::kChunkPieceCostOne;
+    p.piece_cost = kv8 ? fw::kChunkPieceCostFp8 : p.row_tiles > 1 ? fw::kChunkPieceCost : fw::kChunkPieceCostOne;
     std::lock_guard<std::mutex> lk(g_mu);
     DeviceState *d = nullptr;
     if (fw_status_t s = device_state(&d)) return s;
