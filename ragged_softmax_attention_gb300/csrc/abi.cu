@@ -1742,16 +1742,20 @@ fw_status_t fw_paged_prefill(const fw_tensor_t *q, const fw_tensor_t *k_cache, c
     p.tile_tokens = p.G <= 128 ? (int)(128 / p.G < N ? 128 / p.G : N) : 1;
     p.head_chunks = p.G <= 128 ? 1 : (p.G + 127) / 128;
     // Two row tiles a unit where the requests bring more than one on average.
-    p.row_tiles = D == 128 && (p.head_chunks > 1 || N * p.G > 128 * B) ? 2 : 1;
+    p.row_tiles = p.head_chunks > 1 || N * p.G > 128 * B ? 2 : 1;
     p.min_span = fw::kChunkMinSpan;
-    p.piece_cost = kv8 ? fw::kChunkPieceCostFp8 : p.row_tiles > 1 ? fw::kChunkPieceCost : fw::kChunkPieceCostOne;
     std::lock_guard<std::mutex> lk(g_mu);
     DeviceState *d = nullptr;
     if (fw_status_t s = device_state(&d)) return s;
     p.grid = d->num_sms;
     if (g_opt_max_ctas > 0 && p.grid > g_opt_max_ctas) p.grid = (int)g_opt_max_ctas;
-    // As in the decode: the KV heads ride on the CTA index when the grid holds whole groups of them.
-    p.ride = p.Hkv > 1 && p.grid % p.Hkv == 0;
+    // Head dim 256: two row tiles take a pair of CTAs.
+    if (D == 256 && p.grid < 2) p.row_tiles = 1;
+    const bool pairs = D == 256 && p.row_tiles == 2;
+    p.workers = pairs ? p.grid / 2 : p.grid;
+    p.piece_cost = kv8 ? fw::kChunkPieceCostFp8 : p.row_tiles > 1 ? fw::kChunkPieceCost : fw::kChunkPieceCostOne;
+    // As in the decode: the KV heads ride on the worker's number when there are whole groups of them.
+    p.ride = p.Hkv > 1 && p.workers % p.Hkv == 0;
     const size_t need = fw::chunk_workspace_bytes(p.D, d->num_sms);
     void *ws = workspace;
     if (ws) {
@@ -1785,10 +1789,12 @@ fw_status_t fw_paged_prefill(const fw_tensor_t *q, const fw_tensor_t *k_cache, c
         const uint32_t box[3] = {64, (uint32_t)(p.G < 128 ? p.G : 128), (uint32_t)p.tile_tokens};
         if (fw_status_t s = encode_bf16(&tq, q->data, 3, dims, strides, box, "q")) return s;
         const uint64_t esz = p.kv8 ? 1 : 2;
-        const uint32_t kbox[4] = {p.kv8 ? 128u : 64u, 1, (uint32_t)(p.ps < fw::kKvTile ? p.ps : fw::kKvTile), 1};
         const fw_tensor_t *caches[2] = {k_cache, v_cache};
         for (int i = 0; i < 2; ++i) {
             const fw_tensor_t *c = caches[i];
+            // (Each CTA of a pair copies half the keys of a K tile.)
+            const int64_t most = pairs && i == 0 ? fw::kKvTile / 2 : fw::kKvTile;
+            const uint32_t kbox[4] = {p.kv8 ? 128u : 64u, 1, (uint32_t)(p.ps < most ? p.ps : most), 1};
             const uint64_t cd[4] = {(uint64_t)p.D, (uint64_t)p.Hkv, (uint64_t)p.ps, (uint64_t)p.num_pages};
             const uint64_t cs[3] = {(uint64_t)c->stride[2] * esz, (uint64_t)c->stride[1] * esz, (uint64_t)c->stride[0] * esz};
             // As in the decode: a 128-byte FP8 row's neighbour is another head's,

@@ -20,8 +20,9 @@
 //
 // D = 128 with more than a row tile a request: NT = 2, two row tiles take turns on the
 // tensor core over shared K and V tiles, each with its own MMA-issuing thread, softmax
-// warpgroup, S buffer and O.  Otherwise NT = 1 with three S buffers (two at D = 256), QK
-// and PV issued by a thread each.
+// warpgroup, S buffer and O.  D = 256 with more than a row tile runs on pairs of CTAs
+// (another file).  Otherwise NT = 1 with three S buffers (two at D = 256), QK and PV issued
+// by a thread each.
 //
 // FP8 caches: a tile lands as bytes in half of its ring slot, four warps take it into
 // registers and write it back over the whole slot as BF16 (exact), so that every slot can
@@ -32,239 +33,12 @@
 // warpgroup that widens.
 #include <cuda_fp8.h>
 
-#include "tree_common.cuh"
+#include "chunk_common.cuh"
 
 namespace fw {
 namespace {
 
-using namespace tree;
-
-// One piece: a unit's key tiles inside one CTA range.  64 bytes.
-struct alignas(16) ChunkUnit {
-    int b;             // request, -1 ends the CTA's work
-    int g;             // KV head
-    int rt0, nrt;      // first row tile and how many
-    int n, d, q0;      // keys and new tokens of the request, its first packed row
-    int tile0, ntiles; // key tiles
-    int part;          // partial slot, -1: the whole unit, written to the outputs
-    int lo;            // first key that a row sees: pages wholly before it are not copied
-    int pad_[5];
-};
-static_assert(sizeof(ChunkUnit) == 64, "a unit record fills one 64-byte slot");
-
-// ------------------------------------------------------------------ the plan
-
-// A request's units: `steps` runs of tokens (the first `v0` of which see nothing) times
-// `reps` (KV heads, and parts of a token's heads).  All weights in keys.
-struct ChunkRow {
-    int n, d, q0, steps, v0, reps;
-};
-template <int NT>
-__device__ __forceinline__ int step_tokens(const ChunkParams &p) { return p.head_chunks > 1 ? 1 : NT * p.tile_tokens; }
-
-template <int NT>
-__device__ __forceinline__ ChunkRow chunk_row(const ChunkParams &p, int b) {
-    ChunkRow r;
-    r.q0 = __ldg(p.cu + b);
-    const int end = __ldg(p.cu + b + 1);
-    const bool ok = r.q0 >= 0 && end >= r.q0 && end <= p.total_q;
-    if (!ok && blockIdx.x == 0) record_error(p.status, kErrInvalid);
-    r.d = ok ? end - r.q0 : 0;
-    r.n = min(max(__ldg(p.seq_lens + b), 0), p.max_pages * p.ps);
-    const int s = step_tokens<NT>(p);
-    r.steps = ceil_div_i(r.d, s);
-    r.v0 = r.n == 0 ? r.steps : p.causal && r.d > r.n ? (r.d - r.n) / s : 0;
-    r.reps = (p.head_chunks > 1 ? ceil_div_i(p.head_chunks, NT) : 1) * (p.ride ? 1 : p.Hkv);
-    return r;
-}
-// Weight of step v, and of steps v0 .. v - 1.
-template <int NT>
-__device__ __forceinline__ long long step_weight(const ChunkParams &p, const ChunkRow &r, int v) {
-    const long long s = step_tokens<NT>(p), base = r.n - r.d;
-    const long long hi = p.causal ? base + (v + 1) * s : r.n;
-    const long long lo = p.window < 0 ? 0 : max(0ll, base - p.window + v * s);
-    return p.piece_cost + 128 + hi - lo;
-}
-template <int NT>
-__device__ __forceinline__ long long steps_weight(const ChunkParams &p, const ChunkRow &r, int v) {
-    const long long s = step_tokens<NT>(p), base = r.n - r.d, m = v - r.v0;
-    auto sum = [](long long a, long long e) { return (e - a) * (a + e - 1) / 2; };      // a + .. + e - 1
-    long long w = m * (p.piece_cost + 128);
-    w += p.causal ? m * (base + s) + s * sum(r.v0, v) : m * r.n;
-    if (p.window >= 0) {
-        const long long z = base - p.window;                     // lo = z + i s where that is above zero
-        const long long first = max((long long)r.v0, z >= 0 ? 0 : -z / s + 1);
-        if (first < v) w -= (v - first) * z + s * sum(first, v);
-    }
-    return w;
-}
-
-// plan[0] = weight in all, plan[1], plan[2] = start and number of the request that holds
-// the CTA's first key, plan[3] = span.  Ends with every thread past a barrier but plan not
-// yet published.
-template <int NT>
-__device__ __forceinline__ void chunk_plan(const ChunkParams &p, long long *plan, long long *scan) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nthreads = blockDim.x;
-    const int per = (p.B + nthreads - 1) / nthreads;
-    auto weight = [&](int b) -> long long {
-        const ChunkRow r = chunk_row<NT>(p, b);
-        return r.v0 < r.steps ? r.reps * steps_weight<NT>(p, r, r.steps) : 0;
-    };
-    long long mine = 0;
-    const int b0 = threadIdx.x * per;
-    for (int i = 0; i < per && b0 + i < p.B; ++i) mine += weight(b0 + i);
-    long long incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
-    }
-    if (lane == 31) scan[warp] = incl;
-    __syncthreads();
-    long long before = incl - mine, total = 0;
-    for (int w = 0; w < nthreads / 32; ++w) {
-        if (w < warp) before += scan[w];
-        total += scan[w];
-    }
-    const int nranges = p.ride ? (int)gridDim.x / p.Hkv : (int)gridDim.x;
-    const long long span = max((long long)p.min_span, (total + nranges - 1) / nranges);
-    const long long first = span * (p.ride ? (int)blockIdx.x / p.Hkv : (int)blockIdx.x);
-    if (mine > 0 && first >= before && first < before + mine) {
-        int b = b0;
-        for (long long s; first >= before + (s = weight(b)); ++b) before += s;
-        plan[1] = before;
-        plan[2] = b;
-    }
-    if (threadIdx.x == 0) { plan[0] = total; plan[3] = span; }
-}
-
-// Walks the pieces of this CTA's range (one warp, all lanes alike).  A border at weight
-// x of a unit cuts it before tile (x - cost) / 128, for the ranges on both sides alike;
-// a piece without tiles is none.
-template <int NT>
-struct ChunkWalk {
-    long long span, pos, end, start;                  // the range; start of the unit
-    int range, b, rep, v;
-    ChunkRow r;
-    ChunkCut cut;
-
-    __device__ int tile_at(const ChunkParams &p, long long x, int tiles) const {
-        x -= p.piece_cost;
-        return x <= 0 ? 0 : (int)min((long long)tiles, x >> 7);
-    }
-    __device__ void init(const ChunkParams &p, const long long *plan) {
-        span = plan[3];
-        range = p.ride ? (int)blockIdx.x / p.Hkv : (int)blockIdx.x;
-        pos = span * range;
-        end = min(plan[0], pos + span);
-        cut = ChunkCut{};
-        start = end;
-        if (pos >= end) return;
-        b = (int)plan[2];
-        r = chunk_row<NT>(p, b);
-        const long long all = steps_weight<NT>(p, r, r.steps);
-        rep = (int)((pos - plan[1]) / all);
-        const long long off = pos - plan[1] - rep * all;
-        int lo = r.v0, hi = r.steps - 1;              // the last step that starts at or before off
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (steps_weight<NT>(p, r, mid) <= off) lo = mid; else hi = mid - 1;
-        }
-        v = lo;
-        start = plan[1] + rep * all + steps_weight<NT>(p, r, v);
-    }
-    __device__ void next(const ChunkParams &p, ChunkUnit &u) {   // u.b = -1 at the end
-        u.b = -1;
-        const int s = step_tokens<NT>(p);
-        while (start < end) {
-            if (v >= r.steps) {                       // the next KV head, the next request
-                v = r.v0;
-                if (v >= r.steps || ++rep >= r.reps) {
-                    if (++b >= p.B) return;           // (weight is left, so there is one)
-                    r = chunk_row<NT>(p, b);
-                    rep = 0;
-                    v = r.v0;
-                }
-                continue;
-            }
-            const long long w = step_weight<NT>(p, r, v);
-            const int t0 = v * s, t1 = min(r.d, t0 + s) - 1;
-            const int lo = p.window < 0 ? 0 : (int)max(0ll, (long long)r.n - r.d + t0 - p.window);
-            const int hi = p.causal ? r.n - r.d + t1 + 1 : r.n;
-            const int tile0 = lo / kKvTile, tiles = ceil_div_i(hi, kKvTile) - tile0;
-            const int a = tile_at(p, pos - start, tiles);
-            const int e = end >= start + w ? tiles : tile_at(p, end - start, tiles);
-            const long long at = start;
-            const int step = v;
-            start += w;
-            ++v;
-            if (a >= e) continue;
-            const int parts = p.head_chunks > 1 ? ceil_div_i(p.head_chunks, NT) : 1;
-            const int g = rep / parts, part = rep - g * parts;
-            u.b = b;
-            u.g = p.ride ? (int)blockIdx.x % p.Hkv : g;
-            u.rt0 = p.head_chunks > 1 ? step * p.head_chunks + part * NT : step * NT;
-            u.nrt = min(NT, p.head_chunks > 1 ? p.head_chunks - part * NT : ceil_div_i(r.d, p.tile_tokens) - u.rt0);
-            u.n = r.n;
-            u.d = r.d;
-            u.q0 = r.q0;
-            u.tile0 = tile0 + a;
-            u.ntiles = e - a;
-            u.lo = lo;
-            u.part = -1;
-            if (a > 0) {
-                u.part = 2 * blockIdx.x;
-            } else if (e < tiles) {
-                u.part = 2 * blockIdx.x + 1;
-                const long long last = min((at + p.piece_cost + 128ll * tiles + span - 1) / span, (at + w + span - 1) / span);
-                cut.count = (int)last - range;
-                cut.g = u.g; cut.rt0 = u.rt0; cut.nrt = u.nrt; cut.d = r.d; cut.q0 = r.q0;
-            }
-            return;
-        }
-    }
-};
-
-// The (token, head) of row r of row tile rt; false for padding.
-__device__ __forceinline__ bool chunk_tile_row(const ChunkParams &p, int rt, int g, int d, int r, int &t, int &h) {
-    if (p.head_chunks > 1) {
-        t = rt / p.head_chunks;
-        const int hh = (rt - t * p.head_chunks) * 128 + r;
-        h = g * p.G + hh;
-        return hh < p.G && t < d;
-    }
-    const int tt = r / p.G;
-    t = rt * p.tile_tokens + tt;
-    h = g * p.G + (r - tt * p.G);
-    return tt < p.tile_tokens && t < d;
-}
-
-// First and last key that token t sees, as [lo, hi).
-__device__ __forceinline__ int key_lo(const ChunkParams &p, const ChunkUnit &u, int t) {
-    return p.window < 0 ? 0 : (int)max(0ll, (long long)u.n - u.d + t - p.window);
-}
-__device__ __forceinline__ int key_hi(const ChunkParams &p, const ChunkUnit &u, int t) {
-    return p.causal ? max(0, u.n - u.d + t + 1) : u.n;
-}
-// The bits lo .. hi - 1 of 32 keys from `key` on.
-__device__ __forceinline__ uint32_t range_bits(int lo, int hi, int key) {
-    lo = max(lo - key, 0);
-    hi = min(hi - key, 32);
-    if (lo >= hi) return 0u;
-    return (0xffffffffu >> (32 - (hi - lo))) << lo;
-}
-
-// Values that are not finite, in tiles that some row of the unit does not see whole: they
-// must not meet the zero weights of rows that do not see them.  They are cleared before
-// the products, and the rows that see them come out as NaN.  Such tiles are few, for a
-// unit's 256 tokens at most three at either end: bits of a tile's keys in the words of unit
-// k % kBadUnits (a writer is at most four units ahead of a reader), behind a word that
-// says whether there are any.
-constexpr int kBadUnitWords = 4 + 8 * 4;
-__device__ __forceinline__ uint32_t *bad_words(uint32_t *marks, int tile, int any_lo, int all_hi) {
-    const int upper = tile - all_hi / kKvTile;            // >= 0: reaches past what the first row sees
-    return marks + 4 + 4 * ((upper >= 0 ? 4 + upper : tile - any_lo / kKvTile) & 7);
-}
+using namespace chunk;
 
 template <int D_, int NT_, bool KV8_>
 struct ChunkCfg {
@@ -390,7 +164,7 @@ chunk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUte
     }
     if (warp == 1) { tmem_alloc(tmem_slot, 512); tmem_relinquish(); }
     pdl_launch_dependents();                       // the merge may take its place; it waits for this grid
-    chunk_plan<NT>(p, plan, scan);
+    chunk_plan<NT>(p, blockIdx.x, plan, scan);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -643,7 +417,7 @@ chunk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUte
       } else if (warp == 3) {
         // ----------------------------------------------- the pieces; queries
         ChunkWalk<NT> walk;
-        walk.init(p, plan);
+        walk.init(p, blockIdx.x, plan);
         for (int k = 0;; ++k) {
             ChunkUnit u;
             walk.next(p, u);
@@ -1076,7 +850,7 @@ cudaError_t launch_t(const ChunkParams &p, const CUtensorMap &tq, const CUtensor
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     ++*launches;
-    e = launch_after_previous(chunk_merge_kernel<D, NT>, dim3(NT * 4, p.grid), dim3(kMergeThreads), 0, stream, p);
+    e = launch_chunk_merge(p, stream);
     if (e != cudaSuccess) return e;
     ++*launches;
     return cudaSuccess;
@@ -1084,6 +858,15 @@ cudaError_t launch_t(const ChunkParams &p, const CUtensorMap &tq, const CUtensor
 
 }  // namespace
 
+cudaError_t launch_chunk_merge(const ChunkParams &p, cudaStream_t stream) {
+    const dim3 grid(p.row_tiles * 4, p.workers), block(kMergeThreads);
+    if (p.D == 256 && p.row_tiles == 2) return launch_after_previous(chunk_merge_kernel<256, 2>, grid, block, 0, stream, p);
+    if (p.D == 256) return launch_after_previous(chunk_merge_kernel<256, 1>, grid, block, 0, stream, p);
+    if (p.row_tiles == 2) return launch_after_previous(chunk_merge_kernel<128, 2>, grid, block, 0, stream, p);
+    return launch_after_previous(chunk_merge_kernel<128, 1>, grid, block, 0, stream, p);
+}
+
+// (A pair of CTAs has two pieces of two row tiles where two CTAs have four of one.)
 size_t chunk_workspace_bytes(int head_dim, int grid) {
     const int rows = head_dim == 128 ? 256 : 128;
     return (size_t)grid * (2 * (size_t)rows * (head_dim * 4 + 8) + sizeof(ChunkCut));
@@ -1102,6 +885,7 @@ void chunk_place_workspace(ChunkParams *p, void *ws) {
 cudaError_t launch_chunk(const ChunkParams &p, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                          cudaStream_t stream, int *launches) {
     *launches = 0;
+    if (p.D == 256 && p.row_tiles == 2) return launch_chunk_pair(p, tq, tk, tv, stream, launches);
     if (p.D == 256) return launch_t<256, 1, false>(p, tq, tk, tv, stream, launches);
     if (p.kv8)
         return p.row_tiles == 2 ? launch_t<128, 2, true>(p, tq, tk, tv, stream, launches)

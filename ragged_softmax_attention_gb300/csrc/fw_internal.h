@@ -256,11 +256,12 @@ struct ChunkParams {
     int head_chunks;                           // > 1: 128-head row tiles of one token (G > 128)
     int row_tiles;                             // row tiles of a unit, 1 or 2
     int grid;                                  // CTAs
-    int ride;                                  // 1: the KV heads ride on the CTA index
+    int workers;                               // CTAs, or pairs of them, that take a range each
+    int ride;                                  // 1: the KV heads ride on the worker's number
     int min_span, piece_cost;                  // in keys: least a range holds; what a unit's start weighs
-    float *part_o;                             // [2 * grid][row tiles of a unit * 128][D] unnormalised pieces
+    float *part_o;                             // [2 * workers][row tiles of a unit * 128][D] unnormalised pieces
     float2 *part_ml;                           // base (log2) and row sum of each of their rows
-    ChunkCut *cuts;                            // [grid]
+    ChunkCut *cuts;                            // [workers]
     int test_stall;                            // test hook: the producer first waits on a barrier nothing completes
     uint64_t timeout_ns;
     int *status;
@@ -349,6 +350,9 @@ cudaError_t launch_page_tables(const PageTableParams &p, cudaStream_t stream, in
 cudaError_t launch_kv_commit(const CommitParams &p, cudaStream_t stream);
 cudaError_t launch_chunk(const ChunkParams &p, const CUtensorMap &tm_q, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
                          cudaStream_t stream, int *launches);
+cudaError_t launch_chunk_pair(const ChunkParams &p, const CUtensorMap &tm_q, const CUtensorMap &tm_k,
+                              const CUtensorMap &tm_v, cudaStream_t stream, int *launches);
+cudaError_t launch_chunk_merge(const ChunkParams &p, cudaStream_t stream);
 size_t chunk_workspace_bytes(int head_dim, int grid);
 void chunk_place_workspace(ChunkParams *p, void *ws);
 cudaError_t launch_verify(const VerifyParams &p, cudaStream_t stream);
