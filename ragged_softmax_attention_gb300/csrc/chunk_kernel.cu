@@ -736,18 +736,22 @@ chunk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUte
 // opened the following ranges.  Block (chunk, c) takes 32 rows of that unit, a lane a row
 // and a warp an equal share of the columns, and turns the result round in shared memory.
 // The rows of units that see no key are written here too.
-constexpr int kMergeThreads = 128;
+// More threads have more pieces' loads on their way; two row tiles of 128 columns, whose
+// blocks are the most, fit the GPU better in blocks of four warps (as the tree's).
+template <int D, int NT>
+constexpr int kMergeThreads = D == 128 && NT == 2 ? 128 : 256;
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid_constant__ ChunkParams p) {
-    constexpr int kUnits = D / 4 / (kMergeThreads / 32);   // 16-byte FP32 units of a warp's columns
+__global__ void __launch_bounds__(kMergeThreads<D, NT>) chunk_merge_kernel(const __grid_constant__ ChunkParams p) {
+    constexpr int kThreads = kMergeThreads<D, NT>;
+    constexpr int kUnits = D / 4 / (kThreads / 32);   // 16-byte FP32 units of a warp's columns
     constexpr int kPieces = 16 / kUnits;
     __shared__ uint4 stage[32][D / 8 + 1];           // BF16 rows
     __shared__ long long offset[32];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     // Zeros and -inf, a warp to a request; these wait for nothing.
-    const int nwarps = gridDim.x * gridDim.y * (kMergeThreads / 32);
-    for (int b = (blockIdx.y * gridDim.x + blockIdx.x) * (kMergeThreads / 32) + warp; b < p.B; b += nwarps) {
+    const int nwarps = gridDim.x * gridDim.y * (kThreads / 32);
+    for (int b = (blockIdx.y * gridDim.x + blockIdx.x) * (kThreads / 32) + warp; b < p.B; b += nwarps) {
         const ChunkRow r = chunk_row<NT>(p, b);
         const int64_t empty = min((int64_t)r.d, (int64_t)r.v0 * step_tokens<NT>(p));
         for (int64_t i = lane; i < empty * p.Hq * (D / 8); i += 32) {
@@ -826,7 +830,7 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid
                 l != 0.f ? (m + log2f(l)) * 0.69314718055994531f : kNegInf;
     }
     __syncthreads();
-    for (int i = tid; i < 32 * (D / 8); i += kMergeThreads) {
+    for (int i = tid; i < 32 * (D / 8); i += kThreads) {
         const int r = i / (D / 8), c = i % (D / 8);
         if (offset[r] >= 0)
             reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(p.out) + offset[r])[c] = stage[r][c];
@@ -859,11 +863,12 @@ cudaError_t launch_t(const ChunkParams &p, const CUtensorMap &tq, const CUtensor
 }  // namespace
 
 cudaError_t launch_chunk_merge(const ChunkParams &p, cudaStream_t stream) {
-    const dim3 grid(p.row_tiles * 4, p.workers), block(kMergeThreads);
-    if (p.D == 256 && p.row_tiles == 2) return launch_after_previous(chunk_merge_kernel<256, 2>, grid, block, 0, stream, p);
-    if (p.D == 256) return launch_after_previous(chunk_merge_kernel<256, 1>, grid, block, 0, stream, p);
-    if (p.row_tiles == 2) return launch_after_previous(chunk_merge_kernel<128, 2>, grid, block, 0, stream, p);
-    return launch_after_previous(chunk_merge_kernel<128, 1>, grid, block, 0, stream, p);
+    const dim3 grid(p.row_tiles * 4, p.workers);
+    auto launch = [&](auto kernel, int threads) { return launch_after_previous(kernel, grid, dim3(threads), 0, stream, p); };
+    if (p.D == 256 && p.row_tiles == 2) return launch(chunk_merge_kernel<256, 2>, kMergeThreads<256, 2>);
+    if (p.D == 256) return launch(chunk_merge_kernel<256, 1>, kMergeThreads<256, 1>);
+    if (p.row_tiles == 2) return launch(chunk_merge_kernel<128, 2>, kMergeThreads<128, 2>);
+    return launch(chunk_merge_kernel<128, 1>, kMergeThreads<128, 1>);
 }
 
 // (A pair of CTAs has two pieces of two row tiles where two CTAs have four of one.)

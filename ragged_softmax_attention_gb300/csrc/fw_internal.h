@@ -57,11 +57,11 @@ constexpr int kTreePieceCost = 5;
 // Chunk attention: the same, in keys; every unit weighs a tile more than its keys, for
 // the tiles that its first and last key share.  Two row tiles: 16 prompts of 300 .. 5,000
 // tokens 861 us at 0, 828 at 256, 832 at 384, 866 at 640; a mixed batch 349, 329, 330, 326;
-// over FP8 caches, whose steps are longer, 934, 893, 879, 868.
+// over FP8 caches, whose steps are longer, 934, 893, 879, 868; pairs of CTAs 163, 158, 154, 154.
 constexpr int kChunkMinSpan = 256;
 constexpr int kChunkPieceCostOne = 128;
 constexpr int kChunkPieceCost = 384;
-constexpr int kChunkPieceCostFp8 = 640;
+constexpr int kChunkPieceCostLong = 640;
 constexpr int kMaxTableRows = 8192;   // page tables: requests whose sums fit a block's shared memory
 constexpr int kLatentRows = 64;       // latent-head decode: query heads per CTA (MMA N of one CTA)
 constexpr int kLatentPairRows = 128;  // latent-head decode on CTA pairs: query heads per pair
