@@ -477,14 +477,16 @@ chunk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUte
                     mbar_wait(&landed[sl], (rp / C::kSlots) & 1, wc);
                     __syncwarp();
                     uint8_t *at = sRing + sl * C::kSlotBytes;
-                    uint4 b0[4], b1[4];
+                    uint4 b1[4];
 #pragma unroll
-                    for (int it = 0; it < 4; ++it) {
-                        b0[it] = *reinterpret_cast<const uint4 *>(at + it * 1024 + from0);
-                        b1[it] = *reinterpret_cast<const uint4 *>(at + it * 1024 + from1);
+                    for (int it = 0; it < 4; ++it) b1[it] = *reinterpret_cast<const uint4 *>(at + it * 1024 + from1);
+#pragma unroll
+                    for (int it = 0; it < 4; it += 2) {
+                        const uint4 b0 = *reinterpret_cast<const uint4 *>(at + it * 1024 + from0);
+                        const uint4 b2 = *reinterpret_cast<const uint4 *>(at + it * 1024 + 1024 + from0);
+                        put(at + it * 1024, b0);
+                        put(at + it * 1024 + 1024, b2);
                     }
-#pragma unroll
-                    for (int it = 0; it < 4; ++it) put(at + it * 1024, b0[it]);
                     named_bar_sync(2, 128);
 #pragma unroll
                     for (int it = 0; it < 4; ++it) put(at + C::kChunkBytes + it * 1024, b1[it]);
@@ -558,7 +560,7 @@ chunk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUte
                             if (!((i < 32 ? b0 : b1) >> (i & 31) & 1)) v[i] = kNegInf;
                     };
                     // Two streams read the row of S once (over FP8 caches, where that spills a few
-                    // registers, reading its second half twice took 895 us for 859); one reads it
+                    // registers, reading its second half twice took 5 % longer); one reads it
                     // twice, for its maximum and for P, 64 keys at a time in rolled loops, whose code
                     // stays small.
                     float sv[NT == 2 ? kKvTile : 1], ext = kNegInf;
