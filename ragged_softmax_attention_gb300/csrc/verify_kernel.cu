@@ -538,8 +538,8 @@ __global__ void __launch_bounds__(kVerifyThreads, 3) verify_kernel(const __grid_
         __syncthreads();
         u64 S = 0, before = 0;
         for (uint32_t r = 0; r < C; ++r) {
-            if (r < rank) before += sums[r];
-            S += sums[r];
+            if (r < rank) before = min(before + sums[r], kMost);
+            S = min(S + sums[r], kMost);
         }
         if (rank == 0 && tid == 0 && (S == 0 || S >= kMost)) record_error(a.status, kErrInvalid);
         const u64 want = __umul64hi(fraction(sh.u[kMaxDrafts]), S);
@@ -577,8 +577,8 @@ __global__ void __launch_bounds__(kVerifyThreads, 3) verify_kernel(const __grid_
                 __syncthreads();
                 u64 lead = 0, all = 0;
                 for (int i = 0; i < kVerifyWarps; ++i) {
-                    if (i < warp) lead += sh.scan[i];
-                    all += sh.scan[i];
+                    if (i < warp) lead = min(lead + sh.scan[i], kMost);
+                    all = min(all + sh.scan[i], kMost);
                 }
                 lead += incl - own;
                 if (rest >= lead && rest - lead < own) {

@@ -201,6 +201,37 @@ def test_large_rows_repeat_and_graph(fw):
     assert all(torch.equal(a, b) for a, b in zip(ref, got))
 
 
+def test_rows_that_add_up_to_far_more_than_four_are_told(fw):
+    """Halves of a row and its neighbours full of ones: sums of 64 bits must not go round."""
+    for ones in (4096, 2048, 4095, 1024, 3000, 8192):
+        p = torch.zeros(1, 1, 8192)
+        p[..., :ones] = 1.0
+        p[..., 4100] = 0.5
+        x = dict(tokens=i32([[0]]), parents=i32([[-1]]), target_probs=p, uniforms=torch.tensor([[0.0, 0.3]]))
+        for v in (4096, 8192):
+            got = run(fw, dict(x, target_probs=p[..., :v].contiguous()))[2]
+            assert fw.device_status() == 1 and -1 <= got.item() < v
+
+
+def test_long_rows_in_large_batches(fw):
+    """One CTA to a request, or eight: the same tokens, whatever a lane adds up."""
+    x = make(4, 4, 300001, 1, seed=20, sharp=2.0, noise=1.2)
+    x["parents"][:, 1:] = 0
+    x["uniforms"][1:3, 1:4] = 1 - 2.0 ** -20
+    x["uniforms"][0, 1:4] = 0.9
+    few = {k: v.cuda() for k, v in x.items()}
+    many = {k: v.repeat(160, *([1] * (v.dim() - 1))) if k not in ("target_probs", "draft_probs") else v for k, v in few.items()}
+    for draft in (True, False):
+        ref = fw.verify_drafts(**dict(few, draft_probs=few["draft_probs"] if draft else None))
+        for b in range(4):                                 # 640 requests that read one request's rows
+            y = dict(many, target_probs=few["target_probs"][b:b + 1].expand(640, -1, -1),
+                     draft_probs=few["draft_probs"][b:b + 1].expand(640, -1, -1) if draft else None)
+            got = fw.verify_drafts(**y)
+            for a, r in zip(got, ref):
+                assert torch.equal(a[b::4], r[b:b + 1].expand_as(a[b::4]))
+    assert fw.device_status() == 0
+
+
 @pytest.mark.parametrize("draft", [True, False])
 def test_first_token_is_distributed_as_the_targets(fw, draft):
     """80,000 requests with two children drawn from the draft model (or fixed): the
