@@ -555,8 +555,11 @@ fw_status_t fw_verify_drafts(const fw_tensor_t *tokens, const fw_tensor_t *paren
  * their LSE) and leaves the others alone.
  *
  * Arithmetic as fw_paged_decode_tree over BF16 caches: products of BF16 values summed in
- * FP32, weights rounded to BF16 for the product with V and summed unrounded.  E4M3 values
- * are widened to BF16, which holds every one.
+ * FP32, weights rounded to BF16 for the product with V and summed unrounded.  Over an FP8
+ * cache q is carried as the sum of two E4M3 terms on a power of two of its own per row
+ * (exact for elements down to 2^-10 of the row's largest, below to within 2^-17 of it; a
+ * row with an element that is not finite comes out as NaN), and V is widened to BF16, which
+ * holds every E4M3 value.
  *
  * Supported: D in {128, 256} (FP8: 128), B <= 4096, any chunk lengths, page sizes, strides
  * and alignment of fw_paged_decode; any Hq / Hkv, total_q * Hq and Hq * D / 8 below 2^31.

@@ -24,23 +24,25 @@
 // (another file).  Otherwise NT = 1 with three S buffers (two at D = 256), QK and PV issued
 // by a thread each.
 //
-// FP8 caches: a tile lands as bytes in half of its ring slot, four warps take it into
-// registers and write it back over the whole slot as BF16 (exact), so that every slot can
-// be loading and everything behind is the BF16 kernel.
+// FP8 caches: QK is kind::f8f6f4 on the bytes as they land, with each query row split in place
+// into two E4M3 terms (as in the tree decode; two terms of K = 32 take the tensor core as long
+// as one BF16 pass); PV is the BF16 kernel's, on values that four warps widen (exactly) into a
+// ring of two slots, so that most of shared memory is for copies in flight.  (Keys and values
+// widened in place, in a ring of BF16 slots: 811 us for 761 below.)  Their softmax warpgroups
+// have 160 registers, which the whole row of S does not fit, and read it twice.
 //
 // Measured (GB300): 2,048 tokens on 32,768 keys, 40/8 heads, 907 us, 1.56 PFLOP/s, bound by
 // the chain of a row tile (2,800 cycles a key tile of two, 2,048 of them products); 16
 // prompts of 300 .. 5,000 tokens, 32/8 heads, 797 us, 1.24 PFLOP/s, and 500 .. 2,000 tokens
 // with a window of 1,023 keys 144 us, where the ends of units (7,300 cycles) and masked tiles
 // take the rest; 48 requests of which 40 bring one token 322 us, 61 % of DRAM; FP8, 256 ..
-// 1,024 tokens on 2,048 .. 16,384 keys, 848 us, 1.09 PFLOP/s, bound by issue slots (4,000
-// cycles a key tile); 24 tokens on 700 keys 14.6 us, 6 of them before the first scores.
+// 1,024 tokens on 2,048 .. 16,384 keys, 761 us, 1.22 PFLOP/s, 3,800 cycles a key tile, to which
+// everything adds (one QK term less would take 75 us off, the widening 32, the second
+// reading 20); 24 tokens on 700 keys 14.6 us, 6 of them before the first scores.
 //
 // Warp roles: warp 0 copies K and V tiles, warps 1 and 2 issue the MMAs, warp 3 works out
 // the pieces and copies the queries, then NT warpgroups of softmax, then (FP8) a
 // warpgroup that widens.
-#include <cuda_fp8.h>
-
 #include "chunk_common.cuh"
 
 namespace fw {
@@ -58,17 +60,23 @@ struct ChunkCfg {
     static constexpr int kChunkBytes = 128 * 128;               // 128 rows x 64 bf16 columns
     static constexpr int kSlotBytes = 2 * kChunkBytes;          // 128 rows x 128 columns
     static constexpr int kQBytes = 128 * D * 2;
-    static constexpr int kSlots = (229376 - NT * kQBytes) / kSlotBytes;
+    // FP8: two slots of widened values, the rest is for keys and values as they land.
+    static constexpr int kSlots = KV8 ? 2 : (229376 - NT * kQBytes) / kSlotBytes;
+    static constexpr int kRawSlots = KV8 ? (229376 - NT * kQBytes - kSlots * kSlotBytes) / kChunkBytes / 2 : 0;      // of each
     static constexpr int kOffQ = 0;
     static constexpr int kOffRing = NT * kQBytes;
-    static constexpr int kOffBar = kOffRing + kSlots * kSlotBytes;
-    static constexpr int kSched = 4;                            // unit records in flight
+    static constexpr int kOffRaw = kOffRing + kSlots * kSlotBytes;      // keys, then values
+    static constexpr int kOffBar = kOffRaw + 2 * kRawSlots * kChunkBytes;
+    static constexpr int kSched = !KV8 ? 4 : NT == 2 ? 2 : 3;       // unit records in flight (FP8: what there is room for)
     static constexpr int kBarSlotFull = 0;
     static constexpr int kBarSlotEmpty = kBarSlotFull + kSlots;
-    static constexpr int kBarLanded = kBarSlotEmpty + kSlots;   // FP8: a slot's bytes are there
-    static constexpr int kBarQFull = kBarLanded + (KV8 ? kSlots : 0);
+    static constexpr int kBarRawFull = kBarSlotEmpty + kSlots;  // FP8: keys [kRawSlots], then values
+    static constexpr int kBarRawEmpty = kBarRawFull + 2 * kRawSlots;
+    static constexpr int kBarQFull = kBarRawEmpty + 2 * kRawSlots;
     static constexpr int kBarQEmpty = kBarQFull + 1;
-    static constexpr int kBarSFull = kBarQEmpty + 1;            // [NT][kSB]
+    static constexpr int kBarQReady = kBarQEmpty + 1;           // [kQSets], FP8: the queries are split
+    static constexpr int kQSets = KV8 ? kSched : 0;             // rows' exponents, beside the unit's record
+    static constexpr int kBarSFull = kBarQReady + kQSets;       // [NT][kSB]
     static constexpr int kBarPHalf = kBarSFull + NT * kSB;      // [NT][kSB]
     static constexpr int kBarPFull = kBarPHalf + NT * kSB;      // [NT][kSB]
     static constexpr int kBarPvDone = kBarPFull + NT * kSB;     // [NT][kSB]
@@ -83,37 +91,36 @@ struct ChunkCfg {
     static constexpr int kOffPlan = (kOffBad + kBadUnits * kBadUnitWords * 4 + 15) / 16 * 16;
     static constexpr int kOffScan = kOffPlan + 32;              // [16] warp sums
     static constexpr int kOffMisc = kOffScan + 128;
-    static constexpr int kSmemBytes = kOffMisc + 16 + 1024;
+    static constexpr int kOffExp = kOffMisc + 16;               // [kQSets][NT][128]
+    static constexpr int kSmemBytes = kOffExp + kQSets * NT * 128 + 1024;
     static_assert(kSmemBytes <= 232448, "shared memory budget of one CTA exceeded");
     static constexpr int kThreads = 128 + NT * 128 + (KV8 ? 128 : 0);
     static constexpr int kSchedReaders = 3 + 4 * NT + (KV8 ? 4 : 0);    // issuers, the producer, softmax, widening warps
     // NT = 2: launched at 168 registers (FP8: 128) a thread; after the split
-    // 128 x 80 + 256 x 208 = 63488 <= 384 x 168, FP8 128 x (80 + 64) + 256 x 184 = 512 x 128.
-    static constexpr uint32_t kRegsControl = 80, kRegsSoftmax = KV8 ? 184 : 208, kRegsWiden = 64;
+    // 128 x 80 + 256 x 208 = 63488 <= 384 x 168, FP8 128 x (72 + 120) + 256 x 160 = 512 x 128 (72 + 104
+    // and 168: 771 us for 761, 80 + 64 and 184: 837).
+    static constexpr uint32_t kRegsControl = KV8 ? 72 : 80, kRegsSoftmax = KV8 ? 160 : 208, kRegsWiden = 120;
+    static_assert(kRegsControl < 128 && kRegsWiden < 128 && kRegsSoftmax > (KV8 ? 128 : 168), "which way each goes");
     static_assert(NT == 1 || KV8 || 128 * kRegsControl + 256 * kRegsSoftmax <= 384 * 168, "register split");
     static_assert(NT == 1 || !KV8 || 128 * (kRegsControl + kRegsWiden) + 256 * kRegsSoftmax <= 512 * 128, "register split");
-    static constexpr uint32_t kIdescQK = idesc_bf16_f32(128, kKvTile, false, false);
+    static constexpr uint32_t kIdescQK = KV8 ? kIdescF8QK : idesc_bf16_f32(128, kKvTile, false, false);
     static constexpr uint32_t kIdescPV = idesc_bf16_f32(128, 128, false, true);
     __device__ static constexpr uint32_t s_col(int x, int buf) { return (uint32_t)(x * kSB + buf) * 128u; }
     __device__ static constexpr uint32_t o_col(int x) { return (uint32_t)(NT * kSB + x) * 128u; }
     // Ring positions, in whole K or V tiles, of a piece of n key tiles: two streams take
-    // K_j and V_j in turn; one runs QK kSB tiles ahead.
-    __device__ static __forceinline__ int ring_k(int j, int n) { return NT == 2 ? 2 * j : pos_k<kSB>(j, n); }
-    __device__ static __forceinline__ int ring_v(int j, int n) { return NT == 2 ? 2 * j + 1 : pos_v<kSB>(j, n); }
+    // K_j and V_j in turn; one runs QK kSB tiles ahead.  FP8: a ring each.
+    static constexpr int kPerTile = KV8 ? 1 : 2 * kTileSlots;   // positions of a key tile
+    __device__ static __forceinline__ int ring_k(int j, int n) { return KV8 ? j : NT == 2 ? 2 * j : pos_k<kSB>(j, n); }
+    __device__ static __forceinline__ int ring_v(int j, int n) { return KV8 ? j : NT == 2 ? 2 * j + 1 : pos_v<kSB>(j, n); }
 };
 
 // Four E4M3 bytes as BF16 (exact; NaN stays NaN).
-__device__ __forceinline__ uint2 widen4(uint32_t w) {
+__device__ __forceinline__ uint2 widen4_bf16(uint32_t w) {
     uint32_t h0, h1;
-    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
-        : "=r"(h0), "=r"(h1) : "r"(w));
-    uint2 r;
-    float a, b, c, d;
-    asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.f32.f16 %0, x;\n\tcvt.f32.f16 %1, y;\n\t}" : "=f"(a), "=f"(b) : "r"(h0));
-    asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.f32.f16 %0, x;\n\tcvt.f32.f16 %1, y;\n\t}" : "=f"(c), "=f"(d) : "r"(h1));
-    r.x = pack_bf16x2(a, b);
-    r.y = pack_bf16x2(c, d);
-    return r;
+    widen4(w, h0, h1);
+    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&h0));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&h1));
+    return make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(b.x, b.y));
 }
 
 template <int D, int NT, bool KV8>
@@ -129,9 +136,11 @@ chunk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUte
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
     uint64_t *slot_full = bars + C::kBarSlotFull;
     uint64_t *slot_empty = bars + C::kBarSlotEmpty;
-    uint64_t *landed = bars + C::kBarLanded;
+    uint64_t *raw_full = bars + C::kBarRawFull;
+    uint64_t *raw_empty = bars + C::kBarRawEmpty;
     uint64_t *q_full = bars + C::kBarQFull;
     uint64_t *q_empty = bars + C::kBarQEmpty;
+    uint64_t *q_ready = bars + C::kBarQReady;
     uint64_t *s_full = bars + C::kBarSFull;
     uint64_t *p_half = bars + C::kBarPHalf;
     uint64_t *p_full = bars + C::kBarPFull;
@@ -144,6 +153,7 @@ chunk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUte
     uint32_t *bad = reinterpret_cast<uint32_t *>(smem + C::kOffBad);
     long long *plan = reinterpret_cast<long long *>(smem + C::kOffPlan);
     long long *scan = reinterpret_cast<long long *>(smem + C::kOffScan);
+    int8_t *q_exp = reinterpret_cast<int8_t *>(smem + C::kOffExp);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::kOffMisc + 4);
 
@@ -153,10 +163,13 @@ chunk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUte
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kSlots; ++i) {
             mbar_init(&slot_full[i], KV8 ? 4 : 1); mbar_init(&slot_empty[i], NT);
-            if (KV8) mbar_init(&landed[i], 1);
+        }
+        for (int i = 0; i < 2 * C::kRawSlots; ++i) {
+            mbar_init(&raw_full[i], 1); mbar_init(&raw_empty[i], i < C::kRawSlots ? NT : 4);
         }
         mbar_init(q_full, 1);
         mbar_init(q_empty, NT);
+        for (int i = 0; i < C::kQSets; ++i) mbar_init(&q_ready[i], 4);
         for (int i = 0; i < NT * kSB; ++i) {
             mbar_init(&s_full[i], 1); mbar_init(&p_half[i], 4); mbar_init(&p_full[i], 4); mbar_init(&pv_done[i], 1);
         }
@@ -198,9 +211,9 @@ chunk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUte
       if constexpr (NT == 2) setmaxnreg_dec<C::kRegsControl>();
       if (warp == 0) {
         // ------------------------------------------------------------ producer
-        uint64_t *full = KV8 ? landed : slot_full;
         const int box_rows = p.ps < kKvTile ? p.ps : kKvTile;
-        uint32_t rp = 0;                                  // slots filled so far
+        uint32_t rp = 0;                                  // slots filled so far; FP8: key tiles of earlier pieces
+        uint32_t raw[2] = {0, 0};                         // FP8: slots of keys and of values filled so far
         // Test hook for the bounded waits: before it copies anything, this warp waits on
         // a barrier that nothing completes.  Nor do products then begin; the other roles
         // wind down over the units at hand.
@@ -215,23 +228,31 @@ chunk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUte
                                   (p.ps >= kKvTile || key0 + (lane + 1) * p.ps > u.lo);
                 const unsigned who = __ballot_sync(0xffffffffu, mine);
                 const uint32_t bytes = (uint32_t)(__popc(who) * box_rows * (KV8 ? 128 : 256));
-#pragma unroll
-                for (int s = 0; s < TS; ++s, ++rp) {
-                    const int sl = rp % C::kSlots;
-                    if (!warp_wait(&slot_empty[sl], ((rp / C::kSlots) & 1) ^ 1, wc, lane)) return false;
-                    if (lane == 0) mbar_arrive_expect_tx(&full[sl], bytes);
+                if constexpr (KV8) {
+                    const uint32_t r = rp + j;
+                    const int sl = r % C::kRawSlots + (is_v ? C::kRawSlots : 0);
+                    if (!warp_wait(&raw_empty[sl], ((r / C::kRawSlots) & 1) ^ 1, wc, lane)) return false;
+                    if (lane == 0) mbar_arrive_expect_tx(&raw_full[sl], bytes);
                     __syncwarp();
-                    if (mine) {
-                        const int phys = checked_page(p, entry);
-                        const void *map = is_v ? (const void *)&tm_v : (const void *)&tm_k;
-                        if constexpr (KV8) {
-                            tma_load_4d(smem_u32(sRing + sl * C::kSlotBytes + C::kChunkBytes + lane * box_rows * 128), map, &full[sl],
-                                        0, u.g, slot0, phys);
-                        } else {
+                    if (is_v) raw[1] = r + 1;
+                    else raw[0] = r + 1;
+                    if (mine)
+                        tma_load_4d(smem_u32(smem + C::kOffRaw + sl * C::kChunkBytes + lane * box_rows * 128),
+                                    is_v ? (const void *)&tm_v : (const void *)&tm_k, &raw_full[sl], 0, u.g, slot0, checked_page(p, entry));
+                } else {
+#pragma unroll
+                    for (int s = 0; s < TS; ++s, ++rp) {
+                        const int sl = rp % C::kSlots;
+                        if (!warp_wait(&slot_empty[sl], ((rp / C::kSlots) & 1) ^ 1, wc, lane)) return false;
+                        if (lane == 0) mbar_arrive_expect_tx(&slot_full[sl], bytes);
+                        __syncwarp();
+                        if (mine) {
+                            const int phys = checked_page(p, entry);
+                            const void *map = is_v ? (const void *)&tm_v : (const void *)&tm_k;
 #pragma unroll
                             for (int c = 0; c < 2; ++c)
                                 tma_load_4d(smem_u32(sRing + sl * C::kSlotBytes + c * C::kChunkBytes + lane * box_rows * 128), map,
-                                            &full[sl], s * 128 + c * 64, u.g, slot0, phys);
+                                            &slot_full[sl], s * 128 + c * 64, u.g, slot0, phys);
                         }
                     }
                 }
@@ -262,11 +283,21 @@ chunk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUte
                     }
                 }
             }
+            if constexpr (KV8) rp += u.ntiles;
         }
         if (lane == 0) {
-            for (uint32_t i = 0; i < (uint32_t)C::kSlots && i < rp; ++i) {
-                const uint32_t r = rp - 1 - i;
-                mbar_wait_drain(&full[r % C::kSlots], (r / C::kSlots) & 1, wc);
+            // The copies land before the CTA leaves.
+            auto drain = [&](uint64_t *full, uint32_t slots, uint32_t filled) {
+                for (uint32_t i = 0; i < slots && i < filled; ++i) {
+                    const uint32_t r = filled - 1 - i;
+                    mbar_wait_drain(&full[r % slots], (r / slots) & 1, wc);
+                }
+            };
+            if constexpr (KV8) {
+                drain(raw_full, C::kRawSlots, raw[0]);
+                drain(raw_full + C::kRawSlots, C::kRawSlots, raw[1]);
+            } else {
+                drain(slot_full, C::kSlots, rp);
             }
         }
         __syncwarp();
@@ -278,7 +309,7 @@ chunk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUte
             uint32_t steps = 0;                           // this stream's key tiles of earlier pieces
             uint32_t turns = 0;                           // shared steps of earlier pieces (both streams present)
             const SDesc q_d = sdesc_sw128_split(smem_u32(sQ + x * C::kQBytes), 16, 1024);
-            const SDesc k_d = sdesc_sw128_split(smem_u32(sRing), 16, 1024);
+            const SDesc k_d = sdesc_sw128_split(smem_u32(KV8 ? smem + C::kOffRaw : sRing), 16, 1024);
             const SDesc v_d = sdesc_sw128_split(smem_u32(sRing), C::kChunkBytes, 1024);
             auto wait_tile = [&](uint32_t r) -> bool {
 #pragma unroll
@@ -286,20 +317,42 @@ chunk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUte
                     if (!mbar_wait(&slot_full[(r + s) % C::kSlots], ((r + s) / C::kSlots) & 1, wc)) return false;
                 return true;
             };
+            auto wait_keys = [&](uint32_t r) -> bool {
+                if constexpr (KV8) return mbar_wait(&raw_full[r % C::kRawSlots], (r / C::kRawSlots) & 1, wc);
+                return wait_tile(r);
+            };
+            auto wait_queries = [&](int k) -> bool {
+                if constexpr (KV8) return mbar_wait(&q_ready[k % C::kQSets], (k / C::kQSets) & 1, wc);
+                return mbar_wait(q_full, k & 1, wc);
+            };
             auto release_tile = [&](uint32_t r) {
 #pragma unroll
                 for (int s = 0; s < TS; ++s) mma_commit(&slot_empty[(r + s) % C::kSlots]);
             };
+            auto release_keys = [&](uint32_t r) {
+                if constexpr (KV8) mma_commit(&raw_empty[r % C::kRawSlots]);
+                else release_tile(r);
+            };
             const uint32_t idesc_qk = C::kIdescQK | (p.scale_log2 < 0.f ? kIdescNegateA : 0u);
             auto push_qk = [&](uint32_t r, int buf) {
+                if constexpr (KV8) {
+                    const SDesc kd{k_d.lo + (r % C::kRawSlots) * (C::kChunkBytes >> 4), k_d.hi};
 #pragma unroll
-                for (int s = 0; s < TS; ++s) {
-                    const SDesc kd{k_d.lo + ((r + s) % C::kSlots) * (C::kSlotBytes >> 4), k_d.hi};
+                    for (int term = 0; term < 2; ++term)
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk) {
-                        const uint32_t off = (kk >> 2) * C::kChunkBytes + (kk & 3) * 32;
-                        mma_bf16_ss(tmem + C::s_col(x, buf), sdesc_at(q_d, s * C::kSlotBytes + off), sdesc_at(kd, off),
-                                    idesc_qk, s + kk > 0 ? 1u : 0u);
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_f8_ss(tmem + C::s_col(x, buf), sdesc_at(q_d, term * C::kChunkBytes + kk * 32),
+                                      sdesc_at(kd, kk * 32), idesc_qk, term + kk > 0 ? 1u : 0u);
+                } else {
+#pragma unroll
+                    for (int s = 0; s < TS; ++s) {
+                        const SDesc kd{k_d.lo + ((r + s) % C::kSlots) * (C::kSlotBytes >> 4), k_d.hi};
+#pragma unroll
+                        for (int kk = 0; kk < 8; ++kk) {
+                            const uint32_t off = (kk >> 2) * C::kChunkBytes + (kk & 3) * 32;
+                            mma_bf16_ss(tmem + C::s_col(x, buf), sdesc_at(q_d, s * C::kSlotBytes + off), sdesc_at(kd, off),
+                                        idesc_qk, s + kk > 0 ? 1u : 0u);
+                        }
                     }
                 }
             };
@@ -326,7 +379,7 @@ chunk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUte
                 free_unit(k);
                 if (!got) break;
                 const uint32_t r0 = rp;
-                rp += (uint32_t)(2 * n * TS);
+                rp += (uint32_t)(n * C::kPerTile);
                 auto rk = [&](int j) { return r0 + (uint32_t)(C::ring_k(j, n) * TS); };
                 auto rv = [&](int j) { return r0 + (uint32_t)(C::ring_v(j, n) * TS); };
                 if constexpr (NT == 1) {
@@ -334,19 +387,19 @@ chunk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUte
                     // the other's products.  Each waits for the other's step first: what lay
                     // in the ring slot before its tile has then landed, as a parity wait
                     // needs (K_j comes at most kSB tiles before V_j, less than the ring).
-                    if (warp == 2 && !mbar_wait(q_full, k & 1, wc)) break;
+                    if (warp == 2 && !wait_queries(k)) break;
                     for (int j = 0; j < n && ok; ++j) {
                         const uint32_t st = steps + j;
                         const int buf = st % kSB;
                         const uint32_t ph = (st / kSB) & 1;
                         if (warp == 2) {
                             // The buffer's last P has gone through the tensor core.
-                            ok = (st < kSB || mbar_wait(&pv_done[buf], ph ^ 1, wc)) && wait_tile(rk(j));
+                            ok = (st < kSB || mbar_wait(&pv_done[buf], ph ^ 1, wc)) && wait_keys(rk(j));
                             if (!ok) break;
                             tc_fence_after();
                             push_qk(rk(j), buf);
                             mma_commit(&s_full[buf]);
-                            release_tile(rk(j));
+                            release_keys(rk(j));
                             if (j == n - 1) mma_commit(q_empty);
                         } else {
                             ok = mbar_wait(&p_half[buf], ph, wc) && wait_tile(rv(j));
@@ -363,22 +416,27 @@ chunk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUte
                     }
                     steps += n;
                 } else {
-                    if (!mbar_wait(q_full, k & 1, wc)) break;
+                    if (!wait_queries(k)) break;
                     if (x >= nrt) {
                         // No row tile for this stream: it still sees every copy land and
                         // hands every slot back, so that its phases stay in step.
                         mbar_arrive(q_empty);
                         for (uint32_t r = r0; r < rp && ok; ++r) {
+                            if constexpr (KV8) {
+                                ok = wait_keys(r);
+                                if (ok) mbar_arrive(&raw_empty[r % C::kRawSlots]);
+                                if (!ok) break;
+                            }
                             ok = mbar_wait(&slot_full[r % C::kSlots], (r / C::kSlots) & 1, wc);
                             if (ok) mbar_arrive(&slot_empty[r % C::kSlots]);
                         }
                         continue;
                     }
-                    if (!wait_tile(rk(0))) break;
+                    if (!wait_keys(rk(0))) break;
                     tc_fence_after();
                     push_qk(rk(0), 0);
                     mma_commit(&s_full[x]);
-                    release_tile(rk(0));
+                    release_keys(rk(0));
                     if (n == 1) mma_commit(q_empty);
                     for (int j = 0; j < n && ok; ++j) {
                         const uint32_t ph = (steps + j) & 1;
@@ -392,7 +450,7 @@ chunk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUte
                         // A wait between pushes lets the tensor pipe run dry: the tiles of the
                         // whole step first.  (K_{j+1} needs only older slots handed back.)
                         const bool next = j + 1 < n;
-                        if (!wait_tile(rv(j)) || (next && !wait_tile(rk(j + 1))) || !mbar_wait(&p_half[x], ph, wc)) {
+                        if (!wait_tile(rv(j)) || (next && !wait_keys(rk(j + 1))) || !mbar_wait(&p_half[x], ph, wc)) {
                             ok = false;
                             break;
                         }
@@ -409,7 +467,7 @@ chunk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUte
                         release_tile(rv(j));
                         if (next) {
                             mma_commit(&s_full[x]);
-                            release_tile(rk(j + 1));
+                            release_keys(rk(j + 1));
                             if (j + 2 == n) mma_commit(q_empty);
                         }
                     }
@@ -459,19 +517,18 @@ chunk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUte
     } else if (KV8 && warp >= 4 + 4 * NT) {
         if constexpr (KV8) {
             // ------------------------------------------------------ widening
-            // The bytes lie in the slot's second half, where columns 64 .. 127 will be: columns 0 ..
-            // 63 go to the first half at once, the others to where they lie once all threads
-            // have theirs in registers.  Eight lanes take four 16-byte units of two rows whose
-            // numbers differ in bits 0 and 2: their swizzled places then fall on different banks,
-            // read and written.  (The barrier among them has no limit: they wait together, and a
-            // wait that ran out does not part them.)
+            // A unit's queries first, into two E4M3 terms in place; then its values, from where
+            // they landed to a slot that the products read.  Eight lanes take four 16-byte units
+            // of two rows whose numbers differ in bits 0 and 2: their swizzled places then fall on
+            // different banks, read and written.  (The barrier among them has no limit: they wait
+            // together, and a wait that ran out does not part them.)
             if constexpr (NT == 2) setmaxnreg_dec<C::kRegsWiden>();
             const int r = (lane >> 3) ^ (lane & 4 ? 5 : 0), row0 = (warp & 3) * 32 + r, c = 2 * (lane & 3);
-            const uint32_t from0 = C::kChunkBytes + row0 * 128 + (((lane & 3) ^ r) << 4);
-            const uint32_t from1 = C::kChunkBytes + row0 * 128 + (((lane & 3) + 4) ^ r) * 16;
+            const uint32_t from0 = row0 * 128 + (((lane & 3) ^ r) << 4);
+            const uint32_t from1 = row0 * 128 + (((lane & 3) + 4) ^ r) * 16;
             const uint32_t to0 = row0 * 128 + ((c ^ r) << 4), to1 = row0 * 128 + (((c + 1) ^ r) << 4);
             auto put = [&](uint8_t *at, const uint4 &b) {
-                const uint2 x0 = widen4(b.x), x1 = widen4(b.y), x2 = widen4(b.z), x3 = widen4(b.w);
+                const uint2 x0 = widen4_bf16(b.x), x1 = widen4_bf16(b.y), x2 = widen4_bf16(b.z), x3 = widen4_bf16(b.w);
                 *reinterpret_cast<uint4 *>(at + to0) = make_uint4(x0.x, x0.y, x1.x, x1.y);
                 *reinterpret_cast<uint4 *>(at + to1) = make_uint4(x2.x, x2.y, x3.x, x3.y);
             };
@@ -479,34 +536,43 @@ chunk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUte
             for (int k = 0;; ++k) {
                 const ChunkUnit u = warp_unit(k);
                 if (!named_bar_all(2, 128, u.b >= 0)) break;
-                for (int i = 0; i < 2 * u.ntiles; ++i, ++rp) {
-                    const int sl = rp % C::kSlots;
+                mbar_wait(q_full, k & 1, wc);
+                __syncwarp();
+                const int set = k % C::kQSets;
+                for (int x = 0; x < u.nrt; ++x)
+                    split_rows<C::kChunkBytes>(sQ + x * C::kQBytes, p.head_chunks > 1 ? 128 : p.G * p.tile_tokens, warp & 3,
+                                               q_exp + (set * NT + x) * 128);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&q_ready[set]);
+                for (int i = 0; i < u.ntiles; ++i, ++rp) {
+                    const int rl = C::kRawSlots + rp % C::kRawSlots, sl = rp % C::kSlots;
                     // (Every lane waits: those that only hear of it from one that did may have read before.)
-                    mbar_wait(&landed[sl], (rp / C::kSlots) & 1, wc);
+                    mbar_wait(&raw_full[rl], (rp / C::kRawSlots) & 1, wc);
+                    mbar_wait(&slot_empty[sl], ((rp / C::kSlots) & 1) ^ 1, wc);
                     __syncwarp();
+                    const uint8_t *from = smem + C::kOffRaw + rl * C::kChunkBytes;
                     uint8_t *at = sRing + sl * C::kSlotBytes;
-                    uint4 b1[4];
-#pragma unroll
-                    for (int it = 0; it < 4; ++it) b1[it] = *reinterpret_cast<const uint4 *>(at + it * 1024 + from1);
 #pragma unroll
                     for (int it = 0; it < 4; it += 2) {
-                        const uint4 b0 = *reinterpret_cast<const uint4 *>(at + it * 1024 + from0);
-                        const uint4 b2 = *reinterpret_cast<const uint4 *>(at + it * 1024 + 1024 + from0);
+                        const uint4 b0 = *reinterpret_cast<const uint4 *>(from + it * 1024 + from0);
+                        const uint4 b1 = *reinterpret_cast<const uint4 *>(from + it * 1024 + from1);
+                        const uint4 b2 = *reinterpret_cast<const uint4 *>(from + it * 1024 + 1024 + from0);
+                        const uint4 b3 = *reinterpret_cast<const uint4 *>(from + it * 1024 + 1024 + from1);
                         put(at + it * 1024, b0);
+                        put(at + C::kChunkBytes + it * 1024, b1);
                         put(at + it * 1024 + 1024, b2);
+                        put(at + C::kChunkBytes + it * 1024 + 1024, b3);
                     }
-                    named_bar_sync(2, 128);
-#pragma unroll
-                    for (int it = 0; it < 4; ++it) put(at + C::kChunkBytes + it * 1024, b1[it]);
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&slot_full[sl]);
+                    if (lane == 0) { mbar_arrive(&raw_empty[rl]); mbar_arrive(&slot_full[sl]); }
                 }
             }
         }
     } else {
         if constexpr (NT == 2) {
-            if constexpr (C::kRegsSoftmax > (KV8 ? 128 : 168)) setmaxnreg_inc<C::kRegsSoftmax>();
+            setmaxnreg_inc<C::kRegsSoftmax>();
         }
         // ------------------------------------------------- softmax / epilogue
         // The named barriers below have no limit, so the warps that share them never part:
@@ -516,14 +582,32 @@ chunk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUte
         const int q4 = warp & 3;
         const int row = q4 * 32 + lane;
         const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
-        const float scale = fabsf(p.scale_log2);      // the MMA negates Q for a negative one
+        const float scale_all = fabsf(p.scale_log2);  // the MMA negates Q for a negative one
         auto wait_pv = [&](uint32_t step) { mbar_wait(&pv_done[x * kSB + step % kSB], (step / kSB) & 1, wc); };
         uint32_t steps = 0, pieces = 0, rp = 0;
         for (int k = 0;; ++k) {
-            const ChunkUnit u = warp_unit(k);
+            ChunkUnit u;
+            float scale = scale_all;
+            if constexpr (KV8) {
+                // The row's exponent is read before the record goes back: the unit that
+                // reuses its place cannot come before that.  (Bounded from below: a scale of
+                // zero, or a small one times the 2^-126 of a row of zeros, would turn the -inf
+                // of hidden keys into NaN.  Sums here stay below 2^24, so under the bound every
+                // score is zero to the exponential.)
+                const ChunkUnit *ur = wait_unit(k);
+                u.b = -1;
+                if (ur) u = *ur;
+                const int set = k % C::kQSets;
+                if (u.b >= 0) mbar_wait(&q_ready[set], (k / C::kQSets) & 1, wc);
+                scale = fmaxf(scale * __int_as_float((127 - q_exp[(set * NT + x) * 128 + row]) << 23), 1e-37f);
+                __syncwarp();
+                if (lane == 0) free_unit(k);
+            } else {
+                u = warp_unit(k);
+            }
             if (!(x == 0 ? named_bar_all(1, 128, u.b >= 0) : __all_sync(0xffffffffu, u.b >= 0) != 0)) break;
             const uint32_t r0 = rp;
-            rp += (uint32_t)(2 * u.ntiles * TS);
+            rp += (uint32_t)(u.ntiles * C::kPerTile);
             if (x >= u.nrt) continue;
             uint32_t *marks = bad + k % kBadUnits * kBadUnitWords;
             if (x == 0) {
@@ -567,12 +651,12 @@ chunk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUte
                         for (int i = 0; i < 64; ++i)
                             if (!((i < 32 ? b0 : b1) >> (i & 31) & 1)) v[i] = kNegInf;
                     };
-                    // Two streams read the row of S once (over FP8 caches, where that spills a few
-                    // registers, reading its second half twice took 5 % longer); one reads it
-                    // twice, for its maximum and for P, 64 keys at a time in rolled loops, whose code
-                    // stays small.
-                    float sv[NT == 2 ? kKvTile : 1], ext = kNegInf;
-                    if constexpr (NT == 2) {
+                    // Two streams read the row of S once.  One stream, and streams over FP8 caches,
+                    // which have no registers for it (854 us for 768), read it twice, for its maximum
+                    // and for P, 64 keys at a time in rolled loops, whose code stays small (unrolled
+                    // 831 for 771; 32 keys at a time 804 for 761).
+                    float sv[NT == 2 && !KV8 ? kKvTile : 1], ext = kNegInf;
+                    if constexpr (NT == 2 && !KV8) {
                         read_s(0, sv);
                         read_s(1, sv + 64);
                         tmem_wait_ld();
@@ -634,7 +718,7 @@ chunk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUte
                         __syncwarp();
                         if (lane == 0 && !values) mbar_arrive(half == 0 ? &p_half[x * kSB + buf] : &p_full[x * kSB + buf]);
                     };
-                    if constexpr (NT == 2) {
+                    if constexpr (NT == 2 && !KV8) {
                         put_half(0, sv);
                         put_half(1, sv + 64);
                     } else {
@@ -654,14 +738,18 @@ chunk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUte
                     // NaN; nor those that are not finite the weights of rows that do not see
                     // them.  A thread looks after one key, when its row of P is done: the values
                     // have landed meanwhile.
-                    const uint32_t r = r0 + (uint32_t)(C::ring_v(j, u.ntiles) * TS);
+                    const uint32_t r = r0 + (uint32_t)(C::ring_v(j, u.ntiles) * TS);      // (FP8: of widened values)
                     // A parity wait needs the slot's copy before V_j to have landed.
                     // S_j there proves that for all copies up to K_j; with two slots
                     // to a tile the one before V_j's may be V_{j-1}, which its
                     // finished product proves.
-                    static_assert(TS == 2 || NT == 2 || C::kSlots >= 2 * kSB, "the ring holds what QK runs ahead");
+                    // So does that of V_{j-2} for two slots of widened values.
+                    static_assert(TS == 2 || NT == 2 || KV8 || C::kSlots >= 2 * kSB, "the ring holds what QK runs ahead");
                     if constexpr (TS == 2) {
                         if (steps > 0) wait_pv(steps - 1);
+                    }
+                    if constexpr (KV8 && NT == 1) {
+                        if (steps > 1) wait_pv(steps - 2);
                     }
                     const int key = key0 + row;
                     const bool seen = key >= any_lo && key < any_hi;
@@ -724,7 +812,8 @@ chunk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUte
                     }
                 }
                 write_row_at<D, NT>(p, u, x, row, live, (int64_t)(u.q0 + t) * p.out_stride[0] + h * p.out_stride[1],
-                                    (int64_t)(u.q0 + t) * p.lse_stride[0] + h * p.lse_stride[1], m_ref, l_sum, live && poison,
+                                    (int64_t)(u.q0 + t) * p.lse_stride[0] + h * p.lse_stride[1],
+                                    m_ref, l_sum, live && poison,
                                     [&](int c, float (&o)[32]) {
                     tmem_ld32(tmem + lane_off + C::o_col(x) + c * 32, o);
                     tmem_wait_ld();

@@ -6,6 +6,8 @@
 #pragma once
 
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
 
 #include "decode_common.cuh"
 #include "fw_internal.h"
@@ -372,6 +374,78 @@ __device__ __forceinline__ bool sees_bad(const uint32_t *bad, const TreeUnit &u,
 #pragma unroll 1
     for (int w = 0; 32 * w < u.d; ++w) hit |= bad[k % kBadUnits * kBadWords + w] & (uint32_t)__ldg(mrow + w);
     return hit != 0;
+}
+
+// ------------------------------------------------------------ 8-bit caches
+constexpr float kPShift = 7.0f;     // FP16 weights carry 2^7
+
+// kind::f8f6f4, A and B E4M3 K-major, FP32 accumulation.
+constexpr uint32_t kIdescF8QK = (1u << 4) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+// kind::f16, A and B FP16, B MN-major, FP32 accumulation.
+constexpr uint32_t kIdescF16PV = (1u << 4) | (1u << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+
+// Four E4M3 values (one word) as four FP16 values, two words.
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi) : "r"(w));
+}
+
+// Two BF16 values (one word) times `up` as hi + mid, two E4M3 values each.
+__device__ __forceinline__ void split2(uint32_t w, float up, uint32_t &hi, uint32_t &mid) {
+    const float a = __uint_as_float(w << 16) * up, b = __uint_as_float(w & 0xffff0000u) * up;
+    hi = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    const float2 h = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi, __NV_E4M3)));
+    mid = __nv_cvt_float2_to_fp8x2(make_float2(a - h.x, b - h.y), __NV_SATFINITE, __NV_E4M3);
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// BF16 row * 2^e = hi + mid, both E4M3, over the row's own bytes (two blocks of 128 bytes a
+// row, HALF apart, swizzled): 16 lanes hold a row's 16-byte units, four warps eight rows a pass
+// each (each pass waits for its reads and its maxima once), all read before any is written.
+template <int HALF>
+__device__ __forceinline__ void split_rows(uint8_t *q0, int rows, int warp, int8_t *exps) {
+    const int lane = threadIdx.x & 31, un = lane & 15;
+#pragma unroll 1
+    for (int rb = 8 * warp; rb < rows; rb += 32) {
+        const int r0 = rb + (lane >> 4);
+        uint4 w[4];
+        uint32_t big[4];                      // largest magnitude, as the bits of an FP32
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = r0 + 2 * i;
+            w[i] = *reinterpret_cast<const uint4 *>(q0 + (un >> 3) * HALF + r * 128 + (((un & 7) ^ (r & 7)) << 4));
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            auto top = [](uint32_t v) { return max((v << 16) & 0x7fff0000u, v & 0x7fff0000u); };
+            big[i] = max(max(top(w[i].x), top(w[i].y)), max(top(w[i].z), top(w[i].w)));
+        }
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) big[i] = max(big[i], __shfl_xor_sync(0xffffffffu, big[i], o));
+        __syncwarp();                         // the rows are read
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = r0 + 2 * i;
+            const int e = min(126, max(-120, 134 - (int)(big[i] >> 23)));   // 7 - (exponent - 127)
+            if (un == 0) exps[r] = (int8_t)e;
+            // An infinite or NaN element makes the row's scores NaN.
+            const float up = __int_as_float(big[i] >= 0x7f800000u ? 0x7fc00000 : (127 + e) << 23);
+            uint32_t hi[4], mid[4];
+            split2(w[i].x, up, hi[0], mid[0]);
+            split2(w[i].y, up, hi[1], mid[1]);
+            split2(w[i].z, up, hi[2], mid[2]);
+            split2(w[i].w, up, hi[3], mid[3]);
+            uint8_t *to = q0 + r * 128 + (((un >> 1) ^ (r & 7)) << 4) + (un & 1) * 8;
+            *reinterpret_cast<uint2 *>(to) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+            *reinterpret_cast<uint2 *>(to + HALF) = make_uint2(mid[0] | mid[1] << 16, mid[2] | mid[3] << 16);
+        }
+    }
 }
 
 // A piece's partial rows: 16-byte units of four columns, the rows of a unit side by

@@ -45,12 +45,6 @@ namespace {
 using namespace tree;
 
 constexpr int D = 128;
-constexpr float kPShift = 7.0f;     // P carries 2^7
-
-// kind::f8f6f4, A and B E4M3 K-major, FP32 accumulation.
-constexpr uint32_t kIdescQK = (1u << 4) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
-// kind::f16, A and B FP16, B MN-major, FP32 accumulation.
-constexpr uint32_t kIdescPV = (1u << 4) | (1u << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
 
 template <int NT_>
 struct F8TreeCfg {
@@ -113,30 +107,11 @@ struct F8TreeCfg {
     __device__ static constexpr uint32_t o_col(int x) { return (uint32_t)(NT * kSB + x) * 128u; }
 };
 
-// Four E4M3 values (one word) as four FP16 values, two words.
-__device__ __forceinline__ void widen4(uint32_t w, uint32_t &lo, uint32_t &hi) {
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-        : "=r"(lo), "=r"(hi) : "r"(w));
-}
-
-// Two BF16 values (one word) times `up` as hi + mid, two E4M3 values each.
-__device__ __forceinline__ void split2(uint32_t w, float up, uint32_t &hi, uint32_t &mid) {
-    const float a = __uint_as_float(w << 16) * up, b = __uint_as_float(w & 0xffff0000u) * up;
-    hi = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-    const float2 h = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi, __NV_E4M3)));
-    mid = __nv_cvt_float2_to_fp8x2(make_float2(a - h.x, b - h.y), __NV_SATFINITE, __NV_E4M3);
-}
-
 // -inf in place of the scores of hidden keys.
 __device__ __forceinline__ void hide(float (&v)[64], uint32_t lo, uint32_t hi) {
 #pragma unroll
     for (int i = 0; i < 64; ++i)
         if (!((i < 32 ? lo : hi) >> (i & 31) & 1)) v[i] = kNegInf;
-}
-
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-    const __half2 v = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&v);
 }
 
 template <int NT>
@@ -302,7 +277,7 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
             auto k_there = [&](uint32_t i) {
                 return mbar_try_wait(smem_u32(&k_full[i % C::kKSlots]), (i / C::kKSlots) & 1);
             };
-            const uint32_t idesc_qk = kIdescQK | (p.scale_log2 < 0.f ? kIdescNegateA : 0u);
+            const uint32_t idesc_qk = kIdescF8QK | (p.scale_log2 < 0.f ? kIdescNegateA : 0u);
             auto push_qk = [&](uint32_t i, int buf) {
                 const SDesc kd{k_d.lo + (i % C::kKSlots) * (C::kKBytes >> 4), k_d.hi};
 #pragma unroll
@@ -317,7 +292,7 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
 #pragma unroll
                 for (int k4 = 0; k4 < 4; ++k4)
                     mma_bf16_ts(tmem + C::o_col(x), tmem + C::s_col(x, buf) + (half * 4 + k4) * 8,
-                                sdesc_at(vd, k4 * 16 * 128), kIdescPV, (first && half + k4 == 0) ? 0u : 1u);
+                                sdesc_at(vd, k4 * 16 * 128), kIdescF16PV, (first && half + k4 == 0) ? 0u : 1u);
             };
             bool ok = true;
             if constexpr (NT == 1) {
@@ -480,49 +455,8 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
             if (row < kBadWords) bad[k % kBadUnits * kBadWords + row] = 0;
             mbar_wait(q_full, k & 1, wc);
             for (int x = 0; x < u.nrt; ++x) {
-                // BF16 row * 2^e = hi + mid, both E4M3, over the row's own bytes: 16 lanes
-                // hold a row's 16-byte units, eight rows a pass (each pass waits for its
-                // reads and its maxima once), all read before any is written.
-                uint8_t *q0 = sQ + x * C::kQBytes;
-                const int rows = p.head_chunks > 1 ? 128 : p.G * p.tile_tokens;
-                const int un = lane & 15;
-#pragma unroll 1
-                for (int rb = 8 * (warp - 4); rb < rows; rb += 32) {
-                    const int r0 = rb + (lane >> 4);
-                    uint4 w[4];
-                    uint32_t big[4];                      // largest magnitude, as the bits of an FP32
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = r0 + 2 * i;
-                        w[i] = *reinterpret_cast<const uint4 *>(q0 + (un >> 3) * C::kHalf + r * 128 + (((un & 7) ^ (r & 7)) << 4));
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        auto top = [](uint32_t v) { return max((v << 16) & 0x7fff0000u, v & 0x7fff0000u); };
-                        big[i] = max(max(top(w[i].x), top(w[i].y)), max(top(w[i].z), top(w[i].w)));
-                    }
-#pragma unroll
-                    for (int o = 8; o > 0; o >>= 1)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) big[i] = max(big[i], __shfl_xor_sync(0xffffffffu, big[i], o));
-                    __syncwarp();                         // the rows are read
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = r0 + 2 * i;
-                        const int e = min(126, max(-120, 134 - (int)(big[i] >> 23)));   // 7 - (exponent - 127)
-                        if (un == 0) q_exp[(k % C::kSched * NT + x) * 128 + r] = (int8_t)e;
-                        // An infinite or NaN element makes the row's scores NaN.
-                        const float up = __int_as_float(big[i] >= 0x7f800000u ? 0x7fc00000 : (127 + e) << 23);
-                        uint32_t hi[4], mid[4];
-                        split2(w[i].x, up, hi[0], mid[0]);
-                        split2(w[i].y, up, hi[1], mid[1]);
-                        split2(w[i].z, up, hi[2], mid[2]);
-                        split2(w[i].w, up, hi[3], mid[3]);
-                        uint8_t *to = q0 + r * 128 + (((un >> 1) ^ (r & 7)) << 4) + (un & 1) * 8;
-                        *reinterpret_cast<uint2 *>(to) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-                        *reinterpret_cast<uint2 *>(to + C::kHalf) = make_uint2(mid[0] | mid[1] << 16, mid[2] | mid[3] << 16);
-                    }
-                }
+                split_rows<C::kHalf>(sQ + x * C::kQBytes, p.head_chunks > 1 ? 128 : p.G * p.tile_tokens, warp - 4,
+                                     q_exp + (k % C::kSched * NT + x) * 128);
             }
             fence_proxy_async_smem();
             __syncwarp();

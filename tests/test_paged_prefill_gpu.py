@@ -1,7 +1,9 @@
 """Chunk attention over a paged cache against the 64-bit definition.
 
 The bound of an output element, from the arithmetic alone, is that of the tree
-decode over a BF16 cache (E4M3 values are widened exactly): weights rounded to BF16
+decode over a BF16 cache (E4M3 values are widened exactly, and queries over them carried
+exactly down to 2^-10 of a row's largest element; normal ones below, one in 400, are off by
+2^-17 of it, a hundredth of the scores' bound): weights rounded to BF16
 (2u absv, u = 2^-8, covers either way of summing), FP32 scores of D products off by
 (D + 8) 2^-24 sum |q_i k_i| scale, exponentials, sums and the merge by less than 2^-18
 relative, the result rounded to BF16.  LSE: the score's error plus 2^-20 of its
@@ -259,6 +261,54 @@ def test_nan_keys_and_queries(fw, kv8):
     keep = torch.ones(100, 8, dtype=torch.bool, device="cuda")
     keep[3, 2] = False
     assert torch.equal(out[keep], clean[keep]) and torch.isnan(out[3, 2]).all() and torch.isnan(lse[3, 2])
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_queries_that_are_not_finite_over_8_bit_caches(fw, bad):
+    """Both terms of such a row are NaN: the row and its LSE are, the others are as ever."""
+    x = make([100, 3], [400, 50], 8, 2, 128, 16, kv8=True, seed=27)
+    clean, clean_lse = run_and_check(fw, x)
+    y = on_gpu(x)
+    for at in ((3, 2, 5), (99, 7, 127), (101, 0, 0)):
+        y["q"][at] = bad
+    out, lse = fw.paged_prefill(**y)
+    keep = torch.ones(103, 8, dtype=torch.bool, device="cuda")
+    for at in ((3, 2), (99, 7), (101, 0)):
+        keep[at] = False
+    assert torch.equal(out[keep], clean[keep]) and torch.equal(lse[keep], clean_lse[keep])
+    assert torch.isnan(out[~keep]).all() and torch.isnan(lse[~keep]).all()
+
+
+@pytest.mark.parametrize("ratio", [2.0 ** 9, 2.0 ** 12, 2.0 ** 17, 2.0 ** 30])
+def test_queries_of_a_wide_range_over_8_bit_caches(fw, ratio):
+    """An element far above the others of its row: two E4M3 terms are off by at most 2^-17 of
+    it in each other element (and exact down to 2^-10 of it), so a score by 2^-17 max |q| sum
+    |k_i| scale, on top of the other bounds."""
+    x = make([70, 2], [300, 40], 8, 2, 128, 16, kv8=True, seed=28)
+    x["q"][:, :, 17] *= ratio
+    x["scale"] = 0.02 / ratio
+    out, lse = fw.paged_prefill(**on_gpu(x))
+    assert fw.device_status() == 0
+    o_ref, l_ref, absv, reach = step.paged_prefill(**x)
+    k = x["k_cache"].double().nan_to_num(0.0).abs().sum(-1).amax().item() * x["k_scale"]
+    big = x["q"].double().abs().amax(-1).numpy()
+    delta = 136 * 2.0 ** -24 * reach + 2.0 ** -17 * big * k * x["scale"]
+    assert (np.abs(lse.double().cpu().numpy() - l_ref) <= delta + 2.0 ** -20 * np.abs(l_ref) + 2.0 ** -18).all()
+    d = (2 * U + 2 * delta[..., None] + 2.0 ** -18) * absv
+    assert (np.abs(out.double().cpu().numpy() - o_ref) <= d + U * (np.abs(o_ref) + d) + 1e-30).all()
+
+
+@pytest.mark.parametrize("kv8", [False, True])
+@pytest.mark.parametrize("ctas", [0, 1, 2])
+def test_units_of_one_and_two_row_tiles_in_turn(fw, kv8, ctas):
+    """A stream without a row tile keeps step: short units between long ones, one tile or many."""
+    d = [200, 1, 1, 1, 130, 2, 64, 300, 1, 1, 1, 1, 1, 257, 3, 1]
+    n = [200, 1, 300, 2, 131, 900, 64, 700, 5, 128, 129, 1, 640, 300, 3, 1500]
+    fw.set_option(fw.FW_OPT_MAX_CTAS, ctas)
+    try:
+        run_and_check(fw, make(d, n, 8, 2, 128, 16, kv8=kv8, seed=29), "turns")
+    finally:
+        fw.set_option(fw.FW_OPT_MAX_CTAS, 0)
 
 
 @pytest.mark.parametrize("amp,scale", [(1.0, -0.05), (1.0, 0.0), (40.0, 0.3), (1e-3, 0.088), (30.0, -0.2)])
