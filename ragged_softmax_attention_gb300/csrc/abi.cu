@@ -1753,7 +1753,7 @@ fw_status_t fw_paged_prefill(const fw_tensor_t *q, const fw_tensor_t *k_cache, c
     if (D == 256 && p.grid < 2) p.row_tiles = 1;
     const bool pairs = D == 256 && p.row_tiles == 2;
     p.workers = pairs ? p.grid / 2 : p.grid;
-    p.piece_cost = kv8 || pairs ? fw::kChunkPieceCostLong : p.row_tiles > 1 ? fw::kChunkPieceCost : fw::kChunkPieceCostOne;
+    p.piece_cost = pairs ? fw::kChunkPieceCostPair : kv8 || p.row_tiles > 1 ? fw::kChunkPieceCost : fw::kChunkPieceCostOne;
     // As in the decode: the KV heads ride on the worker's number when there are whole groups of them.
     p.ride = p.Hkv > 1 && p.workers % p.Hkv == 0;
     const size_t need = fw::chunk_workspace_bytes(p.D, d->num_sms);

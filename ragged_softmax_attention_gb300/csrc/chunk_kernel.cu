@@ -36,7 +36,7 @@
 // prompts of 300 .. 5,000 tokens, 32/8 heads, 797 us, 1.24 PFLOP/s, and 500 .. 2,000 tokens
 // with a window of 1,023 keys 144 us, where the ends of units (7,300 cycles) and masked tiles
 // take the rest; 48 requests of which 40 bring one token 322 us, 61 % of DRAM; FP8, 256 ..
-// 1,024 tokens on 2,048 .. 16,384 keys, 761 us, 1.22 PFLOP/s, 3,800 cycles a key tile, to which
+// 1,024 tokens on 2,048 .. 16,384 keys, 755 us, 1.23 PFLOP/s, 3,800 cycles a key tile, to which
 // everything adds (one QK term less would take 75 us off, the widening 32, the second
 // reading 20); 24 tokens on 700 keys 14.6 us, 6 of them before the first scores.
 //

@@ -57,11 +57,12 @@ constexpr int kTreePieceCost = 5;
 // Chunk attention: the same, in keys; every unit weighs a tile more than its keys, for
 // the tiles that its first and last key share.  Two row tiles: 16 prompts of 300 .. 5,000
 // tokens 861 us at 0, 828 at 256, 832 at 384, 866 at 640; a mixed batch 349, 329, 330, 326;
-// over FP8 caches, whose steps are longer, 934, 893, 879, 868; pairs of CTAs 163, 158, 154, 154.
+// over FP8 caches 766 at 256, 755 at 384, 760 at 640, and prompts there 980, 959, 995 (one row
+// tile: 174 us at 128, 170 at 384, 172 at 640); pairs of CTAs 163 at 0, 158, 154, 154.
 constexpr int kChunkMinSpan = 256;
 constexpr int kChunkPieceCostOne = 128;
 constexpr int kChunkPieceCost = 384;
-constexpr int kChunkPieceCostLong = 640;
+constexpr int kChunkPieceCostPair = 640;
 constexpr int kMaxTableRows = 8192;   // page tables: requests whose sums fit a block's shared memory
 constexpr int kLatentRows = 64;       // latent-head decode: query heads per CTA (MMA N of one CTA)
 constexpr int kLatentPairRows = 128;  // latent-head decode on CTA pairs: query heads per pair
