@@ -174,6 +174,17 @@ def test_ragged_batches(seed):
                 check(Plan(d, n, G, Hkv, NT, grid, r.random() < 0.7, window, r.choice([128, 640])))
 
 
+@pytest.mark.parametrize("seed", range(12))
+def test_ragged_batches_on_pairs(seed):
+    """Half as many workers, two row tiles a unit."""
+    r = random.Random(1000 + seed)
+    d = [r.choice([1, 7, r.randint(0, 1200)]) for _ in range(r.choice([1, 4, 23]))]
+    n = [x + r.choice([0, 5, r.randint(0, 6000)]) for x in d]
+    for G, Hkv in ((1, 16), (8, 1), (2, 4)):
+        for workers in (76, 1, 5):
+            check(Plan(d, n, G, Hkv, 2, workers, r.random() < 0.7, r.choice([-1, 300]), 640))
+
+
 def test_ranges_are_even():
     p = Plan([4096], [36864], 5, 8, 2, 152)
     load = [sum(t for _, _, t, _, _ in p.walk(c)) for c in range(152)]
