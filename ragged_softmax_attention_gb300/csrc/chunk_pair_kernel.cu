@@ -19,7 +19,11 @@
 // barriers, CTA 0's commits arrive on both CTAs'; P is handed over by CTA 0's four softmax
 // warps and one thread of CTA 1, after its warps have met.  Values in tiles that some row
 // does not see whole are looked after by the CTA that holds their columns, once the issuer
-// has seen them land and said so; what is not finite is marked in both CTAs.
+// has seen them land and said so; what is not finite is marked in both CTAs.  A mark stands
+// in both before P of its tile is handed over (a fence at cluster scope behind it, on that
+// path alone), so before that tile's product begins, and is read after a wait at cluster
+// scope for the unit's last product: the case below as before, 149 us.  (An arrival of the
+// issuer's at cluster scope for every unit that may have marks took 161.)
 //
 // Warp roles: warp 0 copies K and V halves, warp 1 of CTA 0 issues the MMAs, warp 3 works
 // out the pieces and copies the queries, warps 4 .. 7 run the softmax.
@@ -69,6 +73,8 @@ constexpr uint32_t kOCol = 256;                // TMEM: two S buffers of 128 col
 __device__ __forceinline__ void or_cluster(uint32_t addr, uint32_t v) {
     asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
+
+__device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 chunk_pair_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
@@ -455,6 +461,7 @@ chunk_pair_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
                                 or_cluster(cluster_addr(word, cta), 1u << (row & 31));
                                 or_cluster(cluster_addr(marks, cta), 1u);
                             }
+                            fence_cluster();
                         }
                     }
                     if (!some || wild) {
@@ -478,7 +485,7 @@ chunk_pair_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
                 __syncwarp();
             }
             // ------------------------------------------------------ epilogue
-            wait_pv(steps - 1);
+            mbar_wait_cluster(&pv_done[(steps - 1) & 1u], ((steps - 1) >> 1) & 1u, wc);      // the marks, too
             tc_fence_after();
             bool poison = false;
             if (__builtin_expect(*reinterpret_cast<volatile uint32_t *>(marks) != 0, 0)) {
