@@ -603,10 +603,10 @@ fw_status_t fw_paged_prefill_workspace_size(int32_t head_dim, size_t *bytes);
  *   interleaved    0: i' = i + F; else pairs are neighbours, (2 i, 2 i + 1)
  *   q_out [N, Hq, D], k_out [N, Hkv, D]  BF16, written; may be q and k themselves
  *
- * Arithmetic in FP32, one rounding at the end; angles to 2^-28 of a turn for every
- * position.  An axis outside 0 .. axes - 1 is taken as 0 and records FW_ERR_INVALID_ARG
- * in the device status word.  Squares are added in FP32: a head whose elements pass
- * 2^60 comes out as zeros.  One launch, no workspace.
+ * Arithmetic in FP32, one rounding at the end; angles to 1.1 * 2^-28 of a turn for every
+ * position and frequency.  An axis outside 0 .. axes - 1 is taken as 0 and records
+ * FW_ERR_INVALID_ARG in the device status word.  Squares are added in FP32: a head whose
+ * elements pass 2^60 comes out as zeros.  One launch, no workspace.
  */
 fw_status_t fw_qk_norm_rope(const fw_tensor_t *q, const fw_tensor_t *k, const fw_tensor_t *q_weight,
                             const fw_tensor_t *k_weight, float eps, const fw_tensor_t *inv_freq,

@@ -16,18 +16,20 @@
 // so that nothing waits for another warp.
 //
 // Measured (GB300): 8,191 tokens of 40/8 heads into an FP8 cache, 218 MB in 36 us, 0.90 of
-// copy; 5,000 of 32/8 heads with three axes, 102 MB in 19.7, 0.76; 48 tokens 4.0, all of it
+// copy; 5,000 of 32/8 heads with three axes, 102 MB in 19.7, 0.76; 48 tokens 3.9, all of it
 // round trips.  On the way, first case: every warp that shares a token working out its
 // angles, loads by round 85 us; a block's tokens together 64; copies ahead 57; a warp to a
 // token 47; the head groups of all tokens in equal runs, codes without division 36.
 //
 // An angle is needed modulo one turn, and pos * inv_freq in 32 bits loses it (1e5
 // radians are good to 0.008).  inv_freq / 2 pi is kept as a 64-bit fraction of a
-// turn, worked out in 64 bits once a block; the integer product with the position
-// drops whole turns by itself, exactly, for either sign.  Its leading 32 bits would not fit
-// a float either; less the nearest quarter turn they do to 2^-28 of a turn (keys of the first
-// case above that come out as another E4M3 code than in 64 bits: 11 of 8.4 million; 22 with
-// the angle rounded as it was).
+// turn; the integer product with the position drops whole turns by itself, exactly, for
+// either sign.  The fraction is worked out once a block, in integers, since a position of
+// 2^31 multiplies what it lacks (a double leaves 2^-25 of a turn for a frequency of 1, 2^-19
+// for 40; two doubles do, and take 0.3 us more of the 48 tokens above).  The product's leading
+// 32 bits would not fit a float either; less the nearest quarter turn they do to 2^-28 of
+// a turn (keys of the first case above that come out as another E4M3 code than in 64 bits: 11
+// of 8.4 million; 22 with the angle rounded as it was).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -173,6 +175,23 @@ __device__ __forceinline__ void store_codes(char *to0, char *to1, const float *v
     }
 }
 
+// f / 2 pi modulo 1 in units of 2^-64, rounded towards zero: f is m 2^e, and of 1 / 2 pi only
+// the digits count that m 2^e takes to between 2^-1 and 2^-128; those before make whole turns
+// (Payne and Hanek, "Radian reduction for trigonometric functions", 1983).  256 digits
+// do for every float.
+__device__ __forceinline__ uint64_t turn_of(float freq) {
+    const uint32_t w = __float_as_uint(freq), exponent = w >> 23 & 255;
+    const uint64_t m = exponent ? (w & 0x7fffffu) | 0x800000u : w & 0x7fffffu;
+    const int at = (int)max(exponent, 1u) - 150 + 192, i = at >> 6, r = at & 63;       // e + 192 >= 43
+    auto digits = [](int k) -> uint64_t {                                 // 64 of them, after 192 zeros
+        return k == 3 ? 0x28be60db9391054aull : k == 4 ? 0x7f09d5f47d4d3770ull : k == 5 ? 0x36d8a5664f10e410ull
+             : k == 6 ? 0x7f9458eaf7aef158ull : 0;
+    };
+    const uint64_t a = digits(i), b = digits(i + 1), c = digits(i + 2);
+    const uint64_t t = m * (a << r | b >> 1 >> (63 - r)) + __umul64hi(m, b << r | c >> 1 >> (63 - r));
+    return w >> 31 ? 0 - t : t;
+}
+
 template <int D, int E, bool kInter, bool kPartial>
 __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
     constexpr int L = D / E, H = E / 2, P = E / 4;   // lanes of a head; elements and f32x2s of a run
@@ -266,8 +285,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) norm_rope_kernel(co
     }
     if (p.axes == 1) look(n_first);
     if (tid < half) {
-        const double t = (double)freq * 0.15915494309189533577;
-        turn[tid] = __double2ull_rn((t - floor(t)) * 18446744073709551616.0);
+        turn[tid] = turn_of(freq);
         if ((unsigned)on_axis >= (unsigned)p.axes) record_error(p.status, kErrInvalid);
         axis[tid] = (unsigned)on_axis < (unsigned)p.axes ? on_axis : 0;
     }
