@@ -514,9 +514,9 @@ fw_status_t fw_kv_commit(const fw_tensor_t *path, const fw_tensor_t *path_lens, 
  * every run.
  *
  * Probabilities below 0 and NaN count as 0, those above 1 as 1.  A parent outside -1 ..
- * t - 1 is taken as -1; a draft whose token is outside 0 .. V - 1 is passed over; a row
- * that adds up to 4 or more stops there.  These record FW_ERR_INVALID_ARG in the device
- * status word, and so does a request with nothing to draw from (R all zero, or no drafts
+ * t - 1 is taken as -1; a draft whose token is outside 0 .. V - 1 is passed over; a sum
+ * of 4 or more, at the path's end or where a draft is rejected, stops there.  These record
+ * FW_ERR_INVALID_ARG in the device status word, and so does a request with nothing to draw from (R all zero, or no drafts
  * and R = T), whose next token is -1.  1 <= T <= 256.  One launch, no workspace.
  */
 fw_status_t fw_verify_drafts(const fw_tensor_t *tokens, const fw_tensor_t *parents, const fw_tensor_t *draft_lens,

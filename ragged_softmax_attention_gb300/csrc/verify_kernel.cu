@@ -372,6 +372,7 @@ struct Walk {
         if (pending >= 0) {
             u64 s = 0;
             for (int r = 0; r < C; ++r) s = min(s + sums[r], kMost);
+            if (s >= kMost) record_error(a.status, kErrInvalid);
             if (a.draft) {
                 if (s > 0) {
                     c += total >> 8;                       // 2^-60 to 2^-52

@@ -1,0 +1,39 @@
+"""Verification of drafts: rows that are no probabilities, at nodes that the path goes
+through."""
+import pytest
+import torch
+
+from tests.gpu_common import built_library
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def fw():
+    return built_library()
+
+
+def i32(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.parametrize("draft", [True, False])
+@pytest.mark.parametrize("V", [8, 40000])
+def test_a_row_of_four_and_more_is_told_where_a_draft_is_rejected(fw, V, draft):
+    """Draft 1 is rejected at a row of ones, draft 2 accepted there: the path ends at a row
+    that is one, and the call still tells."""
+    target = torch.zeros(1, 3, V, device="cuda")
+    target[0, 0] = 1.0
+    target[0, 0, 5] = 0.0
+    target[0, 1:, 3] = 1.0
+    q = torch.zeros_like(target)
+    q[:, :, 5], q[:, :, 6] = 0.5, 0.125
+    args = (i32([[0, 5, 6]]), i32([[-1, 0, 0]]), target, torch.tensor([[0.0, 0.9, 0.1, 0.5]], device="cuda"))
+    fw.device_status()
+    path, n, nxt = fw.verify_drafts(*args, draft_probs=q if draft else None)
+    assert (path.tolist(), n.tolist(), nxt.tolist()) == ([[0, 2, -1]], [2], [3])
+    assert fw.device_status() == 1
+    target[0, 0, :5] = target[0, 0, 7:] = 0.0             # the one at 6 is left: fine
+    path, n, nxt = fw.verify_drafts(*args, draft_probs=q if draft else None)
+    assert (path.tolist(), n.tolist(), nxt.tolist()) == ([[0, 2, -1]], [2], [3])
+    assert fw.device_status() == 0
