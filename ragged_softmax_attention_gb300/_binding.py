@@ -431,7 +431,8 @@ def verify_drafts(tokens, parents, target_probs, uniforms, draft_probs=None, dra
     0 follows the committed context), drawn from draft_probs (the same shape; None:
     proposed with certainty); uniforms [B, T + 1].  Returns (path [B, max_path]
     padded with -1, path_lens [B], next_tokens [B]), the first two as kv_commit
-    takes them; max_path defaults to T."""
+    takes them; max_path defaults to T, or to the width of a given path, which it
+    has to equal otherwise."""
     return _on(stream, (_fast_module or _fast()).verify_drafts, tokens, parents, target_probs, uniforms, draft_probs,
                draft_lens, max_path, path, path_lens, next_tokens)
 

@@ -301,6 +301,9 @@ PyObject *verify_drafts(PyObject *, PyObject *const *a, Py_ssize_t n) {
     long long most = t[0].size(1);
     if (a[6] != Py_None && !whole(a[6], &most)) return nullptr;
     if (!t[7].defined() && (most < 1 || most > 256)) raise(PyExc_ValueError, "max_path must be 1 to 256");
+    // A given path's width is how many are accepted at most.
+    if (t[7].defined() && a[6] != Py_None && (t[7].dim() != 2 || t[7].size(1) != most))
+        raise(PyExc_ValueError, "path must be [B, max_path] where both are given");
     Where where(args.device);
     const int64_t sizes[3] = {B * (int64_t)most, B, B};
     int64_t total = 0;

@@ -37,3 +37,19 @@ def test_a_row_of_four_and_more_is_told_where_a_draft_is_rejected(fw, V, draft):
     path, n, nxt = fw.verify_drafts(*args, draft_probs=q if draft else None)
     assert (path.tolist(), n.tolist(), nxt.tolist()) == ([[0, 2, -1]], [2], [3])
     assert fw.device_status() == 0
+
+
+def test_a_path_of_another_width_than_max_path_is_refused(fw):
+    """How many drafts may be accepted is said once: by the width of a given path."""
+    probs = torch.full((1, 3, 4), 0.25, device="cuda")
+    args = (i32([[0, 1, 2]]), i32([[-1, 0, 1]]), probs, torch.zeros(1, 4, device="cuda"))
+    path = torch.zeros(1, 3, dtype=torch.int32, device="cuda")
+    before = fw.launch_count()
+    for given, most in ((path, 1), (path, 4), (path[:, :2], 3), (path[0], 3)):
+        with pytest.raises(ValueError, match="max_path"):
+            fw.verify_drafts(*args, max_path=most, path=given)
+    assert fw.launch_count() == before
+    for given, most in ((path, 3), (path, None), (path[:, :1], 1), (None, 2)):
+        got, n, _ = fw.verify_drafts(*args, max_path=most, path=given)
+        want = 3 if given is path else 1 if given is not None else 2
+        assert got.shape == (1, want) and n.tolist() == [want]
