@@ -158,11 +158,11 @@ fw_status_t fw_paged_decode_noalloc(const fw_tensor_t *q, const fw_tensor_t *k_c
  * tensor cores read the E4M3 bytes as stored; the result is that of FP16
  * products of the FP8 values with FP16-exact queries and probabilities and
  * FP32 sums: each BF16 query row is scaled by a power of two and carried as
- * two E4M3 terms (exact for every element down to 2^-10 of the row's largest
- * magnitude), each probability is rounded to FP16 and carried as four E5M2
- * terms (exact).  The same workspace as fw_paged_decode
- * (fw_paged_decode_workspace_size with the same shapes); errors as
- * fw_paged_decode, plus FW_ERR_INVALID_ARG for a non-finite or non-positive
+ * two E4M3 terms (exact for every element down to 2^-9 of the row's largest
+ * magnitude, below to within 2^-17 of it), each probability is rounded to
+ * FP16 and carried as four E5M2 terms (exact).  The same workspace as
+ * fw_paged_decode (fw_paged_decode_workspace_size with the same shapes);
+ * errors as fw_paged_decode, plus FW_ERR_INVALID_ARG for a non-finite or non-positive
  * k_scale / v_scale.
  */
 fw_status_t fw_paged_decode_fp8(const fw_tensor_t *q, const fw_tensor_t *k_cache,
@@ -557,7 +557,7 @@ fw_status_t fw_verify_drafts(const fw_tensor_t *tokens, const fw_tensor_t *paren
  * Arithmetic as fw_paged_decode_tree over BF16 caches: products of BF16 values summed in
  * FP32, weights rounded to BF16 for the product with V and summed unrounded.  Over an FP8
  * cache q is carried as the sum of two E4M3 terms on a power of two of its own per row
- * (exact for elements down to 2^-10 of the row's largest, below to within 2^-17 of it; a
+ * (exact for elements down to 2^-9 of the row's largest, below to within 2^-17 of it; a
  * row with an element that is not finite comes out as NaN), and V is widened to BF16, which
  * holds every E4M3 value.
  *

@@ -12,8 +12,9 @@
 // once:
 //   * Q: each BF16 query row is scaled by a power of two 2^e (its largest
 //     magnitude lands in [128, 256)) and split into hi + mid E4M3 terms.
-//     Every BF16 value of the row down to 2^-10 of that maximum is exactly
-//     hi + mid (8 significant bits = two 4-bit terms); S = S_hi + S_mid and
+//     Every BF16 value of the row down to 2^-9 of that maximum is exactly
+//     hi + mid (8 significant bits = two 4-bit terms, of which E4M3's last
+//     step is 2^-9); S = S_hi + S_mid and
 //     2^-e folds into the row's score scale, k_scale too.
 //   * P: each probability is rounded to FP16 (as a 16-bit MMA would take it)
 //     and split into four E5M2 terms; E5M2 is FP16's upper byte, so the four

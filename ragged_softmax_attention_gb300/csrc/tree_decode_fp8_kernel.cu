@@ -8,7 +8,7 @@
 //   S = Q K^T   kind::f8f6f4 on the E4M3 bytes as they land.  Each BF16 query
 //               row is scaled by a power of two (largest magnitude in
 //               [128, 256)) and carried as two E4M3 terms, hi + mid, exact for
-//               every element down to 2^-10 of the row's largest; below, an
+//               every element down to 2^-9 of the row's largest; below, an
 //               element is off by at most 2^-17 of the largest.  Two terms of
 //               K = 32 products take the tensor core as long as one BF16 pass.
 //   O += P V    kind::f16 on FP16: four warps widen each V tile (exact in FP16),
