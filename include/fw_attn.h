@@ -605,8 +605,11 @@ fw_status_t fw_paged_prefill_workspace_size(int32_t head_dim, size_t *bytes);
  *
  * Arithmetic in FP32, one rounding at the end; angles to 1.1 * 2^-28 of a turn for every
  * position and frequency.  An axis outside 0 .. axes - 1 is taken as 0 and records
- * FW_ERR_INVALID_ARG in the device status word.  Squares are added in FP32: a head whose
- * elements pass 2^60 comes out as zeros.  One launch, no workspace.
+ * FW_ERR_INVALID_ARG in the device status word.  Squares are added in FP32: heads of
+ * elements within 2^-60 .. 2^59 are normed to the full, with an eps of 0 too; a normed head
+ * whose squares add up past FP32 comes out as zeros, or NaN where an element times its
+ * weight is past it as well; below 2^-60 bits are lost where eps does not outweigh the
+ * squares.  One launch, no workspace.
  */
 fw_status_t fw_qk_norm_rope(const fw_tensor_t *q, const fw_tensor_t *k, const fw_tensor_t *q_weight,
                             const fw_tensor_t *k_weight, float eps, const fw_tensor_t *inv_freq,
