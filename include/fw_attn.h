@@ -494,8 +494,10 @@ fw_status_t fw_kv_commit(const fw_tensor_t *path, const fw_tensor_t *path_lens, 
  *                       as it is, other drafts without a parent are nobody's.  R = T +
  *                       1: row 0 follows the committed context, row t + 1 draft t
  *   draft_probs [B, R, V]   F32 or NULL: the probabilities that the children of a row's
- *                       node were drawn from, one after another.  NULL: each draft
- *                       was proposed with certainty (the draft model's likeliest
+ *                       node were drawn from, each by itself, so that a token may come
+ *                       twice (children drawn without putting back have other
+ *                       probabilities, and are not distributed as below).  NULL: each
+ *                       draft was proposed with certainty (the draft model's likeliest
  *                       tokens, a lookup)
  *   uniforms    [B, T + 1]  F32 in [0, 1): entry t decides draft t, entry T draws the
  *                       next token
@@ -533,7 +535,8 @@ fw_status_t fw_verify_drafts(const fw_tensor_t *tokens, const fw_tensor_t *paren
  *   k_cache, v_cache  [num_pages, ps, Hkv, D]  BF16 or FP8_E4M3 (scales k_scale,
  *                                   v_scale; 1 for BF16 caches)
  *   block_table  [B, max_pages]     I32, as fw_paged_decode; entries of pages that no
- *                                   token of the request sees are never read
+ *                                   token of the request sees may hold anything, and
+ *                                   those pages are not read
  *   cu_seqlens_q [B + 1]  I32: request b's tokens are rows cu[b] .. cu[b + 1] - 1
  *                         (none is fine).  Rows of no request are left as they were.  A
  *                         request whose rows go down or past total_q is skipped and

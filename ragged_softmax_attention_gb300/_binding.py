@@ -428,8 +428,8 @@ def verify_drafts(tokens, parents, target_probs, uniforms, draft_probs=None, dra
                   path_lens=None, next_tokens=None, stream=None):
     """fw_verify_drafts: drafts tokens / parents [B, T] against target_probs [B, T,
     V] (row t follows draft t; draft 0 is accepted as it is) or [B, T + 1, V] (row
-    0 follows the committed context), drawn from draft_probs (the same shape; None:
-    proposed with certainty); uniforms [B, T + 1].  Returns (path [B, max_path]
+    0 follows the committed context), each drawn by itself from draft_probs (the same
+    shape; None: proposed with certainty); uniforms [B, T + 1].  Returns (path [B, max_path]
     padded with -1, path_lens [B], next_tokens [B]), the first two as kv_commit
     takes them; max_path defaults to T, or to the width of a given path, which it
     has to equal otherwise."""

@@ -78,8 +78,8 @@ __device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0
 // functions on the IBM RISC System/6000 processor", section 8), as long as nothing over-
 // or underflows: for scales of 2^-60 .. 2^60 and quotients below 2^10; those so small that
 // the remainder is not exact have code 0, and their sign is put back.  Other scales (inv =
-// 0), and lanes with a quotient that large, an infinity or a NaN, divide.  (Division alone:
-// 115 us for 4,864 tokens of 128 key and value heads, 94 so.)
+// 0), and lanes with a quotient that large or infinite, divide; a NaN stays one without.
+// (Division alone: 115 us for 4,864 tokens of 128 key and value heads, 94 so.)
 template <int N>
 __device__ __forceinline__ void codes(const float *v, float scale, float inv, uint32_t *out) {
     float r[N], most = 0.f;

@@ -7,8 +7,8 @@
 // and the walk goes on from the accepted child.  Where no child is accepted the next
 // token is drawn from R: the first x with R(0) + .. + R(x) > u sum R.  Drafts so
 // verified are distributed as the target's own samples (rejection sampling, one
-// draft after another).  Without a draft model's rows a draft is taken as proposed
-// with certainty, and R loses the token.
+// draft after another; a node's children are independent draws).  Without a draft model's
+// rows a draft is taken as proposed with certainty, and R loses the token.
 //
 // A draw compares u with one of V running sums, and sums in 32 bits, or in an order
 // that a split changes, would move the borders between neighbours by more than
