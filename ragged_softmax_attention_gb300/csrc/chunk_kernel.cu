@@ -540,8 +540,8 @@ chunk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUte
                 __syncwarp();
                 const int set = k % C::kQSets;
                 for (int x = 0; x < u.nrt; ++x)
-                    split_rows<C::kChunkBytes>(sQ + x * C::kQBytes, p.head_chunks > 1 ? 128 : p.G * p.tile_tokens, warp & 3,
-                                               q_exp + (set * NT + x) * 128);
+                    split_rows<C::kChunkBytes>(sQ + x * C::kQBytes, p.head_chunks > 1 ? 128 : p.G * p.tile_tokens, warp & 3, lane,
+                                               [&](int r, int8_t e) { q_exp[(set * NT + x) * 128 + r] = e; });
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&q_ready[set]);

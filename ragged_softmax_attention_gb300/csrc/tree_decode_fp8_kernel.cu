@@ -455,8 +455,8 @@ tree_decode_fp8_kernel(const __grid_constant__ TreeParams p, const __grid_consta
             if (row < kBadWords) bad[k % kBadUnits * kBadWords + row] = 0;
             mbar_wait(q_full, k & 1, wc);
             for (int x = 0; x < u.nrt; ++x) {
-                split_rows<C::kHalf>(sQ + x * C::kQBytes, p.head_chunks > 1 ? 128 : p.G * p.tile_tokens, warp - 4,
-                                     q_exp + (k % C::kSched * NT + x) * 128);
+                split_rows<C::kHalf>(sQ + x * C::kQBytes, p.head_chunks > 1 ? 128 : p.G * p.tile_tokens, warp - 4, lane,
+                                     [&](int r, int8_t e) { q_exp[(k % C::kSched * NT + x) * 128 + r] = e; });
             }
             fence_proxy_async_smem();
             __syncwarp();
