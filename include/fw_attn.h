@@ -572,7 +572,8 @@ fw_status_t fw_verify_drafts(const fw_tensor_t *tokens, const fw_tensor_t *paren
  * (256-byte aligned) or, when it is NULL, the workspace of fw_set_workspace() or the
  * internal buffer, whose calls have to be ordered.  Calls with workspaces of their own may
  * overlap.  Outputs and the workspace must not share elements with inputs or with one
- * another.
+ * another.  A CTA's part of a unit has to end within FW_OPT_WAIT_TIMEOUT_MS: at 1 to 2 us
+ * for 128 keys the default does for 2^26 of them.
  */
 fw_status_t fw_paged_prefill(const fw_tensor_t *q, const fw_tensor_t *k_cache, const fw_tensor_t *v_cache,
                              const fw_tensor_t *block_table, const fw_tensor_t *cu_seqlens_q,
@@ -689,8 +690,9 @@ typedef enum {
                                        row max rises more than 8 log2 units).  Same result up to
                                        rounding; kept for comparison. */
     FW_OPT_TEST_STALL = 5           /* test hook, default 0.  1: the copy warp of the grouped-query
-                                       decode kernel and of the tree decode kernels first waits on a barrier that nothing completes,
-                                       so that wait runs out after FW_OPT_WAIT_TIMEOUT_MS: the call
+                                       decode kernel, of the tree decode kernels and of the chunk
+                                       attention kernels first waits on a barrier that nothing
+                                       completes, so that wait runs out after FW_OPT_WAIT_TIMEOUT_MS: the call
                                        records FW_ERR_DEVICE_TIMEOUT (read by fw_get_device_status)
                                        and its outputs are not valid.  No key or value is
                                        copied and nothing multiplied before the wait, so no such
